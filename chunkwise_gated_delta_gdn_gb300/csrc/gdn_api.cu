@@ -75,12 +75,10 @@ bool make_scan_maps(ScanMaps &m, const void *q, const void *k, const void *v,
 
 namespace {
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned16(const void *p) { return gdn::aligned_to(p, 16); }
 
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
+  return gdn::ranges_overlap(a, na, b, nb);
 }
 
 struct Plan {

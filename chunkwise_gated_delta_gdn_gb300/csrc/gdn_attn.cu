@@ -1,0 +1,304 @@
+// gdn_attn.cu -- causal softmax attention with grouped heads, over a whole
+// prompt or over a paged cache, and the merge of partial results.
+//
+//   s_j = scale q.k_j (j <= p), m = max_j s_j, l = sum_j e^(s_j - m),
+//   o = sum_j e^(s_j - m) v_j / l,  lse = m + ln l
+//
+// One pass over the keys with the running maximum and sum; what a row has when
+// no key is visible to it (o = 0, lse = -inf) follows from l = 0.
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "gdn_attn.cuh"
+#include "gdn_device.cuh"
+
+namespace gdn {
+namespace {
+
+// 64 rows x 64 keys per step: four warps of 16 rows, the operands in shared
+// memory as fp32, both products split-tf32 on mma.sync.
+using WarpShape = AttnShape<64, 64, 64, 1>;
+constexpr int kThreads = 128;
+
+template <int D>
+constexpr int smem_bytes() { return 3 * 64 * (D + 4) * 4; }
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// c += A B for one 16 x 8 tile, k = 8: the three products of the two halves
+template <bool BX>
+__device__ __forceinline__ void mma3(float (&c)[4], const uint32_t (&ah)[4],
+                                     const uint32_t (&al)[4], float b0, float b1) {
+  uint32_t h0, l0, h1, l1;
+  split_tf32(b0, h0, l0);
+  split_tf32(b1, h1, l1);
+  mma1688_tf32(c, al, h0, h1);
+  if (!BX) mma1688_tf32(c, ah, l0, l1);
+  mma1688_tf32(c, ah, h0, h1);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load8(float (&x)[8], const typename Elem<BF16>::T *p) {
+  if constexpr (BF16) {
+    const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(p));
+    const __nv_bfloat16 *b = reinterpret_cast<const __nv_bfloat16 *>(&raw);
+#pragma unroll
+    for (int e = 0; e < 8; e++) x[e] = __bfloat162float(b[e]);
+  } else {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4 *>(p + 4));
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+}
+__device__ __forceinline__ void put8(float *d, const float (&x)[8]) {
+  *reinterpret_cast<float4 *>(d) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4 *>(d + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs a) {
+  using E = Elem<BF16>;
+  constexpr int kS = D + 4;  // row stride in floats: fragment reads hit 32 banks
+  extern __shared__ float smem[];
+  float *Qs = smem, *Ks = Qs + 64 * kS, *Vs = Ks + 64 * kS;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
+  const AttnPlan<WarpShape> plan(a.H, a.HKV);
+  const AttnStart st = attn_start<WarpShape, kThreads>(a, plan, blockIdx.x, gridDim.x);
+  AttnWalk<WarpShape> walk(a, plan, st, blockIdx.x);
+  AttnUnit u;
+  while (walk.next(u)) {
+    __syncthreads();  // the previous unit's operands are read
+    for (int i = tid; i < 64 * (D / 8); i += kThreads) {
+      const int r = i / (D / 8), c = (i % (D / 8)) * 8, t = r / u.gp;
+      float x[8] = {};
+      if (t < u.n_tok)
+        load8<BF16>(x, static_cast<const typename E::T *>(a.q) + (long long)(u.row0 + t) * a.q_stride +
+                           (u.head0 + r % u.gp) * D + c);
+      put8(Qs + r * kS + c, x);
+    }
+    float o[D / 8][4] = {}, m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+    const int row[2] = {warp * 16 + gq, warp * 16 + gq + 8};
+    int limit[2];  // last visible key
+#pragma unroll
+    for (int h = 0; h < 2; h++) limit[h] = min(u.pos0 + row[h] / u.gp, u.len - 1);
+    for (int t = u.t0; t < u.t1; t++) {
+      const int key0 = t * 64;
+      __syncthreads();
+      for (int i = tid; i < 2 * 64 * (D / 8); i += kThreads) {
+        const bool is_v = i >= 64 * (D / 8);
+        const int j = is_v ? i - 64 * (D / 8) : i, r = j / (D / 8), c = (j % (D / 8)) * 8;
+        const int key = key0 + r;
+        float x[8] = {};
+        if (key < u.len) {
+          const typename E::T *p = static_cast<const typename E::T *>(is_v ? a.v : a.k);
+          bool ok = true;
+          if (a.table) {
+            const int page = __ldg(a.table + (long long)u.seq * a.max_pages + key / a.page_size);
+            ok = page >= 0 && page < a.n_pages;
+            if (!ok && a.flags) atomicOr(a.flags, kFlagBadSeqlens);
+            p += (((long long)page * a.page_size + key % a.page_size) * a.HKV + u.kvh) * D;
+          } else {
+            // a prompt's keys are its own tokens
+            p += (long long)(u.row0 - u.pos0 + key) * (is_v ? a.v_stride : a.k_stride) + u.kvh * D;
+          }
+          if (ok) load8<BF16>(x, p + c);
+        }
+        put8((is_v ? Vs : Ks) + r * kS + c, x);
+      }
+      __syncthreads();
+      float s[8][4] = {};
+#pragma unroll 4
+      for (int k = 0; k < D; k += 8) {
+        uint32_t ah[4], al[4];
+        const float *q0 = Qs + row[0] * kS + k + tq, *q1 = Qs + row[1] * kS + k + tq;
+        split_tf32(q0[0], ah[0], al[0]);
+        split_tf32(q1[0], ah[1], al[1]);
+        split_tf32(q0[4], ah[2], al[2]);
+        split_tf32(q1[4], ah[3], al[3]);
+#pragma unroll
+        for (int n = 0; n < 8; n++) {
+          const float *b = Ks + (n * 8 + gq) * kS + k + tq;
+          if constexpr (BF16) {  // bf16 inputs are exact in tf32
+            mma1688_tf32(s[n], ah, __float_as_uint(b[0]), __float_as_uint(b[4]));
+          } else {
+            mma3<false>(s[n], ah, al, b[0], b[4]);
+          }
+        }
+      }
+      // running maximum and sum; element e of a tile: row e / 2, key 2 tq + e % 2
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        float top = m[h];
+#pragma unroll
+        for (int n = 0; n < 8; n++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            float &x = s[n][2 * h + e];
+            x = key0 + n * 8 + 2 * tq + e <= limit[h] ? x * a.scale_log2 : -CUDART_INF_F;
+            top = fmaxf(top, x);
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float base = top == -CUDART_INF_F ? 0.f : top;  // nothing visible yet
+        const float alpha = exp2_approx(m[h] - base);
+        m[h] = top;
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < 8; n++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            float &x = s[n][2 * h + e];
+            x = exp2_approx(x - base);
+            sum += x;
+          }
+        l[h] = l[h] * alpha + sum;
+#pragma unroll
+        for (int n = 0; n < D / 8; n++) {
+          o[n][2 * h] *= alpha;
+          o[n][2 * h + 1] *= alpha;
+        }
+      }
+      // the weights are the A operand as they lie: contraction index tq stands
+      // for key 2 tq, index tq + 4 for key 2 tq + 1
+#pragma unroll
+      for (int n = 0; n < 8; n++) {
+        uint32_t ah[4], al[4];
+        split_tf32(s[n][0], ah[0], al[0]);
+        split_tf32(s[n][2], ah[1], al[1]);
+        split_tf32(s[n][1], ah[2], al[2]);
+        split_tf32(s[n][3], ah[3], al[3]);
+        const float *b = Vs + (n * 8 + 2 * tq) * kS + gq;
+#pragma unroll
+        for (int d = 0; d < D / 8; d++) mma3<BF16>(o[d], ah, al, b[d * 8], b[kS + d * 8]);
+      }
+    }
+    bool finite = true;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      const int t = row[h] / u.gp, head = u.head0 + row[h] % u.gp;
+      if (t >= u.n_tok) continue;
+      if (u.slot >= 0) {
+        float2 *po = reinterpret_cast<float2 *>(a.part_o + (long long)u.slot * 64 * (D / 4));
+#pragma unroll
+        for (int n = 0; n < D / 8; n++)  // columns n*8 + 2 tq: half of float4 n*2 + tq/2
+          po[((long long)(n * 2 + (tq >> 1)) * 64 + row[h]) * 2 + (tq & 1)] =
+              make_float2(o[n][2 * h], o[n][2 * h + 1]);
+        if (tq == 0) a.part_ml[(long long)u.slot * 64 + row[h]] = make_float2(m[h], l[h]);
+        continue;
+      }
+      const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
+      const long long at = (long long)(u.row0 + t) * a.H + head;
+#pragma unroll
+      for (int n = 0; n < D / 8; n++) {
+        const float x = o[n][2 * h] * inv, y = o[n][2 * h + 1] * inv;
+        finite &= isfinite(x) && isfinite(y);
+        typename E::T *p = static_cast<typename E::T *>(a.o) + at * D + n * 8 + 2 * tq;
+        if constexpr (BF16)
+          *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
+        else
+          *reinterpret_cast<float2 *>(p) = make_float2(x, y);
+      }
+      if (a.lse && tq == 0) a.lse[at] = l[h] == 0.f ? -CUDART_INF_F : (m[h] + log2f(l[h])) * 0.69314718056f;
+    }
+    if (!finite && a.flags) atomicOr(a.flags, kFlagNonfinite);
+  }
+}
+
+// Joins the partial results of one unit: block b.x looks at the border between
+// ranges b.x and b.x + 1 and works only when it is the first one inside a
+// unit.  A thread owns four columns of a row and adds the pieces up in the
+// order of the blocks that made them.
+constexpr int kMergeThreads = 256;
+template <class S, int D, bool BF16>
+__global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const AttnArgs a, int n_blocks) {
+  const AttnPlan<S> plan(a.H, a.HKV);
+  const int first = blockIdx.x;
+  const AttnStart st = attn_start<S, kMergeThreads>(a, plan, first + 1, n_blocks);
+  const long long c = (first + 1) * st.per;
+  if (st.seq >= a.n_seqs || c >= st.total) return;
+  bool bad;
+  const AttnSeq s = attn_seq(a, st.seq, bad);
+  AttnUnit u;
+  const long long u0 = st.seq0 + plan.find(s, st.seq, c - st.seq0, u);
+  const int w = plan.unit_cost(s);
+  int last;
+  if (!attn_merge(u0, w, u.nt, first + 1, st.per, last)) return;
+  bool finite = true;
+  // work items (row, four columns) in an order that gives a warp adjacent rows
+  const int rows = min(u.n_tok * u.gp, S::kRows);
+  for (int i = blockIdx.y * kMergeThreads + threadIdx.x; i < rows * (D / 4);
+       i += gridDim.y * kMergeThreads) {
+    const int row = i % rows, d4 = i / rows;
+    float m = -CUDART_INF_F;
+    for (int b = first; b <= last; b++)
+      m = fmaxf(m, a.part_ml[(long long)(b == first ? 2 * b + 1 : 2 * b) * S::kRows + row].x);
+    const float base = m == -CUDART_INF_F ? 0.f : m;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = first; b <= last; b++) {
+      const long long slot = b == first ? 2 * b + 1 : 2 * b;
+      const float2 ml = a.part_ml[slot * S::kRows + row];
+      const float4 x = a.part_o[(slot * (D / 4) + d4) * S::kRows + row];
+      const float f = exp2_approx(ml.x - base);
+      l += f * ml.y;
+      o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+    finite &= isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w);
+    const long long at = (long long)(u.row0 + row / u.gp) * a.H + u.head0 + row % u.gp;
+    if constexpr (BF16) {
+      __nv_bfloat162 y[2] = {__floats2bfloat162_rn(o.x, o.y), __floats2bfloat162_rn(o.z, o.w)};
+      *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + d4 * 4) =
+          *reinterpret_cast<uint2 *>(y);
+    } else {
+      *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at * D + d4 * 4) = o;
+    }
+    if (a.lse && d4 == 0)
+      a.lse[at] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718056f;
+  }
+  if (!finite && a.flags) atomicOr(a.flags, kFlagNonfinite);
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();  // no device: sizes can still be asked for
+    return 152;
+  }
+  return n;
+}
+
+template <int D, bool BF16>
+cudaError_t launch(AttnArgs a, cudaStream_t stream) {
+  a.min_cost = 4;
+  const int blocks = attn_blocks(BF16 ? 1 : 0, D);
+  cudaError_t e = cudaFuncSetAttribute(gdn_attn_warp_kernel<D, BF16>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+  if (e != cudaSuccess) return e;
+  gdn_attn_warp_kernel<D, BF16><<<blocks, kThreads, smem_bytes<D>(), stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  gdn_attn_merge_kernel<WarpShape, D, BF16><<<dim3(blocks - 1, 4), kMergeThreads, 0, stream>>>(a, blocks);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int attn_blocks(int, int d) { return sm_count() * (d == 64 ? 4 : 2); }
+int attn_part_rows(int) { return WarpShape::kRows; }
+
+cudaError_t launch_attn(const AttnArgs &a, int d, int dtype, cudaStream_t stream) {
+  if (d == 64) return dtype ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
+  if (d == 128) return dtype ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace gdn

@@ -114,12 +114,53 @@ struct TransferArgs {
   int dk, dv;
 };
 
+// Softmax attention (gdn_attn*.cu): causal over a whole prompt (kv_lens null:
+// keys = new tokens, row-major with token strides) or over a paged cache.
+struct AttnArgs {
+  const void *q, *k, *v;       // paged: k, v are the caches
+  void *o;
+  float *lse;                  // [Ttot][H] or nullptr
+  const int32_t *cu;           // [n_seqs + 1] or nullptr (plain batch of T tokens)
+  const int32_t *kv_lens;      // [n_seqs], paged only
+  const int32_t *table;        // [n_seqs][max_pages], paged only
+  int n_seqs, T, Ttot;
+  int H, HKV;
+  long long q_stride, k_stride, v_stride;  // elements between tokens
+  int page_size, max_pages, n_pages;
+  int max_len;                 // longest length the table can hold
+  float scale;
+  float scale_log2;            // scale * log2(e)
+  int min_cost;                // least cost of a block's range
+  float4 *part_o;              // partial results (see gdn_attn.cuh)
+  float2 *part_ml;
+  uint32_t *flags;             // device status word, or nullptr
+};
+// Writes the keys and values of new tokens into the pages of a cache.
+struct AppendArgs {
+  const void *k, *v;
+  void *k_cache, *v_cache;
+  const int32_t *cu, *kv_lens, *table;
+  int n_seqs, T, Ttot;
+  long long k_stride, v_stride;  // bytes between tokens
+  int row_bytes;                 // HKV * d elements
+  int page_size, max_pages, n_pages, max_len;
+  uint32_t *flags;
+};
+
 // Status-word bits (same values as GDN_FLAG_* in include/gdn.h).
 constexpr uint32_t kFlagPositiveGate = 1u << 0;
 constexpr uint32_t kFlagNonfinite = 1u << 1;
 constexpr uint32_t kFlagBadSeqlens = 1u << 2;
 constexpr uint32_t kFlagTimeout = 1u << 3;
 constexpr uint32_t kFlagLaunchConfig = 1u << 4;
+
+// Host-side argument checks of the C entry points.
+inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline bool ranges_overlap(const void *a, size_t na, const void *b, size_t nb) {
+  if (!a || !b || na == 0 || nb == 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + nb && b0 < a0 + na;
+}
 
 // Launchers; return cudaErrorInvalidValue for an uncompiled combination.
 // dtype: 0 = fp32, 1 = bf16.  gate: 0 = scalar (GDN), 1 = per key (KDA).
@@ -172,6 +213,12 @@ cudaError_t launch_conv1d(const ConvArgs &a, int width, int activation, int dtyp
                           cudaStream_t stream);
 cudaError_t launch_rownorm(const RowNormArgs &a, int dim, int kind, int dtype,
                            cudaStream_t stream);
+// attention: blocks that the launch uses (its partial results are sized by
+// them) and rows of one partial result; d 64 or 128, dtype 0 = fp32, 1 = bf16
+int attn_blocks(int dtype, int d);
+int attn_part_rows(int dtype);
+cudaError_t launch_attn(const AttnArgs &a, int d, int dtype, cudaStream_t stream);
+cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream);
 // S_out = M S_in + S_seg, per state
 cudaError_t launch_state_combine(const TransferArgs &a, cudaStream_t stream);
 // token-serial form; dv a multiple of 32

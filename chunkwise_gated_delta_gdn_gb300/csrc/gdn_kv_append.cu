@@ -1,0 +1,77 @@
+// gdn_kv_append.cu -- writes the keys and values of new tokens into the pages
+// of a cache: token t of sequence n goes to position p = len - nq + t, row
+// p % page_size of page table[n][p / page_size].  A token at a negative
+// position (fewer keys than new tokens: an idle slot of a padded batch) has no
+// place and is left out.
+//
+// A copy, bound by memory (and by launch latency for a decode step's few
+// rows): one 16-byte piece of a key row and the same piece of the value row
+// per thread, adjacent threads on adjacent pieces.
+#include <stdint.h>
+
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+
+// sequence that token row t belongs to: the last n with cu[n] <= t
+__device__ __forceinline__ int sequence_of(const int32_t *cu, int n_seqs, int t) {
+  int lo = 0, hi = n_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) gdn_kv_append_kernel(const AppendArgs a) {
+  const int per_row = a.row_bytes >> 4;
+  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const long long row = i / per_row;
+  if (row >= a.Ttot) return;
+  const int t = (int)row, piece = (int)(i - row * per_row);
+  int n, start, end;
+  if (a.cu) {
+    n = sequence_of(a.cu, a.n_seqs, t);
+    start = __ldg(a.cu + n);
+    end = __ldg(a.cu + n + 1);
+  } else {
+    n = t / a.T;
+    start = n * a.T;
+    end = start + a.T;
+  }
+  const int len = __ldg(a.kv_lens + n);
+  const int p = len - (end - start) + (t - start);
+  bool ok = start >= 0 && start <= t && t < end && end <= a.Ttot && len >= 0 && len <= a.max_len;
+  if (ok && p < 0) return;
+  int page = 0;
+  if (ok) {
+    page = __ldg(a.table + (long long)n * a.max_pages + p / a.page_size);
+    ok = page >= 0 && page < a.n_pages;
+  }
+  if (!ok) {
+    if (a.flags) atomicOr(a.flags, kFlagBadSeqlens);
+    return;
+  }
+  const long long to = ((long long)page * a.page_size + p % a.page_size) * a.row_bytes + piece * 16;
+  const uint4 k = __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(a.k) +
+                                                        t * a.k_stride + piece * 16));
+  const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(a.v) +
+                                                        t * a.v_stride + piece * 16));
+  *reinterpret_cast<uint4 *>(static_cast<char *>(a.k_cache) + to) = k;
+  *reinterpret_cast<uint4 *>(static_cast<char *>(a.v_cache) + to) = v;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream) {
+  const long long pieces = (long long)a.Ttot * (a.row_bytes >> 4);
+  const long long blocks = (pieces + kThreads - 1) / kThreads;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  gdn_kv_append_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace gdn

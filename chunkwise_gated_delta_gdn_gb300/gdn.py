@@ -44,6 +44,8 @@ EXPORTED = ("gdn_version", "gdn_status_string", "gdn_chunk_fwd_workspace_bytes",
             "gdn_chunk_fwd_lockstep",
             "gdn_chunk_fwd_noalloc", "gdn_recurrent_fwd", "gdn_causal_conv1d_fwd",
             "gdn_l2norm_fwd", "gdn_rmsnorm_gated_fwd", "gdn_state_combine",
+            "gdn_attn_fwd_workspace_bytes", "gdn_attn_fwd",
+            "gdn_attn_paged_fwd_workspace_bytes", "gdn_attn_paged_fwd", "gdn_kv_cache_append",
             "gdn_selftest_wait", "gdn_read_device_flags")
 
 _lock = threading.Lock()
@@ -102,6 +104,18 @@ def load(path: Optional[str] = None):
         lib.gdn_rmsnorm_gated_fwd.restype = i32
         lib.gdn_state_combine.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp]
         lib.gdn_state_combine.restype = i32
+        lib.gdn_attn_fwd_workspace_bytes.argtypes = [i32] * 7
+        lib.gdn_attn_fwd_workspace_bytes.restype = sz
+        lib.gdn_attn_fwd.argtypes = [vp] * 6 + [i32] * 6 + [i64] * 3 + [f32, i32, vp, vp, sz, vp]
+        lib.gdn_attn_fwd.restype = i32
+        lib.gdn_attn_paged_fwd_workspace_bytes.argtypes = [i32] * 9
+        lib.gdn_attn_paged_fwd_workspace_bytes.restype = sz
+        lib.gdn_attn_paged_fwd.argtypes = ([vp] * 8 + [i32] * 6 + [i64] + [i32] * 3 +
+                                           [f32, i32, vp, vp, sz, vp])
+        lib.gdn_attn_paged_fwd.restype = i32
+        lib.gdn_kv_cache_append.argtypes = ([vp] * 7 + [i32] * 5 + [i64] * 2 + [i32] * 4 +
+                                            [vp, vp])
+        lib.gdn_kv_cache_append.restype = i32
         lib.gdn_selftest_wait.argtypes = [vp, ctypes.c_longlong, i32, vp]
         lib.gdn_selftest_wait.restype = i32
         lib.gdn_read_device_flags.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
@@ -406,6 +420,197 @@ def gdn_state_combine(M: torch.Tensor, S_in: torch.Tensor, S_seg: torch.Tensor, 
     if status != GDN_OK:
         raise GdnError(status, "gdn_state_combine")
     return out
+
+
+def _tokens(t: torch.Tensor, name: str, dev, dtype, B: int, T: int) -> int:
+    """Check a ``[B, T, heads, d]`` tensor whose tokens may be strided (a slice of a wider
+    projection); returns the elements from one token to the next."""
+    if t.device != dev or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} on {dev}")
+    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != T:
+        raise ValueError(f"{name} must be [{B}, {T}, heads, d]")
+    heads, d = t.shape[2], t.shape[3]
+    sb, st, sh, sd = t.stride()
+    if t.numel() == 0:
+        return heads * d
+    if T == 1:
+        st = sb if B > 1 else heads * d
+    if (d > 1 and sd != 1) or (heads > 1 and sh != d) or (B > 1 and T > 1 and sb != T * st):
+        raise ValueError(f"{name}: a token's heads must be contiguous and tokens evenly spaced")
+    return st
+
+
+def _lengths(cu_seqlens, B: int, dev) -> int:
+    """Number of sequences, with cu_seqlens checked."""
+    if cu_seqlens is None:
+        return B
+    _check(cu_seqlens, "cu_seqlens", dev)
+    if cu_seqlens.dtype != torch.int32:
+        raise TypeError("cu_seqlens must be int32")
+    return cu_seqlens.numel() - 1
+
+
+def _attn_buffers(q, o, lse, output_lse, flags, workspace, nbytes, dev):
+    """Check the buffers a caller passed and allocate the others (on the current stream);
+    returns (o, lse, workspace, its bytes)."""
+    for name, t in (("o", o), ("lse", lse), ("flags", flags), ("workspace", workspace)):
+        _check(t, name, dev)
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("o must match q in shape and dtype")
+    if lse is None:
+        if output_lse:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+    elif lse.shape != q.shape[:3] or lse.dtype != torch.float32:
+        raise ValueError("lse must be float32 [B, T, H]")
+    if flags is not None and (flags.element_size() != 4 or flags.numel() < 1):
+        raise TypeError("flags must hold at least one 4-byte element")
+    if workspace is not None:
+        nbytes = workspace.numel() * workspace.element_size()
+    elif nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return o, lse, workspace, nbytes
+
+
+def _cache(k_cache, v_cache, block_table, kv_lens, n_seqs, HKV, d, dtype, dev):
+    """Check a paged cache; returns (page_size, max_pages, n_pages)."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("block_table", block_table),
+                    ("kv_lens", kv_lens)):
+        _check(t, name, dev)
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise ValueError(f"k_cache and v_cache must be {dtype}")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[2:] != (HKV, d):
+        raise ValueError("k_cache and v_cache must be [n_pages, page_size, HKV, d]")
+    if block_table.dtype != torch.int32 or kv_lens.dtype != torch.int32:
+        raise TypeError("block_table and kv_lens must be int32")
+    if block_table.dim() != 2 or block_table.shape[0] != n_seqs or kv_lens.shape != (n_seqs,):
+        raise ValueError(f"block_table must be [{n_seqs}, max_pages], kv_lens [{n_seqs}]")
+    return k_cache.shape[1], block_table.shape[1], k_cache.shape[0]
+
+
+def gdn_attn_fwd_workspace_bytes(B: int, T: int, H: int, HKV: int, d: int, n_seqs: int,
+                                 dtype: int) -> int:
+    return int(load().gdn_attn_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, dtype))
+
+
+def gdn_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
+                 scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                 o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                 output_lse: bool = True, flags: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None
+                 ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Causal softmax attention over whole prompts; returns ``(o, lse)``.
+
+    q ``[B, T, H, d]``; k, v ``[B, T, HKV, d]`` (bf16 or fp32, d 64 or 128), possibly
+    slices of one projection's output; packed ``[1, Ttot, ..]`` with cu_seqlens
+    (int32 ``[N + 1]``).  lse ``[B, T, H]`` fp32 is the natural log of the softmax
+    denominator (None when not asked).
+    """
+    lib = load()
+    if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape or k.shape[3] != q.shape[3]:
+        raise ValueError("q [B, T, H, d] and k, v [B, T, HKV, d]: inconsistent shapes")
+    B, T, H, d = q.shape
+    HKV = k.shape[2]
+    dev, dt = q.device, _dtype_code(q.dtype)
+    qs, ks, vs = (_tokens(t, name, dev, q.dtype, B, T)
+                  for name, t in (("q", q), ("k", k), ("v", v)))
+    n_seqs = _lengths(cu_seqlens, B, dev)
+    nbytes = 0
+    if workspace is None:
+        nbytes = lib.gdn_attn_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, dt)
+    with torch.cuda.stream(stream):  # what is allocated here belongs to the stream it is used on
+        o, lse, workspace, nbytes = _attn_buffers(q, o, lse, output_lse, flags, workspace, nbytes,
+                                                  dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    status = lib.gdn_attn_fwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens), n_seqs, B, T, H, HKV, d,
+        qs, ks, vs, d ** -0.5 if scale is None else scale, dt, _ptr(flags), _ptr(workspace),
+        nbytes, stream.cuda_stream)
+    if status != GDN_OK:
+        raise GdnError(status, "gdn_attn_fwd")
+    return o, lse
+
+
+def gdn_attn_paged_fwd_workspace_bytes(B: int, T: int, H: int, HKV: int, d: int, n_seqs: int,
+                                       page_size: int, max_pages: int, dtype: int) -> int:
+    return int(load().gdn_attn_paged_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, page_size,
+                                                         max_pages, dtype))
+
+
+def gdn_attn_paged_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       block_table: torch.Tensor, kv_lens: torch.Tensor, *,
+                       scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                       o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                       output_lse: bool = True, flags: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None
+                       ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention of new tokens over a paged cache that already holds them
+    (:func:`gdn_kv_cache_append`); returns ``(o, lse)``.
+
+    q ``[B, T, H, d]`` (T = 1: the decode step) or packed ``[1, Ttot, H, d]`` with
+    cu_seqlens; k_cache, v_cache ``[n_pages, page_size, HKV, d]``; block_table int32
+    ``[N, max_pages]``; kv_lens int32 ``[N]``, new tokens included.
+    """
+    lib = load()
+    if q.dim() != 4 or k_cache.dim() != 4:
+        raise ValueError("q must be [B, T, H, d] and the caches [n_pages, page_size, HKV, d]")
+    B, T, H, d = q.shape
+    HKV = k_cache.shape[2]
+    dev, dt = q.device, _dtype_code(q.dtype)
+    qs = _tokens(q, "q", dev, q.dtype, B, T)
+    n_seqs = _lengths(cu_seqlens, B, dev)
+    page_size, max_pages, n_pages = _cache(k_cache, v_cache, block_table, kv_lens, n_seqs, HKV, d,
+                                           q.dtype, dev)
+    nbytes = 0
+    if workspace is None:
+        nbytes = lib.gdn_attn_paged_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, page_size,
+                                                        max_pages, dt)
+    with torch.cuda.stream(stream):  # what is allocated here belongs to the stream it is used on
+        o, lse, workspace, nbytes = _attn_buffers(q, o, lse, output_lse, flags, workspace, nbytes,
+                                                  dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    status = lib.gdn_attn_paged_fwd(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(kv_lens), _ptr(o),
+        _ptr(lse), _ptr(cu_seqlens), n_seqs, B, T, H, HKV, d, qs, page_size, max_pages, n_pages,
+        d ** -0.5 if scale is None else scale, dt, _ptr(flags), _ptr(workspace), nbytes,
+        stream.cuda_stream)
+    if status != GDN_OK:
+        raise GdnError(status, "gdn_attn_paged_fwd")
+    return o, lse
+
+
+def gdn_kv_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                        *, cu_seqlens: Optional[torch.Tensor] = None,
+                        flags: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Write the keys and values of new tokens (k, v ``[B, T, HKV, d]`` or packed) into the
+    pages, in place; kv_lens counts them already."""
+    lib = load()
+    if k.dim() != 4 or v.shape != k.shape:
+        raise ValueError("k and v must be [B, T, HKV, d]")
+    B, T, HKV, d = k.shape
+    dev, dt = k.device, _dtype_code(k.dtype)
+    ks, vs = (_tokens(t, name, dev, k.dtype, B, T) for name, t in (("k", k), ("v", v)))
+    n_seqs = _lengths(cu_seqlens, B, dev)
+    page_size, max_pages, n_pages = _cache(k_cache, v_cache, block_table, kv_lens, n_seqs, HKV, d,
+                                           k.dtype, dev)
+    _check(flags, "flags", dev)
+    if flags is not None and (flags.element_size() != 4 or flags.numel() < 1):
+        raise TypeError("flags must hold at least one 4-byte element")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    status = lib.gdn_kv_cache_append(
+        _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(kv_lens),
+        _ptr(cu_seqlens), n_seqs, B, T, HKV, d, ks, vs, page_size, max_pages, n_pages, dt,
+        _ptr(flags), stream.cuda_stream)
+    if status != GDN_OK:
+        raise GdnError(status, "gdn_kv_cache_append")
 
 
 def gdn_selftest_wait(flags: torch.Tensor, budget_cycles: int, complete: bool, *,

@@ -343,6 +343,91 @@ GDN_API gdn_status gdn_state_combine(const float *M, const float *S_in, const fl
                                      gdn_stream_t stream);
 
 /*
+ * Softmax attention, for the full-attention layers that stand between
+ * gated-delta layers in a stack: over a whole prompt (gdn_attn_fwd), over a
+ * paged key/value cache (gdn_attn_paged_fwd: one new token per sequence is
+ * the decode step, several are a prompt's next chunk), and the write of new
+ * keys and values into the pages (gdn_kv_cache_append).  The pages of the
+ * method have no counterpart.
+ *
+ * A sequence has L keys, the nq new tokens among them as the last ones (a
+ * whole prompt: L = nq).  New token t is at position p = L - nq + t and sees
+ * the keys j <= p; query head h reads key/value head h / (H / HKV):
+ *     s_j = scale * q.k_j,   m = max_j s_j,   l = sum_j e^(s_j - m),
+ *     o = sum_j e^(s_j - m) v_j / l,          lse = m + ln l
+ * A token that sees no key (p < 0: fewer keys than new tokens, as in an idle
+ * slot of a padded decode batch with L = 0) gets o = 0 and lse = -inf.
+ *
+ * Common arguments ("dt" = dtype; d in {64, 128}; H a multiple of HKV):
+ *   q, o        [B, T, H, d]   dt; T new tokens per sequence, or packed with
+ *               cu_seqlens [n_seqs + 1] int32 (then B == 1 and T is their total)
+ *   k, v        [B, T, HKV, d] dt, the keys and values of the new tokens
+ *   q_stride, k_stride, v_stride   elements from one token to the next (its
+ *               heads contiguous), so that q, k and v may be slices of one
+ *               projection's output; a multiple of 16 bytes, at least the row.
+ *               Sequence b of a plain batch begins b * T tokens in.
+ *   lse         [B, T, H] fp32, or NULL
+ *   k_cache, v_cache   [n_pages, page_size, HKV, d] dt; page_size a multiple
+ *               of 16
+ *   block_table [n_seqs, max_pages] int32: page of positions
+ *               [i * page_size, (i + 1) * page_size) of a sequence at column i.
+ *               Entries past the last page in use are not read.
+ *   kv_lens     [n_seqs] int32: L of each sequence, 0 <= L <= max_pages *
+ *               page_size, new tokens included
+ *   scale       finite and > 0 (d^-0.5 is usual)
+ *   flags       as for gdn_recurrent_fwd.  BAD_SEQLENS: cu_seqlens, kv_lens or
+ *               a page number out of range; such a sequence is skipped, and a
+ *               bad page reads as zeros (gdn_kv_cache_append leaves its tokens
+ *               out).  NONFINITE: a non-finite value was written to o.
+ *   workspace   at least the bytes of the matching query, 256-byte aligned,
+ *               not shared by two calls in flight; contents need no
+ *               preparation and mean nothing afterwards.
+ * Device pointers are 16-byte aligned (lse, cu_seqlens, block_table and
+ * kv_lens: 4-byte).  No output may overlap an input or another output.
+ *
+ * What lies in the cache beyond L, and in other sequences, does not reach a
+ * result, whatever its bits.  Within a sequence a non-finite v at a later
+ * position can turn the outputs of earlier tokens of the same 128-key tile
+ * into NaN (0 * inf).
+ *
+ * Numerics: scores, row maximum and sum, and the output's accumulation in
+ * fp32; o rounded once to dtype.  bf16: tensor-core products of bf16 operands;
+ * the weights e^(s - m) are rounded to bf16 for their product with v, their
+ * sum is not.  fp32: split-tf32 products (about 21 mantissa bits).  Results
+ * are the same from call to call, bit for bit.
+ */
+GDN_API size_t gdn_attn_fwd_workspace_bytes(int B, int T, int H, int HKV, int d, int n_seqs,
+                                            int dtype);
+GDN_API gdn_status gdn_attn_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
+                                const int32_t *cu_seqlens, int n_seqs, int B, int T, int H,
+                                int HKV, int d, int64_t q_stride, int64_t k_stride,
+                                int64_t v_stride, float scale, int dtype, uint32_t *flags,
+                                void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+GDN_API size_t gdn_attn_paged_fwd_workspace_bytes(int B, int T, int H, int HKV, int d,
+                                                  int n_seqs, int page_size, int max_pages,
+                                                  int dtype);
+GDN_API gdn_status gdn_attn_paged_fwd(const void *q, const void *k_cache, const void *v_cache,
+                                      const int32_t *block_table, const int32_t *kv_lens, void *o,
+                                      float *lse, const int32_t *cu_seqlens, int n_seqs, int B,
+                                      int T, int H, int HKV, int d, int64_t q_stride,
+                                      int page_size, int max_pages, int n_pages, float scale,
+                                      int dtype, uint32_t *flags, void *workspace,
+                                      size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * gdn_kv_cache_append -- k and v of the new tokens into the pages, each at its
+ * position; the rest of the cache is left as it is.  A token at a negative
+ * position is left out.  kv_lens counts the new tokens already.
+ */
+GDN_API gdn_status gdn_kv_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,
+                                       const int32_t *block_table, const int32_t *kv_lens,
+                                       const int32_t *cu_seqlens, int n_seqs, int B, int T,
+                                       int HKV, int d, int64_t k_stride, int64_t v_stride,
+                                       int page_size, int max_pages, int n_pages, int dtype,
+                                       uint32_t *flags, gdn_stream_t stream);
+
+/*
  * gdn_selftest_wait -- exercise the bounded wait that every mbarrier wait of
  * the tensor-core kernels uses, with no fault and no hang.  Those waits give
  * up after a clock budget (about two seconds), set GDN_FLAG_TIMEOUT and let

@@ -1,0 +1,151 @@
+"""The attention kernels' work plan on the CPU: the host compiles the plan that
+the kernels use (csrc/gdn_attn.cuh) into a program that deals random batches to
+random numbers of blocks and checks that every key a row may see is covered
+once, that pieces of a unit get distinct slots and that the merge finds exactly
+them."""
+from __future__ import annotations
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from chunkwise_gated_delta_gdn_gb300 import build as cuda_build
+
+PROGRAM = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <map>
+#include <set>
+#include <tuple>
+#include <vector>
+
+#include "gdn_attn.cuh"
+
+using namespace gdn;
+
+#define CHECK(x) do { if (!(x)) { std::printf("line %d: %s\n", __LINE__, #x); return false; } } while (0)
+
+static unsigned rnd_state;
+static int rnd(int lo, int hi) {  // uniform over lo..hi
+  rnd_state = rnd_state * 1664525u + 1013904223u;
+  return lo + (int)((rnd_state >> 8) % (unsigned)(hi - lo + 1));
+}
+
+template <class S>
+bool one(const std::vector<int> &q, const std::vector<int> &kv, int H, int HKV, int blocks, int min_cost) {
+  std::vector<int32_t> cu(1, 0), lens(kv.begin(), kv.end());
+  for (int n : q) cu.push_back(cu.back() + n);
+  AttnArgs a{};
+  a.cu = cu.data(); a.kv_lens = lens.data(); a.n_seqs = (int)q.size(); a.Ttot = cu.back();
+  a.H = H; a.HKV = HKV; a.max_len = 1 << 30; a.min_cost = min_cost;
+  const AttnPlan<S> plan(H, HKV);
+  CHECK(H % plan.gp == 0 && plan.G % plan.gp == 0 && plan.gp * plan.tok == S::kRows);
+  long long total = 0;
+  std::vector<long long> seq0;
+  for (int n = 0; n < a.n_seqs; n++) {
+    bool bad;
+    seq0.push_back(total);
+    total += plan.cost(attn_seq(a, n, bad));
+    CHECK(!bad);
+  }
+  const long long per = attn_per<S>(a, total, blocks);
+  CHECK(per * blocks >= total);
+  std::map<std::pair<int, int>, std::vector<int>> seen;  // (row, head) -> tiles
+  std::map<std::tuple<int, int>, std::vector<int>> pieces;  // (row0, head0) -> slots in order
+  std::map<std::tuple<int, int>, AttnUnit> units;
+  std::set<int> slots;
+  for (int b = 0; b < blocks; b++) {
+    AttnStart st{};
+    st.per = per; st.total = total; st.seq = a.n_seqs;
+    for (int n = 0; n < a.n_seqs; n++) {
+      bool bad;
+      const long long c = plan.cost(attn_seq(a, n, bad));
+      if (b * per >= seq0[n] && b * per < seq0[n] + c) { st.seq = n; st.seq0 = seq0[n]; }
+    }
+    AttnWalk<S> walk(a, plan, st, b);
+    AttnUnit u;
+    while (walk.next(u)) {
+      CHECK(0 <= u.t0 && u.t0 < u.t1 && u.t1 <= u.nt);
+      CHECK(u.n_tok > 0 && u.n_tok * u.gp <= S::kRows && u.kvh == u.head0 / plan.G);
+      CHECK(u.row0 >= cu[u.seq] && u.row0 + u.n_tok <= cu[u.seq + 1]);
+      CHECK(u.len == kv[u.seq] && u.pos0 == kv[u.seq] - q[u.seq] + u.row0 - cu[u.seq]);
+      CHECK((long long)u.nt * S::kTile >= u.pos0 + u.n_tok);
+      CHECK((u.slot < 0) == (u.t0 == 0 && u.t1 == u.nt));
+      if (u.slot >= 0) {
+        CHECK(u.slot / 2 == b && slots.insert(u.slot).second);
+        pieces[{u.row0, u.head0}].push_back(u.slot);
+      }
+      units[{u.row0, u.head0}] = u;
+      for (int t = 0; t < u.n_tok; t++)
+        for (int g = 0; g < u.gp; g++)
+          for (int k = u.t0; k < u.t1; k++) seen[{u.row0 + t, u.head0 + g}].push_back(k);
+    }
+  }
+  for (int n = 0; n < a.n_seqs; n++)
+    for (int t = 0; t < q[n]; t++)
+      for (int h = 0; h < H; h++) {
+        const std::vector<int> &v = seen[{cu[n] + t, h}];
+        const int visible = kv[n] - q[n] + t + 1;
+        CHECK(!v.empty() && (long long)v.size() * S::kTile >= visible);
+        for (size_t i = 0; i < v.size(); i++) CHECK(v[i] == (int)i);  // in order, each once
+      }
+  // the merge, border by border
+  std::set<std::tuple<int, int>> merged;
+  for (int i = 1; i < blocks; i++) {
+    const long long c = i * per;
+    if (c >= total) break;
+    int n = 0;
+    while (n + 1 < a.n_seqs && seq0[n + 1] <= c) n++;
+    bool bad;
+    const AttnSeq s = attn_seq(a, n, bad);
+    if (plan.cost(s) == 0) continue;  // cannot hold a border
+    AttnUnit u;
+    const long long u0 = seq0[n] + plan.find(s, n, c - seq0[n], u);
+    int last;
+    if (!attn_merge(u0, plan.unit_cost(s), u.nt, i, per, last)) continue;
+    CHECK(merged.insert({u.row0, u.head0}).second);
+    std::vector<int> want{2 * (i - 1) + 1};
+    for (int b = i; b <= last; b++) want.push_back(2 * b);
+    CHECK((pieces[{u.row0, u.head0}] == want));
+  }
+  CHECK(merged.size() == pieces.size());
+  return true;
+}
+
+int main() {
+  for (int trial = 0; trial < 600; trial++) {
+    rnd_state = 7u + 977u * trial;
+    const int hkv = rnd(1, 4), g = rnd(1, 4) == 1 ? rnd(1, 20) : 1 << rnd(0, 4);
+    std::vector<int> q, kv;
+    for (int n = rnd(1, 12); n > 0; n--) {
+      const int kind = rnd(0, 5);
+      const int nq = kind == 0 ? 0 : kind < 3 ? 1 : kind < 5 ? rnd(1, 40) : rnd(1, 700);
+      q.push_back(nq);
+      kv.push_back(rnd(0, 9) == 0 ? rnd(0, nq) : nq + rnd(0, rnd(0, 1) ? 100 : 1500));
+    }
+    const int blocks = rnd(0, 1) ? rnd(1, 9) : rnd(10, 200), min_cost = 2 * rnd(1, 4);
+    if (!one<AttnShape<64, 64, 64, 1>>(q, kv, hkv * g, hkv, blocks, min_cost) ||
+        !one<AttnShape<256, 128, 128, 2>>(q, kv, hkv * g, hkv, blocks, min_cost)) {
+      std::printf("trial %d: hkv %d g %d blocks %d\n", trial, hkv, g, blocks);
+      return 1;
+    }
+  }
+  std::printf("ok\n");
+  return 0;
+}
+"""
+
+
+def test_plan_covers_every_visible_key_once(tmp_path):
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("no nvcc")
+    src = tmp_path / "plan.cu"
+    src.write_text(PROGRAM)
+    exe = tmp_path / "plan"
+    subprocess.run([nvcc, *cuda_build.ARCH, "-O1", "-std=c++17", "-I", cuda_build.CSRC, "-I",
+                    cuda_build.INCLUDE, str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
