@@ -1,5 +1,6 @@
 // gdn_attn.cu -- causal softmax attention with grouped heads, over a whole
-// prompt or over a paged cache, and the merge of partial results.
+// prompt or over a paged cache: the fp32 kernel, the merge of partial results
+// (both types) and the launch (bf16: gdn_attn_tc.cu).
 //
 //   s_j = scale q.k_j (j <= p), m = max_j s_j, l = sum_j e^(s_j - m),
 //   o = sum_j e^(s_j - m) v_j / l,  lse = m + ln l
@@ -15,9 +16,10 @@
 namespace gdn {
 namespace {
 
-// 64 rows x 64 keys per step: four warps of 16 rows, the operands in shared
+// fp32: 64 rows x 64 keys per step: four warps of 16 rows, the operands in shared
 // memory as fp32, both products split-tf32 on mma.sync.
 using WarpShape = AttnShape<64, 64, 64, 1>;
+using TcShape = AttnShape<256, 128, 128, 2>;  // of the bf16 kernel (gdn_attn_tc.cu)
 constexpr int kThreads = 128;
 
 template <int D>
@@ -30,45 +32,36 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 // c += A B for one 16 x 8 tile, k = 8: the three products of the two halves
-template <bool BX>
 __device__ __forceinline__ void mma3(float (&c)[4], const uint32_t (&ah)[4],
                                      const uint32_t (&al)[4], float b0, float b1) {
   uint32_t h0, l0, h1, l1;
   split_tf32(b0, h0, l0);
   split_tf32(b1, h1, l1);
   mma1688_tf32(c, al, h0, h1);
-  if (!BX) mma1688_tf32(c, ah, l0, l1);
+  mma1688_tf32(c, ah, l0, l1);
   mma1688_tf32(c, ah, h0, h1);
 }
 
-template <bool BF16>
-__device__ __forceinline__ void load8(float (&x)[8], const typename Elem<BF16>::T *p) {
-  if constexpr (BF16) {
-    const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(p));
-    const __nv_bfloat16 *b = reinterpret_cast<const __nv_bfloat16 *>(&raw);
-#pragma unroll
-    for (int e = 0; e < 8; e++) x[e] = __bfloat162float(b[e]);
-  } else {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4 *>(p + 4));
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
+__device__ __forceinline__ void load8(float (&x)[8], const float *p) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4 *>(p + 4));
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 __device__ __forceinline__ void put8(float *d, const float (&x)[8]) {
   *reinterpret_cast<float4 *>(d) = make_float4(x[0], x[1], x[2], x[3]);
   *reinterpret_cast<float4 *>(d + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-template <int D, bool BF16>
+template <int D>
 __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs a) {
-  using E = Elem<BF16>;
   constexpr int kS = D + 4;  // row stride in floats: fragment reads hit 32 banks
   extern __shared__ float smem[];
   float *Qs = smem, *Ks = Qs + 64 * kS, *Vs = Ks + 64 * kS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
   const AttnPlan<WarpShape> plan(a.H, a.HKV);
-  const AttnStart st = attn_start<WarpShape, kThreads>(a, plan, blockIdx.x, gridDim.x);
+  __shared__ AttnStartScratch<kThreads> scratch;
+  const AttnStart st = attn_start<WarpShape, kThreads>(a, plan, blockIdx.x, gridDim.x, scratch);
   AttnWalk<WarpShape> walk(a, plan, st, blockIdx.x);
   AttnUnit u;
   while (walk.next(u)) {
@@ -77,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs 
       const int r = i / (D / 8), c = (i % (D / 8)) * 8, t = r / u.gp;
       float x[8] = {};
       if (t < u.n_tok)
-        load8<BF16>(x, static_cast<const typename E::T *>(a.q) + (long long)(u.row0 + t) * a.q_stride +
+        load8(x, static_cast<const float *>(a.q) + (long long)(u.row0 + t) * a.q_stride +
                            (u.head0 + r % u.gp) * D + c);
       put8(Qs + r * kS + c, x);
     }
@@ -95,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs 
         const int key = key0 + r;
         float x[8] = {};
         if (key < u.len) {
-          const typename E::T *p = static_cast<const typename E::T *>(is_v ? a.v : a.k);
+          const float *p = static_cast<const float *>(is_v ? a.v : a.k);
           bool ok = true;
           if (a.table) {
             const int page = __ldg(a.table + (long long)u.seq * a.max_pages + key / a.page_size);
@@ -106,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs 
             // a prompt's keys are its own tokens
             p += (long long)(u.row0 - u.pos0 + key) * (is_v ? a.v_stride : a.k_stride) + u.kvh * D;
           }
-          if (ok) load8<BF16>(x, p + c);
+          if (ok) load8(x, p + c);
         }
         put8((is_v ? Vs : Ks) + r * kS + c, x);
       }
@@ -123,11 +116,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs 
 #pragma unroll
         for (int n = 0; n < 8; n++) {
           const float *b = Ks + (n * 8 + gq) * kS + k + tq;
-          if constexpr (BF16) {  // bf16 inputs are exact in tf32
-            mma1688_tf32(s[n], ah, __float_as_uint(b[0]), __float_as_uint(b[4]));
-          } else {
-            mma3<false>(s[n], ah, al, b[0], b[4]);
-          }
+          mma3(s[n], ah, al, b[0], b[4]);
         }
       }
       // running maximum and sum; element e of a tile: row e / 2, key 2 tq + e % 2
@@ -174,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs 
         split_tf32(s[n][3], ah[3], al[3]);
         const float *b = Vs + (n * 8 + 2 * tq) * kS + gq;
 #pragma unroll
-        for (int d = 0; d < D / 8; d++) mma3<BF16>(o[d], ah, al, b[d * 8], b[kS + d * 8]);
+        for (int d = 0; d < D / 8; d++) mma3(o[d], ah, al, b[d * 8], b[kS + d * 8]);
       }
     }
     bool finite = true;
@@ -199,11 +188,8 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs 
       for (int n = 0; n < D / 8; n++) {
         const float x = o[n][2 * h] * inv, y = o[n][2 * h + 1] * inv;
         finite &= isfinite(x) && isfinite(y);
-        typename E::T *p = static_cast<typename E::T *>(a.o) + at * D + n * 8 + 2 * tq;
-        if constexpr (BF16)
-          *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
-        else
-          *reinterpret_cast<float2 *>(p) = make_float2(x, y);
+        *reinterpret_cast<float2 *>(static_cast<float *>(a.o) + at * D + n * 8 + 2 * tq) =
+            make_float2(x, y);
       }
       if (a.lse && tq == 0) a.lse[at] = l[h] == 0.f ? -CUDART_INF_F : (m[h] + log2f(l[h])) * 0.69314718056f;
     }
@@ -220,7 +206,8 @@ template <class S, int D, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const AttnArgs a, int n_blocks) {
   const AttnPlan<S> plan(a.H, a.HKV);
   const int first = blockIdx.x;
-  const AttnStart st = attn_start<S, kMergeThreads>(a, plan, first + 1, n_blocks);
+  __shared__ AttnStartScratch<kMergeThreads> scratch;
+  const AttnStart st = attn_start<S, kMergeThreads>(a, plan, first + 1, n_blocks, scratch);
   const long long c = (first + 1) * st.per;
   if (st.seq >= a.n_seqs || c >= st.total) return;
   bool bad;
@@ -277,28 +264,41 @@ int sm_count() {
   return n;
 }
 
-template <int D, bool BF16>
-cudaError_t launch(AttnArgs a, cudaStream_t stream) {
-  a.min_cost = 4;
-  const int blocks = attn_blocks(BF16 ? 1 : 0, D);
-  cudaError_t e = cudaFuncSetAttribute(gdn_attn_warp_kernel<D, BF16>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+template <class S, int D, bool BF16>
+cudaError_t merge(const AttnArgs &a, int blocks, cudaStream_t stream) {
+  gdn_attn_merge_kernel<S, D, BF16><<<dim3(blocks - 1, 4), kMergeThreads, 0, stream>>>(a, blocks);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs &a, int blocks, cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      gdn_attn_warp_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
   if (e != cudaSuccess) return e;
-  gdn_attn_warp_kernel<D, BF16><<<blocks, kThreads, smem_bytes<D>(), stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  gdn_attn_merge_kernel<WarpShape, D, BF16><<<dim3(blocks - 1, 4), kMergeThreads, 0, stream>>>(a, blocks);
+  gdn_attn_warp_kernel<D><<<blocks, kThreads, smem_bytes<D>(), stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-int attn_blocks(int, int d) { return sm_count() * (d == 64 ? 4 : 2); }
-int attn_part_rows(int) { return WarpShape::kRows; }
+int attn_blocks(int dtype, int d) { return dtype ? sm_count() : sm_count() * (d == 64 ? 4 : 2); }
+int attn_part_rows(int dtype) { return dtype ? TcShape::kRows : WarpShape::kRows; }
 
-cudaError_t launch_attn(const AttnArgs &a, int d, int dtype, cudaStream_t stream) {
-  if (d == 64) return dtype ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
-  if (d == 128) return dtype ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
-  return cudaErrorInvalidValue;
+cudaError_t launch_attn(const AttnArgs &args, int d, int dtype, cudaStream_t stream) {
+  if (d != 64 && d != 128) return cudaErrorInvalidValue;
+  AttnArgs a = args;
+  a.min_cost = 4;
+  const int blocks = attn_blocks(dtype, d);
+  cudaError_t e;
+  if (dtype) {
+    if ((e = launch_attn_tc(a, d, blocks, stream)) != cudaSuccess) return e;
+    return d == 64 ? merge<TcShape, 64, true>(a, blocks, stream)
+                   : merge<TcShape, 128, true>(a, blocks, stream);
+  }
+  if ((e = d == 64 ? launch<64>(a, blocks, stream) : launch<128>(a, blocks, stream)) != cudaSuccess)
+    return e;
+  return d == 64 ? merge<WarpShape, 64, false>(a, blocks, stream)
+                 : merge<WarpShape, 128, false>(a, blocks, stream);
 }
 
 }  // namespace gdn

@@ -8,7 +8,7 @@
 // `gp` heads of one token next to each other.
 //  * packed: nq * G <= kPack rows (G = H / HKV): one unit per key/value head
 //    holds all of them (gp = G), so a decode step reads each key once.
-//  * otherwise gp is the largest power of two that divides G (at most kRows)
+//  * otherwise gp is the largest power of two that divides G (at most kPack)
 //    and a unit is kRows rows: kRows / gp tokens of gp heads.
 // A unit covers the key tiles 0 .. nt-1 of kTile keys up to its last row's
 // position.  Tiles are numbered through all units and sequences, and block i of
@@ -102,7 +102,7 @@ struct AttnPlan {
     HKV = hkv;
     G = H / hkv;
     gp = G & -G;
-    if (gp > S::kRows) gp = S::kRows;
+    if (gp > S::kPack) gp = S::kPack;
     tok = S::kRows / gp;
     groups = H / gp;
   }
@@ -215,12 +215,18 @@ struct AttnStart {
 
 // Every thread of the block calls this (it synchronises the block).  Finds the
 // start of cost block * per; seq = n_seqs when the block has no work.
+template <int THREADS>
+struct AttnStartScratch {
+  long long warp_sum[THREADS / 32];
+  AttnStart out;
+};
 template <class S, int THREADS>
 __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, const AttnPlan<S> &plan,
-                                                long long block, int n_blocks) {
+                                                long long block, int n_blocks,
+                                                AttnStartScratch<THREADS> &scratch) {
   constexpr int kWarps = THREADS / 32;
-  __shared__ long long warp_sum[kWarps];
-  __shared__ AttnStart out;
+  long long *warp_sum = scratch.warp_sum;
+  AttnStart &out = scratch.out;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunk = (a.n_seqs + THREADS - 1) / THREADS;
   const int lo = min(tid * chunk, a.n_seqs), hi = min(lo + chunk, a.n_seqs);

@@ -213,11 +213,17 @@ cudaError_t launch_conv1d(const ConvArgs &a, int width, int activation, int dtyp
                           cudaStream_t stream);
 cudaError_t launch_rownorm(const RowNormArgs &a, int dim, int kind, int dtype,
                            cudaStream_t stream);
+// tensor map of a bf16 array (dims innermost first, strides in bytes from the
+// second dimension on), 128-byte swizzle; false when the driver refuses
+bool encode_bf16_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
+                     const uint64_t *strides, const uint32_t *box);
 // attention: blocks that the launch uses (its partial results are sized by
 // them) and rows of one partial result; d 64 or 128, dtype 0 = fp32, 1 = bf16
+// (bf16: tcgen05, gdn_attn_tc.cu; fp32: gdn_attn.cu)
 int attn_blocks(int dtype, int d);
 int attn_part_rows(int dtype);
 cudaError_t launch_attn(const AttnArgs &a, int d, int dtype, cudaStream_t stream);
+cudaError_t launch_attn_tc(AttnArgs a, int d, int blocks, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream);
 // S_out = M S_in + S_seg, per state
 cudaError_t launch_state_combine(const TransferArgs &a, cudaStream_t stream);
