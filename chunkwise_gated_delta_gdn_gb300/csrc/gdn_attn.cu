@@ -18,8 +18,8 @@ namespace {
 
 // fp32: 64 rows x 64 keys per step: four warps of 16 rows, the operands in shared
 // memory as fp32, both products split-tf32 on mma.sync.
-using WarpShape = AttnShape<64, 64, 64, 1>;
-using TcShape = AttnShape<256, 128, 128, 2>;  // of the bf16 kernel (gdn_attn_tc.cu)
+using WarpShape = AttnShape<64, 64, 64, 1, 1>;
+using TcShape = AttnShape<256, 128, 128, 2, 4>;  // of the bf16 kernel (gdn_attn_tc.cu)
 constexpr int kThreads = 128;
 
 template <int D>
@@ -59,9 +59,8 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs 
   extern __shared__ float smem[];
   float *Qs = smem, *Ks = Qs + 64 * kS, *Vs = Ks + 64 * kS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
-  const AttnPlan<WarpShape> plan(a.H, a.HKV);
-  __shared__ AttnStartScratch<kThreads> scratch;
-  const AttnStart st = attn_start<WarpShape, kThreads>(a, plan, blockIdx.x, gridDim.x, scratch);
+  AttnPlan<WarpShape> plan(a.H, a.HKV);
+  const AttnStart st = attn_start(a, plan, blockIdx.x, gridDim.x);  // each warp for itself
   AttnWalk<WarpShape> walk(a, plan, st, blockIdx.x);
   AttnUnit u;
   while (walk.next(u)) {
@@ -204,19 +203,17 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs 
 constexpr int kMergeThreads = 256;
 template <class S, int D, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const AttnArgs a, int n_blocks) {
-  const AttnPlan<S> plan(a.H, a.HKV);
+  AttnPlan<S> plan(a.H, a.HKV);
   const int first = blockIdx.x;
-  __shared__ AttnStartScratch<kMergeThreads> scratch;
-  const AttnStart st = attn_start<S, kMergeThreads>(a, plan, first + 1, n_blocks, scratch);
-  const long long c = (first + 1) * st.per;
-  if (st.seq >= a.n_seqs || c >= st.total) return;
+  const AttnStart st = attn_start(a, plan, first + 1, n_blocks);  // each warp for itself
+  if (st.seq >= a.n_seqs) return;
+  const long long c = (first + 1) * plan.per;
   bool bad;
   const AttnSeq s = attn_seq(a, st.seq, bad);
   AttnUnit u;
   const long long u0 = st.seq0 + plan.find(s, st.seq, c - st.seq0, u);
-  const int w = plan.unit_cost(s);
   int last;
-  if (!attn_merge(u0, w, u.nt, first + 1, st.per, last)) return;
+  if (!plan.merges(s, u0, u.nt, first + 1, last)) return;
   bool finite = true;
   // work items (row, four columns) in an order that gives a warp adjacent rows
   const int rows = min(u.n_tok * u.gp, S::kRows);
@@ -284,10 +281,8 @@ cudaError_t launch(const AttnArgs &a, int blocks, cudaStream_t stream) {
 int attn_blocks(int dtype, int d) { return dtype ? sm_count() : sm_count() * (d == 64 ? 4 : 2); }
 int attn_part_rows(int dtype) { return dtype ? TcShape::kRows : WarpShape::kRows; }
 
-cudaError_t launch_attn(const AttnArgs &args, int d, int dtype, cudaStream_t stream) {
+cudaError_t launch_attn(const AttnArgs &a, int d, int dtype, cudaStream_t stream) {
   if (d != 64 && d != 128) return cudaErrorInvalidValue;
-  AttnArgs a = args;
-  a.min_cost = 4;
   const int blocks = attn_blocks(dtype, d);
   cudaError_t e;
   if (dtype) {

@@ -11,14 +11,20 @@
 //  * otherwise gp is the largest power of two that divides G (at most kPack)
 //    and a unit is kRows rows: kRows / gp tokens of gp heads.
 // A unit covers the key tiles 0 .. nt-1 of kTile keys up to its last row's
-// position.  Tiles are numbered through all units and sequences, and block i of
-// the grid takes the cost range [i per, (i+1) per): equal shares whatever the
-// lengths, so one long sequence next to many short ones, a causal triangle and
-// a single token over a long cache all fill the GPU.  A unit cut by a range's
-// border leaves partial results (unnormalised output, row maximum and sum) that
-// the merge kernel joins in the order of the blocks, so results do not depend
-// on timing.  The plan depends on lengths that only the device knows (no
-// synchronisation), so every block computes its own range from them.
+// position.  Its tiles are grouped into grains of 2^shift tiles; every unit
+// costs `over` plus its grains (times kWide for an unpacked unit), costs are
+// numbered through all units and sequences, and block i of the grid takes the
+// range [i per, (i+1) per).
+//  * A call with little work takes the smallest grain at which there are no
+//    more grains than blocks, and each block one grain: nothing waits behind
+//    another unit, and no piece is smaller than kMinGrain tiles.
+//  * Otherwise grains are single tiles and ranges equal shares of the cost,
+//    whatever the lengths: one long sequence next to many short ones and a
+//    causal triangle fill the GPU alike.
+// A unit cut by a range's border leaves partial results (unnormalised output,
+// row maximum and sum) that the merge kernel joins in the order of the blocks,
+// so results do not depend on timing.  The plan depends on lengths that only
+// the device knows (no synchronisation), so every block computes it by itself.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -30,20 +36,14 @@
 namespace gdn {
 
 // Shape of a unit: rows, rows of a packed unit, keys per tile, cost of one
-// tile of an unpacked unit (a packed unit's tile costs 1).
-template <int ROWS, int PACK, int TILE, int WIDE>
+// tile of an unpacked unit (a packed unit's tile costs 1), cost of a unit's
+// own start and end.
+template <int ROWS, int PACK, int TILE, int WIDE, int OVER>
 struct AttnShape {
-  static constexpr int kRows = ROWS, kPack = PACK, kTile = TILE, kWide = WIDE;
+  static constexpr int kRows = ROWS, kPack = PACK, kTile = TILE, kWide = WIDE, kOver = OVER;
 };
-
-// Partial results of one block: two slots, one for a unit that began in an
-// earlier block and one for a unit that goes on in a later one.
-//   o  [slot][d/4][row] float4: unnormalised output
-//   ml [slot][row] float2: row maximum (log2 units) and sum
-struct AttnPart {
-  float4 *o;
-  float2 *ml;
-};
+constexpr int kMinGrain = 2;   // log2 of the smallest grain of a small call
+constexpr int kMaxGrain = 6;   // log2 of the largest one that is tried
 
 struct AttnSeq {
   int q0, nq;   // first token row and number of new tokens
@@ -92,54 +92,88 @@ __host__ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &a, int n, b
   return s;
 }
 
+// a / b for a >= 0, b > 0; in 32 bits where that is enough
+__host__ __device__ __forceinline__ long long attn_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 template <class S>
 struct AttnPlan {
-  static constexpr int kTile = S::kTile;
-
-  int G, HKV, gp, tok, groups;  // gp, tok: heads and tokens of an unpacked unit
+  int G, HKV, groups;
+  int gp, tok_log;     // heads and log2 of the tokens of an unpacked unit
+  int shift;           // log2 of the grain, in tiles
+  int wide, over;      // cost of an unpacked unit's grain, and of a unit
+  long long per;       // cost of a block's range
 
   __host__ __device__ AttnPlan(int H, int hkv) {
     HKV = hkv;
     G = H / hkv;
     gp = G & -G;
     if (gp > S::kPack) gp = S::kPack;
-    tok = S::kRows / gp;
+    tok_log = 0;
+    while ((gp << tok_log) < S::kRows) tok_log++;
     groups = H / gp;
+    stream(1);
+  }
+  // equal shares of single tiles / one grain per block
+  __host__ __device__ void stream(long long p) {
+    shift = 0;
+    wide = S::kWide;
+    over = S::kOver;
+    per = p;
+  }
+  __host__ __device__ void grains(int log) {
+    shift = log;
+    wide = 1;
+    over = 0;
+    per = 1;
+  }
+
+  __host__ __device__ bool packed(const AttnSeq &s) const {
+    return G <= S::kPack && s.nq * (long long)G <= S::kPack;
+  }
+  __host__ __device__ int token_tiles(const AttnSeq &s) const {
+    return (s.nq + (1 << tok_log) - 1) >> tok_log;
   }
   __host__ __device__ static int tiles(int keys) {
-    return keys <= kTile ? 1 : (keys + kTile - 1) / kTile;
+    return keys <= S::kTile ? 1 : (int)(((unsigned)keys + S::kTile - 1) / S::kTile);
   }
-  __host__ __device__ bool packed(const AttnSeq &s) const {
-    return G <= S::kPack && s.nq <= S::kPack / G;
+  __host__ __device__ int grains_of(int keys) const {
+    return (tiles(keys) + (1 << shift) - 1) >> shift;
   }
-  __host__ __device__ int token_tiles(const AttnSeq &s) const { return (s.nq + tok - 1) / tok; }
-
-  // sum over i < n of floor(i / r)
-  __host__ __device__ static long long floors(long long n, long long r) {
-    const long long q = n / r;
-    return r * (q * (q - 1) / 2) + q * (n - q * r);
+  __host__ __device__ static int tile_log() {
+    int l = 0;
+    while ((1 << l) < S::kTile) l++;
+    return l;
   }
-  // key tiles of the first x token tiles (all of them full):
-  // sum over i < x of ceil((base + (i + 1) tok) / kTile)
+  // sum over i < n of floor(i / 2^r)
+  __host__ __device__ static long long floors(long long n, int r) {
+    const long long q = n >> r;
+    return ((q * (q - 1) / 2) << r) + q * (n - (q << r));
+  }
+  // grains of the first x token tiles (all of them full):
+  // sum over i < x of ceil((base + (i + 1) tok) / grain)
   __host__ __device__ long long prefix(int base, long long x) const {
-    if (tok >= kTile)
-      return (long long)(tok / kTile) * (x * (x + 1) / 2) +
-             x * ((base + kTile - 1) / kTile);
-    const long long r = kTile / tok;
-    const long long a = (long long)base + kTile - 1 + tok;
-    const long long b = (a % kTile) / tok;
-    return x * (a / kTile) + floors(b + x, r) - floors(b, r);
+    const int grain_log = tile_log() + shift;
+    const long long up = (1LL << grain_log) - 1;
+    if (tok_log > grain_log)
+      return ((x * (x + 1) / 2) << (tok_log - grain_log)) + x * ((base + up) >> grain_log);
+    const int r = grain_log - tok_log;
+    const long long a = base + up + (1 << tok_log);
+    const long long b = (a & up) >> tok_log;
+    return x * (a >> grain_log) + floors(b + x, r) - floors(b, r);
   }
-  // key tiles of one head group of an unpacked sequence
-  __host__ __device__ long long group_tiles(const AttnSeq &s) const {
-    return prefix(s.base, token_tiles(s) - 1) + tiles(s.base + s.nq);
+  // cost of one head group of an unpacked sequence
+  __host__ __device__ long long group_cost(const AttnSeq &s) const {
+    const int n = token_tiles(s);
+    return (prefix(s.base, n - 1) + grains_of(s.base + s.nq)) * wide + (long long)n * over;
   }
   __host__ __device__ long long cost(const AttnSeq &s) const {
     if (s.nq == 0) return 0;
-    if (packed(s)) return (long long)HKV * tiles(s.base + s.nq);
-    return group_tiles(s) * groups * S::kWide;
+    if (packed(s)) return (long long)HKV * (grains_of(s.base + s.nq) + over);
+    return group_cost(s) * groups;
   }
-  __host__ __device__ int unit_cost(const AttnSeq &s) const { return packed(s) ? 1 : S::kWide; }
 
   // Unit that covers cost `c` (0 <= c < cost(s)) of sequence s; returns where
   // the unit begins.  t0, t1 and slot are left to the caller.
@@ -148,136 +182,137 @@ struct AttnPlan {
     u.len = s.len;
     if (packed(s)) {
       u.nt = tiles(s.base + s.nq);
-      u.kvh = (int)(c / u.nt);
+      const int each = ((u.nt + (1 << shift) - 1) >> shift) + over;
+      u.kvh = (int)attn_div(c, each);
       u.head0 = u.kvh * G;
       u.gp = G;
       u.row0 = s.q0;
       u.n_tok = s.nq;
       u.pos0 = s.past;
-      return (long long)u.kvh * u.nt;
+      return (long long)u.kvh * each;
     }
-    const long long per_group = group_tiles(s);
-    const long long t = c / S::kWide;
-    const int group = (int)(t / per_group);
-    const long long rem = t - group * per_group;
+    const long long per_group = group_cost(s);
+    const int group = (int)attn_div(c, per_group);
+    const long long rem = c - group * per_group;
     int lo = 0, hi = token_tiles(s) - 1;  // last token tile that begins at or before rem
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (prefix(s.base, mid) <= rem) lo = mid; else hi = mid - 1;
+      if (prefix(s.base, mid) * wide + (long long)mid * over <= rem) lo = mid; else hi = mid - 1;
     }
-    const int first = lo * tok;
-    u.n_tok = s.nq - first < tok ? s.nq - first : tok;
+    const int first = lo << tok_log;
+    u.n_tok = s.nq - first < (1 << tok_log) ? s.nq - first : 1 << tok_log;
     u.nt = tiles(s.base + first + u.n_tok);
     u.gp = gp;
     u.head0 = group * gp;
     u.kvh = u.head0 / G;
     u.row0 = s.q0 + first;
     u.pos0 = s.past + first;
-    return (group * per_group + prefix(s.base, lo)) * S::kWide;
+    return group * per_group + prefix(s.base, lo) * wide + (long long)lo * over;
   }
-};
-
-// first tile of a unit (beginning at cost u0, tiles of cost w) at or after cost c
-__host__ __device__ __forceinline__ int attn_cut(long long u0, int w, int nt, long long c) {
-  if (c <= u0) return 0;
-  const long long t = (c - u0 + w - 1) / w;
-  return t < nt ? (int)t : nt;
-}
-
-// Whether the border between the ranges of blocks i - 1 and i is the first one
-// that cuts unit `u` (beginning at cost u0, tiles of cost w); `last` is then
-// the last block with a piece of it (block i - 1 has the first piece).
-__host__ __device__ __forceinline__ bool attn_merge(long long u0, int w, int nt, int i,
-                                                    long long per, int &last) {
-  const int cut = attn_cut(u0, w, nt, i * per);
-  if (cut == 0 || cut == nt || attn_cut(u0, w, nt, (i - 1) * per) != 0) return false;
-  last = i;
-  while (attn_cut(u0, w, nt, (last + 1) * per) < nt) last++;
-  return true;
-}
-
-// cost of each block's range
-template <class S>
-__host__ __device__ __forceinline__ long long attn_per(const AttnArgs &a, long long total, int n_blocks) {
-  long long per = (total + n_blocks - 1) / n_blocks;
-  per += per & (S::kWide - 1);
-  return per < a.min_cost ? a.min_cost : per;
-}
-
-// What a block needs to start: the cost per block and the sequence its first
-// cost falls into.
-struct AttnStart {
-  long long per;    // cost of a block's range
-  long long total;  // cost of everything
-  long long seq0;   // cost at which sequence `seq` begins
-  int seq;
-};
-
-// Every thread of the block calls this (it synchronises the block).  Finds the
-// start of cost block * per; seq = n_seqs when the block has no work.
-template <int THREADS>
-struct AttnStartScratch {
-  long long warp_sum[THREADS / 32];
-  AttnStart out;
-};
-template <class S, int THREADS>
-__device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, const AttnPlan<S> &plan,
-                                                long long block, int n_blocks,
-                                                AttnStartScratch<THREADS> &scratch) {
-  constexpr int kWarps = THREADS / 32;
-  long long *warp_sum = scratch.warp_sum;
-  AttnStart &out = scratch.out;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int chunk = (a.n_seqs + THREADS - 1) / THREADS;
-  const int lo = min(tid * chunk, a.n_seqs), hi = min(lo + chunk, a.n_seqs);
-  long long mine = 0;
-  bool any_bad = false;
-  for (int n = lo; n < hi; n++) {
-    bool bad;
-    mine += plan.cost(attn_seq(a, n, bad));
-    any_bad |= bad;
+  // first tile at or after cost c of a unit that begins at cost u0
+  __host__ __device__ int cut(const AttnSeq &s, long long u0, int nt, long long c) const {
+    c -= u0 + over;
+    if (c <= 0) return 0;
+    const int w = packed(s) ? 1 : wide;
+    const long long t = ((c + w - 1) >> (w == 1 ? 0 : 1)) << shift;
+    static_assert(S::kWide == 1 || S::kWide == 2, "a shift in cut()");
+    return t < nt ? (int)t : nt;
   }
-  if (tid == 0 && a.cu) any_bad |= a.cu[0] != 0 || a.cu[a.n_seqs] != a.Ttot;
-  if (any_bad && a.flags && block == 0) atomicOr(a.flags, kFlagBadSeqlens);
-  long long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += up;
+  // Whether the border between the ranges of blocks i - 1 and i is the first
+  // one that cuts the unit beginning at u0; `last` is then the last block with
+  // a piece of it (block i - 1 has the first piece).
+  __host__ __device__ bool merges(const AttnSeq &s, long long u0, int nt, int i, int &last) const {
+    const int at = cut(s, u0, nt, i * per);
+    if (at == 0 || at == nt || cut(s, u0, nt, (i - 1) * per) != 0) return false;
+    last = i;
+    while (cut(s, u0, nt, (last + 1) * per) < nt) last++;
+    return true;
   }
-  if (lane == 31) warp_sum[warp] = incl;
-  if (tid == 0) out.seq = a.n_seqs;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; w++) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
-  }
-  const long long per = attn_per<S>(a, total, n_blocks);
-  const long long c = block * per;
-  if (c >= before && c < before + mine) {
-    long long at = before;
-    for (int n = lo; n < hi; n++) {
-      bool bad;
-      const long long k = plan.cost(attn_seq(a, n, bad));
-      if (c < at + k) {
-        out.seq = n;
-        out.seq0 = at;
-        break;
+
+  // What the totals decide: `weighted` is the cost of everything in stream
+  // form, `pieces(log)` the number of grains of 2^log tiles.  Returns the cost
+  // of everything under the plan that was chosen.
+  template <class F>
+  __host__ __device__ long long choose(long long weighted, int n_blocks, F pieces) {
+    const long long share = attn_div(weighted + n_blocks - 1, n_blocks);
+    // a grain of up to kSlack tiles more than an equal share costs less than a
+    // second unit's start and end
+    constexpr int kSlack = 4;
+    for (int log = kMinGrain; log <= kMaxGrain && (1 << log) <= share + kSlack; log++) {
+      if ((2LL << log) < share / S::kWide) continue;  // far too many grains
+      const long long n = pieces(log);
+      if (n <= n_blocks) {
+        grains(log);
+        return n;
       }
-      at += k;
     }
+    stream(share + (share & (S::kWide - 1)));
+    if (per < S::kWide) per = S::kWide;
+    return weighted;
   }
-  __syncthreads();
-  AttnStart r = out;
-  r.per = per;
-  r.total = total;
+};
+
+// What a block needs to start: the cost of everything and the sequence its
+// first cost falls into.
+struct AttnStart {
+  long long total;
+  long long seq0;   // cost at which sequence `seq` begins
+  int seq;          // n_seqs when the block has no work
+};
+
+// All lanes of one warp: choose the plan and find the start of range `block`.
+template <class S>
+__device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &plan,
+                                                long long block, int n_blocks) {
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t kAll = 0xffffffffu;
+  bool any_bad = lane == 0 && a.cu && (a.cu[0] != 0 || a.cu[a.n_seqs] != a.Ttot);
+  auto sum = [&](bool check) {
+    long long mine = 0;
+    for (int n = lane; n < a.n_seqs; n += 32) {
+      bool bad;
+      mine += plan.cost(attn_seq(a, n, bad));
+      if (check) any_bad |= bad;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(kAll, mine, d);
+    return mine;
+  };
+  AttnStart r;
+  r.total = plan.choose(sum(true), n_blocks, [&](int log) {
+    plan.grains(log);
+    return sum(false);
+  });
+  if (any_bad && a.flags && block == 0) atomicOr(a.flags, kFlagBadSeqlens);
+  r.seq = a.n_seqs;
+  r.seq0 = 0;
+  const long long c = block * plan.per;
+  if (c >= r.total) return r;
+  long long before = 0;
+  for (int n0 = 0; n0 < a.n_seqs; n0 += 32) {
+    bool bad;
+    const int n = n0 + lane;
+    const long long mine = n < a.n_seqs ? plan.cost(attn_seq(a, n, bad)) : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long up = __shfl_up_sync(kAll, incl, d);
+      if (lane >= d) incl += up;
+    }
+    const long long excl = before + incl - mine;
+    const uint32_t hit = __ballot_sync(kAll, c >= excl && c < excl + mine);
+    if (hit) {
+      const int who = __ffs(hit) - 1;
+      r.seq = n0 + who;
+      r.seq0 = __shfl_sync(kAll, excl, who);
+      return r;
+    }
+    before += __shfl_sync(kAll, incl, 31);
+  }
   return r;
 }
 
-// Walks the units of one block's range, in order.  One thread (or warp, all
-// lanes alike) drives it.
+// Walks the units of one block's range, in order.
 template <class S>
 struct AttnWalk {
   const AttnArgs &a;
@@ -286,12 +321,13 @@ struct AttnWalk {
   long long at, end, seq0, seq_cost;  // next cost, end of the range, current sequence's span
   int seq, block;
 
-  __host__ __device__ AttnWalk(const AttnArgs &a_, const AttnPlan<S> &p_, const AttnStart &st, int block_)
+  __host__ __device__ AttnWalk(const AttnArgs &a_, const AttnPlan<S> &p_, const AttnStart &st,
+                               int block_)
       : a(a_), plan(p_), block(block_) {
     seq = st.seq;
     seq0 = st.seq0;
-    at = block * st.per;
-    end = at + st.per < st.total ? at + st.per : st.total;
+    at = block * plan.per;
+    end = at + plan.per < st.total ? at + plan.per : st.total;
     if (seq < a.n_seqs) load();
   }
   __host__ __device__ void load() {
@@ -307,10 +343,11 @@ struct AttnWalk {
         load();
       }
       const long long u0 = seq0 + plan.find(s, seq, at - seq0, u);
-      const int w = plan.unit_cost(s);
-      u.t0 = attn_cut(u0, w, u.nt, at);
-      u.t1 = attn_cut(u0, w, u.nt, end);
-      at = u0 + (long long)u.nt * w;
+      u.t0 = plan.cut(s, u0, u.nt, at);
+      u.t1 = plan.cut(s, u0, u.nt, end);
+      // the range may end inside this unit, or take all of it
+      at = u0 + plan.over +
+           (long long)((u.nt + (1 << plan.shift) - 1) >> plan.shift) * (plan.packed(s) ? 1 : plan.wide);
       if (u.t0 >= u.t1) continue;
       u.slot = u.t0 > 0 ? 2 * block : (u.t1 < u.nt ? 2 * block + 1 : -1);
       return true;

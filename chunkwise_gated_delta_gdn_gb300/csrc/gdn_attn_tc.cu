@@ -11,12 +11,14 @@
 // at most 128 rows (a decode step, a short chunk) is one row tile whose even
 // and odd key tiles go to X = 0 and X = 1, joined at its end.
 //
-// Warps 0-3 and 4-7: softmax of X = 0 and 1, a row per thread.  Warp 8: TMA
-// loads into a ring of key and value tiles.  Warp 9: the products.  Warp 10:
-// the plan, units published through a small ring.  The loader and the product
-// warp go through the same sequence of tiles across units, so the ring stays
-// full and the first scores of a unit are computed while the softmax warps
-// write out the last one.
+// Warps 0-7 and 8-15: softmax of X = 0 and 1, half a row per thread (with a
+// whole row per thread and half the warps, two warps to a scheduler did not
+// cover one another's latencies: 2045 clocks for both tiles where this takes
+// 1470, and the products of both take 2048).  Warp 16: TMA loads into a ring of
+// key and value tiles.  Warp 17: the products.  Warp 18: the plan, units
+// published through a small ring.  The loader and the product warp go through
+// the same sequence of tiles across units, so the ring stays full and the first
+// scores of a unit are computed while the softmax warps write out the last one.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -28,8 +30,8 @@ namespace {
 
 using namespace sm100;
 
-using TcShape = AttnShape<256, 128, 128, 2>;
-constexpr int kThreads = 384;
+using TcShape = AttnShape<256, 128, 128, 2, 4>;
+constexpr int kThreads = 640;
 constexpr int kUnits = 4;              // unit ring
 constexpr int kPanel = 128 * 128;      // bytes of 128 rows x 64 bf16
 constexpr float kRescale = 8.f;        // log2 growth of a row maximum that is let stand
@@ -40,17 +42,51 @@ struct Smem {
   static constexpr int kStages = D == 128 ? 5 : 10;
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTileBytes;
-  static constexpr int kMl = kRing + kStages * kTileBytes;  // [2][128] float2
-  static constexpr int kUnit = kMl + 2 * 128 * 8;
-  static constexpr int kScratch = kUnit + kUnits * (int)sizeof(AttnUnit);
-  static constexpr int kBars = (kScratch + (int)sizeof(AttnStartScratch<kThreads>) + 7) / 8 * 8;
+  static constexpr int kRow = kRing + kStages * kTileBytes;  // [X][half][128] floats
+  static constexpr int kUnit = kRow + 2 * 2 * 128 * 4;
+  static constexpr int kBars = kUnit + kUnits * (int)sizeof(AttnUnit);
   // barriers, in order: Q full, Q empty, S full x2, P ready x2, O full x2,
-  // swap x2, unit full x4, unit empty x4, tile full, tile empty
-  static constexpr int kBarCount = 10 + 2 * kUnits + 2 * kStages;
+  // swap x2, halves x8, unit full x4, unit empty x4, tile full, tile empty
+  static constexpr int kBarCount = 18 + 2 * kUnits + 2 * kStages;
   static constexpr int kSlot = kBars + kBarCount * 8;
   static constexpr int kBytes = kSlot + 16;
 };
 static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "shared memory of one SM");
+
+// Two fp32 values in one 64-bit register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// kCols consecutive columns of this thread's lane (no wait)
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&y)[N]) {
+  static_assert(N == 32 || N == 16, "");
+  if constexpr (N == 32)
+    tmem_ld32_nowait(at, reinterpret_cast<uint32_t(&)[32]>(y));
+  else
+    tmem_ld16_nowait(at, reinterpret_cast<uint32_t(&)[16]>(y));
+}
 
 struct Maps {
   CUtensorMap q_pack, q, k, v;
@@ -64,6 +100,48 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// The products, issued by one lane of a converged warp.  The operands' matrix
+// descriptors differ between steps in the low word's address field only (16
+// bytes a unit), so a step costs an addition: with the descriptors put together
+// from scratch for each product the issue took longer than the product itself.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);  // 1024 bytes between 8-row groups
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFF) | ((lbo >> 4) << 16);
+}
+// S = Q K^T over one 64-column panel of each (four K steps of 16)
+template <bool FIRST>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                             bool elected) {
+  asm volatile(
+      "{\n .reg .pred q, p;\n .reg .b64 da, db;\n .reg .b32 la, lb;\n setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 da, {%1, %3};\n mov.b64 db, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n"
+      " add.u32 la, %1, 2;\n add.u32 lb, %2, 2;\n mov.b64 da, {la, %3};\n mov.b64 db, {lb, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, 1;\n"
+      " add.u32 la, %1, 4;\n add.u32 lb, %2, 4;\n mov.b64 da, {la, %3};\n mov.b64 db, {lb, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, 1;\n"
+      " add.u32 la, %1, 6;\n add.u32 lb, %2, 6;\n mov.b64 da, {la, %3};\n mov.b64 db, {lb, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, 1;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((int)elected), "r"(FIRST ? 0 : 1)
+      : "memory");
+}
+// O (+)= P V over 64 keys (four K steps of 16)
+__device__ __forceinline__ void issue_output(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                             bool accumulate, bool elected) {
+  asm volatile(
+      "{\n .reg .pred q, p;\n .reg .b64 db;\n .reg .b32 la, lb;\n setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 db, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n"
+      " add.u32 la, %1, 8;\n add.u32 lb, %2, 128;\n mov.b64 db, {lb, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [la], db, %4, 1;\n"
+      " add.u32 la, %1, 16;\n add.u32 lb, %2, 256;\n mov.b64 db, {lb, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [la], db, %4, 1;\n"
+      " add.u32 la, %1, 24;\n add.u32 lb, %2, 384;\n mov.b64 db, {lb, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [la], db, %4, 1;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((int)elected), "r"((int)accumulate)
+      : "memory");
 }
 
 // A bounded wait by all lanes of a warp, converged afterwards.
@@ -83,10 +161,11 @@ struct Bars {
   __device__ uint32_t p_ready(int x) const { return at(4 + x); }
   __device__ uint32_t o_full(int x) const { return at(6 + x); }
   __device__ uint32_t swap(int i) const { return at(8 + i); }
-  __device__ uint32_t unit_full(int i) const { return at(10 + i); }
-  __device__ uint32_t unit_empty(int i) const { return at(10 + kUnits + i); }
-  __device__ uint32_t kv_full(int i) const { return at(10 + 2 * kUnits + i); }
-  __device__ uint32_t kv_empty(int i) const { return at(10 + 2 * kUnits + stages + i); }
+  __device__ uint32_t halves(int i) const { return at(10 + i); }
+  __device__ uint32_t unit_full(int i) const { return at(18 + i); }
+  __device__ uint32_t unit_empty(int i) const { return at(18 + kUnits + i); }
+  __device__ uint32_t kv_full(int i) const { return at(18 + 2 * kUnits + i); }
+  __device__ uint32_t kv_empty(int i) const { return at(18 + 2 * kUnits + stages + i); }
 };
 
 // Position in a ring of N: index and how often it has gone round.
@@ -156,20 +235,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t *slot = reinterpret_cast<uint32_t *>(sm + SM::kSlot);
   volatile int *abort = reinterpret_cast<volatile int *>(slot + 1);
   AttnUnit *unit_ring = reinterpret_cast<AttnUnit *>(sm + SM::kUnit);
-  float2 *ml = reinterpret_cast<float2 *>(sm + SM::kMl);
+  float *row_ex = reinterpret_cast<float *>(sm + SM::kRow);
   if (tid == 0) {
     *abort = 0;
     mbar_init(bars.q_full(), 1);
     mbar_init(bars.q_empty(), 1);
     for (int x = 0; x < 2; x++) {
       mbar_init(bars.s_full(x), 1);
-      mbar_init(bars.p_ready(x), 4);
+      mbar_init(bars.p_ready(x), 8);
       mbar_init(bars.o_full(x), 1);
-      mbar_init(bars.swap(x), 8);
+      mbar_init(bars.swap(x), 16);
     }
+    for (int i = 0; i < 8; i++) mbar_init(bars.halves(i), 2);
     for (int i = 0; i < kUnits; i++) {
       mbar_init(bars.unit_full(i), 1);
-      mbar_init(bars.unit_empty(i), 10);  // loader, products, eight softmax warps
+      mbar_init(bars.unit_empty(i), 18);  // loader, products, sixteen softmax warps
     }
     for (int i = 0; i < SM::kStages; i++) {
       mbar_init(bars.kv_full(i), 1);
@@ -177,27 +257,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_fence_init();
   }
-  if (warp == 9) tmem_alloc(smem_addr(slot), 512);
+  if (warp == 17) tmem_alloc(smem_addr(slot), 512);
   fence_before_sync();
-  const AttnPlan<TcShape> plan(a.H, a.HKV);
-  // synchronises the block twice: barriers and tensor memory are ready after it
-  const AttnStart st = attn_start<TcShape, kThreads>(
-      a, plan, blockIdx.x, gridDim.x, *reinterpret_cast<AttnStartScratch<kThreads> *>(sm + SM::kScratch));
+  __syncthreads();
   fence_after_sync();
   const uint32_t tmem = *slot;
   const uint32_t sQ = smem_addr(sm + SM::kQ), sRing = smem_addr(sm + SM::kRing);
   const uint32_t tS = tmem, tO = tmem + 256;
 
-  if (warp < 8) {
+  if (warp < 16) {
     // ------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int x = warp >> 2, r = tid & 127;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
-    const uint32_t s_at = tS + x * 128 + lanes, o_at = tO + x * D + lanes;
+    const int x = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)quarter << 21;  // this warp's 32 lanes of tensor memory
+    const uint32_t s_at = tS + x * 128 + half * 64 + lanes, p_at = tS + x * 128 + half * 32 + lanes;
+    const uint32_t o_at = tO + x * D + lanes;
+    float *own_ex = row_ex + (x * 2 + half) * 128 + r, *other_ex = row_ex + (x * 2 + (half ^ 1)) * 128 + r;
+    const uint32_t halves = bars.halves(x * 4 + quarter);
     const float sl2 = a.scale_log2;
     const float grow = kRescale / sl2;
     Units units{unit_ring, bars, abort, {}};
-    uint32_t s_phase = 0, o_phase = 0, swap_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0, half_phase = 0, swap_phase[2] = {0, 0};
+    auto meet_half = [&] {  // the two warps of these 32 rows
+      __syncwarp();
+      if (lane == 0) mbar_arrive(halves);
+      wait(halves, half_phase, abort);
+      half_phase ^= 1;
+    };
+    auto meet_all = [&](int i) {  // all softmax warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars.swap(i));
+      wait(bars.swap(i), swap_phase[i], abort);
+      swap_phase[i] ^= 1;
+    };
     AttnUnit u;
     while (units.next(u)) {
       const bool narrow = u.n_tok * u.gp <= 128;
@@ -205,30 +297,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int stride = narrow ? 2 : 1;
       const int row = narrow ? r : x * 128 + r;
       const int tok = row / u.gp;
-      const int limit = u.pos0 + min(tok, u.n_tok - 1);  // last visible key
+      const int limit = u.pos0 + min(tok, u.n_tok - 1) - half * 64;  // last visible key, this half's columns
       const int all_see = __reduce_min_sync(0xffffffffu, limit);
       float m = -CUDART_INF_F, l = 0.f;
       const int first = narrow ? u.t0 + x : u.t0;
+      const bool mine = first < u.t1;
+#pragma unroll 1
       for (int t = first; t < u.t1; t += stride) {
         wait(bars.s_full(x), s_phase, abort);
         s_phase ^= 1;
         fence_after_sync();
-        uint32_t s[128];
-#pragma unroll
-        for (int c = 0; c < 4; c++)
-          tmem_ld32_nowait(s_at + c * 32, *reinterpret_cast<uint32_t(*)[32]>(s + c * 32));
+        uint32_t raw[2][32];
+        tmem_ld32_nowait(s_at, raw[0]);
+        tmem_ld32_nowait(s_at + 32, raw[1]);
         tmem_wait_ld();
-        if (t * 128 + 127 > all_see) {
+        float s[64];
+#pragma unroll
+        for (int c = 0; c < 64; c++) s[c] = __uint_as_float(raw[c >> 5][c & 31]);
+        if (t * 128 + 63 > all_see) {
           const int lim = limit - t * 128;
 #pragma unroll
-          for (int c = 0; c < 128; c++)
-            if (c > lim) s[c] = __float_as_uint(-CUDART_INF_F);
+          for (int c = 0; c < 64; c++)
+            if (c > lim) s[c] = -CUDART_INF_F;
         }
-        float top[4] = {__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]),
-                        __uint_as_float(s[3])};
+        float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-        for (int c = 4; c < 128; c++) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
-        const float tile_max = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        for (int c = 0; c < 64; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; i++) top[i] = max3(top[i], s[c + 2 * i], s[c + 2 * i + 1]);
+        float tile_max = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+        *own_ex = tile_max;
+        // past this, both halves of the scores are in registers: the weights
+        // may be written over them
+        fence_before_sync();
+        meet_half();
+        fence_after_sync();
+        tile_max = fmaxf(tile_max, *other_ex);
         // The maximum is moved only when it has grown by a factor of 2^8: the
         // weights then stay below 2^8, the sums in fp32 far from overflow, and
         // the output in tensor memory is rarely touched.
@@ -240,120 +344,132 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (move) m = tile_max;
           l *= f;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32_nowait(o_at + c, o);
+          for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+            uint32_t o[16];
+            tmem_ld16_nowait(o_at + c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32_nowait(o_at + c, o);
+            for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16_nowait(o_at + c, o);
           }
         }
         const float off = m == -CUDART_INF_F ? 0.f : m * sl2;  // nothing visible yet: weights 0
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pair(sl2, sl2), off2 = pair(-off, -off);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < 128; c += 2) {
-          const float p0 = ex2(fmaf(__uint_as_float(s[c]), sl2, -off));
-          const float p1 = ex2(fmaf(__uint_as_float(s[c + 1]), sl2, -off));
-          sum[(c >> 1) & 1] += p0;
-          sum[2 + ((c >> 1) & 1)] += p1;
-          s[c >> 1] = pack2(p0, p1);
+        for (int h = 0; h < 64; h += 32) {
+          uint32_t packed[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float p0, p1;
+            unpair(fma2(pair(s[h + c], s[h + c + 1]), scale2, off2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair(p0, p1));
+            packed[c >> 1] = pack2(p0, p1);
+          }
+          tmem_st16_nowait(p_at + (h >> 1), packed);
         }
-        tmem_st32_nowait(s_at, s);
-        tmem_st32_nowait(s_at + 32, s + 32);
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float l0, l1;
+        unpair(add2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
         tmem_wait_st();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.p_ready(x));
       }
       // ---- the unit's output
-      const bool mine = first < u.t1;
       if (mine) {
         wait(bars.o_full(x), o_phase, abort);
         o_phase ^= 1;
         fence_after_sync();
       }
-      float m_scaled = m * sl2;
-      float f_own = 1.f, f_other = 0.f;
+      float m_scaled = m * sl2, f_own = 1.f, f_other = 0.f;
       if (both) {
-        ml[x * 128 + r] = make_float2(m_scaled, l);
+        // row sums and maxima of both X; the first meeting also says that the
+        // other X's output is complete
+        *own_ex = l;
         fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.swap(0));
-        wait(bars.swap(0), swap_phase, abort);
+        meet_all(0);
         fence_after_sync();
-        const float2 other = ml[(x ^ 1) * 128 + r];
-        const float top = fmaxf(m_scaled, other.x);
+        const float l_own = l + *other_ex;
+        const float l_other = row_ex[(x ^ 1) * 256 + r] + row_ex[(x ^ 1) * 256 + 128 + r];
+        meet_all(1);
+        if (half == 0) *own_ex = m_scaled;
+        meet_all(0);
+        const float m_other = row_ex[(x ^ 1) * 256 + r];
+        const float top = fmaxf(m_scaled, m_other);
         const float base = top == -CUDART_INF_F ? 0.f : top;
         f_own = ex2(m_scaled - base);
-        f_other = ex2(other.x - base);
-        l = f_own * l + f_other * other.y;
+        f_other = ex2(m_other - base);
+        l = f_own * l_own + f_other * l_other;
         m_scaled = top;
+      } else if (mine) {
+        *own_ex = l;
+        meet_half();
+        l += *other_ex;
+        meet_half();  // read, before the next tile's maximum is written
       }
       if (mine) {
         const bool valid = tok < u.n_tok;
-        const float inv = u.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+        const bool part = u.slot >= 0;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         const long long at = (long long)(u.row0 + tok) * a.H + u.head0 + row % u.gp;
         bool finite = true;
-        // both: X = 0 writes the first half of the columns, X = 1 the second
-        const int c0 = both ? x * (D / 2) : 0, c1 = both ? c0 + D / 2 : D;
+        // each half writes half of the columns; of a joined output, each X half of those
+        constexpr int kCols = D / 4;
+        const int c0 = both ? (half * 2 + x) * kCols : half * 2 * kCols;
+        const int c1 = both ? c0 + kCols : c0 + 2 * kCols;
 #pragma unroll 1
-        for (int c = c0; c < c1; c += 32) {
-          uint32_t o[32], other[32];
-          tmem_ld32_nowait(o_at + c, o);
-          if (both) tmem_ld32_nowait(tO + (x ^ 1) * D + lanes + c, other);
+        for (int c = c0; c < c1; c += kCols) {
+          float y[kCols];
+          tmem_ld<kCols>(o_at + c, y);
           tmem_wait_ld();
-          float y[32];
           if (both) {
+            float other[kCols];
+            tmem_ld<kCols>(tO + (x ^ 1) * D + lanes + c, other);
+            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; i++)
-              y[i] = f_own * __uint_as_float(o[i]) + f_other * __uint_as_float(other[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i++) y[i] = __uint_as_float(o[i]);
+            for (int i = 0; i < kCols; i++) y[i] = f_own * y[i] + f_other * other[i];
           }
-          if (valid && u.slot >= 0) {
+          if (valid && part) {
 #pragma unroll
-            for (int i = 0; i < 8; i++)
+            for (int i = 0; i < kCols / 4; i++)
               a.part_o[((long long)u.slot * (D / 4) + (c >> 2) + i) * TcShape::kRows + row] =
                   make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
           } else if (valid) {
-            uint32_t out[16];
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-              const float p = y[2 * i] * inv, q = y[2 * i + 1] * inv;
-              finite &= isfinite(p) && isfinite(q);
-              out[i] = pack2(p, q);
-            }
             uint4 *to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + c);
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-              to[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+            for (int i = 0; i < kCols; i++) {
+              y[i] *= inv;
+              finite &= isfinite(y[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kCols / 8; i++)
+              to[i] = make_uint4(pack2(y[8 * i], y[8 * i + 1]), pack2(y[8 * i + 2], y[8 * i + 3]),
+                                 pack2(y[8 * i + 4], y[8 * i + 5]), pack2(y[8 * i + 6], y[8 * i + 7]));
           }
           __syncwarp();
         }
-        if (valid && (!both || x == 0)) {
-          if (u.slot >= 0)
+        if (valid && half == 0 && (!both || x == 0)) {
+          if (part)
             a.part_ml[(long long)u.slot * TcShape::kRows + row] = make_float2(m_scaled, l);
           else if (a.lse)
             a.lse[at] = l == 0.f ? -CUDART_INF_F : (m_scaled + log2f(l)) * 0.69314718056f;
         }
         if (!finite && a.flags) atomicOr(a.flags, kFlagNonfinite);
       }
-      if (both) {  // the other output has been read: it may be overwritten
+      if (both) {  // the other X's output and maxima have been read: they may be overwritten
         fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.swap(1));
-        wait(bars.swap(1), swap_phase, abort);
+        meet_all(1);
         fence_after_sync();
-        swap_phase ^= 1;
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 10) {
+    if (warp == 18) {
       // -------------------------------------------------------------- plan
+      AttnPlan<TcShape> plan(a.H, a.HKV);
+      const AttnStart st = attn_start(a, plan, blockIdx.x, gridDim.x);
       AttnWalk<TcShape> walk(a, plan, st, blockIdx.x);
       Ring<kUnits> at;
       AttnUnit u;
@@ -369,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         at.step();
       }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
       // ------------------------------------------------------------- loads
       Units units{unit_ring, bars, abort, {}};
       Ring<SM::kStages> ring;
@@ -422,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(bars.q_empty(), q_phase, abort);
             q_phase ^= 1;
             if (lane == 0) {
-              const bool whole = nxt.u.gp == plan.G;  // all heads of a key/value head
+              const bool whole = nxt.u.gp == a.H / a.HKV;  // all heads of a key/value head
               const int toks = 128 / nxt.u.gp, tiles = nxt.narrow ? 1 : 2;
               mbar_arrive_expect_tx(bars.q_full(), tiles * kPanels * toks * nxt.u.gp * 128);
               for (int i = 0; i < tiles; i++)
@@ -439,13 +555,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         cur = nxt;
         nxt.advance(units);
       }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
       // ---------------------------------------------------------- products
       constexpr uint32_t kIdS = idesc_bf16(128, 128, 0, 0), kIdO = idesc_bf16(128, D, 0, 1);
       Units units{unit_ring, bars, abort, {}};
       Ring<SM::kStages> ring;
       uint32_t q_phase = 0, p_phase[2] = {0, 0};
       int v_stage = 0, k_stage = 0;
+      // A stage is handed back when the softmax answers a product issued after
+      // its last use: weights of X that are ready mean that its scores, and
+      // everything issued before them, are done.  A commit for each stage costs
+      // the tensor pipe 40 to 120 clocks each (it does not start the next
+      // product before the committed ones are through).
+      int k_done[2] = {-1, -1}, v_done[2] = {-1, -1};
+      auto free_stage = [&](int &stage) {
+        if (stage >= 0 && lane == 0) mbar_arrive(bars.kv_empty(stage));
+        stage = -1;
+      };
       Step cur, nxt;
       cur.valid = false;
       nxt.begin(units);
@@ -473,15 +599,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             wait(bars.p_ready(x), p_phase[x], abort);
             p_phase[x] ^= 1;
+            free_stage(k_done[x]);
+            free_stage(v_done[x]);
             fence_after_sync();
-            if (lane == 0) {
-              const uint32_t sV = sRing + v_stage * SM::kTileBytes;
-#pragma unroll
-              for (int k = 0; k < 8; k++)
-                mma_f16_ta(tO + x * D, tS + x * 128 + k * 8, make_desc(sV + k * 2048, kPanel, 1024),
-                           kIdO, cur.step > 0 || k > 0);
-              if (cur.frees(x)) mma_commit(bars.kv_empty(v_stage));
-              if (cur.last(x)) mma_commit(bars.o_full(x));
+            const uint32_t v_lo = desc_lo(sRing + v_stage * SM::kTileBytes, kPanel);
+            issue_output(tO + x * D, tS + x * 128, v_lo, kIdO, cur.step > 0, lane == 0);
+            issue_output(tO + x * D, tS + x * 128 + 32, v_lo + 512, kIdO, true, lane == 0);
+            if (cur.last(x)) {
+              if (lane == 0) {
+                if (cur.frees(x)) mma_commit(bars.kv_empty(v_stage));
+                mma_commit(bars.o_full(x));
+              }
+            } else if (cur.frees(x)) {
+              v_done[x] = v_stage;
             }
             __syncwarp();
           }
@@ -496,17 +626,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               ring.step();
             }
             fence_after_sync();
+            const uint32_t q_lo = desc_lo(sQ + (nxt.narrow ? 0 : x * SM::kTileBytes), 16);
+            const uint32_t k_lo = desc_lo(sRing + k_stage * SM::kTileBytes, 16);
+            issue_scores<true>(tS + x * 128, q_lo, k_lo, kIdS, lane == 0);
+            if (D == 128)
+              issue_scores<false>(tS + x * 128, q_lo + (kPanel >> 4), k_lo + (kPanel >> 4), kIdS, lane == 0);
+            if (nxt.frees(x)) k_done[x] = k_stage;
             if (lane == 0) {
-              const uint32_t sK = sRing + k_stage * SM::kTileBytes;
-              const uint32_t sA = sQ + (nxt.narrow ? 0 : x * SM::kTileBytes);
-#pragma unroll
-              for (int k = 0; k < D / 16; k++) {
-                const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
-                mma_f16(tS + x * 128, make_desc(sA + off, 16, 1024), make_desc(sK + off, 16, 1024), kIdS,
-                        k > 0);
-              }
               mma_commit(bars.s_full(x));
-              if (nxt.frees(x)) mma_commit(bars.kv_empty(k_stage));
               // the last scores of a unit: its queries may be replaced
               if (nxt.step == nxt.steps - 1 && (x == 1 || !nxt.active(1))) mma_commit(bars.q_empty());
             }
@@ -523,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after_sync();
   if (tid == 0 && *abort && a.flags) atomicOr(a.flags, kFlagTimeout);
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 bool make_maps(Maps &m, const AttnArgs &a, int d, int box) {

@@ -130,7 +130,6 @@ struct AttnArgs {
   int max_len;                 // longest length the table can hold
   float scale;
   float scale_log2;            // scale * log2(e)
-  int min_cost;                // least cost of a block's range
   float4 *part_o;              // partial results (see gdn_attn.cuh)
   float2 *part_ml;
   uint32_t *flags;             // device status word, or nullptr

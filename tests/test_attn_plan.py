@@ -28,37 +28,51 @@ using namespace gdn;
 #define CHECK(x) do { if (!(x)) { std::printf("line %d: %s\n", __LINE__, #x); return false; } } while (0)
 
 static unsigned rnd_state;
+static int grains_chosen = 0;
 static int rnd(int lo, int hi) {  // uniform over lo..hi
   rnd_state = rnd_state * 1664525u + 1013904223u;
   return lo + (int)((rnd_state >> 8) % (unsigned)(hi - lo + 1));
 }
 
 template <class S>
-bool one(const std::vector<int> &q, const std::vector<int> &kv, int H, int HKV, int blocks, int min_cost) {
+bool one(const std::vector<int> &q, const std::vector<int> &kv, int H, int HKV, int blocks, int force) {
   std::vector<int32_t> cu(1, 0), lens(kv.begin(), kv.end());
   for (int n : q) cu.push_back(cu.back() + n);
   AttnArgs a{};
   a.cu = cu.data(); a.kv_lens = lens.data(); a.n_seqs = (int)q.size(); a.Ttot = cu.back();
-  a.H = H; a.HKV = HKV; a.max_len = 1 << 30; a.min_cost = min_cost;
-  const AttnPlan<S> plan(H, HKV);
-  CHECK(H % plan.gp == 0 && plan.G % plan.gp == 0 && plan.gp * plan.tok == S::kRows);
-  long long total = 0;
+  a.H = H; a.HKV = HKV; a.max_len = 1 << 30;
+  AttnPlan<S> plan(H, HKV);
+  CHECK(H % plan.gp == 0 && plan.G % plan.gp == 0 && plan.gp << plan.tok_log == S::kRows);
   std::vector<long long> seq0;
-  for (int n = 0; n < a.n_seqs; n++) {
+  auto sum = [&] {
+    long long total = 0;
     bool bad;
-    seq0.push_back(total);
-    total += plan.cost(attn_seq(a, n, bad));
-    CHECK(!bad);
+    seq0.clear();
+    for (int n = 0; n < a.n_seqs; n++) {
+      seq0.push_back(total);
+      total += plan.cost(attn_seq(a, n, bad));
+    }
+    return total;
+  };
+  long long total = sum();
+  if (force >= 0) {  // any grain and any share, not only those that the kernels choose
+    plan.grains(force);
+    total = sum();
+    plan.per = total ? (total + blocks - 1) / blocks : 1;
+  } else {
+    total = plan.choose(total, blocks, [&](int log) { plan.grains(log); return sum(); });
+    CHECK(sum() == total);
+    grains_chosen += plan.over == 0;
   }
-  const long long per = attn_per<S>(a, total, blocks);
-  CHECK(per * blocks >= total);
+  const long long per = plan.per;
+  CHECK(per * blocks >= total && per >= 1);
   std::map<std::pair<int, int>, std::vector<int>> seen;  // (row, head) -> tiles
   std::map<std::tuple<int, int>, std::vector<int>> pieces;  // (row0, head0) -> slots in order
   std::map<std::tuple<int, int>, AttnUnit> units;
   std::set<int> slots;
   for (int b = 0; b < blocks; b++) {
     AttnStart st{};
-    st.per = per; st.total = total; st.seq = a.n_seqs;
+    st.total = total; st.seq = a.n_seqs;
     for (int n = 0; n < a.n_seqs; n++) {
       bool bad;
       const long long c = plan.cost(attn_seq(a, n, bad));
@@ -104,7 +118,7 @@ bool one(const std::vector<int> &q, const std::vector<int> &kv, int H, int HKV, 
     AttnUnit u;
     const long long u0 = seq0[n] + plan.find(s, n, c - seq0[n], u);
     int last;
-    if (!attn_merge(u0, plan.unit_cost(s), u.nt, i, per, last)) continue;
+    if (!plan.merges(s, u0, u.nt, i, last)) continue;
     CHECK(merged.insert({u.row0, u.head0}).second);
     std::vector<int> want{2 * (i - 1) + 1};
     for (int b = i; b <= last; b++) want.push_back(2 * b);
@@ -125,13 +139,14 @@ int main() {
       q.push_back(nq);
       kv.push_back(rnd(0, 9) == 0 ? rnd(0, nq) : nq + rnd(0, rnd(0, 1) ? 100 : 1500));
     }
-    const int blocks = rnd(0, 1) ? rnd(1, 9) : rnd(10, 200), min_cost = 2 * rnd(1, 4);
-    if (!one<AttnShape<64, 64, 64, 1>>(q, kv, hkv * g, hkv, blocks, min_cost) ||
-        !one<AttnShape<256, 128, 128, 2>>(q, kv, hkv * g, hkv, blocks, min_cost)) {
+    const int blocks = rnd(0, 1) ? rnd(1, 9) : rnd(10, 200), force = rnd(0, 1) ? -1 : rnd(0, 4);
+    if (!one<AttnShape<64, 64, 64, 1, 1>>(q, kv, hkv * g, hkv, blocks, force) ||
+        !one<AttnShape<256, 128, 128, 2, 4>>(q, kv, hkv * g, hkv, blocks, force)) {
       std::printf("trial %d: hkv %d g %d blocks %d\n", trial, hkv, g, blocks);
       return 1;
     }
   }
+  if (grains_chosen < 50) { std::printf("grains chosen %d times\n", grains_chosen); return 1; }
   std::printf("ok\n");
   return 0;
 }
@@ -145,7 +160,7 @@ def test_plan_covers_every_visible_key_once(tmp_path):
     src = tmp_path / "plan.cu"
     src.write_text(PROGRAM)
     exe = tmp_path / "plan"
-    subprocess.run([nvcc, *cuda_build.ARCH, "-O1", "-std=c++17", "-I", cuda_build.CSRC, "-I",
-                    cuda_build.INCLUDE, str(src), "-o", str(exe)], check=True)
+    subprocess.run([nvcc, *cuda_build.ARCH, *cuda_build.NVCC_FLAGS,
+                    str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
