@@ -198,28 +198,6 @@ struct Units {
   }
 };
 
-// A step of a unit: one key tile for both row tiles (wide), or one key tile
-// for each X (narrow).
-struct Step {
-  AttnUnit u;
-  int step, steps;
-  bool valid, narrow;
-  __device__ void begin(Units &units) {
-    valid = units.next(u);
-    step = 0;
-    narrow = u.n_tok * u.gp <= 128;
-    steps = narrow ? (u.t1 - u.t0 + 1) / 2 : u.t1 - u.t0;
-  }
-  __device__ void advance(Units &units) {
-    if (++step >= steps) begin(units);
-  }
-  __device__ int tile(int x) const { return narrow ? u.t0 + 2 * step + x : u.t0 + step; }
-  __device__ bool active(int x) const { return valid && (!narrow || tile(x) < u.t1); }
-  __device__ bool loads(int x) const { return active(x) && (narrow || x == 0); }
-  __device__ bool frees(int x) const { return narrow || x == 1; }
-  __device__ bool last(int x) const { return narrow ? tile(x) + 2 >= u.t1 : step == steps - 1; }
-};
-
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     gdn_attn_tc_kernel(const AttnArgs a, const __grid_constant__ Maps maps, const int box) {
@@ -487,24 +465,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 16) {
       // ------------------------------------------------------------- loads
+      // The order of the tiles is that of the products below.  A unit's last
+      // tiles go in the order of the keys: the stages of the earlier one are
+      // handed back first, and the ring needs them for what follows.
       Units units{unit_ring, bars, abort, {}};
       Ring<SM::kStages> ring;
       uint32_t q_phase = 1;
-      Step cur, nxt;
-      cur.valid = false;
-      // one tile of keys or values of `s` into the next stage
-      auto load = [&](const Step &s, int tile, const CUtensorMap *map) {
+      AttnUnit u, old;         // this unit, and the one whose last values are still to come
+      int left[2] = {-1, -1};  // its last tiles
+      bool shared = false;     // one value tile for both X
+      // one tile of keys or values of unit w into the next stage
+      auto load = [&](const AttnUnit &w, int tile, const CUtensorMap *map) {
         const uint32_t full = bars.kv_full(ring.i), dst = sRing + ring.i * SM::kTileBytes;
         const int key = tile * 128;
         if constexpr (PAGED) {
           // lane i takes the i-th box of `box` keys; boxes past the last key
           // are not loaded (what they leave in shared memory is masked)
-          const int left = s.u.len - key;
-          const int n = left <= 0 ? 0 : min((left + box - 1) / box, 128 / box);
+          const int rest = w.len - key;
+          const int n = rest <= 0 ? 0 : min((rest + box - 1) / box, 128 / box);
           int page = 0, first = 0;
           if (lane < n) {
             const int k0 = key + lane * box;
-            page = __ldg(a.table + (long long)s.u.seq * a.max_pages + k0 / a.page_size);
+            page = __ldg(a.table + (long long)w.seq * a.max_pages + k0 / a.page_size);
             first = k0 % a.page_size;
             // an out-of-range page reads as zeros
             if ((page < 0 || page >= a.n_pages) && a.flags) atomicOr(a.flags, kFlagBadSeqlens);
@@ -515,135 +497,210 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < n)
 #pragma unroll
             for (int p = 0; p < kPanels; p++)
-              tma_load_4d(dst + p * kPanel + lane * box * 128, map, p * 64, s.u.kvh, first, page, full);
+              tma_load_4d(dst + p * kPanel + lane * box * 128, map, p * 64, w.kvh, first, page, full);
         } else {
           wait(bars.kv_empty(ring.i), ring.round ^ 1, abort);
           if (lane == 0) {
             mbar_arrive_expect_tx(full, SM::kTileBytes);
-            const int row = s.u.row0 - s.u.pos0 + key;  // a prompt's keys are its own tokens
+            const int row = w.row0 - w.pos0 + key;  // a prompt's keys are its own tokens
 #pragma unroll
             for (int p = 0; p < kPanels; p++)
-              tma_load_4d(dst + p * kPanel, map, p * 64, s.u.kvh, row, 0, full);
+              tma_load_4d(dst + p * kPanel, map, p * 64, w.kvh, row, 0, full);
           }
           __syncwarp();
         }
         ring.step();
       };
-      nxt.begin(units);
-      while (true) {
+      auto last_values = [&](int x) {
+        if (left[x] >= 0 && !(shared && x == 1)) load(old, left[x], &maps.v);
+        left[x] = -1;
+      };
+      while (units.next(u)) {
+        const bool narrow = u.n_tok * u.gp <= 128;
+        if (left[1] < left[0]) last_values(1);
+        last_values(0);
+        wait(bars.q_empty(), q_phase, abort);
+        q_phase ^= 1;
+        if (lane == 0) {
+          const bool whole = u.gp == a.H / a.HKV;  // all heads of a key/value head
+          const int toks = 128 / u.gp, tiles = narrow ? 1 : 2;
+          mbar_arrive_expect_tx(bars.q_full(), tiles * kPanels * toks * u.gp * 128);
+          for (int i = 0; i < tiles; i++)
 #pragma unroll
-        for (int x = 0; x < 2; x++) {
-          if (cur.loads(x)) load(cur, cur.tile(x), &maps.v);
-          if (nxt.valid && nxt.step == 0 && x == 0) {
-            wait(bars.q_empty(), q_phase, abort);
-            q_phase ^= 1;
-            if (lane == 0) {
-              const bool whole = nxt.u.gp == a.H / a.HKV;  // all heads of a key/value head
-              const int toks = 128 / nxt.u.gp, tiles = nxt.narrow ? 1 : 2;
-              mbar_arrive_expect_tx(bars.q_full(), tiles * kPanels * toks * nxt.u.gp * 128);
-              for (int i = 0; i < tiles; i++)
-#pragma unroll
-                for (int p = 0; p < kPanels; p++)
-                  tma_load_3d(sQ + i * SM::kTileBytes + p * kPanel, whole ? &maps.q_pack : &maps.q,
-                              p * 64, nxt.u.head0, nxt.u.row0 + i * toks, bars.q_full());
-            }
-            __syncwarp();
-          }
-          if (nxt.loads(x)) load(nxt, nxt.tile(x), &maps.k);
+            for (int p = 0; p < kPanels; p++)
+              tma_load_3d(sQ + i * SM::kTileBytes + p * kPanel, whole ? &maps.q_pack : &maps.q, p * 64,
+                          u.head0, u.row0 + i * toks, bars.q_full());
         }
-        if (!nxt.valid) break;
-        cur = nxt;
-        nxt.advance(units);
+        __syncwarp();
+        load(u, u.t0, &maps.k);
+        last_values(1);
+        if (narrow) {
+          if (u.t0 + 1 < u.t1) load(u, u.t0 + 1, &maps.k);
+          for (int t = u.t0 + 2; t < u.t1; t++) {
+            load(u, t - 2, &maps.v);
+            load(u, t, &maps.k);
+          }
+          const int odd = (u.t1 - 1 - u.t0) & 1;  // which X has the last tile
+          left[0] = u.t1 - 1 - odd;
+          left[1] = u.t0 + 1 < u.t1 ? u.t1 - 2 + odd : -1;
+        } else {
+          for (int t = u.t0; t + 1 < u.t1; t++) {
+            load(u, t, &maps.v);
+            load(u, t + 1, &maps.k);
+          }
+          left[0] = left[1] = u.t1 - 1;
+        }
+        shared = !narrow;
+        old = u;
       }
+      if (left[1] < left[0]) last_values(1);
+      last_values(0);
+      last_values(1);
     } else if (warp == 17) {
       // ---------------------------------------------------------- products
+      // Each X goes through S(0), O(0), S(1), O(1), ...: scores overwrite
+      // weights, so S(i + 1) is issued behind O(i), and the tensor core runs
+      // what it is given in order.  The two X alternate; the last O of a unit
+      // is issued among the first S of the next.
       constexpr uint32_t kIdS = idesc_bf16(128, 128, 0, 0), kIdO = idesc_bf16(128, D, 0, 1);
       Units units{unit_ring, bars, abort, {}};
       Ring<SM::kStages> ring;
       uint32_t q_phase = 0, p_phase[2] = {0, 0};
-      int v_stage = 0, k_stage = 0;
+      AttnUnit u;
+      int left[2] = {-1, -1};  // last tiles of the unit before, their values still to be used
+      int old_len = 0, shared_v = 0;
+      bool shared = false, more[2] = {false, false};  // more: O has been written before
       // A stage is handed back when the softmax answers a product issued after
       // its last use: weights of X that are ready mean that its scores, and
       // everything issued before them, are done.  A commit for each stage costs
-      // the tensor pipe 40 to 120 clocks each (it does not start the next
-      // product before the committed ones are through).
-      int k_done[2] = {-1, -1}, v_done[2] = {-1, -1};
-      auto free_stage = [&](int &stage) {
+      // the tensor pipe 40 to 120 clocks (it does not start the next product
+      // before the committed ones are through).
+      int k_used[2] = {-1, -1}, v_used[2] = {-1, -1};
+      auto hand_back = [&](int &stage) {
         if (stage >= 0 && lane == 0) mbar_arrive(bars.kv_empty(stage));
         stage = -1;
       };
-      Step cur, nxt;
-      cur.valid = false;
-      nxt.begin(units);
-      while (true) {
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
-          if (cur.active(x)) {
-            if (cur.loads(x)) {
-              v_stage = ring.i;
-              wait(bars.kv_full(v_stage), ring.round, abort);
-              ring.step();
-              // weights past the last key are zero, but 0 * NaN is not: clear
-              // the value rows that belong to nobody
-              const int left = cur.u.len - cur.tile(x) * 128;
-              if (left < 128) {
-                const int from = left > 0 ? left : 0;
-                for (int p = 0; p < kPanels; p++) {
-                  uint4 *rows = reinterpret_cast<uint4 *>(sm + SM::kRing + v_stage * SM::kTileBytes +
-                                                          p * kPanel);
-                  for (int i = from * 8 + lane; i < 128 * 8; i += 32) rows[i] = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async();
-                __syncwarp();
-              }
-            }
-            wait(bars.p_ready(x), p_phase[x], abort);
-            p_phase[x] ^= 1;
-            free_stage(k_done[x]);
-            free_stage(v_done[x]);
-            fence_after_sync();
-            const uint32_t v_lo = desc_lo(sRing + v_stage * SM::kTileBytes, kPanel);
-            issue_output(tO + x * D, tS + x * 128, v_lo, kIdO, cur.step > 0, lane == 0);
-            issue_output(tO + x * D, tS + x * 128 + 32, v_lo + 512, kIdO, true, lane == 0);
-            if (cur.last(x)) {
-              if (lane == 0) {
-                if (cur.frees(x)) mma_commit(bars.kv_empty(v_stage));
-                mma_commit(bars.o_full(x));
-              }
-            } else if (cur.frees(x)) {
-              v_done[x] = v_stage;
-            }
-            __syncwarp();
+      auto next_tile = [&] {
+        const int stage = ring.i;
+        wait(bars.kv_full(stage), ring.round, abort);
+        ring.step();
+        return stage;
+      };
+      auto next_values = [&](int tile, int len) {
+        const int stage = next_tile();
+        // weights past the last key are zero, but 0 * NaN is not: clear the
+        // value rows that belong to nobody
+        const int rows = len - tile * 128;
+        if (rows < 128) {
+          for (int p = 0; p < kPanels; p++) {
+            uint4 *to = reinterpret_cast<uint4 *>(sm + SM::kRing + stage * SM::kTileBytes + p * kPanel);
+            for (int i = max(rows, 0) * 8 + lane; i < 128 * 8; i += 32) to[i] = make_uint4(0, 0, 0, 0);
           }
-          if (nxt.active(x)) {
-            if (nxt.step == 0 && x == 0) {
-              wait(bars.q_full(), q_phase, abort);
-              q_phase ^= 1;
-            }
-            if (nxt.loads(x)) {
-              k_stage = ring.i;
-              wait(bars.kv_full(k_stage), ring.round, abort);
-              ring.step();
-            }
-            fence_after_sync();
-            const uint32_t q_lo = desc_lo(sQ + (nxt.narrow ? 0 : x * SM::kTileBytes), 16);
-            const uint32_t k_lo = desc_lo(sRing + k_stage * SM::kTileBytes, 16);
-            issue_scores<true>(tS + x * 128, q_lo, k_lo, kIdS, lane == 0);
-            if (D == 128)
-              issue_scores<false>(tS + x * 128, q_lo + (kPanel >> 4), k_lo + (kPanel >> 4), kIdS, lane == 0);
-            if (nxt.frees(x)) k_done[x] = k_stage;
-            if (lane == 0) {
-              mma_commit(bars.s_full(x));
-              // the last scores of a unit: its queries may be replaced
-              if (nxt.step == nxt.steps - 1 && (x == 1 || !nxt.active(1))) mma_commit(bars.q_empty());
-            }
-            __syncwarp();
-          }
+          fence_proxy_async();
+          __syncwarp();
         }
-        if (!nxt.valid) break;
-        cur = nxt;
-        nxt.advance(units);
+        return stage;
+      };
+      auto weights_ready = [&](int x) {
+        wait(bars.p_ready(x), p_phase[x], abort);
+        p_phase[x] ^= 1;
+        fence_after_sync();
+      };
+      auto scores = [&](int x, int stage, int q_tile) {
+        const uint32_t q_lo = desc_lo(sQ + q_tile * SM::kTileBytes, 16);
+        const uint32_t k_lo = desc_lo(sRing + stage * SM::kTileBytes, 16);
+        fence_after_sync();
+        issue_scores<true>(tS + x * 128, q_lo, k_lo, kIdS, lane == 0);
+        if (D == 128)
+          issue_scores<false>(tS + x * 128, q_lo + (kPanel >> 4), k_lo + (kPanel >> 4), kIdS, lane == 0);
+        if (lane == 0) mma_commit(bars.s_full(x));
+      };
+      auto output = [&](int x, int stage, bool accumulate) {
+        const uint32_t v_lo = desc_lo(sRing + stage * SM::kTileBytes, kPanel);
+        issue_output(tO + x * D, tS + x * 128, v_lo, kIdO, accumulate, lane == 0);
+        issue_output(tO + x * D, tS + x * 128 + 32, v_lo + 512, kIdO, true, lane == 0);
+      };
+      auto last_output = [&](int x) {
+        if (left[x] < 0) return;
+        const bool own = !(shared && x == 1);
+        const int stage = own ? next_values(left[x], old_len) : shared_v;
+        if (own) shared_v = stage;
+        weights_ready(x);
+        hand_back(k_used[x]);
+        hand_back(v_used[x]);
+        output(x, stage, more[x]);
+        if (lane == 0) {
+          if (!shared || x == 1) mma_commit(bars.kv_empty(stage));
+          mma_commit(bars.o_full(x));
+        }
+        __syncwarp();
+        left[x] = -1;
+      };
+      while (units.next(u)) {
+        const bool narrow = u.n_tok * u.gp <= 128;
+        if (left[1] < left[0]) last_output(1);
+        last_output(0);
+        wait(bars.q_full(), q_phase, abort);
+        q_phase ^= 1;
+        int k = next_tile();
+        scores(0, k, 0);
+        last_output(1);
+        if (narrow) {
+          k_used[0] = k;
+          more[0] = u.t0 + 2 < u.t1;
+          more[1] = u.t0 + 3 < u.t1;
+          if (u.t0 + 1 < u.t1) {
+            k_used[1] = next_tile();
+            scores(1, k_used[1], 0);
+          }
+          for (int t0 = u.t0 + 2; t0 < u.t1; t0 += 2) {
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+              const int t = t0 + x;
+              if (t >= u.t1) break;
+              const int v = next_values(t - 2, u.len);
+              weights_ready(x);
+              hand_back(k_used[x]);
+              hand_back(v_used[x]);
+              output(x, v, t >= u.t0 + 4);
+              v_used[x] = v;
+              k_used[x] = next_tile();
+              scores(x, k_used[x], 0);
+            }
+          }
+          const int odd = (u.t1 - 1 - u.t0) & 1;  // which X has the last tile
+          left[0] = u.t1 - 1 - odd;
+          left[1] = u.t0 + 1 < u.t1 ? u.t1 - 2 + odd : -1;
+        } else {
+          scores(1, k, 1);
+          int v_old = -1;
+          for (int t = u.t0; t + 1 < u.t1; t++) {
+            const int v = next_values(t, u.len);
+            weights_ready(0);
+            output(0, v, t > u.t0);
+            const int k_next = next_tile();
+            scores(0, k_next, 0);
+            weights_ready(1);
+            hand_back(k);
+            hand_back(v_old);
+            output(1, v, t > u.t0);
+            scores(1, k_next, 1);
+            k = k_next;
+            v_old = v;
+          }
+          k_used[1] = k;
+          v_used[1] = v_old;
+          more[0] = more[1] = u.t0 + 1 < u.t1;
+          left[0] = left[1] = u.t1 - 1;
+        }
+        if (lane == 0) mma_commit(bars.q_empty());  // behind the last scores: the queries may be replaced
+        __syncwarp();
+        shared = !narrow;
+        old_len = u.len;
       }
+      if (left[1] < left[0]) last_output(1);
+      last_output(0);
+      last_output(1);
     }
   }
   fence_before_sync();

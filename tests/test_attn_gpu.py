@@ -205,6 +205,18 @@ def test_long_cache_is_split_and_joined(dtype, nq):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_units_for_each_block(d):
+    """Far more sequences and heads than blocks, with one to nine key tiles each (odd numbers next
+    to even ones): every block goes through many units in a row."""
+    dt, H, HKV, page = torch.bfloat16, 16, 8, 64
+    kv = [1 + (i * 397) % 1150 for i in range(90)]
+    q_lens = [1 + (i % 3) * (i % 2) for i in range(90)]
+    kv = [max(a, b) for a, b in zip(kv, q_lens)]
+    x = paged(q_lens, kv, H, HKV, d, page, dt, seed=d)
+    check_paged(run_paged(x), x, q_lens, d, dt)
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 def test_append_then_attend_equals_prompt(dtype):
     """A prompt written to pages in two chunks and attended to chunk by chunk gives the whole
