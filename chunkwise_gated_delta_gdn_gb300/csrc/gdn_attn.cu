@@ -251,16 +251,6 @@ __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const Att
   if (!finite && a.flags) atomicOr(a.flags, kFlagNonfinite);
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    (void)cudaGetLastError();  // no device: sizes can still be asked for
-    return 152;
-  }
-  return n;
-}
-
 template <class S, int D, bool BF16>
 cudaError_t merge(const AttnArgs &a, int blocks, cudaStream_t stream) {
   gdn_attn_merge_kernel<S, D, BF16><<<dim3(blocks - 1, 4), kMergeThreads, 0, stream>>>(a, blocks);
@@ -268,32 +258,77 @@ cudaError_t merge(const AttnArgs &a, int blocks, cudaStream_t stream) {
 }
 
 template <int D>
+std::atomic<uint64_t> allowed{0};
+
+template <int D>
 cudaError_t launch(const AttnArgs &a, int blocks, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(
-      gdn_attn_warp_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+  const cudaError_t e = allow_smem(reinterpret_cast<const void *>(&gdn_attn_warp_kernel<D>),
+                                   smem_bytes<D>(), allowed<D>);
   if (e != cudaSuccess) return e;
   gdn_attn_warp_kernel<D><<<blocks, kThreads, smem_bytes<D>(), stream>>>(a);
   return cudaGetLastError();
 }
 
+template <class S>
+AttnLaunch plan_launch(AttnArgs &a, int blocks) {
+  AttnLaunch l;
+  l.blocks = blocks;
+  l.rows = S::kRows;
+  a.plan_total = 0;
+  // Nothing is cut when every unit fits the smallest grain and gets a block.
+  const long long units = attn_most_units<S>(a);
+  const int longest = a.kv_lens ? a.max_len : (a.cu ? a.Ttot : a.T);
+  l.split = !(AttnPlan<S>::tiles(longest) <= 1 << kMinGrain && units <= blocks);
+  if (!l.split) l.blocks = units < 1 ? 1 : (int)units;
+  if (!a.cu && !a.kv_lens && a.T > 0) l.split = attn_plan_prompts<S>(a, l.blocks);
+  return l;
+}
+
 }  // namespace
 
-int attn_blocks(int dtype, int d) { return dtype ? sm_count() : sm_count() * (d == 64 ? 4 : 2); }
-int attn_part_rows(int dtype) { return dtype ? TcShape::kRows : WarpShape::kRows; }
-
-cudaError_t launch_attn(const AttnArgs &a, int d, int dtype, cudaStream_t stream) {
-  if (d != 64 && d != 128) return cudaErrorInvalidValue;
-  const int blocks = attn_blocks(dtype, d);
-  cudaError_t e;
-  if (dtype) {
-    if ((e = launch_attn_tc(a, d, blocks, stream)) != cudaSuccess) return e;
-    return d == 64 ? merge<TcShape, 64, true>(a, blocks, stream)
-                   : merge<TcShape, 128, true>(a, blocks, stream);
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess) {
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) {
+      if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+      return n;
+    }
   }
-  if ((e = d == 64 ? launch<64>(a, blocks, stream) : launch<128>(a, blocks, stream)) != cudaSuccess)
-    return e;
-  return d == 64 ? merge<WarpShape, 64, false>(a, blocks, stream)
-                 : merge<WarpShape, 128, false>(a, blocks, stream);
+  (void)cudaGetLastError();  // no device: sizes can still be asked for
+  return 152;
+}
+
+cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+AttnLaunch attn_launch(AttnArgs &a, int d, int dtype) {
+  return dtype ? plan_launch<TcShape>(a, sm_count())
+               : plan_launch<WarpShape>(a, sm_count() * (d == 64 ? 4 : 2));
+}
+
+cudaError_t launch_attn(const AttnArgs &a, int d, int dtype, const AttnLaunch &l,
+                        cudaStream_t stream) {
+  cudaError_t e;
+  if (dtype)
+    e = launch_attn_tc(a, d, l.blocks, stream);
+  else
+    e = d == 64 ? launch<64>(a, l.blocks, stream) : launch<128>(a, l.blocks, stream);
+  if (e != cudaSuccess || !l.split || l.blocks < 2) return e;
+  if (dtype)
+    return d == 64 ? merge<TcShape, 64, true>(a, l.blocks, stream)
+                   : merge<TcShape, 128, true>(a, l.blocks, stream);
+  return d == 64 ? merge<WarpShape, 64, false>(a, l.blocks, stream)
+                 : merge<WarpShape, 128, false>(a, l.blocks, stream);
 }
 
 }  // namespace gdn

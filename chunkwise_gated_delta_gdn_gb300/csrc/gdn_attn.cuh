@@ -42,7 +42,7 @@ template <int ROWS, int PACK, int TILE, int WIDE, int OVER>
 struct AttnShape {
   static constexpr int kRows = ROWS, kPack = PACK, kTile = TILE, kWide = WIDE, kOver = OVER;
 };
-constexpr int kMinGrain = 2;   // log2 of the smallest grain of a small call
+constexpr int kMinGrain = 3;   // log2 of the smallest grain of a small call
 constexpr int kMaxGrain = 6;   // log2 of the largest one that is tried
 
 struct AttnSeq {
@@ -199,15 +199,41 @@ struct AttnPlan {
       const int mid = (lo + hi + 1) >> 1;
       if (prefix(s.base, mid) * wide + (long long)mid * over <= rem) lo = mid; else hi = mid - 1;
     }
-    const int first = lo << tok_log;
+    place(s, group, lo, u);
+    return group * per_group + prefix(s.base, lo) * wide + (long long)lo * over;
+  }
+  // token tile `tile` of head group `group` of an unpacked sequence
+  __host__ __device__ void place(const AttnSeq &s, int group, int tile, AttnUnit &u) const {
+    const int first = tile << tok_log;
     u.n_tok = s.nq - first < (1 << tok_log) ? s.nq - first : 1 << tok_log;
     u.nt = tiles(s.base + first + u.n_tok);
     u.gp = gp;
     u.head0 = group * gp;
-    u.kvh = u.head0 / G;
+    u.kvh = group / (G / gp);
     u.row0 = s.q0 + first;
     u.pos0 = s.past + first;
-    return group * per_group + prefix(s.base, lo) * wide + (long long)lo * over;
+  }
+  // the unit behind u in the same sequence; false when u is the last one
+  __host__ __device__ bool after(const AttnSeq &s, AttnUnit &u) const {
+    if (packed(s)) {
+      if (u.kvh + 1 == HKV) return false;
+      u.kvh++;
+      u.head0 += G;
+      return true;
+    }
+    const int tile = (u.row0 - s.q0) >> tok_log;
+    int group = u.head0 / gp;
+    if (tile + 1 < token_tiles(s)) {
+      place(s, group, tile + 1, u);
+    } else {
+      if (group + 1 == groups) return false;
+      place(s, group + 1, 0, u);
+    }
+    return true;
+  }
+  // cost of unit u
+  __host__ __device__ long long unit_cost(const AttnSeq &s, const AttnUnit &u) const {
+    return over + (long long)((u.nt + (1 << shift) - 1) >> shift) * (packed(s) ? 1 : wide);
   }
   // first tile at or after cost c of a unit that begins at cost u0
   __host__ __device__ int cut(const AttnSeq &s, long long u0, int nt, long long c) const {
@@ -238,7 +264,8 @@ struct AttnPlan {
     // a grain of up to kSlack tiles more than an equal share costs less than a
     // second unit's start and end
     constexpr int kSlack = 4;
-    for (int log = kMinGrain; log <= kMaxGrain && (1 << log) <= share + kSlack; log++) {
+    for (int log = kMinGrain; log <= kMaxGrain; log++) {
+      if (log > kMinGrain && (1 << log) > share + kSlack) break;
       if ((2LL << log) < share / S::kWide) continue;  // far too many grains
       const long long n = pieces(log);
       if (n <= n_blocks) {
@@ -266,33 +293,53 @@ __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &
                                                 long long block, int n_blocks) {
   const int lane = threadIdx.x & 31;
   constexpr uint32_t kAll = 0xffffffffu;
-  bool any_bad = lane == 0 && a.cu && (a.cu[0] != 0 || a.cu[a.n_seqs] != a.Ttot);
-  auto sum = [&](bool check) {
-    long long mine = 0;
-    for (int n = lane; n < a.n_seqs; n += 32) {
-      bool bad;
-      mine += plan.cost(attn_seq(a, n, bad));
-      if (check) any_bad |= bad;
+  AttnStart r;
+  r.seq = a.n_seqs;
+  r.seq0 = 0;
+  bool bad;
+  if (a.plan_total) {  // equal prompts: the host has made the plan
+    plan.shift = a.plan_shift;
+    if (a.plan_grains) plan.grains(a.plan_shift);
+    plan.per = a.plan_per;
+    r.total = a.plan_total;
+    const long long c = block * plan.per;
+    if (c < r.total) {
+      r.seq = (int)attn_div(c, a.plan_seq);
+      r.seq0 = r.seq * a.plan_seq;
     }
+    return r;
+  }
+  const AttnSeq own = attn_seq(a, min(lane, a.n_seqs - 1), bad);  // of up to 32 sequences, all
+  bool any_bad = bad || (lane == 0 && a.cu && (a.cu[0] != 0 || a.cu[a.n_seqs] != a.Ttot));
+  auto cost_of = [&](int n) {
+    if (n < 32) return plan.cost(own);
+    const AttnSeq s = attn_seq(a, n, bad);
+    any_bad |= bad;
+    return plan.cost(s);
+  };
+  auto sum = [&] {
+    if (a.n_seqs == 1) return plan.cost(own);
+    long long mine = 0;
+    for (int n = lane; n < a.n_seqs; n += 32) mine += cost_of(n);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(kAll, mine, d);
     return mine;
   };
-  AttnStart r;
-  r.total = plan.choose(sum(true), n_blocks, [&](int log) {
+  r.total = plan.choose(sum(), n_blocks, [&](int log) {
     plan.grains(log);
-    return sum(false);
+    return sum();
   });
   if (any_bad && a.flags && block == 0) atomicOr(a.flags, kFlagBadSeqlens);
-  r.seq = a.n_seqs;
-  r.seq0 = 0;
   const long long c = block * plan.per;
   if (c >= r.total) return r;
+  if (a.n_seqs == 1) {
+    r.seq = 0;
+    return r;
+  }
   long long before = 0;
   for (int n0 = 0; n0 < a.n_seqs; n0 += 32) {
-    bool bad;
     const int n = n0 + lane;
-    const long long mine = n < a.n_seqs ? plan.cost(attn_seq(a, n, bad)) : 0;
+    const long long mine = n < a.n_seqs ? cost_of(n) : 0;
     long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -318,42 +365,80 @@ struct AttnWalk {
   const AttnArgs &a;
   const AttnPlan<S> &plan;
   AttnSeq s;
-  long long at, end, seq0, seq_cost;  // next cost, end of the range, current sequence's span
-  int seq, block;
+  AttnUnit u;
+  long long at, end, u0;  // start and end of the range, start of the unit
+  int block;
+  bool more;              // u is a unit that is still to be looked at
 
   __host__ __device__ AttnWalk(const AttnArgs &a_, const AttnPlan<S> &p_, const AttnStart &st,
                                int block_)
       : a(a_), plan(p_), block(block_) {
-    seq = st.seq;
-    seq0 = st.seq0;
     at = block * plan.per;
     end = at + plan.per < st.total ? at + plan.per : st.total;
-    if (seq < a.n_seqs) load();
+    more = st.seq < a.n_seqs;
+    if (more) {
+      bool bad;
+      s = attn_seq(a, st.seq, bad);
+      u0 = st.seq0 + plan.find(s, st.seq, at - st.seq0, u);
+    }
   }
-  __host__ __device__ void load() {
-    bool bad;
-    s = attn_seq(a, seq, bad);
-    seq_cost = plan.cost(s);
-  }
-  __host__ __device__ bool next(AttnUnit &u) {
-    while (at < end) {
-      while (at >= seq0 + seq_cost) {
-        seq0 += seq_cost;
-        if (++seq >= a.n_seqs) return false;
-        load();
+  __host__ __device__ bool next(AttnUnit &out) {
+    while (more && u0 < end) {
+      out = u;
+      out.t0 = plan.cut(s, u0, u.nt, at);
+      out.t1 = plan.cut(s, u0, u.nt, end);
+      out.slot = out.t0 > 0 ? 2 * block : (out.t1 < u.nt ? 2 * block + 1 : -1);
+      u0 += plan.unit_cost(s, u);
+      if (!plan.after(s, u)) {
+        int seq = u.seq;
+        more = false;
+        while (++seq < a.n_seqs) {
+          bool bad;
+          s = attn_seq(a, seq, bad);
+          if (s.nq > 0) {
+            plan.find(s, seq, 0, u);
+            more = true;
+            break;
+          }
+        }
       }
-      const long long u0 = seq0 + plan.find(s, seq, at - seq0, u);
-      u.t0 = plan.cut(s, u0, u.nt, at);
-      u.t1 = plan.cut(s, u0, u.nt, end);
-      // the range may end inside this unit, or take all of it
-      at = u0 + plan.over +
-           (long long)((u.nt + (1 << plan.shift) - 1) >> plan.shift) * (plan.packed(s) ? 1 : plan.wide);
-      if (u.t0 >= u.t1) continue;
-      u.slot = u.t0 > 0 ? 2 * block : (u.t1 < u.nt ? 2 * block + 1 : -1);
-      return true;
+      if (out.t0 < out.t1) return true;
     }
     return false;
   }
 };
+
+// The plan of equal prompts (lengths that the host knows), into `a`; returns
+// whether a unit may be cut between blocks.
+template <class S>
+inline bool attn_plan_prompts(AttnArgs &a, int n_blocks) {
+  AttnPlan<S> plan(a.H, a.HKV);
+  bool bad;
+  const AttnSeq s = attn_seq(a, 0, bad);
+  a.plan_total = plan.choose(plan.cost(s) * a.n_seqs, n_blocks, [&](int log) {
+    plan.grains(log);
+    return plan.cost(s) * a.n_seqs;
+  });
+  a.plan_seq = plan.cost(s);
+  a.plan_per = plan.per;
+  a.plan_shift = plan.shift;
+  a.plan_grains = plan.over == 0;
+  return !(a.plan_grains && plan.tiles(s.nq) <= 1 << plan.shift);
+}
+
+// Most units that a call can have, from what the host knows.
+template <class S>
+inline long long attn_most_units(const AttnArgs &a) {
+  const AttnPlan<S> plan(a.H, a.HKV);
+  const long long groups = plan.groups > a.HKV ? plan.groups : a.HKV;
+  if (!a.cu) {
+    bool bad;
+    AttnArgs one = a;
+    one.kv_lens = nullptr;
+    const AttnSeq s = attn_seq(one, 0, bad);
+    return a.n_seqs * (plan.packed(s) ? (long long)a.HKV : (long long)plan.groups * plan.token_tiles(s));
+  }
+  return a.n_seqs * groups + (long long)plan.groups * (a.Ttot >> plan.tok_log);
+}
 
 }  // namespace gdn

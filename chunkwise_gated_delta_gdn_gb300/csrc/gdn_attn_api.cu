@@ -39,8 +39,9 @@ gdn_status check_cache(int page_size, int max_pages, int n_pages) {
   return GDN_OK;
 }
 
-size_t part_bytes(int d, int dtype) {
-  const size_t rows = (size_t)2 * gdn::attn_blocks(dtype, d) * gdn::attn_part_rows(dtype);
+size_t part_bytes(const gdn::AttnLaunch &l, int d) {
+  if (!l.split) return 0;
+  const size_t rows = (size_t)2 * l.blocks * l.rows;
   return rows * d * sizeof(float) + rows * sizeof(float2);
 }
 
@@ -71,19 +72,30 @@ bool disjoint(const Buf (&outs)[NO], const Buf (&ins)[NI]) {
 
 // Everything that both attention entries share once their own arguments are
 // checked.
-gdn_status launch(gdn::AttnArgs &a, int d, int dtype, float scale, void *workspace,
-                  gdn_stream_t stream_) {
+gdn_status launch(gdn::AttnArgs &a, int d, int dtype, float scale, const gdn::AttnLaunch &l,
+                  void *workspace, gdn_stream_t stream_) {
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (a.flags && cudaMemsetAsync(a.flags, 0, sizeof(uint32_t), stream) != cudaSuccess)
     return GDN_ERR_CUDA;
   if (a.Ttot == 0) return GDN_OK;
-  const size_t rows = (size_t)2 * gdn::attn_blocks(dtype, d) * gdn::attn_part_rows(dtype);
+  const size_t rows = (size_t)2 * l.blocks * l.rows;
   a.scale = scale;
   a.scale_log2 = scale * 1.44269504088896340736f;
   a.part_o = static_cast<float4 *>(workspace);
   a.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + rows * d * sizeof(float));
-  return gdn::launch_attn(a, d, dtype, stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return gdn::launch_attn(a, d, dtype, l, stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
+
+// What the plan goes by.
+void fill_shape(gdn::AttnArgs &a, const int32_t *cu, int n, int T, long Ttot, int H, int HKV) {
+  a.cu = cu;
+  a.n_seqs = n;
+  a.T = T;
+  a.Ttot = (int)Ttot;
+  a.H = H;
+  a.HKV = HKV;
+}
+const int32_t kSomewhere[1] = {0};  // stands for device arrays in a workspace query: not read
 
 }  // namespace
 
@@ -94,7 +106,15 @@ size_t gdn_attn_fwd_workspace_bytes(int B, int T, int H, int HKV, int d, int n_s
   long Ttot;
   const bool packed = B == 1 && n_seqs > 1;
   if (check_shape(B, T, H, HKV, d, n_seqs, packed, dtype, n, Ttot) != GDN_OK) return 0;
-  return part_bytes(d, dtype);
+  // one sequence may come with or without cu_seqlens: the larger of the two
+  size_t most = 0;
+  for (int with_cu = packed || B == 1 ? 1 : 0; with_cu >= (packed ? 1 : 0); with_cu--) {
+    gdn::AttnArgs a{};
+    fill_shape(a, with_cu ? kSomewhere : nullptr, n, T, Ttot, H, HKV);
+    const size_t bytes = part_bytes(gdn::attn_launch(a, d, dtype), d);
+    if (bytes > most) most = bytes;
+  }
+  return most;
 }
 
 gdn_status gdn_attn_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
@@ -117,7 +137,10 @@ gdn_status gdn_attn_fwd(const void *q, const void *k, const void *v, void *o, fl
   if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(o, 16) ||
       !aligned_to(lse, 4) || !aligned_to(cu_seqlens, 4) || !aligned_to(flags, 4))
     return GDN_ERR_INVALID_ARG;
-  const size_t ws = part_bytes(d, dtype);
+  gdn::AttnArgs a{};
+  fill_shape(a, cu_seqlens, n, T, Ttot, H, HKV);
+  const gdn::AttnLaunch l = gdn::attn_launch(a, d, dtype);
+  const size_t ws = part_bytes(l, d);
   if (ws > 0 && (!workspace || workspace_bytes < ws)) return GDN_ERR_WORKSPACE;
   if (!aligned_to(workspace, 256)) return GDN_ERR_INVALID_ARG;
   const Buf outs[] = {{o, (size_t)Ttot * q_row * es}, {lse, (size_t)Ttot * H * 4}, {flags, 4},
@@ -126,12 +149,10 @@ gdn_status gdn_attn_fwd(const void *q, const void *k, const void *v, void *o, fl
                      {v, span(Ttot, v_stride, kv_row, es)},
                      {cu_seqlens, cu_seqlens ? ((size_t)n + 1) * 4 : 0}};
   if (!disjoint(outs, ins)) return GDN_ERR_INVALID_ARG;
-  gdn::AttnArgs a{};
-  a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse; a.cu = cu_seqlens;
-  a.n_seqs = n; a.T = T; a.Ttot = (int)Ttot; a.H = H; a.HKV = HKV;
+  a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
   a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
   a.flags = flags;
-  return launch(a, d, dtype, scale, workspace, stream);
+  return launch(a, d, dtype, scale, l, workspace, stream);
 }
 
 size_t gdn_attn_paged_fwd_workspace_bytes(int B, int T, int H, int HKV, int d, int n_seqs,
@@ -141,7 +162,16 @@ size_t gdn_attn_paged_fwd_workspace_bytes(int B, int T, int H, int HKV, int d, i
   const bool packed = B == 1 && n_seqs > 1;
   if (check_shape(B, T, H, HKV, d, n_seqs, packed, dtype, n, Ttot) != GDN_OK) return 0;
   if (check_cache(page_size, max_pages, 1) != GDN_OK) return 0;
-  return part_bytes(d, dtype);
+  size_t most = 0;
+  for (int with_cu = packed || B == 1 ? 1 : 0; with_cu >= (packed ? 1 : 0); with_cu--) {
+    gdn::AttnArgs a{};
+    fill_shape(a, with_cu ? kSomewhere : nullptr, n, T, Ttot, H, HKV);
+    a.kv_lens = kSomewhere;
+    a.max_len = page_size * max_pages;
+    const size_t bytes = part_bytes(gdn::attn_launch(a, d, dtype), d);
+    if (bytes > most) most = bytes;
+  }
+  return most;
 }
 
 gdn_status gdn_attn_paged_fwd(const void *q, const void *k_cache, const void *v_cache,
@@ -165,7 +195,12 @@ gdn_status gdn_attn_paged_fwd(const void *q, const void *k_cache, const void *v_
       !aligned_to(o, 16) || !aligned_to(block_table, 4) || !aligned_to(kv_lens, 4) ||
       !aligned_to(lse, 4) || !aligned_to(cu_seqlens, 4) || !aligned_to(flags, 4))
     return GDN_ERR_INVALID_ARG;
-  const size_t ws = part_bytes(d, dtype);
+  gdn::AttnArgs a{};
+  fill_shape(a, cu_seqlens, n, T, Ttot, H, HKV);
+  a.kv_lens = kv_lens;
+  a.max_len = page_size * max_pages;
+  const gdn::AttnLaunch l = gdn::attn_launch(a, d, dtype);
+  const size_t ws = part_bytes(l, d);
   if (ws > 0 && (!workspace || workspace_bytes < ws)) return GDN_ERR_WORKSPACE;
   if (!aligned_to(workspace, 256)) return GDN_ERR_INVALID_ARG;
   const size_t cache = (size_t)n_pages * page_size * kv_row * es;
@@ -175,15 +210,11 @@ gdn_status gdn_attn_paged_fwd(const void *q, const void *k_cache, const void *v_
                      {block_table, (size_t)n * max_pages * 4}, {kv_lens, (size_t)n * 4},
                      {cu_seqlens, cu_seqlens ? ((size_t)n + 1) * 4 : 0}};
   if (!disjoint(outs, ins)) return GDN_ERR_INVALID_ARG;
-  gdn::AttnArgs a{};
-  a.q = q; a.k = k_cache; a.v = v_cache; a.o = o; a.lse = lse;
-  a.cu = cu_seqlens; a.kv_lens = kv_lens; a.table = block_table;
-  a.n_seqs = n; a.T = T; a.Ttot = (int)Ttot; a.H = H; a.HKV = HKV;
+  a.q = q; a.k = k_cache; a.v = v_cache; a.o = o; a.lse = lse; a.table = block_table;
   a.q_stride = q_stride;
   a.page_size = page_size; a.max_pages = max_pages; a.n_pages = n_pages;
-  a.max_len = page_size * max_pages;
   a.flags = flags;
-  return launch(a, d, dtype, scale, workspace, stream);
+  return launch(a, d, dtype, scale, l, workspace, stream);
 }
 
 gdn_status gdn_kv_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,

@@ -22,6 +22,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "gdn_attn.cuh"
 #include "gdn_sm100.cuh"
 
@@ -49,7 +51,8 @@ struct Smem {
   // swap x2, halves x8, unit full x4, unit empty x4, tile full, tile empty
   static constexpr int kBarCount = 18 + 2 * kUnits + 2 * kStages;
   static constexpr int kSlot = kBars + kBarCount * 8;
-  static constexpr int kBytes = kSlot + 16;
+  static constexpr int kUsed = kSlot + 8;  // [X] int2: stages that the scores free
+  static constexpr int kBytes = kUsed + 16;
 };
 static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "shared memory of one SM");
 
@@ -198,6 +201,46 @@ struct Units {
   }
 };
 
+// N fp32 values of every lane's row as bf16 to columns [c, c + N) of its row
+// `out`.  Written as they lie, a 16-byte piece per lane and instruction, every
+// instruction touches 32 cache lines; so N / 8 neighbouring lanes exchange
+// pieces first, and each instruction writes whole 2 N byte stretches of rows.
+template <int N>
+__device__ __forceinline__ void store_rows(const float (&y)[N], __nv_bfloat16 *out, bool valid, int c) {
+  constexpr int kPieces = N / 8;  // 16-byte pieces of a row, and lanes that share them: 2 or 4
+  const int lane = threadIdx.x & 31, me = lane & (kPieces - 1);
+  uint4 p[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; i++)
+    p[i] = make_uint4(pack2(y[8 * i], y[8 * i + 1]), pack2(y[8 * i + 2], y[8 * i + 3]),
+                      pack2(y[8 * i + 4], y[8 * i + 5]), pack2(y[8 * i + 6], y[8 * i + 7]));
+  auto swap = [](uint4 &keep, uint4 &give, bool upper, int mask) {
+    // a lane keeps one of two pieces and gives the other to its partner
+    const uint4 send = upper ? keep : give;
+    uint4 got;
+    got.x = __shfl_xor_sync(0xffffffffu, send.x, mask);
+    got.y = __shfl_xor_sync(0xffffffffu, send.y, mask);
+    got.z = __shfl_xor_sync(0xffffffffu, send.z, mask);
+    got.w = __shfl_xor_sync(0xffffffffu, send.w, mask);
+    if (upper) keep = got; else give = got;
+  };
+  // transposes the pieces of kPieces rows: afterwards p[i] is piece `me` of the
+  // row of the group's lane i
+#pragma unroll
+  for (int step = 1; step < kPieces; step <<= 1)
+#pragma unroll
+    for (int i = 0; i < kPieces; i++)
+      if (!(i & step)) swap(p[i], p[i | step], (me & step) != 0, step);
+  const unsigned long long at = reinterpret_cast<unsigned long long>(out);
+#pragma unroll
+  for (int i = 0; i < kPieces; i++) {
+    const int from = (lane & ~(kPieces - 1)) | i;
+    const unsigned long long row = __shfl_sync(0xffffffffu, at, from);
+    const bool ok = __shfl_sync(0xffffffffu, valid ? 1 : 0, from);
+    if (ok) *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(row) + c + me * 8) = p[i];
+  }
+}
+
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     gdn_attn_tc_kernel(const AttnArgs a, const __grid_constant__ Maps maps, const int box) {
@@ -214,12 +257,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *abort = reinterpret_cast<volatile int *>(slot + 1);
   AttnUnit *unit_ring = reinterpret_cast<AttnUnit *>(sm + SM::kUnit);
   float *row_ex = reinterpret_cast<float *>(sm + SM::kRow);
+  int2 *used = reinterpret_cast<int2 *>(sm + SM::kUsed);
   if (tid == 0) {
     *abort = 0;
     mbar_init(bars.q_full(), 1);
     mbar_init(bars.q_empty(), 1);
     for (int x = 0; x < 2; x++) {
-      mbar_init(bars.s_full(x), 1);
+      mbar_init(bars.s_full(x), 2);  // the products' commit, and the stages they free
       mbar_init(bars.p_ready(x), 8);
       mbar_init(bars.o_full(x), 1);
       mbar_init(bars.swap(x), 16);
@@ -235,6 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_fence_init();
   }
+  if (warp == 16 && lane < 4)
+    prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : &maps.q_pack);
   if (warp == 17) tmem_alloc(smem_addr(slot), 512);
   fence_before_sync();
   __syncthreads();
@@ -285,6 +331,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(bars.s_full(x), s_phase, abort);
         s_phase ^= 1;
         fence_after_sync();
+        if (half == 0 && quarter == 0 && lane == 0) {
+          // These scores, and everything issued before them, are done: hand
+          // back the stages that they were the last to read.
+          const int2 stage = used[x];
+          if (stage.x >= 0) mbar_arrive(bars.kv_empty(stage.x));
+          if (stage.y >= 0) mbar_arrive(bars.kv_empty(stage.y));
+        }
         uint32_t raw[2][32];
         tmem_ld32_nowait(s_at, raw[0]);
         tmem_ld32_nowait(s_at + 32, raw[1]);
@@ -393,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool part = u.slot >= 0;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const long long at = (long long)(u.row0 + tok) * a.H + u.head0 + row % u.gp;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + at * D;
         bool finite = true;
         // each half writes half of the columns; of a joined output, each X half of those
         constexpr int kCols = D / 4;
@@ -415,17 +469,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kCols / 4; i++)
               a.part_o[((long long)u.slot * (D / 4) + (c >> 2) + i) * TcShape::kRows + row] =
                   make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-          } else if (valid) {
-            uint4 *to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + c);
+          }
+          if (!part) {
 #pragma unroll
-            for (int i = 0; i < kCols; i++) {
-              y[i] *= inv;
-              finite &= isfinite(y[i]);
+            for (int i = 0; i < kCols; i++) y[i] *= inv;
+            if (a.flags && valid) {
+#pragma unroll
+              for (int i = 0; i < kCols; i++) finite &= isfinite(y[i]);
             }
-#pragma unroll
-            for (int i = 0; i < kCols / 8; i++)
-              to[i] = make_uint4(pack2(y[8 * i], y[8 * i + 1]), pack2(y[8 * i + 2], y[8 * i + 3]),
-                                 pack2(y[8 * i + 4], y[8 * i + 5]), pack2(y[8 * i + 6], y[8 * i + 7]));
+            store_rows<kCols>(y, out, valid, c);
           }
           __syncwarp();
         }
@@ -465,9 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 16) {
       // ------------------------------------------------------------- loads
-      // The order of the tiles is that of the products below.  A unit's last
-      // tiles go in the order of the keys: the stages of the earlier one are
-      // handed back first, and the ring needs them for what follows.
+      // The order of the tiles is that of the products below; a unit's last
+      // tiles go in the order of the keys.
       Units units{unit_ring, bars, abort, {}};
       Ring<SM::kStages> ring;
       uint32_t q_phase = 1;
@@ -570,16 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int left[2] = {-1, -1};  // last tiles of the unit before, their values still to be used
       int old_len = 0, shared_v = 0;
       bool shared = false, more[2] = {false, false};  // more: O has been written before
-      // A stage is handed back when the softmax answers a product issued after
-      // its last use: weights of X that are ready mean that its scores, and
-      // everything issued before them, are done.  A commit for each stage costs
-      // the tensor pipe 40 to 120 clocks (it does not start the next product
-      // before the committed ones are through).
-      int k_used[2] = {-1, -1}, v_used[2] = {-1, -1};
-      auto hand_back = [&](int &stage) {
-        if (stage >= 0 && lane == 0) mbar_arrive(bars.kv_empty(stage));
-        stage = -1;
-      };
+      // A stage goes back to the loader once scores issued after its last use
+      // are there: the softmax, which waits for them anyway, arrives for it.  A
+      // commit for each stage costs the tensor pipe 40 to 120 clocks (it does
+      // not start the next product before the committed ones are through).
       auto next_tile = [&] {
         const int stage = ring.i;
         wait(bars.kv_full(stage), ring.round, abort);
@@ -606,14 +651,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         p_phase[x] ^= 1;
         fence_after_sync();
       };
-      auto scores = [&](int x, int stage, int q_tile) {
+      auto scores = [&](int x, int stage, int q_tile, int free_k, int free_v) {
         const uint32_t q_lo = desc_lo(sQ + q_tile * SM::kTileBytes, 16);
         const uint32_t k_lo = desc_lo(sRing + stage * SM::kTileBytes, 16);
         fence_after_sync();
         issue_scores<true>(tS + x * 128, q_lo, k_lo, kIdS, lane == 0);
         if (D == 128)
           issue_scores<false>(tS + x * 128, q_lo + (kPanel >> 4), k_lo + (kPanel >> 4), kIdS, lane == 0);
-        if (lane == 0) mma_commit(bars.s_full(x));
+        if (lane == 0) {
+          mma_commit(bars.s_full(x));
+          used[x] = make_int2(free_k, free_v);
+          mbar_arrive(bars.s_full(x));
+        }
       };
       auto output = [&](int x, int stage, bool accumulate) {
         const uint32_t v_lo = desc_lo(sRing + stage * SM::kTileBytes, kPanel);
@@ -626,8 +675,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int stage = own ? next_values(left[x], old_len) : shared_v;
         if (own) shared_v = stage;
         weights_ready(x);
-        hand_back(k_used[x]);
-        hand_back(v_used[x]);
         output(x, stage, more[x]);
         if (lane == 0) {
           if (!shared || x == 1) mma_commit(bars.kv_empty(stage));
@@ -642,16 +689,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         last_output(0);
         wait(bars.q_full(), q_phase, abort);
         q_phase ^= 1;
-        int k = next_tile();
-        scores(0, k, 0);
+        const int k = next_tile();
+        scores(0, k, 0, narrow ? k : -1, -1);
         last_output(1);
         if (narrow) {
-          k_used[0] = k;
           more[0] = u.t0 + 2 < u.t1;
           more[1] = u.t0 + 3 < u.t1;
           if (u.t0 + 1 < u.t1) {
-            k_used[1] = next_tile();
-            scores(1, k_used[1], 0);
+            const int k1 = next_tile();
+            scores(1, k1, 0, k1, -1);
           }
           for (int t0 = u.t0 + 2; t0 < u.t1; t0 += 2) {
 #pragma unroll
@@ -660,36 +706,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (t >= u.t1) break;
               const int v = next_values(t - 2, u.len);
               weights_ready(x);
-              hand_back(k_used[x]);
-              hand_back(v_used[x]);
               output(x, v, t >= u.t0 + 4);
-              v_used[x] = v;
-              k_used[x] = next_tile();
-              scores(x, k_used[x], 0);
+              const int k_next = next_tile();
+              scores(x, k_next, 0, k_next, v);
             }
           }
           const int odd = (u.t1 - 1 - u.t0) & 1;  // which X has the last tile
           left[0] = u.t1 - 1 - odd;
           left[1] = u.t0 + 1 < u.t1 ? u.t1 - 2 + odd : -1;
         } else {
-          scores(1, k, 1);
-          int v_old = -1;
+          scores(1, k, 1, k, -1);
           for (int t = u.t0; t + 1 < u.t1; t++) {
             const int v = next_values(t, u.len);
             weights_ready(0);
             output(0, v, t > u.t0);
             const int k_next = next_tile();
-            scores(0, k_next, 0);
+            scores(0, k_next, 0, -1, -1);
             weights_ready(1);
-            hand_back(k);
-            hand_back(v_old);
             output(1, v, t > u.t0);
-            scores(1, k_next, 1);
-            k = k_next;
-            v_old = v;
+            scores(1, k_next, 1, k_next, v);
           }
-          k_used[1] = k;
-          v_used[1] = v_old;
           more[0] = more[1] = u.t0 + 1 < u.t1;
           left[0] = left[1] = u.t1 - 1;
         }
@@ -738,9 +774,12 @@ bool make_maps(Maps &m, const AttnArgs &a, int d, int box) {
 }
 
 template <int D, bool PAGED>
+std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use its shared memory
+
+template <int D, bool PAGED>
 cudaError_t launch(const AttnArgs &a, const Maps &maps, int box, int blocks, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(
-      gdn_attn_tc_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void *>(&gdn_attn_tc_kernel<D, PAGED>),
+                                   Smem<D>::kBytes, allowed<D, PAGED>);
   if (e != cudaSuccess) return e;
   gdn_attn_tc_kernel<D, PAGED><<<blocks, kThreads, Smem<D>::kBytes, stream>>>(a, maps, box);
   return cudaGetLastError();
@@ -748,7 +787,7 @@ cudaError_t launch(const AttnArgs &a, const Maps &maps, int box, int blocks, cud
 
 }  // namespace
 
-cudaError_t launch_attn_tc(AttnArgs a, int d, int blocks, cudaStream_t stream) {
+cudaError_t launch_attn_tc(const AttnArgs &a, int d, int blocks, cudaStream_t stream) {
   int box = 128;
   if (a.table && (a.page_size & -a.page_size) < box) box = a.page_size & -a.page_size;
   Maps maps;

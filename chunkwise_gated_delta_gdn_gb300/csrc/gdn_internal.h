@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace gdn {
 
 // Bytes at the start of the workspace reserved for the device status word.
@@ -130,6 +132,10 @@ struct AttnArgs {
   int max_len;                 // longest length the table can hold
   float scale;
   float scale_log2;            // scale * log2(e)
+  // the plan where the host can make it (gdn_attn.cuh): equal prompts;
+  // plan_total = 0 otherwise
+  long long plan_total, plan_per, plan_seq;
+  int plan_shift, plan_grains;
   float4 *part_o;              // partial results (see gdn_attn.cuh)
   float2 *part_ml;
   uint32_t *flags;             // device status word, or nullptr
@@ -216,13 +222,20 @@ cudaError_t launch_rownorm(const RowNormArgs &a, int dim, int kind, int dtype,
 // second dimension on), 128-byte swizzle; false when the driver refuses
 bool encode_bf16_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
                      const uint64_t *strides, const uint32_t *box);
-// attention: blocks that the launch uses (its partial results are sized by
-// them) and rows of one partial result; d 64 or 128, dtype 0 = fp32, 1 = bf16
-// (bf16: tcgen05, gdn_attn_tc.cu; fp32: gdn_attn.cu)
-int attn_blocks(int dtype, int d);
-int attn_part_rows(int dtype);
-cudaError_t launch_attn(const AttnArgs &a, int d, int dtype, cudaStream_t stream);
-cudaError_t launch_attn_tc(AttnArgs a, int d, int blocks, cudaStream_t stream);
+// attention (bf16: tcgen05, gdn_attn_tc.cu; fp32: gdn_attn.cu).  A launch of
+// `blocks` blocks; `split`: units may be cut between blocks, which takes the
+// merge kernel and 2 * blocks partial results of `rows` rows in the workspace.
+struct AttnLaunch {
+  int blocks, rows;
+  bool split;
+};
+AttnLaunch attn_launch(AttnArgs &a, int d, int dtype);  // also fills the plan in `a`
+cudaError_t launch_attn(const AttnArgs &a, int d, int dtype, const AttnLaunch &l, cudaStream_t stream);
+cudaError_t launch_attn_tc(const AttnArgs &a, int d, int blocks, cudaStream_t stream);
+int sm_count();  // of the current device
+// Let `kernel` use `bytes` of dynamic shared memory, once per device (`done`
+// has a bit for each of the first 64).
+cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done);
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream);
 // S_out = M S_in + S_seg, per state
 cudaError_t launch_state_combine(const TransferArgs &a, cudaStream_t stream);

@@ -241,6 +241,11 @@ __device__ __forceinline__ void bulk_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// fetch a tensor map ahead of its first use
+__device__ __forceinline__ void prefetch_map(const void *tmap) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
+
 // TMA: 3-D tiled load of box {x, y, z} at coordinates (x, y, z) of `tmap`
 // (a __grid_constant__ CUtensorMap), completing transactions on `bar`
 __device__ __forceinline__ void tma_load_3d(uint32_t dst_saddr, const void *tmap, int x, int y,

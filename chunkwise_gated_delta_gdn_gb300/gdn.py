@@ -422,6 +422,10 @@ def gdn_state_combine(M: torch.Tensor, S_in: torch.Tensor, S_seg: torch.Tensor, 
     return out
 
 
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _tokens(t: torch.Tensor, name: str, dev, dtype, B: int, T: int) -> int:
     """Check a ``[B, T, heads, d]`` tensor whose tokens may be strided (a slice of a wider
     projection); returns the elements from one token to the next."""
@@ -450,27 +454,39 @@ def _lengths(cu_seqlens, B: int, dev) -> int:
     return cu_seqlens.numel() - 1
 
 
-def _attn_buffers(q, o, lse, output_lse, flags, workspace, nbytes, dev):
-    """Check the buffers a caller passed and allocate the others (on the current stream);
-    returns (o, lse, workspace, its bytes)."""
+def _attn_buffers(q, o, lse, output_lse, flags, workspace, nbytes, dev, stream):
+    """Check the buffers a caller passed and allocate the others; returns (o, lse, workspace, its
+    bytes, the stream)."""
     for name, t in (("o", o), ("lse", lse), ("flags", flags), ("workspace", workspace)):
-        _check(t, name, dev)
-    if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    elif o.shape != q.shape or o.dtype != q.dtype:
+        if t is not None:
+            _check(t, name, dev)
+    shape = q.shape
+    if o is not None and (o.shape != shape or o.dtype != q.dtype):
         raise ValueError("o must match q in shape and dtype")
-    if lse is None:
-        if output_lse:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
-    elif lse.shape != q.shape[:3] or lse.dtype != torch.float32:
+    if lse is not None and (lse.shape != shape[:3] or lse.dtype != torch.float32):
         raise ValueError("lse must be float32 [B, T, H]")
     if flags is not None and (flags.element_size() != 4 or flags.numel() < 1):
         raise TypeError("flags must hold at least one 4-byte element")
     if workspace is not None:
         nbytes = workspace.numel() * workspace.element_size()
-    elif nbytes:
+    current = torch.cuda.current_stream(dev.index)
+    if stream is None or stream == current:
+        stream = current
+        o, lse, workspace = _allocate(q, o, lse, output_lse, workspace, nbytes, dev)
+    else:  # what is allocated here belongs to the stream it is used on
+        with torch.cuda.stream(stream):
+            o, lse, workspace = _allocate(q, o, lse, output_lse, workspace, nbytes, dev)
+    return o, lse, workspace, nbytes, stream
+
+
+def _allocate(q, o, lse, output_lse, workspace, nbytes, dev):
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if lse is None and output_lse:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+    if workspace is None and nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    return o, lse, workspace, nbytes
+    return o, lse, workspace
 
 
 def _cache(k_cache, v_cache, block_table, kv_lens, n_seqs, HKV, d, dtype, dev):
@@ -520,14 +536,11 @@ def gdn_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     nbytes = 0
     if workspace is None:
         nbytes = lib.gdn_attn_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, dt)
-    with torch.cuda.stream(stream):  # what is allocated here belongs to the stream it is used on
-        o, lse, workspace, nbytes = _attn_buffers(q, o, lse, output_lse, flags, workspace, nbytes,
-                                                  dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    o, lse, workspace, nbytes, stream = _attn_buffers(q, o, lse, output_lse, flags, workspace,
+                                                      nbytes, dev, stream)
     status = lib.gdn_attn_fwd(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens), n_seqs, B, T, H, HKV, d,
-        qs, ks, vs, d ** -0.5 if scale is None else scale, dt, _ptr(flags), _ptr(workspace),
+        _addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), _addr(cu_seqlens), n_seqs, B, T, H, HKV, d,
+        qs, ks, vs, d ** -0.5 if scale is None else scale, dt, _addr(flags), _addr(workspace),
         nbytes, stream.cuda_stream)
     if status != GDN_OK:
         raise GdnError(status, "gdn_attn_fwd")
@@ -569,15 +582,12 @@ def gdn_attn_paged_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     if workspace is None:
         nbytes = lib.gdn_attn_paged_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, page_size,
                                                         max_pages, dt)
-    with torch.cuda.stream(stream):  # what is allocated here belongs to the stream it is used on
-        o, lse, workspace, nbytes = _attn_buffers(q, o, lse, output_lse, flags, workspace, nbytes,
-                                                  dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    o, lse, workspace, nbytes, stream = _attn_buffers(q, o, lse, output_lse, flags, workspace,
+                                                      nbytes, dev, stream)
     status = lib.gdn_attn_paged_fwd(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(kv_lens), _ptr(o),
-        _ptr(lse), _ptr(cu_seqlens), n_seqs, B, T, H, HKV, d, qs, page_size, max_pages, n_pages,
-        d ** -0.5 if scale is None else scale, dt, _ptr(flags), _ptr(workspace), nbytes,
+        _addr(q), _addr(k_cache), _addr(v_cache), _addr(block_table), _addr(kv_lens), _addr(o),
+        _addr(lse), _addr(cu_seqlens), n_seqs, B, T, H, HKV, d, qs, page_size, max_pages, n_pages,
+        d ** -0.5 if scale is None else scale, dt, _addr(flags), _addr(workspace), nbytes,
         stream.cuda_stream)
     if status != GDN_OK:
         raise GdnError(status, "gdn_attn_paged_fwd")
@@ -604,11 +614,11 @@ def gdn_kv_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     if flags is not None and (flags.element_size() != 4 or flags.numel() < 1):
         raise TypeError("flags must hold at least one 4-byte element")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        stream = torch.cuda.current_stream(dev.index)
     status = lib.gdn_kv_cache_append(
-        _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(kv_lens),
-        _ptr(cu_seqlens), n_seqs, B, T, HKV, d, ks, vs, page_size, max_pages, n_pages, dt,
-        _ptr(flags), stream.cuda_stream)
+        _addr(k), _addr(v), _addr(k_cache), _addr(v_cache), _addr(block_table), _addr(kv_lens),
+        _addr(cu_seqlens), n_seqs, B, T, HKV, d, ks, vs, page_size, max_pages, n_pages, dt,
+        _addr(flags), stream.cuda_stream)
     if status != GDN_OK:
         raise GdnError(status, "gdn_kv_cache_append")
 

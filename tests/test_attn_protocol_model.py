@@ -1,8 +1,7 @@
 """A CPU model of the bf16 attention kernel's protocol (csrc/gdn_attn_tc.cu): the loader, the
 product warp and the two softmax groups as processes over the same ring of tiles, barriers and
 in-order tensor pipe.  Random sequences of units must run to their end, every product must read
-the tile that it is meant to read, and no stage may be refilled while a product that reads it is
-still to run."""
+the tile that it is meant to read, and no stage may be handed back twice."""
 from __future__ import annotations
 
 import random
@@ -11,16 +10,18 @@ import pytest
 
 
 class Model:
-    """Units are (wide, tiles).  ``keys_first``: a unit's last tiles in the order of the keys."""
+    """Units are (wide, tiles).  ``keys_first``: a unit's last tiles in the order of the keys.
+    ``late``: stages are handed back by the product warp on the softmax's answer, not by the
+    softmax when it sees the scores."""
 
-    def __init__(self, units, stages, keys_first=True, delay=0):
-        self.units, self.stages, self.keys_first, self.delay = units, stages, keys_first, delay
+    def __init__(self, units, stages, keys_first=True, late=False, delay=0):
+        self.units, self.stages, self.keys_first, self.late, self.delay = units, stages, keys_first, late, delay
         self.full = {}        # load number -> tile
         self.free = {}        # load number -> handed back
         self.loads = 0        # load numbers issued
         self.q_free = [True] + [False] * len(units)
         self.q_full = [False] * len(units)
-        self.scores = ([], [])   # per X: (unit, tile) whose scores are done
+        self.scores = ([], [])   # per X: (unit, tile, stages freed) whose scores are done
         self.ready = [0, 0]      # weights ready, counted
         self.outs = ([], [])     # per X: (unit, last) outputs done
 
@@ -87,25 +88,26 @@ class Model:
     def products(self):
         self.used = 0
         left, shared, old, shared_v = [None, None], False, None, None
-        k_used, v_used, answers = [None, None], [None, None], [0, 0]
+        held, answers = ([], []), [0, 0]
 
-        def hand_back(held, x):
-            if held[x] is not None:
-                self.free[held[x]] = True
-                held[x] = None
+        def scores(x, unit, tile, freed):
+            self.scores[x].append((unit, tile, freed))
+            held[x].extend(freed)
 
         def weights(x):
             answers[x] += 1
             while self.ready[x] < answers[x]:
                 yield
+            if self.late:
+                for n in held[x]:
+                    self.free[n] = True
+                held[x].clear()
 
         def last_output(x):
             nonlocal shared_v
             if not (shared and x == 1):
                 shared_v = yield from self.next_tile((old, "v", left[x]))
             yield from weights(x)
-            hand_back(k_used, x)
-            hand_back(v_used, x)
             self.outs[x].append((old, True))
             if not shared or x == 1:
                 self.free[shared_v] = True
@@ -124,39 +126,29 @@ class Model:
             while not self.q_full[i]:
                 yield
             k = yield from self.next_tile((i, "k", 0))
-            self.scores[0].append((i, 0))
+            scores(0, i, 0, [] if wide else [k])
             if left[1] is not None:
                 yield from last_output(1)
             if wide:
-                self.scores[1].append((i, 0))
-                v_old = None
+                scores(1, i, 0, [k])
                 for t in range(n - 1):
                     v = yield from self.next_tile((i, "v", t))
                     yield from weights(0)
                     k_next = yield from self.next_tile((i, "k", t + 1))
-                    self.scores[0].append((i, t + 1))
+                    scores(0, i, t + 1, [])
                     yield from weights(1)
-                    self.free[k] = True
-                    if v_old is not None:
-                        self.free[v_old] = True
-                    self.scores[1].append((i, t + 1))
-                    k, v_old = k_next, v
-                k_used[1], v_used[1] = k, v_old
+                    scores(1, i, t + 1, [k_next, v])
                 left = [n - 1, n - 1]
             else:
-                k_used[0] = k
                 if n > 1:
-                    k_used[1] = yield from self.next_tile((i, "k", 1))
-                    self.scores[1].append((i, 1))
+                    k = yield from self.next_tile((i, "k", 1))
+                    scores(1, i, 1, [k])
                 for t in range(2, n):
                     x = t & 1
                     v = yield from self.next_tile((i, "v", t - 2))
                     yield from weights(x)
-                    hand_back(k_used, x)
-                    hand_back(v_used, x)
-                    v_used[x] = v
-                    k_used[x] = yield from self.next_tile((i, "k", t))
-                    self.scores[x].append((i, t))
+                    k = yield from self.next_tile((i, "k", t))
+                    scores(x, i, t, [k, v])
                 odd = (n - 1) & 1
                 left = [n - 1 - odd, n - 2 + odd if n > 1 else None]
             self.q_free[i + 1] = True
@@ -170,7 +162,11 @@ class Model:
             for t in tiles:
                 while len(self.scores[x]) <= seen:
                     yield
-                assert self.scores[x][seen] == (i, t)
+                assert self.scores[x][seen][:2] == (i, t)
+                if not self.late:
+                    for n_load in self.scores[x][seen][2]:
+                        assert not self.free.get(n_load)
+                        self.free[n_load] = True
                 for _ in range(random.randint(0, self.delay)):
                     yield
                 seen += 1
@@ -212,8 +208,11 @@ def test_every_sequence_of_units_ends(stages):
         assert Model(units, stages, delay=trial % 5).run(), units
 
 
-def test_model_finds_the_deadlock_of_the_other_order():
-    """With a unit's last tiles in the order of the X instead, an odd number of tiles leaves the
-    ring waiting for a stage that is handed back only after the tile that waits for it."""
-    assert not Model([(False, 3), (False, 3)], 5, keys_first=False).run()
-    assert Model([(False, 3), (False, 3)], 5).run()
+def test_model_finds_a_deadlock():
+    """Handing stages back on the softmax's answer, with a unit's last tiles in the order of the
+    X, an odd number of tiles leaves the ring waiting for a stage that is handed back only after
+    the tile that waits for it."""
+    units = [(False, 3), (False, 3)]
+    assert not Model(units, 5, keys_first=False, late=True).run()
+    assert Model(units, 5, keys_first=True, late=True).run()
+    assert Model(units, 5).run()
