@@ -39,7 +39,7 @@ bool encode_bf16_map(CUtensorMap *m, const void *base, int rank, const uint64_t 
                      const uint64_t *strides, const uint32_t *box) {
   if (!encode_fn()) return false;
   static_assert(sizeof(cuuint64_t) == sizeof(uint64_t) && sizeof(cuuint32_t) == sizeof(uint32_t), "");
-  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base),
                      reinterpret_cast<const cuuint64_t *>(dims),
                      reinterpret_cast<const cuuint64_t *>(strides), box, es,

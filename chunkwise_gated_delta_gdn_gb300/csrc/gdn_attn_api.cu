@@ -34,7 +34,9 @@ gdn_status check_shape(int B, int T, int H, int HKV, int d, int n_seqs, bool pac
 
 gdn_status check_cache(int page_size, int max_pages, int n_pages) {
   if (page_size <= 0 || max_pages <= 0 || n_pages <= 0) return GDN_ERR_INVALID_ARG;
-  if (page_size % 16 != 0 || (long)page_size * max_pages > INT32_MAX - 1024)
+  // positions, and 8-row groups of the whole cache, are counted in 32 bits
+  if (page_size % 16 != 0 || (long)page_size * max_pages > INT32_MAX - 1024 ||
+      (n_pages + 1L) * (page_size / 8) > INT32_MAX)
     return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }

@@ -109,41 +109,46 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // descriptors differ between steps in the low word's address field only (16
 // bytes a unit), so a step costs an addition: with the descriptors put together
 // from scratch for each product the issue took longer than the product itself.
-constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);  // 1024 bytes between 8-row groups
+// high word: bytes from one 8-row group to the next
+__host__ __device__ constexpr uint32_t desc_hi(int group_bytes) {
+  return (uint32_t)(group_bytes >> 4) | (1u << 14) | (2u << 29);
+}
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
   return ((saddr >> 4) & 0x3FFF) | ((lbo >> 4) << 16);
 }
 // S = Q K^T over one 64-column panel of each (four K steps of 16)
 template <bool FIRST>
-__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                             bool elected) {
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi,
+                                             uint32_t idesc, bool elected) {
   asm volatile(
-      "{\n .reg .pred q, p;\n .reg .b64 da, db;\n .reg .b32 la, lb;\n setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %6, 0;\n"
-      " mov.b64 da, {%1, %3};\n mov.b64 db, {%2, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n"
-      " add.u32 la, %1, 2;\n add.u32 lb, %2, 2;\n mov.b64 da, {la, %3};\n mov.b64 db, {lb, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, 1;\n"
-      " add.u32 la, %1, 4;\n add.u32 lb, %2, 4;\n mov.b64 da, {la, %3};\n mov.b64 db, {lb, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, 1;\n"
-      " add.u32 la, %1, 6;\n add.u32 lb, %2, 6;\n mov.b64 da, {la, %3};\n mov.b64 db, {lb, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, 1;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((int)elected), "r"(FIRST ? 0 : 1)
+      "{\n .reg .pred q, p;\n .reg .b64 da, db;\n .reg .b32 la, lb;\n setp.ne.b32 q, %6, 0;\n setp.ne.b32 p, %7, 0;\n"
+      " mov.b64 da, {%1, %3};\n mov.b64 db, {%2, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n"
+      " add.u32 la, %1, 2;\n add.u32 lb, %2, 2;\n mov.b64 da, {la, %3};\n mov.b64 db, {lb, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, 1;\n"
+      " add.u32 la, %1, 4;\n add.u32 lb, %2, 4;\n mov.b64 da, {la, %3};\n mov.b64 db, {lb, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, 1;\n"
+      " add.u32 la, %1, 6;\n add.u32 lb, %2, 6;\n mov.b64 da, {la, %3};\n mov.b64 db, {lb, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, 1;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc_hi(1024)), "r"(b_hi), "r"(idesc), "r"((int)elected), "r"(FIRST ? 0 : 1)
       : "memory");
 }
-// O (+)= P V over 64 keys (four K steps of 16)
-__device__ __forceinline__ void issue_output(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                             bool accumulate, bool elected) {
+// O (+)= P V over 64 keys (four K steps of 16, STEP bytes of V apart)
+template <int STEP>
+__device__ __forceinline__ void issue_output(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi,
+                                             uint32_t idesc, bool accumulate, bool elected) {
   asm volatile(
       "{\n .reg .pred q, p;\n .reg .b64 db;\n .reg .b32 la, lb;\n setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %6, 0;\n"
       " mov.b64 db, {%2, %3};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n"
-      " add.u32 la, %1, 8;\n add.u32 lb, %2, 128;\n mov.b64 db, {lb, %3};\n"
+      " add.u32 la, %1, 8;\n add.u32 lb, %2, %7;\n mov.b64 db, {lb, %3};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [la], db, %4, 1;\n"
-      " add.u32 la, %1, 16;\n add.u32 lb, %2, 256;\n mov.b64 db, {lb, %3};\n"
+      " add.u32 la, %1, 16;\n add.u32 lb, %2, %8;\n mov.b64 db, {lb, %3};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [la], db, %4, 1;\n"
-      " add.u32 la, %1, 24;\n add.u32 lb, %2, 384;\n mov.b64 db, {lb, %3};\n"
+      " add.u32 la, %1, 24;\n add.u32 lb, %2, %9;\n mov.b64 db, {lb, %3};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [la], db, %4, 1;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((int)elected), "r"((int)accumulate)
+      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"((int)elected), "r"((int)accumulate), "n"(STEP >> 4),
+      "n"(2 * STEP >> 4), "n"(3 * STEP >> 4)
       : "memory");
 }
 
@@ -246,6 +251,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     gdn_attn_tc_kernel(const AttnArgs a, const __grid_constant__ Maps maps, const int box) {
   using SM = Smem<D>;
   constexpr int kPanels = D / 64;
+  // A key or value tile in shared memory, 8-row groups of 1024 bytes in the
+  // 128-byte swizzle.  A prompt's: 64-column panels one after the other, each
+  // one box of its tensor map.  A cache's: the panels of a group next to each
+  // other, so that one box brings whole rows of a page (a page of 16 rows in
+  // boxes of one panel held the loads at 4.3 TB/s).
+  constexpr int kGroup = PAGED ? kPanels * 1024 : 1024;  // bytes from one 8-row group to the next
+  constexpr int kPanelAt = PAGED ? 1024 : kPanel;        // and from one panel to the next
   extern __shared__ __align__(1024) unsigned char sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (smem_addr(sm) & 1023u) {
@@ -326,6 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -CUDART_INF_F, l = 0.f;
       const int first = narrow ? u.t0 + x : u.t0;
       const bool mine = first < u.t1;
+      // rows past the unit's last one (most of a decode step's tile): their
+      // weights are whatever the scores leave, and nobody reads their output
+      const bool idle = narrow && quarter * 32 >= u.n_tok * u.gp;
 #pragma unroll 1
       for (int t = first; t < u.t1; t += stride) {
         wait(bars.s_full(x), s_phase, abort);
@@ -337,6 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int2 stage = used[x];
           if (stage.x >= 0) mbar_arrive(bars.kv_empty(stage.x));
           if (stage.y >= 0) mbar_arrive(bars.kv_empty(stage.y));
+        }
+        if (idle) {
+          if (lane == 0) mbar_arrive(bars.p_ready(x));
+          continue;
         }
         uint32_t raw[2][32];
         tmem_ld32_nowait(s_at, raw[0]);
@@ -435,13 +454,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         f_other = ex2(m_other - base);
         l = f_own * l_own + f_other * l_other;
         m_scaled = top;
-      } else if (mine) {
+      } else if (mine && !idle) {
         *own_ex = l;
         meet_half();
         l += *other_ex;
         meet_half();  // read, before the next tile's maximum is written
       }
-      if (mine) {
+      if (mine && !idle) {
         const bool valid = tok < u.n_tok;
         const bool part = u.slot >= 0;
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -540,15 +559,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             page = __ldg(a.table + (long long)w.seq * a.max_pages + k0 / a.page_size);
             first = k0 % a.page_size;
             // an out-of-range page reads as zeros
-            if ((page < 0 || page >= a.n_pages) && a.flags) atomicOr(a.flags, kFlagBadSeqlens);
+            if (page < 0 || page >= a.n_pages) {
+              if (a.flags) atomicOr(a.flags, kFlagBadSeqlens);
+              page = a.n_pages;  // just past the cache
+            }
           }
           wait(bars.kv_empty(ring.i), ring.round ^ 1, abort);
           if (lane == 0) mbar_arrive_expect_tx(full, n * box * 128 * kPanels);
           __syncwarp();
           if (lane < n)
-#pragma unroll
-            for (int p = 0; p < kPanels; p++)
-              tma_load_4d(dst + p * kPanel + lane * box * 128, map, p * 64, w.kvh, first, page, full);
+            tma_load_5d(dst + lane * box * 128 * kPanels, map, 0, 0, 0,
+                        page * (a.page_size >> 3) + (first >> 3), w.kvh, full);
         } else {
           wait(bars.kv_empty(ring.i), ring.round ^ 1, abort);
           if (lane == 0) {
@@ -556,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = w.row0 - w.pos0 + key;  // a prompt's keys are its own tokens
 #pragma unroll
             for (int p = 0; p < kPanels; p++)
-              tma_load_4d(dst + p * kPanel, map, p * 64, w.kvh, row, 0, full);
+              tma_load_3d(dst + p * kPanel, map, p * 64, w.kvh, row, full);
           }
           __syncwarp();
         }
@@ -637,9 +658,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // value rows that belong to nobody
         const int rows = len - tile * 128;
         if (rows < 128) {
-          for (int p = 0; p < kPanels; p++) {
-            uint4 *to = reinterpret_cast<uint4 *>(sm + SM::kRing + stage * SM::kTileBytes + p * kPanel);
-            for (int i = max(rows, 0) * 8 + lane; i < 128 * 8; i += 32) to[i] = make_uint4(0, 0, 0, 0);
+          unsigned char *tile_at = sm + SM::kRing + stage * SM::kTileBytes;
+          for (int i = max(rows, 0) * 8 + lane; i < 128 * 8; i += 32) {
+            const int row = i >> 3;
+#pragma unroll
+            for (int p = 0; p < kPanels; p++)
+              *reinterpret_cast<uint4 *>(tile_at + (row >> 3) * kGroup + p * kPanelAt + (row & 7) * 128 +
+                                         (i & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async();
           __syncwarp();
@@ -655,9 +680,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t q_lo = desc_lo(sQ + q_tile * SM::kTileBytes, 16);
         const uint32_t k_lo = desc_lo(sRing + stage * SM::kTileBytes, 16);
         fence_after_sync();
-        issue_scores<true>(tS + x * 128, q_lo, k_lo, kIdS, lane == 0);
+        issue_scores<true>(tS + x * 128, q_lo, k_lo, desc_hi(kGroup), kIdS, lane == 0);
         if (D == 128)
-          issue_scores<false>(tS + x * 128, q_lo + (kPanel >> 4), k_lo + (kPanel >> 4), kIdS, lane == 0);
+          issue_scores<false>(tS + x * 128, q_lo + (kPanel >> 4), k_lo + (kPanelAt >> 4), desc_hi(kGroup),
+                              kIdS, lane == 0);
         if (lane == 0) {
           mma_commit(bars.s_full(x));
           used[x] = make_int2(free_k, free_v);
@@ -665,9 +691,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto output = [&](int x, int stage, bool accumulate) {
-        const uint32_t v_lo = desc_lo(sRing + stage * SM::kTileBytes, kPanel);
-        issue_output(tO + x * D, tS + x * 128, v_lo, kIdO, accumulate, lane == 0);
-        issue_output(tO + x * D, tS + x * 128 + 32, v_lo + 512, kIdO, true, lane == 0);
+        const uint32_t v_lo = desc_lo(sRing + stage * SM::kTileBytes, kPanelAt);
+        issue_output<2 * kGroup>(tO + x * D, tS + x * 128, v_lo, desc_hi(kGroup), kIdO, accumulate,
+                                 lane == 0);
+        issue_output<2 * kGroup>(tO + x * D, tS + x * 128 + 32, v_lo + (8 * kGroup >> 4), desc_hi(kGroup),
+                                 kIdO, true, lane == 0);
       };
       auto last_output = [&](int x) {
         if (left[x] < 0) return;
@@ -758,19 +786,19 @@ bool make_maps(Maps &m, const AttnArgs &a, int d, int box) {
     const uint32_t pack_box[3] = {64, (uint32_t)plan.G, (uint32_t)(128 / plan.G)};
     if (!encode_bf16_map(&m.q_pack, a.q, 3, q_dims, q_strides, pack_box)) return false;
   }
-  const uint32_t kv_box[4] = {64, 1, (uint32_t)box, 1};
-  if (a.table) {
+  if (a.table) {  // [64 columns][8 rows][panel][8-row group of all pages][head]
     const uint64_t row = (uint64_t)a.HKV * D * 2;
-    const uint64_t dims[4] = {D, (uint64_t)a.HKV, (uint64_t)a.page_size, (uint64_t)a.n_pages};
-    const uint64_t strides[3] = {D * 2, row, row * a.page_size};
-    return encode_bf16_map(&m.k, a.k, 4, dims, strides, kv_box) &&
-           encode_bf16_map(&m.v, a.v, 4, dims, strides, kv_box);
+    const uint64_t dims[5] = {64, 8, D / 64, (uint64_t)a.n_pages * (a.page_size / 8), (uint64_t)a.HKV};
+    const uint64_t strides[4] = {row, 128, row * 8, D * 2};
+    const uint32_t kv_box[5] = {64, 8, (uint32_t)(D / 64), (uint32_t)box / 8, 1};
+    return encode_bf16_map(&m.k, a.k, 5, dims, strides, kv_box) &&
+           encode_bf16_map(&m.v, a.v, 5, dims, strides, kv_box);
   }
-  const uint64_t dims[4] = {D, (uint64_t)a.HKV, (uint64_t)a.Ttot, 1};
-  const uint64_t ks[3] = {D * 2, (uint64_t)a.k_stride * 2, (uint64_t)a.k_stride * 2 * a.Ttot};
-  const uint64_t vs[3] = {D * 2, (uint64_t)a.v_stride * 2, (uint64_t)a.v_stride * 2 * a.Ttot};
-  return encode_bf16_map(&m.k, a.k, 4, dims, ks, kv_box) &&
-         encode_bf16_map(&m.v, a.v, 4, dims, vs, kv_box);
+  const uint32_t kv_box[3] = {64, 1, 128};
+  const uint64_t dims[3] = {D, (uint64_t)a.HKV, (uint64_t)a.Ttot};
+  const uint64_t ks[2] = {D * 2, (uint64_t)a.k_stride * 2}, vs[2] = {D * 2, (uint64_t)a.v_stride * 2};
+  return encode_bf16_map(&m.k, a.k, 3, dims, ks, kv_box) &&
+         encode_bf16_map(&m.v, a.v, 3, dims, vs, kv_box);
 }
 
 template <int D, bool PAGED>

@@ -257,13 +257,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst_saddr, const void *tmap
       : "memory");
 }
 
-// the same for a 4-D map
-__device__ __forceinline__ void tma_load_4d(uint32_t dst_saddr, const void *tmap, int x, int y,
-                                            int z, int w, uint32_t bar) {
+// the same for a 5-D map
+__device__ __forceinline__ void tma_load_5d(uint32_t dst_saddr, const void *tmap, int x, int y,
+                                            int z, int w, int v, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst_saddr),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst_saddr),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
       : "memory");
 }
 
