@@ -60,11 +60,16 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs 
   float *Qs = smem, *Ks = Qs + 64 * kS, *Vs = Ks + 64 * kS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
   AttnPlan<WarpShape> plan(a.H, a.HKV);
-  const AttnStart st = attn_start(a, plan, blockIdx.x, gridDim.x);  // each warp for itself
+  AttnStaged *staged = reinterpret_cast<AttnStaged *>(smem);  // until the first operands
+  attn_stage(a, staged, blockIdx.x);
+  __syncthreads();
+  const AttnStart st = attn_start(a, plan, staged, blockIdx.x, gridDim.x);  // each warp for itself
   AttnWalk<WarpShape> walk(a, plan, st, blockIdx.x);
   AttnUnit u;
+  if (a.jobs && tid == 0) a.jobs[blockIdx.x].rows = 0;
   while (walk.next(u)) {
-    __syncthreads();  // the previous unit's operands are read
+    if (tid == 0 && u.slot == 2 * (int)blockIdx.x + 1) a.jobs[blockIdx.x] = attn_job(u);
+    __syncthreads();  // the previous unit's operands (or the plan's) are read
     for (int i = tid; i < 64 * (D / 8); i += kThreads) {
       const int r = i / (D / 8), c = (i % (D / 8)) * 8, t = r / u.gp;
       float x[8] = {};
@@ -196,48 +201,105 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs 
   }
 }
 
-// Joins the partial results of one unit: block b.x looks at the border between
-// ranges b.x and b.x + 1 and works only when it is the first one inside a
-// unit.  A thread owns four columns of a row and adds the pieces up in the
-// order of the blocks that made them.
-constexpr int kMergeThreads = 256;
+// Joins the pieces of the unit that block b.x of the attention kernel began
+// and did not end, 32 rows per b.y.  Work items are (row, four columns), 32
+// adjacent rows to a warp; each adds its pieces up in the order of the blocks
+// that made them.  With many pieces (a single token over a long cache) and few
+// rows there are more threads than items: they share an item's pieces.
+constexpr int kMergeThreads = 512;
+constexpr int kMergeRows = 32;
+constexpr int kMergeUnroll = 4;
 template <class S, int D, bool BF16>
-__global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const AttnArgs a, int n_blocks) {
-  AttnPlan<S> plan(a.H, a.HKV);
-  const int first = blockIdx.x;
-  const AttnStart st = attn_start(a, plan, first + 1, n_blocks);  // each warp for itself
-  if (st.seq >= a.n_seqs) return;
-  const long long c = (first + 1) * plan.per;
-  bool bad;
-  const AttnSeq s = attn_seq(a, st.seq, bad);
-  AttnUnit u;
-  const long long u0 = st.seq0 + plan.find(s, st.seq, c - st.seq0, u);
-  int last;
-  if (!plan.merges(s, u0, u.nt, first + 1, last)) return;
-  bool finite = true;
-  // work items (row, four columns) in an order that gives a warp adjacent rows
-  const int rows = min(u.n_tok * u.gp, S::kRows);
-  for (int i = blockIdx.y * kMergeThreads + threadIdx.x; i < rows * (D / 4);
-       i += gridDim.y * kMergeThreads) {
-    const int row = i % rows, d4 = i / rows;
+__global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const AttnArgs a) {
+  __shared__ float weight[kMergeRows], total[kMergeRows];
+  __shared__ float4 part[kMergeThreads];
+  __shared__ float top[kMergeRows][kMergeThreads / kMergeRows];
+  const int first = blockIdx.x, r0 = blockIdx.y * kMergeRows, tid = threadIdx.x;
+  // launched while the attention kernel runs; its results are there after this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const AttnJob job = a.jobs[first];
+  if (r0 >= job.rows) return;
+  const int n = job.last - first + 1;  // pieces
+  const int rows = min(job.rows - r0, kMergeRows);
+  auto slot = [&](int i) { return (long long)(i == 0 ? 2 * first + 1 : 2 * (first + i)); };
+  // row maximum and sum: kMergeThreads / 32 threads to a row
+  {
+    const int row = tid % kMergeRows, lane = tid / kMergeRows;
+    constexpr int kLanes = kMergeThreads / kMergeRows;
     float m = -CUDART_INF_F;
-    for (int b = first; b <= last; b++)
-      m = fmaxf(m, a.part_ml[(long long)(b == first ? 2 * b + 1 : 2 * b) * S::kRows + row].x);
+    if (row < rows)
+      for (int i = lane; i < n; i += kLanes)
+        m = fmaxf(m, a.part_ml[slot(i) * S::kRows + r0 + row].x);
+    top[row][lane] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kLanes; i++) m = fmaxf(m, top[row][i]);
     const float base = m == -CUDART_INF_F ? 0.f : m;
     float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int b = first; b <= last; b++) {
-      const long long slot = b == first ? 2 * b + 1 : 2 * b;
-      const float2 ml = a.part_ml[slot * S::kRows + row];
-      const float4 x = a.part_o[(slot * (D / 4) + d4) * S::kRows + row];
-      const float f = exp2_approx(ml.x - base);
-      l += f * ml.y;
-      o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+    if (row < rows)
+      for (int i = lane; i < n; i += kLanes) {
+        const float2 ml = a.part_ml[slot(i) * S::kRows + r0 + row];
+        l += exp2_approx(ml.x - base) * ml.y;
+      }
+    __syncthreads();
+    top[row][lane] = l;
+    __syncthreads();
+    if (lane == 0 && row < rows) {
+      l = 0.f;
+      for (int i = 0; i < kLanes; i++) l += top[row][i];
+      weight[row] = base;
+      total[row] = l;
+      if (a.lse) {
+        const long long at = (long long)(job.row0 + (r0 + row) / job.gp) * a.H + job.head0 + (r0 + row) % job.gp;
+        a.lse[at] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718056f;
+      }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __syncthreads();
+  }
+  // rows rounded up to a power of two, so that a warp's threads have adjacent rows
+  int wide = 1;
+  while (wide < rows) wide <<= 1;
+  const int items = wide * (D / 4);
+  const int share = items >= kMergeThreads ? 1 : kMergeThreads / items;  // threads to an item
+  bool finite = true;
+  for (int i0 = 0; i0 < items; i0 += kMergeThreads / share) {
+    const int item = i0 + tid % (kMergeThreads / share), who = tid / (kMergeThreads / share);
+    const int row = item % wide, d4 = item / wide;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row < rows) {
+      const float base = weight[row];
+      for (int i = who * kMergeUnroll; i < n; i += share * kMergeUnroll) {
+        float4 x[kMergeUnroll];
+        float f[kMergeUnroll];
+#pragma unroll
+        for (int k = 0; k < kMergeUnroll; k++) {
+          const bool have = i + k < n;
+          const long long at = slot(have ? i + k : 0);
+          f[k] = have ? exp2_approx(a.part_ml[at * S::kRows + r0 + row].x - base) : 0.f;
+          x[k] = a.part_o[(at * (D / 4) + d4) * S::kRows + r0 + row];
+        }
+#pragma unroll
+        for (int k = 0; k < kMergeUnroll; k++)
+          if (i + k < n) {
+            o.x += f[k] * x[k].x; o.y += f[k] * x[k].y; o.z += f[k] * x[k].z; o.w += f[k] * x[k].w;
+          }
+      }
+    }
+    if (share > 1) {
+      part[tid] = o;
+      __syncthreads();
+      if (who == 0)
+        for (int w = 1; w < share; w++) {
+          const float4 x = part[tid + w * (kMergeThreads / share)];
+          o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+        }
+      __syncthreads();
+    }
+    if (row >= rows || who != 0) continue;
+    const float inv = total[row] == 0.f ? 0.f : 1.f / total[row];
     o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
     finite &= isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w);
-    const long long at = (long long)(u.row0 + row / u.gp) * a.H + u.head0 + row % u.gp;
+    const long long at = (long long)(job.row0 + (r0 + row) / job.gp) * a.H + job.head0 + (r0 + row) % job.gp;
     if constexpr (BF16) {
       __nv_bfloat162 y[2] = {__floats2bfloat162_rn(o.x, o.y), __floats2bfloat162_rn(o.z, o.w)};
       *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + d4 * 4) =
@@ -245,16 +307,23 @@ __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const Att
     } else {
       *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at * D + d4 * 4) = o;
     }
-    if (a.lse && d4 == 0)
-      a.lse[at] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718056f;
   }
   if (!finite && a.flags) atomicOr(a.flags, kFlagNonfinite);
 }
 
 template <class S, int D, bool BF16>
 cudaError_t merge(const AttnArgs &a, int blocks, cudaStream_t stream) {
-  gdn_attn_merge_kernel<S, D, BF16><<<dim3(blocks - 1, 4), kMergeThreads, 0, stream>>>(a, blocks);
-  return cudaGetLastError();
+  // may be set up while the attention kernel still runs
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(blocks - 1, S::kRows / kMergeRows);
+  config.blockDim = dim3(kMergeThreads);
+  config.stream = stream;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, gdn_attn_merge_kernel<S, D, BF16>, a);
 }
 
 template <int D>

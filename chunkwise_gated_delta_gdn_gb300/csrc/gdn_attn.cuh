@@ -65,7 +65,21 @@ struct AttnUnit {
   int t0, t1;   // key tiles of this block
   int nt;       // key tiles of the unit
   int slot;     // slot of the partial result, or -1 when the unit is whole
+  int last;     // last block with a piece of the unit
 };
+
+// What the merge kernel does for block b: join the pieces of the unit that
+// block b began and did not end.  Pieces: slot 2 b + 1, then slots 2 i for
+// i = b + 1 .. last.
+struct AttnJob {
+  int row0, rows, gp, head0;  // rows = 0: nothing to do
+  int last;
+  int pad[3];
+};
+static_assert(sizeof(AttnJob) == kAttnJobBytes, "a job's place in the workspace");
+__host__ __device__ __forceinline__ AttnJob attn_job(const AttnUnit &u) {
+  return AttnJob{u.row0, u.n_tok * u.gp, u.gp, u.head0, u.last, {0, 0, 0}};
+}
 
 // Sequence n as the kernels see it; nq = 0 when its lengths are malformed
 // (`bad` is then set).
@@ -244,15 +258,11 @@ struct AttnPlan {
     static_assert(S::kWide == 1 || S::kWide == 2, "a shift in cut()");
     return t < nt ? (int)t : nt;
   }
-  // Whether the border between the ranges of blocks i - 1 and i is the first
-  // one that cuts the unit beginning at u0; `last` is then the last block with
-  // a piece of it (block i - 1 has the first piece).
-  __host__ __device__ bool merges(const AttnSeq &s, long long u0, int nt, int i, int &last) const {
-    const int at = cut(s, u0, nt, i * per);
-    if (at == 0 || at == nt || cut(s, u0, nt, (i - 1) * per) != 0) return false;
-    last = i;
-    while (cut(s, u0, nt, (last + 1) * per) < nt) last++;
-    return true;
+  // last block with a piece of the unit that begins at cost u0
+  __host__ __device__ int last_block(const AttnSeq &s, long long u0, int nt) const {
+    const int w = packed(s) ? 1 : wide;
+    const long long grains = (nt + (1 << shift) - 1) >> shift;
+    return (int)attn_div(u0 + over + (grains - 1) * w, per);
   }
 
   // What the totals decide: `weighted` is the cost of everything in stream
@@ -287,16 +297,37 @@ struct AttnStart {
   int seq;          // n_seqs when the block has no work
 };
 
+// What the cost of a sequence goes by, in shared memory for the first
+// kStaged sequences.
+constexpr int kStaged = 4096;
+struct AttnStaged {
+  int nq, base;
+};
+// All THREADS threads of a block (which then synchronise); block 0 reports
+// malformed lengths.
+__device__ __forceinline__ void attn_stage(const AttnArgs &a, AttnStaged *staged, int block) {
+  if (a.plan_total) return;
+  bool any_bad = threadIdx.x == 0 && a.cu && (a.cu[0] != 0 || a.cu[a.n_seqs] != a.Ttot);
+  for (int n = threadIdx.x; n < a.n_seqs; n += blockDim.x) {
+    bool bad;
+    const AttnSeq s = attn_seq(a, n, bad);
+    any_bad |= bad;
+    if (n < kStaged) staged[n] = AttnStaged{s.nq, s.base};
+    else if (block != 0) break;
+  }
+  if (any_bad && a.flags && block == 0) atomicOr(a.flags, kFlagBadSeqlens);
+}
+
 // All lanes of one warp: choose the plan and find the start of range `block`.
 template <class S>
 __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &plan,
-                                                long long block, int n_blocks) {
+                                                const AttnStaged *staged, long long block,
+                                                int n_blocks) {
   const int lane = threadIdx.x & 31;
   constexpr uint32_t kAll = 0xffffffffu;
   AttnStart r;
   r.seq = a.n_seqs;
   r.seq0 = 0;
-  bool bad;
   if (a.plan_total) {  // equal prompts: the host has made the plan
     plan.shift = a.plan_shift;
     if (a.plan_grains) plan.grains(a.plan_shift);
@@ -309,16 +340,18 @@ __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &
     }
     return r;
   }
-  const AttnSeq own = attn_seq(a, min(lane, a.n_seqs - 1), bad);  // of up to 32 sequences, all
-  bool any_bad = bad || (lane == 0 && a.cu && (a.cu[0] != 0 || a.cu[a.n_seqs] != a.Ttot));
   auto cost_of = [&](int n) {
-    if (n < 32) return plan.cost(own);
-    const AttnSeq s = attn_seq(a, n, bad);
-    any_bad |= bad;
+    if (n >= kStaged) {
+      bool bad;
+      return plan.cost(attn_seq(a, n, bad));
+    }
+    AttnSeq s;
+    s.nq = staged[n].nq;
+    s.base = staged[n].base;
     return plan.cost(s);
   };
   auto sum = [&] {
-    if (a.n_seqs == 1) return plan.cost(own);
+    if (a.n_seqs == 1) return cost_of(0);
     long long mine = 0;
     for (int n = lane; n < a.n_seqs; n += 32) mine += cost_of(n);
 #pragma unroll
@@ -329,7 +362,6 @@ __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &
     plan.grains(log);
     return sum();
   });
-  if (any_bad && a.flags && block == 0) atomicOr(a.flags, kFlagBadSeqlens);
   const long long c = block * plan.per;
   if (c >= r.total) return r;
   if (a.n_seqs == 1) {
@@ -388,6 +420,7 @@ struct AttnWalk {
       out.t0 = plan.cut(s, u0, u.nt, at);
       out.t1 = plan.cut(s, u0, u.nt, end);
       out.slot = out.t0 > 0 ? 2 * block : (out.t1 < u.nt ? 2 * block + 1 : -1);
+      out.last = out.slot == 2 * block + 1 ? plan.last_block(s, u0, u.nt) : block;
       u0 += plan.unit_cost(s, u);
       if (!plan.after(s, u)) {
         int seq = u.seq;

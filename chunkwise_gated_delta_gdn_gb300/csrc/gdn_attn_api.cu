@@ -44,7 +44,7 @@ gdn_status check_cache(int page_size, int max_pages, int n_pages) {
 size_t part_bytes(const gdn::AttnLaunch &l, int d) {
   if (!l.split) return 0;
   const size_t rows = (size_t)2 * l.blocks * l.rows;
-  return rows * d * sizeof(float) + rows * sizeof(float2);
+  return rows * d * sizeof(float) + rows * sizeof(float2) + (size_t)l.blocks * gdn::kAttnJobBytes;
 }
 
 // A token stride: at least the row, in 16-byte steps.
@@ -85,6 +85,7 @@ gdn_status launch(gdn::AttnArgs &a, int d, int dtype, float scale, const gdn::At
   a.scale_log2 = scale * 1.44269504088896340736f;
   a.part_o = static_cast<float4 *>(workspace);
   a.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + rows * d * sizeof(float));
+  a.jobs = l.split ? reinterpret_cast<gdn::AttnJob *>(a.part_ml + rows) : nullptr;
   return gdn::launch_attn(a, d, dtype, l, stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -215,6 +216,9 @@ gdn_status gdn_attn_paged_fwd(const void *q, const void *k_cache, const void *v_
   a.q = q; a.k = k_cache; a.v = v_cache; a.o = o; a.lse = lse; a.table = block_table;
   a.q_stride = q_stride;
   a.page_size = page_size; a.max_pages = max_pages; a.n_pages = n_pages;
+  a.page_log = -1;
+  for (int log = 4; log < 31; log++)
+    if (page_size == 1 << log) a.page_log = log;
   a.flags = flags;
   return launch(a, d, dtype, scale, l, workspace, stream);
 }

@@ -54,6 +54,7 @@ struct Smem {
   static constexpr int kUsed = kSlot + 8;  // [X] int2: stages that the scores free
   static constexpr int kBytes = kUsed + 16;
 };
+static_assert(kStaged * sizeof(AttnStaged) <= Smem<128>::kStages * Smem<128>::kTileBytes, "staging in the ring");
 static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "shared memory of one SM");
 
 // Two fp32 values in one 64-bit register pair: one instruction for both.
@@ -294,6 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 16 && lane < 4)
     prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : &maps.q_pack);
   if (warp == 17) tmem_alloc(smem_addr(slot), 512);
+  AttnStaged *staged = reinterpret_cast<AttnStaged *>(sm + SM::kRing);  // until the first unit
+  attn_stage(a, staged, blockIdx.x);
+  fence_proxy_async();
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel waits for this one's end
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -518,14 +523,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 18) {
       // -------------------------------------------------------------- plan
       AttnPlan<TcShape> plan(a.H, a.HKV);
-      const AttnStart st = attn_start(a, plan, blockIdx.x, gridDim.x);
+      const AttnStart st = attn_start(a, plan, staged, blockIdx.x, gridDim.x);
+      fence_proxy_async();  // what was staged has been read: the ring may be filled
+      __syncwarp();
       AttnWalk<TcShape> walk(a, plan, st, blockIdx.x);
       Ring<kUnits> at;
       AttnUnit u;
       bool more = true;
+      if (a.jobs && lane == 0) a.jobs[blockIdx.x].rows = 0;
       while (more) {
         more = walk.next(u);
         if (!more) u.seq = -1;
+        else if (lane == 0 && u.slot == 2 * (int)blockIdx.x + 1) a.jobs[blockIdx.x] = attn_job(u);
         if (!__all_sync(0xffffffffu, mbar_wait(bars.unit_empty(at.i), at.round ^ 1, abort))) break;
         if (lane == 0) {
           unit_ring[at.i] = u;
@@ -544,8 +553,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       AttnUnit u, old;         // this unit, and the one whose last values are still to come
       int left[2] = {-1, -1};  // its last tiles
       bool shared = false;     // one value tile for both X
-      // one tile of keys or values of unit w into the next stage
-      auto load = [&](const AttnUnit &w, int tile, const CUtensorMap *map) {
+      // Page numbers of 32 pages in a row, a lane each, for the key tiles and
+      // for the value tiles that follow them: read once in 32 pages, not once
+      // per tile, where their latency held the loads at 2700 clocks a tile.
+      struct Window {
+        int seq, base, page;
+      } win[2] = {{-1, 0, 0}, {-1, 0, 0}};
+      auto page_of = [&](int key) {
+        return a.page_log >= 0 ? key >> a.page_log : key / a.page_size;
+      };
+      // one tile of keys (which = 0) or values (1) of unit w into the next stage
+      auto load = [&](const AttnUnit &w, int tile, int which) {
+        const CUtensorMap *map = which ? &maps.v : &maps.k;
         const uint32_t full = bars.kv_full(ring.i), dst = sRing + ring.i * SM::kTileBytes;
         const int key = tile * 128;
         if constexpr (PAGED) {
@@ -553,16 +572,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           // are not loaded (what they leave in shared memory is masked)
           const int rest = w.len - key;
           const int n = rest <= 0 ? 0 : min((rest + box - 1) / box, 128 / box);
-          int page = 0, first = 0;
-          if (lane < n) {
-            const int k0 = key + lane * box;
-            page = __ldg(a.table + (long long)w.seq * a.max_pages + k0 / a.page_size);
-            first = k0 % a.page_size;
-            // an out-of-range page reads as zeros
-            if (page < 0 || page >= a.n_pages) {
-              if (a.flags) atomicOr(a.flags, kFlagBadSeqlens);
-              page = a.n_pages;  // just past the cache
-            }
+          Window &pages = win[which];
+          const int last = w.len - 1, k0 = min(key + lane * box, last);
+          const int index = page_of(k0);
+          const int lo = __shfl_sync(0xffffffffu, index, 0), hi = __shfl_sync(0xffffffffu, index, max(n, 1) - 1);
+          if (n > 0 && (pages.seq != w.seq || lo < pages.base || hi >= pages.base + 32)) {
+            pages.seq = w.seq;
+            pages.base = lo;
+            pages.page = __ldg(a.table + (long long)w.seq * a.max_pages + min(lo + lane, page_of(last)));
+          }
+          int page = __shfl_sync(0xffffffffu, pages.page, (index - pages.base) & 31);
+          const int first = k0 - index * a.page_size;
+          if (lane < n && (page < 0 || page >= a.n_pages)) {
+            if (a.flags) atomicOr(a.flags, kFlagBadSeqlens);
+            page = a.n_pages;  // just past the cache: reads as zeros
           }
           wait(bars.kv_empty(ring.i), ring.round ^ 1, abort);
           if (lane == 0) mbar_arrive_expect_tx(full, n * box * 128 * kPanels);
@@ -584,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ring.step();
       };
       auto last_values = [&](int x) {
-        if (left[x] >= 0 && !(shared && x == 1)) load(old, left[x], &maps.v);
+        if (left[x] >= 0 && !(shared && x == 1)) load(old, left[x], 1);
         left[x] = -1;
       };
       while (units.next(u)) {
@@ -604,21 +627,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                           u.head0, u.row0 + i * toks, bars.q_full());
         }
         __syncwarp();
-        load(u, u.t0, &maps.k);
+        load(u, u.t0, 0);
         last_values(1);
         if (narrow) {
-          if (u.t0 + 1 < u.t1) load(u, u.t0 + 1, &maps.k);
+          if (u.t0 + 1 < u.t1) load(u, u.t0 + 1, 0);
           for (int t = u.t0 + 2; t < u.t1; t++) {
-            load(u, t - 2, &maps.v);
-            load(u, t, &maps.k);
+            load(u, t - 2, 1);
+            load(u, t, 0);
           }
           const int odd = (u.t1 - 1 - u.t0) & 1;  // which X has the last tile
           left[0] = u.t1 - 1 - odd;
           left[1] = u.t0 + 1 < u.t1 ? u.t1 - 2 + odd : -1;
         } else {
           for (int t = u.t0; t + 1 < u.t1; t++) {
-            load(u, t, &maps.v);
-            load(u, t + 1, &maps.k);
+            load(u, t, 1);
+            load(u, t + 1, 0);
           }
           left[0] = left[1] = u.t1 - 1;
         }

@@ -118,6 +118,7 @@ struct TransferArgs {
 
 // Softmax attention (gdn_attn*.cu): causal over a whole prompt (kv_lens null:
 // keys = new tokens, row-major with token strides) or over a paged cache.
+struct AttnJob;
 struct AttnArgs {
   const void *q, *k, *v;       // paged: k, v are the caches
   void *o;
@@ -129,6 +130,7 @@ struct AttnArgs {
   int H, HKV;
   long long q_stride, k_stride, v_stride;  // elements between tokens
   int page_size, max_pages, n_pages;
+  int page_log;                // log2 of page_size, or -1
   int max_len;                 // longest length the table can hold
   float scale;
   float scale_log2;            // scale * log2(e)
@@ -138,6 +140,7 @@ struct AttnArgs {
   int plan_shift, plan_grains;
   float4 *part_o;              // partial results (see gdn_attn.cuh)
   float2 *part_ml;
+  AttnJob *jobs;         // [blocks] what is to be joined, or nullptr when nothing is cut
   uint32_t *flags;             // device status word, or nullptr
 };
 // Writes the keys and values of new tokens into the pages of a cache.
@@ -224,7 +227,9 @@ bool encode_bf16_map(CUtensorMap *m, const void *base, int rank, const uint64_t 
                      const uint64_t *strides, const uint32_t *box);
 // attention (bf16: tcgen05, gdn_attn_tc.cu; fp32: gdn_attn.cu).  A launch of
 // `blocks` blocks; `split`: units may be cut between blocks, which takes the
-// merge kernel and 2 * blocks partial results of `rows` rows in the workspace.
+// merge kernel and, in the workspace, 2 * blocks partial results of `rows`
+// rows and a job for each block.
+constexpr size_t kAttnJobBytes = 32;  // of an AttnJob
 struct AttnLaunch {
   int blocks, rows;
   bool split;

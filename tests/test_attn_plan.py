@@ -70,6 +70,7 @@ bool one(const std::vector<int> &q, const std::vector<int> &kv, int H, int HKV, 
   std::map<std::tuple<int, int>, std::vector<int>> pieces;  // (row0, head0) -> slots in order
   std::map<std::tuple<int, int>, AttnUnit> units;
   std::set<int> slots;
+  std::vector<AttnUnit> begun;
   for (int b = 0; b < blocks; b++) {
     AttnStart st{};
     st.total = total; st.seq = a.n_seqs;
@@ -90,6 +91,7 @@ bool one(const std::vector<int> &q, const std::vector<int> &kv, int H, int HKV, 
       if (u.slot >= 0) {
         CHECK(u.slot / 2 == b && slots.insert(u.slot).second);
         pieces[{u.row0, u.head0}].push_back(u.slot);
+        if (u.slot & 1) begun.push_back(u);
       }
       units[{u.row0, u.head0}] = u;
       for (int t = 0; t < u.n_tok; t++)
@@ -105,24 +107,15 @@ bool one(const std::vector<int> &q, const std::vector<int> &kv, int H, int HKV, 
         CHECK(!v.empty() && (long long)v.size() * S::kTile >= visible);
         for (size_t i = 0; i < v.size(); i++) CHECK(v[i] == (int)i);  // in order, each once
       }
-  // the merge, border by border
+  // the merge goes by what each unit's first block says of the last one
   std::set<std::tuple<int, int>> merged;
-  for (int i = 1; i < blocks; i++) {
-    const long long c = i * per;
-    if (c >= total) break;
-    int n = 0;
-    while (n + 1 < a.n_seqs && seq0[n + 1] <= c) n++;
-    bool bad;
-    const AttnSeq s = attn_seq(a, n, bad);
-    if (plan.cost(s) == 0) continue;  // cannot hold a border
-    AttnUnit u;
-    const long long u0 = seq0[n] + plan.find(s, n, c - seq0[n], u);
-    int last;
-    if (!plan.merges(s, u0, u.nt, i, last)) continue;
+  for (const AttnUnit &u : begun) {
     CHECK(merged.insert({u.row0, u.head0}).second);
-    std::vector<int> want{2 * (i - 1) + 1};
-    for (int b = i; b <= last; b++) want.push_back(2 * b);
+    std::vector<int> want{u.slot};
+    for (int b = u.slot / 2 + 1; b <= u.last; b++) want.push_back(2 * b);
     CHECK((pieces[{u.row0, u.head0}] == want));
+    const AttnJob job = attn_job(u);
+    CHECK(job.rows == u.n_tok * u.gp && job.rows <= S::kRows && job.last == u.last);
   }
   CHECK(merged.size() == pieces.size());
   return true;
