@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs 
   extern __shared__ float smem[];
   float *Qs = smem, *Ks = Qs + 64 * kS, *Vs = Ks + 64 * kS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
-  AttnPlan<WarpShape> plan(a.H, a.HKV);
+  AttnPlan<WarpShape> plan(a.H, a.HKV, a.plan_coarse);
   AttnStaged *staged = reinterpret_cast<AttnStaged *>(smem);  // until the first operands
   attn_stage(a, staged, blockIdx.x);
   __syncthreads();
@@ -349,6 +349,11 @@ AttnLaunch plan_launch(AttnArgs &a, int blocks) {
   const int longest = a.kv_lens ? a.max_len : (a.cu ? a.Ttot : a.T);
   l.split = !(AttnPlan<S>::tiles(longest) <= 1 << kMinGrain && units <= blocks);
   if (!l.split) l.blocks = units < 1 ? 1 : (int)units;
+  a.plan_coarse = attn_coarse<S>(units, longest);
+  if (a.plan_coarse < 0) {
+    l.blocks = 0;
+    return l;
+  }
   if (!a.cu && !a.kv_lens && a.T > 0) l.split = attn_plan_prompts<S>(a, l.blocks);
   return l;
 }

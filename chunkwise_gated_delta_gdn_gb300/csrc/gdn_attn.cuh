@@ -106,21 +106,22 @@ __host__ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &a, int n, b
   return s;
 }
 
-// a / b for a >= 0, b > 0; in 32 bits where that is enough
-__host__ __device__ __forceinline__ long long attn_div(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
+// Costs are counted in 32 bits: the host picks the grain of equal shares so
+// that everything costs less than 2^31 (single tiles, but for prompts beyond a
+// million tokens).  The plan is on the way of every call's first load, where
+// 64-bit products and divisions showed.
+using AttnCost = uint32_t;
 
 template <class S>
 struct AttnPlan {
   int G, HKV, groups;
   int gp, tok_log;     // heads and log2 of the tokens of an unpacked unit
+  int coarse;          // log2 of the grain of equal shares
   int shift;           // log2 of the grain, in tiles
   int wide, over;      // cost of an unpacked unit's grain, and of a unit
-  long long per;       // cost of a block's range
+  AttnCost per;        // cost of a block's range
 
-  __host__ __device__ AttnPlan(int H, int hkv) {
+  __host__ __device__ AttnPlan(int H, int hkv, int coarse_) {
     HKV = hkv;
     G = H / hkv;
     gp = G & -G;
@@ -128,11 +129,12 @@ struct AttnPlan {
     tok_log = 0;
     while ((gp << tok_log) < S::kRows) tok_log++;
     groups = H / gp;
+    coarse = coarse_;
     stream(1);
   }
   // equal shares of single tiles / one grain per block
-  __host__ __device__ void stream(long long p) {
-    shift = 0;
+  __host__ __device__ void stream(AttnCost p) {
+    shift = coarse;
     wide = S::kWide;
     over = S::kOver;
     per = p;
@@ -144,77 +146,80 @@ struct AttnPlan {
     per = 1;
   }
 
-  __host__ __device__ bool packed(const AttnSeq &s) const {
-    return G <= S::kPack && s.nq * (long long)G <= S::kPack;
+  __host__ __device__ bool packed(int nq) const {
+    return G <= S::kPack && nq <= S::kPack && nq * G <= S::kPack;
   }
-  __host__ __device__ int token_tiles(const AttnSeq &s) const {
-    return (s.nq + (1 << tok_log) - 1) >> tok_log;
-  }
+  __host__ __device__ int token_tiles(int nq) const { return (nq + (1 << tok_log) - 1) >> tok_log; }
   __host__ __device__ static int tiles(int keys) {
     return keys <= S::kTile ? 1 : (int)(((unsigned)keys + S::kTile - 1) / S::kTile);
   }
   __host__ __device__ int grains_of(int keys) const {
     return (tiles(keys) + (1 << shift) - 1) >> shift;
   }
-  __host__ __device__ static int tile_log() {
-    int l = 0;
-    while ((1 << l) < S::kTile) l++;
-    return l;
-  }
+  __host__ __device__ static constexpr int tile_log() { return S::kTile == 128 ? 7 : 6; }
+  static_assert(S::kTile == 128 || S::kTile == 64, "tile_log()");
   // sum over i < n of floor(i / 2^r)
-  __host__ __device__ static long long floors(long long n, int r) {
-    const long long q = n >> r;
+  __host__ __device__ static AttnCost floors(AttnCost n, int r) {
+    const AttnCost q = n >> r;
     return ((q * (q - 1) / 2) << r) + q * (n - (q << r));
   }
   // grains of the first x token tiles (all of them full):
   // sum over i < x of ceil((base + (i + 1) tok) / grain)
-  __host__ __device__ long long prefix(int base, long long x) const {
+  __host__ __device__ AttnCost prefix(int base, AttnCost x) const {
     const int grain_log = tile_log() + shift;
-    const long long up = (1LL << grain_log) - 1;
+    const AttnCost up = (1u << grain_log) - 1;
     if (tok_log > grain_log)
       return ((x * (x + 1) / 2) << (tok_log - grain_log)) + x * ((base + up) >> grain_log);
     const int r = grain_log - tok_log;
-    const long long a = base + up + (1 << tok_log);
-    const long long b = (a & up) >> tok_log;
+    const AttnCost a = base + up + (1u << tok_log);
+    const AttnCost b = (a & up) >> tok_log;
     return x * (a >> grain_log) + floors(b + x, r) - floors(b, r);
   }
   // cost of one head group of an unpacked sequence
-  __host__ __device__ long long group_cost(const AttnSeq &s) const {
-    const int n = token_tiles(s);
-    return (prefix(s.base, n - 1) + grains_of(s.base + s.nq)) * wide + (long long)n * over;
+  __host__ __device__ AttnCost group_cost(int nq, int base) const {
+    const int n = token_tiles(nq);
+    return (prefix(base, n - 1) + grains_of(base + nq)) * wide + (AttnCost)n * over;
   }
-  __host__ __device__ long long cost(const AttnSeq &s) const {
-    if (s.nq == 0) return 0;
-    if (packed(s)) return (long long)HKV * (grains_of(s.base + s.nq) + over);
-    return group_cost(s) * groups;
+  __host__ __device__ AttnCost cost(int nq, int base) const {
+    if (nq == 0) return 0;
+    if (packed(nq)) return (AttnCost)HKV * (grains_of(base + nq) + over);
+    return group_cost(nq, base) * groups;
   }
 
-  // Unit that covers cost `c` (0 <= c < cost(s)) of sequence s; returns where
-  // the unit begins.  t0, t1 and slot are left to the caller.
-  __host__ __device__ long long find(const AttnSeq &s, int seq, long long c, AttnUnit &u) const {
+  // Unit that covers cost `c` (0 <= c < cost) of sequence s; returns where the
+  // unit begins.  t0, t1, slot and last are left to the caller.
+  __host__ __device__ AttnCost find(const AttnSeq &s, int seq, AttnCost c, AttnUnit &u) const {
     u.seq = seq;
     u.len = s.len;
-    if (packed(s)) {
+    if (packed(s.nq)) {
+      const AttnCost each = grains_of(s.base + s.nq) + over;
       u.nt = tiles(s.base + s.nq);
-      const int each = ((u.nt + (1 << shift) - 1) >> shift) + over;
-      u.kvh = (int)attn_div(c, each);
+      u.kvh = (int)(c / each);
       u.head0 = u.kvh * G;
       u.gp = G;
       u.row0 = s.q0;
       u.n_tok = s.nq;
       u.pos0 = s.past;
-      return (long long)u.kvh * each;
+      return u.kvh * each;
     }
-    const long long per_group = group_cost(s);
-    const int group = (int)attn_div(c, per_group);
-    const long long rem = c - group * per_group;
-    int lo = 0, hi = token_tiles(s) - 1;  // last token tile that begins at or before rem
+    const AttnCost per_group = group_cost(s.nq, s.base);
+    const int group = (int)(c / per_group);
+    const AttnCost rem = c - group * per_group;
+    // last token tile that begins at or before rem
+    int lo = 0, hi = rem == 0 ? 0 : token_tiles(s.nq) - 1;
+    AttnCost at = 0;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (prefix(s.base, mid) * wide + (long long)mid * over <= rem) lo = mid; else hi = mid - 1;
+      const AttnCost here = prefix(s.base, mid) * wide + (AttnCost)mid * over;
+      if (here <= rem) {
+        lo = mid;
+        at = here;
+      } else {
+        hi = mid - 1;
+      }
     }
     place(s, group, lo, u);
-    return group * per_group + prefix(s.base, lo) * wide + (long long)lo * over;
+    return group * per_group + at;
   }
   // token tile `tile` of head group `group` of an unpacked sequence
   __host__ __device__ void place(const AttnSeq &s, int group, int tile, AttnUnit &u) const {
@@ -223,68 +228,71 @@ struct AttnPlan {
     u.nt = tiles(s.base + first + u.n_tok);
     u.gp = gp;
     u.head0 = group * gp;
-    u.kvh = group / (G / gp);
+    u.kvh = u.head0 / G;
     u.row0 = s.q0 + first;
     u.pos0 = s.past + first;
   }
   // the unit behind u in the same sequence; false when u is the last one
   __host__ __device__ bool after(const AttnSeq &s, AttnUnit &u) const {
-    if (packed(s)) {
-      if (u.kvh + 1 == HKV) return false;
+    if (packed(s.nq)) {
       u.kvh++;
       u.head0 += G;
-      return true;
+      return u.kvh < HKV;
     }
-    const int tile = (u.row0 - s.q0) >> tok_log;
-    int group = u.head0 / gp;
-    if (tile + 1 < token_tiles(s)) {
-      place(s, group, tile + 1, u);
-    } else {
-      if (group + 1 == groups) return false;
-      place(s, group + 1, 0, u);
+    int tile = ((u.row0 - s.q0) >> tok_log) + 1, group = u.head0 / gp;
+    if (tile == token_tiles(s.nq)) {
+      tile = 0;
+      if (++group == groups) return false;
     }
+    place(s, group, tile, u);
     return true;
   }
+  __host__ __device__ int weight(const AttnSeq &s) const { return packed(s.nq) ? 1 : wide; }
   // cost of unit u
-  __host__ __device__ long long unit_cost(const AttnSeq &s, const AttnUnit &u) const {
-    return over + (long long)((u.nt + (1 << shift) - 1) >> shift) * (packed(s) ? 1 : wide);
+  __host__ __device__ AttnCost unit_cost(const AttnSeq &s, const AttnUnit &u) const {
+    return over + (AttnCost)((u.nt + (1 << shift) - 1) >> shift) * weight(s);
   }
   // first tile at or after cost c of a unit that begins at cost u0
-  __host__ __device__ int cut(const AttnSeq &s, long long u0, int nt, long long c) const {
+  __host__ __device__ int cut(const AttnSeq &s, AttnCost u0, int nt, AttnCost c) const {
+    if (c <= u0 + over) return 0;
     c -= u0 + over;
-    if (c <= 0) return 0;
-    const int w = packed(s) ? 1 : wide;
-    const long long t = ((c + w - 1) >> (w == 1 ? 0 : 1)) << shift;
     static_assert(S::kWide == 1 || S::kWide == 2, "a shift in cut()");
-    return t < nt ? (int)t : nt;
+    const AttnCost grain = weight(s) == 1 ? c : (c + 1) >> 1;
+    return grain < (AttnCost)((nt + (1 << shift) - 1) >> shift) ? (int)(grain << shift) : nt;
   }
   // last block with a piece of the unit that begins at cost u0
-  __host__ __device__ int last_block(const AttnSeq &s, long long u0, int nt) const {
-    const int w = packed(s) ? 1 : wide;
-    const long long grains = (nt + (1 << shift) - 1) >> shift;
-    return (int)attn_div(u0 + over + (grains - 1) * w, per);
+  __host__ __device__ int last_block(const AttnSeq &s, AttnCost u0, int nt) const {
+    const AttnCost grains = (nt + (1 << shift) - 1) >> shift;
+    return (int)((u0 + over + (grains - 1) * weight(s)) / per);
   }
 
-  // What the totals decide: `weighted` is the cost of everything in stream
-  // form, `pieces(log)` the number of grains of 2^log tiles.  Returns the cost
-  // of everything under the plan that was chosen.
+  // Chooses; `total()` is the cost of everything under the plan as it stands.
+  // Returns it for the plan that was chosen.
   template <class F>
-  __host__ __device__ long long choose(long long weighted, int n_blocks, F pieces) {
-    const long long share = attn_div(weighted + n_blocks - 1, n_blocks);
+  __host__ __device__ AttnCost choose(int n_blocks, F total) {
     // a grain of up to kSlack tiles more than an equal share costs less than a
     // second unit's start and end
     constexpr int kSlack = 4;
-    for (int log = kMinGrain; log <= kMaxGrain; log++) {
-      if (log > kMinGrain && (1 << log) > share + kSlack) break;
-      if ((2LL << log) < share / S::kWide) continue;  // far too many grains
-      const long long n = pieces(log);
-      if (n <= n_blocks) {
-        grains(log);
-        return n;
+    AttnCost weighted = 0, share = 0;
+    int log = kMinGrain - 1;
+    stream(1);
+    while (true) {
+      const AttnCost t = total();
+      if (log < kMinGrain) {
+        weighted = t;
+        share = (t + n_blocks - 1) / n_blocks;
+        log = kMinGrain;
+      } else if (t <= (AttnCost)n_blocks) {
+        return t;
+      } else {
+        log++;
       }
+      while (log <= kMaxGrain && (2u << log) < share / S::kWide) log++;  // far too many grains
+      if (log > kMaxGrain || (log > kMinGrain && (1u << log) > share + kSlack)) break;
+      grains(log);
     }
-    stream(share + (share & (S::kWide - 1)));
-    if (per < S::kWide) per = S::kWide;
+    share += share & (S::kWide - 1);
+    stream(share < S::kWide ? S::kWide : share);
     return weighted;
   }
 };
@@ -292,8 +300,8 @@ struct AttnPlan {
 // What a block needs to start: the cost of everything and the sequence its
 // first cost falls into.
 struct AttnStart {
-  long long total;
-  long long seq0;   // cost at which sequence `seq` begins
+  AttnCost total;
+  AttnCost seq0;    // cost at which sequence `seq` begins
   int seq;          // n_seqs when the block has no work
 };
 
@@ -321,7 +329,7 @@ __device__ __forceinline__ void attn_stage(const AttnArgs &a, AttnStaged *staged
 // All lanes of one warp: choose the plan and find the start of range `block`.
 template <class S>
 __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &plan,
-                                                const AttnStaged *staged, long long block,
+                                                const AttnStaged *staged, int block,
                                                 int n_blocks) {
   const int lane = threadIdx.x & 31;
   constexpr uint32_t kAll = 0xffffffffu;
@@ -333,52 +341,37 @@ __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &
     if (a.plan_grains) plan.grains(a.plan_shift);
     plan.per = a.plan_per;
     r.total = a.plan_total;
-    const long long c = block * plan.per;
+    const AttnCost c = block * plan.per;
     if (c < r.total) {
-      r.seq = (int)attn_div(c, a.plan_seq);
+      r.seq = (int)(c / a.plan_seq);
       r.seq0 = r.seq * a.plan_seq;
     }
     return r;
   }
   auto cost_of = [&](int n) {
-    if (n >= kStaged) {
-      bool bad;
-      return plan.cost(attn_seq(a, n, bad));
-    }
-    AttnSeq s;
-    s.nq = staged[n].nq;
-    s.base = staged[n].base;
-    return plan.cost(s);
+    if (n < kStaged) return plan.cost(staged[n].nq, staged[n].base);
+    bool bad;
+    const AttnSeq s = attn_seq(a, n, bad);
+    return plan.cost(s.nq, s.base);
   };
-  auto sum = [&] {
-    if (a.n_seqs == 1) return cost_of(0);
-    long long mine = 0;
+  r.total = plan.choose(n_blocks, [&] {
+    AttnCost mine = 0;
     for (int n = lane; n < a.n_seqs; n += 32) mine += cost_of(n);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(kAll, mine, d);
-    return mine;
-  };
-  r.total = plan.choose(sum(), n_blocks, [&](int log) {
-    plan.grains(log);
-    return sum();
+    return __reduce_add_sync(kAll, mine);
   });
-  const long long c = block * plan.per;
+  const AttnCost c = block * plan.per;
   if (c >= r.total) return r;
-  if (a.n_seqs == 1) {
-    r.seq = 0;
-    return r;
-  }
-  long long before = 0;
+  AttnCost before = 0;
   for (int n0 = 0; n0 < a.n_seqs; n0 += 32) {
     const int n = n0 + lane;
-    const long long mine = n < a.n_seqs ? cost_of(n) : 0;
-    long long incl = mine;
+    const AttnCost mine = n < a.n_seqs ? cost_of(n) : 0;
+    AttnCost incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long up = __shfl_up_sync(kAll, incl, d);
+      const AttnCost up = __shfl_up_sync(kAll, incl, d);
       if (lane >= d) incl += up;
     }
-    const long long excl = before + incl - mine;
+    const AttnCost excl = before + incl - mine;
     const uint32_t hit = __ballot_sync(kAll, c >= excl && c < excl + mine);
     if (hit) {
       const int who = __ffs(hit) - 1;
@@ -398,24 +391,31 @@ struct AttnWalk {
   const AttnPlan<S> &plan;
   AttnSeq s;
   AttnUnit u;
-  long long at, end, u0;  // start and end of the range, start of the unit
-  int block;
-  bool more;              // u is a unit that is still to be looked at
+  AttnCost at, end, u0;  // start and end of the range, start of the sequence or unit
+  int seq, block;
+  bool fresh;            // the sequence is still to be looked up
 
   __host__ __device__ AttnWalk(const AttnArgs &a_, const AttnPlan<S> &p_, const AttnStart &st,
                                int block_)
       : a(a_), plan(p_), block(block_) {
     at = block * plan.per;
     end = at + plan.per < st.total ? at + plan.per : st.total;
-    more = st.seq < a.n_seqs;
-    if (more) {
-      bool bad;
-      s = attn_seq(a, st.seq, bad);
-      u0 = st.seq0 + plan.find(s, st.seq, at - st.seq0, u);
-    }
+    seq = st.seq;
+    u0 = st.seq0;
+    fresh = true;
   }
   __host__ __device__ bool next(AttnUnit &out) {
-    while (more && u0 < end) {
+    while (seq < a.n_seqs && u0 < end) {
+      if (fresh) {
+        bool bad;
+        s = attn_seq(a, seq, bad);
+        if (s.nq == 0) {
+          seq++;
+          continue;
+        }
+        u0 += plan.find(s, seq, at > u0 ? at - u0 : 0, u);
+        fresh = false;
+      }
       out = u;
       out.t0 = plan.cut(s, u0, u.nt, at);
       out.t1 = plan.cut(s, u0, u.nt, end);
@@ -423,17 +423,8 @@ struct AttnWalk {
       out.last = out.slot == 2 * block + 1 ? plan.last_block(s, u0, u.nt) : block;
       u0 += plan.unit_cost(s, u);
       if (!plan.after(s, u)) {
-        int seq = u.seq;
-        more = false;
-        while (++seq < a.n_seqs) {
-          bool bad;
-          s = attn_seq(a, seq, bad);
-          if (s.nq > 0) {
-            plan.find(s, seq, 0, u);
-            more = true;
-            break;
-          }
-        }
+        fresh = true;
+        seq++;
       }
       if (out.t0 < out.t1) return true;
     }
@@ -441,37 +432,38 @@ struct AttnWalk {
   }
 };
 
+// Most units that a call can have, from what the host knows.
+template <class S>
+inline long long attn_most_units(const AttnArgs &a) {
+  const AttnPlan<S> plan(a.H, a.HKV, 0);
+  const long long groups = plan.groups > a.HKV ? plan.groups : a.HKV;
+  if (!a.cu)
+    return a.n_seqs * (plan.packed(a.T) ? (long long)a.HKV : (long long)plan.groups * plan.token_tiles(a.T));
+  return a.n_seqs * groups + (long long)plan.groups * (a.Ttot >> plan.tok_log);
+}
+
+// Grain of equal shares for which at most `units` units of up to `longest`
+// keys cost less than 2^31; -1 when there is none.
+template <class S>
+inline int attn_coarse(long long units, int longest) {
+  for (int log = 0; log < 24; log++) {
+    const long long grains = (AttnPlan<S>::tiles(longest) + (1LL << log) - 1) >> log;
+    if (units <= (1LL << 31) / (grains * S::kWide + S::kOver)) return log;
+  }
+  return -1;
+}
+
 // The plan of equal prompts (lengths that the host knows), into `a`; returns
 // whether a unit may be cut between blocks.
 template <class S>
 inline bool attn_plan_prompts(AttnArgs &a, int n_blocks) {
-  AttnPlan<S> plan(a.H, a.HKV);
-  bool bad;
-  const AttnSeq s = attn_seq(a, 0, bad);
-  a.plan_total = plan.choose(plan.cost(s) * a.n_seqs, n_blocks, [&](int log) {
-    plan.grains(log);
-    return plan.cost(s) * a.n_seqs;
-  });
-  a.plan_seq = plan.cost(s);
+  AttnPlan<S> plan(a.H, a.HKV, a.plan_coarse);
+  a.plan_total = plan.choose(n_blocks, [&] { return plan.cost(a.T, 0) * a.n_seqs; });
+  a.plan_seq = plan.cost(a.T, 0);
   a.plan_per = plan.per;
   a.plan_shift = plan.shift;
   a.plan_grains = plan.over == 0;
-  return !(a.plan_grains && plan.tiles(s.nq) <= 1 << plan.shift);
-}
-
-// Most units that a call can have, from what the host knows.
-template <class S>
-inline long long attn_most_units(const AttnArgs &a) {
-  const AttnPlan<S> plan(a.H, a.HKV);
-  const long long groups = plan.groups > a.HKV ? plan.groups : a.HKV;
-  if (!a.cu) {
-    bool bad;
-    AttnArgs one = a;
-    one.kv_lens = nullptr;
-    const AttnSeq s = attn_seq(one, 0, bad);
-    return a.n_seqs * (plan.packed(s) ? (long long)a.HKV : (long long)plan.groups * plan.token_tiles(s));
-  }
-  return a.n_seqs * groups + (long long)plan.groups * (a.Ttot >> plan.tok_log);
+  return !(a.plan_grains && plan.tiles(a.T) <= 1 << plan.shift);
 }
 
 }  // namespace gdn

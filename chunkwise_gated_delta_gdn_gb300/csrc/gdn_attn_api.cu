@@ -143,6 +143,7 @@ gdn_status gdn_attn_fwd(const void *q, const void *k, const void *v, void *o, fl
   gdn::AttnArgs a{};
   fill_shape(a, cu_seqlens, n, T, Ttot, H, HKV);
   const gdn::AttnLaunch l = gdn::attn_launch(a, d, dtype);
+  if (l.blocks == 0) return GDN_ERR_UNSUPPORTED;
   const size_t ws = part_bytes(l, d);
   if (ws > 0 && (!workspace || workspace_bytes < ws)) return GDN_ERR_WORKSPACE;
   if (!aligned_to(workspace, 256)) return GDN_ERR_INVALID_ARG;
@@ -203,6 +204,7 @@ gdn_status gdn_attn_paged_fwd(const void *q, const void *k_cache, const void *v_
   a.kv_lens = kv_lens;
   a.max_len = page_size * max_pages;
   const gdn::AttnLaunch l = gdn::attn_launch(a, d, dtype);
+  if (l.blocks == 0) return GDN_ERR_UNSUPPORTED;
   const size_t ws = part_bytes(l, d);
   if (ws > 0 && (!workspace || workspace_bytes < ws)) return GDN_ERR_WORKSPACE;
   if (!aligned_to(workspace, 256)) return GDN_ERR_INVALID_ARG;

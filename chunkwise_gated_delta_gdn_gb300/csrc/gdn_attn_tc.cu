@@ -441,23 +441,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m_scaled = m * sl2, f_own = 1.f, f_other = 0.f;
       if (both) {
-        // row sums and maxima of both X; the first meeting also says that the
-        // other X's output is complete
-        *own_ex = l;
+        // Row sums and maxima of both X: the sum of the halves and the maximum
+        // in the places of the two halves' tile maxima.  The meeting also says
+        // that the other X's output is complete.
+        float *place = row_ex + x * 256 + r, *other = row_ex + (x ^ 1) * 256 + r;
+        if (!idle) {
+          if (half == 1) *own_ex = l;
+          meet_half();
+          if (half == 0) {
+            const float sum = l + *other_ex;
+            place[0] = sum;
+            place[128] = m_scaled;
+          }
+        }
         fence_before_sync();
         meet_all(0);
         fence_after_sync();
-        const float l_own = l + *other_ex;
-        const float l_other = row_ex[(x ^ 1) * 256 + r] + row_ex[(x ^ 1) * 256 + 128 + r];
-        meet_all(1);
-        if (half == 0) *own_ex = m_scaled;
-        meet_all(0);
-        const float m_other = row_ex[(x ^ 1) * 256 + r];
-        const float top = fmaxf(m_scaled, m_other);
+        const float top = fmaxf(m_scaled, other[128]);
         const float base = top == -CUDART_INF_F ? 0.f : top;
         f_own = ex2(m_scaled - base);
-        f_other = ex2(m_other - base);
-        l = f_own * l_own + f_other * l_other;
+        f_other = ex2(other[128] - base);
+        l = f_own * place[0] + f_other * other[0];
         m_scaled = top;
       } else if (mine && !idle) {
         *own_ex = l;
@@ -522,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     if (warp == 18) {
       // -------------------------------------------------------------- plan
-      AttnPlan<TcShape> plan(a.H, a.HKV);
+      AttnPlan<TcShape> plan(a.H, a.HKV, a.plan_coarse);
       const AttnStart st = attn_start(a, plan, staged, blockIdx.x, gridDim.x);
       fence_proxy_async();  // what was staged has been read: the ring may be filled
       __syncwarp();
@@ -798,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 bool make_maps(Maps &m, const AttnArgs &a, int d, int box) {
-  const AttnPlan<TcShape> plan(a.H, a.HKV);
+  const AttnPlan<TcShape> plan(a.H, a.HKV, 0);
   const uint64_t D = d;
   const uint64_t q_dims[3] = {D, (uint64_t)a.H, (uint64_t)a.Ttot};
   const uint64_t q_strides[2] = {D * 2, (uint64_t)a.q_stride * 2};

@@ -136,8 +136,9 @@ struct AttnArgs {
   float scale_log2;            // scale * log2(e)
   // the plan where the host can make it (gdn_attn.cuh): equal prompts;
   // plan_total = 0 otherwise
-  long long plan_total, plan_per, plan_seq;
+  uint32_t plan_total, plan_per, plan_seq;
   int plan_shift, plan_grains;
+  int plan_coarse;             // log2 of the grain of equal shares
   float4 *part_o;              // partial results (see gdn_attn.cuh)
   float2 *part_ml;
   AttnJob *jobs;         // [blocks] what is to be joined, or nullptr when nothing is cut
@@ -231,7 +232,7 @@ bool encode_bf16_map(CUtensorMap *m, const void *base, int rank, const uint64_t 
 // rows and a job for each block.
 constexpr size_t kAttnJobBytes = 32;  // of an AttnJob
 struct AttnLaunch {
-  int blocks, rows;
+  int blocks, rows;  // blocks = 0: more work than the plan can count
   bool split;
 };
 AttnLaunch attn_launch(AttnArgs &a, int d, int dtype);  // also fills the plan in `a`

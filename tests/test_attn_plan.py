@@ -35,32 +35,33 @@ static int rnd(int lo, int hi) {  // uniform over lo..hi
 }
 
 template <class S>
-bool one(const std::vector<int> &q, const std::vector<int> &kv, int H, int HKV, int blocks, int force) {
+bool one(const std::vector<int> &q, const std::vector<int> &kv, int H, int HKV, int blocks, int force, int coarse) {
   std::vector<int32_t> cu(1, 0), lens(kv.begin(), kv.end());
   for (int n : q) cu.push_back(cu.back() + n);
   AttnArgs a{};
   a.cu = cu.data(); a.kv_lens = lens.data(); a.n_seqs = (int)q.size(); a.Ttot = cu.back();
   a.H = H; a.HKV = HKV; a.max_len = 1 << 30;
-  AttnPlan<S> plan(H, HKV);
+  AttnPlan<S> plan(H, HKV, coarse);
   CHECK(H % plan.gp == 0 && plan.G % plan.gp == 0 && plan.gp << plan.tok_log == S::kRows);
   std::vector<long long> seq0;
   auto sum = [&] {
-    long long total = 0;
+    AttnCost total = 0;
     bool bad;
     seq0.clear();
     for (int n = 0; n < a.n_seqs; n++) {
       seq0.push_back(total);
-      total += plan.cost(attn_seq(a, n, bad));
+      const AttnSeq s = attn_seq(a, n, bad);
+      total += plan.cost(s.nq, s.base);
     }
     return total;
   };
-  long long total = sum();
+  AttnCost total = sum();
   if (force >= 0) {  // any grain and any share, not only those that the kernels choose
     plan.grains(force);
     total = sum();
     plan.per = total ? (total + blocks - 1) / blocks : 1;
   } else {
-    total = plan.choose(total, blocks, [&](int log) { plan.grains(log); return sum(); });
+    total = plan.choose(blocks, sum);
     CHECK(sum() == total);
     grains_chosen += plan.over == 0;
   }
@@ -76,7 +77,8 @@ bool one(const std::vector<int> &q, const std::vector<int> &kv, int H, int HKV, 
     st.total = total; st.seq = a.n_seqs;
     for (int n = 0; n < a.n_seqs; n++) {
       bool bad;
-      const long long c = plan.cost(attn_seq(a, n, bad));
+      const AttnSeq s = attn_seq(a, n, bad);
+      const long long c = plan.cost(s.nq, s.base);
       if (b * per >= seq0[n] && b * per < seq0[n] + c) { st.seq = n; st.seq0 = seq0[n]; }
     }
     AttnWalk<S> walk(a, plan, st, b);
@@ -133,8 +135,8 @@ int main() {
       kv.push_back(rnd(0, 9) == 0 ? rnd(0, nq) : nq + rnd(0, rnd(0, 1) ? 100 : 1500));
     }
     const int blocks = rnd(0, 1) ? rnd(1, 9) : rnd(10, 200), force = rnd(0, 1) ? -1 : rnd(0, 4);
-    if (!one<AttnShape<64, 64, 64, 1, 1>>(q, kv, hkv * g, hkv, blocks, force) ||
-        !one<AttnShape<256, 128, 128, 2, 4>>(q, kv, hkv * g, hkv, blocks, force)) {
+    if (!one<AttnShape<64, 64, 64, 1, 1>>(q, kv, hkv * g, hkv, blocks, force, trial % 3) ||
+        !one<AttnShape<256, 128, 128, 2, 4>>(q, kv, hkv * g, hkv, blocks, force, trial % 3)) {
       std::printf("trial %d: hkv %d g %d blocks %d\n", trial, hkv, g, blocks);
       return 1;
     }
