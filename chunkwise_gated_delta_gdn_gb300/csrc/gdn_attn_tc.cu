@@ -560,6 +560,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Page numbers of 32 pages in a row, a lane each, for the key tiles and
       // for the value tiles that follow them: read once in 32 pages, not once
       // per tile, where their latency held the loads at 2700 clocks a tile.
+      // A decode step reads a cache once: its keys and values make room for one
+      // another in L2, not in place of what others need (this kernel's code for
+      // the next call among it).
+      const uint64_t once = l2_evict_first(), often = l2_evict_normal();
       struct Window {
         int seq, base, page;
       } win[2] = {{-1, 0, 0}, {-1, 0, 0}};
@@ -596,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane < n)
             tma_load_5d(dst + lane * box * 128 * kPanels, map, 0, 0, 0,
-                        page * (a.page_size >> 3) + (first >> 3), w.kvh, full);
+                        page * (a.page_size >> 3) + (first >> 3), w.kvh, full,
+                        w.n_tok * w.gp <= 128 ? once : often);
         } else {
           wait(bars.kv_empty(ring.i), ring.round ^ 1, abort);
           if (lane == 0) {
