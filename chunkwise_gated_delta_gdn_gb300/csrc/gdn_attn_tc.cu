@@ -36,6 +36,7 @@ using TcShape = AttnShape<256, 128, 128, 2, 4>;
 constexpr int kThreads = 640;
 constexpr int kUnits = 4;              // unit ring
 constexpr int kPanel = 128 * 128;      // bytes of 128 rows x 64 bf16
+constexpr float kBf16Inf = 0x1.ffp127f;  // what rounds to infinity in bf16
 constexpr float kRescale = 8.f;        // log2 growth of a row maximum that is let stand
 
 template <int D>
@@ -209,10 +210,14 @@ struct Units {
 
 // N fp32 values of every lane's row as bf16 to columns [c, c + N) of its row
 // `out`.  Written as they lie, a 16-byte piece per lane and instruction, every
-// instruction touches 32 cache lines; so N / 8 neighbouring lanes exchange
-// pieces first, and each instruction writes whole 2 N byte stretches of rows.
+// instruction touches 32 cache lines, one a clock: 4096 clocks for the 256 rows
+// of a wide unit (`many`).  So N / 8 neighbouring lanes exchange pieces first,
+// and each instruction writes 2 N byte stretches of rows (between two lanes
+// only, packed prompts took 10% longer).  A narrow unit's few rows are written
+// as they lie.
 template <int N>
-__device__ __forceinline__ void store_rows(const float (&y)[N], __nv_bfloat16 *out, bool valid, int c) {
+__device__ __forceinline__ void store_rows(const float (&y)[N], __nv_bfloat16 *out, bool valid,
+                                           bool many, int c) {
   constexpr int kPieces = N / 8;  // 16-byte pieces of a row, and lanes that share them: 2 or 4
   const int lane = threadIdx.x & 31, me = lane & (kPieces - 1);
   uint4 p[kPieces];
@@ -220,6 +225,12 @@ __device__ __forceinline__ void store_rows(const float (&y)[N], __nv_bfloat16 *o
   for (int i = 0; i < kPieces; i++)
     p[i] = make_uint4(pack2(y[8 * i], y[8 * i + 1]), pack2(y[8 * i + 2], y[8 * i + 3]),
                       pack2(y[8 * i + 4], y[8 * i + 5]), pack2(y[8 * i + 6], y[8 * i + 7]));
+  if (!many) {
+    if (valid)
+#pragma unroll
+      for (int i = 0; i < kPieces; i++) *reinterpret_cast<uint4 *>(out + c + 8 * i) = p[i];
+    return;
+  }
   auto swap = [](uint4 &keep, uint4 &give, bool upper, int mask) {
     // a lane keeps one of two pieces and gives the other to its partner
     const uint4 send = upper ? keep : give;
@@ -369,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float s[64];
 #pragma unroll
         for (int c = 0; c < 64; c++) s[c] = __uint_as_float(raw[c >> 5][c & 31]);
-        if (t * 128 + 63 > all_see) {
+        if (__builtin_expect(t * 128 + 63 > all_see, 0)) {
           const int lim = limit - t * 128;
 #pragma unroll
           for (int c = 0; c < 64; c++)
@@ -394,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool move = tile_max > m + grow;
         if (t == first) {
           m = tile_max;
-        } else if (__any_sync(0xffffffffu, move)) {
+        } else if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
           const float f = move ? ex2((m - tile_max) * sl2) : 1.f;
           if (move) m = tile_max;
           l *= f;
@@ -503,9 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kCols; i++) y[i] *= inv;
             if (a.flags && valid) {
 #pragma unroll
-              for (int i = 0; i < kCols; i++) finite &= isfinite(y[i]);
+              for (int i = 0; i < kCols; i++) finite &= fabsf(y[i]) < kBf16Inf;
             }
-            store_rows<kCols>(y, out, valid, c);
+            store_rows<kCols>(y, out, valid, !narrow, c);
           }
           __syncwarp();
         }
@@ -513,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (part)
             a.part_ml[(long long)u.slot * TcShape::kRows + row] = make_float2(m_scaled, l);
           else if (a.lse)
-            a.lse[at] = l == 0.f ? -CUDART_INF_F : (m_scaled + log2f(l)) * 0.69314718056f;
+            a.lse[at] = l == 0.f ? -CUDART_INF_F : (m_scaled + __log2f(l)) * 0.69314718056f;
         }
         if (!finite && a.flags) atomicOr(a.flags, kFlagNonfinite);
       }
