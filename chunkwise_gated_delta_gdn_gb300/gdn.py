@@ -422,6 +422,10 @@ def gdn_state_combine(M: torch.Tensor, S_in: torch.Tensor, S_seg: torch.Tensor, 
     return out
 
 
+# The entries below run in a few microseconds on the GPU at their smallest, less
+# than a generous binding takes: each makes one pass over cheap conditions and
+# looks for what is wrong only when one of them fails.
+
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -429,14 +433,15 @@ def _addr(t: Optional[torch.Tensor]):
 def _tokens(t: torch.Tensor, name: str, dev, dtype, B: int, T: int) -> int:
     """Check a ``[B, T, heads, d]`` tensor whose tokens may be strided (a slice of a wider
     projection); returns the elements from one token to the next."""
-    if t.device != dev or t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} on {dev}")
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != T:
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != T:
         raise ValueError(f"{name} must be [{B}, {T}, heads, d]")
-    heads, d = t.shape[2], t.shape[3]
-    sb, st, sh, sd = t.stride()
-    if t.numel() == 0:
+    if t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name} must be {dtype} on {dev}")
+    heads, d = shape[2], shape[3]
+    if t.is_contiguous():
         return heads * d
+    sb, st, sh, sd = t.stride()
     if T == 1:
         st = sb if B > 1 else heads * d
     if (d > 1 and sd != 1) or (heads > 1 and sh != d) or (B > 1 and T > 1 and sb != T * st):
@@ -444,7 +449,7 @@ def _tokens(t: torch.Tensor, name: str, dev, dtype, B: int, T: int) -> int:
     return st
 
 
-def _lengths(cu_seqlens, B: int, dev) -> int:
+def _sequences(cu_seqlens, B: int, dev) -> int:
     """Number of sequences, with cu_seqlens checked."""
     if cu_seqlens is None:
         return B
@@ -454,55 +459,65 @@ def _lengths(cu_seqlens, B: int, dev) -> int:
     return cu_seqlens.numel() - 1
 
 
-def _attn_buffers(q, o, lse, output_lse, flags, workspace, nbytes, dev, stream):
-    """Check the buffers a caller passed and allocate the others; returns (o, lse, workspace, its
-    bytes, the stream)."""
+def _given(q, o, lse, flags, workspace, dev) -> None:
+    """Check the buffers that a caller passed."""
     for name, t in (("o", o), ("lse", lse), ("flags", flags), ("workspace", workspace)):
-        if t is not None:
-            _check(t, name, dev)
-    shape = q.shape
-    if o is not None and (o.shape != shape or o.dtype != q.dtype):
+        _check(t, name, dev)
+    if o is not None and (o.shape != q.shape or o.dtype != q.dtype):
         raise ValueError("o must match q in shape and dtype")
-    if lse is not None and (lse.shape != shape[:3] or lse.dtype != torch.float32):
+    if lse is not None and (lse.shape != q.shape[:3] or lse.dtype != torch.float32):
         raise ValueError("lse must be float32 [B, T, H]")
     if flags is not None and (flags.element_size() != 4 or flags.numel() < 1):
         raise TypeError("flags must hold at least one 4-byte element")
-    if workspace is not None:
-        nbytes = workspace.numel() * workspace.element_size()
-    current = torch.cuda.current_stream(dev.index)
-    if stream is None or stream == current:
-        stream = current
-        o, lse, workspace = _allocate(q, o, lse, output_lse, workspace, nbytes, dev)
-    else:  # what is allocated here belongs to the stream it is used on
-        with torch.cuda.stream(stream):
-            o, lse, workspace = _allocate(q, o, lse, output_lse, workspace, nbytes, dev)
-    return o, lse, workspace, nbytes, stream
-
-
-def _allocate(q, o, lse, output_lse, workspace, nbytes, dev):
-    if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    if lse is None and output_lse:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
-    if workspace is None and nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    return o, lse, workspace
 
 
 def _cache(k_cache, v_cache, block_table, kv_lens, n_seqs, HKV, d, dtype, dev):
     """Check a paged cache; returns (page_size, max_pages, n_pages)."""
+    shape, table = k_cache.shape, block_table.shape
+    if (v_cache.shape == shape and shape[2:] == (HKV, d) and len(table) == 2 and table[0] == n_seqs
+            and kv_lens.shape == (n_seqs,) and k_cache.dtype == dtype and v_cache.dtype == dtype
+            and block_table.dtype == torch.int32 and kv_lens.dtype == torch.int32
+            and k_cache.device == dev and v_cache.device == dev and block_table.device == dev
+            and kv_lens.device == dev and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_table.is_contiguous() and kv_lens.is_contiguous()):
+        return shape[1], table[1], shape[0]
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("block_table", block_table),
                     ("kv_lens", kv_lens)):
         _check(t, name, dev)
     if k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise ValueError(f"k_cache and v_cache must be {dtype}")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[2:] != (HKV, d):
-        raise ValueError("k_cache and v_cache must be [n_pages, page_size, HKV, d]")
     if block_table.dtype != torch.int32 or kv_lens.dtype != torch.int32:
         raise TypeError("block_table and kv_lens must be int32")
-    if block_table.dim() != 2 or block_table.shape[0] != n_seqs or kv_lens.shape != (n_seqs,):
-        raise ValueError(f"block_table must be [{n_seqs}, max_pages], kv_lens [{n_seqs}]")
-    return k_cache.shape[1], block_table.shape[1], k_cache.shape[0]
+    if v_cache.shape != shape or shape[2:] != (HKV, d):
+        raise ValueError("k_cache and v_cache must be [n_pages, page_size, HKV, d]")
+    raise ValueError(f"block_table must be [{n_seqs}, max_pages], kv_lens [{n_seqs}]")
+
+
+def _attn_call(call, workspace_bytes, what, q, o, lse, output_lse, workspace, stream, dev):
+    """Allocate what the caller did not pass and run ``call(o, lse, workspace, its bytes,
+    stream)``.  Buffers allocated here belong to the stream that they are used on.  Small calls
+    need no workspace: it is sized only when the library asks for one."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _attn_call(call, workspace_bytes, what, q, o, lse, output_lse, workspace, None, dev)
+    if o is None:
+        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if lse is None and output_lse:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    out, out_lse = o.data_ptr(), _addr(lse)
+    if workspace is not None:
+        status = call(out, out_lse, workspace.data_ptr(),
+                      workspace.numel() * workspace.element_size(), raw)
+    else:
+        status = call(out, out_lse, None, 0, raw)
+        if status == GDN_ERR_WORKSPACE:
+            nbytes = workspace_bytes()
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            status = call(out, out_lse, workspace.data_ptr(), nbytes, raw)
+    if status != GDN_OK:
+        raise GdnError(status, what)
+    return o, lse
 
 
 def gdn_attn_fwd_workspace_bytes(B: int, T: int, H: int, HKV: int, d: int, n_seqs: int,
@@ -528,23 +543,22 @@ def gdn_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape or k.shape[3] != q.shape[3]:
         raise ValueError("q [B, T, H, d] and k, v [B, T, HKV, d]: inconsistent shapes")
     B, T, H, d = q.shape
-    HKV = k.shape[2]
-    dev, dt = q.device, _dtype_code(q.dtype)
-    qs, ks, vs = (_tokens(t, name, dev, q.dtype, B, T)
-                  for name, t in (("q", q), ("k", k), ("v", v)))
-    n_seqs = _lengths(cu_seqlens, B, dev)
-    nbytes = 0
-    if workspace is None:
-        nbytes = lib.gdn_attn_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, dt)
-    o, lse, workspace, nbytes, stream = _attn_buffers(q, o, lse, output_lse, flags, workspace,
-                                                      nbytes, dev, stream)
-    status = lib.gdn_attn_fwd(
-        _addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), _addr(cu_seqlens), n_seqs, B, T, H, HKV, d,
-        qs, ks, vs, d ** -0.5 if scale is None else scale, dt, _addr(flags), _addr(workspace),
-        nbytes, stream.cuda_stream)
-    if status != GDN_OK:
-        raise GdnError(status, "gdn_attn_fwd")
-    return o, lse
+    HKV, dev, dtype = k.shape[2], q.device, q.dtype
+    dt = _dtype_code(dtype)
+    qs = _tokens(q, "q", dev, dtype, B, T)
+    ks = _tokens(k, "k", dev, dtype, B, T)
+    vs = _tokens(v, "v", dev, dtype, B, T)
+    n_seqs = _sequences(cu_seqlens, B, dev)
+    if not (o is lse is flags is workspace is None):
+        _given(q, o, lse, flags, workspace, dev)
+    if scale is None:
+        scale = d ** -0.5
+    return _attn_call(
+        lambda out, out_lse, ws, nbytes, raw: lib.gdn_attn_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out, out_lse, _addr(cu_seqlens), n_seqs, B, T,
+            H, HKV, d, qs, ks, vs, scale, dt, _addr(flags), ws, nbytes, raw),
+        lambda: lib.gdn_attn_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, dt),
+        "gdn_attn_fwd", q, o, lse, output_lse, workspace, stream, dev)
 
 
 def gdn_attn_paged_fwd_workspace_bytes(B: int, T: int, H: int, HKV: int, d: int, n_seqs: int,
@@ -572,26 +586,24 @@ def gdn_attn_paged_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     if q.dim() != 4 or k_cache.dim() != 4:
         raise ValueError("q must be [B, T, H, d] and the caches [n_pages, page_size, HKV, d]")
     B, T, H, d = q.shape
-    HKV = k_cache.shape[2]
-    dev, dt = q.device, _dtype_code(q.dtype)
-    qs = _tokens(q, "q", dev, q.dtype, B, T)
-    n_seqs = _lengths(cu_seqlens, B, dev)
+    HKV, dev, dtype = k_cache.shape[2], q.device, q.dtype
+    dt = _dtype_code(dtype)
+    qs = _tokens(q, "q", dev, dtype, B, T)
+    n_seqs = _sequences(cu_seqlens, B, dev)
     page_size, max_pages, n_pages = _cache(k_cache, v_cache, block_table, kv_lens, n_seqs, HKV, d,
-                                           q.dtype, dev)
-    nbytes = 0
-    if workspace is None:
-        nbytes = lib.gdn_attn_paged_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, page_size,
-                                                        max_pages, dt)
-    o, lse, workspace, nbytes, stream = _attn_buffers(q, o, lse, output_lse, flags, workspace,
-                                                      nbytes, dev, stream)
-    status = lib.gdn_attn_paged_fwd(
-        _addr(q), _addr(k_cache), _addr(v_cache), _addr(block_table), _addr(kv_lens), _addr(o),
-        _addr(lse), _addr(cu_seqlens), n_seqs, B, T, H, HKV, d, qs, page_size, max_pages, n_pages,
-        d ** -0.5 if scale is None else scale, dt, _addr(flags), _addr(workspace), nbytes,
-        stream.cuda_stream)
-    if status != GDN_OK:
-        raise GdnError(status, "gdn_attn_paged_fwd")
-    return o, lse
+                                           dtype, dev)
+    if not (o is lse is flags is workspace is None):
+        _given(q, o, lse, flags, workspace, dev)
+    if scale is None:
+        scale = d ** -0.5
+    return _attn_call(
+        lambda out, out_lse, ws, nbytes, raw: lib.gdn_attn_paged_fwd(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+            kv_lens.data_ptr(), out, out_lse, _addr(cu_seqlens), n_seqs, B, T, H, HKV, d, qs,
+            page_size, max_pages, n_pages, scale, dt, _addr(flags), ws, nbytes, raw),
+        lambda: lib.gdn_attn_paged_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, page_size,
+                                                       max_pages, dt),
+        "gdn_attn_paged_fwd", q, o, lse, output_lse, workspace, stream, dev)
 
 
 def gdn_kv_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -602,23 +614,22 @@ def gdn_kv_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     """Write the keys and values of new tokens (k, v ``[B, T, HKV, d]`` or packed) into the
     pages, in place; kv_lens counts them already."""
     lib = load()
-    if k.dim() != 4 or v.shape != k.shape:
-        raise ValueError("k and v must be [B, T, HKV, d]")
+    if k.dim() != 4 or v.shape != k.shape or k_cache.dim() != 4:
+        raise ValueError("k and v must be [B, T, HKV, d], the caches [n_pages, page_size, HKV, d]")
     B, T, HKV, d = k.shape
-    dev, dt = k.device, _dtype_code(k.dtype)
-    ks, vs = (_tokens(t, name, dev, k.dtype, B, T) for name, t in (("k", k), ("v", v)))
-    n_seqs = _lengths(cu_seqlens, B, dev)
+    dev, dtype = k.device, k.dtype
+    dt = _dtype_code(dtype)
+    ks, vs = _tokens(k, "k", dev, dtype, B, T), _tokens(v, "v", dev, dtype, B, T)
+    n_seqs = _sequences(cu_seqlens, B, dev)
     page_size, max_pages, n_pages = _cache(k_cache, v_cache, block_table, kv_lens, n_seqs, HKV, d,
-                                           k.dtype, dev)
-    _check(flags, "flags", dev)
-    if flags is not None and (flags.element_size() != 4 or flags.numel() < 1):
-        raise TypeError("flags must hold at least one 4-byte element")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev.index)
+                                           dtype, dev)
+    if flags is not None:
+        _given(k, None, None, flags, None, dev)
+    raw = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream)
     status = lib.gdn_kv_cache_append(
-        _addr(k), _addr(v), _addr(k_cache), _addr(v_cache), _addr(block_table), _addr(kv_lens),
-        _addr(cu_seqlens), n_seqs, B, T, HKV, d, ks, vs, page_size, max_pages, n_pages, dt,
-        _addr(flags), stream.cuda_stream)
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+        kv_lens.data_ptr(), _addr(cu_seqlens), n_seqs, B, T, HKV, d, ks, vs, page_size, max_pages,
+        n_pages, dt, _addr(flags), raw)
     if status != GDN_OK:
         raise GdnError(status, "gdn_kv_cache_append")
 
