@@ -15,10 +15,11 @@
 // whole row per thread and half the warps, two warps to a scheduler did not
 // cover one another's latencies: 2045 clocks for both tiles where this takes
 // 1470, and the products of both take 2048).  Warp 16: TMA loads into a ring of
-// key and value tiles.  Warp 17: the products.  Warp 18: the plan, units
-// published through a small ring.  The loader and the product warp go through
-// the same sequence of tiles across units, so the ring stays full and the first
-// scores of a unit are computed while the softmax warps write out the last one.
+// key and value tiles.  Warps 17 and 19: the products of X = 0 and 1.  Warp 18:
+// the plan, units published through a small ring.  The loader and the product
+// warps go through the same sequence of tiles across units, so the ring stays
+// full and the first scores of a unit are computed while the softmax warps write
+// out the last one.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -49,8 +50,9 @@ struct Smem {
   static constexpr int kUnit = kRow + 2 * 2 * 128 * 4;
   static constexpr int kBars = kUnit + kUnits * (int)sizeof(AttnUnit);
   // barriers, in order: Q full, Q empty, S full x2, P ready x2, O full x2,
-  // swap x2, halves x8, unit full x4, unit empty x4, tile full, tile empty
-  static constexpr int kBarCount = 18 + 2 * kUnits + 2 * kStages;
+  // swap x2, halves x8, turn x2, unit full x4, unit empty x4, tile full, tile
+  // empty
+  static constexpr int kBarCount = 20 + 2 * kUnits + 2 * kStages;
   static constexpr int kSlot = kBars + kBarCount * 8;
   static constexpr int kUsed = kSlot + 8;  // [X] int2: stages that the scores free
   static constexpr int kBytes = kUsed + 16;
@@ -172,10 +174,11 @@ struct Bars {
   __device__ uint32_t o_full(int x) const { return at(6 + x); }
   __device__ uint32_t swap(int i) const { return at(8 + i); }
   __device__ uint32_t halves(int i) const { return at(10 + i); }
-  __device__ uint32_t unit_full(int i) const { return at(18 + i); }
-  __device__ uint32_t unit_empty(int i) const { return at(18 + kUnits + i); }
-  __device__ uint32_t kv_full(int i) const { return at(18 + 2 * kUnits + i); }
-  __device__ uint32_t kv_empty(int i) const { return at(18 + 2 * kUnits + stages + i); }
+  __device__ uint32_t turn(int x) const { return at(18 + x); }
+  __device__ uint32_t unit_full(int i) const { return at(20 + i); }
+  __device__ uint32_t unit_empty(int i) const { return at(20 + kUnits + i); }
+  __device__ uint32_t kv_full(int i) const { return at(20 + 2 * kUnits + i); }
+  __device__ uint32_t kv_empty(int i) const { return at(20 + 2 * kUnits + stages + i); }
 };
 
 // Position in a ring of N: index and how often it has gone round.
@@ -190,6 +193,10 @@ struct Ring {
     }
   }
 };
+
+// The same value in all lanes, known to be so by the compiler: what follows from
+// it stays in uniform registers.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
 // A reader of the unit ring.
 struct Units {
@@ -285,21 +292,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     *abort = 0;
     mbar_init(bars.q_full(), 1);
-    mbar_init(bars.q_empty(), 1);
+    mbar_init(bars.q_empty(), 2);
     for (int x = 0; x < 2; x++) {
       mbar_init(bars.s_full(x), 2);  // the products' commit, and the stages they free
       mbar_init(bars.p_ready(x), 8);
       mbar_init(bars.o_full(x), 1);
       mbar_init(bars.swap(x), 16);
+      mbar_init(bars.turn(x), 1);
     }
     for (int i = 0; i < 8; i++) mbar_init(bars.halves(i), 2);
     for (int i = 0; i < kUnits; i++) {
       mbar_init(bars.unit_full(i), 1);
-      mbar_init(bars.unit_empty(i), 18);  // loader, products, sixteen softmax warps
+      mbar_init(bars.unit_empty(i), 19);  // loader, products x2, sixteen softmax warps
     }
     for (int i = 0; i < SM::kStages; i++) {
       mbar_init(bars.kv_full(i), 1);
-      mbar_init(bars.kv_empty(i), 1);
+      mbar_init(bars.kv_empty(i), 2);  // one from each X, or two from the one that reads it
     }
     mbar_fence_init();
   }
@@ -363,11 +371,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_phase ^= 1;
         fence_after_sync();
         if (half == 0 && quarter == 0 && lane == 0) {
-          // These scores, and everything issued before them, are done: hand
-          // back the stages that they were the last to read.
+          // These scores, and what this X was given before them, are done: hand
+          // back their key tile and the value tile before.
           const int2 stage = used[x];
-          if (stage.x >= 0) mbar_arrive(bars.kv_empty(stage.x));
+          mbar_arrive(bars.kv_empty(stage.x));
           if (stage.y >= 0) mbar_arrive(bars.kv_empty(stage.y));
+          if (narrow) {
+            mbar_arrive(bars.kv_empty(stage.x));
+            if (stage.y >= 0) mbar_arrive(bars.kv_empty(stage.y));
+          }
         }
         if (idle) {
           if (lane == 0) mbar_arrive(bars.p_ready(x));
@@ -671,37 +683,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (left[1] < left[0]) last_values(1);
       last_values(0);
       last_values(1);
-    } else if (warp == 17) {
+    } else {
       // ---------------------------------------------------------- products
-      // Each X goes through S(0), O(0), S(1), O(1), ...: scores overwrite
-      // weights, so S(i + 1) is issued behind O(i), and the tensor core runs
-      // what it is given in order.  The two X alternate; the last O of a unit
-      // is issued among the first S of the next.
+      // A warp for each X: S(0), O(0), S(1), O(1), ...; scores overwrite weights,
+      // so S(i + 1) is issued behind O(i), and the tensor core runs what it is
+      // given in order.  Issuing blocks while the tensor core's queue is full,
+      // which is short: one warp for both X left it idle for 270 clocks around
+      // each product while it waited and prepared the next.  In a wide unit the
+      // warps take turns, each ready to issue when its turn comes: without turns
+      // the two X's products mix and their softmaxes fall together (a
+      // 32768-token prompt 4.13 ms, with one warp 3.10 ms).
+      const int x = warp == 17 ? 0 : 1;
       constexpr uint32_t kIdS = idesc_bf16(128, 128, 0, 0), kIdO = idesc_bf16(128, D, 0, 1);
       Units units{unit_ring, bars, abort, {}};
       Ring<SM::kStages> ring;
-      uint32_t q_phase = 0, p_phase[2] = {0, 0};
+      uint32_t q_phase = 0, p_phase = 0, turn = 0;
       AttnUnit u;
-      int left[2] = {-1, -1};  // last tiles of the unit before, their values still to be used
-      int old_len = 0, shared_v = 0;
-      bool shared = false, more[2] = {false, false};  // more: O has been written before
-      // A stage goes back to the loader once scores issued after its last use
-      // are there: the softmax, which waits for them anyway, arrives for it.  A
-      // commit for each stage costs the tensor pipe 40 to 120 clocks (it does
-      // not start the next product before the committed ones are through).
-      auto next_tile = [&] {
-        const int stage = ring.i;
-        wait(bars.kv_full(stage), ring.round, abort);
-        ring.step();
-        return stage;
+      // last tiles of the unit before, their values still to be used; `shared`:
+      // one tile for both X
+      int left0 = -1, left1 = -1, old_len = 0;
+      bool shared = false, more = false;  // more: O has been written before
+      struct Tile {
+        int stage;
+        uint32_t round;
       };
-      auto next_values = [&](int tile, int len) {
-        const int stage = next_tile();
+      auto next_tile = [&] {
+        const Tile t{ring.i, ring.round};
+        ring.step();
+        return t;
+      };
+      auto loaded = [&](const Tile &t) { wait(bars.kv_full(t.stage), t.round, abort); };
+      auto values_loaded = [&](const Tile &t, int tile, int len) {
+        loaded(t);
         // weights past the last key are zero, but 0 * NaN is not: clear the
-        // value rows that belong to nobody
+        // value rows that belong to nobody (both X do, where they share a tile)
         const int rows = len - tile * 128;
         if (rows < 128) {
-          unsigned char *tile_at = sm + SM::kRing + stage * SM::kTileBytes;
+          unsigned char *tile_at = sm + SM::kRing + t.stage * SM::kTileBytes;
           for (int i = max(rows, 0) * 8 + lane; i < 128 * 8; i += 32) {
             const int row = i >> 3;
 #pragma unroll
@@ -712,16 +730,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async();
           __syncwarp();
         }
-        return stage;
       };
-      auto weights_ready = [&](int x) {
-        wait(bars.p_ready(x), p_phase[x], abort);
-        p_phase[x] ^= 1;
-        fence_after_sync();
-      };
-      auto scores = [&](int x, int stage, int q_tile, int free_k, int free_v) {
+      // S from key tile k; the softmax hands back k and value tile free_v (a
+      // stage, or -1) when it sees the scores.  (A commit for each stage would
+      // cost the tensor pipe 40 to 120 clocks: it does not start the next product
+      // before the committed ones are through.)
+      auto scores = [&](const Tile &k, int q_tile, int free_v) {
         const uint32_t q_lo = desc_lo(sQ + q_tile * SM::kTileBytes, 16);
-        const uint32_t k_lo = desc_lo(sRing + stage * SM::kTileBytes, 16);
+        const uint32_t k_lo = desc_lo(sRing + k.stage * SM::kTileBytes, 16);
         fence_after_sync();
         issue_scores<true>(tS + x * 128, q_lo, k_lo, desc_hi(kGroup), kIdS, lane == 0);
         if (D == 128)
@@ -729,85 +745,116 @@ __global__ void __launch_bounds__(kThreads, 1)
                               kIdS, lane == 0);
         if (lane == 0) {
           mma_commit(bars.s_full(x));
-          used[x] = make_int2(free_k, free_v);
+          used[x] = make_int2(k.stage, free_v);
           mbar_arrive(bars.s_full(x));
         }
       };
-      auto output = [&](int x, int stage, bool accumulate) {
+      auto weights_ready = [&] {
+        wait(bars.p_ready(x), p_phase, abort);
+        p_phase ^= 1;
+        fence_after_sync();
+      };
+      auto output = [&](int stage, bool accumulate) {
         const uint32_t v_lo = desc_lo(sRing + stage * SM::kTileBytes, kPanelAt);
         issue_output<2 * kGroup>(tO + x * D, tS + x * 128, v_lo, desc_hi(kGroup), kIdO, accumulate,
                                  lane == 0);
         issue_output<2 * kGroup>(tO + x * D, tS + x * 128 + 32, v_lo + (8 * kGroup >> 4), desc_hi(kGroup),
                                  kIdO, true, lane == 0);
       };
-      auto last_output = [&](int x) {
-        if (left[x] < 0) return;
-        const bool own = !(shared && x == 1);
-        const int stage = own ? next_values(left[x], old_len) : shared_v;
-        if (own) shared_v = stage;
-        weights_ready(x);
-        output(x, stage, more[x]);
+      auto last_output = [&](const Tile &v, int tile) {
+        values_loaded(v, tile, old_len);
+        weights_ready();
+        output(v.stage, more);
         if (lane == 0) {
-          if (!shared || x == 1) mma_commit(bars.kv_empty(stage));
+          mma_commit(bars.kv_empty(v.stage));  // each stage waits for two arrivals
+          if (!shared) mma_commit(bars.kv_empty(v.stage));
           mma_commit(bars.o_full(x));
         }
         __syncwarp();
-        left[x] = -1;
+      };
+      // the last values up to those of X = 0, in the loader's order
+      auto last_values = [&] {
+        if (left1 >= 0 && left1 < left0) {
+          const Tile v = next_tile();
+          if (x == 1) last_output(v, left1);
+          left1 = -1;
+        }
+        if (left0 >= 0) {
+          const Tile v = next_tile();
+          if (x == 0 || shared) last_output(v, left0);
+          if (shared) left1 = -1;
+          left0 = -1;
+        }
+      };
+      auto last_values_1 = [&] {
+        if (left1 < 0) return;
+        const Tile v = next_tile();
+        if (x == 1) last_output(v, left1);
+        left1 = -1;
       };
       while (units.next(u)) {
-        const bool narrow = u.n_tok * u.gp <= 128;
-        if (left[1] < left[0]) last_output(1);
-        last_output(0);
+        const int t0 = uniform(u.t0), t1 = uniform(u.t1), len = uniform(u.len);
+        const bool narrow = uniform(u.n_tok * u.gp) <= 128;
+        last_values();
+        const Tile k = next_tile();
         wait(bars.q_full(), q_phase, abort);
         q_phase ^= 1;
-        const int k = next_tile();
-        scores(0, k, 0, narrow ? k : -1, -1);
-        last_output(1);
+        if (x == 0) {
+          loaded(k);
+          scores(k, 0, -1);
+        }
+        last_values_1();
         if (narrow) {
-          more[0] = u.t0 + 2 < u.t1;
-          more[1] = u.t0 + 3 < u.t1;
-          if (u.t0 + 1 < u.t1) {
-            const int k1 = next_tile();
-            scores(1, k1, 0, k1, -1);
-          }
-          for (int t0 = u.t0 + 2; t0 < u.t1; t0 += 2) {
-#pragma unroll
-            for (int x = 0; x < 2; x++) {
-              const int t = t0 + x;
-              if (t >= u.t1) break;
-              const int v = next_values(t - 2, u.len);
-              weights_ready(x);
-              output(x, v, t >= u.t0 + 4);
-              const int k_next = next_tile();
-              scores(x, k_next, 0, k_next, v);
+          if (t0 + 1 < t1) {
+            const Tile k1 = next_tile();
+            if (x == 1) {
+              loaded(k1);
+              scores(k1, 0, -1);
             }
           }
-          const int odd = (u.t1 - 1 - u.t0) & 1;  // which X has the last tile
-          left[0] = u.t1 - 1 - odd;
-          left[1] = u.t0 + 1 < u.t1 ? u.t1 - 2 + odd : -1;
-        } else {
-          scores(1, k, 1, k, -1);
-          for (int t = u.t0; t + 1 < u.t1; t++) {
-            const int v = next_values(t, u.len);
-            weights_ready(0);
-            output(0, v, t > u.t0);
-            const int k_next = next_tile();
-            scores(0, k_next, 0, -1, -1);
-            weights_ready(1);
-            output(1, v, t > u.t0);
-            scores(1, k_next, 1, k_next, v);
+          for (int t = t0 + 2; t < t1; t++) {
+            const Tile v = next_tile(), k_next = next_tile();
+            if (((t - t0) & 1) != x) continue;
+            values_loaded(v, t - 2, len);
+            weights_ready();
+            output(v.stage, t >= t0 + 4);
+            loaded(k_next);
+            scores(k_next, 0, v.stage);
           }
-          more[0] = more[1] = u.t0 + 1 < u.t1;
-          left[0] = left[1] = u.t1 - 1;
+          const int odd = (t1 - 1 - t0) & 1;  // which X has the last tile
+          left0 = t1 - 1 - odd;
+          left1 = t0 + 1 < t1 ? t1 - 2 + odd : -1;
+          more = t0 + 2 + x < t1;
+        } else {
+          if (x == 1) {
+            loaded(k);
+            scores(k, 1, -1);
+          }
+          for (int t = t0; t + 1 < t1; t++) {
+            const Tile v = next_tile(), k_next = next_tile();
+            values_loaded(v, t, len);
+            loaded(k_next);
+            weights_ready();
+            wait(bars.turn(x), turn ^ (x == 0 ? 1 : 0), abort);
+            turn ^= 1;
+            output(v.stage, t > t0);
+            scores(k_next, x, v.stage);
+            if (lane == 0) mbar_arrive(bars.turn(x ^ 1));
+          }
+          left0 = left1 = t1 - 1;
+          more = t0 + 1 < t1;
         }
-        if (lane == 0) mma_commit(bars.q_empty());  // behind the last scores: the queries may be replaced
+        // behind the last scores: the queries may be replaced
+        if (lane == 0) {
+          if (x == 0 || !narrow || t0 + 1 < t1) mma_commit(bars.q_empty());
+          else mbar_arrive(bars.q_empty());
+        }
         __syncwarp();
         shared = !narrow;
-        old_len = u.len;
+        old_len = len;
       }
-      if (left[1] < left[0]) last_output(1);
-      last_output(0);
-      last_output(1);
+      last_values();
+      last_values_1();
     }
   }
   fence_before_sync();

@@ -1,7 +1,8 @@
-"""A CPU model of the bf16 attention kernel's protocol (csrc/gdn_attn_tc.cu): the loader, the
-product warp and the two softmax groups as processes over the same ring of tiles, barriers and
-in-order tensor pipe.  Random sequences of units must run to their end, every product must read
-the tile that it is meant to read, and no stage may be handed back twice."""
+"""A CPU model of the bf16 attention kernel's protocol (csrc/gdn_attn_tc.cu): the loader, the two
+product warps and the two softmax groups as processes over the same ring of tiles and barriers.
+Random sequences of units must run to their end, every product must read the tile that it is
+meant to read, and each stage must be handed back twice (once by each X, or twice by the one X
+that reads it) before it is filled again."""
 from __future__ import annotations
 
 import random
@@ -10,31 +11,30 @@ import pytest
 
 
 class Model:
-    """Units are (wide, tiles).  ``keys_first``: a unit's last tiles in the order of the keys.
-    ``late``: stages are handed back by the product warp on the softmax's answer, not by the
-    softmax when it sees the scores."""
+    """Units are (wide, tiles).  ``arrivals``: how often a stage is handed back before the loader
+    fills it again (2 in the kernel)."""
 
-    def __init__(self, units, stages, keys_first=True, late=False, delay=0):
-        self.units, self.stages, self.keys_first, self.late, self.delay = units, stages, keys_first, late, delay
-        self.full = {}        # load number -> tile
-        self.free = {}        # load number -> handed back
-        self.loads = 0        # load numbers issued
-        self.q_free = [True] + [False] * len(units)
+    def __init__(self, units, stages, delay=0, arrivals=2):
+        self.units, self.stages, self.delay, self.arrivals = units, stages, delay, arrivals
+        self.full = {}           # load number -> tile
+        self.free = {}           # load number -> arrivals
+        self.loads = 0           # load numbers issued
+        self.q_free = [2] + [0] * len(units)
         self.q_full = [False] * len(units)
-        self.scores = ([], [])   # per X: (unit, tile, stages freed) whose scores are done
+        self.scores = ([], [])   # per X: (unit, tile, loads freed) whose scores are done
         self.ready = [0, 0]      # weights ready, counted
-        self.outs = ([], [])     # per X: (unit, last) outputs done
+        self.outs = (set(), set())  # per X: units whose last output is done
+        self.steps = 0
 
-    def last_order(self, left):
-        order = [0, 1]
-        if self.keys_first and left[1] is not None and (left[0] is None or left[1] < left[0]):
-            order = [1, 0]
-        return [x for x in order if left[x] is not None]
+    def hand_back(self, n, times):
+        self.free[n] = self.free.get(n, 0) + times
+        assert self.free[n] <= 2, n
+        self.steps += 1
 
     # -- the loader
     def load(self, tile):
         n = self.loads
-        while n >= self.stages and not self.free.get(n - self.stages):
+        while n >= self.stages and self.free.get(n - self.stages, 0) < self.arrivals:
             yield
         self.full[n] = tile
         self.loads += 1
@@ -43,24 +43,20 @@ class Model:
         left, shared, old = [None, None], False, None
         for i, (wide, n) in enumerate(self.units + [(None, 0)]):
             def values(x):
-                if not (shared and x == 1):
+                if left[x] is not None and not (shared and x == 1):
                     yield from self.load((old, "v", left[x]))
                 left[x] = None
-            order = self.last_order(left)
-            if order and order[0] == 1:
+            if left[1] is not None and left[1] < left[0]:
                 yield from values(1)
-            if left[0] is not None:
-                yield from values(0)
+            yield from values(0)
             if wide is None:
-                if left[1] is not None:
-                    yield from values(1)
+                yield from values(1)
                 return
-            while not self.q_free[i]:
+            while self.q_free[i] < 2:
                 yield
             self.q_full[i] = True
             yield from self.load((i, "k", 0))
-            if left[1] is not None:
-                yield from values(1)
+            yield from values(1)
             if wide:
                 for t in range(n - 1):
                     yield from self.load((i, "v", t))
@@ -76,122 +72,126 @@ class Model:
                 left = [n - 1 - odd, n - 2 + odd if n > 1 else None]
             shared, old = wide, i
 
-    # -- the products
-    def next_tile(self, want):
-        n = self.used
-        while n not in self.full:
-            yield
-        assert self.full[n] == want, (n, self.full[n], want)
-        self.used += 1
-        return n
+    # -- the products of one X
+    def products(self, x):
+        ring = 0
+        left, shared, old = [None, None], False, None
+        answers = 0
 
-    def products(self):
-        self.used = 0
-        left, shared, old, shared_v = [None, None], False, None, None
-        held, answers = ([], []), [0, 0]
-
-        def scores(x, unit, tile, freed):
-            self.scores[x].append((unit, tile, freed))
-            held[x].extend(freed)
-
-        def weights(x):
-            answers[x] += 1
-            while self.ready[x] < answers[x]:
+        def tile(n, want):
+            while n not in self.full:
                 yield
-            if self.late:
-                for n in held[x]:
-                    self.free[n] = True
-                held[x].clear()
+            assert self.full[n] == want, (n, self.full[n], want)
 
-        def last_output(x):
-            nonlocal shared_v
-            if not (shared and x == 1):
-                shared_v = yield from self.next_tile((old, "v", left[x]))
-            yield from weights(x)
-            self.outs[x].append((old, True))
-            if not shared or x == 1:
-                self.free[shared_v] = True
-            left[x] = None
+        def output():
+            nonlocal answers
+            answers += 1
+            while self.ready[x] < answers:
+                yield
+
+        def last_output(n, t):
+            yield from tile(n, (old, "v", t))
+            yield from output()
+            self.hand_back(n, 1 if shared else 2)
+            self.outs[x].add(old)
 
         for i, (wide, n) in enumerate(self.units + [(None, 0)]):
-            order = self.last_order(left)
-            if order and order[0] == 1:
-                yield from last_output(1)
+            if left[1] is not None and not shared and left[1] < left[0]:
+                ring += 1
+                if x == 1:
+                    yield from last_output(ring - 1, left[1])
+                left[1] = None
             if left[0] is not None:
-                yield from last_output(0)
-            if wide is None:
-                if left[1] is not None:
-                    yield from last_output(1)
-                return
-            while not self.q_full[i]:
-                yield
-            k = yield from self.next_tile((i, "k", 0))
-            scores(0, i, 0, [] if wide else [k])
+                ring += 1
+                if x == 0 or shared:
+                    yield from last_output(ring - 1, left[0])
+                if shared:
+                    left[1] = None
+                left[0] = None
+            if wide is not None:
+                k, ring = ring, ring + 1
+                while not self.q_full[i]:
+                    yield
+                if x == 0:
+                    yield from tile(k, (i, "k", 0))
+                    self.scores[0].append((i, 0, [k], wide))
             if left[1] is not None:
-                yield from last_output(1)
+                ring += 1
+                if x == 1:
+                    yield from last_output(ring - 1, left[1])
+                left[1] = None
+            if wide is None:
+                return
             if wide:
-                scores(1, i, 0, [k])
+                if x == 1:
+                    yield from tile(k, (i, "k", 0))
+                    self.scores[1].append((i, 0, [k], wide))
                 for t in range(n - 1):
-                    v = yield from self.next_tile((i, "v", t))
-                    yield from weights(0)
-                    k_next = yield from self.next_tile((i, "k", t + 1))
-                    scores(0, i, t + 1, [])
-                    yield from weights(1)
-                    scores(1, i, t + 1, [k_next, v])
+                    v, k, ring = ring, ring + 1, ring + 2
+                    yield from tile(v, (i, "v", t))
+                    yield from output()
+                    yield from tile(k, (i, "k", t + 1))
+                    self.scores[x].append((i, t + 1, [k, v], wide))
                 left = [n - 1, n - 1]
             else:
                 if n > 1:
-                    k = yield from self.next_tile((i, "k", 1))
-                    scores(1, i, 1, [k])
+                    k, ring = ring, ring + 1
+                    if x == 1:
+                        yield from tile(k, (i, "k", 1))
+                        self.scores[1].append((i, 1, [k], wide))
                 for t in range(2, n):
-                    x = t & 1
-                    v = yield from self.next_tile((i, "v", t - 2))
-                    yield from weights(x)
-                    k = yield from self.next_tile((i, "k", t))
-                    scores(x, i, t, [k, v])
+                    v, k, ring = ring, ring + 1, ring + 2
+                    if t & 1 != x:
+                        continue
+                    yield from tile(v, (i, "v", t - 2))
+                    yield from output()
+                    yield from tile(k, (i, "k", t))
+                    self.scores[x].append((i, t, [k, v], wide))
                 odd = (n - 1) & 1
                 left = [n - 1 - odd, n - 2 + odd if n > 1 else None]
-            self.q_free[i + 1] = True
+            self.q_free[i + 1] += 1
             shared, old = wide, i
 
     # -- the softmax of one X
     def softmax(self, x):
         seen = 0
+        met = self.met
         for i, (wide, n) in enumerate(self.units):
             tiles = range(n) if wide else range(x, n, 2)
             for t in tiles:
                 while len(self.scores[x]) <= seen:
                     yield
                 assert self.scores[x][seen][:2] == (i, t)
-                if not self.late:
-                    for n_load in self.scores[x][seen][2]:
-                        assert not self.free.get(n_load)
-                        self.free[n_load] = True
+                for n_load in self.scores[x][seen][2]:
+                    self.hand_back(n_load, 1 if wide else 2)
                 for _ in range(random.randint(0, self.delay)):
                     yield
                 seen += 1
                 self.ready[x] += 1
-            both = not wide and n > 1
-            for y in ((0, 1) if both else (x,)):
-                while tiles and (i, True) not in self.outs[y]:
+            while tiles and i not in self.outs[x]:
+                yield
+            if not wide and n > 1:  # both X meet to join their outputs
+                met[x] += 1
+                while met[x ^ 1] < met[x]:
                     yield
 
     def run(self):
-        procs = [self.loader(), self.products(), self.softmax(0), self.softmax(1)]
-        idle = 0
+        self.met = [0, 0]
+        procs = [self.loader(), self.products(0), self.products(1), self.softmax(0), self.softmax(1)]
+        idle, before = 0, None
         while procs:
-            before = (self.loads, getattr(self, "used", 0), len(self.scores[0]), len(self.scores[1]),
-                      tuple(self.ready), len(self.outs[0]), len(self.outs[1]), len(self.free), len(procs))
             for p in list(procs):
                 try:
                     next(p)
                 except StopIteration:
                     procs.remove(p)
-            after = (self.loads, getattr(self, "used", 0), len(self.scores[0]), len(self.scores[1]),
-                     tuple(self.ready), len(self.outs[0]), len(self.outs[1]), len(self.free), len(procs))
+            after = (self.loads, len(self.scores[0]), len(self.scores[1]), tuple(self.ready),
+                     len(self.outs[0]), len(self.outs[1]), self.steps, tuple(self.met), len(procs))
             idle = idle + 1 if before == after else 0
+            before = after
             if idle > 10 + 4 * self.delay:
                 return False
+        assert all(v == 2 for v in self.free.values())
         return True
 
 
@@ -209,10 +209,9 @@ def test_every_sequence_of_units_ends(stages):
 
 
 def test_model_finds_a_deadlock():
-    """Handing stages back on the softmax's answer, with a unit's last tiles in the order of the
-    X, an odd number of tiles leaves the ring waiting for a stage that is handed back only after
-    the tile that waits for it."""
+    """Too few stages for what the two X hold at once, and a stage that waits for an arrival that
+    nobody makes."""
     units = [(False, 3), (False, 3)]
-    assert not Model(units, 5, keys_first=False, late=True).run()
-    assert Model(units, 5, keys_first=True, late=True).run()
+    assert not Model(units, 1).run()
+    assert not Model(units, 5, arrivals=3).run()
     assert Model(units, 5).run()
