@@ -352,21 +352,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     AttnUnit u;
     while (units.next(u)) {
-      const bool narrow = u.n_tok * u.gp <= 128;
-      const bool both = narrow && u.t1 - u.t0 > 1;
+      const int t0 = uniform(u.t0), t1 = uniform(u.t1), rows = uniform(u.n_tok * u.gp);
+      const bool narrow = rows <= 128;
+      const bool both = narrow && t1 - t0 > 1;
       const int stride = narrow ? 2 : 1;
       const int row = narrow ? r : x * 128 + r;
       const int tok = row / u.gp;
       const int limit = u.pos0 + min(tok, u.n_tok - 1) - half * 64;  // last visible key, this half's columns
       const int all_see = __reduce_min_sync(0xffffffffu, limit);
       float m = -CUDART_INF_F, l = 0.f;
-      const int first = narrow ? u.t0 + x : u.t0;
-      const bool mine = first < u.t1;
+      const int first = narrow ? t0 + x : t0;
+      const bool mine = first < t1;
       // rows past the unit's last one (most of a decode step's tile): their
       // weights are whatever the scores leave, and nobody reads their output
-      const bool idle = narrow && quarter * 32 >= u.n_tok * u.gp;
+      const bool idle = narrow && quarter * 32 >= rows;
 #pragma unroll 1
-      for (int t = first; t < u.t1; t += stride) {
+      for (int t = first; t < t1; t += stride) {
         wait(bars.s_full(x), s_phase, abort);
         s_phase ^= 1;
         fence_after_sync();
@@ -385,39 +386,70 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(bars.p_ready(x));
           continue;
         }
-        uint32_t raw[2][32];
-        tmem_ld32_nowait(s_at, raw[0]);
-        tmem_ld32_nowait(s_at + 32, raw[1]);
-        tmem_wait_ld();
-        float s[64];
+        // The weights are e^(s - m) for a maximum m that is moved only when the
+        // scores have outgrown it by 2^8: they then stay below 2^8, the sums in
+        // fp32 far from overflow, and the output in tensor memory is rarely
+        // touched.  So after a unit's first tile the weights are made from the m
+        // at hand, while the halves of the rows exchange their maxima, and made
+        // again in the rare case that m moves.
+        float s[64], tile_max;
+        auto load_scores = [&] {
+          uint32_t raw[2][32];
+          tmem_ld32_nowait(s_at, raw[0]);
+          tmem_ld32_nowait(s_at + 32, raw[1]);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 64; c++) s[c] = __uint_as_float(raw[c >> 5][c & 31]);
-        if (__builtin_expect(t * 128 + 63 > all_see, 0)) {
-          const int lim = limit - t * 128;
+          for (int c = 0; c < 64; c++) s[c] = __uint_as_float(raw[c >> 5][c & 31]);
+          if (__builtin_expect(t * 128 + 63 > all_see, 0)) {
+            const int lim = limit - t * 128;
 #pragma unroll
-          for (int c = 0; c < 64; c++)
-            if (c > lim) s[c] = -CUDART_INF_F;
-        }
-        float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+            for (int c = 0; c < 64; c++)
+              if (c > lim) s[c] = -CUDART_INF_F;
+          }
+          float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-        for (int c = 0; c < 64; c += 8)
+          for (int c = 0; c < 64; c += 8)
 #pragma unroll
-          for (int i = 0; i < 4; i++) top[i] = max3(top[i], s[c + 2 * i], s[c + 2 * i + 1]);
-        float tile_max = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-        *own_ex = tile_max;
-        // past this, both halves of the scores are in registers: the weights
-        // may be written over them
-        fence_before_sync();
-        meet_half();
-        fence_after_sync();
-        tile_max = fmaxf(tile_max, *other_ex);
-        // The maximum is moved only when it has grown by a factor of 2^8: the
-        // weights then stay below 2^8, the sums in fp32 far from overflow, and
-        // the output in tensor memory is rarely touched.
-        const bool move = tile_max > m + grow;
+            for (int i = 0; i < 4; i++) top[i] = max3(top[i], s[c + 2 * i], s[c + 2 * i + 1]);
+          tile_max = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+          *own_ex = tile_max;
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(halves);
+        };
+        auto other_half = [&] {
+          // Both halves of the scores have been read: past this the weights may
+          // be written over them.
+          wait(halves, half_phase, abort);
+          half_phase ^= 1;
+          fence_after_sync();
+          tile_max = fmaxf(tile_max, *other_ex);
+        };
         if (t == first) {
+          load_scores();
+          other_half();
           m = tile_max;
-        } else if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
+          meet_half();  // read, before it is written again
+        }
+        uint32_t packed[32];
+        uint64_t sum[2];
+        while (true) {
+          load_scores();
+          const float off = m == -CUDART_INF_F ? 0.f : m * sl2;  // nothing visible yet: weights 0
+          const uint64_t scale2 = pair(sl2, sl2), off2 = pair(-off, -off);
+          sum[0] = sum[1] = 0;
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            float p0, p1;
+            unpair(fma2(pair(s[c], s[c + 1]), scale2, off2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair(p0, p1));
+            packed[c >> 1] = pack2(p0, p1);
+          }
+          other_half();
+          const bool move = tile_max > m + grow;
+          if (__builtin_expect(!__any_sync(0xffffffffu, move), 1)) break;
           const float f = move ? ex2((m - tile_max) * sl2) : 1.f;
           if (move) m = tile_max;
           l *= f;
@@ -430,24 +462,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
             tmem_st16_nowait(o_at + c, o);
           }
+          meet_half();
         }
-        const float off = m == -CUDART_INF_F ? 0.f : m * sl2;  // nothing visible yet: weights 0
-        const uint64_t scale2 = pair(sl2, sl2), off2 = pair(-off, -off);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int h = 0; h < 64; h += 32) {
-          uint32_t packed[16];
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            float p0, p1;
-            unpair(fma2(pair(s[h + c], s[h + c + 1]), scale2, off2), p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair(p0, p1));
-            packed[c >> 1] = pack2(p0, p1);
-          }
-          tmem_st16_nowait(p_at + (h >> 1), packed);
-        }
+        tmem_st32_nowait(p_at, packed);
         float l0, l1;
         unpair(add2(sum[0], sum[1]), l0, l1);
         l += l0 + l1;
