@@ -16,49 +16,53 @@
 namespace gdn {
 namespace {
 
-// fp32: 64 rows x 64 keys per step: four warps of 16 rows, the operands in shared
-// memory as fp32, both products split-tf32 on mma.sync.
+// fp32: a unit of 64 rows, 64 keys per step, four warps of 16 rows, both
+// products in fp32 multiply-adds.  Products of split operands on the tensor
+// cores (three tf32 ones each, on mma.sync) took as long: 159 us, this 158 (2 x
+// 1023 tokens, 16 heads of 64); 926 and 914 us at 8192 tokens of 4 heads, where
+// their error was 4.7e-6 against 2.5e-6, since those accumulations are cut off
+// and not rounded.
+//
+// S = Q K^T: a thread has 8 rows and 4 keys; queries and keys lie transposed in
+// shared memory, so that each step of the contraction is three 16-byte reads
+// for 32 multiply-adds.  The 16 threads of a row are half a warp.  O = P V: the
+// weights go through shared memory (over the keys), and a thread has 8 rows and
+// D / 16 columns.  Those reads bound it: 12 wavefronts of shared memory for 32
+// clocks of multiply-adds in each of four schedulers, 27 to 38 TFLOP/s of 74.
 using WarpShape = AttnShape<64, 64, 64, 1, 1>;
 using TcShape = AttnShape<256, 128, 128, 2, 4>;  // of the bf16 kernel (gdn_attn_tc.cu)
 constexpr int kThreads = 128;
+constexpr int kPRow = 20;  // floats from one key's 16 weights to the next: 8 lanes hit 32 banks
 
 template <int D>
-constexpr int smem_bytes() { return 3 * 64 * (D + 4) * 4; }
+struct WarpSmem {
+  static constexpr int kQ = 0, kK = 64 * D;                          // [D][64] each
+  static constexpr int kP = 4 * 64 * kPRow;                          // [warp][64 keys][kPRow]
+  static constexpr int kV = kK + (64 * D > kP ? 64 * D : kP);        // [64][D]
+  static constexpr int kBytes = (kV + 64 * D) * 4;
+};
+template <int D>
+constexpr int blocks_per_sm() { return D == 64 ? 3 : 2; }
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-// c += A B for one 16 x 8 tile, k = 8: the three products of the two halves
-__device__ __forceinline__ void mma3(float (&c)[4], const uint32_t (&ah)[4],
-                                     const uint32_t (&al)[4], float b0, float b1) {
-  uint32_t h0, l0, h1, l1;
-  split_tf32(b0, h0, l0);
-  split_tf32(b1, h1, l1);
-  mma1688_tf32(c, al, h0, h1);
-  mma1688_tf32(c, ah, l0, l1);
-  mma1688_tf32(c, ah, h0, h1);
-}
-
-__device__ __forceinline__ void load8(float (&x)[8], const float *p) {
-  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4 *>(p + 4));
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void put8(float *d, const float (&x)[8]) {
-  *reinterpret_cast<float4 *>(d) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4 *>(d + 4) = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void get4(float *x, const float *p) {
+  const float4 v = *reinterpret_cast<const float4 *>(p);
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs a) {
-  constexpr int kS = D + 4;  // row stride in floats: fragment reads hit 32 banks
-  extern __shared__ float smem[];
-  float *Qs = smem, *Ks = Qs + 64 * kS, *Vs = Ks + 64 * kS;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_kernel(const AttnArgs a) {
+  using SM = WarpSmem<D>;
+  constexpr int kCols = D / 16;  // columns of a thread: 4 from 4 cg on, and for D = 128 4 from 64 + 4 cg on
+  extern __shared__ __align__(16) float smem[];
+  float *Qt = smem + SM::kQ, *Kt = smem + SM::kK, *Vs = smem + SM::kV;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rg = lane >> 4, cg = lane & 15;  // rows warp * 16 + rg * 8 .. + 7; keys (columns) 4 cg .. + 3
+  float *P = smem + SM::kK + warp * 64 * kPRow + rg * 8;
   AttnPlan<WarpShape> plan(a.H, a.HKV, a.plan_coarse);
   AttnStaged *staged = reinterpret_cast<AttnStaged *>(smem);  // until the first operands
   attn_stage(a, staged, blockIdx.x);
@@ -70,132 +74,150 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_warp_kernel(const AttnArgs 
   while (walk.next(u)) {
     if (tid == 0 && u.slot == 2 * (int)blockIdx.x + 1) a.jobs[blockIdx.x] = attn_job(u);
     __syncthreads();  // the previous unit's operands (or the plan's) are read
-    for (int i = tid; i < 64 * (D / 8); i += kThreads) {
-      const int r = i / (D / 8), c = (i % (D / 8)) * 8, t = r / u.gp;
-      float x[8] = {};
-      if (t < u.n_tok)
-        load8(x, static_cast<const float *>(a.q) + (long long)(u.row0 + t) * a.q_stride +
-                           (u.head0 + r % u.gp) * D + c);
-      put8(Qs + r * kS + c, x);
+    {
+      const int r = tid & 63, t = r / u.gp;
+      const float *q = static_cast<const float *>(a.q) + (long long)(u.row0 + t) * a.q_stride +
+                       (u.head0 + r % u.gp) * D;
+      for (int c = (tid >> 6) * 4; c < D; c += 8) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < u.n_tok) x = __ldg(reinterpret_cast<const float4 *>(q + c));
+        Qt[c * 64 + r] = x.x; Qt[(c + 1) * 64 + r] = x.y;
+        Qt[(c + 2) * 64 + r] = x.z; Qt[(c + 3) * 64 + r] = x.w;
+      }
     }
-    float o[D / 8][4] = {}, m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
-    const int row[2] = {warp * 16 + gq, warp * 16 + gq + 8};
-    int limit[2];  // last visible key
+    float o[8][kCols] = {}, m[8], l[8] = {};  // l: this thread's keys only
+    int limit[8];                             // last visible key
 #pragma unroll
-    for (int h = 0; h < 2; h++) limit[h] = min(u.pos0 + row[h] / u.gp, u.len - 1);
-    for (int t = u.t0; t < u.t1; t++) {
-      const int key0 = t * 64;
+    for (int i = 0; i < 8; i++) {
+      m[i] = -CUDART_INF_F;
+      limit[i] = min(u.pos0 + (warp * 16 + rg * 8 + i) / u.gp, u.len - 1);
+    }
+    const int end = min(u.t1 * 64, max(u.pos0 + u.n_tok, 0));  // behind the last key that anybody sees
+    for (int key0 = u.t0 * 64; key0 < end; key0 += 64) {
       __syncthreads();
-      for (int i = tid; i < 2 * 64 * (D / 8); i += kThreads) {
-        const bool is_v = i >= 64 * (D / 8);
-        const int j = is_v ? i - 64 * (D / 8) : i, r = j / (D / 8), c = (j % (D / 8)) * 8;
-        const int key = key0 + r;
-        float x[8] = {};
-        if (key < u.len) {
-          const float *p = static_cast<const float *>(is_v ? a.v : a.k);
-          bool ok = true;
-          if (a.table) {
-            const int page = __ldg(a.table + (long long)u.seq * a.max_pages + key / a.page_size);
-            ok = page >= 0 && page < a.n_pages;
-            if (!ok && a.flags) atomicOr(a.flags, kFlagBadSeqlens);
-            p += (((long long)page * a.page_size + key % a.page_size) * a.HKV + u.kvh) * D;
-          } else {
-            // a prompt's keys are its own tokens
-            p += (long long)(u.row0 - u.pos0 + key) * (is_v ? a.v_stride : a.k_stride) + u.kvh * D;
-          }
-          if (ok) load8(x, p + c);
+      // a key's row of the tile; a bad page reads as zeros
+      auto row_of = [&](int key, const void *base, long long stride) -> const float * {
+        if (key >= u.len) return nullptr;
+        const float *p = static_cast<const float *>(base);
+        // a prompt's keys are its own tokens
+        if (!a.table) return p + (u.row0 - u.pos0 + key) * stride + u.kvh * D;
+        const int index = a.page_log >= 0 ? key >> a.page_log : key / a.page_size;
+        const int page = __ldg(a.table + (long long)u.seq * a.max_pages + index);
+        if (page < 0 || page >= a.n_pages) {
+          if (a.flags) atomicOr(a.flags, kFlagBadSeqlens);
+          return nullptr;
         }
-        put8((is_v ? Vs : Ks) + r * kS + c, x);
+        return p + (((long long)page * a.page_size + key - index * a.page_size) * a.HKV + u.kvh) * D;
+      };
+      {
+        const int r = tid & 63;
+        const float *k = row_of(key0 + r, a.k, a.k_stride);
+        for (int c = (tid >> 6) * 4; c < D; c += 8) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k) x = __ldg(reinterpret_cast<const float4 *>(k + c));
+          Kt[c * 64 + r] = x.x; Kt[(c + 1) * 64 + r] = x.y;
+          Kt[(c + 2) * 64 + r] = x.z; Kt[(c + 3) * 64 + r] = x.w;
+        }
+        for (int i = tid; i < 64 * (D / 4); i += kThreads) {
+          const int j = i / (D / 4), c = (i % (D / 4)) * 4;
+          const float *v = row_of(key0 + j, a.v, a.v_stride);
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (v) x = __ldg(reinterpret_cast<const float4 *>(v + c));
+          *reinterpret_cast<float4 *>(Vs + j * D + c) = x;
+        }
       }
       __syncthreads();
       float s[8][4] = {};
-#pragma unroll 4
-      for (int k = 0; k < D; k += 8) {
-        uint32_t ah[4], al[4];
-        const float *q0 = Qs + row[0] * kS + k + tq, *q1 = Qs + row[1] * kS + k + tq;
-        split_tf32(q0[0], ah[0], al[0]);
-        split_tf32(q1[0], ah[1], al[1]);
-        split_tf32(q0[4], ah[2], al[2]);
-        split_tf32(q1[4], ah[3], al[3]);
+      {
+        const float *q = Qt + warp * 16 + rg * 8, *k = Kt + cg * 4;
+#pragma unroll 8
+        for (int c = 0; c < D; c++) {
+          float x[8], y[4];
+          get4(x, q + c * 64);
+          get4(x + 4, q + c * 64 + 4);
+          get4(y, k + c * 64);
 #pragma unroll
-        for (int n = 0; n < 8; n++) {
-          const float *b = Ks + (n * 8 + gq) * kS + k + tq;
-          mma3(s[n], ah, al, b[0], b[4]);
+          for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) s[i][j] = fmaf(x[i], y[j], s[i][j]);
         }
       }
-      // running maximum and sum; element e of a tile: row e / 2, key 2 tq + e % 2
+      // running maximum and sum
+      const bool all_seen = key0 + 63 <= min(u.pos0, u.len - 1);
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        float top = m[h];
+      for (int i = 0; i < 8; i++) {
+        if (!all_seen)
 #pragma unroll
-        for (int n = 0; n < 8; n++)
+          for (int j = 0; j < 4; j++)
+            if (key0 + cg * 4 + j > limit[i]) s[i][j] = -CUDART_INF_F;
+        float top = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
 #pragma unroll
-          for (int e = 0; e < 2; e++) {
-            float &x = s[n][2 * h + e];
-            x = key0 + n * 8 + 2 * tq + e <= limit[h] ? x * a.scale_log2 : -CUDART_INF_F;
-            top = fmaxf(top, x);
-          }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float base = top == -CUDART_INF_F ? 0.f : top;  // nothing visible yet
-        const float alpha = exp2_approx(m[h] - base);
-        m[h] = top;
-        float sum = 0.f;
+        for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = fmaxf(top, m[i]);
+        const float off = top == -CUDART_INF_F ? 0.f : top * a.scale_log2;  // nothing visible yet
+        const float alpha = exp2_approx(fmaf(m[i], a.scale_log2, -off));
+        m[i] = top;
+        l[i] *= alpha;
 #pragma unroll
-        for (int n = 0; n < 8; n++)
-#pragma unroll
-          for (int e = 0; e < 2; e++) {
-            float &x = s[n][2 * h + e];
-            x = exp2_approx(x - base);
-            sum += x;
-          }
-        l[h] = l[h] * alpha + sum;
-#pragma unroll
-        for (int n = 0; n < D / 8; n++) {
-          o[n][2 * h] *= alpha;
-          o[n][2 * h + 1] *= alpha;
+        for (int j = 0; j < 4; j++) {
+          s[i][j] = exp2_approx(fmaf(s[i][j], a.scale_log2, -off));
+          l[i] += s[i][j];
         }
+#pragma unroll
+        for (int j = 0; j < kCols; j++) o[i][j] *= alpha;
       }
-      // the weights are the A operand as they lie: contraction index tq stands
-      // for key 2 tq, index tq + 4 for key 2 tq + 1
+      __syncthreads();  // every warp has read the keys
+      // key 4 cg + j at place 16 j + cg
 #pragma unroll
-      for (int n = 0; n < 8; n++) {
-        uint32_t ah[4], al[4];
-        split_tf32(s[n][0], ah[0], al[0]);
-        split_tf32(s[n][2], ah[1], al[1]);
-        split_tf32(s[n][1], ah[2], al[2]);
-        split_tf32(s[n][3], ah[3], al[3]);
-        const float *b = Vs + (n * 8 + 2 * tq) * kS + gq;
+      for (int j = 0; j < 4; j++) {
+        float *p = P + (j * 16 + cg) * kPRow;
+        *reinterpret_cast<float4 *>(p) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+        *reinterpret_cast<float4 *>(p + 4) = make_float4(s[4][j], s[5][j], s[6][j], s[7][j]);
+      }
+      __syncwarp();
+#pragma unroll 8
+      for (int i0 = 0; i0 < 64; i0++) {
+        float x[8], y[kCols];
+        get4(x, P + i0 * kPRow);
+        get4(x + 4, P + i0 * kPRow + 4);
+        const float *v = Vs + ((i0 & 15) * 4 + (i0 >> 4)) * D + cg * 4;
+        get4(y, v);
+        if constexpr (kCols == 8) get4(y + 4, v + 64);
 #pragma unroll
-        for (int d = 0; d < D / 8; d++) mma3(o[d], ah, al, b[d * 8], b[kS + d * 8]);
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+          for (int j = 0; j < kCols; j++) o[i][j] = fmaf(x[i], y[j], o[i][j]);
       }
     }
     bool finite = true;
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      const int t = row[h] / u.gp, head = u.head0 + row[h] % u.gp;
-      if (t >= u.n_tok) continue;
-      if (u.slot >= 0) {
-        float2 *po = reinterpret_cast<float2 *>(a.part_o + (long long)u.slot * 64 * (D / 4));
+    for (int i = 0; i < 8; i++) {
 #pragma unroll
-        for (int n = 0; n < D / 8; n++)  // columns n*8 + 2 tq: half of float4 n*2 + tq/2
-          po[((long long)(n * 2 + (tq >> 1)) * 64 + row[h]) * 2 + (tq & 1)] =
-              make_float2(o[n][2 * h], o[n][2 * h + 1]);
-        if (tq == 0) a.part_ml[(long long)u.slot * 64 + row[h]] = make_float2(m[h], l[h]);
-        continue;
-      }
-      const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
+      for (int d = 1; d < 16; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+      const int row = warp * 16 + rg * 8 + i;
+      const float m_scaled = m[i] * a.scale_log2;
+      const int t = row / u.gp, head = u.head0 + row % u.gp;
+      if (t >= u.n_tok) continue;
+      const bool part = u.slot >= 0;
+      const float inv = part ? 1.f : (l[i] == 0.f ? 0.f : 1.f / l[i]);
       const long long at = (long long)(u.row0 + t) * a.H + head;
 #pragma unroll
-      for (int n = 0; n < D / 8; n++) {
-        const float x = o[n][2 * h] * inv, y = o[n][2 * h + 1] * inv;
-        finite &= isfinite(x) && isfinite(y);
-        *reinterpret_cast<float2 *>(static_cast<float *>(a.o) + at * D + n * 8 + 2 * tq) =
-            make_float2(x, y);
+      for (int b = 0; b < kCols; b += 4) {
+        const int c = cg * 4 + b * 16;
+        const float4 x = make_float4(o[i][b] * inv, o[i][b + 1] * inv, o[i][b + 2] * inv, o[i][b + 3] * inv);
+        if (part) {
+          a.part_o[((long long)u.slot * (D / 4) + (c >> 2)) * 64 + row] = x;
+        } else {
+          finite &= isfinite(x.x) && isfinite(x.y) && isfinite(x.z) && isfinite(x.w);
+          *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at * D + c) = x;
+        }
       }
-      if (a.lse && tq == 0) a.lse[at] = l[h] == 0.f ? -CUDART_INF_F : (m[h] + log2f(l[h])) * 0.69314718056f;
+      if (cg == 0) {
+        if (part)
+          a.part_ml[(long long)u.slot * 64 + row] = make_float2(m_scaled, l[i]);
+        else if (a.lse)
+          a.lse[at] = l[i] == 0.f ? -CUDART_INF_F : (m_scaled + log2f(l[i])) * 0.69314718056f;
+      }
     }
     if (!finite && a.flags) atomicOr(a.flags, kFlagNonfinite);
   }
@@ -332,9 +354,9 @@ std::atomic<uint64_t> allowed{0};
 template <int D>
 cudaError_t launch(const AttnArgs &a, int blocks, cudaStream_t stream) {
   const cudaError_t e = allow_smem(reinterpret_cast<const void *>(&gdn_attn_warp_kernel<D>),
-                                   smem_bytes<D>(), allowed<D>);
+                                   WarpSmem<D>::kBytes, allowed<D>);
   if (e != cudaSuccess) return e;
-  gdn_attn_warp_kernel<D><<<blocks, kThreads, smem_bytes<D>(), stream>>>(a);
+  gdn_attn_warp_kernel<D><<<blocks, kThreads, WarpSmem<D>::kBytes, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -387,7 +409,7 @@ cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &don
 
 AttnLaunch attn_launch(AttnArgs &a, int d, int dtype) {
   return dtype ? plan_launch<TcShape>(a, sm_count())
-               : plan_launch<WarpShape>(a, sm_count() * (d == 64 ? 4 : 2));
+               : plan_launch<WarpShape>(a, sm_count() * (d == 64 ? blocks_per_sm<64>() : blocks_per_sm<128>()));
 }
 
 cudaError_t launch_attn(const AttnArgs &a, int d, int dtype, const AttnLaunch &l,
