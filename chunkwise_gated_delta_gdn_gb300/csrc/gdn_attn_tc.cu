@@ -720,23 +720,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       // one tile for both X
       int left0 = -1, left1 = -1, old_len = 0;
       bool shared = false, more = false;  // more: O has been written before
-      struct Tile {
-        int stage;
-        uint32_t round;
-      };
+      // The next tile of the ring, once it is there.  Also the other X's tiles
+      // are waited for: a wait tells two fillings of a stage apart by parity
+      // only, and would take the one before last for the one it wants if the
+      // last one had not arrived yet.
       auto next_tile = [&] {
-        const Tile t{ring.i, ring.round};
+        const int stage = ring.i;
+        wait(bars.kv_full(stage), ring.round, abort);
         ring.step();
-        return t;
+        return stage;
       };
-      auto loaded = [&](const Tile &t) { wait(bars.kv_full(t.stage), t.round, abort); };
-      auto values_loaded = [&](const Tile &t, int tile, int len) {
-        loaded(t);
+      auto clear_values = [&](int stage, int tile, int len) {
         // weights past the last key are zero, but 0 * NaN is not: clear the
         // value rows that belong to nobody (both X do, where they share a tile)
         const int rows = len - tile * 128;
         if (rows < 128) {
-          unsigned char *tile_at = sm + SM::kRing + t.stage * SM::kTileBytes;
+          unsigned char *tile_at = sm + SM::kRing + stage * SM::kTileBytes;
           for (int i = max(rows, 0) * 8 + lane; i < 128 * 8; i += 32) {
             const int row = i >> 3;
 #pragma unroll
@@ -752,9 +751,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // stage, or -1) when it sees the scores.  (A commit for each stage would
       // cost the tensor pipe 40 to 120 clocks: it does not start the next product
       // before the committed ones are through.)
-      auto scores = [&](const Tile &k, int q_tile, int free_v) {
+      auto scores = [&](int k, int q_tile, int free_v) {
         const uint32_t q_lo = desc_lo(sQ + q_tile * SM::kTileBytes, 16);
-        const uint32_t k_lo = desc_lo(sRing + k.stage * SM::kTileBytes, 16);
+        const uint32_t k_lo = desc_lo(sRing + k * SM::kTileBytes, 16);
         fence_after_sync();
         issue_scores<true>(tS + x * 128, q_lo, k_lo, desc_hi(kGroup), kIdS, lane == 0);
         if (D == 128)
@@ -762,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                               kIdS, lane == 0);
         if (lane == 0) {
           mma_commit(bars.s_full(x));
-          used[x] = make_int2(k.stage, free_v);
+          used[x] = make_int2(k, free_v);
           mbar_arrive(bars.s_full(x));
         }
       };
@@ -778,13 +777,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         issue_output<2 * kGroup>(tO + x * D, tS + x * 128 + 32, v_lo + (8 * kGroup >> 4), desc_hi(kGroup),
                                  kIdO, true, lane == 0);
       };
-      auto last_output = [&](const Tile &v, int tile) {
-        values_loaded(v, tile, old_len);
+      auto last_output = [&](int v, int tile) {
+        clear_values(v, tile, old_len);
         weights_ready();
-        output(v.stage, more);
+        output(v, more);
         if (lane == 0) {
-          mma_commit(bars.kv_empty(v.stage));  // each stage waits for two arrivals
-          if (!shared) mma_commit(bars.kv_empty(v.stage));
+          mma_commit(bars.kv_empty(v));  // each stage waits for two arrivals
+          if (!shared) mma_commit(bars.kv_empty(v));
           mma_commit(bars.o_full(x));
         }
         __syncwarp();
@@ -792,12 +791,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the last values up to those of X = 0, in the loader's order
       auto last_values = [&] {
         if (left1 >= 0 && left1 < left0) {
-          const Tile v = next_tile();
+          const int v = next_tile();
           if (x == 1) last_output(v, left1);
           left1 = -1;
         }
         if (left0 >= 0) {
-          const Tile v = next_tile();
+          const int v = next_tile();
           if (x == 0 || shared) last_output(v, left0);
           if (shared) left1 = -1;
           left0 = -1;
@@ -805,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto last_values_1 = [&] {
         if (left1 < 0) return;
-        const Tile v = next_tile();
+        const int v = next_tile();
         if (x == 1) last_output(v, left1);
         left1 = -1;
       };
@@ -813,49 +812,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t0 = uniform(u.t0), t1 = uniform(u.t1), len = uniform(u.len);
         const bool narrow = uniform(u.n_tok * u.gp) <= 128;
         last_values();
-        const Tile k = next_tile();
+        const int k = next_tile();
         wait(bars.q_full(), q_phase, abort);
         q_phase ^= 1;
-        if (x == 0) {
-          loaded(k);
-          scores(k, 0, -1);
-        }
+        if (x == 0) scores(k, 0, -1);
         last_values_1();
         if (narrow) {
           if (t0 + 1 < t1) {
-            const Tile k1 = next_tile();
-            if (x == 1) {
-              loaded(k1);
-              scores(k1, 0, -1);
-            }
+            const int k1 = next_tile();
+            if (x == 1) scores(k1, 0, -1);
           }
           for (int t = t0 + 2; t < t1; t++) {
-            const Tile v = next_tile(), k_next = next_tile();
+            const int v = next_tile(), k_next = next_tile();
             if (((t - t0) & 1) != x) continue;
-            values_loaded(v, t - 2, len);
+            clear_values(v, t - 2, len);
             weights_ready();
-            output(v.stage, t >= t0 + 4);
-            loaded(k_next);
-            scores(k_next, 0, v.stage);
+            output(v, t >= t0 + 4);
+            scores(k_next, 0, v);
           }
           const int odd = (t1 - 1 - t0) & 1;  // which X has the last tile
           left0 = t1 - 1 - odd;
           left1 = t0 + 1 < t1 ? t1 - 2 + odd : -1;
           more = t0 + 2 + x < t1;
         } else {
-          if (x == 1) {
-            loaded(k);
-            scores(k, 1, -1);
-          }
+          if (x == 1) scores(k, 1, -1);
           for (int t = t0; t + 1 < t1; t++) {
-            const Tile v = next_tile(), k_next = next_tile();
-            values_loaded(v, t, len);
-            loaded(k_next);
+            const int v = next_tile(), k_next = next_tile();
+            clear_values(v, t, len);
             weights_ready();
             wait(bars.turn(x), turn ^ (x == 0 ? 1 : 0), abort);
             turn ^= 1;
-            output(v.stage, t > t0);
-            scores(k_next, x, v.stage);
+            output(v, t > t0);
+            scores(k_next, x, v);
             if (lane == 0) mbar_arrive(bars.turn(x ^ 1));
           }
           left0 = left1 = t1 - 1;
