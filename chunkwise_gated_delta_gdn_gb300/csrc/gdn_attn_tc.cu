@@ -607,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       struct Window {
         int seq, base, page;
       } win[2] = {{-1, 0, 0}, {-1, 0, 0}};
+      const int groups = a.page_size >> 3, my_key = lane * box;  // 8-row groups of a page
       auto page_of = [&](int key) {
         return a.page_log >= 0 ? key >> a.page_log : key / a.page_size;
       };
@@ -618,29 +619,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (PAGED) {
           // lane i takes the i-th box of `box` keys; boxes past the last key
           // are not loaded (what they leave in shared memory is masked)
-          const int rest = w.len - key;
-          const int n = rest <= 0 ? 0 : min((rest + box - 1) / box, 128 / box);
           Window &pages = win[which];
-          const int last = w.len - 1, k0 = min(key + lane * box, last);
-          const int index = page_of(k0);
-          const int lo = __shfl_sync(0xffffffffu, index, 0), hi = __shfl_sync(0xffffffffu, index, max(n, 1) - 1);
-          if (n > 0 && (pages.seq != w.seq || lo < pages.base || hi >= pages.base + 32)) {
+          const int last = w.len - 1, k0 = min(key + my_key, last);
+          const int lo = page_of(key), index = page_of(k0);
+          if (key <= last && (pages.seq != w.seq || lo < pages.base || lo + 8 >= pages.base + 32)) {
             pages.seq = w.seq;
             pages.base = lo;
             pages.page = __ldg(a.table + (long long)w.seq * a.max_pages + min(lo + lane, page_of(last)));
           }
-          int page = __shfl_sync(0xffffffffu, pages.page, (index - pages.base) & 31);
-          const int first = k0 - index * a.page_size;
-          if (lane < n && (page < 0 || page >= a.n_pages)) {
-            if (a.flags) atomicOr(a.flags, kFlagBadSeqlens);
-            page = a.n_pages;  // just past the cache: reads as zeros
-          }
+          const int held = __shfl_sync(0xffffffffu, pages.page, (index - pages.base) & 31);
+          const bool mine = key + my_key <= last && my_key < 128;
+          const bool good = (unsigned)held < (unsigned)a.n_pages;
+          if (mine && !good && a.flags) atomicOr(a.flags, kFlagBadSeqlens);
+          // a bad page reads as zeros: the box just past the cache
+          const int group = (good ? held : a.n_pages) * groups + ((k0 - index * a.page_size) >> 3);
+          const int n = min((last - key + box) / box, 128 / box);  // boxes; may be <= 0
           wait(bars.kv_empty(ring.i), ring.round ^ 1, abort);
-          if (lane == 0) mbar_arrive_expect_tx(full, n * box * 128 * kPanels);
+          if (lane == 0) mbar_arrive_expect_tx(full, max(n, 0) * box * 128 * kPanels);
           __syncwarp();
-          if (lane < n)
-            tma_load_5d(dst + lane * box * 128 * kPanels, map, 0, 0, 0,
-                        page * (a.page_size >> 3) + (first >> 3), w.kvh, full,
+          if (mine)
+            tma_load_5d(dst + my_key * 128 * kPanels, map, 0, 0, 0, group, w.kvh, full,
                         w.n_tok * w.gp <= 128 ? once : often);
         } else {
           wait(bars.kv_empty(ring.i), ring.round ^ 1, abort);
