@@ -30,7 +30,6 @@ namespace {
 // D / 16 columns.  Those reads bound it: 12 wavefronts of shared memory for 32
 // clocks of multiply-adds in each of four schedulers, 27 to 38 TFLOP/s of 74.
 using WarpShape = AttnShape<64, 64, 64, 1, 1>;
-using TcShape = AttnShape<256, 128, 128, 2, 4>;  // of the bf16 kernel (gdn_attn_tc.cu)
 constexpr int kThreads = 128;
 constexpr int kPRow = 20;  // floats from one key's 16 weights to the next: 8 lanes hit 32 banks
 

@@ -12,9 +12,9 @@
 //    and a unit is kRows rows: kRows / gp tokens of gp heads.
 // A unit covers the key tiles 0 .. nt-1 of kTile keys up to its last row's
 // position.  Its tiles are grouped into grains of 2^shift tiles; every unit
-// costs `over` plus its grains (times kWide for an unpacked unit), costs are
-// numbered through all units and sequences, and block i of the grid takes the
-// range [i per, (i+1) per).
+// costs `over` plus its grains times a weight (both differ between packed and
+// unpacked units), costs are numbered through all units and sequences, and block
+// i of the grid takes the range [i per, (i+1) per).
 //  * A call with little work takes the smallest grain at which there are no
 //    more grains than blocks, and each block one grain: nothing waits behind
 //    another unit, and no piece is smaller than kMinGrain tiles.
@@ -35,16 +35,22 @@
 
 namespace gdn {
 
-// Shape of a unit: rows, rows of a packed unit, keys per tile, cost of one
-// tile of an unpacked unit (a packed unit's tile costs 1), cost of an unpacked
-// unit's own start and end (a packed one's is half of it).  For bf16 that cost
-// is 4: with 0, 2, 4, 8 four prompts of 2048 tokens took 295, 160, 152, 160 us
-// and packed prompts 663, 488, 422, 424; 256 sequences of one token with 0, 1,
-// 2, 4 for a packed unit 443, 410, 422, 432.
-template <int ROWS, int PACK, int TILE, int WIDE, int OVER>
+// Shape of a unit: rows, rows of a packed unit, keys per tile; cost of one tile
+// of an unpacked unit and of that unit's own start and end; the same of a packed
+// one.
+template <int ROWS, int PACK, int TILE, int WIDE, int OVER, int NARROW = 1, int PACKED_OVER = OVER / 2>
 struct AttnShape {
-  static constexpr int kRows = ROWS, kPack = PACK, kTile = TILE, kWide = WIDE, kOver = OVER;
+  static constexpr int kRows = ROWS, kPack = PACK, kTile = TILE;
+  static constexpr int kWide = WIDE, kOver = OVER, kNarrow = NARROW, kPackedOver = PACKED_OVER;
 };
+// The bf16 kernel's (gdn_attn_tc.cu).  A packed unit's tile takes 3/4 of an
+// unpacked one's: 1/2, 2/3, 3/4 and 1 gave 129, 107, 104 and 109 us for two
+// chunks of up to 500 tokens among 14 single ones (32 heads of 64), and 164, 153,
+// 151, 189 for one of up to 1000 among 63 (heads of 128).  A unit's start and end
+// take two tiles.  An unpacked one's as 0, 1, 2, 4 tiles: four prompts of 2048
+// tokens 295, 160, 152, 160 us, packed prompts 663, 488, 422, 424; a packed one's
+// as 0, 2, 4, 8: 256 sequences of one token 443, 410, 422, 432.
+using TcShape = AttnShape<256, 128, 128, 4, 8, 3, 6>;
 // log2 of the smallest grain of a small call (4, 8 and 16 tiles were alike in all
 // cases measured: below this a piece's start and the joining outweigh its tiles)
 constexpr int kMinGrain = 3;
@@ -123,7 +129,8 @@ struct AttnPlan {
   int gp, tok_log;     // heads and log2 of the tokens of an unpacked unit
   int coarse;          // log2 of the grain of equal shares
   int shift;           // log2 of the grain, in tiles
-  int wide, over;      // cost of an unpacked unit's grain, and of a unit
+  int wide, over;      // cost of an unpacked unit's grain, and of the unit
+  int narrow, packed_over;  // of a packed one
   AttnCost per;        // cost of a block's range
 
   __host__ __device__ AttnPlan(int H, int hkv, int coarse_) {
@@ -142,12 +149,14 @@ struct AttnPlan {
     shift = coarse;
     wide = S::kWide;
     over = S::kOver;
+    narrow = S::kNarrow;
+    packed_over = S::kPackedOver;
     per = p;
   }
   __host__ __device__ void grains(int log) {
     shift = log;
-    wide = 1;
-    over = 0;
+    wide = narrow = 1;
+    over = packed_over = 0;
     per = 1;
   }
 
@@ -181,7 +190,7 @@ struct AttnPlan {
     return x * (a >> grain_log) + floors(b + x, r) - floors(b, r);
   }
   // a unit's own cost: a packed one has fewer rows to write
-  __host__ __device__ AttnCost own_cost(int nq) const { return packed(nq) ? over >> 1 : over; }
+  __host__ __device__ AttnCost own_cost(int nq) const { return packed(nq) ? packed_over : over; }
   // cost of one head group of an unpacked sequence
   __host__ __device__ AttnCost group_cost(int nq, int base) const {
     const int n = token_tiles(nq);
@@ -189,7 +198,7 @@ struct AttnPlan {
   }
   __host__ __device__ AttnCost cost(int nq, int base) const {
     if (nq == 0) return 0;
-    if (packed(nq)) return (AttnCost)HKV * (grains_of(base + nq) + own_cost(nq));
+    if (packed(nq)) return (AttnCost)HKV * (grains_of(base + nq) * narrow + own_cost(nq));
     return group_cost(nq, base) * groups;
   }
 
@@ -199,7 +208,7 @@ struct AttnPlan {
     u.seq = seq;
     u.len = s.len;
     if (packed(s.nq)) {
-      const AttnCost each = grains_of(s.base + s.nq) + own_cost(s.nq);
+      const AttnCost each = grains_of(s.base + s.nq) * narrow + own_cost(s.nq);
       u.nt = tiles(s.base + s.nq);
       u.kvh = (int)(c / each);
       u.head0 = u.kvh * G;
@@ -254,7 +263,7 @@ struct AttnPlan {
     place(s, group, tile, u);
     return true;
   }
-  __host__ __device__ int weight(const AttnSeq &s) const { return packed(s.nq) ? 1 : wide; }
+  __host__ __device__ int weight(const AttnSeq &s) const { return packed(s.nq) ? narrow : wide; }
   // cost of unit u
   __host__ __device__ AttnCost unit_cost(const AttnSeq &s, const AttnUnit &u) const {
     return own_cost(s.nq) + (AttnCost)((u.nt + (1 << shift) - 1) >> shift) * weight(s);
@@ -264,8 +273,10 @@ struct AttnPlan {
     u0 += own_cost(s.nq);
     if (c <= u0) return 0;
     c -= u0;
-    static_assert(S::kWide == 1 || S::kWide == 2, "a shift in cut()");
-    const AttnCost grain = weight(s) == 1 ? c : (c + 1) >> 1;
+    // by constants: a call waits for this
+    const AttnCost grain = wide == 1 ? c
+                           : packed(s.nq) ? (c + S::kNarrow - 1) / S::kNarrow
+                                          : (c + S::kWide - 1) / S::kWide;
     return grain < (AttnCost)((nt + (1 << shift) - 1) >> shift) ? (int)(grain << shift) : nt;
   }
   // last block with a piece of the unit that begins at cost u0
@@ -296,10 +307,9 @@ struct AttnPlan {
         log++;
       }
       while (log <= kMaxGrain && (2u << log) < share / S::kWide) log++;  // far too many grains
-      if (log > kMaxGrain || (log > kMinGrain && (1u << log) > share + kSlack)) break;
+      if (log > kMaxGrain || (log > kMinGrain && (1u << log) > share / S::kNarrow + kSlack)) break;
       grains(log);
     }
-    share += share & (S::kWide - 1);
     stream(share < S::kWide ? S::kWide : share);
     return weighted;
   }

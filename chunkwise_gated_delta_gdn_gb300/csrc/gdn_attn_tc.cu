@@ -33,7 +33,6 @@ namespace {
 
 using namespace sm100;
 
-using TcShape = AttnShape<256, 128, 128, 2, 4>;
 constexpr int kThreads = 640;
 constexpr int kUnits = 4;              // unit ring
 constexpr int kPanel = 128 * 128;      // bytes of 128 rows x 64 bf16

@@ -136,7 +136,8 @@ int main() {
     }
     const int blocks = rnd(0, 1) ? rnd(1, 9) : rnd(10, 200), force = rnd(0, 1) ? -1 : rnd(0, 4);
     if (!one<AttnShape<64, 64, 64, 1, 1>>(q, kv, hkv * g, hkv, blocks, force, trial % 3) ||
-        !one<AttnShape<256, 128, 128, 2, 4>>(q, kv, hkv * g, hkv, blocks, force, trial % 3)) {
+        !one<AttnShape<256, 128, 128, 2, 4>>(q, kv, hkv * g, hkv, blocks, force, trial % 3) ||
+        !one<TcShape>(q, kv, hkv * g, hkv, blocks, force, trial % 3)) {
       std::printf("trial %d: hkv %d g %d blocks %d\n", trial, hkv, g, blocks);
       return 1;
     }
