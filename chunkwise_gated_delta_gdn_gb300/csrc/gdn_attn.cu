@@ -17,18 +17,20 @@ namespace gdn {
 namespace {
 
 // fp32: a unit of 64 rows, 64 keys per step, four warps of 16 rows, both
-// products in fp32 multiply-adds.  Products of split operands on the tensor
-// cores (three tf32 ones each, on mma.sync) took as long: 159 us, this 158 (2 x
-// 1023 tokens, 16 heads of 64); 926 and 914 us at 8192 tokens of 4 heads, where
-// their error was 4.7e-6 against 2.5e-6, since those accumulations are cut off
-// and not rounded.
+// products in fp32 multiply-adds: 146 us for 2 x 1023 tokens, 16 heads of 64; 906
+// for 8192 tokens of 4 heads, 1007 for 4096 tokens of 8 heads of 128.  Products of
+// split operands on the tensor cores (three tf32 ones each, on mma.sync) took as
+// long, and their error at 8192 tokens was 4.7e-6 against 2.5e-6, since those
+// accumulations are cut off and not rounded.
 //
 // S = Q K^T: a thread has 8 rows and 4 keys; queries and keys lie transposed in
 // shared memory, so that each step of the contraction is three 16-byte reads
 // for 32 multiply-adds.  The 16 threads of a row are half a warp.  O = P V: the
 // weights go through shared memory (over the keys), and a thread has 8 rows and
-// D / 16 columns.  Those reads bound it: 12 wavefronts of shared memory for 32
-// clocks of multiply-adds in each of four schedulers, 27 to 38 TFLOP/s of 74.
+// D / 16 columns.  28 to 38 TFLOP/s of 74, and no unit is full: multiply-adds 46%,
+// shared memory 44%, issue 59%.  Neither two multiply-adds in an instruction
+// (149, 926 and 967 us) nor keys and values copied in the background besides
+// (148, 908, 956) nor other numbers of blocks helped at both widths.
 using WarpShape = AttnShape<64, 64, 64, 1, 1>;
 constexpr int kThreads = 128;
 constexpr int kPRow = 20;  // floats from one key's 16 weights to the next: 8 lanes hit 32 banks

@@ -381,20 +381,22 @@ GDN_API gdn_status gdn_state_combine(const float *M, const float *S_in, const fl
  *               out).  NONFINITE: a non-finite value was written to o.
  *   workspace   at least the bytes of the matching query, 256-byte aligned,
  *               not shared by two calls in flight; contents need no
- *               preparation and mean nothing afterwards.
+ *               preparation and mean nothing afterwards.  NULL with 0 bytes
+ *               where the query gives 0 (small calls); a call whose lengths
+ *               the host knows may need less than the query's answer.
  * Device pointers are 16-byte aligned (lse, cu_seqlens, block_table and
  * kv_lens: 4-byte).  No output may overlap an input or another output.
  *
  * What lies in the cache beyond L, and in other sequences, does not reach a
  * result, whatever its bits.  Within a sequence a non-finite v at a later
- * position can turn the outputs of earlier tokens of the same 128-key tile
- * into NaN (0 * inf).
+ * position can turn the outputs of earlier tokens of the same key tile (128
+ * keys, 64 in fp32) into NaN (0 * inf).
  *
  * Numerics: scores, row maximum and sum, and the output's accumulation in
  * fp32; o rounded once to dtype.  bf16: tensor-core products of bf16 operands;
  * the weights e^(s - m) are rounded to bf16 for their product with v, their
- * sum is not.  fp32: split-tf32 products (about 21 mantissa bits).  Results
- * are the same from call to call, bit for bit.
+ * sum is not.  fp32: fp32 multiply-adds.  Results are the same from call to
+ * call, bit for bit.
  */
 GDN_API size_t gdn_attn_fwd_workspace_bytes(int B, int T, int H, int HKV, int d, int n_seqs,
                                             int dtype);

@@ -3,9 +3,9 @@ the 64-bit definition in oracle/attn.py, through the C ABI.
 
 Tolerances, derived from the arithmetic.  Let A = sum_j w_j |v_j| (elementwise) and
 S = max_j scale sum_i |q_i k_ji| over a row's visible keys.
-* A score is a sum of at most 128 products accumulated in fp32 (fp32 inputs: of operands split to
-  about 21 bits), so it is off by at most about 2^-18 S; the log-sum-exp by as much, plus its own
-  rounding: |d lse| <= 2^-18 S + 2^-20 |lse| + 1e-6.
+* A score is a sum of at most 128 products accumulated in fp32, so it is off by at most about
+  2^-18 S; the log-sum-exp by as much, plus its own rounding:
+  |d lse| <= 2^-18 S + 2^-20 |lse| + 1e-6.
 * Scores off by e move the weights by a factor within 1 +- 2 e, the accumulation of the output in
   fp32 adds 2^-17 A: |d o| <= (2^-17 S + 2^-17) A for fp32.
 * bf16 adds one rounding of each weight and one of the output.  bf16 has 8 significant bits, so a
