@@ -10,6 +10,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gdn_attn.cuh"
 #include "gdn_device.cuh"
 
@@ -31,16 +33,17 @@ namespace {
 // shared memory 44%, issue 59%.  Neither two multiply-adds in an instruction
 // (149, 926 and 967 us) nor keys and values copied in the background besides
 // (148, 908, 956) nor other numbers of blocks helped at both widths.
-using WarpShape = AttnShape<64, 64, 64, 1, 1>;
+using WarpShape = AttnShape<64, 64, 64, 1, 1, 1, 0, 16, 0>;
 constexpr int kThreads = 128;
-constexpr int kPRow = 20;  // floats from one key's 16 weights to the next: 8 lanes hit 32 banks
 
 template <int D>
 struct WarpSmem {
-  static constexpr int kQ = 0, kK = 64 * D;                          // [D][64] each
-  static constexpr int kP = 4 * 64 * kPRow;                          // [warp][64 keys][kPRow]
-  static constexpr int kV = kK + (64 * D > kP ? 64 * D : kP);        // [64][D]
-  static constexpr int kBytes = (kV + 64 * D) * 4;
+  static constexpr int kKRow = D + 4;         // floats from one key to the next: 8 lanes hit 32 banks
+  static constexpr int kQ = 0;                // [D][64], queries transposed
+  static constexpr int kK = 64 * D;           // [64][kKRow]
+  static constexpr int kV = kK + 64 * kKRow;  // [64][D]
+  static constexpr int kP = kV + 64 * D;      // [warp][64 keys][16 rows]
+  static constexpr int kBytes = (kP + 4 * 64 * 16) * 4;
 };
 template <int D>
 constexpr int blocks_per_sm() { return D == 64 ? 3 : 2; }
@@ -55,15 +58,34 @@ __device__ __forceinline__ void get4(float *x, const float *p) {
   x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
 
+// eight values as four pairs
+__device__ __forceinline__ void get_pairs(uint64_t *x, const float *p, const float *p4) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p), b = *reinterpret_cast<const ulonglong2 *>(p4);
+  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+}
+// 16 bytes from global to shared memory, in the background; zeros when !valid
+__device__ __forceinline__ void copy16(float *to, const float *from, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from), "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// until all groups but the last N are there
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_kernel(const AttnArgs a) {
   using SM = WarpSmem<D>;
   constexpr int kCols = D / 16;  // columns of a thread: 4 from 4 cg on, and for D = 128 4 from 64 + 4 cg on
   extern __shared__ __align__(16) float smem[];
-  float *Qt = smem + SM::kQ, *Kt = smem + SM::kK, *Vs = smem + SM::kV;
+  float *Qt = smem + SM::kQ, *Ks = smem + SM::kK, *Vs = smem + SM::kV;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rg = lane >> 4, cg = lane & 15;  // rows warp * 16 + rg * 8 .. + 7; keys (columns) 4 cg .. + 3
-  float *P = smem + SM::kK + warp * 64 * kPRow + rg * 8;
+  const int rg = lane >> 4, cg = lane & 15;  // rows rg * 8 .. + 7 of the warp's 16; keys cg, cg + 16, ..
+  float *P = smem + SM::kP + warp * 64 * 16;
+  // weights of key j, rows 4 c .. 4 c + 3: the four chunks of a key are swapped
+  // about so that 8 keys' lie in different banks
+  auto chunk = [&](int j, int c) { return P + j * 16 + ((c ^ (j >> 1)) & 3) * 4; };
   AttnPlan<WarpShape> plan(a.H, a.HKV, a.plan_coarse);
   AttnStaged *staged = reinterpret_cast<AttnStaged *>(smem);  // until the first operands
   attn_stage(a, staged, blockIdx.x);
@@ -75,6 +97,37 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_ke
   while (walk.next(u)) {
     if (tid == 0 && u.slot == 2 * (int)blockIdx.x + 1) a.jobs[blockIdx.x] = attn_job(u);
     __syncthreads();  // the previous unit's operands (or the plan's) are read
+    const int end = min(u.t1 * 64, max(u.pos0 + u.n_tok, 0));  // behind the last key that anybody sees
+    // a key's row of the tile; a bad page reads as zeros
+    auto row_of = [&](int key, const void *base, long long stride) -> const float * {
+      if (key >= u.len) return nullptr;
+      const float *p = static_cast<const float *>(base);
+      // a prompt's keys are its own tokens
+      if (!a.table) return p + (u.row0 - u.pos0 + key) * stride + u.kvh * D;
+      const int index = a.page_log >= 0 ? key >> a.page_log : key / a.page_size;
+      const int page = __ldg(a.table + (long long)u.seq * a.max_pages + index);
+      if (page < 0 || page >= a.n_pages) {
+        if (a.flags) atomicOr(a.flags, kFlagBadSeqlens);
+        return nullptr;
+      }
+      return p + (((long long)page * a.page_size + key - index * a.page_size) * a.HKV + u.kvh) * D;
+    };
+    // 64 rows from key0 on into shared memory, on their way while others are
+    // worked on; one group of copies, empty behind the last tile
+    auto fetch = [&](int key0, const void *base, long long stride, float *to, int row_floats) {
+      if (key0 < end) {
+        constexpr int kRow = D / 4;  // 16-byte pieces
+#pragma unroll
+        for (int i = tid; i < 64 * kRow; i += kThreads) {
+          const float *from = row_of(key0 + i / kRow, base, stride);
+          copy16(to + (i / kRow) * row_floats + (i % kRow) * 4,
+                 from ? from + (i % kRow) * 4 : static_cast<const float *>(base), from != nullptr);
+        }
+      }
+      copies_end();
+    };
+    fetch(u.t0 * 64, a.k, a.k_stride, Ks, SM::kKRow);
+    fetch(u.t0 * 64, a.v, a.v_stride, Vs, D);
     {
       const int r = tid & 63, t = r / u.gp;
       const float *q = static_cast<const float *>(a.q) + (long long)(u.row0 + t) * a.q_stride +
@@ -86,126 +139,173 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_ke
         Qt[(c + 2) * 64 + r] = x.z; Qt[(c + 3) * 64 + r] = x.w;
       }
     }
-    float o[8][kCols] = {}, m[8], l[8] = {};  // l: this thread's keys only
-    int limit[8];                             // last visible key
+    // Few rows: every warp has the same 16 and a quarter of a tile's keys (key cg
+    // of its 16 is a thread's), joined at the end.
+    const bool few = u.n_tok * u.gp <= 16;
+    const int warp_row = few ? 0 : warp * 16;
+    uint64_t o[4][kCols] = {};  // pairs of rows
+    float m[8], l[8] = {};      // l: this thread's keys only
+    int limit[8];               // last visible key
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       m[i] = -CUDART_INF_F;
-      limit[i] = min(u.pos0 + (warp * 16 + rg * 8 + i) / u.gp, u.len - 1);
+      limit[i] = min(u.pos0 + (warp_row + rg * 8 + i) / u.gp, u.len - 1);
     }
-    const int end = min(u.t1 * 64, max(u.pos0 + u.n_tok, 0));  // behind the last key that anybody sees
     for (int key0 = u.t0 * 64; key0 < end; key0 += 64) {
+      copies_wait<1>();  // the keys
       __syncthreads();
-      // a key's row of the tile; a bad page reads as zeros
-      auto row_of = [&](int key, const void *base, long long stride) -> const float * {
-        if (key >= u.len) return nullptr;
-        const float *p = static_cast<const float *>(base);
-        // a prompt's keys are its own tokens
-        if (!a.table) return p + (u.row0 - u.pos0 + key) * stride + u.kvh * D;
-        const int index = a.page_log >= 0 ? key >> a.page_log : key / a.page_size;
-        const int page = __ldg(a.table + (long long)u.seq * a.max_pages + index);
-        if (page < 0 || page >= a.n_pages) {
-          if (a.flags) atomicOr(a.flags, kFlagBadSeqlens);
-          return nullptr;
+      auto work = [&](auto keys) {
+        constexpr int KEYS = decltype(keys)::value;
+        float s[8][KEYS];
+        {
+          uint64_t acc[4][KEYS] = {};  // pairs of rows
+          const float *q = Qt + warp_row + rg * 8, *k = Ks + (KEYS == 4 ? cg : warp * 16 + cg) * SM::kKRow;
+#pragma unroll 2
+          for (int c0 = 0; c0 < D; c0 += 4) {
+            float y[KEYS][4];
+#pragma unroll
+            for (int j = 0; j < KEYS; j++) get4(y[j], k + j * 16 * SM::kKRow + c0);
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+              uint64_t x[4];
+              get_pairs(x, q + (c0 + c) * 64, q + (c0 + c) * 64 + 4);
+#pragma unroll
+              for (int j = 0; j < KEYS; j++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) acc[i][j] = fma2(x[i], pair(y[j][c], y[j][c]), acc[i][j]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int j = 0; j < KEYS; j++) unpair(acc[i][j], s[2 * i][j], s[2 * i + 1][j]);
         }
-        return p + (((long long)page * a.page_size + key - index * a.page_size) * a.HKV + u.kvh) * D;
+        __syncthreads();  // every warp has read the keys
+        fetch(key0 + 64, a.k, a.k_stride, Ks, SM::kKRow);
+        // running maximum and sum
+        const int first = key0 + (KEYS == 4 ? cg : warp * 16 + cg);  // this thread's first key
+        float alpha[8];
+        const bool all_seen = key0 + 63 <= min(u.pos0, u.len - 1);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          if (!all_seen)
+#pragma unroll
+            for (int j = 0; j < KEYS; j++)
+              if (first + j * 16 > limit[i]) s[i][j] = -CUDART_INF_F;
+          float top = s[i][0];
+#pragma unroll
+          for (int j = 1; j < KEYS; j++) top = fmaxf(top, s[i][j]);
+#pragma unroll
+          for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          top = fmaxf(top, m[i]);
+          const float off = top == -CUDART_INF_F ? 0.f : top * a.scale_log2;  // nothing visible yet
+          alpha[i] = exp2_approx(fmaf(m[i], a.scale_log2, -off));
+          m[i] = top;
+          l[i] *= alpha[i];
+#pragma unroll
+          for (int j = 0; j < KEYS; j++) {
+            s[i][j] = exp2_approx(fmaf(s[i][j], a.scale_log2, -off));
+            l[i] += s[i][j];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+          for (int j = 0; j < kCols; j++) o[i][j] = mul2(o[i][j], pair(alpha[2 * i], alpha[2 * i + 1]));
+#pragma unroll
+        for (int j = 0; j < KEYS; j++) {
+          *reinterpret_cast<float4 *>(chunk(j * 16 + cg, rg * 2)) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+          *reinterpret_cast<float4 *>(chunk(j * 16 + cg, rg * 2 + 1)) = make_float4(s[4][j], s[5][j], s[6][j], s[7][j]);
+        }
+        copies_wait<1>();  // the values
+        __syncthreads();
+#pragma unroll 8
+        for (int j0 = 0; j0 < 16 * KEYS; j0++) {
+          uint64_t x[4];
+          float y[kCols];
+          get_pairs(x, chunk(j0, rg * 2), chunk(j0, rg * 2 + 1));
+          const float *v = Vs + (KEYS == 4 ? j0 : warp * 16 + j0) * D + cg * 4;
+          get4(y, v);
+          if constexpr (kCols == 8) get4(y + 4, v + 64);
+#pragma unroll
+          for (int j = 0; j < kCols; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) o[i][j] = fma2(x[i], pair(y[j], y[j]), o[i][j]);
+        }
+        __syncthreads();  // every warp has read the values
+        fetch(key0 + 64, a.v, a.v_stride, Vs, D);
       };
-      {
-        const int r = tid & 63;
-        const float *k = row_of(key0 + r, a.k, a.k_stride);
-        for (int c = (tid >> 6) * 4; c < D; c += 8) {
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (k) x = __ldg(reinterpret_cast<const float4 *>(k + c));
-          Kt[c * 64 + r] = x.x; Kt[(c + 1) * 64 + r] = x.y;
-          Kt[(c + 2) * 64 + r] = x.z; Kt[(c + 3) * 64 + r] = x.w;
-        }
-        for (int i = tid; i < 64 * (D / 4); i += kThreads) {
-          const int j = i / (D / 4), c = (i % (D / 4)) * 4;
-          const float *v = row_of(key0 + j, a.v, a.v_stride);
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (v) x = __ldg(reinterpret_cast<const float4 *>(v + c));
-          *reinterpret_cast<float4 *>(Vs + j * D + c) = x;
+      if (few) work(std::integral_constant<int, 1>{});
+      else work(std::integral_constant<int, 4>{});
+    }
+    float out[8][kCols];
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int j = 0; j < kCols; j++) unpair(o[i][j], out[2 * i][j], out[2 * i + 1][j]);
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+    if (few) {
+      // Warps 1-3 leave their outputs, maxima and sums in the places of the keys
+      // and values (no copy is on its way there), warp 0 adds them up in order.
+      constexpr int kRow = D + 4, kNext = 16 * kRow;
+      float *place = smem + SM::kK + (warp * 16 + rg * 8) * kRow;
+      __syncthreads();
+      if (warp > 0) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          float *p = place + i * kRow;
+#pragma unroll
+          for (int b = 0; b < kCols; b += 4)
+            *reinterpret_cast<float4 *>(p + cg * 4 + b * 16) =
+                make_float4(out[i][b], out[i][b + 1], out[i][b + 2], out[i][b + 3]);
+          if (cg == 0) *reinterpret_cast<float2 *>(p + D) = make_float2(m[i], l[i]);
         }
       }
       __syncthreads();
-      float s[8][4] = {};
-      {
-        const float *q = Qt + warp * 16 + rg * 8, *k = Kt + cg * 4;
-#pragma unroll 8
-        for (int c = 0; c < D; c++) {
-          float x[8], y[4];
-          get4(x, q + c * 64);
-          get4(x + 4, q + c * 64 + 4);
-          get4(y, k + c * 64);
+      if (warp == 0) {
 #pragma unroll
-          for (int i = 0; i < 8; i++)
+        for (int i = 0; i < 8; i++) {
+          const float *p = place + i * kRow;
+          float2 ml[4];
+          ml[0] = make_float2(m[i], l[i]);
 #pragma unroll
-            for (int j = 0; j < 4; j++) s[i][j] = fmaf(x[i], y[j], s[i][j]);
+          for (int w = 1; w < 4; w++) ml[w] = *reinterpret_cast<const float2 *>(p + w * kNext + D);
+          m[i] = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+          const float off = m[i] == -CUDART_INF_F ? 0.f : m[i] * a.scale_log2;
+          l[i] = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; w++) {
+            const float f = exp2_approx(fmaf(ml[w].x, a.scale_log2, -off));
+            l[i] += f * ml[w].y;
+#pragma unroll
+            for (int b = 0; b < kCols; b += 4) {
+              float y[4] = {};
+              if (w > 0) get4(y, p + w * kNext + cg * 4 + b * 16);
+#pragma unroll
+              for (int j = 0; j < 4; j++)
+                out[i][b + j] = w == 0 ? out[i][b + j] * f : fmaf(y[j], f, out[i][b + j]);
+            }
+          }
         }
-      }
-      // running maximum and sum
-      const bool all_seen = key0 + 63 <= min(u.pos0, u.len - 1);
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        if (!all_seen)
-#pragma unroll
-          for (int j = 0; j < 4; j++)
-            if (key0 + cg * 4 + j > limit[i]) s[i][j] = -CUDART_INF_F;
-        float top = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        top = fmaxf(top, m[i]);
-        const float off = top == -CUDART_INF_F ? 0.f : top * a.scale_log2;  // nothing visible yet
-        const float alpha = exp2_approx(fmaf(m[i], a.scale_log2, -off));
-        m[i] = top;
-        l[i] *= alpha;
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          s[i][j] = exp2_approx(fmaf(s[i][j], a.scale_log2, -off));
-          l[i] += s[i][j];
-        }
-#pragma unroll
-        for (int j = 0; j < kCols; j++) o[i][j] *= alpha;
-      }
-      __syncthreads();  // every warp has read the keys
-      // key 4 cg + j at place 16 j + cg
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        float *p = P + (j * 16 + cg) * kPRow;
-        *reinterpret_cast<float4 *>(p) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
-        *reinterpret_cast<float4 *>(p + 4) = make_float4(s[4][j], s[5][j], s[6][j], s[7][j]);
-      }
-      __syncwarp();
-#pragma unroll 8
-      for (int i0 = 0; i0 < 64; i0++) {
-        float x[8], y[kCols];
-        get4(x, P + i0 * kPRow);
-        get4(x + 4, P + i0 * kPRow + 4);
-        const float *v = Vs + ((i0 & 15) * 4 + (i0 >> 4)) * D + cg * 4;
-        get4(y, v);
-        if constexpr (kCols == 8) get4(y + 4, v + 64);
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-#pragma unroll
-          for (int j = 0; j < kCols; j++) o[i][j] = fmaf(x[i], y[j], o[i][j]);
       }
     }
     bool finite = true;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-#pragma unroll
-      for (int d = 1; d < 16; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
-      const int row = warp * 16 + rg * 8 + i;
+      const int row = warp_row + rg * 8 + i;
       const float m_scaled = m[i] * a.scale_log2;
       const int t = row / u.gp, head = u.head0 + row % u.gp;
-      if (t >= u.n_tok) continue;
+      if (t >= u.n_tok || (few && warp > 0)) continue;
       const bool part = u.slot >= 0;
       const float inv = part ? 1.f : (l[i] == 0.f ? 0.f : 1.f / l[i]);
       const long long at = (long long)(u.row0 + t) * a.H + head;
 #pragma unroll
       for (int b = 0; b < kCols; b += 4) {
         const int c = cg * 4 + b * 16;
-        const float4 x = make_float4(o[i][b] * inv, o[i][b + 1] * inv, o[i][b + 2] * inv, o[i][b + 3] * inv);
+        const float4 x = make_float4(out[i][b] * inv, out[i][b + 1] * inv, out[i][b + 2] * inv, out[i][b + 3] * inv);
         if (part) {
           a.part_o[((long long)u.slot * (D / 4) + (c >> 2)) * 64 + row] = x;
         } else {
@@ -411,7 +511,7 @@ AttnLaunch plan_launch(AttnArgs &a, int blocks) {
   // Nothing is cut when every unit fits the smallest grain and gets a block.
   const long long units = attn_most_units<S>(a);
   const int longest = a.kv_lens ? a.max_len : (a.cu ? a.Ttot : a.T);
-  l.split = !(AttnPlan<S>::tiles(longest) <= 1 << kMinGrain && units <= blocks);
+  l.split = !(AttnPlan<S>::tiles(longest) <= 1 << S::kMinGrain && units <= blocks);
   if (!l.split) l.blocks = units < 1 ? 1 : (int)units;
   a.plan_coarse = attn_coarse<S>(units, longest);
   if (a.plan_coarse < 0) {

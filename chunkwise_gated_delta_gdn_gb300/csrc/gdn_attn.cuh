@@ -35,12 +35,38 @@
 
 namespace gdn {
 
+// Two fp32 values in one 64-bit register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Shape of a unit: rows, rows of a packed unit, keys per tile; cost of one tile
-// of an unpacked unit and of that unit's own start and end; the same of a packed
-// one.
-template <int ROWS, int PACK, int TILE, int WIDE, int OVER, int NARROW = 1, int PACKED_OVER = OVER / 2>
+// of a unit and of its start and end; the same of a packed one of at most `FEW`
+// rows; log2 of the smallest grain of a small call.
+template <int ROWS, int PACK, int TILE, int WIDE, int OVER, int NARROW = 1, int PACKED_OVER = OVER / 2,
+          int FEW = PACK, int MIN_GRAIN = 3>
 struct AttnShape {
-  static constexpr int kRows = ROWS, kPack = PACK, kTile = TILE;
+  static constexpr int kRows = ROWS, kPack = PACK, kTile = TILE, kFew = FEW, kMinGrain = MIN_GRAIN;
   static constexpr int kWide = WIDE, kOver = OVER, kNarrow = NARROW, kPackedOver = PACKED_OVER;
 };
 // The bf16 kernel's (gdn_attn_tc.cu).  A packed unit's tile takes 3/4 of an
@@ -50,10 +76,9 @@ struct AttnShape {
 // take two tiles.  An unpacked one's as 0, 1, 2, 4 tiles: four prompts of 2048
 // tokens 295, 160, 152, 160 us, packed prompts 663, 488, 422, 424; a packed one's
 // as 0, 2, 4, 8: 256 sequences of one token 443, 410, 422, 432.
+// Smallest grains of 4, 8 and 16 tiles were alike in all cases measured: below
+// that a piece's start and the joining outweigh its tiles.
 using TcShape = AttnShape<256, 128, 128, 4, 8, 3, 6>;
-// log2 of the smallest grain of a small call (4, 8 and 16 tiles were alike in all
-// cases measured: below this a piece's start and the joining outweigh its tiles)
-constexpr int kMinGrain = 3;
 constexpr int kMaxGrain = 6;   // log2 of the largest one that is tried
 
 struct AttnSeq {
@@ -189,8 +214,10 @@ struct AttnPlan {
     const AttnCost b = (a & up) >> tok_log;
     return x * (a >> grain_log) + floors(b + x, r) - floors(b, r);
   }
-  // a unit's own cost: a packed one has fewer rows to write
-  __host__ __device__ AttnCost own_cost(int nq) const { return packed(nq) ? packed_over : over; }
+  // a sequence whose units have few rows to work on and to write
+  __host__ __device__ bool few(int nq) const { return packed(nq) && nq * G <= S::kFew; }
+  __host__ __device__ AttnCost own_cost(int nq) const { return few(nq) ? packed_over : over; }
+  __host__ __device__ AttnCost weight(int nq) const { return few(nq) ? narrow : wide; }
   // cost of one head group of an unpacked sequence
   __host__ __device__ AttnCost group_cost(int nq, int base) const {
     const int n = token_tiles(nq);
@@ -198,7 +225,7 @@ struct AttnPlan {
   }
   __host__ __device__ AttnCost cost(int nq, int base) const {
     if (nq == 0) return 0;
-    if (packed(nq)) return (AttnCost)HKV * (grains_of(base + nq) * narrow + own_cost(nq));
+    if (packed(nq)) return (AttnCost)HKV * (grains_of(base + nq) * weight(nq) + own_cost(nq));
     return group_cost(nq, base) * groups;
   }
 
@@ -208,7 +235,7 @@ struct AttnPlan {
     u.seq = seq;
     u.len = s.len;
     if (packed(s.nq)) {
-      const AttnCost each = grains_of(s.base + s.nq) * narrow + own_cost(s.nq);
+      const AttnCost each = grains_of(s.base + s.nq) * weight(s.nq) + own_cost(s.nq);
       u.nt = tiles(s.base + s.nq);
       u.kvh = (int)(c / each);
       u.head0 = u.kvh * G;
@@ -263,10 +290,9 @@ struct AttnPlan {
     place(s, group, tile, u);
     return true;
   }
-  __host__ __device__ int weight(const AttnSeq &s) const { return packed(s.nq) ? narrow : wide; }
   // cost of unit u
   __host__ __device__ AttnCost unit_cost(const AttnSeq &s, const AttnUnit &u) const {
-    return own_cost(s.nq) + (AttnCost)((u.nt + (1 << shift) - 1) >> shift) * weight(s);
+    return own_cost(s.nq) + (AttnCost)((u.nt + (1 << shift) - 1) >> shift) * weight(s.nq);
   }
   // first tile at or after cost c of a unit that begins at cost u0
   __host__ __device__ int cut(const AttnSeq &s, AttnCost u0, int nt, AttnCost c) const {
@@ -275,14 +301,14 @@ struct AttnPlan {
     c -= u0;
     // by constants: a call waits for this
     const AttnCost grain = wide == 1 ? c
-                           : packed(s.nq) ? (c + S::kNarrow - 1) / S::kNarrow
+                           : few(s.nq) ? (c + S::kNarrow - 1) / S::kNarrow
                                           : (c + S::kWide - 1) / S::kWide;
     return grain < (AttnCost)((nt + (1 << shift) - 1) >> shift) ? (int)(grain << shift) : nt;
   }
   // last block with a piece of the unit that begins at cost u0
   __host__ __device__ int last_block(const AttnSeq &s, AttnCost u0, int nt) const {
     const AttnCost grains = (nt + (1 << shift) - 1) >> shift;
-    return (int)((u0 + own_cost(s.nq) + (grains - 1) * weight(s)) / per);
+    return (int)((u0 + own_cost(s.nq) + (grains - 1) * weight(s.nq)) / per);
   }
 
   // Chooses; `total()` is the cost of everything under the plan as it stands.
@@ -293,21 +319,21 @@ struct AttnPlan {
     // second unit's start and end
     constexpr int kSlack = 4;
     AttnCost weighted = 0, share = 0;
-    int log = kMinGrain - 1;
+    int log = S::kMinGrain - 1;
     stream(1);
     while (true) {
       const AttnCost t = total();
-      if (log < kMinGrain) {
+      if (log < S::kMinGrain) {
         weighted = t;
         share = (t + n_blocks - 1) / n_blocks;
-        log = kMinGrain;
+        log = S::kMinGrain;
       } else if (t <= (AttnCost)n_blocks) {
         return t;
       } else {
         log++;
       }
       while (log <= kMaxGrain && (2u << log) < share / S::kWide) log++;  // far too many grains
-      if (log > kMaxGrain || (log > kMinGrain && (1u << log) > share / S::kNarrow + kSlack)) break;
+      if (log > kMaxGrain || (log > S::kMinGrain && (1u << log) > share / S::kNarrow + kSlack)) break;
       grains(log);
     }
     stream(share < S::kWide ? S::kWide : share);
