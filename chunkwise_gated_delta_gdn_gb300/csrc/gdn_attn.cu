@@ -98,30 +98,32 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_ke
     if (tid == 0 && u.slot == 2 * (int)blockIdx.x + 1) a.jobs[blockIdx.x] = attn_job(u);
     __syncthreads();  // the previous unit's operands (or the plan's) are read
     const int end = min(u.t1 * 64, max(u.pos0 + u.n_tok, 0));  // behind the last key that anybody sees
-    // a key's row of the tile; a bad page reads as zeros
-    auto row_of = [&](int key, const void *base, long long stride) -> const float * {
-      if (key >= u.len) return nullptr;
-      const float *p = static_cast<const float *>(base);
+    // where a key's row begins; a bad page reads as zeros (-1)
+    auto row_of = [&](int key, long long stride) -> long long {
+      if (key >= u.len) return -1;
       // a prompt's keys are its own tokens
-      if (!a.table) return p + (u.row0 - u.pos0 + key) * stride + u.kvh * D;
+      if (!a.table) return (u.row0 - u.pos0 + key) * stride + u.kvh * D;
       const int index = a.page_log >= 0 ? key >> a.page_log : key / a.page_size;
       const int page = __ldg(a.table + (long long)u.seq * a.max_pages + index);
       if (page < 0 || page >= a.n_pages) {
         if (a.flags) atomicOr(a.flags, kFlagBadSeqlens);
-        return nullptr;
+        return -1;
       }
-      return p + (((long long)page * a.page_size + key - index * a.page_size) * a.HKV + u.kvh) * D;
+      return (((long long)page * a.page_size + key - index * a.page_size) * a.HKV + u.kvh) * D;
     };
     // 64 rows from key0 on into shared memory, on their way while others are
-    // worked on; one group of copies, empty behind the last tile
+    // worked on; one group of copies, empty behind the last tile.  Each lane looks
+    // up two rows, all at once, for the whole warp: looked up for each copy, the
+    // page numbers' latency was most of a decode step.
     auto fetch = [&](int key0, const void *base, long long stride, float *to, int row_floats) {
       if (key0 < end) {
-        constexpr int kRow = D / 4;  // 16-byte pieces
+        constexpr int kRow = D / 4, kStep = kThreads / kRow;  // 16-byte pieces of a row, rows at a time
+        const long long low = row_of(key0 + lane, stride), high = row_of(key0 + 32 + lane, stride);
 #pragma unroll
-        for (int i = tid; i < 64 * kRow; i += kThreads) {
-          const float *from = row_of(key0 + i / kRow, base, stride);
-          copy16(to + (i / kRow) * row_floats + (i % kRow) * 4,
-                 from ? from + (i % kRow) * 4 : static_cast<const float *>(base), from != nullptr);
+        for (int r0 = 0; r0 < 64; r0 += kStep) {
+          const int r = r0 + tid / kRow, c = tid % kRow * 4;
+          const long long at = __shfl_sync(0xffffffffu, r0 < 32 ? low : high, r & 31);
+          copy16(to + r * row_floats + c, static_cast<const float *>(base) + (at < 0 ? 0 : at + c), at >= 0);
         }
       }
       copies_end();
