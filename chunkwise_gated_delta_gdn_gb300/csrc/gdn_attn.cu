@@ -19,21 +19,29 @@ namespace gdn {
 namespace {
 
 // fp32: a unit of 64 rows, 64 keys per step, four warps of 16 rows, both
-// products in fp32 multiply-adds: 146 us for 2 x 1023 tokens, 16 heads of 64; 906
-// for 8192 tokens of 4 heads, 1007 for 4096 tokens of 8 heads of 128.  Products of
-// split operands on the tensor cores (three tf32 ones each, on mma.sync) took as
-// long, and their error at 8192 tokens was 4.7e-6 against 2.5e-6, since those
-// accumulations are cut off and not rounded.
+// products in fp32 multiply-adds: 125 us for 2 x 1023 tokens, 16 heads of 64; 1095
+// for ten prompts of 2199 tokens, 4 heads of 128 (35 and 45 TFLOP/s of 74).
+// Products of split operands on the tensor cores (three tf32 ones each, on
+// mma.sync) took 159 us for the first, and their error at 8192 tokens was 4.7e-6
+// against 2.5e-6, since those accumulations are cut off and not rounded.
 //
-// S = Q K^T: a thread has 8 rows and 4 keys; queries and keys lie transposed in
-// shared memory, so that each step of the contraction is three 16-byte reads
-// for 32 multiply-adds.  The 16 threads of a row are half a warp.  O = P V: the
-// weights go through shared memory (over the keys), and a thread has 8 rows and
-// D / 16 columns.  28 to 38 TFLOP/s of 74, and no unit is full: multiply-adds 46%,
-// shared memory 44%, issue 59%.  Neither two multiply-adds in an instruction
-// (149, 926 and 967 us) nor keys and values copied in the background besides
-// (148, 908, 956) nor other numbers of blocks helped at both widths.
-using WarpShape = AttnShape<64, 64, 64, 1, 1, 1, 0, 16, 0>;
+// S = Q K^T: a thread has 8 rows, as pairs, and 4 keys 16 apart; queries lie
+// transposed in shared memory, keys as they come.  The 16 threads of a row are
+// half a warp.  O = P V: the weights go through shared memory, and a thread has 8
+// rows and D / 16 columns.  The next keys are on their way while a tile's weights
+// are made and used, the next values during its scores.  What is left: 57% of the
+// multiply-adds' clocks are used, and the instructions around them (reads of
+// shared memory, the second copy of a pair's factor) wait for one another; more
+// warps do not fit the registers.  One multiply-add to an instruction: 135 us where
+// pairs took 134, 1243 where they took 1151.  Loops unrolled 2 and 8 fold: 131 and
+// 1095; 4 and 16: these figures; 8 and 32: 127 and 1100.
+//
+// At most 16 rows (a decode step): every warp has them, and 16 of the 64 keys.  32
+// sequences over 8192 keys, 8 heads of 128: 572 us, 3.8 TB/s; one over 300, 16 us.
+// A tile of theirs takes as long as one of 64 rows (both wait for loads): with
+// 1/2 and 1/3 of its cost, chunks among single tokens took 1.5 times as long.  A
+// unit's start and end take half a tile; with 1/4 and a whole one, 1129 and 1095.
+using WarpShape = AttnShape<64, 64, 64, 2, 1, 2, 1, 16, 0>;
 constexpr int kThreads = 128;
 
 template <int D>
@@ -162,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_ke
         {
           uint64_t acc[4][KEYS] = {};  // pairs of rows
           const float *q = Qt + warp_row + rg * 8, *k = Ks + (KEYS == 4 ? cg : warp * 16 + cg) * SM::kKRow;
-#pragma unroll 2
+#pragma unroll 4
           for (int c0 = 0; c0 < D; c0 += 4) {
             float y[KEYS][4];
 #pragma unroll
@@ -221,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_ke
         }
         copies_wait<1>();  // the values
         __syncthreads();
-#pragma unroll 8
+#pragma unroll 16
         for (int j0 = 0; j0 < 16 * KEYS; j0++) {
           uint64_t x[4];
           float y[kCols];
