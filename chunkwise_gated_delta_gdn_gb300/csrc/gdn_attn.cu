@@ -40,8 +40,11 @@ namespace {
 // sequences over 8192 keys, 8 heads of 128: 572 us, 3.8 TB/s; one over 300, 16 us.
 // A tile of theirs takes as long as one of 64 rows (both wait for loads): with
 // 1/2 and 1/3 of its cost, chunks among single tokens took 1.5 times as long.  A
-// unit's start and end take half a tile; with 1/4 and a whole one, 1129 and 1095.
-using WarpShape = AttnShape<64, 64, 64, 2, 1, 2, 1, 16, 0>;
+// unit's start and end take half a tile (with a quarter, ten prompts of 2199
+// tokens 1129 us).  Units of up to two tiles stay whole where each gets a block: a
+// 100-token prompt takes 18 us with its launch, cut and joined 28; one of 200, 39
+// whole and 27 cut.
+using WarpShape = AttnShape<64, 64, 64, 2, 1, 2, 1, 16, 0, 1>;
 constexpr int kThreads = 128;
 
 template <int D>
@@ -94,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_ke
   // weights of key j, rows 4 c .. 4 c + 3: the four chunks of a key are swapped
   // about so that 8 keys' lie in different banks
   auto chunk = [&](int j, int c) { return P + j * 16 + ((c ^ (j >> 1)) & 3) * 4; };
-  AttnPlan<WarpShape> plan(a.H, a.HKV, a.plan_coarse);
+  AttnPlan<WarpShape> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
   AttnStaged *staged = reinterpret_cast<AttnStaged *>(smem);  // until the first operands
   attn_stage(a, staged, blockIdx.x);
   __syncthreads();
@@ -518,10 +521,11 @@ AttnLaunch plan_launch(AttnArgs &a, int blocks) {
   l.blocks = blocks;
   l.rows = S::kRows;
   a.plan_total = 0;
-  // Nothing is cut when every unit fits the smallest grain and gets a block.
+  // Nothing is cut when every unit is short and gets a block.
   const long long units = attn_most_units<S>(a);
   const int longest = a.kv_lens ? a.max_len : (a.cu ? a.Ttot : a.T);
-  l.split = !(AttnPlan<S>::tiles(longest) <= 1 << S::kMinGrain && units <= blocks);
+  l.split = !(AttnPlan<S>::tiles(longest) <= 1 << S::kWhole && units <= blocks);
+  a.plan_least = l.split ? S::kMinGrain : S::kWhole;
   if (!l.split) l.blocks = units < 1 ? 1 : (int)units;
   a.plan_coarse = attn_coarse<S>(units, longest);
   if (a.plan_coarse < 0) {

@@ -62,11 +62,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // Shape of a unit: rows, rows of a packed unit, keys per tile; cost of one tile
 // of a unit and of its start and end; the same of a packed one of at most `FEW`
-// rows; log2 of the smallest grain of a small call.
+// rows; log2 of the smallest grain of a small call, and of the tiles up to which
+// a small call's units stay whole (then it needs no workspace and no joining).
 template <int ROWS, int PACK, int TILE, int WIDE, int OVER, int NARROW = 1, int PACKED_OVER = OVER / 2,
-          int FEW = PACK, int MIN_GRAIN = 3>
+          int FEW = PACK, int MIN_GRAIN = 3, int WHOLE = MIN_GRAIN>
 struct AttnShape {
-  static constexpr int kRows = ROWS, kPack = PACK, kTile = TILE, kFew = FEW, kMinGrain = MIN_GRAIN;
+  static constexpr int kRows = ROWS, kPack = PACK, kTile = TILE, kFew = FEW;
+  static constexpr int kMinGrain = MIN_GRAIN, kWhole = WHOLE;
   static constexpr int kWide = WIDE, kOver = OVER, kNarrow = NARROW, kPackedOver = PACKED_OVER;
 };
 // The bf16 kernel's (gdn_attn_tc.cu).  A packed unit's tile takes 3/4 of an
@@ -153,12 +155,13 @@ struct AttnPlan {
   int G, HKV, groups;
   int gp, tok_log;     // heads and log2 of the tokens of an unpacked unit
   int coarse;          // log2 of the grain of equal shares
+  int least;           // log2 of the smallest other one
   int shift;           // log2 of the grain, in tiles
   int wide, over;      // cost of an unpacked unit's grain, and of the unit
   int narrow, packed_over;  // of a packed one
   AttnCost per;        // cost of a block's range
 
-  __host__ __device__ AttnPlan(int H, int hkv, int coarse_) {
+  __host__ __device__ AttnPlan(int H, int hkv, int coarse_, int least_ = S::kMinGrain) {
     HKV = hkv;
     G = H / hkv;
     gp = G & -G;
@@ -167,6 +170,7 @@ struct AttnPlan {
     while ((gp << tok_log) < S::kRows) tok_log++;
     groups = H / gp;
     coarse = coarse_;
+    least = least_;
     stream(1);
   }
   // equal shares of single tiles / one grain per block
@@ -319,21 +323,21 @@ struct AttnPlan {
     // second unit's start and end
     constexpr int kSlack = 4;
     AttnCost weighted = 0, share = 0;
-    int log = S::kMinGrain - 1;
+    int log = least - 1;
     stream(1);
     while (true) {
       const AttnCost t = total();
-      if (log < S::kMinGrain) {
+      if (log < least) {
         weighted = t;
         share = (t + n_blocks - 1) / n_blocks;
-        log = S::kMinGrain;
+        log = least;
       } else if (t <= (AttnCost)n_blocks) {
         return t;
       } else {
         log++;
       }
       while (log <= kMaxGrain && (2u << log) < share / S::kWide) log++;  // far too many grains
-      if (log > kMaxGrain || (log > S::kMinGrain && (1u << log) > share / S::kNarrow + kSlack)) break;
+      if (log > kMaxGrain || (log > least && (1u << log) > share / S::kNarrow + kSlack)) break;
       grains(log);
     }
     stream(share < S::kWide ? S::kWide : share);
@@ -501,7 +505,7 @@ inline int attn_coarse(long long units, int longest) {
 // whether a unit may be cut between blocks.
 template <class S>
 inline bool attn_plan_prompts(AttnArgs &a, int n_blocks) {
-  AttnPlan<S> plan(a.H, a.HKV, a.plan_coarse);
+  AttnPlan<S> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
   a.plan_total = plan.choose(n_blocks, [&] { return plan.cost(a.T, 0) * a.n_seqs; });
   a.plan_seq = plan.cost(a.T, 0);
   a.plan_per = plan.per;

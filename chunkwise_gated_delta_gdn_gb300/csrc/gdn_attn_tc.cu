@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     if (warp == 18) {
       // -------------------------------------------------------------- plan
-      AttnPlan<TcShape> plan(a.H, a.HKV, a.plan_coarse);
+      AttnPlan<TcShape> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
       const AttnStart st = attn_start(a, plan, staged, blockIdx.x, gridDim.x);
       fence_proxy_async();  // what was staged has been read: the ring may be filled
       __syncwarp();

@@ -139,6 +139,7 @@ struct AttnArgs {
   uint32_t plan_total, plan_per, plan_seq;
   int plan_shift, plan_grains;
   int plan_coarse;             // log2 of the grain of equal shares
+  int plan_least;              // log2 of the smallest other grain
   float4 *part_o;              // partial results (see gdn_attn.cuh)
   float2 *part_ml;
   AttnJob *jobs;         // [blocks] what is to be joined, or nullptr when nothing is cut

@@ -137,7 +137,8 @@ int main() {
     const int blocks = rnd(0, 1) ? rnd(1, 9) : rnd(10, 200), force = rnd(0, 1) ? -1 : rnd(0, 4);
     if (!one<AttnShape<64, 64, 64, 1, 1>>(q, kv, hkv * g, hkv, blocks, force, trial % 3) ||
         !one<AttnShape<256, 128, 128, 2, 4>>(q, kv, hkv * g, hkv, blocks, force, trial % 3) ||
-        !one<TcShape>(q, kv, hkv * g, hkv, blocks, force, trial % 3)) {
+        !one<TcShape>(q, kv, hkv * g, hkv, blocks, force, trial % 3) ||
+        !one<AttnShape<64, 64, 64, 2, 1, 2, 1, 16, 0, 1>>(q, kv, hkv * g, hkv, blocks, force, trial % 3)) {
       std::printf("trial %d: hkv %d g %d blocks %d\n", trial, hkv, g, blocks);
       return 1;
     }
@@ -156,6 +157,61 @@ def test_plan_covers_every_visible_key_once(tmp_path):
     src = tmp_path / "plan.cu"
     src.write_text(PROGRAM)
     exe = tmp_path / "plan"
+    subprocess.run([nvcc, *cuda_build.ARCH, *cuda_build.NVCC_FLAGS,
+                    str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+WHOLE = PROGRAM[:PROGRAM.index("int main() {")] + r"""
+// Calls of short units with a block for each (or more): nothing may be cut, there is no workspace.
+template <class S>
+bool whole(const std::vector<int> &q, const std::vector<int> &kv, int H, int HKV, int spare) {
+  std::vector<int32_t> cu(1, 0), lens(kv.begin(), kv.end());
+  for (int n : q) cu.push_back(cu.back() + n);
+  AttnArgs a{};
+  a.cu = cu.data(); a.kv_lens = lens.data(); a.n_seqs = (int)q.size(); a.Ttot = cu.back();
+  a.H = H; a.HKV = HKV; a.max_len = 1 << 30;
+  const int blocks = (int)attn_most_units<S>(a) + spare;
+  if (blocks < 1) return true;
+  AttnPlan<S> plan(H, HKV, 0, S::kWhole);
+  bool bad;
+  auto sum = [&] {
+    AttnCost total = 0;
+    for (int n = 0; n < a.n_seqs; n++) { const AttnSeq s = attn_seq(a, n, bad); total += plan.cost(s.nq, s.base); }
+    return total;
+  };
+  const AttnCost total = plan.choose(blocks, sum);
+  CHECK(plan.over == 0 && plan.per == 1 && total <= (AttnCost)blocks && 1 << plan.shift >= 1 << S::kWhole);
+  for (int n = 0; n < a.n_seqs; n++) CHECK(plan.grains_of(kv[n] > q[n] ? kv[n] : q[n]) == 1);
+  return true;
+}
+int main() {
+  for (int trial = 0; trial < 3000; trial++) {
+    rnd_state = 11u + 613u * trial;
+    const int hkv = rnd(1, 4), g = rnd(1, 20);
+    std::vector<int> q, kv;
+    for (int n = rnd(1, 12); n > 0; n--) {
+      q.push_back(rnd(0, rnd(0, 1) ? 3 : 128));
+      kv.push_back(rnd(0, 128));
+    }
+    const int spare = rnd(0, 1) ? 0 : rnd(0, 100);
+    if (!whole<TcShape>(q, kv, hkv * g, hkv, spare) ||
+        !whole<AttnShape<64, 64, 64, 2, 1, 2, 1, 16, 0, 1>>(q, kv, hkv * g, hkv, spare)) return 1;
+  }
+  std::printf("ok\n");
+  return 0;
+}
+"""
+
+
+def test_short_units_with_a_block_each_stay_whole(tmp_path):
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("no nvcc")
+    src = tmp_path / "whole.cu"
+    src.write_text(WHOLE)
+    exe = tmp_path / "whole"
     subprocess.run([nvcc, *cuda_build.ARCH, *cuda_build.NVCC_FLAGS,
                     str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
