@@ -22,8 +22,11 @@ namespace {
 // products in fp32 multiply-adds: 125 us for 2 x 1023 tokens, 16 heads of 64; 1095
 // for ten prompts of 2199 tokens, 4 heads of 128 (35 and 45 TFLOP/s of 74).
 // Products of split operands on the tensor cores (three tf32 ones each, on
-// mma.sync) took 159 us for the first, and their error at 8192 tokens was 4.7e-6
-// against 2.5e-6, since those accumulations are cut off and not rounded.
+// mma.sync) took 159 us for the first, with several times the error, since those
+// accumulations are cut off and not rounded.  The error against 64 bits is that
+// of plain 32-bit operations, 6e-7 at 1023 tokens and 1.2e-6 at 8192; sums of 16
+// products and of a tile's keys by themselves would make it 4e-7 (126 and 1106 us;
+// 200-token prompts a tenth slower).
 //
 // S = Q K^T: a thread has 8 rows, as pairs, and 4 keys 16 apart; queries lie
 // transposed in shared memory, keys as they come.  The 16 threads of a row are
@@ -211,8 +214,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_ke
 #pragma unroll
           for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           top = fmaxf(top, m[i]);
-          const float off = top == -CUDART_INF_F ? 0.f : top * a.scale_log2;  // nothing visible yet
-          alpha[i] = exp2_approx(fmaf(m[i], a.scale_log2, -off));
+          // Nothing visible yet: weights 0.  The factor between two maxima is that of
+          // their rounded products, which the weights were made with: from the
+          // unrounded one, errors of 1e-6 in the factor added up with every new
+          // maximum (8192 tokens 2.5e-6 of the result, so 1.2e-6).
+          const float off = top == -CUDART_INF_F ? 0.f : __fmul_rn(top, a.scale_log2);
+          alpha[i] = exp2_approx(__fmul_rn(m[i], a.scale_log2) - off);
           m[i] = top;
           l[i] *= alpha[i];
 #pragma unroll
@@ -287,11 +294,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_ke
 #pragma unroll
           for (int w = 1; w < 4; w++) ml[w] = *reinterpret_cast<const float2 *>(p + w * kNext + D);
           m[i] = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
-          const float off = m[i] == -CUDART_INF_F ? 0.f : m[i] * a.scale_log2;
+          const float off = m[i] == -CUDART_INF_F ? 0.f : __fmul_rn(m[i], a.scale_log2);
           l[i] = 0.f;
 #pragma unroll
           for (int w = 0; w < 4; w++) {
-            const float f = exp2_approx(fmaf(ml[w].x, a.scale_log2, -off));
+            const float f = exp2_approx(__fmul_rn(ml[w].x, a.scale_log2) - off);
             l[i] += f * ml[w].y;
 #pragma unroll
             for (int b = 0; b < kCols; b += 4) {

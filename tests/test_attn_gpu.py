@@ -390,3 +390,21 @@ def test_binding_refuses_what_it_cannot_pass_on():
         call(o=d["q"])
     with pytest.raises(TypeError):
         gdn.gdn_attn_fwd(*(torch.zeros(1, 2, 2, 64, dtype=torch.float16, device="cuda"),) * 3)
+
+
+@pytest.mark.parametrize("T, H, HKV, d", [(2500, 2, 1, 128), (6000, 1, 1, 64)])
+def test_fp32_long_prompt_error(T, H, HKV, d):
+    """The error of a whole fp32 result.  A score is a sum of d products in order: its partial sums
+    are at most about max |s| in size, and each addition rounds by 2^-24 of them, at random, so it
+    is off by about 2^-24 sqrt(d / 3) max|s|, at most 2^-24 * 6.5 * 12 = 4.6e-6 for the scores here
+    in the rare largest, a third of it (1.5e-6) in a typical one; scores off by e, independently,
+    move a result by about e.  T additions of the output round by 2^-24 sqrt(T / 3) = 2.7e-6 at
+    most, on partial sums that are on average half of it.  A factor between two maxima, if it were
+    off by the rounding of a scaled score (2^-24 * 16 = 1e-6), would add as much with each of the
+    ln(T / 64) = 5 new maxima.  2e-6 holds for the first two together, not with the third."""
+    q = normal((1, T, H, d), torch.float32, T, 2.0)
+    k, v = normal((1, T, HKV, d), torch.float32, T + 1), normal((1, T, HKV, d), torch.float32, T + 2)
+    o, _ = gdn.gdn_attn_fwd(q.cuda(), k.cuda(), v.cuda())
+    ref = attn.attention(f64(q)[0], [f64(k)[0]], [f64(v)[0]], [T], d ** -0.5)[0]
+    err = np.linalg.norm(f64(o)[0] - ref) / np.linalg.norm(ref)
+    assert err <= 2e-6, err
