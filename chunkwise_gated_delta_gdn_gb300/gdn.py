@@ -473,10 +473,10 @@ def _given(q, o, lse, flags, workspace, dev) -> None:
 
 def _cache(k_cache, v_cache, block_table, kv_lens, n_seqs, HKV, d, dtype, dev):
     """Check a paged cache; returns (page_size, max_pages, n_pages)."""
-    shape, table = k_cache.shape, block_table.shape
-    if (v_cache.shape == shape and shape[2:] == (HKV, d) and len(table) == 2 and table[0] == n_seqs
-            and kv_lens.shape == (n_seqs,) and k_cache.dtype == dtype and v_cache.dtype == dtype
-            and block_table.dtype == torch.int32 and kv_lens.dtype == torch.int32
+    shape, table, i32 = k_cache.shape, block_table.shape, torch.int32
+    if (v_cache.shape == shape and shape[2] == HKV and shape[3] == d and len(table) == 2
+            and table[0] == n_seqs and kv_lens.shape == (n_seqs,) and k_cache.dtype is dtype
+            and v_cache.dtype is dtype and block_table.dtype is i32 and kv_lens.dtype is i32
             and k_cache.device == dev and v_cache.device == dev and block_table.device == dev
             and kv_lens.device == dev and k_cache.is_contiguous() and v_cache.is_contiguous()
             and block_table.is_contiguous() and kv_lens.is_contiguous()):
@@ -493,31 +493,8 @@ def _cache(k_cache, v_cache, block_table, kv_lens, n_seqs, HKV, d, dtype, dev):
     raise ValueError(f"block_table must be [{n_seqs}, max_pages], kv_lens [{n_seqs}]")
 
 
-def _attn_call(call, workspace_bytes, what, q, o, lse, output_lse, workspace, stream, dev):
-    """Allocate what the caller did not pass and run ``call(o, lse, workspace, its bytes,
-    stream)``.  Buffers allocated here belong to the stream that they are used on.  Small calls
-    need no workspace: it is sized only when the library asks for one."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return _attn_call(call, workspace_bytes, what, q, o, lse, output_lse, workspace, None, dev)
-    if o is None:
-        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=q.dtype, device=dev)
-    if lse is None and output_lse:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
-    raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    out, out_lse = o.data_ptr(), _addr(lse)
-    if workspace is not None:
-        status = call(out, out_lse, workspace.data_ptr(),
-                      workspace.numel() * workspace.element_size(), raw)
-    else:
-        status = call(out, out_lse, None, 0, raw)
-        if status == GDN_ERR_WORKSPACE:
-            nbytes = workspace_bytes()
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            status = call(out, out_lse, workspace.data_ptr(), nbytes, raw)
-    if status != GDN_OK:
-        raise GdnError(status, what)
-    return o, lse
+def _workspace(nbytes: int, dev) -> torch.Tensor:
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
 def gdn_attn_fwd_workspace_bytes(B: int, T: int, H: int, HKV: int, d: int, n_seqs: int,
@@ -539,7 +516,11 @@ def gdn_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     (int32 ``[N + 1]``).  lse ``[B, T, H]`` fp32 is the natural log of the softmax
     denominator (None when not asked).
     """
-    lib = load()
+    if stream is not None:  # what is allocated here belongs to the stream that it is used on
+        with torch.cuda.stream(stream):
+            return gdn_attn_fwd(q, k, v, scale=scale, cu_seqlens=cu_seqlens, o=o, lse=lse,
+                                output_lse=output_lse, flags=flags, workspace=workspace)
+    lib = _lib or load()
     if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape or k.shape[3] != q.shape[3]:
         raise ValueError("q [B, T, H, d] and k, v [B, T, HKV, d]: inconsistent shapes")
     B, T, H, d = q.shape
@@ -553,12 +534,25 @@ def gdn_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
         _given(q, o, lse, flags, workspace, dev)
     if scale is None:
         scale = d ** -0.5
-    return _attn_call(
-        lambda out, out_lse, ws, nbytes, raw: lib.gdn_attn_fwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), out, out_lse, _addr(cu_seqlens), n_seqs, B, T,
-            H, HKV, d, qs, ks, vs, scale, dt, _addr(flags), ws, nbytes, raw),
-        lambda: lib.gdn_attn_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, dt),
-        "gdn_attn_fwd", q, o, lse, output_lse, workspace, stream, dev)
+    if o is None:
+        o = torch.empty_like(q) if qs == H * d else torch.empty(q.shape, dtype=dtype, device=dev)
+    if lse is None and output_lse:
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _addr(lse), _addr(cu_seqlens),
+            n_seqs, B, T, H, HKV, d, qs, ks, vs, scale, dt, _addr(flags))
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    if workspace is not None:
+        status = lib.gdn_attn_fwd(*args, workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), raw)
+    else:  # small calls need none: it is sized only when the library asks for one
+        status = lib.gdn_attn_fwd(*args, None, 0, raw)
+        if status == GDN_ERR_WORKSPACE:
+            nbytes = lib.gdn_attn_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, dt)
+            workspace = _workspace(nbytes, dev)
+            status = lib.gdn_attn_fwd(*args, workspace.data_ptr(), nbytes, raw)
+    if status != GDN_OK:
+        raise GdnError(status, "gdn_attn_fwd")
+    return o, lse
 
 
 def gdn_attn_paged_fwd_workspace_bytes(B: int, T: int, H: int, HKV: int, d: int, n_seqs: int,
@@ -582,7 +576,12 @@ def gdn_attn_paged_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     cu_seqlens; k_cache, v_cache ``[n_pages, page_size, HKV, d]``; block_table int32
     ``[N, max_pages]``; kv_lens int32 ``[N]``, new tokens included.
     """
-    lib = load()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gdn_attn_paged_fwd(q, k_cache, v_cache, block_table, kv_lens, scale=scale,
+                                      cu_seqlens=cu_seqlens, o=o, lse=lse, output_lse=output_lse,
+                                      flags=flags, workspace=workspace)
+    lib = _lib or load()
     if q.dim() != 4 or k_cache.dim() != 4:
         raise ValueError("q must be [B, T, H, d] and the caches [n_pages, page_size, HKV, d]")
     B, T, H, d = q.shape
@@ -596,14 +595,27 @@ def gdn_attn_paged_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         _given(q, o, lse, flags, workspace, dev)
     if scale is None:
         scale = d ** -0.5
-    return _attn_call(
-        lambda out, out_lse, ws, nbytes, raw: lib.gdn_attn_paged_fwd(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-            kv_lens.data_ptr(), out, out_lse, _addr(cu_seqlens), n_seqs, B, T, H, HKV, d, qs,
-            page_size, max_pages, n_pages, scale, dt, _addr(flags), ws, nbytes, raw),
-        lambda: lib.gdn_attn_paged_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, page_size,
-                                                       max_pages, dt),
-        "gdn_attn_paged_fwd", q, o, lse, output_lse, workspace, stream, dev)
+    if o is None:
+        o = torch.empty_like(q) if qs == H * d else torch.empty(q.shape, dtype=dtype, device=dev)
+    if lse is None and output_lse:
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+            kv_lens.data_ptr(), o.data_ptr(), _addr(lse), _addr(cu_seqlens), n_seqs, B, T, H, HKV,
+            d, qs, page_size, max_pages, n_pages, scale, dt, _addr(flags))
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    if workspace is not None:
+        status = lib.gdn_attn_paged_fwd(*args, workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), raw)
+    else:
+        status = lib.gdn_attn_paged_fwd(*args, None, 0, raw)
+        if status == GDN_ERR_WORKSPACE:
+            nbytes = lib.gdn_attn_paged_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, page_size,
+                                                            max_pages, dt)
+            workspace = _workspace(nbytes, dev)
+            status = lib.gdn_attn_paged_fwd(*args, workspace.data_ptr(), nbytes, raw)
+    if status != GDN_OK:
+        raise GdnError(status, "gdn_attn_paged_fwd")
+    return o, lse
 
 
 def gdn_kv_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -613,7 +625,7 @@ def gdn_kv_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
                         stream: Optional[torch.cuda.Stream] = None) -> None:
     """Write the keys and values of new tokens (k, v ``[B, T, HKV, d]`` or packed) into the
     pages, in place; kv_lens counts them already."""
-    lib = load()
+    lib = _lib or load()
     if k.dim() != 4 or v.shape != k.shape or k_cache.dim() != 4:
         raise ValueError("k and v must be [B, T, HKV, d], the caches [n_pages, page_size, HKV, d]")
     B, T, HKV, d = k.shape
