@@ -345,24 +345,32 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_ke
 }
 
 // Joins the pieces of the unit that block b.x of the attention kernel began
-// and did not end, 32 rows per b.y.  Work items are (row, four columns), 32
-// adjacent rows to a warp; each adds its pieces up in the order of the blocks
-// that made them.  With many pieces (a single token over a long cache) and few
-// rows there are more threads than items: they share an item's pieces.
+// and did not end, 32 rows per b.y, or, of many pieces of few rows, a slice of the
+// columns.
+// Work items are (row, four columns), 32 adjacent rows to a warp; each adds its
+// pieces up in the order of the blocks that made them.  With many pieces (a
+// single token over a long cache) and few rows there are more threads than items:
+// they share an item's pieces.
 constexpr int kMergeThreads = 512;
 constexpr int kMergeRows = 32;
 constexpr int kMergeUnroll = 4;
+constexpr int kMergeMany = 16;  // from here on slices of columns pay (131072 keys in 64 pieces 41.5
+                                // -> 35.8 us; 4 sequences of 16384 in 6 pieces each 54.8 -> 57.2)
 template <class S, int D, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const AttnArgs a) {
   __shared__ float weight[kMergeRows], total[kMergeRows];
   __shared__ float4 part[kMergeThreads];
   __shared__ float top[kMergeRows][kMergeThreads / kMergeRows];
-  const int first = blockIdx.x, r0 = blockIdx.y * kMergeRows, tid = threadIdx.x;
+  const int first = blockIdx.x, tid = threadIdx.x;
   // launched while the attention kernel runs; its results are there after this
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const AttnJob job = a.jobs[first];
-  if (r0 >= job.rows) return;
   const int n = job.last - first + 1;  // pieces
+  constexpr int kSlice = D / 4 / (S::kRows / kMergeRows);  // of the columns, in fours
+  const bool sliced = job.rows <= kMergeRows && n > kMergeMany;
+  const int r0 = sliced ? 0 : blockIdx.y * kMergeRows;
+  if (r0 >= job.rows) return;
+  const int c0 = sliced ? blockIdx.y * kSlice : 0, c1 = sliced ? c0 + kSlice : D / 4;
   const int rows = min(job.rows - r0, kMergeRows);
   auto slot = [&](int i) { return (long long)(i == 0 ? 2 * first + 1 : 2 * (first + i)); };
   auto place = [&](int row) {  // of a row's head in the output
@@ -382,7 +390,7 @@ __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const Att
     }
   };
   auto store_lse = [&](int row, float m, float l) {
-    if (a.lse) a.lse[place(row)] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718056f;
+    if (a.lse && c0 == 0) a.lse[place(row)] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718056f;
   };
   // Few pieces (every unit of a call with much work): each thread reads what it
   // needs for its row at once, and none waits for another.  With the phases
@@ -391,8 +399,8 @@ __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const Att
   if (n <= kMergeUnroll) {
     const int row = tid % kMergeRows;
     if (row < rows) {
-#pragma unroll
-      for (int d4 = tid / kMergeRows; d4 < D / 4; d4 += kMergeThreads / kMergeRows) {
+#pragma unroll 2
+      for (int d4 = c0 + tid / kMergeRows; d4 < c1; d4 += kMergeThreads / kMergeRows) {
         float2 ml[kMergeUnroll];
         float4 x[kMergeUnroll];
 #pragma unroll
@@ -454,11 +462,11 @@ __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const Att
   // rows rounded up to a power of two, so that a warp's threads have adjacent rows
   int wide = 1;
   while (wide < rows) wide <<= 1;
-  const int items = wide * (D / 4);
+  const int items = wide * (c1 - c0);
   const int share = items >= kMergeThreads ? 1 : kMergeThreads / items;  // threads to an item
   for (int i0 = 0; i0 < items; i0 += kMergeThreads / share) {
     const int item = i0 + tid % (kMergeThreads / share), who = tid / (kMergeThreads / share);
-    const int row = item % wide, d4 = item / wide;
+    const int row = item % wide, d4 = c0 + item / wide;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < rows) {
       const float base = weight[row];
