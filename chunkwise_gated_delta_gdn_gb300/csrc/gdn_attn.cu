@@ -538,7 +538,10 @@ AttnLaunch plan_launch(AttnArgs &a, int blocks) {
   a.plan_total = 0;
   // Nothing is cut when every unit is short and gets a block.
   const long long units = attn_most_units<S>(a);
-  const int longest = a.kv_lens ? a.max_len : (a.cu ? a.Ttot : a.T);
+  // A sequence's tiles are counted to the position of its last new token as if
+  // its first were at 0 or later: past its keys where it has fewer of them.
+  const int tokens = a.cu ? a.Ttot : a.T;
+  const int longest = a.kv_lens && a.max_len > tokens ? a.max_len : tokens;
   l.split = !(AttnPlan<S>::tiles(longest) <= 1 << S::kWhole && units <= blocks);
   a.plan_least = l.split ? S::kMinGrain : S::kWhole;
   if (!l.split) l.blocks = units < 1 ? 1 : (int)units;

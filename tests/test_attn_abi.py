@@ -173,3 +173,14 @@ def test_query_covers_what_the_call_asks_for(lib):
         assert call(lib.gdn_attn_fwd, a, dict(ws_bytes=need - 1)) == WORKSPACE
     need = gdn.gdn_attn_paged_fwd_workspace_bytes(4, 1, 8, 2, 128, 0, 64, 100, 1)
     assert call(lib.gdn_attn_paged_fwd, PAGED, dict(ws_bytes=need - 1)) == WORKSPACE
+
+
+@pytest.mark.parametrize("dtype, T", [(0, 257), (1, 3000)])
+def test_more_new_tokens_than_the_table_holds(lib, dtype, T):
+    """A table of one page and many new tokens (most see no key): the plan counts tiles up to the
+    last token's position and may cut them, so there has to be a workspace."""
+    assert gdn.gdn_attn_paged_fwd_workspace_bytes(1, T, 8, 8, 128, 0, 16, 1, dtype) > 0
+    assert gdn.gdn_attn_paged_fwd_workspace_bytes(1, T, 8, 8, 128, 1, 16, 1, dtype) > 0
+    kw = dict(B=1, T=T, H=8, HKV=8, page_size=16, max_pages=1, dtype=dtype, ws=None, ws_bytes=0)
+    assert call(lib.gdn_attn_paged_fwd, PAGED, kw) == WORKSPACE
+    assert call(lib.gdn_attn_paged_fwd, PAGED, {**kw, "cu": addr(20), "n_seqs": 1}) == WORKSPACE

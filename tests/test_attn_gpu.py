@@ -408,3 +408,12 @@ def test_fp32_long_prompt_error(T, H, HKV, d):
     ref = attn.attention(f64(q)[0], [f64(k)[0]], [f64(v)[0]], [T], d ** -0.5)[0]
     err = np.linalg.norm(f64(o)[0] - ref) / np.linalg.norm(ref)
     assert err <= 2e-6, err
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("q_lens, kv", [([257], [0]), ([1500, 2], [10, 2]), ([3000], [16])])
+def test_more_new_tokens_than_keys(dtype, q_lens, kv):
+    """Most tokens see no key; the pages hold far fewer positions than there are tokens."""
+    dt, H, HKV, d = DTYPES[dtype], 8, 8, 128
+    x = paged(q_lens, kv, H, HKV, d, 16, dt, seed=sum(q_lens))
+    check_paged(run_paged(x), x, q_lens, d, dt)
