@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_ke
   attn_stage(a, staged, blockIdx.x);
   __syncthreads();
   const AttnStart st = attn_start(a, plan, staged, blockIdx.x, gridDim.x);  // each warp for itself
-  AttnWalk<WarpShape> walk(a, plan, st, blockIdx.x);
+  AttnWalk<WarpShape> walk(a, plan, st, blockIdx.x, gridDim.x);
   AttnUnit u;
   if (a.jobs && tid == 0) a.jobs[blockIdx.x].rows = 0;
   while (walk.next(u)) {
@@ -536,6 +536,7 @@ AttnLaunch plan_launch(AttnArgs &a, int blocks) {
   l.blocks = blocks;
   l.rows = S::kRows;
   a.plan_total = 0;
+  a.plan_whole = 0;
   // Nothing is cut when every unit is short and gets a block.
   const long long units = attn_most_units<S>(a);
   // A sequence's tiles are counted to the position of its last new token as if

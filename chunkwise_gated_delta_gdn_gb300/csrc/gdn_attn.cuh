@@ -21,6 +21,16 @@
 //  * Otherwise grains are single tiles and ranges equal shares of the cost,
 //    whatever the lengths: one long sequence next to many short ones and a
 //    causal triangle fill the GPU alike.
+//  * bf16 prompts with enough units (equal ones, or up to 32 packed) are dealt
+//    whole, the longest first, to the blocks back and forth: two rounds in a row
+//    add up to about the same for all, and the last, unpaired one is of the
+//    shortest.  Cutting and joining costs about 16 us (kCut), so a longest block
+//    that takes up to that much more than an equal share is no loss: four prompts
+//    of 2048 tokens took 145 us cut, 124 whole; 16 of 512 tokens 87 and 64; one of
+//    4096 tokens, 16 heads (1.7 units for each block) 80 and 63; one of 16384, 4
+//    heads (1.7, the longest 520 of a share of 448) 209 and 220, and stays cut; 12001
+//    packed tokens 409 and 386.  In fp32 shares come out as fast or faster (10 x 2199
+//    tokens 1100 and 1108 us).  The units of a decode step are too much alike.
 // A unit cut by a range's border leaves partial results (unnormalised output,
 // row maximum and sum) that the merge kernel joins in the order of the blocks,
 // so results do not depend on timing.  The plan depends on lengths that only
@@ -63,12 +73,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // Shape of a unit: rows, rows of a packed unit, keys per tile; cost of one tile
 // of a unit and of its start and end; the same of a packed one of at most `FEW`
 // rows; log2 of the smallest grain of a small call, and of the tiles up to which
-// a small call's units stay whole (then it needs no workspace and no joining).
+// a small call's units stay whole (then it needs no workspace and no joining);
+// what cutting and joining costs a block (0: prompts are not dealt whole).
 template <int ROWS, int PACK, int TILE, int WIDE, int OVER, int NARROW = 1, int PACKED_OVER = OVER / 2,
-          int FEW = PACK, int MIN_GRAIN = 3, int WHOLE = MIN_GRAIN>
+          int FEW = PACK, int MIN_GRAIN = 3, int WHOLE = MIN_GRAIN, int CUT = 0>
 struct AttnShape {
   static constexpr int kRows = ROWS, kPack = PACK, kTile = TILE, kFew = FEW;
-  static constexpr int kMinGrain = MIN_GRAIN, kWhole = WHOLE;
+  static constexpr int kMinGrain = MIN_GRAIN, kWhole = WHOLE, kCut = CUT;
   static constexpr int kWide = WIDE, kOver = OVER, kNarrow = NARROW, kPackedOver = PACKED_OVER;
 };
 // The bf16 kernel's (gdn_attn_tc.cu).  A packed unit's tile takes 3/4 of an
@@ -80,7 +91,7 @@ struct AttnShape {
 // as 0, 2, 4, 8: 256 sequences of one token 443, 410, 422, 432.
 // Smallest grains of 4, 8 and 16 tiles were alike in all cases measured: below
 // that a piece's start and the joining outweigh its tiles.
-using TcShape = AttnShape<256, 128, 128, 4, 8, 3, 6>;
+using TcShape = AttnShape<256, 128, 128, 4, 8, 3, 6, 128, 3, 3, 40>;
 constexpr int kMaxGrain = 6;   // log2 of the largest one that is tried
 
 struct AttnSeq {
@@ -160,6 +171,7 @@ struct AttnPlan {
   int wide, over;      // cost of an unpacked unit's grain, and of the unit
   int narrow, packed_over;  // of a packed one
   AttnCost per;        // cost of a block's range
+  bool whole = false;  // packed prompts' units are dealt whole
 
   __host__ __device__ AttnPlan(int H, int hkv, int coarse_, int least_ = S::kMinGrain) {
     HKV = hkv;
@@ -267,6 +279,29 @@ struct AttnPlan {
     }
     place(s, group, lo, u);
     return group * per_group + at;
+  }
+  // token tiles of an unpacked sequence with less than t key tiles
+  __host__ __device__ int shorter(int nq, int base, int t) const {
+    const int n = token_tiles(nq), room = (t - 1) * S::kTile - base;
+    if (nq <= room) return n;
+    return room <= 0 ? 0 : (room >> tok_log < n - 1 ? room >> tok_log : n - 1);
+  }
+  // units of a sequence with t key tiles or more
+  __host__ __device__ int units_from(int nq, int base, int t) const {
+    if (nq == 0) return 0;
+    if (packed(nq)) return tiles(base + nq) >= t ? HKV : 0;
+    return (token_tiles(nq) - shorter(nq, base, t)) * groups;
+  }
+  // unit r of those of sequence s with t key tiles
+  __host__ __device__ void pick(const AttnSeq &s, int t, int r, AttnUnit &u) const {
+    if (!packed(s.nq)) return place(s, r % groups, shorter(s.nq, s.base, t) + r / groups, u);
+    u.nt = t;
+    u.kvh = r;
+    u.head0 = r * G;
+    u.gp = G;
+    u.row0 = s.q0;
+    u.n_tok = s.nq;
+    u.pos0 = s.past;
   }
   // token tile `tile` of head group `group` of an unpacked sequence
   __host__ __device__ void place(const AttnSeq &s, int group, int tile, AttnUnit &u) const {
@@ -407,6 +442,14 @@ __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &
     for (int n = lane; n < a.n_seqs; n += 32) mine += cost_of(n);
     return __reduce_add_sync(kAll, mine);
   });
+  if (S::kCut != 0 && !a.kv_lens && a.n_seqs <= 32 && plan.over != 0) {
+    const int nq = lane < a.n_seqs ? staged[lane].nq : 0;
+    const int units = __reduce_add_sync(kAll, plan.units_from(nq, 0, 1));
+    const AttnCost longest =
+        __reduce_max_sync(kAll, nq ? plan.grains_of(nq) * plan.weight(nq) + plan.own_cost(nq) : 0u);
+    plan.whole = units >= 2 * n_blocks && longest <= plan.per + S::kCut;
+    if (plan.whole) return r;
+  }
   const AttnCost c = block * plan.per;
   if (c >= r.total) return r;
   AttnCost before = 0;
@@ -442,17 +485,64 @@ struct AttnWalk {
   AttnCost at, end, u0;  // start and end of the range, start of the sequence or unit
   int seq, block;
   bool fresh;            // the sequence is still to be looked up
+  int blocks, round;     // units dealt whole
+  AttnSeq mine;          // of packed prompts: lane i has sequence i
 
   __host__ __device__ AttnWalk(const AttnArgs &a_, const AttnPlan<S> &p_, const AttnStart &st,
-                               int block_)
-      : a(a_), plan(p_), block(block_) {
+                               int block_, int blocks_ = 0)
+      : a(a_), plan(p_), block(block_), blocks(blocks_), round(0) {
     at = block * plan.per;
     end = at + plan.per < st.total ? at + plan.per : st.total;
     seq = st.seq;
     u0 = st.seq0;
     fresh = true;
+#ifdef __CUDA_ARCH__
+    if (S::kCut != 0 && plan.whole) {
+      bool bad;
+      mine.nq = mine.base = 0;
+      if ((threadIdx.x & 31) < a.n_seqs) mine = attn_seq(a, threadIdx.x & 31, bad);
+    }
+#endif
   }
+  // place of this block's next unit among those that are dealt whole
+  __host__ __device__ int turn() {
+    const int r = round++;
+    return r * blocks + (r & 1 ? blocks - 1 - block : block);
+  }
+#ifdef __CUDA_ARCH__
+  // unit i of packed prompts in order of length; all lanes of a warp
+  __device__ bool deal(int i, AttnUnit &out) const {
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    auto from = [&](int t) { return __reduce_add_sync(kAll, plan.units_from(mine.nq, mine.base, t)); };
+    if (i >= from(1)) return false;
+    int lo = 1, hi = __reduce_max_sync(kAll, plan.tiles(mine.base + mine.nq));
+    while (lo < hi) {  // the most tiles that more than i units have
+      const int mid = (lo + hi + 1) >> 1;
+      if (from(mid) > i) lo = mid; else hi = mid - 1;
+    }
+    i -= from(lo + 1);
+    const int have = plan.units_from(mine.nq, mine.base, lo) - plan.units_from(mine.nq, mine.base, lo + 1);
+    int upto = have;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(kAll, upto, d);
+      if (lane >= d) upto += up;
+    }
+    const int who = __ffs(__ballot_sync(kAll, i < upto)) - 1;
+    i -= __shfl_sync(kAll, upto - have, who);
+    bool bad;
+    const AttnSeq one = attn_seq(a, who, bad);
+    plan.pick(one, lo, i, out);
+    out.seq = who;
+    out.len = one.len;
+    return true;
+  }
+#endif
   __host__ __device__ bool next(AttnUnit &out) {
+    if constexpr (S::kCut != 0) {
+      if (plan.whole || a.plan_whole) return next_whole(out);
+    }
     while (seq < a.n_seqs && u0 < end) {
       if (fresh) {
         bool bad;
@@ -477,6 +567,28 @@ struct AttnWalk {
       if (out.t0 < out.t1) return true;
     }
     return false;
+  }
+  __host__ __device__ bool next_whole(AttnUnit &out) {
+#ifdef __CUDA_ARCH__
+    if (plan.whole) {
+      if (!deal(turn(), out)) return false;
+    } else
+#endif
+    {
+      const int all = a.n_seqs * plan.groups, i = turn();
+      const int tile = plan.token_tiles(a.T) - 1 - i / all;
+      if (tile < 0) return false;
+      bool bad;
+      out.seq = i % all / plan.groups;
+      const AttnSeq one = attn_seq(a, out.seq, bad);
+      plan.place(one, i % plan.groups, tile, out);
+      out.len = one.len;
+    }
+    out.t0 = 0;
+    out.t1 = out.nt;
+    out.slot = -1;
+    out.last = block;
+    return true;
   }
 };
 
@@ -511,6 +623,22 @@ inline bool attn_plan_prompts(AttnArgs &a, int n_blocks) {
   a.plan_per = plan.per;
   a.plan_shift = plan.shift;
   a.plan_grains = plan.over == 0;
+  const int all = a.n_seqs * plan.groups;
+  const long long units = (long long)all * plan.token_tiles(a.T);
+  a.plan_whole = S::kCut != 0 && !a.plan_grains && !plan.packed(a.T) && units >= n_blocks &&
+                 units < INT32_MAX / 2;
+  // the block with the most to do; with many units each they are all alike
+  for (int b = 0; a.plan_whole && units < 4LL * n_blocks && b < n_blocks; b++) {
+    AttnCost load = 0;
+    for (int r = 0; r < 4; r++) {
+      const int tile = plan.token_tiles(a.T) - 1 - (r * n_blocks + (r & 1 ? n_blocks - 1 - b : b)) / all;
+      if (tile < 0) break;
+      const int tokens = (tile + 1) << plan.tok_log;
+      load += plan.tiles(tokens < a.T ? tokens : a.T) * plan.wide + plan.over;
+    }
+    a.plan_whole = load <= plan.per + S::kCut;
+  }
+  if (a.plan_whole) return false;
   return !(a.plan_grains && plan.tiles(a.T) <= 1 << plan.shift);
 }
 

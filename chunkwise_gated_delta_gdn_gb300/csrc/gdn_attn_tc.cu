@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const AttnStart st = attn_start(a, plan, staged, blockIdx.x, gridDim.x);
       fence_proxy_async();  // what was staged has been read: the ring may be filled
       __syncwarp();
-      AttnWalk<TcShape> walk(a, plan, st, blockIdx.x);
+      AttnWalk<TcShape> walk(a, plan, st, blockIdx.x, gridDim.x);
       Ring<kUnits> at;
       AttnUnit u;
       bool more = true;

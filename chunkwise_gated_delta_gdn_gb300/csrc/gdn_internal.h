@@ -138,6 +138,7 @@ struct AttnArgs {
   // plan_total = 0 otherwise
   uint32_t plan_total, plan_per, plan_seq;
   int plan_shift, plan_grains;
+  int plan_whole;              // units are dealt whole
   int plan_coarse;             // log2 of the grain of equal shares
   int plan_least;              // log2 of the smallest other grain
   float4 *part_o;              // partial results (see gdn_attn.cuh)

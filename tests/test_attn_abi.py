@@ -25,10 +25,10 @@ def lib():
     return gdn.load()
 
 
-# Long enough that units are cut between blocks: only then is a workspace asked for.
 PROMPT = dict(q=addr(0), k=addr(1), v=addr(2), o=addr(3), lse=addr(4), cu=None, n_seqs=0, B=2,
               T=20000, H=8, HKV=2, d=128, q_stride=1024, k_stride=256, v_stride=256, scale=0.088,
               dtype=1, flags=addr(5), ws=addr(6), ws_bytes=1 << 32)
+CUT = dict(H=2, T=5000)  # few and long units, cut between blocks: only then is a workspace asked for
 PAGED = dict(q=addr(0), k_cache=addr(1), v_cache=addr(2), table=addr(3), kv_lens=addr(4),
              o=addr(5), lse=addr(6), cu=None, n_seqs=0, B=4, T=1, H=8, HKV=2, d=128, q_stride=1024,
              page_size=64, max_pages=100, n_pages=500, scale=0.088, dtype=1, flags=addr(7),
@@ -89,14 +89,14 @@ def call(entry, base, kw):
     (dict(q_stride=1016), ARG),                  # less than a token
     (dict(k_stride=260), ARG),                   # not a multiple of 16 bytes
     (dict(v_stride=1 << 32), ARG),
-    (dict(ws=None), WORKSPACE),
-    (dict(ws_bytes=1000), WORKSPACE),
+    (dict(ws=None, **CUT), WORKSPACE),
+    (dict(ws_bytes=1000, **CUT), WORKSPACE),
     (dict(ws=addr(6, 16)), ARG),
     (dict(o=addr(0)), ARG),                      # output over an input
     (dict(o=addr(2, 256)), ARG),
     (dict(lse=addr(3, 1024)), ARG),              # output over an output
-    (dict(ws=addr(1)), ARG),
-    (dict(flags=addr(6)), ARG),                  # status word inside the workspace
+    (dict(ws=addr(1), **CUT), ARG),
+    (dict(flags=addr(6), **CUT), ARG),           # status word inside the workspace
 ], ids=str)
 def test_prompt_refusals(lib, kw, status):
     assert call(lib.gdn_attn_fwd, PROMPT, kw) == status
@@ -145,26 +145,29 @@ def test_workspace_queries(lib):
     # per block: 152 blocks of bf16, 2 or 3 per processor in fp32 (also where no GPU is present)
     for d in (64, 128):
         part = 2 * 256 * (d + 2) * 4 + 32
-        assert prompt(4, 2048, 32, 8, d, 0, gdn.GDN_BF16) % part == 0
-        assert prompt(4, 2048, 32, 8, d, 0, gdn.GDN_BF16) > 0
+        for need in (prompt(1, 8192, 32, 8, d, 4, gdn.GDN_BF16), prompt(1, 20000, 1, 1, d, 0, gdn.GDN_BF16),
+                     prompt(2, 5000, 2, 2, d, 0, gdn.GDN_BF16)):
+            assert need % part == 0 and need > 0
         part = 2 * 64 * (d + 2) * 4 + 32
         assert prompt(4, 2048, 32, 8, d, 0, gdn.GDN_F32) % part == 0
     assert paged(256, 1, 32, 8, 128, 0, 64, 64, gdn.GDN_BF16) > 0
     # nothing can be cut, so nothing is stored: few short prompts, short caches
     assert prompt(1, 33, 16, 2, 128, 0, gdn.GDN_BF16) == 0
     assert paged(1, 1, 16, 2, 128, 0, 16, 20, gdn.GDN_BF16) == 0
+    # equal prompts with enough units for each block: dealt whole
+    assert prompt(4, 2048, 32, 8, 128, 0, gdn.GDN_BF16) == 0
     # what the entry points refuse needs nothing
     assert prompt(1, 4096, 16, 3, 128, 0, gdn.GDN_BF16) == 0
     assert prompt(1, 4096, 16, 2, 96, 0, gdn.GDN_BF16) == 0
     assert paged(1, 1, 16, 2, 128, 0, 24, 4096, gdn.GDN_BF16) == 0
     # a few more sequences never need less: blocks have the same parts whatever they hold
-    assert prompt(1, 32768, 16, 2, 128, 0, 1) == prompt(4, 2048, 32, 8, 128, 0, 1)
+    assert prompt(1, 32768, 16, 2, 128, 0, 1) == prompt(1, 8192, 32, 8, 128, 4, 1)
 
 
 def test_query_covers_what_the_call_asks_for(lib):
     """One byte less than the query's answer is refused for the same shape, unless the query had
     to cover another form of it (one sequence, with and without cu_seqlens)."""
-    for kw in (dict(), dict(T=5170, d=64), dict(dtype=0, T=3000), dict(B=70, T=1024)):
+    for kw in (CUT, dict(T=5170, d=64, **{"H": 2}), dict(dtype=0, T=3000), dict(dtype=0, B=70, T=1024)):
         a = {**PROMPT, **kw}
         a.update(q_stride=a["H"] * a["d"], k_stride=a["HKV"] * a["d"], v_stride=a["HKV"] * a["d"])
         need = gdn.gdn_attn_fwd_workspace_bytes(a["B"], a["T"], a["H"], a["HKV"], a["d"], 0,

@@ -216,3 +216,115 @@ def test_short_units_with_a_block_each_stay_whole(tmp_path):
                     str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+DEAL = PROGRAM[:PROGRAM.index("int main() {")] + r"""
+// Prompts whose units are dealt whole: every (row, head) in one unit with all of its keys, the
+// units in order of length, and (equal prompts) every unit to one block.
+template <class S>
+bool covered(const std::vector<AttnUnit> &units, const std::vector<int> &q, int H, const AttnPlan<S> &plan) {
+  std::set<std::pair<int, int>> rows;
+  std::vector<int> at(1, 0);
+  for (int n : q) at.push_back(at.back() + n);
+  for (const AttnUnit &u : units) {
+    CHECK(u.seq >= 0 && u.seq < (int)q.size() && u.len == q[u.seq] && u.kvh == u.head0 / plan.G);
+    CHECK(u.n_tok > 0 && u.n_tok * u.gp <= S::kRows && u.row0 >= at[u.seq] && u.row0 + u.n_tok <= at[u.seq + 1]);
+    CHECK(u.pos0 == u.row0 - at[u.seq] && u.nt == AttnPlan<S>::tiles(u.pos0 + u.n_tok));
+    for (int t = 0; t < u.n_tok; t++)
+      for (int g = 0; g < u.gp; g++) CHECK(rows.insert({u.row0 + t, u.head0 + g}).second);
+  }
+  CHECK((long long)rows.size() == (long long)at.back() * H);
+  return true;
+}
+template <class S>
+bool ragged(const std::vector<int> &q, int H, int HKV) {
+  std::vector<int32_t> cu(1, 0);
+  for (int n : q) cu.push_back(cu.back() + n);
+  AttnArgs a{};
+  a.cu = cu.data(); a.n_seqs = (int)q.size(); a.Ttot = cu.back(); a.H = H; a.HKV = HKV;
+  const AttnPlan<S> plan(H, HKV, 0);
+  auto from = [&](int t) {
+    int n = 0;
+    for (int x : q) n += plan.units_from(x, 0, t);
+    return n;
+  };
+  std::vector<AttnUnit> units;
+  int longest = 1 << 30;
+  for (int i = 0; i < from(1); i++) {
+    int t = 1;
+    while (from(t + 1) > i) t++;
+    int r = i - from(t + 1), who = 0;
+    for (; who < (int)q.size(); who++) {
+      const int have = plan.units_from(q[who], 0, t) - plan.units_from(q[who], 0, t + 1);
+      if (r < have) break;
+      r -= have;
+    }
+    CHECK(who < (int)q.size());
+    bool bad;
+    AttnUnit u;
+    const AttnSeq s = attn_seq(a, who, bad);
+    plan.pick(s, t, r, u);
+    u.seq = who; u.len = s.len;
+    CHECK(u.nt == t && t <= longest);
+    longest = t;
+    units.push_back(u);
+  }
+  return covered<S>(units, q, H, plan);
+}
+template <class S>
+bool equal(int n, int T, int H, int HKV, int blocks) {
+  AttnArgs a{};
+  a.n_seqs = n; a.T = T; a.Ttot = n * T; a.H = H; a.HKV = HKV; a.plan_least = S::kMinGrain;
+  if (attn_plan_prompts<S>(a, blocks) || !a.plan_whole) return true;
+  const AttnPlan<S> plan(H, HKV, 0);
+  std::vector<AttnUnit> units;
+  long long most = 0, total = 0;
+  for (int b = 0; b < blocks; b++) {
+    AttnStart st{};
+    st.seq = n;
+    AttnWalk<S> walk(a, plan, st, b, blocks);
+    AttnUnit u;
+    long long load = 0;
+    while (walk.next(u)) {
+      CHECK(u.t0 == 0 && u.t1 == u.nt && u.slot == -1);
+      load += u.nt;
+      units.push_back(u);
+    }
+    most = load > most ? load : most;
+    total += load;
+  }
+  grains_chosen++;
+  // two rounds in a row differ by no more than neighbouring lengths, the last one is short
+  const long long longest = plan.tiles(T);
+  CHECK(most <= total / blocks + longest + (long long)units.size() / blocks + 2);
+  return covered<S>(units, std::vector<int>(n, T), H, plan);
+}
+int main() {
+  for (int trial = 0; trial < 400; trial++) {
+    rnd_state = 5u + 811u * trial;
+    const int hkv = rnd(1, 4), g = rnd(1, 4) == 1 ? rnd(1, 20) : 1 << rnd(0, 4);
+    std::vector<int> q;
+    for (int n = rnd(1, 12); n > 0; n--) q.push_back(rnd(0, 5) == 0 ? 0 : rnd(1, rnd(0, 1) ? 9 : 900));
+    using F = AttnShape<64, 64, 64, 2, 1, 2, 1, 16, 0, 1, 40>;
+    if (!ragged<TcShape>(q, hkv * g, hkv) || !ragged<F>(q, hkv * g, hkv)) return 1;
+    const int n = rnd(1, 6), T = rnd(1, rnd(0, 1) ? 200 : 3000), blocks = rnd(1, 60);
+    if (!equal<TcShape>(n, T, hkv * g, hkv, blocks) || !equal<F>(n, T, hkv * g, hkv, blocks)) return 1;
+  }
+  if (grains_chosen < 50) { std::printf("dealt %d times\n", grains_chosen); return 1; }
+  std::printf("ok\n");
+  return 0;
+}
+"""
+
+
+def test_units_dealt_whole_cover_every_row_once(tmp_path):
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("no nvcc")
+    src = tmp_path / "deal.cu"
+    src.write_text(DEAL)
+    exe = tmp_path / "deal"
+    subprocess.run([nvcc, *cuda_build.ARCH, *cuda_build.NVCC_FLAGS,
+                    str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
