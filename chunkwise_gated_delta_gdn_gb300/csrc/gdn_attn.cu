@@ -394,8 +394,8 @@ __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const Att
   };
   // Few pieces (every unit of a call with much work): each thread reads what it
   // needs for its row at once, and none waits for another.  With the phases
-  // below for these too, four prompts of 2048 tokens took 152 us, this 145; two
-  // of 1023 in fp32 152 and 146.
+  // below for these too, four prompts of 2048 tokens took 152 us cut, and 145 so;
+  // two of 1023 in fp32 152 and 146.
   if (n <= kMergeUnroll) {
     const int row = tid % kMergeRows;
     if (row < rows) {

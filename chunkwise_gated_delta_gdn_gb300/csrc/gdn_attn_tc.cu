@@ -28,7 +28,8 @@
 // would hide it, does not fit tensor memory beside two outputs of 128 columns.  A
 // unit's start and end take 10000 clocks beside its tiles, most of it for the
 // 64 KB of its rows to leave the processor.  32768 tokens of 16 heads of 128:
-// 2960 us, 1485 TFLOP/s; four of 2048 tokens, 32 heads: 144 us, 955 TFLOP/s.
+// 2860 to 2930 us, 1500 to 1540 TFLOP/s; four of 2048 tokens, 32 heads: 125 us,
+// 1100 TFLOP/s.
 // One token per sequence: memory where heads are 128 wide (64 sequences over 8192
 // keys 335 us, 6.4 TB/s), the chain of products and barriers, 2000 clocks a tile,
 // where they are 64 wide (130 us for 32 sequences, 4.1 TB/s).  A call's start, plan
