@@ -17,7 +17,7 @@
 // i of the grid takes the range [i per, (i+1) per).
 //  * A call with little work takes the smallest grain at which there are no
 //    more grains than blocks, and each block one grain: nothing waits behind
-//    another unit, and no piece is smaller than kMinGrain tiles.
+//    another unit, and no piece is smaller than 2^kMinGrain tiles.
 //  * Otherwise grains are single tiles and ranges equal shares of the cost,
 //    whatever the lengths: one long sequence next to many short ones and a
 //    causal triangle fill the GPU alike.
