@@ -59,6 +59,7 @@ struct WarpSmem {
   static constexpr int kP = kV + 64 * D;      // [warp][64 keys][16 rows]
   static constexpr int kBytes = (kP + 4 * 64 * 16) * 4;
 };
+static_assert(kStaged * sizeof(AttnStaged) + kThreads * sizeof(AttnChunk) <= WarpSmem<64>::kBytes, "staging");
 template <int D>
 constexpr int blocks_per_sm() { return D == 64 ? 3 : 2; }
 
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_ke
   auto chunk = [&](int j, int c) { return P + j * 16 + ((c ^ (j >> 1)) & 3) * 4; };
   AttnPlan<WarpShape> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
   AttnStaged *staged = reinterpret_cast<AttnStaged *>(smem);  // until the first operands
-  attn_stage(a, staged, blockIdx.x);
+  attn_stage<kThreads>(a, staged, blockIdx.x);
   __syncthreads();
   const AttnStart st = attn_start(a, plan, staged, blockIdx.x, gridDim.x);  // each warp for itself
   AttnWalk<WarpShape> walk(a, plan, st, blockIdx.x, gridDim.x);
@@ -530,31 +531,6 @@ cudaError_t launch(const AttnArgs &a, int blocks, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <class S>
-AttnLaunch plan_launch(AttnArgs &a, int blocks) {
-  AttnLaunch l;
-  l.blocks = blocks;
-  l.rows = S::kRows;
-  a.plan_total = 0;
-  a.plan_whole = 0;
-  // Nothing is cut when every unit is short and gets a block.
-  const long long units = attn_most_units<S>(a);
-  // A sequence's tiles are counted to the position of its last new token as if
-  // its first were at 0 or later: past its keys where it has fewer of them.
-  const int tokens = a.cu ? a.Ttot : a.T;
-  const int longest = a.kv_lens && a.max_len > tokens ? a.max_len : tokens;
-  l.split = !(AttnPlan<S>::tiles(longest) <= 1 << S::kWhole && units <= blocks);
-  a.plan_least = l.split ? S::kMinGrain : S::kWhole;
-  if (!l.split) l.blocks = units < 1 ? 1 : (int)units;
-  a.plan_coarse = attn_coarse<S>(units, longest);
-  if (a.plan_coarse < 0) {
-    l.blocks = 0;
-    return l;
-  }
-  if (!a.cu && !a.kv_lens && a.T > 0) l.split = attn_plan_prompts<S>(a, l.blocks);
-  return l;
-}
-
 }  // namespace
 
 int sm_count() {
@@ -583,8 +559,8 @@ cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &don
 }
 
 AttnLaunch attn_launch(AttnArgs &a, int d, int dtype) {
-  return dtype ? plan_launch<TcShape>(a, sm_count())
-               : plan_launch<WarpShape>(a, sm_count() * (d == 64 ? blocks_per_sm<64>() : blocks_per_sm<128>()));
+  return dtype ? attn_plan_launch<TcShape>(a, sm_count())
+               : attn_plan_launch<WarpShape>(a, sm_count() * (d == 64 ? blocks_per_sm<64>() : blocks_per_sm<128>()));
 }
 
 cudaError_t launch_attn(const AttnArgs &a, int d, int dtype, const AttnLaunch &l,

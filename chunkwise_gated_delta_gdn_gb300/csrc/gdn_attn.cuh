@@ -380,6 +380,76 @@ struct AttnPlan {
   }
 };
 
+// The 32 lanes of the warp that makes the plan; `f(lane)` is what a lane has.  In
+// a kernel this thread is one of them; on the host, where the plan is tested, they
+// are gone through in order.
+struct AttnLanes {
+#ifdef __CUDA_ARCH__
+  static constexpr int kHere = 1;  // lanes whose values a thread keeps
+#else
+  static constexpr int kHere = 32;
+#endif
+  // calls f(lane, place of its values among those kept here)
+  template <class F>
+  __host__ __device__ static void each(F f) {
+#ifdef __CUDA_ARCH__
+    f((int)(threadIdx.x & 31), 0);
+#else
+    for (int lane = 0; lane < 32; lane++) f(lane, lane);
+#endif
+  }
+  template <class F>
+  __host__ __device__ static uint32_t sum(F f) {
+#ifdef __CUDA_ARCH__
+    return __reduce_add_sync(0xffffffffu, (uint32_t)f((int)(threadIdx.x & 31)));
+#else
+    uint32_t r = 0;
+    for (int lane = 0; lane < 32; lane++) r += f(lane);
+    return r;
+#endif
+  }
+  template <class F>
+  __host__ __device__ static uint32_t max(F f) {
+#ifdef __CUDA_ARCH__
+    return __reduce_max_sync(0xffffffffu, (uint32_t)f((int)(threadIdx.x & 31)));
+#else
+    uint32_t r = 0;
+    for (int lane = 0; lane < 32; lane++) {
+      const uint32_t x = f(lane);
+      r = x > r ? x : r;
+    }
+    return r;
+#endif
+  }
+  // The lane that x falls into when their values are laid end to end, -1 when it
+  // is past them; `before`: the values before that lane, or all of them.
+  template <class F>
+  __host__ __device__ static int holder(F f, uint32_t x, uint32_t &before) {
+#ifdef __CUDA_ARCH__
+    const int lane = threadIdx.x & 31;
+    const uint32_t mine = f(lane);
+    uint32_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += up;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, x >= incl - mine && x < incl);
+    const int who = hit ? __ffs(hit) - 1 : -1;
+    before = __shfl_sync(0xffffffffu, hit ? incl - mine : incl, hit ? who : 31);
+    return who;
+#else
+    before = 0;
+    for (int lane = 0; lane < 32; lane++) {
+      const uint32_t mine = f(lane);
+      if (x < before + mine) return lane;
+      before += mine;
+    }
+    return -1;
+#endif
+  }
+};
+
 // What a block needs to start: the cost of everything and the sequence its
 // first cost falls into.
 struct AttnStart {
@@ -394,28 +464,89 @@ constexpr int kStaged = 4096;
 struct AttnStaged {
   int nq, base;
 };
-// All THREADS threads of a block (which then synchronise); block 0 reports
-// malformed lengths.
-__device__ __forceinline__ void attn_stage(const AttnArgs &a, AttnStaged *staged, int block) {
-  if (a.plan_total) return;
-  bool any_bad = threadIdx.x == 0 && a.cu && (a.cu[0] != 0 || a.cu[a.n_seqs] != a.Ttot);
-  for (int n = threadIdx.x; n < a.n_seqs; n += blockDim.x) {
+// Thread `first` of `step` of a block (which then synchronise); returns whether it
+// has seen malformed lengths.  `all`: look at every sequence's also where nothing
+// but the flag depends on them.
+__host__ __device__ __forceinline__ bool attn_stage(const AttnArgs &a, AttnStaged *staged, int first,
+                                                    int step, bool all) {
+  bool any_bad = first == 0 && a.cu && (a.cu[0] != 0 || a.cu[a.n_seqs] != a.Ttot);
+  for (int n = first; n < a.n_seqs; n += step) {
     bool bad;
     const AttnSeq s = attn_seq(a, n, bad);
     any_bad |= bad;
     if (n < kStaged) staged[n] = AttnStaged{s.nq, s.base};
-    else if (block != 0) break;
+    else if (!all && !a.cu) break;
   }
-  if (any_bad && a.flags && block == 0) atomicOr(a.flags, kFlagBadSeqlens);
+  return any_bad;
+}
+
+// cu_seqlens that fall back: a sequence, as well formed as it may be by itself,
+// begins before the end of an earlier one.  Together such sequences can hold more
+// tokens than there are, and what the host has judged by the number of tokens does
+// not hold: that costs stay below 2^31, and that nothing is cut in a call without a
+// workspace.  So nothing is done then.  Looked for only where lengths are malformed,
+// each thread in a chunk of the sequences, then chunk against chunk.
+struct AttnChunk {
+  int first, reach;  // where the first sequence with tokens begins and the last one
+                     // ends; first = -1: there is none
+};
+constexpr int kNothing = -1;  // in the first staged sequence's nq: nothing is done
+__host__ __device__ __forceinline__ bool attn_falls_back(const AttnArgs &a, int n0, int n1, AttnChunk &c) {
+  c.first = -1;
+  c.reach = 0;
+  bool back = false, bad;
+  for (int n = n0; n < n1 && n < a.n_seqs; n++) {
+    const AttnSeq s = attn_seq(a, n, bad);
+    if (s.nq == 0) continue;
+    back |= s.q0 < c.reach;
+    if (c.first < 0) c.first = s.q0;
+    c.reach = s.q0 + s.nq;
+  }
+  return back;
+}
+// chunk i against the ones before it
+__host__ __device__ __forceinline__ bool attn_falls_back(const AttnChunk *chunks, int i) {
+  if (chunks[i].first < 0) return false;
+  int before = i - 1;
+  while (before >= 0 && chunks[before].first < 0) before--;
+  return before >= 0 && chunks[i].first < chunks[before].reach;
+}
+
+// All THREADS threads of a block, where lengths are malformed.  Called, and with what
+// it needs by value, so that it lies apart from the kernels' own code: inlined, it
+// changed how that was laid out (256 sequences of one token 402 -> 405 us).
+template <int THREADS>
+__device__ __noinline__ void attn_stage_order(const int32_t *cu, const int32_t *kv_lens, int n_seqs,
+                                              int Ttot, int max_len, AttnStaged *staged) {
+  AttnArgs a{};
+  a.cu = cu;
+  a.kv_lens = kv_lens;
+  a.n_seqs = n_seqs;
+  a.Ttot = Ttot;
+  a.max_len = max_len;
+  AttnChunk *chunks = reinterpret_cast<AttnChunk *>(staged + kStaged);
+  const int tid = threadIdx.x, per = (a.n_seqs + THREADS - 1) / THREADS;
+  bool back = attn_falls_back(a, tid * per, (tid + 1) * per, chunks[tid]);
+  __syncthreads();
+  back |= attn_falls_back(chunks, tid);
+  if (__syncthreads_or(back)) staged[0].nq = kNothing;
+}
+// All THREADS threads of a block, which then synchronise; block 0 reports malformed
+// lengths.
+template <int THREADS>
+__device__ __forceinline__ void attn_stage(const AttnArgs &a, AttnStaged *staged, int block) {
+  if (a.plan_total) return;
+  const bool bad = attn_stage(a, staged, threadIdx.x, THREADS, block == 0);
+  if (bad && a.flags && block == 0) atomicOr(a.flags, kFlagBadSeqlens);
+  if (__syncthreads_or(bad) && a.cu)
+    attn_stage_order<THREADS>(a.cu, a.kv_lens, a.n_seqs, a.Ttot, a.max_len, staged);
 }
 
 // All lanes of one warp: choose the plan and find the start of range `block`.
 template <class S>
-__device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &plan,
-                                                const AttnStaged *staged, int block,
-                                                int n_blocks) {
-  const int lane = threadIdx.x & 31;
-  constexpr uint32_t kAll = 0xffffffffu;
+__host__ __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &plan,
+                                                         const AttnStaged *staged, int block,
+                                                         int n_blocks) {
   AttnStart r;
   r.seq = a.n_seqs;
   r.seq0 = 0;
@@ -431,6 +562,10 @@ __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &
     }
     return r;
   }
+  if (staged[0].nq == kNothing) {
+    r.total = 0;
+    return r;
+  }
   auto cost_of = [&](int n) {
     if (n < kStaged) return plan.cost(staged[n].nq, staged[n].base);
     bool bad;
@@ -438,15 +573,18 @@ __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &
     return plan.cost(s.nq, s.base);
   };
   r.total = plan.choose(n_blocks, [&] {
-    AttnCost mine = 0;
-    for (int n = lane; n < a.n_seqs; n += 32) mine += cost_of(n);
-    return __reduce_add_sync(kAll, mine);
+    return AttnLanes::sum([&](int lane) {
+      AttnCost mine = 0;
+      for (int n = lane; n < a.n_seqs; n += 32) mine += cost_of(n);
+      return mine;
+    });
   });
   if (S::kCut != 0 && !a.kv_lens && a.n_seqs <= 32 && plan.over != 0) {
-    const int nq = lane < a.n_seqs ? staged[lane].nq : 0;
-    const int units = __reduce_add_sync(kAll, plan.units_from(nq, 0, 1));
-    const AttnCost longest =
-        __reduce_max_sync(kAll, nq ? plan.grains_of(nq) * plan.weight(nq) + plan.own_cost(nq) : 0u);
+    auto nq = [&](int lane) { return lane < a.n_seqs ? staged[lane].nq : 0; };
+    const int units = AttnLanes::sum([&](int lane) { return plan.units_from(nq(lane), 0, 1); });
+    const AttnCost longest = AttnLanes::max([&](int lane) {
+      return nq(lane) ? plan.grains_of(nq(lane)) * plan.weight(nq(lane)) + plan.own_cost(nq(lane)) : 0u;
+    });
     plan.whole = units >= 2 * n_blocks && longest <= plan.per + S::kCut;
     if (plan.whole) return r;
   }
@@ -454,23 +592,15 @@ __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, AttnPlan<S> &
   if (c >= r.total) return r;
   AttnCost before = 0;
   for (int n0 = 0; n0 < a.n_seqs; n0 += 32) {
-    const int n = n0 + lane;
-    const AttnCost mine = n < a.n_seqs ? cost_of(n) : 0;
-    AttnCost incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const AttnCost up = __shfl_up_sync(kAll, incl, d);
-      if (lane >= d) incl += up;
-    }
-    const AttnCost excl = before + incl - mine;
-    const uint32_t hit = __ballot_sync(kAll, c >= excl && c < excl + mine);
-    if (hit) {
-      const int who = __ffs(hit) - 1;
+    AttnCost here;
+    const int who = AttnLanes::holder(
+        [&](int lane) { return n0 + lane < a.n_seqs ? cost_of(n0 + lane) : 0u; }, c - before, here);
+    before += here;
+    if (who >= 0) {
       r.seq = n0 + who;
-      r.seq0 = __shfl_sync(kAll, excl, who);
+      r.seq0 = before;
       return r;
     }
-    before += __shfl_sync(kAll, incl, 31);
   }
   return r;
 }
@@ -486,7 +616,7 @@ struct AttnWalk {
   int seq, block;
   bool fresh;            // the sequence is still to be looked up
   int blocks, round;     // units dealt whole
-  AttnSeq mine;          // of packed prompts: lane i has sequence i
+  AttnSeq mine[AttnLanes::kHere];  // of packed prompts: lane i has sequence i
 
   __host__ __device__ AttnWalk(const AttnArgs &a_, const AttnPlan<S> &p_, const AttnStart &st,
                                int block_, int blocks_ = 0)
@@ -496,49 +626,44 @@ struct AttnWalk {
     seq = st.seq;
     u0 = st.seq0;
     fresh = true;
-#ifdef __CUDA_ARCH__
-    if (S::kCut != 0 && plan.whole) {
-      bool bad;
-      mine.nq = mine.base = 0;
-      if ((threadIdx.x & 31) < a.n_seqs) mine = attn_seq(a, threadIdx.x & 31, bad);
-    }
-#endif
+    if (S::kCut != 0 && plan.whole)
+      AttnLanes::each([&](int lane, int i) {
+        bool bad;
+        mine[i].nq = mine[i].base = 0;
+        if (lane < a.n_seqs) mine[i] = attn_seq(a, lane, bad);
+      });
   }
   // place of this block's next unit among those that are dealt whole
   __host__ __device__ int turn() {
     const int r = round++;
     return r * blocks + (r & 1 ? blocks - 1 - block : block);
   }
-#ifdef __CUDA_ARCH__
   // unit i of packed prompts in order of length; all lanes of a warp
-  __device__ bool deal(int i, AttnUnit &out) const {
-    constexpr uint32_t kAll = 0xffffffffu;
-    const int lane = threadIdx.x & 31;
-    auto from = [&](int t) { return __reduce_add_sync(kAll, plan.units_from(mine.nq, mine.base, t)); };
+  __host__ __device__ bool deal(int i, AttnUnit &out) const {
+    auto at = [&](int lane) -> const AttnSeq & { return mine[lane & (AttnLanes::kHere - 1)]; };
+    auto from = [&](int t) {
+      return (int)AttnLanes::sum([&](int lane) { return plan.units_from(at(lane).nq, at(lane).base, t); });
+    };
     if (i >= from(1)) return false;
-    int lo = 1, hi = __reduce_max_sync(kAll, plan.tiles(mine.base + mine.nq));
+    int lo = 1, hi = AttnLanes::max([&](int lane) { return plan.tiles(at(lane).base + at(lane).nq); });
     while (lo < hi) {  // the most tiles that more than i units have
       const int mid = (lo + hi + 1) >> 1;
       if (from(mid) > i) lo = mid; else hi = mid - 1;
     }
     i -= from(lo + 1);
-    const int have = plan.units_from(mine.nq, mine.base, lo) - plan.units_from(mine.nq, mine.base, lo + 1);
-    int upto = have;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(kAll, upto, d);
-      if (lane >= d) upto += up;
-    }
-    const int who = __ffs(__ballot_sync(kAll, i < upto)) - 1;
-    i -= __shfl_sync(kAll, upto - have, who);
+    uint32_t before;
+    const int who = AttnLanes::holder(
+        [&](int lane) {
+          return plan.units_from(at(lane).nq, at(lane).base, lo) - plan.units_from(at(lane).nq, at(lane).base, lo + 1);
+        },
+        i, before);
     bool bad;
     const AttnSeq one = attn_seq(a, who, bad);
-    plan.pick(one, lo, i, out);
+    plan.pick(one, lo, i - (int)before, out);
     out.seq = who;
     out.len = one.len;
     return true;
   }
-#endif
   __host__ __device__ bool next(AttnUnit &out) {
     if constexpr (S::kCut != 0) {
       if (plan.whole || a.plan_whole) return next_whole(out);
@@ -569,12 +694,9 @@ struct AttnWalk {
     return false;
   }
   __host__ __device__ bool next_whole(AttnUnit &out) {
-#ifdef __CUDA_ARCH__
     if (plan.whole) {
       if (!deal(turn(), out)) return false;
-    } else
-#endif
-    {
+    } else {
       const int all = a.n_seqs * plan.groups, i = turn();
       const int tile = plan.token_tiles(a.T) - 1 - i / all;
       if (tile < 0) return false;
@@ -640,6 +762,33 @@ inline bool attn_plan_prompts(AttnArgs &a, int n_blocks) {
   }
   if (a.plan_whole) return false;
   return !(a.plan_grains && plan.tiles(a.T) <= 1 << plan.shift);
+}
+
+// The launch of a call, given the blocks that the GPU holds, and the plan where
+// the host can make it, into `a`.
+template <class S>
+AttnLaunch attn_plan_launch(AttnArgs &a, int blocks) {
+  AttnLaunch l;
+  l.blocks = blocks;
+  l.rows = S::kRows;
+  a.plan_total = 0;
+  a.plan_whole = 0;
+  // Nothing is cut when every unit is short and gets a block.
+  const long long units = attn_most_units<S>(a);
+  // A sequence's tiles are counted to the position of its last new token as if
+  // its first were at 0 or later: past its keys where it has fewer of them.
+  const int tokens = a.cu ? a.Ttot : a.T;
+  const int longest = a.kv_lens && a.max_len > tokens ? a.max_len : tokens;
+  l.split = !(AttnPlan<S>::tiles(longest) <= 1 << S::kWhole && units <= blocks);
+  a.plan_least = l.split ? S::kMinGrain : S::kWhole;
+  if (!l.split) l.blocks = units < 1 ? 1 : (int)units;
+  a.plan_coarse = attn_coarse<S>(units, longest);
+  if (a.plan_coarse < 0) {
+    l.blocks = 0;
+    return l;
+  }
+  if (!a.cu && !a.kv_lens && a.T > 0) l.split = attn_plan_prompts<S>(a, l.blocks);
+  return l;
 }
 
 }  // namespace gdn

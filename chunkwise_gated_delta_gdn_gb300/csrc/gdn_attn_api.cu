@@ -27,8 +27,8 @@ gdn_status check_shape(int B, int T, int H, int HKV, int d, int n_seqs, bool pac
   }
   if (d != 64 && d != 128) return GDN_ERR_UNSUPPORTED;
   Ttot = (long)B * T;
-  // rows are counted in 32 bits, with room for a tile past the last one
-  if (Ttot > INT32_MAX - 1024 || H > 65535) return GDN_ERR_UNSUPPORTED;
+  // rows and sequences are counted in 32 bits, with room for a tile past the last one
+  if (Ttot > INT32_MAX - 1024 || n > INT32_MAX - 1024 || H > 65535) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 

@@ -70,7 +70,8 @@ struct Smem {
   static constexpr int kUsed = kSlot + 8;  // [X] int2: stages that the scores free
   static constexpr int kBytes = kUsed + 16;
 };
-static_assert(kStaged * sizeof(AttnStaged) <= Smem<128>::kStages * Smem<128>::kTileBytes, "staging in the ring");
+static_assert(kStaged * sizeof(AttnStaged) + kThreads * sizeof(AttnChunk) <= Smem<128>::kStages * Smem<128>::kTileBytes,
+              "staging in the ring");
 static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "shared memory of one SM");
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : &maps.q_pack);
   if (warp == 17) tmem_alloc(smem_addr(slot), 512);
   AttnStaged *staged = reinterpret_cast<AttnStaged *>(sm + SM::kRing);  // until the first unit
-  attn_stage(a, staged, blockIdx.x);
+  attn_stage<kThreads>(a, staged, blockIdx.x);
   fence_proxy_async();
   asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel waits for this one's end
   fence_before_sync();

@@ -378,7 +378,8 @@ GDN_API gdn_status gdn_state_combine(const float *M, const float *S_in, const fl
  *   flags       as for gdn_recurrent_fwd.  BAD_SEQLENS: cu_seqlens, kv_lens or
  *               a page number out of range; such a sequence is skipped, and a
  *               bad page reads as zeros (gdn_kv_cache_append leaves its tokens
- *               out).  NONFINITE: a non-finite value was written to o.
+ *               out).  Attention does nothing where a sequence begins before the
+ *               end of an earlier one.  NONFINITE: a non-finite value was written to o.
  *   workspace   at least the bytes of the matching query, 256-byte aligned,
  *               not shared by two calls in flight; contents need no
  *               preparation and mean nothing afterwards.  NULL with 0 bytes
