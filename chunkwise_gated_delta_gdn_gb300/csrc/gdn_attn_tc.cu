@@ -66,9 +66,10 @@ struct Smem {
   // swap x2, halves x8, turn x2, unit full x4, unit empty x4, tile full, tile
   // empty
   static constexpr int kBarCount = 20 + 2 * kUnits + 2 * kStages;
+  // tensor memory, abort, [X] stages that the scores free
   static constexpr int kSlot = kBars + kBarCount * 8;
-  static constexpr int kUsed = kSlot + 8;  // [X] int2: stages that the scores free
-  static constexpr int kBytes = kUsed + 16;
+  static constexpr int kBytes = kSlot + 16;
+  static_assert(kSlot % 16 == 0, "read at once");
 };
 static_assert(kStaged * sizeof(AttnStaged) + kThreads * sizeof(AttnChunk) <= Smem<128>::kStages * Smem<128>::kTileBytes,
               "staging in the ring");
@@ -88,6 +89,12 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, float (&y)[N]) {
     tmem_ld32_nowait(at, reinterpret_cast<uint32_t(&)[32]>(y));
   else
     tmem_ld16_nowait(at, reinterpret_cast<uint32_t(&)[16]>(y));
+}
+
+__device__ __forceinline__ uint4 shared_uint4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
 }
 
 struct Maps {
@@ -151,7 +158,10 @@ __device__ __forceinline__ void issue_output(uint32_t d, uint32_t a, uint32_t b,
       : "memory");
 }
 
-// A bounded wait by all lanes of a warp, converged afterwards.
+// A bounded wait by all lanes of a warp, converged afterwards.  After one that gave
+// up (`abort`), the roles go on over whatever there is, within the same bounds, but
+// nobody hands a place back to the loader any more, which so comes to its end: a
+// place may not be filled while an earlier copy into it is on its way.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort) {
   const bool ok = mbar_wait(bar, parity, abort);
   __syncwarp();
@@ -283,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *abort = reinterpret_cast<volatile int *>(slot + 1);
   AttnUnit *unit_ring = reinterpret_cast<AttnUnit *>(sm + SM::kUnit);
   float *row_ex = reinterpret_cast<float *>(sm + SM::kRow);
-  int2 *used = reinterpret_cast<int2 *>(sm + SM::kUsed);
+  uint32_t *used = slot + 2;
   if (tid == 0) {
     *abort = 0;
     mbar_init(bars.q_full(), 1);
@@ -369,12 +379,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (half == 0 && quarter == 0 && lane == 0) {
           // These scores, and what this X was given before them, are done: hand
           // back their key tile and the value tile before.
-          const int2 stage = used[x];
-          mbar_arrive(bars.kv_empty(stage.x));
-          if (stage.y >= 0) mbar_arrive(bars.kv_empty(stage.y));
-          if (narrow) {
-            mbar_arrive(bars.kv_empty(stage.x));
-            if (stage.y >= 0) mbar_arrive(bars.kv_empty(stage.y));
+          const uint4 now = shared_uint4(smem_addr(slot));
+          if (now.y == 0) {  // or there may not have been scores yet
+            const uint32_t stages = x == 0 ? now.z : now.w;
+            const int key = stages & 255, value = (int)(stages >> 8) - 1;
+            mbar_arrive(bars.kv_empty(key));
+            if (value >= 0) mbar_arrive(bars.kv_empty(value));
+            if (narrow) {
+              mbar_arrive(bars.kv_empty(key));
+              if (value >= 0) mbar_arrive(bars.kv_empty(value));
+            }
           }
         }
         if (idle) {
@@ -592,6 +606,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       AttnUnit u, old;         // this unit, and the one whose last values are still to come
       int left[2] = {-1, -1};  // its last tiles
       bool shared = false;     // one value tile for both X
+      bool lost = false;       // a wait of this lane gave up: it loads nothing any more
+      auto place = [&](uint32_t bar, uint32_t parity) {
+        lost |= !mbar_wait(bar, parity, abort);
+        __syncwarp();
+      };
       // Page numbers of 32 pages in a row, a lane each, for the key tiles and
       // for the value tiles that follow them: read once in 32 pages, not once
       // per tile, where their latency held the loads at 2700 clocks a tile.
@@ -629,15 +648,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           // a bad page reads as zeros: the box just past the cache
           const int group = (good ? held : a.n_pages) * groups + ((k0 - index * a.page_size) >> 3);
           const int n = min((last - key + box) / box, 128 / box);  // boxes; may be <= 0
-          wait(bars.kv_empty(ring.i), ring.round ^ 1, abort);
-          if (lane == 0) mbar_arrive_expect_tx(full, max(n, 0) * box * 128 * kPanels);
+          place(bars.kv_empty(ring.i), ring.round ^ 1);
+          if (lane == 0 && !lost) mbar_arrive_expect_tx(full, max(n, 0) * box * 128 * kPanels);
           __syncwarp();
-          if (mine)
+          if (mine && !lost)
             tma_load_5d(dst + my_key * 128 * kPanels, map, 0, 0, 0, group, w.kvh, full,
                         w.n_tok * w.gp <= 128 ? once : often);
         } else {
-          wait(bars.kv_empty(ring.i), ring.round ^ 1, abort);
-          if (lane == 0) {
+          place(bars.kv_empty(ring.i), ring.round ^ 1);
+          if (lane == 0 && !lost) {
             mbar_arrive_expect_tx(full, SM::kTileBytes);
             const int row = w.row0 - w.pos0 + key;  // a prompt's keys are its own tokens
 #pragma unroll
@@ -656,9 +675,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool narrow = u.n_tok * u.gp <= 128;
         if (left[1] < left[0]) last_values(1);
         last_values(0);
-        wait(bars.q_empty(), q_phase, abort);
+        place(bars.q_empty(), q_phase);
         q_phase ^= 1;
-        if (lane == 0) {
+        if (lane == 0 && !lost) {
           const bool whole = u.gp == a.H / a.HKV;  // all heads of a key/value head
           const int toks = 128 / u.gp, tiles = narrow ? 1 : 2;
           mbar_arrive_expect_tx(bars.q_full(), tiles * kPanels * toks * u.gp * 128);
@@ -754,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                               kIdS, lane == 0);
         if (lane == 0) {
           mma_commit(bars.s_full(x));
-          used[x] = make_int2(k, free_v);
+          used[x] = k | (free_v + 1) << 8;
           mbar_arrive(bars.s_full(x));
         }
       };
@@ -775,8 +794,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         weights_ready();
         output(v, more);
         if (lane == 0) {
-          mma_commit(bars.kv_empty(v));  // each stage waits for two arrivals
-          if (!shared) mma_commit(bars.kv_empty(v));
+          if (!*abort) {
+            mma_commit(bars.kv_empty(v));  // each stage waits for two arrivals
+            if (!shared) mma_commit(bars.kv_empty(v));
+          }
           mma_commit(bars.o_full(x));
         }
         __syncwarp();
@@ -843,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           more = t0 + 1 < t1;
         }
         // behind the last scores: the queries may be replaced
-        if (lane == 0) {
+        if (lane == 0 && !*abort) {
           if (x == 0 || !narrow || t0 + 1 < t1) mma_commit(bars.q_empty());
           else mbar_arrive(bars.q_empty());
         }
@@ -858,7 +879,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  if (tid == 0 && *abort && a.flags) atomicOr(a.flags, kFlagTimeout);
+  if (*abort) {
+    // a wait gave up, and no warp issues anything any more: let copies and products
+    // still in flight land before the shared and tensor memory are released
+    // (bounded, about 10 ms)
+    if (tid == 0 && a.flags) atomicOr(a.flags, kFlagTimeout);
+    const long long t0 = clock64();
+    while (clock64() - t0 < 20000000LL) {
+    }
+    __syncwarp();
+  }
   if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
