@@ -110,6 +110,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<D>()) gdn_attn_warp_ke
   AttnUnit u;
   if (a.jobs && tid == 0) a.jobs[blockIdx.x].rows = 0;
   while (walk.next(u)) {
+    if (u.slot >= 0 && !a.jobs) {  // a cut unit has no place: never by the plan
+      if (tid == 0 && a.flags) atomicOr(a.flags, kFlagLaunchConfig);
+      continue;
+    }
     if (tid == 0 && u.slot == 2 * (int)blockIdx.x + 1) a.jobs[blockIdx.x] = attn_job(u);
     __syncthreads();  // the previous unit's operands (or the plan's) are read
     const int end = min(u.t1 * 64, max(u.pos0 + u.n_tok, 0));  // behind the last key that anybody sees

@@ -80,12 +80,13 @@ gdn_status launch(gdn::AttnArgs &a, int d, int dtype, float scale, const gdn::At
   if (a.flags && cudaMemsetAsync(a.flags, 0, sizeof(uint32_t), stream) != cudaSuccess)
     return GDN_ERR_CUDA;
   if (a.Ttot == 0) return GDN_OK;
-  const size_t rows = (size_t)2 * l.blocks * l.rows;
-  a.scale = scale;
   a.scale_log2 = scale * 1.44269504088896340736f;
-  a.part_o = static_cast<float4 *>(workspace);
-  a.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + rows * d * sizeof(float));
-  a.jobs = l.split ? reinterpret_cast<gdn::AttnJob *>(a.part_ml + rows) : nullptr;
+  if (l.split) {  // otherwise there is no place for partial results
+    const size_t rows = (size_t)2 * l.blocks * l.rows;
+    a.part_o = static_cast<float4 *>(workspace);
+    a.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + rows * d * sizeof(float));
+    a.jobs = reinterpret_cast<gdn::AttnJob *>(a.part_ml + rows);
+  }
   return gdn::launch_attn(a, d, dtype, l, stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

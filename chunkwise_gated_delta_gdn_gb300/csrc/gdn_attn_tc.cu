@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (smem_addr(sm) & 1023u) {
     if (tid == 0 && a.flags) atomicOr(a.flags, kFlagLaunchConfig);
+    if (tid == 0 && a.jobs) a.jobs[blockIdx.x].rows = 0;  // the merge kernel reads it
     return;
   }
   const Bars bars{smem_addr(sm + SM::kBars), SM::kStages};
@@ -586,6 +587,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (a.jobs && lane == 0) a.jobs[blockIdx.x].rows = 0;
       while (more) {
         more = walk.next(u);
+        if (more && u.slot >= 0 && !a.jobs) {  // a cut unit has no place: never by the plan
+          if (lane == 0 && a.flags) atomicOr(a.flags, kFlagLaunchConfig);
+          continue;
+        }
         if (!more) u.seq = -1;
         else if (lane == 0 && u.slot == 2 * (int)blockIdx.x + 1) a.jobs[blockIdx.x] = attn_job(u);
         if (!__all_sync(0xffffffffu, mbar_wait(bars.unit_empty(at.i), at.round ^ 1, abort))) break;

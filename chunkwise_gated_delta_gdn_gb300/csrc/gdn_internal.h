@@ -132,7 +132,6 @@ struct AttnArgs {
   int page_size, max_pages, n_pages;
   int page_log;                // log2 of page_size, or -1
   int max_len;                 // longest length the table can hold
-  float scale;
   float scale_log2;            // scale * log2(e)
   // the plan where the host can make it (gdn_attn.cuh): equal prompts;
   // plan_total = 0 otherwise
@@ -141,9 +140,9 @@ struct AttnArgs {
   int plan_whole;              // units are dealt whole
   int plan_coarse;             // log2 of the grain of equal shares
   int plan_least;              // log2 of the smallest other grain
-  float4 *part_o;              // partial results (see gdn_attn.cuh)
-  float2 *part_ml;
-  AttnJob *jobs;         // [blocks] what is to be joined, or nullptr when nothing is cut
+  float4 *part_o;              // partial results (see gdn_attn.cuh); these three are
+  float2 *part_ml;             // nullptr when nothing is cut
+  AttnJob *jobs;               // [blocks] what is to be joined
   uint32_t *flags;             // device status word, or nullptr
 };
 // Writes the keys and values of new tokens into the pages of a cache.
