@@ -30,6 +30,13 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int n_seqs, int t)
 __global__ void __launch_bounds__(kThreads) gdn_kv_append_kernel(const AppendArgs a) {
   const int per_row = a.row_bytes >> 4;
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  // A token finds its sequence by halving, and so need not meet a sequence that is
+  // malformed: they are looked at by themselves.
+  if (a.cu && a.flags)
+    for (long long n = i; n < a.n_seqs; n += (long long)gridDim.x * kThreads) {
+      const int from = __ldg(a.cu + n), to = __ldg(a.cu + n + 1);
+      if (from < 0 || to < from || to > a.Ttot) atomicOr(a.flags, kFlagBadSeqlens);
+    }
   const long long row = i / per_row;
   if (row >= a.Ttot) return;
   const int t = (int)row, piece = (int)(i - row * per_row);

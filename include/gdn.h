@@ -421,7 +421,8 @@ GDN_API gdn_status gdn_attn_paged_fwd(const void *q, const void *k_cache, const 
 /*
  * gdn_kv_cache_append -- k and v of the new tokens into the pages, each at its
  * position; the rest of the cache is left as it is.  A token at a negative
- * position is left out.  kv_lens counts the new tokens already.
+ * position is left out.  kv_lens counts the new tokens already.  A token of two
+ * sequences (cu_seqlens that fall back) goes to one of them.
  */
 GDN_API gdn_status gdn_kv_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,
                                        const int32_t *block_table, const int32_t *kv_lens,

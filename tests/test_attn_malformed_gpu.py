@@ -55,3 +55,29 @@ def test_one_entry_out_of_range(dtype):
             for x, x0 in ((o, o0), (lse, lse0)):
                 assert (x[:, 40:200] == 77.0).all()
                 assert torch.equal(x[:, :40], x0[:, :40]) and torch.equal(x[:, 200:], x0[:, 200:])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("cu, written", [
+    ([0, 6, 0, 6], 6),                     # each token is in the first sequence
+    ([0, 2, 2, 2, 1, 6], 6),               # back by one
+    ([0, 6] + [0] * 40 + [6], 6),
+    ([0, 4, 4, 3], 4),                     # the last two tokens belong to nobody
+], ids=str)
+def test_cache_write_reports_malformed_sequences(dtype, cu, written):
+    """Also where every token finds a sequence that is well formed by itself."""
+    HKV, d, page, T, n = 2, 64, 16, 6, len(cu) - 1
+    gen = torch.Generator().manual_seed(1)
+    k, v = (torch.randn((1, T, HKV, d), generator=gen).to(dtype).cuda() for _ in range(2))
+    kc, vc = torch.zeros((n, page, HKV, d), dtype=dtype, device="cuda"), torch.zeros((n, page, HKV, d), dtype=dtype, device="cuda")
+    table = torch.arange(n, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    lens = torch.full((n,), T, dtype=torch.int32, device="cuda")
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdn.gdn_kv_cache_append(k, v, kc, vc, table, lens, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                            flags=flags)
+    assert gdn.gdn_read_device_flags(flags) == gdn.GDN_FLAG_BAD_SEQLENS
+    for cache, new in ((kc, k), (vc, v)):  # each token once, no others
+        rows = cache.flatten(0, 1).flatten(1)
+        rows = rows[rows.any(1)]
+        assert len(rows) == written
+        assert all((rows == x).all(1).any() for x in new[0, :written].flatten(1))
