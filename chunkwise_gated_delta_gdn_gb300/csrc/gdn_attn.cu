@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const Att
   auto store = [&](int row, int d4, float4 o, float l) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
     o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-    finite &= isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w);
+    const float kInf = BF16 ? kBf16Inf : CUDART_INF_F;  // from here on it is written as infinity
+    finite &= fabsf(o.x) < kInf && fabsf(o.y) < kInf && fabsf(o.z) < kInf && fabsf(o.w) < kInf;
     const long long at = place(row) * D + d4 * 4;
     if constexpr (BF16) {
       __nv_bfloat162 y[2] = {__floats2bfloat162_rn(o.x, o.y), __floats2bfloat162_rn(o.z, o.w)};

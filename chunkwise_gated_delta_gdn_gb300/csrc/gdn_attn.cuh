@@ -93,6 +93,7 @@ struct AttnShape {
 // that a piece's start and the joining outweigh its tiles.
 using TcShape = AttnShape<256, 128, 128, 4, 8, 3, 6, 128, 3, 3, 40>;
 constexpr int kMaxGrain = 6;   // log2 of the largest one that is tried
+constexpr float kBf16Inf = 0x1.ffp127f;  // what rounds to infinity in bf16
 
 struct AttnSeq {
   int q0, nq;   // first token row and number of new tokens

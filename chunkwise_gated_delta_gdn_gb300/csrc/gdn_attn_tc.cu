@@ -50,7 +50,6 @@ using namespace sm100;
 constexpr int kThreads = 640;
 constexpr int kUnits = 4;              // unit ring
 constexpr int kPanel = 128 * 128;      // bytes of 128 rows x 64 bf16
-constexpr float kBf16Inf = 0x1.ffp127f;  // what rounds to infinity in bf16
 constexpr float kRescale = 8.f;        // log2 growth of a row maximum that is let stand
 
 template <int D>
