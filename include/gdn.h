@@ -389,9 +389,11 @@ GDN_API gdn_status gdn_state_combine(const float *M, const float *S_in, const fl
  * kv_lens: 4-byte).  No output may overlap an input or another output.
  *
  * What lies in the cache beyond L, and in other sequences, does not reach a
- * result, whatever its bits.  Within a sequence a non-finite v at a later
- * position can turn the outputs of earlier tokens of the same key tile (128
- * keys, 64 in fp32) into NaN (0 * inf).
+ * result, whatever its bits, and a k at a later position not that of an earlier
+ * token.  A non-finite v at a later position j can turn outputs of earlier
+ * tokens into NaN (0 * inf), from position j - 382 on (fp32: j - 126) and not
+ * before: up to 256 rows (64) are worked on together, over key tiles of 128
+ * (64) up to the one that the last of them sees.
  *
  * Numerics: scores, row maximum and sum, and the output's accumulation in
  * fp32; o rounded once to dtype.  bf16: tensor-core products of bf16 operands;

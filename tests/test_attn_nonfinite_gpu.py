@@ -39,3 +39,45 @@ def test_bf16_infinity_from_a_finite_sum(kv):
     o, lse = gdn.gdn_attn_paged_fwd(*args, scale=scale, flags=flags)
     assert torch.isfinite(lse).all() and torch.isinf(o).all()
     assert gdn.gdn_read_device_flags(flags) == gdn.GDN_FLAG_NONFINITE
+
+
+@pytest.mark.parametrize("dtype, reach", [(torch.bfloat16, 382), (torch.float32, 126)], ids=str)
+@pytest.mark.parametrize("H, HKV, d", [(2, 2, 64), (1, 1, 128), (8, 2, 64), (3, 1, 128)])
+@pytest.mark.parametrize("new, past, at", [(256, 0, 200), (1200, 0, 900), (1200, 0, 1023), (700, 77, 300), (90, 1001, 1080),
+                                           (12, 500, 505)])
+def test_a_later_value_reaches_no_further_than_its_tiles(dtype, reach, H, HKV, d, new, past, at):
+    """A non-finite key or value at position `at` of a prompt's chunk over a cache (and of a whole
+    prompt, where there is no past).  It is everybody's from there on.  Tokens before see it with
+    weight 0, which makes NaN of a non-finite value: a token's rows are worked on with those of up to
+    255 later positions (63 in fp32), over key tiles that end up to 127 (63) positions behind."""
+    page, T = 16, past + new
+    gen = torch.Generator().manual_seed(T)
+    q, k, v = (torch.randn((1, n, h, d), generator=gen).to(dtype).cuda() for n, h in ((new, H), (T, HKV), (T, HKV)))
+    n = -(-T // page)
+    table = torch.randperm(n, generator=gen).to(torch.int32)[None].cuda()
+    lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+
+    def run(k, v):
+        kc, vc = (torch.full((n, page, HKV, d), float("nan"), dtype=dtype, device="cuda") for _ in range(2))
+        gdn.gdn_kv_cache_append(k, v, kc, vc, table, lens)
+        out = [gdn.gdn_attn_paged_fwd(q, kc, vc, table, lens)]
+        if past == 0:
+            out.append(gdn.gdn_attn_fwd(q, k, v))
+        return out
+
+    clean = run(k, v)
+    row, G = at - past, H // HKV
+    for x in (float("inf"), float("nan")):
+        bad_k, bad_v = k.clone(), v.clone()
+        bad_k[0, at, 0, 5], bad_v[0, at, 0, 5] = float("nan"), x
+        for (o, lse), (o0, lse0) in zip(run(bad_k, v), clean):
+            assert torch.isnan(o[0, row:, :G]).all()
+            assert torch.equal(o[0, :row], o0[0, :row]) and torch.equal(o[0, row:, G:], o0[0, row:, G:])
+            assert torch.equal(lse[0, :row], lse0[0, :row])
+        for (o, lse), (o0, lse0) in zip(run(k, bad_v), clean):
+            assert torch.equal(lse, lse0)
+            assert not torch.isfinite(o[0, row:, :G, 5]).any()
+            first = max(row - reach, 0)
+            assert torch.equal(o[0, :first], o0[0, :first])
+            o[0, first:, :G, 5] = o0[0, first:, :G, 5]
+            assert torch.equal(o, o0)  # no other column, no other key/value head
