@@ -29,7 +29,12 @@
 //    of 2048 tokens took 145 us cut, 124 whole; 16 of 512 tokens 87 and 64; one of
 //    4096 tokens, 16 heads (1.7 units for each block) 80 and 63; one of 16384, 4
 //    heads (1.7, the longest 520 of a share of 448) 209 and 220, and stays cut; 12001
-//    packed tokens 409 and 386.  In fp32 shares come out as fast or faster (10 x 2199
+//    packed tokens 409 and 386.  Packed prompts ask for two units for each block
+//    (with one: 1 of 4096 tokens, 16 heads 80 cut, 66 whole; 6 of 400 tokens 32 and
+//    26; 2 of 3000, 8 heads of 64 47 and 48) and for at most 32 sequences, a lane of
+//    the plan's warp each (the same work with empty sequences up to 33, so cut: 32 of
+//    512 tokens 158 us for 130, 32 of 200 73 for 59, 32 of 100 to 1500 312 for 255, 32
+//    of 2048 alike).  In fp32 shares come out as fast or faster (10 x 2199
 //    tokens 1100 and 1108 us).  The units of a decode step are too much alike.
 // A unit cut by a range's border leaves partial results (unnormalised output,
 // row maximum and sum) that the merge kernel joins in the order of the blocks,

@@ -23,13 +23,13 @@
 //
 // What bounds it.  Prompts: the latency of the chain scores - softmax - weights
 // - product of each X.  Two tiles of a wide unit take 3300 clocks: the products of
-// both 2048 of them, a tile's softmax 1350 (the special functions alone 1024),
-// the way through the barriers the rest; a second pair of score tiles, which
+// both 2048 of them, a tile's softmax 1350 (the special functions, 32 results a
+// clock, 512 of those), the way through the barriers the rest; a second pair of score tiles, which
 // would hide it, does not fit tensor memory beside two outputs of 128 columns.  A
 // unit's start and end take 10000 clocks beside its tiles, most of it for the
 // 64 KB of its rows to leave the processor.  32768 tokens of 16 heads of 128:
-// 2860 to 2930 us, 1500 to 1540 TFLOP/s; four of 2048 tokens, 32 heads: 125 us,
-// 1100 TFLOP/s.
+// 2860 to 2990 us, 1470 to 1540 TFLOP/s; four of 2048 tokens, 32 heads: 126 us,
+// 1090 TFLOP/s.
 // One token per sequence: memory where heads are 128 wide (64 sequences over 8192
 // keys 335 us, 6.4 TB/s), the chain of products and barriers, 2000 clocks a tile,
 // where they are 64 wide (130 us for 32 sequences, 4.1 TB/s).  A call's start, plan
