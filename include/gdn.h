@@ -379,7 +379,10 @@ GDN_API gdn_status gdn_state_combine(const float *M, const float *S_in, const fl
  *               a page number out of range; such a sequence is skipped, and a
  *               bad page reads as zeros (gdn_kv_cache_append leaves its tokens
  *               out).  Attention does nothing where a sequence begins before the
- *               end of an earlier one.  NONFINITE: a non-finite value was written to o.
+ *               end of an earlier one.  NONFINITE: a non-finite value was
+ *               written to o.  TIMEOUT: as in the workspace of gdn_chunk_fwd.
+ *               LAUNCH_CONFIG: as there, or work without a place for its
+ *               partial result was left out (lengths that changed meanwhile).
  *   workspace   at least the bytes of the matching query, 256-byte aligned,
  *               not shared by two calls in flight; contents need no
  *               preparation and mean nothing afterwards.  NULL with 0 bytes
