@@ -361,6 +361,9 @@ constexpr int kMergeRows = 32;
 constexpr int kMergeUnroll = 4;
 constexpr int kMergeMany = 16;  // from here on slices of columns pay (131072 keys in 64 pieces 41.5
                                 // -> 35.8 us; 4 sequences of 16384 in 6 pieces each 54.8 -> 57.2)
+// blocks to a job: 32 rows each, and at least four for slices of the columns
+template <class S>
+constexpr int merge_blocks() { return S::kRows < kMergeRows ? 4 : S::kRows / kMergeRows; }
 template <class S, int D, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const AttnArgs a) {
   __shared__ float weight[kMergeRows], total[kMergeRows];
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const Att
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const AttnJob job = a.jobs[first];
   const int n = job.last - first + 1;  // pieces
-  constexpr int kSlice = D / 4 / (S::kRows / kMergeRows);  // of the columns, in fours
+  constexpr int kSlice = D / 4 / merge_blocks<S>();  // of the columns, in fours
   const bool sliced = job.rows <= kMergeRows && n > kMergeMany;
   const int r0 = sliced ? 0 : blockIdx.y * kMergeRows;
   if (r0 >= job.rows) return;
@@ -516,7 +519,7 @@ cudaError_t merge(const AttnArgs &a, int blocks, cudaStream_t stream) {
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t config{};
-  config.gridDim = dim3(blocks - 1, S::kRows / kMergeRows);
+  config.gridDim = dim3(blocks - 1, merge_blocks<S>());
   config.blockDim = dim3(kMergeThreads);
   config.stream = stream;
   config.attrs = &early;
@@ -561,6 +564,10 @@ cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &don
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
+}
+
+cudaError_t launch_attn8_merge(const AttnArgs &a, int d, int blocks, cudaStream_t stream) {
+  return d == 64 ? merge<Shape8, 64, true>(a, blocks, stream) : merge<Shape8, 128, true>(a, blocks, stream);
 }
 
 AttnLaunch attn_launch(AttnArgs &a, int d, int dtype) {

@@ -97,6 +97,8 @@ struct AttnShape {
 // Smallest grains of 4, 8 and 16 tiles were alike in all cases measured: below
 // that a piece's start and the joining outweigh its tiles.
 using TcShape = AttnShape<256, 128, 128, 4, 8, 3, 6, 128, 3, 3, 40>;
+// The kernel's for few rows over a cache in 8 bits (gdn_attn8.cu).
+using Shape8 = AttnShape<16, 16, 128, 2, 4, 2, 4, 16, 1, 3>;
 constexpr int kMaxGrain = 6;   // log2 of the largest one that is tried
 constexpr float kBf16Inf = 0x1.ffp127f;  // what rounds to infinity in bf16
 

@@ -1,0 +1,427 @@
+// gdn_attn8.cu -- attention of few query rows (a decode step) over a paged cache
+// held in 8 bits: e4m3 values with an fp32 scale for each block of 16 tokens and
+// key/value head.
+//
+//   s_j = scale a_j q.k_j,  m = max_j s_j,  l = sum_j e^(s_j - m),
+//   o = sum_j e^(s_j - m) b_j v_j / l,      lse = m + ln l
+// with k_j, v_j the 8-bit values and a_j, b_j their blocks' scales.
+//
+// A decode step reads each key and value once and has 8 products for each value
+// read, so memory is to be the bound, and what stands between the loads and it is
+// kept small: a unit (a sequence's rows of one key/value head, at most 16) has
+// eight warps, each of which takes every eighth block of 16 keys by itself, from
+// copying it (cp.async into a ring of its own) to the weighted sum; nothing
+// synchronises warps until a unit's end.  With the keys as the M and the query rows
+// as the N dimension of mma.sync (m16n8k16), 8 rows cost no more than there are:
+//   S^T = K Q^T   (16 keys x 8 rows),  O^T += V^T P^T  (D x 8 rows)
+// The 8-bit values go to fp16, where they are exact, straight into the fragments:
+// which of a key's elements a thread takes for which k is free as long as Q's
+// fragment does the same, so a thread reads 32 bytes of a key in a row; V's keys are
+// paired by byte permutes.  Scales are applied to scores and weights, a scalar each
+// for the 16 keys of a step.  Q is scaled by a power of two for each row into the
+// middle of fp16's range (exact but for elements below 2^-28 of the row's largest).
+//
+// Weights are rounded to fp16 for the product with V: e^(s - m) b 2^6 relative to
+// the largest such product so far, moved when it is outgrown by 2^8, so they stay
+// below 2^15 and what is below 2^-30 of the largest one is lost.  The sum l has a
+// maximum of its own (of s alone), in fp32.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "gdn_attn.cuh"
+#include "gdn_sm100.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace sm100;
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kSlice = kScaleBlock;  // keys of a warp's step
+constexpr int kSlices = Shape8::kTile / kSlice;
+static_assert(kSlices == kWarps, "a slice of each tile for each warp");
+constexpr float kLag = 8.f;    // log2 growth of a maximum that is let stand
+constexpr float kShift = 6.f;  // log2 of the weights' factor
+
+template <int D, int NT>
+struct Smem {
+  static constexpr int kSliceBytes = 2 * kSlice * D;
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kRow = D + 4;  // floats of a row where warps are joined
+  static constexpr int kRing = 0;     // [warp][stage][keys, values]
+  static constexpr int kScale = kWarps * kStages * kSliceBytes;  // [warp][stage][2]
+  static constexpr int kQ = kScale + kWarps * kStages * 8;       // [nt][k step][lane] two registers
+  static constexpr int kFactor = kQ + NT * (D / 16) * 32 * 8;    // [rows]
+  static constexpr int kJoin = kFactor + NT * 8 * 4;             // [warp][rows] maximum, sum, maximum with V's scale
+  static constexpr int kBytes = kJoin + kWarps * NT * 8 * 12;
+  static_assert(kWarps * NT * 8 * kRow * 4 <= kScale, "joined in the ring's place");
+  static_assert(kStaged * sizeof(AttnStaged) + kThreads * sizeof(AttnChunk) <= kScale, "staging in the ring's place");
+};
+static_assert(2 * (Smem<128, 2>::kBytes + 1024) <= 233472 && 2 * (Smem<64, 2>::kBytes + 1024) <= 233472, "two blocks to an SM");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two 8-bit values (the low or high half of x) as two fp16
+__device__ __forceinline__ uint32_t half_lo(uint32_t x) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t half_hi(uint32_t x) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&p);
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+// 16 bytes in the background, read once; zeros when !valid
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool valid, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(to), "l"(from), "r"(valid ? 16 : 0), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// NT: groups of 8 rows
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a) {
+  using SM = Smem<D, NT>;
+  constexpr int kSteps = D / 16;          // of 16 elements
+  constexpr int kWords = D / 16;          // 32-bit words of a key that a thread takes
+  extern __shared__ __align__(128) unsigned char sm[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_addr(sm) + warp * SM::kStages * SM::kSliceBytes;
+  float *scales = reinterpret_cast<float *>(sm + SM::kScale) + warp * SM::kStages * 2;
+  float *factor = reinterpret_cast<float *>(sm + SM::kFactor), *join = reinterpret_cast<float *>(sm + SM::kJoin);
+  const uint32_t q_at = smem_addr(sm + SM::kQ);
+  AttnPlan<Shape8> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
+  AttnStaged *staged = reinterpret_cast<AttnStaged *>(sm);  // until the first copies
+  attn_stage<kThreads>(a, staged, blockIdx.x);
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel waits for this one's end
+  __syncthreads();
+  const AttnStart st = attn_start(a, plan, staged, blockIdx.x, gridDim.x);  // each warp for itself
+  AttnWalk<Shape8> walk(a, plan, st, blockIdx.x, gridDim.x);
+  if (a.jobs && tid == 0) a.jobs[blockIdx.x].rows = 0;
+  const uint64_t once = l2_evict_first();
+  const long long row_bytes = (long long)a.HKV * D;
+  AttnUnit u;
+  while (walk.next(u)) {
+    if (u.slot >= 0 && !a.jobs) {  // a cut unit has no place: never by the plan
+      if (tid == 0 && a.flags) atomicOr(a.flags, kFlagLaunchConfig);
+      continue;
+    }
+    if (tid == 0 && u.slot == 2 * (int)blockIdx.x + 1) a.jobs[blockIdx.x] = attn_job(u);
+    __syncthreads();  // the previous unit's (or the plan's) shared memory has been read
+    const int end = min(u.t1 * Shape8::kTile, max(u.pos0 + u.n_tok, 0));  // behind the last key that anybody sees
+    const int first = u.t0 * kSlices + warp, n_slices = (end + kSlice - 1) / kSlice;
+    const int steps = n_slices > first ? (n_slices - first + kWarps - 1) / kWarps : 0;  // this warp's
+    // The pages of 32 steps, a lane each.
+    int page = 0;
+    auto look_up = [&](int i) {
+      const int key = min((first + (i + lane) * kWarps) * kSlice, u.len - 1);
+      page = __ldg(a.table + (long long)u.seq * a.max_pages + (a.page_log >= 0 ? key >> a.page_log : key / a.page_size));
+      if ((unsigned)page >= (unsigned)a.n_pages) {  // reads as zeros
+        page = -1;
+        if (a.flags && i + lane < steps) atomicOr(a.flags, kFlagBadSeqlens);
+      }
+    };
+    auto fetch = [&](int i) {  // step i, into its stage; an empty group behind the last one
+      if (i < steps) {
+        if ((i & 31) == 0) look_up(i);
+        const int mine = __shfl_sync(0xffffffffu, page, i & 31);
+        const int key = (first + i * kWarps) * kSlice;
+        const int inside = a.page_log >= 0 ? key & (a.page_size - 1) : key % a.page_size;
+        const int rows = mine < 0 ? 0 : min(u.len - key, kSlice);
+        const int at_page = max(mine, 0);
+        const int stage = i % SM::kStages;
+        const long long from = ((long long)at_page * a.page_size + inside) * row_bytes + (long long)u.kvh * D;
+        const uint32_t to = ring + stage * SM::kSliceBytes;
+        constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks;
+        const int chunk = lane % kChunks;
+#pragma unroll
+        for (int j = 0; j < kSlice / kAtOnce; j++) {
+          const int r = j * kAtOnce + lane / kChunks;
+          const uint32_t dst = to + r * D + ((chunk ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+          const long long src = from + (r < rows ? r * row_bytes : 0) + chunk * 16;
+          copy16(dst, static_cast<const char *>(a.k) + src, r < rows, once);
+          copy16(dst + kSlice * D, static_cast<const char *>(a.v) + src, r < rows, once);
+        }
+        if (lane < 2) {
+          const float *s = lane ? a.v_scale : a.k_scale;
+          cp_async4(smem_addr(scales + stage * 2 + lane),
+                    s + ((long long)at_page * (a.page_size / kScaleBlock) + inside / kScaleBlock) * a.HKV + u.kvh, mine < 0 ? 0 : 4);
+        }
+      }
+      copies_end();
+    };
+#pragma unroll
+    for (int i = 0; i < SM::kStages - 1; i++) fetch(i);
+    // Q's fragments: row r of group nt, for k step s the elements 2 D / 8 t' + 4 s .. + 3
+    // of thread t' of a row.  A warp has whole rows, so that each row's largest
+    // exponent is at hand.
+    for (int r = warp; r < NT * 8; r += kWarps) {
+      const int tok = r / u.gp;
+      uint2 x = make_uint2(0, 0);  // 4 elements for each lane (d = 64: lanes 0-15)
+      if (tok < u.n_tok && lane * 4 < D)
+        x = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + (long long)(u.row0 + tok) * a.q_stride +
+                                                  (u.head0 + r % u.gp) * D + lane * 4));
+      const uint32_t lo0 = x.x << 16, hi0 = x.x & 0xffff0000u, lo1 = x.y << 16, hi1 = x.y & 0xffff0000u;
+      const uint32_t top = __reduce_max_sync(0xffffffffu, max(max(lo0 & 0x7fffffffu, hi0 & 0x7fffffffu), max(lo1 & 0x7fffffffu, hi1 & 0x7fffffffu)));
+      // 2^up brings the largest element to [2^14, 2^15); non-finite rows stay as they are
+      const int e = (int)(top >> 23) - 127, up = e == 128 ? 0 : max(14 - e, -113);
+      const float f1 = __int_as_float((127 + up / 2) << 23), f2 = __int_as_float((127 + up - up / 2) << 23);
+      auto scaled = [&](uint32_t y) { return __uint_as_float(y) * f1 * f2; };
+      if (lane * 4 < D) {
+        // thread t' has elements t' D / 4 ..: 4 of them a k step
+        const int owner = lane / (D / 16), step = lane % (D / 16);
+        const uint32_t to = q_at + (((r >> 3) * kSteps + step) * 32 + (r & 7) * 4 + owner) * 8;
+        const uint32_t b0 = pack_f16(scaled(lo0), scaled(hi0)), b1 = pack_f16(scaled(lo1), scaled(hi1));
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(b0), "r"(b1) : "memory");
+      }
+      // scale log2(e) 2^-up: of the scores
+      if (lane == 0) factor[r] = a.scale_log2 * __int_as_float((127 - up / 2) << 23) * __int_as_float((127 - up + up / 2) << 23);
+    }
+    __syncthreads();
+    float o[NT][D / 16][4];
+    float m[NT][2], mv[NT][2], l[NT][2], ratio[NT][2], f[NT][2];
+    int limit[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+#pragma unroll
+      for (int i = 0; i < D / 16; i++)
+#pragma unroll
+        for (int c = 0; c < 4; c++) o[n][i][c] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; c++) {
+        const int r = n * 8 + 2 * t + c;
+        m[n][c] = mv[n][c] = -CUDART_INF_F;
+        l[n][c] = ratio[n][c] = 0.f;
+        f[n][c] = factor[r];
+        limit[n][c] = u.pos0 + min(r / u.gp, u.n_tok - 1);
+      }
+    }
+    for (int i = 0; i < steps; i++) {
+      copies_wait<SM::kStages - 2>();
+      __syncwarp();  // step i is there, and step i - 1 has been read
+      fetch(i + SM::kStages - 1);
+      const int stage = i % SM::kStages;
+      const uint32_t at = ring + stage * SM::kSliceBytes;
+      const float2 scale = *reinterpret_cast<const float2 *>(scales + stage * 2);
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; n++) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      {
+        uint32_t k0[kWords], k1[kWords];  // keys g and g + 8
+#pragma unroll
+        for (int w = 0; w < kWords; w += 4) {
+          const int c = D == 128 ? (2 * t + w / 4) ^ g : t ^ ((g >> 1) & 3);
+          const uint4 x = lds128(at + g * D + c * 16), y = lds128(at + (g + 8) * D + c * 16);
+          k0[w] = x.x; k0[w + 1] = x.y; k0[w + 2] = x.z; k0[w + 3] = x.w;
+          k1[w] = y.x; k1[w + 1] = y.y; k1[w + 2] = y.z; k1[w + 3] = y.w;
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; k++) {
+          const uint32_t a0 = half_lo(k0[k]), a1 = half_lo(k1[k]), a2 = half_hi(k0[k]), a3 = half_hi(k1[k]);
+#pragma unroll
+          for (int n = 0; n < NT; n++) {
+            const uint2 b = lds64(q_at + ((n * kSteps + k) * 32 + lane) * 8);
+            mma(s[n], a0, a1, a2, a3, b.x, b.y);
+          }
+        }
+      }
+      // s[n][0], [1]: key g of rows 2 t, 2 t + 1; [2], [3]: key g + 8
+      const int key = (first + i * kWarps) * kSlice;
+      // V's scale is below 2^(fv + 1); not below -117, so that `ratio` is finite for a zero one too
+      const float fv = (float)max((int)(__float_as_uint(scale.y) >> 23 & 255) - 127, -117);
+      bool move = false;
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          const float fk = f[n][c] * scale.x;
+          s[n][c] *= fk;
+          s[n][2 + c] *= fk;
+          if (key + g > limit[n][c]) s[n][c] = -CUDART_INF_F;
+          if (key + g + 8 > limit[n][c]) s[n][2 + c] = -CUDART_INF_F;
+          move |= fmaxf(s[n][c], s[n][2 + c]) > fminf(m[n][c], mv[n][c] - fv) + kLag;
+        }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int c = 0; c < 2; c++) {
+            float top = fmaxf(s[n][c], s[n][2 + c]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float mn = fmaxf(m[n][c], top), vn = fmaxf(mv[n][c], top + fv);
+            const bool some = mn != -CUDART_INF_F;  // something is visible by now
+            l[n][c] *= some ? ex2(m[n][c] - mn) : 0.f;
+            const float down = some ? ex2(mv[n][c] - vn) : 0.f;
+            ratio[n][c] = some ? ex2(mn - vn + kShift) : 0.f;
+            m[n][c] = mn;
+            mv[n][c] = vn;
+#pragma unroll
+            for (int j = 0; j < D / 16; j++) {
+              o[n][j][c] *= down;
+              o[n][j][2 + c] *= down;
+            }
+          }
+      }
+      uint32_t p[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        float w[4];
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          const float off = m[n][c] == -CUDART_INF_F ? 0.f : m[n][c];
+          const float p0 = ex2(s[n][c] - off), p1 = ex2(s[n][2 + c] - off), fw = scale.y * ratio[n][c];
+          l[n][c] += p0 + p1;
+          w[c] = p0 * fw;
+          w[2 + c] = p1 * fw;
+        }
+        p[n][0] = transpose8(pack_f16(w[0], w[1]));
+        p[n][1] = transpose8(pack_f16(w[2], w[3]));
+      }
+      // V^T: elements g D / 8 .. of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9; products 2 j and
+      // 2 j + 1 of 16 x 8 take the elements 4 j .. + 3
+      constexpr int kWordsV = D / 32;
+      uint32_t v[4][kWordsV];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int r = 2 * t + (j & 1) + (j >> 1) * 8;
+        if constexpr (D == 128) {
+          const uint4 x = lds128(at + kSlice * D + r * D + ((g ^ (r & 7)) << 4));
+          v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
+        } else {
+          const uint2 x = lds64(at + kSlice * D + r * D + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
+          v[j][0] = x.x; v[j][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < kWordsV; w++) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const uint32_t x = __byte_perm(v[0][w], v[1][w], h ? 0x7362 : 0x5140), y = __byte_perm(v[2][w], v[3][w], h ? 0x7362 : 0x5140);
+          const uint32_t a0 = half_lo(x), a1 = half_hi(x), a2 = half_lo(y), a3 = half_hi(y);
+#pragma unroll
+          for (int n = 0; n < NT; n++) mma(o[n][2 * w + h], a0, a1, a2, a3, p[n][0], p[n][1]);
+        }
+      }
+    }
+    copies_wait<0>();
+    // ---- the eight warps' results, joined in order
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int c = 0; c < 2; c++)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
+    __syncthreads();  // every warp's ring has been read
+    const int rows = u.n_tok * u.gp;
+    float *place = reinterpret_cast<float *>(sm) + warp * NT * 8 * SM::kRow;
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int c = 0; c < 2; c++) {
+        const int r = n * 8 + 2 * t + c;
+        if (r >= rows) continue;
+        float *to = place + r * SM::kRow + g * (D / 8);
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 2)
+          *reinterpret_cast<float4 *>(to + 2 * j) = make_float4(o[n][j][c], o[n][j][2 + c], o[n][j + 1][c], o[n][j + 1][2 + c]);
+        if (g == 0) {
+          float *x = join + (warp * NT * 8 + r) * 3;
+          x[0] = m[n][c];
+          x[1] = l[n][c];
+          x[2] = mv[n][c];
+        }
+      }
+    __syncthreads();
+    bool finite = true;
+    const bool part = u.slot >= 0;
+    for (int item = tid; item < rows * (D / 4); item += kThreads) {
+      const int r = item / (D / 4), d4 = item % (D / 4);
+      float top = -CUDART_INF_F, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; w++) top = fmaxf(top, join[(w * NT * 8 + r) * 3]);
+      const float base = top == -CUDART_INF_F ? 0.f : top;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; w++) {
+        const float *x = join + (w * NT * 8 + r) * 3;
+        sum += x[1] * ex2(x[0] - base);
+        const float fo = ex2(x[2] - base - kShift);
+        const float4 z = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm) + (w * NT * 8 + r) * SM::kRow + d4 * 4);
+        y.x += fo * z.x; y.y += fo * z.y; y.z += fo * z.z; y.w += fo * z.w;
+      }
+      if (part) {
+        a.part_o[((long long)u.slot * (D / 4) + d4) * Shape8::kRows + r] = y;
+        if (d4 == 0) a.part_ml[(long long)u.slot * Shape8::kRows + r] = make_float2(top, sum);
+      } else {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
+        finite &= fabsf(y.x) < kBf16Inf && fabsf(y.y) < kBf16Inf && fabsf(y.z) < kBf16Inf && fabsf(y.w) < kBf16Inf;
+        const long long at = (long long)(u.row0 + r / u.gp) * a.H + u.head0 + r % u.gp;
+        __nv_bfloat162 z[2] = {__floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + d4 * 4) = *reinterpret_cast<uint2 *>(z);
+        if (d4 == 0 && a.lse) a.lse[at] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * 0.69314718056f;
+      }
+    }
+    if (!finite && a.flags) atomicOr(a.flags, kFlagNonfinite);
+  }
+}
+
+template <int D, int NT>
+std::atomic<uint64_t> allowed{0};
+
+template <int D, int NT>
+cudaError_t launch(const AttnArgs &a, int blocks, cudaStream_t stream) {
+  const cudaError_t e = allow_smem(reinterpret_cast<const void *>(&gdn_attn8_kernel<D, NT>), Smem<D, NT>::kBytes, allowed<D, NT>);
+  if (e != cudaSuccess) return e;
+  gdn_attn8_kernel<D, NT><<<blocks, kThreads, Smem<D, NT>::kBytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+AttnLaunch attn8_launch(AttnArgs &a) { return attn_plan_launch<Shape8>(a, 2 * sm_count()); }
+
+cudaError_t launch_attn8(const AttnArgs &a, int d, const AttnLaunch &l, cudaStream_t stream) {
+  // one group of 8 rows where no sequence has more
+  const bool one = !a.cu && (long long)a.T * (a.H / a.HKV) <= 8;
+  const cudaError_t e = d == 64 ? (one ? launch<64, 1>(a, l.blocks, stream) : launch<64, 2>(a, l.blocks, stream))
+                                : (one ? launch<128, 1>(a, l.blocks, stream) : launch<128, 2>(a, l.blocks, stream));
+  if (e != cudaSuccess || !l.split || l.blocks < 2) return e;
+  return launch_attn8_merge(a, d, l.blocks, stream);
+}
+
+}  // namespace gdn

@@ -144,7 +144,10 @@ struct AttnArgs {
   float2 *part_ml;             // nullptr when nothing is cut
   AttnJob *jobs;               // [blocks] what is to be joined
   uint32_t *flags;             // device status word, or nullptr
+  const float *k_scale, *v_scale;  // of a cache in 8 bits: [n_pages][page_size / kScaleBlock][HKV]
 };
+// Tokens of a cache in 8 bits that share a scale (for each head).
+constexpr int kScaleBlock = 16;
 // Writes the keys and values of new tokens into the pages of a cache.
 struct AppendArgs {
   const void *k, *v;
@@ -154,6 +157,39 @@ struct AppendArgs {
   long long k_stride, v_stride;  // bytes between tokens
   int row_bytes;                 // HKV * d elements
   int page_size, max_pages, n_pages, max_len;
+  uint32_t *flags;
+};
+
+// The same into a cache in 8 bits.
+struct Append8Args {
+  const void *k, *v;
+  uint8_t *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  const int32_t *cu, *kv_lens, *table;
+  int n_seqs, T, Ttot;
+  long long k_stride, v_stride;  // elements between tokens
+  int HKV;
+  int page_size, max_pages, n_pages, max_len;
+  uint32_t *flags;
+};
+// Copies pages of a cache (gdn_kv_copy.cu): arrays of `bytes[i]` bytes a page.
+struct CopyPagesArgs {
+  char *base[4];       // k, v, and of a cache in 8 bits their scales (or nullptr)
+  long long bytes[4];
+  const int32_t *src, *dst;
+  int n, n_pages;
+  uint32_t *flags;
+};
+// Rotary positions (gdn_rope.cu) of `HQ` query and `HK` key heads.
+struct RopeArgs {
+  const void *q, *k;
+  void *qo, *ko;
+  long long q_stride, k_stride, qo_stride, ko_stride;  // elements between tokens
+  const float *inv_freq;
+  const int32_t *cu, *kv_lens;  // either may be nullptr
+  int n_seqs, T, Ttot;
+  int HQ, HK, rot;
+  float mscale, sign;
   uint32_t *flags;
 };
 
@@ -244,6 +280,13 @@ int sm_count();  // of the current device
 // has a bit for each of the first 64).
 cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done);
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream);
+// the same over a cache in 8 bits (bf16 queries; gdn_attn8.cu)
+AttnLaunch attn8_launch(AttnArgs &a);
+cudaError_t launch_attn8(const AttnArgs &a, int d, const AttnLaunch &l, cudaStream_t stream);
+cudaError_t launch_attn8_merge(const AttnArgs &a, int d, int blocks, cudaStream_t stream);
+cudaError_t launch_kv_append8(const Append8Args &a, int d, int dtype, cudaStream_t stream);
+cudaError_t launch_kv_copy_pages(const CopyPagesArgs &a, cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs &a, int d, bool interleaved, int dtype, cudaStream_t stream);
 // S_out = M S_in + S_seg, per state
 cudaError_t launch_state_combine(const TransferArgs &a, cudaStream_t stream);
 // token-serial form; dv a multiple of 32

@@ -28,6 +28,7 @@ GDN_GATE_SCALAR = 0
 GDN_GATE_PER_KEY = 1
 GDN_F32 = 0
 GDN_BF16 = 1
+GDN_E4M3 = 2
 
 GDN_ACT_NONE = 0
 GDN_ACT_SILU = 1
@@ -46,6 +47,8 @@ EXPORTED = ("gdn_version", "gdn_status_string", "gdn_chunk_fwd_workspace_bytes",
             "gdn_l2norm_fwd", "gdn_rmsnorm_gated_fwd", "gdn_state_combine",
             "gdn_attn_fwd_workspace_bytes", "gdn_attn_fwd",
             "gdn_attn_paged_fwd_workspace_bytes", "gdn_attn_paged_fwd", "gdn_kv_cache_append",
+            "gdn_kv_cache_append_fp8", "gdn_attn_paged_fp8_fwd_workspace_bytes",
+            "gdn_attn_paged_fp8_fwd", "gdn_kv_cache_copy_pages", "gdn_rope_fwd", "gdn_rope_bwd",
             "gdn_selftest_wait", "gdn_read_device_flags")
 
 _lock = threading.Lock()
@@ -116,6 +119,21 @@ def load(path: Optional[str] = None):
         lib.gdn_kv_cache_append.argtypes = ([vp] * 7 + [i32] * 5 + [i64] * 2 + [i32] * 4 +
                                             [vp, vp])
         lib.gdn_kv_cache_append.restype = i32
+        lib.gdn_kv_cache_append_fp8.argtypes = ([vp] * 9 + [i32] * 5 + [i64] * 2 + [i32] * 4 +
+                                                [vp, vp])
+        lib.gdn_kv_cache_append_fp8.restype = i32
+        lib.gdn_attn_paged_fp8_fwd_workspace_bytes.argtypes = [i32] * 8
+        lib.gdn_attn_paged_fp8_fwd_workspace_bytes.restype = sz
+        lib.gdn_attn_paged_fp8_fwd.argtypes = ([vp] * 10 + [i32] * 6 + [i64] + [i32] * 3 +
+                                               [f32, i32, vp, vp, sz, vp])
+        lib.gdn_attn_paged_fp8_fwd.restype = i32
+        lib.gdn_kv_cache_copy_pages.argtypes = [vp] * 6 + [i32] * 6 + [vp, vp]
+        lib.gdn_kv_cache_copy_pages.restype = i32
+        for name in ("gdn_rope_fwd", "gdn_rope_bwd"):
+            fn = getattr(lib, name)
+            fn.argtypes = ([vp] * 5 + [i32] * 2 + [f32] + [vp] * 2 + [i32] * 6 + [i64] * 4 +
+                           [i32, vp, vp])
+            fn.restype = i32
         lib.gdn_selftest_wait.argtypes = [vp, ctypes.c_longlong, i32, vp]
         lib.gdn_selftest_wait.restype = i32
         lib.gdn_read_device_flags.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
@@ -644,6 +662,267 @@ def gdn_kv_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
         n_pages, dt, _addr(flags), raw)
     if status != GDN_OK:
         raise GdnError(status, "gdn_kv_cache_append")
+
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _scales(k_scale, v_scale, k_cache, dev) -> None:
+    """Check the scales of a cache in 8 bits."""
+    n_pages, page_size, HKV, _ = k_cache.shape
+    shape, f32 = (n_pages, page_size // 16, HKV), torch.float32
+    if (k_scale.shape == shape and v_scale.shape == shape and k_scale.dtype is f32
+            and v_scale.dtype is f32 and k_scale.device == dev and v_scale.device == dev
+            and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        return
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _check(t, name, dev)
+        if t.dtype != f32:
+            raise TypeError(f"{name} must be float32")
+    raise ValueError("k_scale and v_scale must be [n_pages, page_size / 16, HKV]")
+
+
+def gdn_kv_cache_append_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                            v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                            block_table: torch.Tensor, kv_lens: torch.Tensor, *,
+                            cu_seqlens: Optional[torch.Tensor] = None,
+                            flags: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> None:
+    """:func:`gdn_kv_cache_append` into a cache held in 8 bits, in place.
+
+    k, v ``[B, T, HKV, d]`` or packed (bf16 or fp32); caches float8_e4m3fn ``[n_pages,
+    page_size, HKV, d]``; scales fp32 ``[n_pages, page_size / 16, HKV]``, a power of two for
+    each block of 16 positions and head, which grows with what is written into the block.
+    """
+    lib = _lib or load()
+    if k.dim() != 4 or v.shape != k.shape or k_cache.dim() != 4:
+        raise ValueError("k and v must be [B, T, HKV, d], the caches [n_pages, page_size, HKV, d]")
+    B, T, HKV, d = k.shape
+    dev, dtype = k.device, k.dtype
+    dt = _dtype_code(dtype)
+    ks, vs = _tokens(k, "k", dev, dtype, B, T), _tokens(v, "v", dev, dtype, B, T)
+    n_seqs = _sequences(cu_seqlens, B, dev)
+    page_size, max_pages, n_pages = _cache(k_cache, v_cache, block_table, kv_lens, n_seqs, HKV, d,
+                                           _E4M3, dev)
+    _scales(k_scale, v_scale, k_cache, dev)
+    if flags is not None:
+        _given(k, None, None, flags, None, dev)
+    raw = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream)
+    status = lib.gdn_kv_cache_append_fp8(
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), _addr(cu_seqlens), n_seqs,
+        B, T, HKV, d, ks, vs, page_size, max_pages, n_pages, dt, _addr(flags), raw)
+    if status != GDN_OK:
+        raise GdnError(status, "gdn_kv_cache_append_fp8")
+
+
+def gdn_attn_paged_fp8_fwd_workspace_bytes(B: int, T: int, H: int, HKV: int, d: int, n_seqs: int,
+                                           page_size: int, max_pages: int) -> int:
+    return int(load().gdn_attn_paged_fp8_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, page_size,
+                                                             max_pages))
+
+
+def gdn_attn_paged_fp8_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           k_scale: torch.Tensor, v_scale: torch.Tensor,
+                           block_table: torch.Tensor, kv_lens: torch.Tensor, *,
+                           scale: Optional[float] = None,
+                           cu_seqlens: Optional[torch.Tensor] = None,
+                           o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                           output_lse: bool = True, flags: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None,
+                           stream: Optional[torch.cuda.Stream] = None
+                           ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """:func:`gdn_attn_paged_fwd` over a cache held in 8 bits
+    (:func:`gdn_kv_cache_append_fp8`); q and o are bf16; returns ``(o, lse)``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gdn_attn_paged_fp8_fwd(q, k_cache, v_cache, k_scale, v_scale, block_table,
+                                          kv_lens, scale=scale, cu_seqlens=cu_seqlens, o=o,
+                                          lse=lse, output_lse=output_lse, flags=flags,
+                                          workspace=workspace)
+    lib = _lib or load()
+    if q.dim() != 4 or k_cache.dim() != 4:
+        raise ValueError("q must be [B, T, H, d] and the caches [n_pages, page_size, HKV, d]")
+    B, T, H, d = q.shape
+    HKV, dev, dtype = k_cache.shape[2], q.device, q.dtype
+    dt = _dtype_code(dtype)
+    qs = _tokens(q, "q", dev, dtype, B, T)
+    n_seqs = _sequences(cu_seqlens, B, dev)
+    page_size, max_pages, n_pages = _cache(k_cache, v_cache, block_table, kv_lens, n_seqs, HKV, d,
+                                           _E4M3, dev)
+    _scales(k_scale, v_scale, k_cache, dev)
+    if not (o is lse is flags is workspace is None):
+        _given(q, o, lse, flags, workspace, dev)
+    if scale is None:
+        scale = d ** -0.5
+    if o is None:
+        o = torch.empty_like(q) if qs == H * d else torch.empty(q.shape, dtype=dtype, device=dev)
+    if lse is None and output_lse:
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), o.data_ptr(),
+            _addr(lse), _addr(cu_seqlens), n_seqs, B, T, H, HKV, d, qs, page_size, max_pages,
+            n_pages, scale, dt, _addr(flags))
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    if workspace is not None:
+        status = lib.gdn_attn_paged_fp8_fwd(*args, workspace.data_ptr(),
+                                            workspace.numel() * workspace.element_size(), raw)
+    else:
+        status = lib.gdn_attn_paged_fp8_fwd(*args, None, 0, raw)
+        if status == GDN_ERR_WORKSPACE:
+            nbytes = lib.gdn_attn_paged_fp8_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, page_size,
+                                                                max_pages)
+            workspace = _workspace(nbytes, dev)
+            status = lib.gdn_attn_paged_fp8_fwd(*args, workspace.data_ptr(), nbytes, raw)
+    if status != GDN_OK:
+        raise GdnError(status, "gdn_attn_paged_fp8_fwd")
+    return o, lse
+
+
+def gdn_kv_cache_copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tensor,
+                            dst: torch.Tensor, *, k_scale: Optional[torch.Tensor] = None,
+                            v_scale: Optional[torch.Tensor] = None,
+                            flags: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Copy page ``src[i]`` of both caches to page ``dst[i]``, in place (int32 ``[n]`` on the
+    device): bf16 and fp32 caches, and float8_e4m3fn ones with their scales.
+
+    Every source is read as it was before the call.  A page that is a destination twice, or a
+    destination and another pair's source, is left as it is (GDN_FLAG_BAD_SEQLENS in ``flags``).
+    """
+    lib = _lib or load()
+    dev, dtype, shape = k_cache.device, k_cache.dtype, k_cache.shape
+    dt = GDN_E4M3 if dtype is _E4M3 else _dtype_code(dtype)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("src", src), ("dst", dst)):
+        _check(t, name, dev)
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != dtype:
+        raise ValueError("k_cache and v_cache must be [n_pages, page_size, HKV, d] of one type")
+    if src.dtype != torch.int32 or dst.dtype != torch.int32:
+        raise TypeError("src and dst must be int32")
+    if src.dim() != 1 or dst.shape != src.shape:
+        raise ValueError("src and dst must be [n]")
+    if (dt == GDN_E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go with a float8_e4m3fn cache, and with no other")
+    if k_scale is not None:
+        _scales(k_scale, v_scale, k_cache, dev)
+    if flags is not None:
+        _given(k_cache, None, None, flags, None, dev)
+    raw = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream)
+    n_pages, page_size, HKV, d = shape
+    status = lib.gdn_kv_cache_copy_pages(
+        k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), src.data_ptr(),
+        dst.data_ptr(), src.shape[0], HKV, d, page_size, n_pages, dt, _addr(flags), raw)
+    if status != GDN_OK:
+        raise GdnError(status, "gdn_kv_cache_copy_pages")
+
+
+def _rope(entry: str, q, k, inv_freq, interleaved, mscale, kv_lens, cu_seqlens, q_out, k_out,
+          flags, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _rope(entry, q, k, inv_freq, interleaved, mscale, kv_lens, cu_seqlens, q_out,
+                         k_out, flags, None)
+    lib = _lib or load()
+    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[3] != q.shape[3])):
+        raise ValueError("q [B, T, H, d] and k [B, T, HKV, d]: inconsistent shapes")
+    B, T, H, d = q.shape
+    dev, dtype = q.device, q.dtype
+    dt = _dtype_code(dtype)
+    qs = _tokens(q, "q", dev, dtype, B, T)
+    n_seqs = _sequences(cu_seqlens, B, dev)
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32:
+        raise ValueError("inv_freq must be float32 [rot / 2]")
+    _check(inv_freq, "inv_freq", dev)
+    if kv_lens is not None:
+        _check(kv_lens, "kv_lens", dev)
+        if kv_lens.dtype != torch.int32:
+            raise TypeError("kv_lens must be int32")
+        if kv_lens.shape != (n_seqs,):
+            raise ValueError(f"kv_lens must be [{n_seqs}]")
+    if flags is not None:
+        _given(q, None, None, flags, None, dev)
+    if q_out is None:
+        q_out = torch.empty((B, T, H, d), dtype=dtype, device=dev)
+        qos = H * d
+    else:
+        qos = qs if q_out is q else _tokens(q_out, "q_out", dev, dtype, B, T)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must match q in shape")
+    HKV = ks = kos = 0
+    if k is not None:
+        HKV = k.shape[2]
+        ks = _tokens(k, "k", dev, dtype, B, T)
+        if k_out is None:
+            k_out = torch.empty((B, T, HKV, d), dtype=dtype, device=dev)
+            kos = HKV * d
+        else:
+            kos = ks if k_out is k else _tokens(k_out, "k_out", dev, dtype, B, T)
+            if k_out.shape != k.shape:
+                raise ValueError("k_out must match k in shape")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    status = getattr(lib, entry)(
+        q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out), inv_freq.data_ptr(),
+        2 * inv_freq.shape[0], 1 if interleaved else 0, mscale, _addr(kv_lens), _addr(cu_seqlens),
+        n_seqs, B, T, H, HKV, d, qs, ks, qos, kos, dt, _addr(flags),
+        torch._C._cuda_getCurrentRawStream(dev.index))
+    if status != GDN_OK:
+        raise GdnError(status, entry)
+    return q_out, k_out
+
+
+def gdn_rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor, *,
+                 interleaved: bool = False, mscale: float = 1.0,
+                 kv_lens: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 flags: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None
+                 ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Rotary positions of q ``[B, T, H, d]`` and k ``[B, T, HKV, d]`` (or None); returns
+    ``(q_out, k_out)``.
+
+    The first ``rot = 2 * len(inv_freq)`` elements of a head are turned: pair i, elements
+    (i, i + rot / 2) or, interleaved, (2 i, 2 i + 1), by position * inv_freq[i]
+    (:func:`rope_inv_freq`), and multiplied by mscale.  Positions are those of attention: the
+    new tokens are the last of kv_lens (int32 ``[N]``, new tokens included), or, without
+    kv_lens, the whole sequence.  q and k may be slices of one projection's output; pass
+    ``q_out=q, k_out=k`` to turn them in place.
+    """
+    return _rope("gdn_rope_fwd", q, k, inv_freq, interleaved, mscale, kv_lens, cu_seqlens, q_out,
+                 k_out, flags, stream)
+
+
+def gdn_rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], inv_freq: torch.Tensor, *,
+                 interleaved: bool = False, mscale: float = 1.0,
+                 kv_lens: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 flags: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None
+                 ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The gradient of :func:`gdn_rope_fwd`: of its outputs to that of its inputs, same
+    arguments."""
+    return _rope("gdn_rope_bwd", dq, dk, inv_freq, interleaved, mscale, kv_lens, cu_seqlens, q_out,
+                 k_out, flags, stream)
+
+
+def rope_inv_freq(rot: int, base: float = 10000.0, *, stretch: float = 1.0,
+                  trained: Optional[int] = None, fast: float = 32.0, slow: float = 1.0,
+                  device="cpu") -> torch.Tensor:
+    """Frequencies of :func:`gdn_rope_fwd`, base^(-2 i / rot) for i < rot / 2, as fp32.
+
+    ``stretch`` > 1 is for contexts that many times longer than trained on: every frequency is
+    divided by it (positions are squeezed into the trained range), or, with ``trained`` (the
+    length trained on) given, each by its wavelength: pairs that turn ``fast`` times or more
+    within that length keep theirs, those that turn ``slow`` times or less are divided, those
+    between in part.  The mscale that is usual with the latter is 0.1 ln(stretch) + 1.
+    """
+    if rot <= 0 or rot % 2 or not base > 0 or not stretch >= 1 or not fast > slow:
+        raise ValueError("rot even and positive, base positive, stretch at least 1, fast above slow")
+    freq = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    keep = torch.zeros_like(freq)
+    if trained is not None:
+        keep = ((trained * freq / (2 * torch.pi) - slow) / (fast - slow)).clamp(0, 1)
+    return (freq * keep + freq / stretch * (1 - keep)).to(device=device, dtype=torch.float32)
 
 
 def gdn_selftest_wait(flags: torch.Tensor, budget_cycles: int, complete: bool, *,

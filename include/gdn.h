@@ -76,7 +76,9 @@ typedef enum gdn_gate_mode {
 
 typedef enum gdn_dtype {
   GDN_F32 = 0,  /* q, k, v, o are float32 */
-  GDN_BF16 = 1  /* q, k, v, o are bfloat16 */
+  GDN_BF16 = 1, /* q, k, v, o are bfloat16 */
+  GDN_E4M3 = 2  /* 8-bit floating point (4 exponent, 3 mantissa bits), of caches
+                   only: gdn_kv_cache_copy_pages */
 } gdn_dtype;
 
 typedef enum gdn_activation {
@@ -435,6 +437,110 @@ GDN_API gdn_status gdn_kv_cache_append(const void *k, const void *v, void *k_cac
                                        int HKV, int d, int64_t k_stride, int64_t v_stride,
                                        int page_size, int max_pages, int n_pages, int dtype,
                                        uint32_t *flags, gdn_stream_t stream);
+
+/*
+ * A cache in 8 bits.  Half the bytes of a bf16 cache, and so up to twice the
+ * sequences or lengths in the same memory and half the time of a decode step.
+ *   k_cache, v_cache  [n_pages, page_size, HKV, d] e4m3 (bytes: 4 exponent, 3
+ *               mantissa bits, bias 7, largest 448, 0x7f and 0xff NaN)
+ *   k_scale, v_scale  [n_pages, page_size / 16, HKV] fp32: a scale for each
+ *               block of 16 positions of a page and head; an element stands for
+ *               its 8-bit value times its block's scale
+ * Everything else as for the caches above (pages, tables, lengths, flags,
+ * alignment: scales 4 bytes).
+ *
+ * gdn_kv_cache_append_fp8 -- k and v (dtype F32 or BF16) of the new tokens into
+ * the pages.  Of a block that new tokens reach,
+ *     need = the smallest power of two, 2^-117 or more, for which the new
+ *            elements' magnitudes are at most 448 need (non-finite ones aside),
+ *     a'   = need where no earlier token of the sequence lies in the block,
+ *            max(a, need) where one does (a: the block's scale so far);
+ *     earlier elements c become round(c a / a'), new ones round(x / a'),
+ * rounded to the nearest e4m3 value, ties to even (quotients in fp32).  With
+ * powers of two an earlier element changes only where it falls below 2^-6 a'.
+ * A non-finite x becomes NaN and sets GDN_FLAG_NONFINITE.  Positions of a block
+ * that lie behind the sequence's last token keep their bytes.  A token at a
+ * negative position is left out, one in a bad page too.  A block may belong to
+ * one sequence of a call only, since its earlier elements may be rewritten: a
+ * page that two sequences share is to be copied before one of them writes to it
+ * (gdn_kv_cache_copy_pages); what a block holds that two sequences of one call
+ * write is not specified.
+ */
+GDN_API gdn_status gdn_kv_cache_append_fp8(const void *k, const void *v, void *k_cache,
+                                           void *v_cache, float *k_scale, float *v_scale,
+                                           const int32_t *block_table, const int32_t *kv_lens,
+                                           const int32_t *cu_seqlens, int n_seqs, int B, int T,
+                                           int HKV, int d, int64_t k_stride, int64_t v_stride,
+                                           int page_size, int max_pages, int n_pages, int dtype,
+                                           uint32_t *flags, gdn_stream_t stream);
+
+/*
+ * gdn_attn_paged_fp8_fwd -- gdn_attn_paged_fwd over such a cache; q and o bf16
+ * (dtype BF16; others are GDN_ERR_UNSUPPORTED).  Scales are any positive finite
+ * numbers.  Numerics: e4m3 values are exact in the tensor cores' operands; the
+ * weights are rounded to 16 bits for their product with v.
+ */
+GDN_API size_t gdn_attn_paged_fp8_fwd_workspace_bytes(int B, int T, int H, int HKV, int d,
+                                                      int n_seqs, int page_size, int max_pages);
+GDN_API gdn_status gdn_attn_paged_fp8_fwd(const void *q, const void *k_cache, const void *v_cache,
+                                          const float *k_scale, const float *v_scale,
+                                          const int32_t *block_table, const int32_t *kv_lens,
+                                          void *o, float *lse, const int32_t *cu_seqlens,
+                                          int n_seqs, int B, int T, int H, int HKV, int d,
+                                          int64_t q_stride, int page_size, int max_pages,
+                                          int n_pages, float scale, int dtype, uint32_t *flags,
+                                          void *workspace, size_t workspace_bytes,
+                                          gdn_stream_t stream);
+
+/*
+ * gdn_kv_cache_copy_pages -- page src[i] to page dst[i] (int32 [n_copies], device)
+ * of both caches, i < n_copies: as a sequence forks (both go on writing to its
+ * last page) or a pool is put in order.  dtype F32, BF16 or E4M3; k_scale and
+ * v_scale for E4M3 (copied too), NULL for the others.  Every source is read as it
+ * was before the call: a page that is the destination of two pairs, or of one and
+ * the source of another, is left as it is, and so is one with a page number out of
+ * range in its pair; both set GDN_FLAG_BAD_SEQLENS.
+ */
+GDN_API gdn_status gdn_kv_cache_copy_pages(void *k_cache, void *v_cache, float *k_scale,
+                                           float *v_scale, const int32_t *src, const int32_t *dst,
+                                           int n_copies, int HKV, int d, int page_size,
+                                           int n_pages, int dtype, uint32_t *flags,
+                                           gdn_stream_t stream);
+
+/*
+ * gdn_rope_fwd -- rotary positions: the first `rot` elements of every head of q
+ * [B, T, H, d] and k [B, T, HKV, d] turned by their token's position p (as for
+ * attention: p = L - nq + t with kv_lens, new tokens included; t without), each
+ * pair (x, y) by the angle p * inv_freq[i]:
+ *     x' = mscale (x cos - y sin),   y' = mscale (x sin + y cos)
+ * Pair i is elements (i, i + rot / 2), or, interleaved = 1, (2 i, 2 i + 1); the
+ * other d - rot elements are copied.  inv_freq [rot / 2] fp32, finite and below
+ * 2^63 in magnitude: frequencies stretched for long contexts are the caller's
+ * choice, mscale the factor that goes with them (1: none).  Angles are off by at
+ * most 2^-29 for every position; outputs rounded once.
+ * gdn_rope_bwd -- its gradient: dq, dk of the outputs to those of the inputs (the
+ * same with -sin).
+ *
+ * dtype F32 or BF16; d 64 or 128, rot a multiple of 16.  HKV = 0 with k and k_out
+ * NULL: queries only; H need be no multiple of HKV.  Each array has a token stride
+ * of its own (as for attention).  An output may be its own input at the same
+ * stride; other than that outputs have no element in common with any array, though
+ * they may interleave with one by token (slices of one projection's output at its
+ * stride).  Tokens of a sequence with malformed lengths are not written
+ * (GDN_FLAG_BAD_SEQLENS).
+ */
+GDN_API gdn_status gdn_rope_fwd(const void *q, const void *k, void *q_out, void *k_out,
+                                const float *inv_freq, int rot, int interleaved, float mscale,
+                                const int32_t *kv_lens, const int32_t *cu_seqlens, int n_seqs,
+                                int B, int T, int H, int HKV, int d, int64_t q_stride,
+                                int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride,
+                                int dtype, uint32_t *flags, gdn_stream_t stream);
+GDN_API gdn_status gdn_rope_bwd(const void *dq, const void *dk, void *dq_in, void *dk_in,
+                                const float *inv_freq, int rot, int interleaved, float mscale,
+                                const int32_t *kv_lens, const int32_t *cu_seqlens, int n_seqs,
+                                int B, int T, int H, int HKV, int d, int64_t dq_stride,
+                                int64_t dk_stride, int64_t dq_in_stride, int64_t dk_in_stride,
+                                int dtype, uint32_t *flags, gdn_stream_t stream);
 
 /*
  * gdn_selftest_wait -- exercise the bounded wait that every mbarrier wait of
