@@ -566,8 +566,9 @@ cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &don
   return e;
 }
 
-cudaError_t launch_attn8_merge(const AttnArgs &a, int d, int blocks, cudaStream_t stream) {
-  return d == 64 ? merge<Shape8, 64, true>(a, blocks, stream) : merge<Shape8, 128, true>(a, blocks, stream);
+cudaError_t launch_attn8_merge(const AttnArgs &a, int d, bool few, int blocks, cudaStream_t stream) {
+  if (few) return d == 64 ? merge<Shape8, 64, true>(a, blocks, stream) : merge<Shape8, 128, true>(a, blocks, stream);
+  return d == 64 ? merge<TcShape, 64, true>(a, blocks, stream) : merge<TcShape, 128, true>(a, blocks, stream);
 }
 
 AttnLaunch attn_launch(AttnArgs &a, int d, int dtype) {

@@ -86,7 +86,9 @@ struct AttnShape {
   static constexpr int kRows = ROWS, kPack = PACK, kTile = TILE, kFew = FEW;
   static constexpr int kMinGrain = MIN_GRAIN, kWhole = WHOLE, kCut = CUT;
   static constexpr int kWide = WIDE, kOver = OVER, kNarrow = NARROW, kPackedOver = PACKED_OVER;
+  static constexpr int kOnly = 0;  // sequences: all; 1: with at most kFewRows rows for a key/value head; 2: with more
 };
+constexpr int kFewRows = 16;
 // The bf16 kernel's (gdn_attn_tc.cu).  A packed unit's tile takes 3/4 of an
 // unpacked one's: 1/2, 2/3, 3/4 and 1 gave 129, 107, 104 and 109 us for two
 // chunks of up to 500 tokens among 14 single ones (32 heads of 64), and 164, 153,
@@ -97,8 +99,14 @@ struct AttnShape {
 // Smallest grains of 4, 8 and 16 tiles were alike in all cases measured: below
 // that a piece's start and the joining outweigh its tiles.
 using TcShape = AttnShape<256, 128, 128, 4, 8, 3, 6, 128, 3, 3, 40>;
-// The kernel's for few rows over a cache in 8 bits (gdn_attn8.cu).
-using Shape8 = AttnShape<16, 16, 128, 2, 4, 2, 4, 16, 1, 3>;
+// Over a cache in 8 bits two kernels share a call's sequences: few rows go to that of
+// gdn_attn8.cu, more to the bf16 one's over such a cache.
+struct Shape8 : AttnShape<kFewRows, kFewRows, 128, 2, 4, 2, 4, kFewRows, 1, 3> {
+  static constexpr int kOnly = 1;
+};
+struct TcShape8 : TcShape {
+  static constexpr int kOnly = 2;
+};
 constexpr int kMaxGrain = 6;   // log2 of the largest one that is tried
 constexpr float kBf16Inf = 0x1.ffp127f;  // what rounds to infinity in bf16
 
@@ -160,6 +168,17 @@ __host__ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &a, int n, b
   }
   s.past = s.len - s.nq;
   s.base = s.past > 0 ? s.past : 0;
+  return s;
+}
+
+// The same as a kernel with shape S sees it: nq = 0 also where another one has it.
+template <class S>
+__host__ __device__ __forceinline__ AttnSeq attn_seq_of(const AttnArgs &a, int n, bool &bad) {
+  AttnSeq s = attn_seq(a, n, bad);
+  if constexpr (S::kOnly != 0) {
+    const bool few = (long long)s.nq * (a.H / a.HKV) <= kFewRows;
+    if (few != (S::kOnly == 1)) s.nq = 0;
+  }
   return s;
 }
 
@@ -475,12 +494,13 @@ struct AttnStaged {
 // Thread `first` of `step` of a block (which then synchronise); returns whether it
 // has seen malformed lengths.  `all`: look at every sequence's also where nothing
 // but the flag depends on them.
+template <class S = TcShape>
 __host__ __device__ __forceinline__ bool attn_stage(const AttnArgs &a, AttnStaged *staged, int first,
                                                     int step, bool all) {
   bool any_bad = first == 0 && a.cu && (a.cu[0] != 0 || a.cu[a.n_seqs] != a.Ttot);
   for (int n = first; n < a.n_seqs; n += step) {
     bool bad;
-    const AttnSeq s = attn_seq(a, n, bad);
+    const AttnSeq s = attn_seq_of<S>(a, n, bad);
     any_bad |= bad;
     if (n < kStaged) staged[n] = AttnStaged{s.nq, s.base};
     else if (!all && !a.cu) break;
@@ -541,10 +561,10 @@ __device__ __noinline__ void attn_stage_order(const int32_t *cu, const int32_t *
 }
 // All THREADS threads of a block, which then synchronise; block 0 reports malformed
 // lengths.
-template <int THREADS>
+template <int THREADS, class S = TcShape>
 __device__ __forceinline__ void attn_stage(const AttnArgs &a, AttnStaged *staged, int block) {
   if (a.plan_total) return;
-  const bool bad = attn_stage(a, staged, threadIdx.x, THREADS, block == 0);
+  const bool bad = attn_stage<S>(a, staged, threadIdx.x, THREADS, block == 0);
   if (bad && a.flags && block == 0) atomicOr(a.flags, kFlagBadSeqlens);
   if (__syncthreads_or(bad) && a.cu)
     attn_stage_order<THREADS>(a.cu, a.kv_lens, a.n_seqs, a.Ttot, a.max_len, staged);
@@ -577,7 +597,7 @@ __host__ __device__ __forceinline__ AttnStart attn_start(const AttnArgs &a, Attn
   auto cost_of = [&](int n) {
     if (n < kStaged) return plan.cost(staged[n].nq, staged[n].base);
     bool bad;
-    const AttnSeq s = attn_seq(a, n, bad);
+    const AttnSeq s = attn_seq_of<S>(a, n, bad);
     return plan.cost(s.nq, s.base);
   };
   r.total = plan.choose(n_blocks, [&] {
@@ -638,7 +658,7 @@ struct AttnWalk {
       AttnLanes::each([&](int lane, int i) {
         bool bad;
         mine[i].nq = mine[i].base = 0;
-        if (lane < a.n_seqs) mine[i] = attn_seq(a, lane, bad);
+        if (lane < a.n_seqs) mine[i] = attn_seq_of<S>(a, lane, bad);
       });
   }
   // place of this block's next unit among those that are dealt whole
@@ -666,7 +686,7 @@ struct AttnWalk {
         },
         i, before);
     bool bad;
-    const AttnSeq one = attn_seq(a, who, bad);
+    const AttnSeq one = attn_seq_of<S>(a, who, bad);
     plan.pick(one, lo, i - (int)before, out);
     out.seq = who;
     out.len = one.len;
@@ -679,7 +699,7 @@ struct AttnWalk {
     while (seq < a.n_seqs && u0 < end) {
       if (fresh) {
         bool bad;
-        s = attn_seq(a, seq, bad);
+        s = attn_seq_of<S>(a, seq, bad);
         if (s.nq == 0) {
           seq++;
           continue;
@@ -710,7 +730,7 @@ struct AttnWalk {
       if (tile < 0) return false;
       bool bad;
       out.seq = i % all / plan.groups;
-      const AttnSeq one = attn_seq(a, out.seq, bad);
+      const AttnSeq one = attn_seq_of<S>(a, out.seq, bad);
       plan.place(one, i % plan.groups, tile, out);
       out.len = one.len;
     }

@@ -51,8 +51,7 @@ struct Smem {
   static constexpr int kSliceBytes = 2 * kSlice * D;
   static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr int kRow = D + 4;  // floats of a row where warps are joined
-  static constexpr int kRing = 0;     // [warp][stage][keys, values]
-  static constexpr int kScale = kWarps * kStages * kSliceBytes;  // [warp][stage][2]
+  static constexpr int kScale = kWarps * kStages * kSliceBytes;  // [warp][stage][2], behind the ring [warp][stage][keys, values]
   static constexpr int kQ = kScale + kWarps * kStages * 8;       // [nt][k step][lane] two registers
   static constexpr int kFactor = kQ + NT * (D / 16) * 32 * 8;    // [rows]
   static constexpr int kJoin = kFactor + NT * 8 * 4;             // [warp][rows] maximum, sum, maximum with V's scale
@@ -125,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a
   const uint32_t q_at = smem_addr(sm + SM::kQ);
   AttnPlan<Shape8> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
   AttnStaged *staged = reinterpret_cast<AttnStaged *>(sm);  // until the first copies
-  attn_stage<kThreads>(a, staged, blockIdx.x);
+  attn_stage<kThreads, Shape8>(a, staged, blockIdx.x);
   asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel waits for this one's end
   __syncthreads();
   const AttnStart st = attn_start(a, plan, staged, blockIdx.x, gridDim.x);  // each warp for itself
@@ -413,15 +412,35 @@ cudaError_t launch(const AttnArgs &a, int blocks, cudaStream_t stream) {
 
 }  // namespace
 
-AttnLaunch attn8_launch(AttnArgs &a) { return attn_plan_launch<Shape8>(a, 2 * sm_count()); }
+bool attn8_launch(const AttnArgs &a, Attn8Launch &l) {
+  const long long G = a.H / a.HKV, most = (a.cu ? (long long)a.Ttot : (long long)a.T) * G;  // rows of a sequence
+  l.few = l.many = a;
+  l.has_few = a.cu ? G <= kFewRows : most <= kFewRows;
+  l.has_many = most > kFewRows;
+  l.few_launch = l.many_launch = AttnLaunch{};
+  if (l.has_few) l.few_launch = attn_plan_launch<Shape8>(l.few, 2 * sm_count());
+  if (l.has_many) l.many_launch = attn_plan_launch<TcShape8>(l.many, sm_count());
+  return (!l.has_few || l.few_launch.blocks > 0) && (!l.has_many || l.many_launch.blocks > 0);
+}
 
-cudaError_t launch_attn8(const AttnArgs &a, int d, const AttnLaunch &l, cudaStream_t stream) {
+cudaError_t launch_attn8(const Attn8Launch &l, int d, cudaStream_t stream) {
+  if (l.has_many) {
+    const cudaError_t e = launch_attn8_tc(l.many, d, l.many_launch.blocks, stream);
+    if (e != cudaSuccess) return e;
+    if (l.many_launch.split && l.many_launch.blocks > 1) {
+      const cudaError_t m = launch_attn8_merge(l.many, d, false, l.many_launch.blocks, stream);
+      if (m != cudaSuccess) return m;
+    }
+  }
+  if (!l.has_few) return cudaSuccess;
   // one group of 8 rows where no sequence has more
+  const AttnArgs &a = l.few;
+  const int blocks = l.few_launch.blocks;
   const bool one = !a.cu && (long long)a.T * (a.H / a.HKV) <= 8;
-  const cudaError_t e = d == 64 ? (one ? launch<64, 1>(a, l.blocks, stream) : launch<64, 2>(a, l.blocks, stream))
-                                : (one ? launch<128, 1>(a, l.blocks, stream) : launch<128, 2>(a, l.blocks, stream));
-  if (e != cudaSuccess || !l.split || l.blocks < 2) return e;
-  return launch_attn8_merge(a, d, l.blocks, stream);
+  const cudaError_t e = d == 64 ? (one ? launch<64, 1>(a, blocks, stream) : launch<64, 2>(a, blocks, stream))
+                                : (one ? launch<128, 1>(a, blocks, stream) : launch<128, 2>(a, blocks, stream));
+  if (e != cudaSuccess || !l.few_launch.split || blocks < 2) return e;
+  return launch_attn8_merge(a, d, true, blocks, stream);
 }
 
 }  // namespace gdn

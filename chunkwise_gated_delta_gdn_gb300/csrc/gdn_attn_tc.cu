@@ -38,6 +38,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "gdn_attn.cuh"
 #include "gdn_sm100.cuh"
@@ -48,11 +49,12 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 640;
+constexpr int kThreads8 = 768;         // over a cache in 8 bits: four warps more
 constexpr int kUnits = 4;              // unit ring
 constexpr int kPanel = 128 * 128;      // bytes of 128 rows x 64 bf16
 constexpr float kRescale = 8.f;        // log2 growth of a row maximum that is let stand
 
-template <int D>
+template <int D, bool FP8 = false>
 struct Smem {
   static constexpr int kTileBytes = D / 64 * kPanel;  // 128 rows of D
   static constexpr int kStages = D == 128 ? 5 : 10;
@@ -64,15 +66,19 @@ struct Smem {
   // barriers, in order: Q full, Q empty, S full x2, P ready x2, O full x2,
   // swap x2, halves x8, turn x2, unit full x4, unit empty x4, tile full, tile
   // empty
-  static constexpr int kBarCount = 20 + 2 * kUnits + 2 * kStages;
+  // (8 bits: and tile ready)
+  static constexpr int kBarCount = (20 + 2 * kUnits + (FP8 ? 3 : 2) * kStages + 1) / 2 * 2;
   // tensor memory, abort, [X] stages that the scores free
   static constexpr int kSlot = kBars + kBarCount * 8;
-  static constexpr int kBytes = kSlot + 16;
+  static constexpr int kScale = kSlot + 16;  // [stage][8], of a tile in 8 bits
+  static constexpr int kBytes = kScale + (FP8 ? kStages * 8 * 4 : 0);
   static_assert(kSlot % 16 == 0, "read at once");
 };
 static_assert(kStaged * sizeof(AttnStaged) + kThreads * sizeof(AttnChunk) <= Smem<128>::kStages * Smem<128>::kTileBytes,
               "staging in the ring");
-static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "shared memory of one SM");
+static_assert(kStaged * sizeof(AttnStaged) + kThreads8 * sizeof(AttnChunk) <= Smem<128, true>::kStages * Smem<128, true>::kTileBytes,
+              "staging in the ring");
+static_assert(Smem<128, true>::kBytes <= 232448 && Smem<64, true>::kBytes <= 232448, "shared memory of one SM");
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -99,6 +105,29 @@ __device__ __forceinline__ uint4 shared_uint4(uint32_t at) {
 struct Maps {
   CUtensorMap q_pack, q, k, v;
 };
+
+__device__ __forceinline__ void store_uint4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// two e4m3 values (the low half of x) times f as two bf16
+__device__ __forceinline__ uint32_t bf16_of(uint32_t x, float f) {
+  uint32_t r;
+  asm("{\n .reg .b16 b, l, h;\n .reg .b32 p;\n .reg .f32 u, v;\n cvt.u16.u32 b, %1;\n"
+      " cvt.rn.f16x2.e4m3x2 p, b;\n mov.b32 {l, h}, p;\n cvt.f32.f16 u, l;\n cvt.f32.f16 v, h;\n"
+      " mul.f32 u, u, %2;\n mul.f32 v, v, %2;\n cvt.rn.bf16x2.f32 %0, v, u;\n}"
+      : "=r"(r)
+      : "r"(x), "f"(f));
+  return r;
+}
+// TMA: a box at (x, y, z, w) of a 4-D map, with a policy for the lines in L2
+__device__ __forceinline__ void tma_load_4d(uint32_t dst_saddr, const void *tmap, int x, int y, int z, int w, uint32_t bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst_saddr),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
+      : "memory");
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -183,6 +212,8 @@ struct Bars {
   __device__ uint32_t unit_empty(int i) const { return at(20 + kUnits + i); }
   __device__ uint32_t kv_full(int i) const { return at(20 + 2 * kUnits + i); }
   __device__ uint32_t kv_empty(int i) const { return at(20 + 2 * kUnits + stages + i); }
+  // 8 bits: what was loaded is there as bf16
+  __device__ uint32_t kv_ready(int i) const { return at(20 + 2 * kUnits + 2 * stages + i); }
 };
 
 // Position in a ring of N: index and how often it has gone round.
@@ -269,10 +300,13 @@ __device__ __forceinline__ void store_rows(const float (&y)[N], __nv_bfloat16 *o
   }
 }
 
-template <int D, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 1)
+// FP8: over a cache in 8 bits, one that four warps more turn into bf16 on its way.
+template <int D, bool PAGED, bool FP8 = false>
+__global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
     gdn_attn_tc_kernel(const AttnArgs a, const __grid_constant__ Maps maps, const int box) {
-  using SM = Smem<D>;
+  using SM = Smem<D, FP8>;
+  using S = std::conditional_t<FP8, TcShape8, TcShape>;
+  constexpr int THREADS = FP8 ? kThreads8 : kThreads;
   constexpr int kPanels = D / 64;
   // A key or value tile in shared memory, 8-row groups of 1024 bytes in the
   // 128-byte swizzle.  A prompt's: 64-column panels one after the other, each
@@ -308,10 +342,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 8; i++) mbar_init(bars.halves(i), 2);
     for (int i = 0; i < kUnits; i++) {
       mbar_init(bars.unit_full(i), 1);
-      mbar_init(bars.unit_empty(i), 19);  // loader, products x2, sixteen softmax warps
+      mbar_init(bars.unit_empty(i), FP8 ? 23 : 19);  // loader, products x2, sixteen softmax warps (and those that turn)
     }
     for (int i = 0; i < SM::kStages; i++) {
-      mbar_init(bars.kv_full(i), 1);
+      mbar_init(bars.kv_full(i), FP8 ? 33 : 1);  // 8 bits: and the loader's lanes, behind their scales
+      if (FP8) mbar_init(bars.kv_ready(i), 4);
       mbar_init(bars.kv_empty(i), 2);  // one from each X, or two from the one that reads it
     }
     mbar_fence_init();
@@ -320,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : &maps.q_pack);
   if (warp == 17) tmem_alloc(smem_addr(slot), 512);
   AttnStaged *staged = reinterpret_cast<AttnStaged *>(sm + SM::kRing);  // until the first unit
-  attn_stage<kThreads>(a, staged, blockIdx.x);
+  attn_stage<THREADS, S>(a, staged, blockIdx.x);
   fence_proxy_async();
   asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel waits for this one's end
   fence_before_sync();
@@ -330,6 +365,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sQ = smem_addr(sm + SM::kQ), sRing = smem_addr(sm + SM::kRing);
   const uint32_t tS = tmem, tO = tmem + 256;
 
+  // 768 threads leave 80 registers each: the softmax takes of the others'
+  if constexpr (FP8) {
+    if (warp < 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+  }
   if (warp < 16) {
     // ------------------------------------------------------------- softmax
     const int x = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
@@ -573,13 +613,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    if (warp == 18) {
+    if (FP8 && warp >= 20) {
+      // ------------------------------------------------------ 8 bits to bf16
+      // A warp has 32 rows of every tile, and turns them where they lie: they were
+      // loaded into the second half of the place that they take as bf16, so the
+      // first 16 rows are written before what is left, read beforehand, is
+      // overwritten.  Lanes 0-7 have 8 rows of one 16-byte piece (16 columns), whose
+      // 16-byte pieces of bf16 lie in different banks.
+      constexpr int kRegion = SM::kTileBytes / 4, kPieces = D / 16;
+      const int w = warp - 20, r = lane & 7, j0 = lane >> 3;
+      Units units{unit_ring, bars, abort, {}};
+      Ring<SM::kStages> ring;
+      const float *scales = reinterpret_cast<const float *>(sm + SM::kScale);
+      AttnUnit u;
+      while (units.next(u)) {
+        const int tiles = uniform(2 * (u.t1 - u.t0));  // keys and values; the order is the loader's
+        for (int i = 0; i < tiles; i++) {
+          wait(bars.kv_full(ring.i), ring.round, abort);
+          const uint32_t region = sRing + ring.i * SM::kTileBytes + w * kRegion, raw = region + kRegion / 2;
+          const float2 scale = *reinterpret_cast<const float2 *>(scales + ring.i * 8 + w * 2);  // rows 0-15, 16-31
+          auto read = [&](int group, int j) {
+            const int row = group * 8 + r;
+            return shared_uint4(raw + row * D + ((D == 128 ? j ^ r : j ^ ((r >> 1) & 3)) << 4));
+          };
+          auto write = [&](int group, int j, const uint4 &x) {
+            const float f = group < 2 ? scale.x : scale.y;
+            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+            uint32_t out[8];
+#pragma unroll
+            for (int c = 0; c < 8; c++) out[c] = bf16_of(c & 1 ? in[c >> 1] >> 16 : in[c >> 1], f);
+            const uint32_t to = region + group * kGroup + (j >> 2) * 1024 + r * 128;
+            const int c0 = (2 * j) & 7;
+            store_uint4(to + ((c0 ^ r) << 4), out[0], out[1], out[2], out[3]);
+            store_uint4(to + (((c0 + 1) ^ r) << 4), out[4], out[5], out[6], out[7]);
+          };
+          uint4 x[2][kPieces / 4];
+#pragma unroll
+          for (int part = 0; part < 2; part++) {
+#pragma unroll
+            for (int g = 0; g < 2; g++)
+#pragma unroll
+              for (int p = 0; p < kPieces / 4; p++) x[g][p] = read(part * 2 + g, p * 4 + j0);
+            __syncwarp();
+#pragma unroll
+            for (int g = 0; g < 2; g++)
+#pragma unroll
+              for (int p = 0; p < kPieces / 4; p++) write(part * 2 + g, p * 4 + j0, x[g][p]);
+            __syncwarp();
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.kv_ready(ring.i));
+          ring.step();
+        }
+      }
+    } else if (warp == 18) {
       // -------------------------------------------------------------- plan
-      AttnPlan<TcShape> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
+      AttnPlan<S> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
       const AttnStart st = attn_start(a, plan, staged, blockIdx.x, gridDim.x);
       fence_proxy_async();  // what was staged has been read: the ring may be filled
       __syncwarp();
-      AttnWalk<TcShape> walk(a, plan, st, blockIdx.x, gridDim.x);
+      AttnWalk<S> walk(a, plan, st, blockIdx.x, gridDim.x);
       Ring<kUnits> at;
       AttnUnit u;
       bool more = true;
@@ -653,6 +747,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int group = (good ? held : a.n_pages) * groups + ((k0 - index * a.page_size) >> 3);
           const int n = min((last - key + box) / box, 128 / box);  // boxes; may be <= 0
           place(bars.kv_empty(ring.i), ring.round ^ 1);
+          if constexpr (FP8) {
+            if (lane == 0 && !lost) mbar_arrive_expect_tx(full, max(n, 0) * box * D);
+            __syncwarp();
+            // into the second half of what 32 rows take as bf16
+            if (mine && !lost)
+              tma_load_4d(dst + (my_key >> 5) * (SM::kTileBytes / 4) + SM::kTileBytes / 8 + (my_key & 31) * D, map, 0, 0, group,
+                          w.kvh, full, w.n_tok * w.gp <= 128 ? once : often);
+            // lane i < 8 takes the i-th block's scale: zero in a bad page and past the last key
+            const int k1 = min(key + (lane & 7) * kScaleBlock, last), page1 = page_of(max(k1, 0));
+            const int from = __shfl_sync(0xffffffffu, pages.page, (page1 - pages.base) & 31);
+            const bool there = key + (lane & 7) * kScaleBlock <= last && (unsigned)from < (unsigned)a.n_pages;
+            if (lane < 8 && !lost)
+              cp_async4(smem_addr(sm + SM::kScale) + (ring.i * 8 + lane) * 4,
+                        (which ? a.v_scale : a.k_scale) +
+                            (there ? ((long long)from * (a.page_size / kScaleBlock) + (k1 - page1 * a.page_size) / kScaleBlock) * a.HKV + w.kvh : 0),
+                        there ? 4 : 0);
+            if (!lost) cp_async_arrive_noinc(full);
+            __syncwarp();
+            ring.step();
+            return;
+          }
           if (lane == 0 && !lost) mbar_arrive_expect_tx(full, max(n, 0) * box * 128 * kPanels);
           __syncwarp();
           if (mine && !lost)
@@ -742,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // last one had not arrived yet.
       auto next_tile = [&] {
         const int stage = ring.i;
-        wait(bars.kv_full(stage), ring.round, abort);
+        wait(FP8 ? bars.kv_ready(stage) : bars.kv_full(stage), ring.round, abort);
         ring.step();
         return stage;
       };
@@ -896,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
-bool make_maps(Maps &m, const AttnArgs &a, int d, int box) {
+bool make_maps(Maps &m, const AttnArgs &a, int d, int box, bool fp8) {
   const AttnPlan<TcShape> plan(a.H, a.HKV, 0);
   const uint64_t D = d;
   const uint64_t q_dims[3] = {D, (uint64_t)a.H, (uint64_t)a.Ttot};
@@ -907,6 +1022,13 @@ bool make_maps(Maps &m, const AttnArgs &a, int d, int box) {
   if (plan.G != plan.gp && plan.G <= 128) {
     const uint32_t pack_box[3] = {64, (uint32_t)plan.G, (uint32_t)(128 / plan.G)};
     if (!encode_bf16_map(&m.q_pack, a.q, 3, q_dims, q_strides, pack_box)) return false;
+  }
+  if (fp8) {  // [columns][8 rows][8-row group of all pages][head]
+    const uint64_t row = (uint64_t)a.HKV * D;
+    const uint64_t dims[4] = {D, 8, (uint64_t)a.n_pages * (a.page_size / 8), (uint64_t)a.HKV};
+    const uint64_t strides[3] = {row, row * 8, D};
+    const uint32_t kv_box[4] = {(uint32_t)D, 8, (uint32_t)box / 8, 1};
+    return encode_byte_map(&m.k, a.k, 4, dims, strides, kv_box, d) && encode_byte_map(&m.v, a.v, 4, dims, strides, kv_box, d);
   }
   if (a.table) {  // [64 columns][8 rows][panel][8-row group of all pages][head]
     const uint64_t row = (uint64_t)a.HKV * D * 2;
@@ -923,15 +1045,16 @@ bool make_maps(Maps &m, const AttnArgs &a, int d, int box) {
          encode_bf16_map(&m.v, a.v, 3, dims, vs, kv_box);
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool FP8>
 std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use its shared memory
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool FP8 = false>
 cudaError_t launch(const AttnArgs &a, const Maps &maps, int box, int blocks, cudaStream_t stream) {
-  const cudaError_t e = allow_smem(reinterpret_cast<const void *>(&gdn_attn_tc_kernel<D, PAGED>),
-                                   Smem<D>::kBytes, allowed<D, PAGED>);
+  constexpr int kBytes = Smem<D, FP8>::kBytes;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void *>(&gdn_attn_tc_kernel<D, PAGED, FP8>), kBytes,
+                                   allowed<D, PAGED, FP8>);
   if (e != cudaSuccess) return e;
-  gdn_attn_tc_kernel<D, PAGED><<<blocks, kThreads, Smem<D>::kBytes, stream>>>(a, maps, box);
+  gdn_attn_tc_kernel<D, PAGED, FP8><<<blocks, FP8 ? kThreads8 : kThreads, kBytes, stream>>>(a, maps, box);
   return cudaGetLastError();
 }
 
@@ -941,12 +1064,20 @@ cudaError_t launch_attn_tc(const AttnArgs &a, int d, int blocks, cudaStream_t st
   int box = 128;
   if (a.table && (a.page_size & -a.page_size) < box) box = a.page_size & -a.page_size;
   Maps maps;
-  if (!make_maps(maps, a, d, box)) return cudaErrorInvalidValue;
+  if (!make_maps(maps, a, d, box, false)) return cudaErrorInvalidValue;
   if (d == 64)
     return a.table ? launch<64, true>(a, maps, box, blocks, stream)
                    : launch<64, false>(a, maps, box, blocks, stream);
   return a.table ? launch<128, true>(a, maps, box, blocks, stream)
                  : launch<128, false>(a, maps, box, blocks, stream);
+}
+
+cudaError_t launch_attn8_tc(const AttnArgs &a, int d, int blocks, cudaStream_t stream) {
+  // rows of one warp's share of a tile at most: they are turned to bf16 in place
+  const int box = (a.page_size & -a.page_size) < 32 ? a.page_size & -a.page_size : 32;
+  Maps maps;
+  if (!make_maps(maps, a, d, box, true)) return cudaErrorInvalidValue;
+  return d == 64 ? launch<64, true, true>(a, maps, box, blocks, stream) : launch<128, true, true>(a, maps, box, blocks, stream);
 }
 
 }  // namespace gdn

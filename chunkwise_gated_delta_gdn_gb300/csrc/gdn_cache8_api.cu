@@ -10,6 +10,12 @@ size_t scale_bytes(int n_pages, int page_size, int HKV) {
   return (size_t)n_pages * (page_size / gdn::kScaleBlock) * HKV * sizeof(float);
 }
 
+// Partial results of the two kernels' plans, one behind the other.
+size_t few_bytes(const gdn::Attn8Launch &l, int d) { return (part_bytes(l.few_launch, d) + 255) / 256 * 256; }
+size_t parts8_bytes(const gdn::Attn8Launch &l, int d) {
+  return few_bytes(l, d) + part_bytes(l.many_launch, d);
+}
+
 // Token arrays that may interleave: no element in common.
 struct Rows {
   const void *p;
@@ -41,7 +47,9 @@ size_t gdn_attn_paged_fp8_fwd_workspace_bytes(int B, int T, int H, int HKV, int 
     fill_shape(a, with_cu ? kSomewhere : nullptr, n, T, Ttot, H, HKV);
     a.kv_lens = kSomewhere;
     a.max_len = page_size * max_pages;
-    const size_t bytes = part_bytes(gdn::attn8_launch(a), d);
+    gdn::Attn8Launch l;
+    if (!gdn::attn8_launch(a, l)) continue;
+    const size_t bytes = parts8_bytes(l, d);
     if (bytes > most) most = bytes;
   }
   return most;
@@ -76,9 +84,18 @@ gdn_status gdn_attn_paged_fp8_fwd(const void *q, const void *k_cache, const void
   fill_shape(a, cu_seqlens, n, T, Ttot, H, HKV);
   a.kv_lens = kv_lens;
   a.max_len = page_size * max_pages;
-  const gdn::AttnLaunch l = gdn::attn8_launch(a);
-  if (l.blocks == 0) return GDN_ERR_UNSUPPORTED;
-  const size_t ws = part_bytes(l, d);
+  a.q = q; a.k = k_cache; a.v = v_cache; a.o = o; a.lse = lse; a.table = block_table;
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  a.q_stride = q_stride;
+  a.page_size = page_size; a.max_pages = max_pages; a.n_pages = n_pages;
+  a.page_log = -1;
+  for (int log = 4; log < 31; log++)
+    if (page_size == 1 << log) a.page_log = log;
+  a.flags = flags;
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  gdn::Attn8Launch l;
+  if (!gdn::attn8_launch(a, l)) return GDN_ERR_UNSUPPORTED;
+  const size_t ws = parts8_bytes(l, d);
   if (ws > 0 && (!workspace || workspace_bytes < ws)) return GDN_ERR_WORKSPACE;
   if (!aligned_to(workspace, 256)) return GDN_ERR_INVALID_ARG;
   const size_t cache = (size_t)n_pages * page_size * kv_row, scales = scale_bytes(n_pages, page_size, HKV);
@@ -89,21 +106,13 @@ gdn_status gdn_attn_paged_fp8_fwd(const void *q, const void *k_cache, const void
                      {block_table, (size_t)n * max_pages * 4}, {kv_lens, (size_t)n * 4},
                      {cu_seqlens, cu_seqlens ? ((size_t)n + 1) * 4 : 0}};
   if (!disjoint(outs, ins)) return GDN_ERR_INVALID_ARG;
-  a.q = q; a.k = k_cache; a.v = v_cache; a.o = o; a.lse = lse; a.table = block_table;
-  a.k_scale = k_scale; a.v_scale = v_scale;
-  a.q_stride = q_stride;
-  a.page_size = page_size; a.max_pages = max_pages; a.n_pages = n_pages;
-  a.page_log = -1;
-  for (int log = 4; log < 31; log++)
-    if (page_size == 1 << log) a.page_log = log;
-  a.flags = flags;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (a.flags && cudaMemsetAsync(a.flags, 0, sizeof(uint32_t), s) != cudaSuccess)
     return GDN_ERR_CUDA;
   if (a.Ttot == 0) return GDN_OK;
-  a.scale_log2 = scale * 1.44269504088896340736f;
-  place_parts(a, d, l, workspace);
-  return gdn::launch_attn8(a, d, l, s) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  place_parts(l.few, d, l.few_launch, workspace);
+  place_parts(l.many, d, l.many_launch, static_cast<char *>(workspace) + few_bytes(l, d));
+  return gdn::launch_attn8(l, d, s) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 gdn_status gdn_kv_cache_append_fp8(const void *k, const void *v, void *k_cache, void *v_cache,

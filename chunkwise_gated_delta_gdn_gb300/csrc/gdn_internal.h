@@ -281,9 +281,20 @@ int sm_count();  // of the current device
 cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done);
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream);
 // the same over a cache in 8 bits (bf16 queries; gdn_attn8.cu)
-AttnLaunch attn8_launch(AttnArgs &a);
-cudaError_t launch_attn8(const AttnArgs &a, int d, const AttnLaunch &l, cudaStream_t stream);
-cudaError_t launch_attn8_merge(const AttnArgs &a, int d, int blocks, cudaStream_t stream);
+// Sequences of few rows for a key/value head go to one kernel, the others to another,
+// each with a plan and places for partial results of its own.
+struct Attn8Launch {
+  AttnArgs few, many;
+  AttnLaunch few_launch, many_launch;
+  bool has_few, has_many;  // a call may have such sequences
+};
+bool attn8_launch(const AttnArgs &a, Attn8Launch &l);  // false: more work than the plan can count
+cudaError_t launch_attn8(const Attn8Launch &l, int d, cudaStream_t stream);
+cudaError_t launch_attn8_tc(const AttnArgs &a, int d, int blocks, cudaStream_t stream);
+cudaError_t launch_attn8_merge(const AttnArgs &a, int d, bool few, int blocks, cudaStream_t stream);
+// tensor map of bytes, in the swizzle of `row` bytes (64 or 128)
+bool encode_byte_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
+                     const uint64_t *strides, const uint32_t *box, int row);
 cudaError_t launch_kv_append8(const Append8Args &a, int d, int dtype, cudaStream_t stream);
 cudaError_t launch_kv_copy_pages(const CopyPagesArgs &a, cudaStream_t stream);
 cudaError_t launch_rope(const RopeArgs &a, int d, bool interleaved, int dtype, cudaStream_t stream);
