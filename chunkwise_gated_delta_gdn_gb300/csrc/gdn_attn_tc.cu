@@ -53,6 +53,7 @@ constexpr int kThreads8 = 768;         // over a cache in 8 bits: four warps mor
 constexpr int kUnits = 4;              // unit ring
 constexpr int kPanel = 128 * 128;      // bytes of 128 rows x 64 bf16
 constexpr float kRescale = 8.f;        // log2 growth of a row maximum that is let stand
+constexpr float kShift8 = 6.f;         // 8 bits: log2 of the weights' factor (fp16, below 2^14)
 
 template <int D, bool FP8 = false>
 struct Smem {
@@ -66,12 +67,15 @@ struct Smem {
   // barriers, in order: Q full, Q empty, S full x2, P ready x2, O full x2,
   // swap x2, halves x8, turn x2, unit full x4, unit empty x4, tile full, tile
   // empty
-  // (8 bits: and tile ready)
-  static constexpr int kBarCount = (20 + 2 * kUnits + (FP8 ? 3 : 2) * kStages + 1) / 2 * 2;
+  // (8 bits: and tile ready, Q ready)
+  static constexpr int kBarCount = (20 + 2 * kUnits + (FP8 ? 3 * kStages + 1 : 2 * kStages) + 1) / 2 * 2;
   // tensor memory, abort, [X] stages that the scores free
   static constexpr int kSlot = kBars + kBarCount * 8;
-  static constexpr int kScale = kSlot + 16;  // [stage][8], of a tile in 8 bits
-  static constexpr int kBytes = kScale + (FP8 ? kStages * 8 * 4 : 0);
+  // 8 bits: a tile's scales [stage][16], Q's powers [two units][row tile][32 rows], and
+  // what a tile's values are relative to, [stage] and [X]
+  static constexpr int kScale = kSlot + 16, kUp = kScale + kStages * 64, kRef = kUp + 64;
+  static constexpr int kTileRef = kRef + kStages * 4;
+  static constexpr int kBytes = FP8 ? kTileRef + 8 : kScale;
   static_assert(kSlot % 16 == 0, "read at once");
 };
 static_assert(kStaged * sizeof(AttnStaged) + kThreads * sizeof(AttnChunk) <= Smem<128>::kStages * Smem<128>::kTileBytes,
@@ -109,16 +113,33 @@ struct Maps {
 __device__ __forceinline__ void store_uint4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-// two e4m3 values (the low half of x) times f as two bf16
-__device__ __forceinline__ uint32_t bf16_of(uint32_t x, float f) {
+// two e4m3 values (the low or high half of x) times f, a pair of the same, as two fp16
+template <bool HIGH>
+__device__ __forceinline__ uint32_t f16_of(uint32_t x, uint32_t f) {
   uint32_t r;
-  asm("{\n .reg .b16 b, l, h;\n .reg .b32 p;\n .reg .f32 u, v;\n cvt.u16.u32 b, %1;\n"
-      " cvt.rn.f16x2.e4m3x2 p, b;\n mov.b32 {l, h}, p;\n cvt.f32.f16 u, l;\n cvt.f32.f16 v, h;\n"
-      " mul.f32 u, u, %2;\n mul.f32 v, v, %2;\n cvt.rn.bf16x2.f32 %0, v, u;\n}"
-      : "=r"(r)
-      : "r"(x), "f"(f));
+  if constexpr (HIGH)
+    asm("{\n .reg .b16 l, h;\n .reg .b32 p;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 p, h;\n mul.rn.f16x2 %0, p, %2;\n}"
+        : "=r"(r) : "r"(x), "r"(f));
+  else
+    asm("{\n .reg .b16 l, h;\n .reg .b32 p;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 p, l;\n mul.rn.f16x2 %0, p, %2;\n}"
+        : "=r"(r) : "r"(x), "r"(f));
   return r;
 }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&p);
+}
+// exponent of the power of two that is x or the next above it, within -117 .. 120
+__device__ __forceinline__ int ref_exponent(float x) {
+  return min(max((int)((__float_as_uint(x) + 0x7fffffu) >> 23 & 255) - 127, -117), 120);
+}
+__device__ __forceinline__ float two_to(int e) { return __int_as_float((127 + e) << 23); }
+__device__ __forceinline__ int shared_int(uint32_t at) {
+  int v;
+  asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_int(uint32_t at, int v) { asm volatile("st.shared.s32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
 // TMA: a box at (x, y, z, w) of a 4-D map, with a policy for the lines in L2
 __device__ __forceinline__ void tma_load_4d(uint32_t dst_saddr, const void *tmap, int x, int y, int z, int w, uint32_t bar,
                                             uint64_t policy) {
@@ -214,6 +235,7 @@ struct Bars {
   __device__ uint32_t kv_empty(int i) const { return at(20 + 2 * kUnits + stages + i); }
   // 8 bits: what was loaded is there as bf16
   __device__ uint32_t kv_ready(int i) const { return at(20 + 2 * kUnits + 2 * stages + i); }
+  __device__ uint32_t q_ready() const { return at(20 + 2 * kUnits + 3 * stages); }
 };
 
 // Position in a ring of N: index and how often it has gone round.
@@ -300,7 +322,7 @@ __device__ __forceinline__ void store_rows(const float (&y)[N], __nv_bfloat16 *o
   }
 }
 
-// FP8: over a cache in 8 bits, one that four warps more turn into bf16 on its way.
+// FP8: over a cache in 8 bits, one that four warps more turn into fp16 on its way.
 template <int D, bool PAGED, bool FP8 = false>
 __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
     gdn_attn_tc_kernel(const AttnArgs a, const __grid_constant__ Maps maps, const int box) {
@@ -347,6 +369,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
     for (int i = 0; i < SM::kStages; i++) {
       mbar_init(bars.kv_full(i), FP8 ? 33 : 1);  // 8 bits: and the loader's lanes, behind their scales
       if (FP8) mbar_init(bars.kv_ready(i), 4);
+      if (FP8 && i == 0) mbar_init(bars.q_ready(), 4);
       mbar_init(bars.kv_empty(i), 2);  // one from each X, or two from the one that reads it
     }
     mbar_fence_init();
@@ -396,7 +419,9 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
       swap_phase[i] ^= 1;
     };
     AttnUnit u;
+    [[maybe_unused]] int unit_parity = 1;
     while (units.next(u)) {
+      if constexpr (FP8) unit_parity ^= 1;
       const int t0 = uniform(u.t0), t1 = uniform(u.t1), rows = uniform(u.n_tok * u.gp);
       const bool narrow = rows <= 128;
       const bool both = narrow && t1 - t0 > 1;
@@ -405,7 +430,14 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
       const int tok = row / u.gp;
       const int limit = u.pos0 + min(tok, u.n_tok - 1) - half * 64;  // last visible key, this half's columns
       const int all_see = __reduce_min_sync(0xffffffffu, limit);
+      // 8 bits: m is the maximum of log2(weight times V's scale).  Scores are 2^-up (K's
+      // scale) S, and weights have V's scale 2^vs in them, which is taken out of l again;
+      // the scales are those that the tile's operands are relative to.
       float m = -CUDART_INF_F, l = 0.f;
+      [[maybe_unused]] int up = 0;
+      // Values below 2^-90 count as that for m: l, which has weights without scales in
+      // units of 2^m, stays below 2^98 for each key.
+      [[maybe_unused]] float xs = sl2, vs = 0.f, vs_top = 0.f, vs_inv = 1.f;
       const int first = narrow ? t0 + x : t0;
       const bool mine = first < t1;
       // rows past the unit's last one (most of a decode step's tile): their
@@ -441,6 +473,14 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         // touched.  So after a unit's first tile the weights are made from the m
         // at hand, while the halves of the rows exchange their maxima, and made
         // again in the rare case that m moves.
+        if constexpr (FP8) {
+          if (t == first) up = shared_int(smem_addr(sm + SM::kUp) + (unit_parity * 8 + (row >> 5)) * 4);
+          const int ref = shared_int(smem_addr(sm + SM::kTileRef) + x * 4), k_ref = ref >> 16, v_ref = (short)ref;
+          xs = fmaxf(sl2 * two_to(-(up / 2)) * two_to(up / 2 - up) * two_to(k_ref), 1e-37f);  // -inf times it stays that
+          vs = (float)v_ref;
+          vs_top = (float)max(v_ref, -90);
+          vs_inv = two_to(-v_ref);
+        }
         float s[64], tile_max;
         auto load_scores = [&] {
           uint32_t raw[2][32];
@@ -477,15 +517,16 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         if (t == first) {
           load_scores();
           other_half();
-          m = tile_max;
+          m = FP8 ? fmaf(tile_max, xs, vs_top) : tile_max;
           meet_half();  // read, before it is written again
         }
         uint32_t packed[32];
         uint64_t sum[2];
         while (true) {
           load_scores();
-          const float off = m == -CUDART_INF_F ? 0.f : m * sl2;  // nothing visible yet: weights 0
-          const uint64_t scale2 = pair(sl2, sl2), off2 = pair(-off, -off);
+          // nothing visible yet: weights 0
+          const float off = FP8 ? (m == -CUDART_INF_F ? 0.f : m - kShift8) - vs : m == -CUDART_INF_F ? 0.f : m * sl2;
+          const uint64_t scale2 = FP8 ? pair(xs, xs) : pair(sl2, sl2), off2 = pair(-off, -off);
           sum[0] = sum[1] = 0;
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
@@ -494,13 +535,14 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             p0 = ex2(p0);
             p1 = ex2(p1);
             sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair(p0, p1));
-            packed[c >> 1] = pack2(p0, p1);
+            packed[c >> 1] = FP8 ? pack_f16(p0, p1) : pack2(p0, p1);
           }
           other_half();
-          const bool move = tile_max > m + grow;
+          const float top = FP8 ? fmaf(tile_max, xs, vs_top) : tile_max;
+          const bool move = top > m + (FP8 ? kRescale : grow);
           if (__builtin_expect(!__any_sync(0xffffffffu, move), 1)) break;
-          const float f = move ? ex2((m - tile_max) * sl2) : 1.f;
-          if (move) m = tile_max;
+          const float f = move ? ex2(FP8 ? m - top : (m - top) * sl2) : 1.f;
+          if (move) m = top;
           l *= f;
 #pragma unroll 1
           for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
@@ -516,7 +558,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         tmem_st32_nowait(p_at, packed);
         float l0, l1;
         unpair(add2(sum[0], sum[1]), l0, l1);
-        l += l0 + l1;
+        l += FP8 ? (l0 + l1) * vs_inv : l0 + l1;
         tmem_wait_st();
         fence_before_sync();
         __syncwarp();
@@ -528,7 +570,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         o_phase ^= 1;
         fence_after_sync();
       }
-      float m_scaled = m * sl2, f_own = 1.f, f_other = 0.f;
+      float m_scaled = FP8 ? m - kShift8 : m * sl2, f_own = 1.f, f_other = 0.f;
       if (both) {
         // Row sums and maxima of both X: the sum of the halves and the maximum
         // in the places of the two halves' tile maxima.  The meeting also says
@@ -614,38 +656,99 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
     }
   } else {
     if (FP8 && warp >= 20) {
-      // ------------------------------------------------------ 8 bits to bf16
+      // ------------------------------------------------------ 8 bits to fp16
+      // Operands are fp16 here: an e4m3 value is exact in it, times its block's scale
+      // relative to the tile's largest one (a power of two, down to 2^-24 of it); 32 rows
+      // of Q are scaled by a power of two into the middle of its range, which leaves a
+      // score's error below 2^-39 of the largest one's products.  (bf16 could hold values
+      // with their scales, but takes six instructions for two values where this takes
+      // two: 512 tokens over 32768 keys 367 us.)
       // A warp has 32 rows of every tile, and turns them where they lie: they were
-      // loaded into the second half of the place that they take as bf16, so the
+      // loaded into the second half of the place that they take as fp16, so the
       // first 16 rows are written before what is left, read beforehand, is
       // overwritten.  Lanes 0-7 have 8 rows of one 16-byte piece (16 columns), whose
-      // 16-byte pieces of bf16 lie in different banks.
+      // 16-byte pieces of fp16 lie in different banks.
       constexpr int kRegion = SM::kTileBytes / 4, kPieces = D / 16;
       const int w = warp - 20, r = lane & 7, j0 = lane >> 3;
       Units units{unit_ring, bars, abort, {}};
       Ring<SM::kStages> ring;
-      const float *scales = reinterpret_cast<const float *>(sm + SM::kScale);
+      uint32_t q_phase = 0;
+      int unit_parity = 1;
       AttnUnit u;
       while (units.next(u)) {
         const int tiles = uniform(2 * (u.t1 - u.t0));  // keys and values; the order is the loader's
+        const int rows = uniform(u.n_tok * u.gp);
+        unit_parity ^= 1;
+        wait(bars.q_full(), q_phase, abort);
+        q_phase ^= 1;
+        // Q: this warp's 32 rows of each row tile, four at a time, 8 lanes to a row
+        for (int r0 = w * 32; r0 < rows; r0 += 128) {
+          const uint32_t at = sQ + (r0 >> 7) * SM::kTileBytes + (w * 32 + (lane >> 3)) * 128 + (lane & 7) * 16;
+          const int steps = min((rows - r0 + 3) >> 2, 8);
+          uint32_t top = 0;
+          bool odd = false;  // something is not finite
+          auto look = [&](bool all) {
+            top = 0;
+            for (int i = 0; i < steps; i++)
+#pragma unroll
+              for (int p = 0; p < kPanels; p++) {
+                const uint4 x = shared_uint4(at + i * 512 + p * kPanel);
+                const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                  const uint32_t lo = in[c] & 0x7fffu, hi = in[c] >> 16 & 0x7fffu;
+                  top = max(top, max(all || lo < 0x7f80u ? lo : 0u, all || hi < 0x7f80u ? hi : 0u));
+                }
+              }
+            top = __reduce_max_sync(0xffffffffu, top);
+            odd = top >= 0x7f80u;
+          };
+          look(true);
+          if (odd) look(false);  // a row's infinity is its own
+          // 2^up brings the largest element to [2^14, 2^15)
+          const int up = top == 0 ? 0 : 14 - ((int)(top >> 7) - 127);
+          const float f1 = two_to(up / 2), f2 = two_to(up - up / 2);
+          for (int i = 0; i < steps; i++)
+#pragma unroll
+            for (int p = 0; p < kPanels; p++) {
+              const uint4 x = shared_uint4(at + i * 512 + p * kPanel);
+              const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+              uint32_t out[4];
+#pragma unroll
+              for (int c = 0; c < 4; c++)
+                out[c] = pack_f16(__uint_as_float(in[c] << 16) * f1 * f2, __uint_as_float(in[c] & 0xffff0000u) * f1 * f2);
+              store_uint4(at + i * 512 + p * kPanel, out[0], out[1], out[2], out[3]);
+            }
+          if (lane == 0) store_int(smem_addr(sm + SM::kUp) + (unit_parity * 8 + (r0 >> 5)) * 4, up);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.q_ready());
         for (int i = 0; i < tiles; i++) {
           wait(bars.kv_full(ring.i), ring.round, abort);
           const uint32_t region = sRing + ring.i * SM::kTileBytes + w * kRegion, raw = region + kRegion / 2;
-          const float2 scale = *reinterpret_cast<const float2 *>(scales + ring.i * 8 + w * 2);  // rows 0-15, 16-31
+          const uint32_t scale_at = smem_addr(sm + SM::kScale) + ring.i * 64;
+          auto largest = [&](uint32_t at) {
+            const uint4 x = shared_uint4(at), y = shared_uint4(at + 16);
+            return fmaxf(fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)), fmaxf(__uint_as_float(x.z), __uint_as_float(x.w))),
+                         fmaxf(fmaxf(__uint_as_float(y.x), __uint_as_float(y.y)), fmaxf(__uint_as_float(y.z), __uint_as_float(y.w))));
+          };
+          const int ref = ref_exponent(largest(scale_at));
+          if (w == 0 && lane == 0)  // of a key tile: also that of the values that go with it
+            store_int(smem_addr(sm + SM::kRef) + ring.i * 4, (int)((uint32_t)ref << 16) | (ref_exponent(largest(scale_at + 32)) & 0xffff));
+          const uint4 four = shared_uint4(scale_at + (w >> 1) * 16);  // rows 0-15 and 16-31 of this warp's: two of these
+          const float s0 = __uint_as_float(w & 1 ? four.z : four.x) * two_to(-ref), s1 = __uint_as_float(w & 1 ? four.w : four.y) * two_to(-ref);
+          const uint32_t f[2] = {pack_f16(s0, s0), pack_f16(s1, s1)};
           auto read = [&](int group, int j) {
             const int row = group * 8 + r;
             return shared_uint4(raw + row * D + ((D == 128 ? j ^ r : j ^ ((r >> 1) & 3)) << 4));
           };
           auto write = [&](int group, int j, const uint4 &x) {
-            const float f = group < 2 ? scale.x : scale.y;
-            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-            uint32_t out[8];
-#pragma unroll
-            for (int c = 0; c < 8; c++) out[c] = bf16_of(c & 1 ? in[c >> 1] >> 16 : in[c >> 1], f);
+            const uint32_t g = f[group >> 1];
             const uint32_t to = region + group * kGroup + (j >> 2) * 1024 + r * 128;
             const int c0 = (2 * j) & 7;
-            store_uint4(to + ((c0 ^ r) << 4), out[0], out[1], out[2], out[3]);
-            store_uint4(to + (((c0 + 1) ^ r) << 4), out[4], out[5], out[6], out[7]);
+            store_uint4(to + ((c0 ^ r) << 4), f16_of<false>(x.x, g), f16_of<true>(x.x, g), f16_of<false>(x.y, g), f16_of<true>(x.y, g));
+            store_uint4(to + (((c0 + 1) ^ r) << 4), f16_of<false>(x.z, g), f16_of<true>(x.z, g), f16_of<false>(x.w, g), f16_of<true>(x.w, g));
           };
           uint4 x[2][kPieces / 4];
 #pragma unroll
@@ -754,13 +857,14 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             if (mine && !lost)
               tma_load_4d(dst + (my_key >> 5) * (SM::kTileBytes / 4) + SM::kTileBytes / 8 + (my_key & 31) * D, map, 0, 0, group,
                           w.kvh, full, w.n_tok * w.gp <= 128 ? once : often);
-            // lane i < 8 takes the i-th block's scale: zero in a bad page and past the last key
+            // lane i < 8 takes the i-th block's scale: zero in a bad page and past the last
+            // key; with a key tile come the scales of its values, lanes 8-15
             const int k1 = min(key + (lane & 7) * kScaleBlock, last), page1 = page_of(max(k1, 0));
             const int from = __shfl_sync(0xffffffffu, pages.page, (page1 - pages.base) & 31);
             const bool there = key + (lane & 7) * kScaleBlock <= last && (unsigned)from < (unsigned)a.n_pages;
-            if (lane < 8 && !lost)
-              cp_async4(smem_addr(sm + SM::kScale) + (ring.i * 8 + lane) * 4,
-                        (which ? a.v_scale : a.k_scale) +
+            if (lane < (which ? 8 : 16) && !lost)
+              cp_async4(smem_addr(sm + SM::kScale) + (ring.i * 16 + lane) * 4,
+                        (which || lane >= 8 ? a.v_scale : a.k_scale) +
                             (there ? ((long long)from * (a.page_size / kScaleBlock) + (k1 - page1 * a.page_size) / kScaleBlock) * a.HKV + w.kvh : 0),
                         there ? 4 : 0);
             if (!lost) cp_async_arrive_noinc(full);
@@ -842,7 +946,8 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
       // the two X's products mix and their softmaxes fall together (a
       // 32768-token prompt 4.13 ms, with one warp 3.10 ms).
       const int x = warp == 17 ? 0 : 1;
-      constexpr uint32_t kIdS = idesc_bf16(128, 128, 0, 0), kIdO = idesc_bf16(128, D, 0, 1);
+      constexpr uint32_t kIdS = FP8 ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t kIdO = FP8 ? idesc_f16(128, D, 0, 1) : idesc_bf16(128, D, 0, 1);
       Units units{unit_ring, bars, abort, {}};
       Ring<SM::kStages> ring;
       uint32_t q_phase = 0, p_phase = 0, turn = 0;
@@ -892,6 +997,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
                               kIdS, lane == 0);
         if (lane == 0) {
           mma_commit(bars.s_full(x));
+          if constexpr (FP8) store_int(smem_addr(sm + SM::kTileRef) + x * 4, shared_int(smem_addr(sm + SM::kRef) + k * 4));
           used[x] = k | (free_v + 1) << 8;
           mbar_arrive(bars.s_full(x));
         }
@@ -946,7 +1052,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         const bool narrow = uniform(u.n_tok * u.gp) <= 128;
         last_values();
         const int k = next_tile();
-        wait(bars.q_full(), q_phase, abort);
+        wait(FP8 ? bars.q_ready() : bars.q_full(), q_phase, abort);
         q_phase ^= 1;
         if (x == 0) scores(k, 0, -1);
         last_values_1();
