@@ -129,6 +129,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 p = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&p);
 }
+__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// a whole number within 1 of x
+__device__ __forceinline__ float whole(float x) { return __fadd_rn(__fadd_rn(x, 0x1.8p23f), -0x1.8p23f); }
 // exponent of the power of two that is x or the next above it, within -117 .. 120
 __device__ __forceinline__ int ref_exponent(float x) {
   return min(max((int)((__float_as_uint(x) + 0x7fffffu) >> 23 & 255) - 127, -117), 120);
@@ -430,7 +437,8 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
       const int tok = row / u.gp;
       const int limit = u.pos0 + min(tok, u.n_tok - 1) - half * 64;  // last visible key, this half's columns
       const int all_see = __reduce_min_sync(0xffffffffu, limit);
-      // 8 bits: m is the maximum of log2(weight times V's scale).  Scores are 2^-up (K's
+      // 8 bits: m is the maximum of log2(weight times V's scale), a whole number, so that
+      // the factor between two of them is exact in fp16.  Scores are 2^-up (K's
       // scale) S, and weights have V's scale 2^vs in them, which is taken out of l again;
       // the scales are those that the tile's operands are relative to.
       float m = -CUDART_INF_F, l = 0.f;
@@ -517,15 +525,24 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         if (t == first) {
           load_scores();
           other_half();
-          m = FP8 ? fmaf(tile_max, xs, vs_top) : tile_max;
+          m = FP8 ? whole(fmaf(tile_max, xs, vs_top)) : tile_max;
           meet_half();  // read, before it is written again
         }
         uint32_t packed[32];
         uint64_t sum[2];
         while (true) {
           load_scores();
+          // 8 bits: where this half of the row alone has outgrown m, its own maximum is
+          // taken, and what that is off by after the exchange is made good by a factor, not
+          // by a second pass: with keys of different sizes a third of the tiles has a row
+          // that moves (512 tokens over 32768 keys 341 -> 308 us).
+          float at_hand = m;
+          if constexpr (FP8) {
+            const float y = fmaf(tile_max, xs, vs_top);
+            if (y > m + kRescale) at_hand = whole(y);
+          }
           // nothing visible yet: weights 0
-          const float off = FP8 ? (m == -CUDART_INF_F ? 0.f : m - kShift8) - vs : m == -CUDART_INF_F ? 0.f : m * sl2;
+          const float off = FP8 ? (at_hand == -CUDART_INF_F ? 0.f : at_hand - kShift8) - vs : m == -CUDART_INF_F ? 0.f : m * sl2;
           const uint64_t scale2 = FP8 ? pair(xs, xs) : pair(sl2, sl2), off2 = pair(-off, -off);
           sum[0] = sum[1] = 0;
 #pragma unroll
@@ -538,11 +555,22 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             packed[c >> 1] = FP8 ? pack_f16(p0, p1) : pack2(p0, p1);
           }
           other_half();
-          const float top = FP8 ? fmaf(tile_max, xs, vs_top) : tile_max;
+          float top = FP8 ? fmaf(tile_max, xs, vs_top) : tile_max;
           const bool move = top > m + (FP8 ? kRescale : grow);
+          if constexpr (FP8) top = whole(top);
           if (__builtin_expect(!__any_sync(0xffffffffu, move), 1)) break;
           const float f = move ? ex2(FP8 ? m - top : (m - top) * sl2) : 1.f;
           if (move) m = top;
+          if constexpr (FP8) {
+            // a power of two, in two steps: weights of up to 2^14 times 2^-38 still count
+            const float e = at_hand == m ? 0.f : fmaxf(at_hand - m, -48.f), e1 = truncf(0.5f * e);
+            const float g = ex2(e), g1 = ex2(e1), g2 = ex2(e - e1);
+            const uint32_t g1_2 = pack_f16(g1, g1), g2_2 = pack_f16(g2, g2);
+#pragma unroll
+            for (int c = 0; c < 32; c++) packed[c] = mul_f16(mul_f16(packed[c], g1_2), g2_2);
+            sum[0] = mul2(sum[0], pair(g, g));
+            sum[1] = mul2(sum[1], pair(g, g));
+          }
           l *= f;
 #pragma unroll 1
           for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
@@ -553,6 +581,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
             tmem_st16_nowait(o_at + c, o);
           }
+          if constexpr (FP8) break;
           meet_half();
         }
         tmem_st32_nowait(p_at, packed);
