@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
       // scale) S, and weights have V's scale 2^vs in them, which is taken out of l again;
       // the scales are those that the tile's operands are relative to.
       float m = -CUDART_INF_F, l = 0.f;
-      [[maybe_unused]] int up = 0;
+      [[maybe_unused]] float row_factor = 0.f;
       // Values below 2^-90 count as that for m: l, which has weights without scales in
       // units of 2^m, stays below 2^98 for each key.
       [[maybe_unused]] float xs = sl2, vs = 0.f, vs_top = 0.f, vs_inv = 1.f;
@@ -482,9 +482,12 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         // at hand, while the halves of the rows exchange their maxima, and made
         // again in the rare case that m moves.
         if constexpr (FP8) {
-          if (t == first) up = shared_int(smem_addr(sm + SM::kUp) + (unit_parity * 8 + (row >> 5)) * 4);
+          if (t == first) {
+            const int up = shared_int(smem_addr(sm + SM::kUp) + (unit_parity * 8 + (row >> 5)) * 4);
+            row_factor = sl2 * two_to(-(up / 2)) * two_to(up / 2 - up);
+          }
           const int ref = shared_int(smem_addr(sm + SM::kTileRef) + x * 4), k_ref = ref >> 16, v_ref = (short)ref;
-          xs = fmaxf(sl2 * two_to(-(up / 2)) * two_to(up / 2 - up) * two_to(k_ref), 1e-37f);  // -inf times it stays that
+          xs = fmaxf(row_factor * two_to(k_ref), 1e-37f);  // -inf times it stays that
           vs = (float)v_ref;
           vs_top = (float)max(v_ref, -90);
           vs_inv = two_to(-v_ref);
@@ -522,18 +525,18 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
           fence_after_sync();
           tile_max = fmaxf(tile_max, *other_ex);
         };
-        if (t == first) {
+        if (!FP8 && t == first) {
           load_scores();
           other_half();
-          m = FP8 ? whole(fmaf(tile_max, xs, vs_top)) : tile_max;
+          m = tile_max;
           meet_half();  // read, before it is written again
         }
         uint32_t packed[32];
         uint64_t sum[2];
         while (true) {
           load_scores();
-          // 8 bits: where this half of the row alone has outgrown m, its own maximum is
-          // taken, and what that is off by after the exchange is made good by a factor, not
+          // 8 bits: where this half of the row alone has outgrown m (in a unit's first tile
+          // always), its own maximum is taken, and what that is off by after the exchange is made good by a factor, not
           // by a second pass: with keys of different sizes a third of the tiles has a row
           // that moves (512 tokens over 32768 keys 341 -> 308 us).
           float at_hand = m;
@@ -572,6 +575,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             sum[1] = mul2(sum[1], pair(g, g));
           }
           l *= f;
+          if (FP8 && t == first) break;  // no output yet
 #pragma unroll 1
           for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
             uint32_t o[16];

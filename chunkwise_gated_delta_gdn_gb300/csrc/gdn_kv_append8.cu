@@ -53,34 +53,78 @@ __device__ __forceinline__ void from_e4m3(uint32_t x, float (&y)[4]) {
       : "r"(x));
 }
 
+// Eight elements of a row, as they came, and as numbers.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 w;
+  __device__ void get(const void *p) { w = __ldg(static_cast<const uint4 *>(p)); }
+  __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  // the largest magnitude, as the bits of an fp32 number
+  __device__ uint32_t top() const {
+    const uint32_t m = 0x7fff7fffu;
+    const uint32_t t = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+    return max(t << 16, t & 0x7fff0000u);
+  }
+  __device__ void put(float (&y)[8]) const {
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      y[2 * e] = __uint_as_float(ws[e] << 16);
+      y[2 * e + 1] = __uint_as_float(ws[e] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Eight<float> {
+  float4 u, w;
+  __device__ void get(const void *p) {
+    u = __ldg(static_cast<const float4 *>(p));
+    w = __ldg(static_cast<const float4 *>(p) + 1);
+  }
+  __device__ void zero() { u = w = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ uint32_t top() const {
+    float y[8];
+    put(y);
+    uint32_t t = 0;
+#pragma unroll
+    for (int e = 0; e < 8; e++) t = max(t, __float_as_uint(y[e]) & 0x7fffffffu);
+    return t;
+  }
+  __device__ void put(float (&y)[8]) const {
+    y[0] = u.x; y[1] = u.y; y[2] = u.z; y[3] = u.w;
+    y[4] = w.x; y[5] = w.y; y[6] = w.z; y[7] = w.w;
+  }
+};
+
+// A block of warps has the heads, keys and values, of a slot (of a block of tokens),
+// several blocks where there are more than kWarps of them.
 template <int D, typename T>
 __global__ void __launch_bounds__(kWarps * 32) gdn_kv_append8_kernel(const Append8Args a, const int per_seq) {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kPasses = kScaleBlock / kAtOnce;
   const int lane = threadIdx.x & 31;
-  if (a.cu && a.flags)  // a slot finds its sequence, and so need not meet a malformed one
+  if (a.cu && a.flags && blockIdx.y == 0)  // a slot finds its sequence, and so need not meet a malformed one
     for (long long n = (long long)blockIdx.x * blockDim.x + threadIdx.x; n < a.n_seqs; n += (long long)gridDim.x * blockDim.x) {
       const int from = __ldg(a.cu + n), to = __ldg(a.cu + n + 1);
       if (from < 0 || to < from || to > a.Ttot) atomicOr(a.flags, kFlagBadSeqlens);
     }
-  // slot of a block of tokens, and within it head and keys (0) or values (1)
-  const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const long long slot = item / (2 * a.HKV);
-  const int rest = (int)(item - slot * 2 * a.HKV), head = rest >> 1, which = rest & 1;
+  const int slot = blockIdx.x, rest = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (rest >= 2 * a.HKV) return;
+  const int head = rest >> 1, which = rest & 1;  // keys (0) or values (1)
   // Sequence n has per_seq slots, or, packed, those from floor(cu[n] / 16) + 2 n on: it
   // reaches at most floor((nq + 30) / 16) blocks.
   int n, start, end, j;
   if (a.cu) {
-    if (slot >= (long long)(a.Ttot / kScaleBlock) + 2LL * a.n_seqs) return;
-    n = last_at([&](int i) { return (int)min((long long)(__ldg(a.cu + i) / kScaleBlock) + 2LL * i, (long long)INT32_MAX); }, a.n_seqs, (int)slot);
+    n = last_at([&](int i) { return __ldg(a.cu + i) / kScaleBlock + 2 * i; }, a.n_seqs, slot);
     start = __ldg(a.cu + n);
     end = __ldg(a.cu + n + 1);
-    const long long at = slot - (start / kScaleBlock) - 2LL * n;
-    if (start < 0 || end < start || end > a.Ttot || at < 0 || at > INT32_MAX) return;  // reported above
-    j = (int)at;
+    if (start < 0 || end < start || end > a.Ttot) return;  // reported above
+    j = slot - start / kScaleBlock - 2 * n;
+    if (j < 0) return;
   } else {
-    if (slot >= (long long)a.n_seqs * per_seq) return;
-    n = (int)(slot / per_seq);
-    j = (int)(slot - (long long)n * per_seq);
+    n = per_seq == 1 ? slot : slot / per_seq;
+    j = slot - n * per_seq;
     start = n * a.T;
     end = start + a.T;
   }
@@ -92,8 +136,21 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_kv_append8_kernel(const Appen
   // the block's first position
   const long long p0 = ((long long)(max(past, 0) / kScaleBlock) + j) * kScaleBlock;
   if (p0 >= len || end == start) return;
-  const int pos0 = (int)p0, inside = pos0 % a.page_size;
-  const int page = __ldg(a.table + (long long)n * a.max_pages + pos0 / a.page_size);
+  const int pos0 = (int)p0, place = pos0 / a.page_size, inside = pos0 - place * a.page_size;
+  const int page = __ldg(a.table + (long long)n * a.max_pages + place);
+  const int row = lane / kLanes, col = lane % kLanes * 8;
+  // All rows' reads are on their way before anything waits for one.
+  Eight<T> x[kPasses];
+  {
+    const T *from = static_cast<const T *>(which ? a.v : a.k) + head * D + col;
+    const long long stride = which ? a.v_stride : a.k_stride;
+#pragma unroll
+    for (int i = 0; i < kPasses; i++) {
+      const int pos = pos0 + i * kAtOnce + row;
+      x[i].zero();
+      if (pos >= past && pos < len) x[i].get(from + (long long)(start + (pos - past)) * stride);
+    }
+  }
   if (page < 0 || page >= a.n_pages) {
     if (a.flags && lane == 0) atomicOr(a.flags, kFlagBadSeqlens);
     return;
@@ -101,49 +158,25 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_kv_append8_kernel(const Appen
   float *scale_at = (which ? a.v_scale : a.k_scale) + ((long long)page * (a.page_size / kScaleBlock) + inside / kScaleBlock) * a.HKV + head;
   const bool holds = pos0 < past;
   const float held = holds ? *scale_at : 0.f;
-  const int row = lane / kLanes, col = lane % kLanes * 8;
-  const long long stride = which ? a.v_stride : a.k_stride;
-  const T *x = static_cast<const T *>(which ? a.v : a.k) + head * D + col;
-  float y[kPasses][8];
   uint32_t top = 0;
-  bool odd = false;  // something is not finite
 #pragma unroll
-  for (int i = 0; i < kPasses; i++) {
-    const int pos = pos0 + i * kAtOnce + row;
-#pragma unroll
-    for (int e = 0; e < 8; e++) y[i][e] = 0.f;
-    if (pos >= past && pos < len) {
-      const T *from = x + (long long)(start + (pos - past)) * stride;
-      if constexpr (sizeof(T) == 2) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(from));
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          y[i][2 * e] = __uint_as_float(ws[e] << 16);
-          y[i][2 * e + 1] = __uint_as_float(ws[e] & 0xffff0000u);
-        }
-      } else {
-        const float4 u = __ldg(reinterpret_cast<const float4 *>(from)), w = __ldg(reinterpret_cast<const float4 *>(from) + 1);
-        y[i][0] = u.x; y[i][1] = u.y; y[i][2] = u.z; y[i][3] = u.w;
-        y[i][4] = w.x; y[i][5] = w.y; y[i][6] = w.z; y[i][7] = w.w;
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kPasses; i++)
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      const uint32_t b = __float_as_uint(y[i][e]) & 0x7fffffffu;
-      odd |= b >= 0x7f800000u;
-      top = max(top, b >= 0x7f800000u ? 0u : b);
-    }
+  for (int i = 0; i < kPasses; i++) top = max(top, x[i].top());
   top = __reduce_max_sync(0xffffffffu, top);
-  if (__any_sync(0xffffffffu, odd)) {
+  const bool odd = top >= 0x7f800000u;  // something is not finite: it becomes NaN and does not count for the scale
+  if (odd) {
+    top = 0;
+#pragma unroll 1
+    for (int i = 0; i < kPasses; i++) {
+      float y[8];
+      x[0].put(y);
 #pragma unroll
-    for (int i = 0; i < kPasses; i++)
+      for (int k = 1; k < kPasses; k++)
+        if (k == i) x[k].put(y);
 #pragma unroll
-      for (int e = 0; e < 8; e++)
-        if (!isfinite(y[i][e])) y[i][e] = CUDART_NAN_F;
+      for (int c = 0; c < 8; c++)
+        if (isfinite(y[c])) top = max(top, __float_as_uint(y[c]) & 0x7fffffffu);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
     if (a.flags && lane == 0) atomicOr(a.flags, kFlagNonfinite);
   }
   // top = f 2^k with f in [1, 2): top <= 1.75 2^8 2^e
@@ -151,18 +184,23 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_kv_append8_kernel(const Appen
   const float need = __int_as_float((127 + e) << 23), scale = fmaxf(held, need);
   uint8_t *cache = (which ? a.v_cache : a.k_cache) + (((long long)page * a.page_size + inside) * a.HKV + head) * D + col;
   const long long cache_row = (long long)a.HKV * D;
-  const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0 && scale < 0x1p127f;
-  const float inv = power ? __fdiv_rn(1.f, scale) : 0.f;
+  auto write = [&](auto quotient) {
 #pragma unroll
-  for (int i = 0; i < kPasses; i++) {
-    const int r = i * kAtOnce + row, pos = pos0 + r;
-    uint2 *to = reinterpret_cast<uint2 *>(cache + r * cache_row);
-    if (pos >= past && pos < len) {
-      float z[8];
-#pragma unroll
-      for (int c = 0; c < 8; c++) z[c] = power ? y[i][c] * inv : __fdiv_rn(y[i][c], scale);
-      *to = make_uint2(to_e4m3(z[0], z[1], z[2], z[3]), to_e4m3(z[4], z[5], z[6], z[7]));
+    for (int i = 0; i < kPasses; i++) {
+      const int r = i * kAtOnce + row, pos = pos0 + r;
+      float y[8];
+      x[i].put(y);
+      const uint2 z = make_uint2(to_e4m3(quotient(y[0]), quotient(y[1]), quotient(y[2]), quotient(y[3])),
+                                 to_e4m3(quotient(y[4]), quotient(y[5]), quotient(y[6]), quotient(y[7])));
+      if (pos >= past && pos < len) *reinterpret_cast<uint2 *>(cache + r * cache_row) = z;
     }
+  };
+  const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0 && scale < 0x1p127f;
+  if (power && !odd) {
+    const float inv = __int_as_float((254 << 23) - __float_as_int(scale));  // 1 / scale, exact
+    write([&](float y) { return y * inv; });
+  } else {
+    write([&](float y) { return isfinite(y) ? __fdiv_rn(y, scale) : CUDART_NAN_F; });
   }
   if (!(scale > held)) return;
   if (holds) {
@@ -192,9 +230,9 @@ template <int D, typename T>
 cudaError_t launch(const Append8Args &a, cudaStream_t stream) {
   const int per_seq = (int)(((long long)a.T + 2 * kScaleBlock - 2) / kScaleBlock);
   const long long slots = a.cu ? a.Ttot / kScaleBlock + 2LL * a.n_seqs : (long long)a.n_seqs * per_seq;
-  const long long blocks = (slots * 2 * a.HKV + kWarps - 1) / kWarps;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  gdn_kv_append8_kernel<D, T><<<(unsigned)blocks, kWarps * 32, 0, stream>>>(a, per_seq);
+  const int warps = 2 * a.HKV < kWarps ? 2 * a.HKV : kWarps;
+  if (slots > INT32_MAX) return cudaErrorInvalidValue;
+  gdn_kv_append8_kernel<D, T><<<dim3((unsigned)slots, (2 * a.HKV + warps - 1) / warps), warps * 32, 0, stream>>>(a, per_seq);
   return cudaGetLastError();
 }
 
