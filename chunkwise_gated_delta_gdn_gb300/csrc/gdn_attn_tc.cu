@@ -67,14 +67,16 @@ struct Smem {
   // barriers, in order: Q full, Q empty, S full x2, P ready x2, O full x2,
   // swap x2, halves x8, turn x2, unit full x4, unit empty x4, tile full, tile
   // empty
-  // (8 bits: and tile ready, Q ready)
-  static constexpr int kBarCount = (20 + 2 * kUnits + (FP8 ? 3 * kStages + 1 : 2 * kStages) + 1) / 2 * 2;
+  // (8 bits: and tile ready, Q ready, scales full)
+  static constexpr int kScaleSlots = D == 128 ? 4 : 8;  // see the loads
+  static constexpr int kBarCount = (20 + 2 * kUnits + (FP8 ? 3 * kStages + 1 + kScaleSlots : 2 * kStages) + 1) / 2 * 2;
   // tensor memory, abort, [X] stages that the scores free
   static constexpr int kSlot = kBars + kBarCount * 8;
-  // 8 bits: a tile's scales [stage][16], Q's powers [two units][row tile][32 rows], and
-  // what a tile's values are relative to, [stage] and [X]
-  static constexpr int kScale = kSlot + 16, kUp = kScale + kStages * 64, kRef = kUp + 64;
-  static constexpr int kTileRef = kRef + kStages * 4;
+  // 8 bits: scales of key tiles and of the values that go with them [slot][16], Q's
+  // powers [two units][row tile][32 rows], what a tile's values are relative to [stage]
+  // and [X], and whether a stage has values
+  static constexpr int kScale = kSlot + 16, kUp = kScale + kScaleSlots * 64, kRef = kUp + 64;
+  static constexpr int kKind = kRef + kStages * 4, kTileRef = kKind + kStages * 4;
   static constexpr int kBytes = FP8 ? kTileRef + 8 : kScale;
   static_assert(kSlot % 16 == 0, "read at once");
 };
@@ -243,6 +245,7 @@ struct Bars {
   // 8 bits: what was loaded is there as bf16
   __device__ uint32_t kv_ready(int i) const { return at(20 + 2 * kUnits + 2 * stages + i); }
   __device__ uint32_t q_ready() const { return at(20 + 2 * kUnits + 3 * stages); }
+  __device__ uint32_t scales(int i) const { return at(21 + 2 * kUnits + 3 * stages + i); }
 };
 
 // Position in a ring of N: index and how often it has gone round.
@@ -374,9 +377,10 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
       mbar_init(bars.unit_empty(i), FP8 ? 23 : 19);  // loader, products x2, sixteen softmax warps (and those that turn)
     }
     for (int i = 0; i < SM::kStages; i++) {
-      mbar_init(bars.kv_full(i), FP8 ? 33 : 1);  // 8 bits: and the loader's lanes, behind their scales
+      mbar_init(bars.kv_full(i), 1);
       if (FP8) mbar_init(bars.kv_ready(i), 4);
       if (FP8 && i == 0) mbar_init(bars.q_ready(), 4);
+      if (FP8 && i < SM::kScaleSlots) mbar_init(bars.scales(i), 32);  // the loader's lanes
       mbar_init(bars.kv_empty(i), 2);  // one from each X, or two from the one that reads it
     }
     mbar_fence_init();
@@ -398,7 +402,8 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
   // 768 threads leave 80 registers each: the softmax takes of the others'
   if constexpr (FP8) {
     if (warp < 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    else if (warp < 20) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   }
   if (warp < 16) {
     // ------------------------------------------------------------- softmax
@@ -533,12 +538,15 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         }
         uint32_t packed[32];
         uint64_t sum[2];
+        float f = 1.f;       // 8 bits: of the output, where rows of the warp
+        bool moved = false;  // have a new maximum
         while (true) {
           load_scores();
           // 8 bits: where this half of the row alone has outgrown m (in a unit's first tile
-          // always), its own maximum is taken, and what that is off by after the exchange is made good by a factor, not
-          // by a second pass: with keys of different sizes a third of the tiles has a row
-          // that moves (512 tokens over 32768 keys 341 -> 308 us).
+          // always), its own maximum is taken, and what that is off by after the exchange
+          // is made good by a factor, not by a second pass: with keys of different sizes a
+          // third of the tiles has a row that moves (512 tokens over 32768 keys 341 -> 308
+          // us).
           float at_hand = m;
           if constexpr (FP8) {
             const float y = fmaf(tile_max, xs, vs_top);
@@ -562,20 +570,29 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
           const bool move = top > m + (FP8 ? kRescale : grow);
           if constexpr (FP8) top = whole(top);
           if (__builtin_expect(!__any_sync(0xffffffffu, move), 1)) break;
-          const float f = move ? ex2(FP8 ? m - top : (m - top) * sl2) : 1.f;
+          f = move ? ex2(FP8 ? m - top : (m - top) * sl2) : 1.f;
           if (move) m = top;
-          if constexpr (FP8) {
-            // a power of two, in two steps: weights of up to 2^14 times 2^-38 still count
-            const float e = at_hand == m ? 0.f : fmaxf(at_hand - m, -48.f), e1 = truncf(0.5f * e);
-            const float g = ex2(e), g1 = ex2(e1), g2 = ex2(e - e1);
-            const uint32_t g1_2 = pack_f16(g1, g1), g2_2 = pack_f16(g2, g2);
-#pragma unroll
-            for (int c = 0; c < 32; c++) packed[c] = mul_f16(mul_f16(packed[c], g1_2), g2_2);
-            sum[0] = mul2(sum[0], pair(g, g));
-            sum[1] = mul2(sum[1], pair(g, g));
-          }
           l *= f;
-          if (FP8 && t == first) break;  // no output yet
+          if constexpr (FP8) {
+            // a power of two; below 2^-24 in two steps: weights of up to 2^14 times 2^-38
+            // still count
+            const float e = at_hand == m ? 0.f : fmaxf(at_hand - m, -48.f);
+            if (__any_sync(0xffffffffu, e != 0.f)) {
+              auto scale_weights = [&](float by) {
+                const float g = ex2(by);
+                const uint32_t g2 = pack_f16(g, g);
+#pragma unroll
+                for (int c = 0; c < 32; c++) packed[c] = mul_f16(packed[c], g2);
+              };
+              scale_weights(fmaxf(e, -24.f));
+              if (__any_sync(0xffffffffu, e < -24.f)) scale_weights(fminf(e + 24.f, 0.f));
+              const float g = ex2(e);
+              sum[0] = mul2(sum[0], pair(g, g));
+              sum[1] = mul2(sum[1], pair(g, g));
+            }
+            moved = t != first;  // before, there is no output
+            break;
+          }
 #pragma unroll 1
           for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
             uint32_t o[16];
@@ -585,10 +602,27 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
             tmem_st16_nowait(o_at + c, o);
           }
-          if constexpr (FP8) break;
           meet_half();
         }
         tmem_st32_nowait(p_at, packed);
+        if constexpr (FP8) {
+          if (__builtin_expect(moved, 0)) {
+#pragma unroll 1
+            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+              uint32_t o[32];
+              tmem_ld32_nowait(o_at + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float y0, y1;
+                unpair(mul2(pair(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), pair(f, f)), y0, y1);
+                o[i] = __float_as_uint(y0);
+                o[i + 1] = __float_as_uint(y1);
+              }
+              tmem_st32_nowait(o_at + c, o);
+            }
+          }
+        }
         float l0, l1;
         unpair(add2(sum[0], sum[1]), l0, l1);
         l += FP8 ? (l0 + l1) * vs_inv : l0 + l1;
@@ -697,14 +731,14 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
       // with their scales, but takes six instructions for two values where this takes
       // two: 512 tokens over 32768 keys 367 us.)
       // A warp has 32 rows of every tile, and turns them where they lie: they were
-      // loaded into the second half of the place that they take as fp16, so the
-      // first 16 rows are written before what is left, read beforehand, is
-      // overwritten.  Lanes 0-7 have 8 rows of one 16-byte piece (16 columns), whose
+      // loaded into the second half of the place that they take as fp16, so eight rows
+      // after the other never overwrite what all lanes have not read.  Lanes 0-7 have 8 rows of one 16-byte piece (16 columns), whose
       // 16-byte pieces of fp16 lie in different banks.
       constexpr int kRegion = SM::kTileBytes / 4, kPieces = D / 16;
       const int w = warp - 20, r = lane & 7, j0 = lane >> 3;
       Units units{unit_ring, bars, abort, {}};
       Ring<SM::kStages> ring;
+      uint32_t n_keys = 0, n_values = 0;  // tiles so far
       uint32_t q_phase = 0;
       int unit_parity = 1;
       AttnUnit u;
@@ -760,14 +794,22 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         for (int i = 0; i < tiles; i++) {
           wait(bars.kv_full(ring.i), ring.round, abort);
           const uint32_t region = sRing + ring.i * SM::kTileBytes + w * kRegion, raw = region + kRegion / 2;
-          const uint32_t scale_at = smem_addr(sm + SM::kScale) + ring.i * 64;
+          const bool values = shared_int(smem_addr(sm + SM::kKind) + ring.i * 4) != 0;
+          const int slot_i = (values ? n_values : n_keys) & (SM::kScaleSlots - 1);
+          const uint32_t scale_at = smem_addr(sm + SM::kScale) + slot_i * 64 + (values ? 32 : 0);
+          if (values) {
+            n_values++;
+          } else {
+            wait(bars.scales(slot_i), n_keys / SM::kScaleSlots & 1, abort);
+            n_keys++;
+          }
           auto largest = [&](uint32_t at) {
             const uint4 x = shared_uint4(at), y = shared_uint4(at + 16);
             return fmaxf(fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)), fmaxf(__uint_as_float(x.z), __uint_as_float(x.w))),
                          fmaxf(fmaxf(__uint_as_float(y.x), __uint_as_float(y.y)), fmaxf(__uint_as_float(y.z), __uint_as_float(y.w))));
           };
           const int ref = ref_exponent(largest(scale_at));
-          if (w == 0 && lane == 0)  // of a key tile: also that of the values that go with it
+          if (!values && w == 0 && lane == 0)  // also that of the values that go with it
             store_int(smem_addr(sm + SM::kRef) + ring.i * 4, (int)((uint32_t)ref << 16) | (ref_exponent(largest(scale_at + 32)) & 0xffff));
           const uint4 four = shared_uint4(scale_at + (w >> 1) * 16);  // rows 0-15 and 16-31 of this warp's: two of these
           const float s0 = __uint_as_float(w & 1 ? four.z : four.x) * two_to(-ref), s1 = __uint_as_float(w & 1 ? four.w : four.y) * two_to(-ref);
@@ -783,19 +825,14 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             store_uint4(to + ((c0 ^ r) << 4), f16_of<false>(x.x, g), f16_of<true>(x.x, g), f16_of<false>(x.y, g), f16_of<true>(x.y, g));
             store_uint4(to + (((c0 + 1) ^ r) << 4), f16_of<false>(x.z, g), f16_of<true>(x.z, g), f16_of<false>(x.w, g), f16_of<true>(x.w, g));
           };
-          uint4 x[2][kPieces / 4];
 #pragma unroll
-          for (int part = 0; part < 2; part++) {
+          for (int g = 0; g < 4; g++) {
+            uint4 x[kPieces / 4];
 #pragma unroll
-            for (int g = 0; g < 2; g++)
-#pragma unroll
-              for (int p = 0; p < kPieces / 4; p++) x[g][p] = read(part * 2 + g, p * 4 + j0);
+            for (int p = 0; p < kPieces / 4; p++) x[p] = read(g, p * 4 + j0);
             __syncwarp();
 #pragma unroll
-            for (int g = 0; g < 2; g++)
-#pragma unroll
-              for (int p = 0; p < kPieces / 4; p++) write(part * 2 + g, p * 4 + j0, x[g][p]);
-            __syncwarp();
+            for (int p = 0; p < kPieces / 4; p++) write(g, p * 4 + j0, x[p]);
           }
           fence_proxy_async();
           __syncwarp();
@@ -856,6 +893,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         int seq, base, page;
       } win[2] = {{-1, 0, 0}, {-1, 0, 0}};
       const int groups = a.page_size >> 3, my_key = lane * box;  // 8-row groups of a page
+      [[maybe_unused]] int scale_slot = 0;
       auto page_of = [&](int key) {
         return a.page_log >= 0 ? key >> a.page_log : key / a.page_size;
       };
@@ -884,23 +922,31 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
           const int n = min((last - key + box) / box, 128 / box);  // boxes; may be <= 0
           place(bars.kv_empty(ring.i), ring.round ^ 1);
           if constexpr (FP8) {
-            if (lane == 0 && !lost) mbar_arrive_expect_tx(full, max(n, 0) * box * D);
+            if (lane == 0 && !lost) {
+              store_int(smem_addr(sm + SM::kKind) + ring.i * 4, which);
+              mbar_arrive_expect_tx(full, max(n, 0) * box * D);
+            }
             __syncwarp();
-            // into the second half of what 32 rows take as bf16
+            // into the second half of what 32 rows take as fp16
             if (mine && !lost)
               tma_load_4d(dst + (my_key >> 5) * (SM::kTileBytes / 4) + SM::kTileBytes / 8 + (my_key & 31) * D, map, 0, 0, group,
                           w.kvh, full, w.n_tok * w.gp <= 128 ? once : often);
-            // lane i < 8 takes the i-th block's scale: zero in a bad page and past the last
-            // key; with a key tile come the scales of its values, lanes 8-15
-            const int k1 = min(key + (lane & 7) * kScaleBlock, last), page1 = page_of(max(k1, 0));
-            const int from = __shfl_sync(0xffffffffu, pages.page, (page1 - pages.base) & 31);
-            const bool there = key + (lane & 7) * kScaleBlock <= last && (unsigned)from < (unsigned)a.n_pages;
-            if (lane < (which ? 8 : 16) && !lost)
-              cp_async4(smem_addr(sm + SM::kScale) + (ring.i * 16 + lane) * 4,
-                        (which || lane >= 8 ? a.v_scale : a.k_scale) +
-                            (there ? ((long long)from * (a.page_size / kScaleBlock) + (k1 - page1 * a.page_size) / kScaleBlock) * a.HKV + w.kvh : 0),
-                        there ? 4 : 0);
-            if (!lost) cp_async_arrive_noinc(full);
+            // With a key tile come its scales (lanes 0-7) and those of its values (8-15),
+            // which follow in the same order: zero in a bad page and past the last key.  A
+            // slot's values have been turned before its next filling: that is for a key
+            // tile behind at least as many stages.
+            if (which == 0) {
+              const int k1 = min(key + (lane & 7) * kScaleBlock, last), page1 = page_of(max(k1, 0));
+              const int from = __shfl_sync(0xffffffffu, pages.page, (page1 - pages.base) & 31);
+              const bool there = key + (lane & 7) * kScaleBlock <= last && (unsigned)from < (unsigned)a.n_pages;
+              if (lane < 16 && !lost)
+                cp_async4(smem_addr(sm + SM::kScale) + (scale_slot * 16 + lane) * 4,
+                          (lane >= 8 ? a.v_scale : a.k_scale) +
+                              (there ? ((long long)from * (a.page_size / kScaleBlock) + (k1 - page1 * a.page_size) / kScaleBlock) * a.HKV + w.kvh : 0),
+                          there ? 4 : 0);
+              if (!lost) cp_async_arrive_noinc(bars.scales(scale_slot));
+              scale_slot = (scale_slot + 1) % SM::kScaleSlots;
+            }
             __syncwarp();
             ring.step();
             return;
