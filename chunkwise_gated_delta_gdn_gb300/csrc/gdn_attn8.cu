@@ -44,6 +44,7 @@ constexpr int kSlice = kScaleBlock;  // keys of a warp's step
 constexpr int kSlices = Shape8::kTile / kSlice;
 static_assert(kSlices == kWarps, "a slice of each tile for each warp");
 constexpr float kLag = 8.f;    // log2 growth of a maximum that is let stand
+constexpr float kNone = -0x1p120f;  // a maximum before any key: finite, so that -inf scores weigh 0
 constexpr float kShift = 6.f;  // log2 of the weights' factor
 
 template <int D, int NT>
@@ -52,7 +53,7 @@ struct Smem {
   static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr int kRow = D + 4;  // floats of a row where warps are joined
   static constexpr int kScale = kWarps * kStages * kSliceBytes;  // [warp][stage][2], behind the ring [warp][stage][keys, values]
-  static constexpr int kQ = kScale + kWarps * kStages * 8;       // [nt][k step][lane] two registers
+  static constexpr int kQ = kScale + kWarps * kStages * 8;       // [nt][two k steps][lane][k step] two registers
   static constexpr int kFactor = kQ + NT * (D / 16) * 32 * 8;    // [rows]
   static constexpr int kJoin = kFactor + NT * 8 * 4;             // [warp][rows] maximum, sum, maximum with V's scale
   static constexpr int kBytes = kJoin + kWarps * NT * 8 * 12;
@@ -101,10 +102,13 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
   return v;
 }
-// 16 bytes in the background, read once; zeros when !valid
-__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool valid, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(to), "l"(from), "r"(valid ? 16 : 0), "l"(policy)
+// 16 bytes in the background, read once; zeros for those past `bytes`
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, uint64_t policy, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(to), "l"(from), "r"(bytes), "l"(policy)
                : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -131,7 +135,17 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a
   AttnWalk<Shape8> walk(a, plan, st, blockIdx.x, gridDim.x);
   if (a.jobs && tid == 0) a.jobs[blockIdx.x].rows = 0;
   const uint64_t once = l2_evict_first();
-  const long long row_bytes = (long long)a.HKV * D;
+  // A lane copies a 16-byte piece of every kAtOnce-th row of a step.
+  constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks, kCopies = kSlice / kAtOnce;
+  const int my_row = lane / kChunks, chunk = lane % kChunks;
+  const long long row_bytes = (long long)a.HKV * D, rows_apart = kAtOnce * row_bytes;
+  uint32_t copy_to[kCopies];  // within a stage
+#pragma unroll
+  for (int j = 0; j < kCopies; j++) {
+    const int r = j * kAtOnce + my_row;
+    copy_to[j] = ring + r * D + ((chunk ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+  }
+  const int scale_blocks = a.page_size / kScaleBlock;
   AttnUnit u;
   while (walk.next(u)) {
     if (u.slot >= 0 && !a.jobs) {  // a cut unit has no place: never by the plan
@@ -153,32 +167,37 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a
         if (a.flags && i + lane < steps) atomicOr(a.flags, kFlagBadSeqlens);
       }
     };
-    auto fetch = [&](int i) {  // step i, into its stage; an empty group behind the last one
+    const long long lane_from = (long long)u.kvh * D + my_row * row_bytes + chunk * 16;
+    int to_stage = 0;
+    auto fetch = [&](int i) {  // step i, into the next stage; an empty group behind the last one
       if (i < steps) {
         if ((i & 31) == 0) look_up(i);
-        const int mine = __shfl_sync(0xffffffffu, page, i & 31);
+        const int mine = __shfl_sync(0xffffffffu, page, i & 31), at_page = max(mine, 0);
         const int key = (first + i * kWarps) * kSlice;
         const int inside = a.page_log >= 0 ? key & (a.page_size - 1) : key % a.page_size;
-        const int rows = mine < 0 ? 0 : min(u.len - key, kSlice);
-        const int at_page = max(mine, 0);
-        const int stage = i % SM::kStages;
-        const long long from = ((long long)at_page * a.page_size + inside) * row_bytes + (long long)u.kvh * D;
-        const uint32_t to = ring + stage * SM::kSliceBytes;
-        constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks;
-        const int chunk = lane % kChunks;
+        const long long from = ((long long)at_page * a.page_size + inside) * row_bytes + lane_from;
+        const char *k = static_cast<const char *>(a.k) + from, *v = static_cast<const char *>(a.v) + from;
+        const uint32_t stage = to_stage * SM::kSliceBytes;
+        if (mine >= 0 && key + kSlice <= u.len) {
 #pragma unroll
-        for (int j = 0; j < kSlice / kAtOnce; j++) {
-          const int r = j * kAtOnce + lane / kChunks;
-          const uint32_t dst = to + r * D + ((chunk ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
-          const long long src = from + (r < rows ? r * row_bytes : 0) + chunk * 16;
-          copy16(dst, static_cast<const char *>(a.k) + src, r < rows, once);
-          copy16(dst + kSlice * D, static_cast<const char *>(a.v) + src, r < rows, once);
+          for (int j = 0; j < kCopies; j++) {
+            copy16(copy_to[j] + stage, k + j * rows_apart, once);
+            copy16(copy_to[j] + stage + kSlice * D, v + j * rows_apart, once);
+          }
+        } else {
+          const int rows = mine < 0 ? 0 : u.len - key;
+#pragma unroll
+          for (int j = 0; j < kCopies; j++) {
+            const bool valid = j * kAtOnce + my_row < rows;
+            const long long at = valid ? from + j * rows_apart : 0;
+            copy16(copy_to[j] + stage, static_cast<const char *>(a.k) + at, once, valid ? 16 : 0);
+            copy16(copy_to[j] + stage + kSlice * D, static_cast<const char *>(a.v) + at, once, valid ? 16 : 0);
+          }
         }
-        if (lane < 2) {
-          const float *s = lane ? a.v_scale : a.k_scale;
-          cp_async4(smem_addr(scales + stage * 2 + lane),
-                    s + ((long long)at_page * (a.page_size / kScaleBlock) + inside / kScaleBlock) * a.HKV + u.kvh, mine < 0 ? 0 : 4);
-        }
+        if (lane < 2)
+          cp_async4(smem_addr(scales + to_stage * 2 + lane),
+                    (lane ? a.v_scale : a.k_scale) + ((long long)at_page * scale_blocks + inside / kScaleBlock) * a.HKV + u.kvh, mine < 0 ? 0 : 4);
+        to_stage = to_stage == SM::kStages - 1 ? 0 : to_stage + 1;
       }
       copies_end();
     };
@@ -202,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a
       if (lane * 4 < D) {
         // thread t' has elements t' D / 4 ..: 4 of them a k step
         const int owner = lane / (D / 16), step = lane % (D / 16);
-        const uint32_t to = q_at + (((r >> 3) * kSteps + step) * 32 + (r & 7) * 4 + owner) * 8;
+        const uint32_t to = q_at + (((r >> 3) * kSteps + (step & ~1)) * 32 + 2 * ((r & 7) * 4 + owner) + (step & 1)) * 8;
         const uint32_t b0 = pack_f16(scaled(lo0), scaled(hi0)), b1 = pack_f16(scaled(lo1), scaled(hi1));
         asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(b0), "r"(b1) : "memory");
       }
@@ -211,8 +230,9 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a
     }
     __syncthreads();
     float o[NT][D / 16][4];
+    // Of a row: the maximum of the scores and that of them with V's scale (powers of
+    // two), the sum of the weights, the factor of V's scale in weights, of K's in scores.
     float m[NT][2], mv[NT][2], l[NT][2], ratio[NT][2], f[NT][2];
-    int limit[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; n++) {
 #pragma unroll
@@ -222,19 +242,19 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a
 #pragma unroll
       for (int c = 0; c < 2; c++) {
         const int r = n * 8 + 2 * t + c;
-        m[n][c] = mv[n][c] = -CUDART_INF_F;
+        m[n][c] = mv[n][c] = kNone;
         l[n][c] = ratio[n][c] = 0.f;
         f[n][c] = factor[r];
-        limit[n][c] = u.pos0 + min(r / u.gp, u.n_tok - 1);
       }
     }
+    int stage = 0;
     for (int i = 0; i < steps; i++) {
       copies_wait<SM::kStages - 2>();
       __syncwarp();  // step i is there, and step i - 1 has been read
       fetch(i + SM::kStages - 1);
-      const int stage = i % SM::kStages;
       const uint32_t at = ring + stage * SM::kSliceBytes;
       const float2 scale = *reinterpret_cast<const float2 *>(scales + stage * 2);
+      stage = stage == SM::kStages - 1 ? 0 : stage + 1;
       float s[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; n++) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
@@ -248,41 +268,52 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a
           k1[w] = y.x; k1[w + 1] = y.y; k1[w + 2] = y.z; k1[w + 3] = y.w;
         }
 #pragma unroll
-        for (int k = 0; k < kSteps; k++) {
-          const uint32_t a0 = half_lo(k0[k]), a1 = half_lo(k1[k]), a2 = half_hi(k0[k]), a3 = half_hi(k1[k]);
+        for (int k = 0; k < kSteps; k += 2) {
+          uint4 b[NT];  // two steps' of Q
 #pragma unroll
-          for (int n = 0; n < NT; n++) {
-            const uint2 b = lds64(q_at + ((n * kSteps + k) * 32 + lane) * 8);
-            mma(s[n], a0, a1, a2, a3, b.x, b.y);
+          for (int n = 0; n < NT; n++) b[n] = lds128(q_at + ((n * kSteps + k) * 32 + 2 * lane) * 8);
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const uint32_t a0 = half_lo(k0[k + e]), a1 = half_lo(k1[k + e]), a2 = half_hi(k0[k + e]), a3 = half_hi(k1[k + e]);
+#pragma unroll
+            for (int n = 0; n < NT; n++) mma(s[n], a0, a1, a2, a3, e ? b[n].z : b[n].x, e ? b[n].w : b[n].y);
           }
         }
       }
       // s[n][0], [1]: key g of rows 2 t, 2 t + 1; [2], [3]: key g + 8
       const int key = (first + i * kWarps) * kSlice;
+      if (key + kSlice - 1 > u.pos0) {  // some row does not see all of them
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int c = 0; c < 2; c++) {
+            const int limit = u.pos0 + min((n * 8 + 2 * t + c) / u.gp, u.n_tok - 1);
+            if (key + g > limit) s[n][c] = -CUDART_INF_F;
+            if (key + g + 8 > limit) s[n][2 + c] = -CUDART_INF_F;
+          }
+      }
       // V's scale is below 2^(fv + 1); not below -117, so that `ratio` is finite for a zero one too
       const float fv = (float)max((int)(__float_as_uint(scale.y) >> 23 & 255) - 127, -117);
       bool move = false;
+      float fk[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; n++)
 #pragma unroll
         for (int c = 0; c < 2; c++) {
-          const float fk = f[n][c] * scale.x;
-          s[n][c] *= fk;
-          s[n][2 + c] *= fk;
-          if (key + g > limit[n][c]) s[n][c] = -CUDART_INF_F;
-          if (key + g + 8 > limit[n][c]) s[n][2 + c] = -CUDART_INF_F;
-          move |= fmaxf(s[n][c], s[n][2 + c]) > fminf(m[n][c], mv[n][c] - fv) + kLag;
+          fk[n][c] = fmaxf(f[n][c] * scale.x, 1e-37f);  // -inf times it stays that
+          const float top = fmaxf(s[n][c], s[n][2 + c]) * fk[n][c] - kLag;
+          move |= top > m[n][c] || top + fv > mv[n][c];
         }
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
           for (int c = 0; c < 2; c++) {
-            float top = fmaxf(s[n][c], s[n][2 + c]);
+            float top = fmaxf(s[n][c], s[n][2 + c]) * fk[n][c];
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             const float mn = fmaxf(m[n][c], top), vn = fmaxf(mv[n][c], top + fv);
-            const bool some = mn != -CUDART_INF_F;  // something is visible by now
+            const bool some = mn > kNone;  // something is visible by now
             l[n][c] *= some ? ex2(m[n][c] - mn) : 0.f;
             const float down = some ? ex2(mv[n][c] - vn) : 0.f;
             ratio[n][c] = some ? ex2(mn - vn + kShift) : 0.f;
@@ -301,8 +332,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a
         float w[4];
 #pragma unroll
         for (int c = 0; c < 2; c++) {
-          const float off = m[n][c] == -CUDART_INF_F ? 0.f : m[n][c];
-          const float p0 = ex2(s[n][c] - off), p1 = ex2(s[n][2 + c] - off), fw = scale.y * ratio[n][c];
+          const float p0 = ex2(fmaf(s[n][c], fk[n][c], -m[n][c])), p1 = ex2(fmaf(s[n][2 + c], fk[n][c], -m[n][c])), fw = scale.y * ratio[n][c];
           l[n][c] += p0 + p1;
           w[c] = p0 * fw;
           w[2 + c] = p1 * fw;
@@ -369,10 +399,11 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a
     const bool part = u.slot >= 0;
     for (int item = tid; item < rows * (D / 4); item += kThreads) {
       const int r = item / (D / 4), d4 = item % (D / 4);
-      float top = -CUDART_INF_F, sum = 0.f;
+      float top = kNone, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; w++) top = fmaxf(top, join[(w * NT * 8 + r) * 3]);
-      const float base = top == -CUDART_INF_F ? 0.f : top;
+      const float base = top;
+      if (top <= kNone) top = -CUDART_INF_F;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; w++) {
