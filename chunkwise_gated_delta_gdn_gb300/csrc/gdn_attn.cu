@@ -363,7 +363,7 @@ constexpr int kMergeMany = 16;  // from here on slices of columns pay (131072 ke
                                 // -> 35.8 us; 4 sequences of 16384 in 6 pieces each 54.8 -> 57.2)
 // blocks to a job: 32 rows each, and at least four for slices of the columns
 template <class S>
-constexpr int merge_blocks() { return S::kRows < kMergeRows ? 4 : S::kRows / kMergeRows; }
+constexpr int merge_blocks() { return S::kRows <= kMergeRows ? 4 : S::kRows / kMergeRows; }
 template <class S, int D, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads) gdn_attn_merge_kernel(const AttnArgs a) {
   __shared__ float weight[kMergeRows], total[kMergeRows];
@@ -566,8 +566,11 @@ cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &don
   return e;
 }
 
-cudaError_t launch_attn8_merge(const AttnArgs &a, int d, bool few, int blocks, cudaStream_t stream) {
-  if (few) return d == 64 ? merge<Shape8, 64, true>(a, blocks, stream) : merge<Shape8, 128, true>(a, blocks, stream);
+cudaError_t launch_attn8_merge(const AttnArgs &a, int d, int rows, int blocks, cudaStream_t stream) {
+  if (rows == 16)
+    return d == 64 ? merge<FewShape8<16>, 64, true>(a, blocks, stream) : merge<FewShape8<16>, 128, true>(a, blocks, stream);
+  if (rows == 32)
+    return d == 64 ? merge<FewShape8<32>, 64, true>(a, blocks, stream) : merge<FewShape8<32>, 128, true>(a, blocks, stream);
   return d == 64 ? merge<TcShape, 64, true>(a, blocks, stream) : merge<TcShape, 128, true>(a, blocks, stream);
 }
 

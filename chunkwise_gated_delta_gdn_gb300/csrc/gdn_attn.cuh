@@ -86,9 +86,9 @@ struct AttnShape {
   static constexpr int kRows = ROWS, kPack = PACK, kTile = TILE, kFew = FEW;
   static constexpr int kMinGrain = MIN_GRAIN, kWhole = WHOLE, kCut = CUT;
   static constexpr int kWide = WIDE, kOver = OVER, kNarrow = NARROW, kPackedOver = PACKED_OVER;
-  static constexpr int kOnly = 0;  // sequences: all; 1: with at most kFewRows rows for a key/value head; 2: with more
+  // sequences: all; 1: with at most AttnArgs::few_rows rows for a key/value head; 2: with more
+  static constexpr int kOnly = 0;
 };
-constexpr int kFewRows = 16;
 // The bf16 kernel's (gdn_attn_tc.cu).  A packed unit's tile takes 3/4 of an
 // unpacked one's: 1/2, 2/3, 3/4 and 1 gave 129, 107, 104 and 109 us for two
 // chunks of up to 500 tokens among 14 single ones (32 heads of 64), and 164, 153,
@@ -101,7 +101,8 @@ constexpr int kFewRows = 16;
 using TcShape = AttnShape<256, 128, 128, 4, 8, 3, 6, 128, 3, 3, 40>;
 // Over a cache in 8 bits two kernels share a call's sequences: few rows go to that of
 // gdn_attn8.cu, more to the bf16 one's over such a cache.
-struct Shape8 : AttnShape<kFewRows, kFewRows, 128, 2, 4, 2, 4, kFewRows, 1, 3> {
+template <int ROWS>
+struct FewShape8 : AttnShape<ROWS, ROWS, 128, 2, 4, 2, 4, ROWS, 1, 3> {
   static constexpr int kOnly = 1;
 };
 struct TcShape8 : TcShape {
@@ -176,7 +177,7 @@ template <class S>
 __host__ __device__ __forceinline__ AttnSeq attn_seq_of(const AttnArgs &a, int n, bool &bad) {
   AttnSeq s = attn_seq(a, n, bad);
   if constexpr (S::kOnly != 0) {
-    const bool few = (long long)s.nq * (a.H / a.HKV) <= kFewRows;
+    const bool few = (long long)s.nq * (a.H / a.HKV) <= a.few_rows;
     if (few != (S::kOnly == 1)) s.nq = 0;
   }
   return s;

@@ -41,8 +41,13 @@ using namespace sm100;
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kSlice = kScaleBlock;  // keys of a warp's step
-constexpr int kSlices = Shape8::kTile / kSlice;
+template <int NT>
+using Shape8 = FewShape8<NT == 4 ? 32 : 16>;
+constexpr int kSlices = Shape8<1>::kTile / kSlice;
 static_assert(kSlices == kWarps, "a slice of each tile for each warp");
+// Blocks of an SM: 32 rows take 255 registers of a thread for their output alone.
+template <int NT>
+constexpr int blocks_per_sm() { return NT == 4 ? 1 : 2; }
 constexpr float kLag = 8.f;    // log2 growth of a maximum that is let stand
 constexpr float kNone = -0x1p120f;  // a maximum before any key: finite, so that -inf scores weigh 0
 constexpr float kShift = 6.f;  // log2 of the weights' factor
@@ -50,7 +55,7 @@ constexpr float kShift = 6.f;  // log2 of the weights' factor
 template <int D, int NT>
 struct Smem {
   static constexpr int kSliceBytes = 2 * kSlice * D;
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = (D == 128 ? 6 : 12) / blocks_per_sm<NT>();
   static constexpr int kRow = D + 4;  // floats of a row where warps are joined
   static constexpr int kScale = kWarps * kStages * kSliceBytes;  // [warp][stage][2], behind the ring [warp][stage][keys, values]
   static constexpr int kQ = kScale + kWarps * kStages * 8;       // [nt][two k steps][lane][k step] two registers
@@ -60,7 +65,9 @@ struct Smem {
   static_assert(kWarps * NT * 8 * kRow * 4 <= kScale, "joined in the ring's place");
   static_assert(kStaged * sizeof(AttnStaged) + kThreads * sizeof(AttnChunk) <= kScale, "staging in the ring's place");
 };
-static_assert(2 * (Smem<128, 2>::kBytes + 1024) <= 233472 && 2 * (Smem<64, 2>::kBytes + 1024) <= 233472, "two blocks to an SM");
+template <int D, int NT>
+constexpr bool fits() { return blocks_per_sm<NT>() * (Smem<D, NT>::kBytes + 1024) <= 233472; }
+static_assert(fits<64, 2>() && fits<128, 2>() && fits<64, 4>() && fits<128, 4>(), "shared memory of one SM");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -102,13 +109,16 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
   return v;
 }
-// 16 bytes in the background, read once; zeros for those past `bytes`
+// 16 bytes in the background, read once; zeros for those past `bytes`.  L2 fetches no
+// more than 64 bytes around them: with its default, a 64-byte row came with the next
+// head's, gone again before that was read (64 sequences over 4096 keys, 8 heads of 64:
+// 95 us, twice the bytes; so 62.5).
 __device__ __forceinline__ void copy16(uint32_t to, const void *from, uint64_t policy, int bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(to), "l"(from), "r"(bytes), "l"(policy)
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::64B [%0], [%1], 16, %2, %3;" ::"r"(to), "l"(from), "r"(bytes), "l"(policy)
                : "memory");
 }
 __device__ __forceinline__ void copy16(uint32_t to, const void *from, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::64B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -116,8 +126,9 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 
 // NT: groups of 8 rows
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kernel(const AttnArgs a) {
   using SM = Smem<D, NT>;
+  using S = Shape8<NT>;
   constexpr int kSteps = D / 16;          // of 16 elements
   constexpr int kWords = D / 16;          // 32-bit words of a key that a thread takes
   extern __shared__ __align__(128) unsigned char sm[];
@@ -126,13 +137,13 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a
   float *scales = reinterpret_cast<float *>(sm + SM::kScale) + warp * SM::kStages * 2;
   float *factor = reinterpret_cast<float *>(sm + SM::kFactor), *join = reinterpret_cast<float *>(sm + SM::kJoin);
   const uint32_t q_at = smem_addr(sm + SM::kQ);
-  AttnPlan<Shape8> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
+  AttnPlan<S> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
   AttnStaged *staged = reinterpret_cast<AttnStaged *>(sm);  // until the first copies
-  attn_stage<kThreads, Shape8>(a, staged, blockIdx.x);
+  attn_stage<kThreads, S>(a, staged, blockIdx.x);
   asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel waits for this one's end
   __syncthreads();
   const AttnStart st = attn_start(a, plan, staged, blockIdx.x, gridDim.x);  // each warp for itself
-  AttnWalk<Shape8> walk(a, plan, st, blockIdx.x, gridDim.x);
+  AttnWalk<S> walk(a, plan, st, blockIdx.x, gridDim.x);
   if (a.jobs && tid == 0) a.jobs[blockIdx.x].rows = 0;
   const uint64_t once = l2_evict_first();
   // A lane copies a 16-byte piece of every kAtOnce-th row of a step.
@@ -154,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a
     }
     if (tid == 0 && u.slot == 2 * (int)blockIdx.x + 1) a.jobs[blockIdx.x] = attn_job(u);
     __syncthreads();  // the previous unit's (or the plan's) shared memory has been read
-    const int end = min(u.t1 * Shape8::kTile, max(u.pos0 + u.n_tok, 0));  // behind the last key that anybody sees
+    const int end = min(u.t1 * S::kTile, max(u.pos0 + u.n_tok, 0));  // behind the last key that anybody sees
     const int first = u.t0 * kSlices + warp, n_slices = (end + kSlice - 1) / kSlice;
     const int steps = n_slices > first ? (n_slices - first + kWarps - 1) / kWarps : 0;  // this warp's
     // The pages of 32 steps, a lane each.
@@ -414,8 +425,8 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_attn8_kernel(const AttnArgs a
         y.x += fo * z.x; y.y += fo * z.y; y.z += fo * z.z; y.w += fo * z.w;
       }
       if (part) {
-        a.part_o[((long long)u.slot * (D / 4) + d4) * Shape8::kRows + r] = y;
-        if (d4 == 0) a.part_ml[(long long)u.slot * Shape8::kRows + r] = make_float2(top, sum);
+        a.part_o[((long long)u.slot * (D / 4) + d4) * S::kRows + r] = y;
+        if (d4 == 0) a.part_ml[(long long)u.slot * S::kRows + r] = make_float2(top, sum);
       } else {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
@@ -443,13 +454,21 @@ cudaError_t launch(const AttnArgs &a, int blocks, cudaStream_t stream) {
 
 }  // namespace
 
-bool attn8_launch(const AttnArgs &a, Attn8Launch &l) {
+bool attn8_launch(const AttnArgs &a, int d, Attn8Launch &l) {
   const long long G = a.H / a.HKV, most = (a.cu ? (long long)a.Ttot : (long long)a.T) * G;  // rows of a sequence
+  // Up to 32 rows: 64 sequences over 4096 keys, 8 key/value heads of 128, with 20 to 32
+  // rows each take 250 us as many ones, @@ as few.  In a packed call most sequences have
+  // one token, G rows, which the kernel for 16 does faster.
+  const int limit = a.cu && G <= 16 ? 16 : 32;
   l.few = l.many = a;
-  l.has_few = a.cu ? G <= kFewRows : most <= kFewRows;
-  l.has_many = most > kFewRows;
+  l.few.few_rows = l.many.few_rows = limit;
+  l.has_few = a.cu ? G <= limit : most <= limit;
+  l.has_many = most > limit;
+  l.groups = a.cu ? limit / 8 : most <= 8 ? 1 : most <= 16 ? 2 : 4;
   l.few_launch = l.many_launch = AttnLaunch{};
-  if (l.has_few) l.few_launch = attn_plan_launch<Shape8>(l.few, 2 * sm_count());
+  if (l.has_few)
+    l.few_launch = l.groups == 4 ? attn_plan_launch<Shape8<4>>(l.few, blocks_per_sm<4>() * sm_count())
+                                 : attn_plan_launch<Shape8<2>>(l.few, blocks_per_sm<2>() * sm_count());
   if (l.has_many) l.many_launch = attn_plan_launch<TcShape8>(l.many, sm_count());
   return (!l.has_few || l.few_launch.blocks > 0) && (!l.has_many || l.many_launch.blocks > 0);
 }
@@ -459,19 +478,20 @@ cudaError_t launch_attn8(const Attn8Launch &l, int d, cudaStream_t stream) {
     const cudaError_t e = launch_attn8_tc(l.many, d, l.many_launch.blocks, stream);
     if (e != cudaSuccess) return e;
     if (l.many_launch.split && l.many_launch.blocks > 1) {
-      const cudaError_t m = launch_attn8_merge(l.many, d, false, l.many_launch.blocks, stream);
+      const cudaError_t m = launch_attn8_merge(l.many, d, l.many_launch.rows, l.many_launch.blocks, stream);
       if (m != cudaSuccess) return m;
     }
   }
   if (!l.has_few) return cudaSuccess;
-  // one group of 8 rows where no sequence has more
   const AttnArgs &a = l.few;
   const int blocks = l.few_launch.blocks;
-  const bool one = !a.cu && (long long)a.T * (a.H / a.HKV) <= 8;
-  const cudaError_t e = d == 64 ? (one ? launch<64, 1>(a, blocks, stream) : launch<64, 2>(a, blocks, stream))
-                                : (one ? launch<128, 1>(a, blocks, stream) : launch<128, 2>(a, blocks, stream));
+  cudaError_t e;
+  if (d == 64)
+    e = l.groups == 1 ? launch<64, 1>(a, blocks, stream) : l.groups == 2 ? launch<64, 2>(a, blocks, stream) : launch<64, 4>(a, blocks, stream);
+  else
+    e = l.groups == 1 ? launch<128, 1>(a, blocks, stream) : l.groups == 2 ? launch<128, 2>(a, blocks, stream) : launch<128, 4>(a, blocks, stream);
   if (e != cudaSuccess || !l.few_launch.split || blocks < 2) return e;
-  return launch_attn8_merge(a, d, true, blocks, stream);
+  return launch_attn8_merge(a, d, l.few_launch.rows, blocks, stream);
 }
 
 }  // namespace gdn

@@ -48,7 +48,7 @@ size_t gdn_attn_paged_fp8_fwd_workspace_bytes(int B, int T, int H, int HKV, int 
     a.kv_lens = kSomewhere;
     a.max_len = page_size * max_pages;
     gdn::Attn8Launch l;
-    if (!gdn::attn8_launch(a, l)) continue;
+    if (!gdn::attn8_launch(a, d, l)) continue;
     const size_t bytes = parts8_bytes(l, d);
     if (bytes > most) most = bytes;
   }
@@ -94,7 +94,7 @@ gdn_status gdn_attn_paged_fp8_fwd(const void *q, const void *k_cache, const void
   a.flags = flags;
   a.scale_log2 = scale * 1.44269504088896340736f;
   gdn::Attn8Launch l;
-  if (!gdn::attn8_launch(a, l)) return GDN_ERR_UNSUPPORTED;
+  if (!gdn::attn8_launch(a, d, l)) return GDN_ERR_UNSUPPORTED;
   const size_t ws = parts8_bytes(l, d);
   if (ws > 0 && (!workspace || workspace_bytes < ws)) return GDN_ERR_WORKSPACE;
   if (!aligned_to(workspace, 256)) return GDN_ERR_INVALID_ARG;

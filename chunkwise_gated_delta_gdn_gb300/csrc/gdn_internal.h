@@ -145,6 +145,8 @@ struct AttnArgs {
   AttnJob *jobs;               // [blocks] what is to be joined
   uint32_t *flags;             // device status word, or nullptr
   const float *k_scale, *v_scale;  // of a cache in 8 bits: [n_pages][page_size / kScaleBlock][HKV]
+  int few_rows;                // rows for a key/value head up to which a sequence goes to the kernel
+                               // for few rows (a cache in 8 bits)
 };
 // Tokens of a cache in 8 bits that share a scale (for each head).
 constexpr int kScaleBlock = 16;
@@ -287,11 +289,13 @@ struct Attn8Launch {
   AttnArgs few, many;
   AttnLaunch few_launch, many_launch;
   bool has_few, has_many;  // a call may have such sequences
+  int groups;              // of 8 rows, that the kernel for few rows has: 1, 2 or 4
 };
-bool attn8_launch(const AttnArgs &a, Attn8Launch &l);  // false: more work than the plan can count
+bool attn8_launch(const AttnArgs &a, int d, Attn8Launch &l);  // false: more work than the plan can count
 cudaError_t launch_attn8(const Attn8Launch &l, int d, cudaStream_t stream);
 cudaError_t launch_attn8_tc(const AttnArgs &a, int d, int blocks, cudaStream_t stream);
-cudaError_t launch_attn8_merge(const AttnArgs &a, int d, bool few, int blocks, cudaStream_t stream);
+// rows: of a unit (16, 32 or 256)
+cudaError_t launch_attn8_merge(const AttnArgs &a, int d, int rows, int blocks, cudaStream_t stream);
 // tensor map of bytes, in the swizzle of `row` bytes (64 or 128)
 bool encode_byte_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
                      const uint64_t *strides, const uint32_t *box, int row);

@@ -151,7 +151,8 @@ def test_chunks_and_tokens_together(d, page, H, HKV):
     check_paged(run(x), x, q_lens, d)
 
 
-@pytest.mark.parametrize("B, T, H, HKV, d", [(3, 2, 8, 2, 64), (2, 4, 4, 1, 128), (2, 33, 16, 2, 128), (1, 515, 3, 3, 64)])
+@pytest.mark.parametrize("B, T, H, HKV, d", [(3, 2, 8, 2, 64), (2, 4, 4, 1, 128), (2, 33, 16, 2, 128), (1, 515, 3, 3, 64),
+                                             (3, 6, 8, 2, 128), (2, 32, 2, 2, 64), (2, 17, 2, 1, 128), (2, 1, 64, 2, 64)])
 def test_equal_chunks(B, T, H, HKV, d):
     kv = [T + 37 * i + 5 for i in range(B)]
     x = paged([T] * B, kv, H, HKV, d, 32, seed=B + T)
