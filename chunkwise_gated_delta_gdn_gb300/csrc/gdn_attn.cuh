@@ -105,6 +105,10 @@ template <int ROWS>
 struct FewShape8 : AttnShape<ROWS, ROWS, 128, 2, 4, 2, 4, ROWS, 1, 3> {
   static constexpr int kOnly = 1;
 };
+// where a unit is one warp's
+struct SoloShape8 : AttnShape<16, 16, 128, 4, 2, 4, 2, 16, 1, 3> {
+  static constexpr int kOnly = 1;
+};
 struct TcShape8 : TcShape {
   static constexpr int kOnly = 2;
 };

@@ -30,6 +30,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "gdn_attn.cuh"
 #include "gdn_sm100.cuh"
@@ -41,8 +42,8 @@ using namespace sm100;
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kSlice = kScaleBlock;  // keys of a warp's step
-template <int NT>
-using Shape8 = FewShape8<NT == 4 ? 32 : 16>;
+template <int NT, bool SOLO = false>
+using Shape8 = std::conditional_t<SOLO, SoloShape8, FewShape8<NT == 4 ? 32 : 16>>;
 constexpr int kSlices = Shape8<1>::kTile / kSlice;
 static_assert(kSlices == kWarps, "a slice of each tile for each warp");
 // Blocks of an SM: 32 rows take 255 registers of a thread for their output alone.
@@ -52,22 +53,29 @@ constexpr float kLag = 8.f;    // log2 growth of a maximum that is let stand
 constexpr float kNone = -0x1p120f;  // a maximum before any key: finite, so that -inf scores weigh 0
 constexpr float kShift = 6.f;  // log2 of the weights' factor
 
-template <int D, int NT>
+template <int D, int NT, bool MANY = false>
 struct Smem {
   static constexpr int kSliceBytes = 2 * kSlice * D;
   static constexpr int kStages = (D == 128 ? 6 : 12) / blocks_per_sm<NT>();
+  static constexpr int kCopies = MANY ? kWarps : 1;  // of Q
   static constexpr int kRow = D + 4;  // floats of a row where warps are joined
   static constexpr int kScale = kWarps * kStages * kSliceBytes;  // [warp][stage][2], behind the ring [warp][stage][keys, values]
   static constexpr int kQ = kScale + kWarps * kStages * 8;       // [nt][two k steps][lane][k step] two registers
-  static constexpr int kFactor = kQ + NT * (D / 16) * 32 * 8;    // [rows]
-  static constexpr int kJoin = kFactor + NT * 8 * 4;             // [warp][rows] maximum, sum, maximum with V's scale
-  static constexpr int kBytes = kJoin + kWarps * NT * 8 * 12;
+  static constexpr int kQBytes = NT * (D / 16) * 32 * 8;
+  static constexpr int kFactor = kQ + kCopies * kQBytes;         // [rows]
+  // [warp][rows] maximum, sum, maximum with V's scale (where a unit is a block's, in the
+  // place of a second copy of Q)
+  static constexpr int kEnd = kFactor + kCopies * NT * 8 * 4, kJoinBytes = kWarps * NT * 8 * 12;
+  static constexpr int kJoin = MANY ? kQ + kQBytes : kEnd;
+  static constexpr int kBytes = kEnd + (MANY ? 0 : kJoinBytes);
+  static_assert(!MANY || kJoinBytes <= kQBytes, "in a copy's place");
   static_assert(kWarps * NT * 8 * kRow * 4 <= kScale, "joined in the ring's place");
   static_assert(kStaged * sizeof(AttnStaged) + kThreads * sizeof(AttnChunk) <= kScale, "staging in the ring's place");
 };
-template <int D, int NT>
-constexpr bool fits() { return blocks_per_sm<NT>() * (Smem<D, NT>::kBytes + 1024) <= 233472; }
+template <int D, int NT, bool MANY = false>
+constexpr bool fits() { return blocks_per_sm<NT>() * (Smem<D, NT, MANY>::kBytes + 1024) <= 233472; }
 static_assert(fits<64, 2>() && fits<128, 2>() && fits<64, 4>() && fits<128, 4>(), "shared memory of one SM");
+static_assert(fits<64, 1, true>() && fits<128, 1, true>(), "shared memory of one SM");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -124,27 +132,37 @@ __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_gro
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// NT: groups of 8 rows
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kernel(const AttnArgs a) {
-  using SM = Smem<D, NT>;
-  using S = Shape8<NT>;
+// NT: groups of 8 rows.  SOLO: a unit is one warp's, all of its keys, so that nothing
+// but the plan's start is shared by a block's warps.  MANY: partial results lie as
+// gdn_attn8_merge_kernel reads them.  All threads of a block, lengths staged.
+template <int D, int NT, bool SOLO, bool MANY>
+__device__ __forceinline__ void run(const AttnArgs &a, unsigned char *sm) {
+  using SM = Smem<D, NT, MANY>;
+  using S = Shape8<NT, SOLO>;
+  constexpr int kStride = SOLO ? 1 : kWarps;  // steps from one of a warp's to the next
   constexpr int kSteps = D / 16;          // of 16 elements
   constexpr int kWords = D / 16;          // 32-bit words of a key that a thread takes
-  extern __shared__ __align__(128) unsigned char sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_addr(sm) + warp * SM::kStages * SM::kSliceBytes;
   float *scales = reinterpret_cast<float *>(sm + SM::kScale) + warp * SM::kStages * 2;
-  float *factor = reinterpret_cast<float *>(sm + SM::kFactor), *join = reinterpret_cast<float *>(sm + SM::kJoin);
-  const uint32_t q_at = smem_addr(sm + SM::kQ);
+  float *factor = reinterpret_cast<float *>(sm + SM::kFactor) + (SOLO ? warp * NT * 8 : 0);
+  [[maybe_unused]] float *join = reinterpret_cast<float *>(sm + SM::kJoin);
+  const uint32_t q_at = smem_addr(sm + SM::kQ) + (SOLO ? warp * SM::kQBytes : 0);
+  // what the plan deals to: blocks, or warps
+  const int me = SOLO ? blockIdx.x * kWarps + warp : blockIdx.x, all = SOLO ? gridDim.x * kWarps : gridDim.x;
+  const bool speaks = SOLO ? lane == 0 : tid == 0;
+  auto meet = [] {
+    if constexpr (SOLO) __syncwarp();
+    else __syncthreads();
+  };
   AttnPlan<S> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
-  AttnStaged *staged = reinterpret_cast<AttnStaged *>(sm);  // until the first copies
-  attn_stage<kThreads, S>(a, staged, blockIdx.x);
-  asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel waits for this one's end
-  __syncthreads();
-  const AttnStart st = attn_start(a, plan, staged, blockIdx.x, gridDim.x);  // each warp for itself
-  AttnWalk<S> walk(a, plan, st, blockIdx.x, gridDim.x);
-  if (a.jobs && tid == 0) a.jobs[blockIdx.x].rows = 0;
+  const AttnStaged *staged = reinterpret_cast<const AttnStaged *>(sm);  // until the first copies
+  const AttnStart st = attn_start(a, plan, staged, me, all);  // each warp for itself
+  AttnWalk<S> walk(a, plan, st, me, all);
+  if (a.jobs && speaks) a.jobs[me].rows = 0;
+  if (MANY && !SOLO && a.jobs)  // the merge kernel looks at a job for each warp
+    for (int i = all + me * (kWarps - 1) + tid; i < all + (me + 1) * (kWarps - 1); i += kThreads) a.jobs[i].rows = 0;
+  __syncthreads();  // what was staged has been read
   const uint64_t once = l2_evict_first();
   // A lane copies a 16-byte piece of every kAtOnce-th row of a step.
   constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks, kCopies = kSlice / kAtOnce;
@@ -160,18 +178,18 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kerne
   AttnUnit u;
   while (walk.next(u)) {
     if (u.slot >= 0 && !a.jobs) {  // a cut unit has no place: never by the plan
-      if (tid == 0 && a.flags) atomicOr(a.flags, kFlagLaunchConfig);
+      if (speaks && a.flags) atomicOr(a.flags, kFlagLaunchConfig);
       continue;
     }
-    if (tid == 0 && u.slot == 2 * (int)blockIdx.x + 1) a.jobs[blockIdx.x] = attn_job(u);
-    __syncthreads();  // the previous unit's (or the plan's) shared memory has been read
+    if (speaks && u.slot == 2 * me + 1) a.jobs[me] = attn_job(u);
+    meet();  // the previous unit's (or the plan's) shared memory has been read
     const int end = min(u.t1 * S::kTile, max(u.pos0 + u.n_tok, 0));  // behind the last key that anybody sees
-    const int first = u.t0 * kSlices + warp, n_slices = (end + kSlice - 1) / kSlice;
-    const int steps = n_slices > first ? (n_slices - first + kWarps - 1) / kWarps : 0;  // this warp's
+    const int first = u.t0 * kSlices + (SOLO ? 0 : warp), n_slices = (end + kSlice - 1) / kSlice;
+    const int steps = n_slices > first ? (n_slices - first + kStride - 1) / kStride : 0;  // this warp's
     // The pages of 32 steps, a lane each.
     int page = 0;
     auto look_up = [&](int i) {
-      const int key = min((first + (i + lane) * kWarps) * kSlice, u.len - 1);
+      const int key = min((first + (i + lane) * kStride) * kSlice, u.len - 1);
       page = __ldg(a.table + (long long)u.seq * a.max_pages + (a.page_log >= 0 ? key >> a.page_log : key / a.page_size));
       if ((unsigned)page >= (unsigned)a.n_pages) {  // reads as zeros
         page = -1;
@@ -184,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kerne
       if (i < steps) {
         if ((i & 31) == 0) look_up(i);
         const int mine = __shfl_sync(0xffffffffu, page, i & 31), at_page = max(mine, 0);
-        const int key = (first + i * kWarps) * kSlice;
+        const int key = (first + i * kStride) * kSlice;
         const int inside = a.page_log >= 0 ? key & (a.page_size - 1) : key % a.page_size;
         const long long from = ((long long)at_page * a.page_size + inside) * row_bytes + lane_from;
         const char *k = static_cast<const char *>(a.k) + from, *v = static_cast<const char *>(a.v) + from;
@@ -217,12 +235,21 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kerne
     // Q's fragments: row r of group nt, for k step s the elements 2 D / 8 t' + 4 s .. + 3
     // of thread t' of a row.  A warp has whole rows, so that each row's largest
     // exponent is at hand.
-    for (int r = warp; r < NT * 8; r += kWarps) {
-      const int tok = r / u.gp;
-      uint2 x = make_uint2(0, 0);  // 4 elements for each lane (d = 64: lanes 0-15)
+    constexpr int kMine = SOLO ? NT * 8 : NT;  // rows of a warp
+    auto row_of = [&](int i) { return SOLO ? i : warp + i * kWarps; };
+    uint2 q[kMine];  // 4 elements for each lane (d = 64: lanes 0-15)
+#pragma unroll
+    for (int i = 0; i < kMine; i++) {
+      const int r = row_of(i), tok = r / u.gp;
+      q[i] = make_uint2(0, 0);
       if (tok < u.n_tok && lane * 4 < D)
-        x = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + (long long)(u.row0 + tok) * a.q_stride +
-                                                  (u.head0 + r % u.gp) * D + lane * 4));
+        q[i] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + (long long)(u.row0 + tok) * a.q_stride +
+                                                     (u.head0 + r % u.gp) * D + lane * 4));
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; i++) {
+      const int r = row_of(i);
+      const uint2 x = q[i];
       const uint32_t lo0 = x.x << 16, hi0 = x.x & 0xffff0000u, lo1 = x.y << 16, hi1 = x.y & 0xffff0000u;
       const uint32_t top = __reduce_max_sync(0xffffffffu, max(max(lo0 & 0x7fffffffu, hi0 & 0x7fffffffu), max(lo1 & 0x7fffffffu, hi1 & 0x7fffffffu)));
       // 2^up brings the largest element to [2^14, 2^15); non-finite rows stay as they are
@@ -239,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kerne
       // scale log2(e) 2^-up: of the scores
       if (lane == 0) factor[r] = a.scale_log2 * __int_as_float((127 - up / 2) << 23) * __int_as_float((127 - up + up / 2) << 23);
     }
-    __syncthreads();
+    meet();
     float o[NT][D / 16][4];
     // Of a row: the maximum of the scores and that of them with V's scale (powers of
     // two), the sum of the weights, the factor of V's scale in weights, of K's in scores.
@@ -292,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kerne
         }
       }
       // s[n][0], [1]: key g of rows 2 t, 2 t + 1; [2], [3]: key g + 8
-      const int key = (first + i * kWarps) * kSlice;
+      const int key = (first + i * kStride) * kSlice;
       if (key + kSlice - 1 > u.pos0) {  // some row does not see all of them
 #pragma unroll
         for (int n = 0; n < NT; n++)
@@ -378,15 +405,56 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kerne
       }
     }
     copies_wait<0>();
-    // ---- the eight warps' results, joined in order
 #pragma unroll
     for (int n = 0; n < NT; n++)
 #pragma unroll
       for (int c = 0; c < 2; c++)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
-    __syncthreads();  // every warp's ring has been read
     const int rows = u.n_tok * u.gp;
+    const bool part = u.slot >= 0;
+    bool finite = true;
+    if constexpr (SOLO) {
+      // a thread has D / 8 elements in a row of two rows of each group
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          const int r = n * 8 + 2 * t + c;
+          if (r >= rows) continue;
+          const float top = m[n][c] <= kNone ? -CUDART_INF_F : m[n][c], sum = l[n][c];
+          const float back = ex2(mv[n][c] - m[n][c] - kShift), by = part ? back : sum == 0.f ? 0.f : back / sum;
+          float y[D / 8];
+#pragma unroll
+          for (int j = 0; j < D / 16; j++) {
+            y[2 * j] = o[n][j][c] * by;
+            y[2 * j + 1] = o[n][j][2 + c] * by;
+          }
+          const long long at = (long long)(u.row0 + r / u.gp) * a.H + u.head0 + r % u.gp;
+          if (part) {
+#pragma unroll
+            for (int j = 0; j < D / 8; j += 4)
+              a.part_o[((long long)u.slot * S::kRows + r) * (D / 4) + g * (D / 32) + j / 4] = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+            if (g == 0) a.part_ml[(long long)u.slot * S::kRows + r] = make_float2(top, sum);
+          } else {
+            uint32_t z[D / 16];
+#pragma unroll
+            for (int j = 0; j < D / 16; j++) {
+              finite &= fabsf(y[2 * j]) < kBf16Inf && fabsf(y[2 * j + 1]) < kBf16Inf;
+              const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+              z[j] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            uint4 *to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + g * (D / 8));
+#pragma unroll
+            for (int j = 0; j < D / 16; j += 4) to[j / 4] = make_uint4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+            if (g == 0 && a.lse) a.lse[at] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * 0.69314718056f;
+          }
+        }
+      if (!finite && a.flags) atomicOr(a.flags, kFlagNonfinite);
+      continue;
+    }
+    // ---- the eight warps' results, joined in order
+    __syncthreads();  // every warp's ring has been read
     float *place = reinterpret_cast<float *>(sm) + warp * NT * 8 * SM::kRow;
 #pragma unroll
     for (int n = 0; n < NT; n++)
@@ -406,8 +474,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kerne
         }
       }
     __syncthreads();
-    bool finite = true;
-    const bool part = u.slot >= 0;
     for (int item = tid; item < rows * (D / 4); item += kThreads) {
       const int r = item / (D / 4), d4 = item % (D / 4);
       float top = kNone, sum = 0.f;
@@ -425,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kerne
         y.x += fo * z.x; y.y += fo * z.y; y.z += fo * z.z; y.w += fo * z.w;
       }
       if (part) {
-        a.part_o[((long long)u.slot * (D / 4) + d4) * S::kRows + r] = y;
+        a.part_o[MANY ? ((long long)u.slot * S::kRows + r) * (D / 4) + d4 : ((long long)u.slot * (D / 4) + d4) * S::kRows + r] = y;
         if (d4 == 0) a.part_ml[(long long)u.slot * S::kRows + r] = make_float2(top, sum);
       } else {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -441,15 +507,117 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kerne
   }
 }
 
-template <int D, int NT>
+// MANY: there are units enough for thousands of warps.  Where they are short, each is
+// one warp's: 256 sequences over 300 keys, 8 key/value heads, 54.7 us as blocks', 36.7 as
+// warps'; 1000 over 50 keys 104 and 57; but 256 over 1000, 16 heads, 192 and 205, since
+// 2432 warps each somewhere else in its unit read memory in a worse order.
+constexpr int kShort = 6;  // key tiles of a unit, on average
+template <int D, int NT, bool MANY>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kernel(const AttnArgs a) {
+  extern __shared__ __align__(128) unsigned char sm[];
+  AttnStaged *staged = reinterpret_cast<AttnStaged *>(sm);
+  attn_stage<kThreads, Shape8<NT>>(a, staged, blockIdx.x);
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel waits for this one's end
+  __syncthreads();
+  if constexpr (MANY) {
+    // every warp for itself, of the first kStaged sequences
+    uint32_t tiles = 0, seqs = 0;
+    for (int n = threadIdx.x & 31; n < a.n_seqs && n < kStaged; n += 32)
+      if (staged[n].nq > 0) {
+        tiles += (uint32_t)AttnPlan<SoloShape8>::tiles(staged[n].base + staged[n].nq);
+        seqs++;
+      }
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    seqs = __reduce_add_sync(0xffffffffu, seqs);
+    // (without places for partial results there is a warp for each unit)
+    if (!a.jobs || tiles <= kShort * (unsigned long long)seqs) return run<D, NT, true, true>(a, sm);
+  }
+  run<D, NT, false, MANY>(a, sm);
+}
+
+// Joins the pieces of the unit that block or warp blockIdx.x of the plan began and did
+// not end, in their order: a thread has four columns of a row.  There are a few pieces to
+// a unit, and thousands of units.
+constexpr int kMergeThreads = 128;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) gdn_attn8_merge_kernel(const AttnArgs a) {
+  // launched while the attention kernel runs; its results are there after this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const AttnJob job = a.jobs[blockIdx.x];
+  const int n = job.last - (int)blockIdx.x + 1;  // pieces
+  auto slot = [&](int i) { return (long long)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)); };
+  bool finite = true;
+  for (int item = threadIdx.x; item < job.rows * (D / 4); item += kMergeThreads) {
+    const int r = item / (D / 4), d4 = item % (D / 4);
+    float top = -CUDART_INF_F, sum = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      float2 ml[4];
+      float4 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const long long at = slot(i0 + k < n ? i0 + k : i0) * SoloShape8::kRows + r;
+        ml[k] = i0 + k < n ? a.part_ml[at] : make_float2(-CUDART_INF_F, 0.f);
+        x[k] = a.part_o[at * (D / 4) + d4];
+      }
+      float next = top;
+#pragma unroll
+      for (int k = 0; k < 4; k++) next = fmaxf(next, ml[k].x);
+      const float base = next == -CUDART_INF_F ? 0.f : next, down = ex2(top - base);
+      sum *= down;
+      y.x *= down; y.y *= down; y.z *= down; y.w *= down;
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        if (i0 + k < n) {
+          const float f = ex2(ml[k].x - base);
+          sum += f * ml[k].y;
+          y.x += f * x[k].x; y.y += f * x[k].y; y.z += f * x[k].z; y.w += f * x[k].w;
+        }
+      top = next;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
+    finite &= fabsf(y.x) < kBf16Inf && fabsf(y.y) < kBf16Inf && fabsf(y.z) < kBf16Inf && fabsf(y.w) < kBf16Inf;
+    const long long at = (long long)(job.row0 + r / job.gp) * a.H + job.head0 + r % job.gp;
+    __nv_bfloat162 z[2] = {__floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + d4 * 4) = *reinterpret_cast<uint2 *>(z);
+    if (d4 == 0 && a.lse) a.lse[at] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * 0.69314718056f;
+  }
+  if (!finite && a.flags) atomicOr(a.flags, kFlagNonfinite);
+}
+
+template <int D, int NT, bool MANY>
 std::atomic<uint64_t> allowed{0};
 
-template <int D, int NT>
-cudaError_t launch(const AttnArgs &a, int blocks, cudaStream_t stream) {
-  const cudaError_t e = allow_smem(reinterpret_cast<const void *>(&gdn_attn8_kernel<D, NT>), Smem<D, NT>::kBytes, allowed<D, NT>);
+template <int D, int NT, bool MANY>
+cudaError_t launch(const AttnArgs &a, const AttnLaunch &l, cudaStream_t stream) {
+  constexpr int kBytes = Smem<D, NT, MANY>::kBytes;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void *>(&gdn_attn8_kernel<D, NT, MANY>), kBytes, allowed<D, NT, MANY>);
   if (e != cudaSuccess) return e;
-  gdn_attn8_kernel<D, NT><<<blocks, kThreads, Smem<D, NT>::kBytes, stream>>>(a);
-  return cudaGetLastError();
+  const int blocks = MANY ? (l.blocks + kWarps - 1) / kWarps : l.blocks;
+  gdn_attn8_kernel<D, NT, MANY><<<blocks, kThreads, kBytes, stream>>>(a);
+  const cudaError_t k = cudaGetLastError();
+  if (k != cudaSuccess || !l.split || l.blocks < 2) return k;
+  if constexpr (!MANY) return launch_attn8_merge(a, D, l.rows, l.blocks, stream);
+  // may be set up while the attention kernel still runs
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(l.blocks - 1);
+  config.blockDim = dim3(kMergeThreads);
+  config.stream = stream;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, gdn_attn8_merge_kernel<D>, a);
+}
+
+template <int D>
+cudaError_t launch_few(const Attn8Launch &l, cudaStream_t stream) {
+  const AttnLaunch &f = l.few_launch;
+  if (l.groups == 4) return launch<D, 4, false>(l.few, f, stream);
+  if (l.groups == 2) return launch<D, 2, false>(l.few, f, stream);
+  return l.warps ? launch<D, 1, true>(l.few, f, stream) : launch<D, 1, false>(l.few, f, stream);
 }
 
 }  // namespace
@@ -466,9 +634,13 @@ bool attn8_launch(const AttnArgs &a, int d, Attn8Launch &l) {
   l.has_many = most > limit;
   l.groups = a.cu ? limit / 8 : most <= 8 ? 1 : most <= 16 ? 2 : 4;
   l.few_launch = l.many_launch = AttnLaunch{};
+  // Enough units that a warp's equal share is not a small part of one: its pieces are few.
+  const int blocks = blocks_per_sm<2>() * sm_count();
+  l.warps = l.groups == 1 && 4LL * a.n_seqs * a.HKV >= (long long)blocks * kWarps;
   if (l.has_few)
-    l.few_launch = l.groups == 4 ? attn_plan_launch<Shape8<4>>(l.few, blocks_per_sm<4>() * sm_count())
-                                 : attn_plan_launch<Shape8<2>>(l.few, blocks_per_sm<2>() * sm_count());
+    l.few_launch = l.warps ? attn_plan_launch<SoloShape8>(l.few, blocks * kWarps)
+                   : l.groups == 4 ? attn_plan_launch<Shape8<4>>(l.few, blocks_per_sm<4>() * sm_count())
+                                   : attn_plan_launch<Shape8<2>>(l.few, blocks);
   if (l.has_many) l.many_launch = attn_plan_launch<TcShape8>(l.many, sm_count());
   return (!l.has_few || l.few_launch.blocks > 0) && (!l.has_many || l.many_launch.blocks > 0);
 }
@@ -483,15 +655,7 @@ cudaError_t launch_attn8(const Attn8Launch &l, int d, cudaStream_t stream) {
     }
   }
   if (!l.has_few) return cudaSuccess;
-  const AttnArgs &a = l.few;
-  const int blocks = l.few_launch.blocks;
-  cudaError_t e;
-  if (d == 64)
-    e = l.groups == 1 ? launch<64, 1>(a, blocks, stream) : l.groups == 2 ? launch<64, 2>(a, blocks, stream) : launch<64, 4>(a, blocks, stream);
-  else
-    e = l.groups == 1 ? launch<128, 1>(a, blocks, stream) : l.groups == 2 ? launch<128, 2>(a, blocks, stream) : launch<128, 4>(a, blocks, stream);
-  if (e != cudaSuccess || !l.few_launch.split || blocks < 2) return e;
-  return launch_attn8_merge(a, d, l.few_launch.rows, blocks, stream);
+  return d == 64 ? launch_few<64>(l, stream) : launch_few<128>(l, stream);
 }
 
 }  // namespace gdn

@@ -290,6 +290,8 @@ struct Attn8Launch {
   AttnLaunch few_launch, many_launch;
   bool has_few, has_many;  // a call may have such sequences
   int groups;              // of 8 rows, that the kernel for few rows has: 1, 2 or 4
+  bool warps;              // there are so many units of few rows that `blocks` of the plan may be
+                           // warps: a unit is then one warp's where they are short
 };
 bool attn8_launch(const AttnArgs &a, int d, Attn8Launch &l);  // false: more work than the plan can count
 cudaError_t launch_attn8(const Attn8Launch &l, int d, cudaStream_t stream);

@@ -191,6 +191,27 @@ def test_many_units_for_each_block(d):
     check_paged(run(x), x, q_lens, d)
 
 
+@pytest.mark.parametrize("d, H, HKV, T", [(128, 16, 4, 1), (64, 8, 8, 1), (128, 4, 4, 3)])
+@pytest.mark.parametrize("lens", ["short", "one long", "long", "whole"])
+def test_many_short_sequences(d, H, HKV, T, lens):
+    """Thousands of units: short ones (a warp's each), one very long sequence among them (its units
+    in many pieces), longer ones (a block's each), and few enough that none is cut."""
+    n = {"short": 700, "one long": 650, "long": 160, "whole": 320}[lens] * 4 // HKV
+    rng = np.random.RandomState(n)
+    kv = [int(x) for x in {"short": rng.randint(0, 200, n), "one long": rng.randint(1, 100, n), "long": rng.randint(700, 1400, n),
+                           "whole": rng.randint(0, 500, n)}[lens]]
+    if lens == "one long":
+        kv[n // 2] = 9000
+    x = paged([T] * n, kv, H, HKV, d, 32, seed=n + d)
+    x["q"] = x["q"].reshape(n, T, H, d)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run(x, cu_seqlens=None, flags=flags)
+    assert gdn.gdn_read_device_flags(flags) == 0
+    check_paged(got, x, [T] * n, d)
+    again = run(x, cu_seqlens=None)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
 @pytest.mark.parametrize("q_lens", [[1], [64]], ids=str)
 @pytest.mark.parametrize("spread", [0.0, 12.0, 40.0])
 def test_scales_far_apart(q_lens, spread):
