@@ -7,8 +7,9 @@
 // block looks that up for the pairs that it copies, kOwn at a time, while it goes
 // through all pairs once: n^2 / blocks comparisons, 108 for each thread with 4096 pairs.
 //
-// A copy, bound by memory: 16 bytes to a thread, four in flight; a pair is split
-// between blocks while there are fewer pairs than the SMs want.
+// A copy, bound by memory: 16 bytes to a thread, eight in flight (with four, in blocks of
+// 512 threads, 4096 pages of an 8-bit cache took 183 us for 175); a pair is split between
+// blocks while there are fewer pairs than the SMs want.
 #include <stdint.h>
 
 #include "gdn_internal.h"
@@ -16,25 +17,37 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kFlight = 8;
+constexpr int kPiece = 8192;  // bytes of an array's page for a block, at least
 constexpr int kOwn = 32;
 
-__device__ __forceinline__ void copy(char *to, const char *from, long long bytes, int part, int parts) {
-  if (((uintptr_t)to | (uintptr_t)from | (uintptr_t)bytes) & 15) {  // scales of few heads
+// A part of a page of two arrays at once, so that a small part's reads are all on their way.
+__device__ __forceinline__ void copy(char *const (&base)[2], long long bytes, int dst, int src, int part, int parts) {
+  const char *from[2] = {base[0] + src * bytes, base[1] + src * bytes};
+  char *to[2] = {base[0] + dst * bytes, base[1] + dst * bytes};
+  if (((uintptr_t)to[0] | (uintptr_t)from[0] | (uintptr_t)to[1] | (uintptr_t)from[1] | (uintptr_t)bytes) & 15) {  // scales of few heads
     for (long long i = ((long long)part * kThreads + threadIdx.x) * 4; i < bytes; i += (long long)parts * kThreads * 4)
-      *reinterpret_cast<uint32_t *>(to + i) = *reinterpret_cast<const uint32_t *>(from + i);
+#pragma unroll
+      for (int x = 0; x < 2; x++) *reinterpret_cast<uint32_t *>(to[x] + i) = *reinterpret_cast<const uint32_t *>(from[x] + i);
     return;
   }
   const long long step = (long long)parts * kThreads * 16;
-  long long i = ((long long)part * kThreads + threadIdx.x) * 16;
-  for (; i + 3 * step < bytes; i += 4 * step) {
-    uint4 x[4];
+  for (long long i = ((long long)part * kThreads + threadIdx.x) * 16; i < bytes; i += kFlight / 2 * step) {
+    uint4 x[2][kFlight / 2];
 #pragma unroll
-    for (int k = 0; k < 4; k++) x[k] = *reinterpret_cast<const uint4 *>(from + i + k * step);
+    for (int k = 0; k < kFlight / 2; k++)
+      if (i + k * step < bytes) {
+        x[0][k] = *reinterpret_cast<const uint4 *>(from[0] + i + k * step);
+        x[1][k] = *reinterpret_cast<const uint4 *>(from[1] + i + k * step);
+      }
 #pragma unroll
-    for (int k = 0; k < 4; k++) *reinterpret_cast<uint4 *>(to + i + k * step) = x[k];
+    for (int k = 0; k < kFlight / 2; k++)
+      if (i + k * step < bytes) {
+        *reinterpret_cast<uint4 *>(to[0] + i + k * step) = x[0][k];
+        *reinterpret_cast<uint4 *>(to[1] + i + k * step) = x[1][k];
+      }
   }
-  for (; i < bytes; i += step) *reinterpret_cast<uint4 *>(to + i) = *reinterpret_cast<const uint4 *>(from + i);
 }
 
 __global__ void __launch_bounds__(kThreads) gdn_kv_copy_kernel(const CopyPagesArgs a, const int parts) {
@@ -63,9 +76,8 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_copy_kernel(const CopyPagesAr
         continue;
       }
       if (own_src[k] == own_dst[k]) continue;  // nothing to do
-#pragma unroll
-      for (int x = 0; x < 4; x++)
-        if (a.base[x]) copy(a.base[x] + own_dst[k] * a.bytes[x], a.base[x] + own_src[k] * a.bytes[x], a.bytes[x], part, parts);
+      copy({a.base[0], a.base[1]}, a.bytes[0], own_dst[k], own_src[k], part, parts);
+      if (a.base[2]) copy({a.base[2], a.base[3]}, a.bytes[2], own_dst[k], own_src[k], part, parts);
     }
   }
 }
@@ -73,9 +85,9 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_copy_kernel(const CopyPagesAr
 }  // namespace
 
 cudaError_t launch_kv_copy_pages(const CopyPagesArgs &a, cudaStream_t stream) {
-  const long long most = 4LL * sm_count();  // blocks that the GPU holds
+  const long long most = 8LL * sm_count();  // blocks that the GPU holds
   const long long pairs = a.n < most ? a.n : most;
-  const long long pieces = (a.bytes[0] + kThreads * 16 - 1) / (kThreads * 16);
+  const long long pieces = (a.bytes[0] + kPiece - 1) / kPiece;
   long long parts = most / pairs;
   if (parts > pieces) parts = pieces;
   if (parts < 1) parts = 1;

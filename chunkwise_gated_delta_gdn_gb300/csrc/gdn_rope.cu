@@ -22,7 +22,8 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;  // of a block
+constexpr int kMaxTokens = 16;  // of a block
+constexpr int kItemsWanted = 2560;  // of a block: ten for each thread
 
 // f / 2 pi modulo 1, in 2^-64 (less than one of them too small in magnitude), for f
 // finite and below 2^63: the mantissa of f, an integer, times the 128 binary places of
@@ -111,26 +112,59 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_kernel(const RopeArgs a, co
   using P = Piece<T>;
   constexpr int kN = P::kN, kItems = D / (2 * kN);  // of a head
   __shared__ float2 turn[kMaxTokens][D / 2];  // (cos, sin)
-  __shared__ int valid[kMaxTokens];
+  __shared__ int place[kMaxTokens];           // positions
+  __shared__ bool valid[kMaxTokens];
   const int first = blockIdx.x * tokens, here = min(tokens, a.Ttot - first);
-  const int pairs = a.rot / 2;
+  const int pairs = a.rot / 2, heads = a.HQ + a.HK, items = here * heads * kItems;
+  // The two pieces of item i: their first elements, where they are read and written.
+  struct Item {
+    int tok, e0, e1;
+    const T *x;
+    T *y;
+  };
+  auto item = [&](int i) {
+    const int j = i % kItems, row = i / kItems, tok = row / heads, head = row - tok * heads;
+    const bool is_q = head < a.HQ;
+    const long long at = first + tok;
+    Item r;
+    r.tok = tok;
+    r.x = is_q ? static_cast<const T *>(a.q) + at * a.q_stride + head * D
+               : static_cast<const T *>(a.k) + at * a.k_stride + (head - a.HQ) * D;
+    r.y = is_q ? static_cast<T *>(a.qo) + at * a.qo_stride + head * D
+               : static_cast<T *>(a.ko) + at * a.ko_stride + (head - a.HQ) * D;
+    const int turned = pairs / kN;  // items that are turned, where halves are paired
+    if (INTERLEAVED || j >= turned) {
+      r.e0 = INTERLEAVED ? 2 * j * kN : 2 * pairs + 2 * (j - turned) * kN;
+      r.e1 = r.e0 + kN;
+    } else {
+      r.e0 = j * kN;
+      r.e1 = pairs + r.e0;
+    }
+    return r;
+  };
+  // The first item's pieces are on their way while the angles are made.
+  Item next = item(min((int)threadIdx.x, items - 1));
+  uint4 n0 = *reinterpret_cast<const uint4 *>(next.x + next.e0), n1 = *reinterpret_cast<const uint4 *>(next.x + next.e1);
   // A token finds its sequence by halving, and so need not meet a malformed one.
   if (a.cu && a.flags)
     for (long long n = (long long)blockIdx.x * kThreads + threadIdx.x; n < a.n_seqs; n += (long long)gridDim.x * kThreads) {
       const int from = __ldg(a.cu + n), to = __ldg(a.cu + n + 1);
       if (from < 0 || to < from || to > a.Ttot) atomicOr(a.flags, kFlagBadSeqlens);
     }
-  for (int i = threadIdx.x; i < here * pairs; i += kThreads) {
-    const int tok = i / pairs, pair = i - tok * pairs;
-    const uint64_t t = turns_of(__ldg(a.inv_freq + pair));
+  if (threadIdx.x < here) {
     int pos;
-    const bool ok = position(a, first + tok, pos);
-    if (pair == 0) {
-      valid[tok] = ok;
-      if (!ok && a.flags) atomicOr(a.flags, kFlagBadSeqlens);
-    }
+    const bool ok = position(a, first + threadIdx.x, pos);
+    place[threadIdx.x] = pos;
+    valid[threadIdx.x] = ok;
+    if (!ok && a.flags) atomicOr(a.flags, kFlagBadSeqlens);
+  }
+  // A thread has a pair of every few tokens.
+  const int apart = kThreads / pairs, pair = threadIdx.x % pairs, tok0 = threadIdx.x / pairs;
+  const uint64_t t = turns_of(__ldg(a.inv_freq + pair));
+  __syncthreads();
+  for (int tok = tok0; tok < here && tok0 < apart; tok += apart) {
     // the angle in 2^-32 turns: a quarter, and the rest from -1/8 to 1/8
-    const uint32_t angle = (uint32_t)(((uint64_t)(int64_t)pos * t) >> 32);
+    const uint32_t angle = (uint32_t)(((uint64_t)(int64_t)place[tok] * t) >> 32);
     const uint32_t quarter = (angle + 0x20000000u) >> 30;
     float s, c;
     sincospif((float)(int)(angle - (quarter << 30)) * 0x1p-31f, &s, &c);
@@ -139,36 +173,24 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_kernel(const RopeArgs a, co
                                   (quarter & 2 ? -qs : qs) * a.mscale * a.sign);
   }
   __syncthreads();
-  const int heads = a.HQ + a.HK, items = here * heads * kItems;
-#pragma unroll 2
   for (int i = threadIdx.x; i < items; i += kThreads) {
-    const int j = i % kItems, row = i / kItems, tok = row / heads, head = row - tok * heads;
-    if (!valid[tok]) continue;
-    const bool is_q = head < a.HQ;
-    const long long at = first + tok;
-    const T *x = is_q ? static_cast<const T *>(a.q) + at * a.q_stride + head * D
-                      : static_cast<const T *>(a.k) + at * a.k_stride + (head - a.HQ) * D;
-    T *y = is_q ? static_cast<T *>(a.qo) + at * a.qo_stride + head * D
-                : static_cast<T *>(a.ko) + at * a.ko_stride + (head - a.HQ) * D;
-    const int turned = pairs / kN;  // items that are turned, where halves are paired
-    int e0, e1;                     // first elements of the two pieces
-    if (INTERLEAVED || j >= turned) {
-      e0 = INTERLEAVED ? 2 * j * kN : 2 * pairs + 2 * (j - turned) * kN;
-      e1 = e0 + kN;
-    } else {
-      e0 = j * kN;
-      e1 = pairs + e0;
+    const Item r = next;
+    const uint4 w0 = n0, w1 = n1;
+    if (i + kThreads < items) {
+      next = item(i + kThreads);
+      n0 = *reinterpret_cast<const uint4 *>(next.x + next.e0);
+      n1 = *reinterpret_cast<const uint4 *>(next.x + next.e1);
     }
-    const uint4 w0 = *reinterpret_cast<const uint4 *>(x + e0), w1 = *reinterpret_cast<const uint4 *>(x + e1);
+    if (!valid[r.tok]) continue;
     uint4 z0 = w0, z1 = w1;
-    if (e0 < a.rot) {
+    if (r.e0 < a.rot) {
       float u[kN], v[kN], p[kN], q[kN];
       P::get(w0, u);
       P::get(w1, v);
       if constexpr (INTERLEAVED) {
 #pragma unroll
         for (int k = 0; k < kN; k += 2) {
-          const float2 c0 = turn[tok][(e0 + k) / 2], c1 = turn[tok][(e1 + k) / 2];
+          const float2 c0 = turn[r.tok][(r.e0 + k) / 2], c1 = turn[r.tok][(r.e1 + k) / 2];
           p[k] = u[k] * c0.x - u[k + 1] * c0.y;
           p[k + 1] = u[k] * c0.y + u[k + 1] * c0.x;
           q[k] = v[k] * c1.x - v[k + 1] * c1.y;
@@ -177,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_kernel(const RopeArgs a, co
       } else {
 #pragma unroll
         for (int k = 0; k < kN; k++) {
-          const float2 c = turn[tok][e0 + k];
+          const float2 c = turn[r.tok][r.e0 + k];
           p[k] = u[k] * c.x - v[k] * c.y;
           q[k] = u[k] * c.y + v[k] * c.x;
         }
@@ -185,15 +207,19 @@ __global__ void __launch_bounds__(kThreads) gdn_rope_kernel(const RopeArgs a, co
       z0 = P::put(p);
       z1 = P::put(q);
     }
-    *reinterpret_cast<uint4 *>(y + e0) = z0;
-    *reinterpret_cast<uint4 *>(y + e1) = z1;
+    *reinterpret_cast<uint4 *>(r.y + r.e0) = z0;
+    *reinterpret_cast<uint4 *>(r.y + r.e1) = z1;
   }
 }
 
 template <typename T, int D>
 cudaError_t launch(const RopeArgs &a, bool interleaved, cudaStream_t stream) {
-  // several tokens to a block once every SM has enough of them
-  const int tokens = a.Ttot >= 4096 ? kMaxTokens : 1;
+  // several tokens to a block where they have few heads and every SM has blocks enough
+  const int items = (a.HQ + a.HK) * D / (2 * Piece<T>::kN), most = a.Ttot / (4 * sm_count());
+  int tokens = kItemsWanted / items;
+  if (tokens > most) tokens = most;
+  if (tokens > kMaxTokens) tokens = kMaxTokens;
+  if (tokens < 1) tokens = 1;
   const unsigned blocks = (unsigned)((a.Ttot + tokens - 1) / tokens);
   if (interleaved) gdn_rope_kernel<T, D, true><<<blocks, kThreads, 0, stream>>>(a, tokens);
   else gdn_rope_kernel<T, D, false><<<blocks, kThreads, 0, stream>>>(a, tokens);
