@@ -7,6 +7,10 @@ Layers are given as a string, "G" for a gated-delta layer (projection, causal co
 of q and k, recurrence, gated RMS norm) and "A" for an attention layer with grouped heads over a
 paged cache; each adds to its input.  Weights are random.  A gated-delta layer keeps a state of
 fixed size per sequence, an attention layer its keys and values in pages that any sequence may hold.
+
+Attention layers may turn queries and keys by their positions (rot: elements of a head that turn), and
+hold their cache in 8 bits (cache8, bf16 only).  A sequence can fork: two then share the pages
+that are full, and the one that both go on writing is copied.
 """
 from __future__ import annotations
 
@@ -30,14 +34,15 @@ def rms(x):
 
 
 class Stack:
-    def __init__(self, layers="GGAG", dtype=torch.bfloat16, seed=0, device="cuda"):
+    def __init__(self, layers="GGAG", dtype=torch.bfloat16, seed=0, device="cuda", rot=0, cache8=False):
         gen = torch.Generator().manual_seed(seed)
 
         def weight(rows, cols, std=None, dt=dtype):
             w = torch.randn((rows, cols), generator=gen) * (std or rows ** -0.5)
             return w.to(device=device, dtype=dt)
 
-        self.dtype, self.device, self.layers = dtype, device, []
+        self.dtype, self.device, self.layers, self.cache8 = dtype, device, [], cache8
+        self.freq = gdn.rope_inv_freq(rot, device=device) if rot else None
         for kind in layers:
             if kind == "A":
                 p = dict(qkv=weight(WIDTH, (AH + 2 * AHKV) * AD), out=weight(AH * AD, WIDTH))
@@ -57,8 +62,13 @@ class Stack:
         self.cache = []
         for kind, _ in self.layers:
             if kind == "A":
-                pages = torch.zeros((2, n_seqs * per, PAGE, AHKV, AD), dtype=self.dtype, device=dev)
-                self.cache.append((pages[0], pages[1]))
+                dt = torch.uint8 if self.cache8 else self.dtype
+                pages = torch.zeros((2, n_seqs * per, PAGE, AHKV, AD), dtype=dt, device=dev)
+                if self.cache8:
+                    scales = torch.zeros((2, n_seqs * per, PAGE // 16, AHKV), device=dev)
+                    self.cache.append((*pages.view(torch.float8_e4m3fn), *scales))
+                else:
+                    self.cache.append((pages[0], pages[1]))
             else:
                 self.cache.append((torch.zeros((n_seqs, (2 * H + HV) * DK, TAPS - 1), device=dev),
                                    torch.zeros((n_seqs, HV, DK, DK), device=dev)))
@@ -83,16 +93,18 @@ class Stack:
         return gdn.gdn_rmsnorm_gated_fwd(o, p["norm"], z).view(B, T, HV * DK) @ p["out"]
 
     def attention(self, p, x, cache, cu, whole):
-        k_cache, v_cache = cache
         B, T = x.shape[:2]
         # slices of the projection: their tokens lie (AH + 2 AHKV) AD elements apart
         q, k, v = (x @ p["qkv"]).view(B, T, AH + 2 * AHKV, AD).split([AH, AHKV, AHKV], 2)
-        gdn.gdn_kv_cache_append(k, v, k_cache, v_cache, self.table, self.lens, cu_seqlens=cu)
-        if whole:  # nothing was cached before: the keys are the prompt's own
+        if self.freq is not None:  # where they lie
+            gdn.gdn_rope_fwd(q, k, self.freq, kv_lens=self.lens, cu_seqlens=cu, q_out=q, k_out=k)
+        append = gdn.gdn_kv_cache_append_fp8 if self.cache8 else gdn.gdn_kv_cache_append
+        append(k, v, *cache, self.table, self.lens, cu_seqlens=cu)
+        if whole and not self.cache8:  # nothing was cached before: the keys are the prompt's own
             o, _ = gdn.gdn_attn_fwd(q, k, v, cu_seqlens=cu, output_lse=False)
         else:
-            o, _ = gdn.gdn_attn_paged_fwd(q, k_cache, v_cache, self.table, self.lens,
-                                          cu_seqlens=cu, output_lse=False)
+            attend = gdn.gdn_attn_paged_fp8_fwd if self.cache8 else gdn.gdn_attn_paged_fwd
+            o, _ = attend(q, *cache, self.table, self.lens, cu_seqlens=cu, output_lse=False)
         return o.reshape(B, T, AH * AD) @ p["out"]
 
     def run(self, x, cu=None, whole=False):
@@ -103,6 +115,23 @@ class Stack:
             y = rms(x)
             x = x + (self.attention(p, y, cache, cu, whole) if kind == "A" else self.delta(p, y, cache, cu))
         return x
+
+
+    def fork(self, parent, child):
+        """Sequence `child` becomes a copy of `parent` (both indices).  Full pages are shared, the
+        one that `parent` is in the middle of is copied; `child` keeps its own pages for later."""
+        held = int(self.lens[parent])
+        full, rest = held // PAGE, held % PAGE
+        page = self.table[[parent, child], min(full, self.table.shape[1] - 1)]
+        for (kind, _), cache in zip(self.layers, self.cache):
+            if kind != "A":
+                for state in cache:
+                    state[child] = state[parent]
+            elif rest:
+                scales = dict(k_scale=cache[2], v_scale=cache[3]) if self.cache8 else {}
+                gdn.gdn_kv_cache_copy_pages(cache[0], cache[1], page[:1].contiguous(), page[1:].contiguous(), **scales)
+        self.table[child, :full] = self.table[parent, :full]
+        self.lens[child] = held
 
 
 def packed(seqs, device="cuda"):
