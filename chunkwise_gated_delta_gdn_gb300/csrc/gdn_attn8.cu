@@ -625,14 +625,20 @@ cudaError_t launch_few(const Attn8Launch &l, cudaStream_t stream) {
 bool attn8_launch(const AttnArgs &a, int d, Attn8Launch &l) {
   const long long G = a.H / a.HKV, most = (a.cu ? (long long)a.Ttot : (long long)a.T) * G;  // rows of a sequence
   // Up to 32 rows: 64 sequences over 4096 keys, 8 key/value heads of 128, with 20 to 32
-  // rows each take 250 us as many ones, @@ as few.  In a packed call most sequences have
-  // one token, G rows, which the kernel for 16 does faster.
-  const int limit = a.cu && G <= 16 ? 16 : 32;
+  // rows each take 250 us as many ones, 170 to 177 as few.  In a packed call most sequences
+  // have one token, G rows, which the kernel for 16 does faster.
+  // A call of little work, as far as the host knows, is left to the kernel for few rows
+  // altogether, which has longer sequences 16 rows at a time: one kernel's launches, and a
+  // start without tensor maps and tensor memory.  One chunk of 64 tokens over 4000 keys, 32/8
+  // heads (8.2e6 rows times keys times heads) 36.5 us so, 43.7 as many rows; 16 over 30000
+  // (15e6) 53 and 55; 32 over 16000 (16e6) 56 and 45.
+  const bool small = (double)a.Ttot * G * a.max_len * a.HKV <= 1e7;
+  const int limit = small ? INT32_MAX : a.cu && G <= 16 ? 16 : 32;
   l.few = l.many = a;
   l.few.few_rows = l.many.few_rows = limit;
   l.has_few = a.cu ? G <= limit : most <= limit;
   l.has_many = most > limit;
-  l.groups = a.cu ? limit / 8 : most <= 8 ? 1 : most <= 16 ? 2 : 4;
+  l.groups = a.cu ? (G <= 16 ? 2 : 4) : most <= 8 ? 1 : most <= 16 || most > 32 ? 2 : 4;
   l.few_launch = l.many_launch = AttnLaunch{};
   // Enough units that a warp's equal share is not a small part of one: its pieces are few.
   const int blocks = blocks_per_sm<2>() * sm_count();

@@ -73,13 +73,26 @@ def quantised(x, spread, rng):
     return codes, scales, values[:L]
 
 
+@pytest.fixture(params=[0, 1 << 18], ids=["short table", "long table"])
+def room(request):
+    """Positions that a table has room for at least.  A call's kernels are chosen by that: with a short
+    table all of these calls are small, and the kernel for few rows has chunks too."""
+    global _room
+    _room = request.param
+    yield
+    _room = 0
+
+
+_room = 0
+
+
 def paged(q_lens, kv_lens, H, HKV, d, page, seed, spare=3, spread=2.0, q_std=2.0, change=None):
     """A cache whose unheld rows are NaN, unheld blocks' scales too, pages in random order, table
     entries past the last page out of range.  change(which, codes, scales, n): of one sequence."""
     rng = np.random.RandomState(seed)
     N = len(kv_lens)
     held = [-(-n // page) for n in kv_lens]
-    n_pages, width = sum(held) + spare, max(max(held), 1) + 1
+    n_pages, width = sum(held) + spare, max(max(held), 1, _room // page) + 1
     order = rng.permutation(n_pages)
     table = np.full((N, width), 1 << 30, dtype=np.int32)
     x = dict(codes=[], scales=[], values=[])
@@ -142,7 +155,7 @@ def test_decode(d, page, H, HKV):
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("page, H, HKV", [(16, 8, 2), (64, 6, 2), (48, 4, 4), (128, 16, 1), (32, 48, 1)])
-def test_chunks_and_tokens_together(d, page, H, HKV):
+def test_chunks_and_tokens_together(room, d, page, H, HKV):
     """Chunks of odd sizes over odd caches next to single tokens, an empty sequence and sequences
     with fewer keys than new tokens."""
     q_lens = [1, 70, 0, 1, 33, 5, 130, 9, 1, 300]
@@ -153,7 +166,7 @@ def test_chunks_and_tokens_together(d, page, H, HKV):
 
 @pytest.mark.parametrize("B, T, H, HKV, d", [(3, 2, 8, 2, 64), (2, 4, 4, 1, 128), (2, 33, 16, 2, 128), (1, 515, 3, 3, 64),
                                              (3, 6, 8, 2, 128), (2, 32, 2, 2, 64), (2, 17, 2, 1, 128), (2, 1, 64, 2, 64)])
-def test_equal_chunks(B, T, H, HKV, d):
+def test_equal_chunks(room, B, T, H, HKV, d):
     kv = [T + 37 * i + 5 for i in range(B)]
     x = paged([T] * B, kv, H, HKV, d, 32, seed=B + T)
     x["q"] = x["q"].reshape(B, T, H, d)
@@ -169,7 +182,7 @@ def test_equal_chunks(B, T, H, HKV, d):
 
 @pytest.mark.parametrize("nq", [1, 3, 40])
 @pytest.mark.parametrize("d", [64, 128])
-def test_long_cache_is_split_and_joined(nq, d):
+def test_long_cache_is_split_and_joined(room, nq, d):
     x = paged([nq, 1], [9001, 3], 4, 1, d, 64, seed=nq)
     a, b = run(x), run(x)
     check_paged(a, x, [nq, 1], d)
@@ -182,7 +195,7 @@ def test_one_token_over_very_many_keys():
 
 
 @pytest.mark.parametrize("d", [64, 128])
-def test_many_units_for_each_block(d):
+def test_many_units_for_each_block(room, d):
     """Far more sequences and heads than blocks, with one to nine key tiles each."""
     kv = [1 + (i * 397) % 1150 for i in range(90)]
     q_lens = [1 + (i % 3) * (i % 2) for i in range(90)]
@@ -214,7 +227,7 @@ def test_many_short_sequences(d, H, HKV, T, lens):
 
 @pytest.mark.parametrize("q_lens", [[1], [64]], ids=str)
 @pytest.mark.parametrize("spread", [0.0, 12.0, 40.0])
-def test_scales_far_apart(q_lens, spread):
+def test_scales_far_apart(room, q_lens, spread):
     """Blocks of V that differ by up to 2^80 in size: neither the weights' sum nor what a small weight
     of a large block gives may be lost."""
     x = paged(q_lens, [611], 8, 2, 128, 32, seed=3, spread=(1.0, spread))
@@ -222,7 +235,7 @@ def test_scales_far_apart(q_lens, spread):
 
 
 @pytest.mark.parametrize("q_lens", [[1], [64]], ids=str)
-def test_scales_that_are_no_powers_of_two(q_lens):
+def test_scales_that_are_no_powers_of_two(room, q_lens):
     """Any positive scale: a chunk's operands are rounded to bf16 then, 2^-8 of each k and v more."""
     rng = np.random.RandomState(1)
 
@@ -240,7 +253,7 @@ def test_scales_that_are_no_powers_of_two(q_lens):
 
 
 @pytest.mark.parametrize("q_lens", [[1], [50]], ids=str)
-def test_blocks_of_zeros(q_lens):
+def test_blocks_of_zeros(room, q_lens):
     """Whole blocks and a whole sequence of zero values, at the smallest scale: their weights count."""
     def change(which, c, s, n):
         if which:
@@ -258,7 +271,7 @@ def test_blocks_of_zeros(q_lens):
 
 @pytest.mark.parametrize("q_lens", [[1], [50]], ids=str)
 @pytest.mark.parametrize("rise", [4.0, -4.0, 60.0])
-def test_running_maximum(q_lens, rise):
+def test_running_maximum(room, q_lens, rise):
     """Scores that climb (or fall) along the keys, slowly and by hundreds."""
     L, H, d = 700, 2, 128
     x = paged(q_lens, [L], H, H, d, 64, seed=21)
@@ -276,7 +289,7 @@ def test_running_maximum(q_lens, rise):
 
 @pytest.mark.parametrize("std", [1e-30, 1e-6, 1e4, 1e30])
 @pytest.mark.parametrize("q_lens", [[1], [40]], ids=str)
-def test_size_of_queries(q_lens, std):
+def test_size_of_queries(room, q_lens, std):
     """Queries of any size, with a scale that brings the scores back."""
     x = paged(q_lens, [200], 4, 2, 64, 16, seed=4, q_std=std)
     check_paged(run(x, scale=0.3 / std), x, q_lens, 64, scale=float(np.float32(0.3 / std)))
@@ -293,7 +306,7 @@ def test_rows_of_zeros_and_small_elements():
 
 
 @pytest.mark.parametrize("nq", [1, 30])
-def test_malformed_lengths_and_pages_are_flagged(nq):
+def test_malformed_lengths_and_pages_are_flagged(room, nq):
     H, HKV, d, page = 4, 2, 64, 16
     q_lens, kv = [nq] * 3, [40, 40, 40]
     x = paged(q_lens, kv, H, HKV, d, page, seed=9)
@@ -323,7 +336,7 @@ def test_malformed_lengths_and_pages_are_flagged(nq):
 
 
 @pytest.mark.parametrize("nq", [1, 30])
-def test_non_finite_values_are_reported(nq):
+def test_non_finite_values_are_reported(room, nq):
     x = paged([nq, nq], [60, 70], 4, 2, 64, 16, seed=10)
     x["codes"][1][x["table"][0, 0], 3, 1, 7] = 0x7f  # of the first sequence, second head
     flags = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -334,7 +347,7 @@ def test_non_finite_values_are_reported(nq):
 
 
 @pytest.mark.parametrize("nq", [1, 33])
-def test_strided_queries_streams_and_graphs(nq):
+def test_strided_queries_streams_and_graphs(room, nq):
     B, H, HKV, d = 3, 8, 2, 64
     kv = [5000, 77, 900]
     x = paged([nq] * B, kv, H, HKV, d, 16, seed=8)
