@@ -1,6 +1,6 @@
 // gdn_attn8.cu -- attention of few query rows (a decode step) over a paged cache
 // held in 8 bits: e4m3 values with an fp32 scale for each block of 16 tokens and
-// key/value head.
+// key/value head; and the choice of kernels of a call (more rows: gdn_attn_tc.cu).
 //
 //   s_j = scale a_j q.k_j,  m = max_j s_j,  l = sum_j e^(s_j - m),
 //   o = sum_j e^(s_j - m) b_j v_j / l,      lse = m + ln l
@@ -8,23 +8,37 @@
 //
 // A decode step reads each key and value once and has 8 products for each value
 // read, so memory is to be the bound, and what stands between the loads and it is
-// kept small: a unit (a sequence's rows of one key/value head, at most 16) has
+// kept small: a unit (a sequence's rows of one key/value head, at most 16 or 32) has
 // eight warps, each of which takes every eighth block of 16 keys by itself, from
 // copying it (cp.async into a ring of its own) to the weighted sum; nothing
-// synchronises warps until a unit's end.  With the keys as the M and the query rows
-// as the N dimension of mma.sync (m16n8k16), 8 rows cost no more than there are:
+// synchronises warps until a unit's end.  Thousands of short units (kShort) are one
+// warp's each, and nothing is joined but what the plan has cut.  With the keys as the M
+// and the query rows as the N dimension of mma.sync (m16n8k16), 8 rows cost no more
+// than there are:
 //   S^T = K Q^T   (16 keys x 8 rows),  O^T += V^T P^T  (D x 8 rows)
-// The 8-bit values go to fp16, where they are exact, straight into the fragments:
-// which of a key's elements a thread takes for which k is free as long as Q's
-// fragment does the same, so a thread reads 32 bytes of a key in a row; V's keys are
-// paired by byte permutes.  Scales are applied to scores and weights, a scalar each
-// for the 16 keys of a step.  Q is scaled by a power of two for each row into the
-// middle of fp16's range (exact but for elements below 2^-28 of the row's largest).
+// (One 128-row tile of the tcgen05 instructions would be mostly empty, and its way
+// through tensor memory and barriers, 2000 clocks for 128 keys, longer than the 1400 in
+// which memory brings them.)  The 8-bit values go to fp16, where they are exact,
+// straight into the fragments: which of a key's elements a thread takes for which k is
+// free as long as Q's fragment does the same, so a thread reads 32 bytes of a key in a
+// row; V's keys are paired by byte permutes.  Scales are applied to scores and weights,
+// a scalar each for the 16 keys of a step.  Q is scaled by a power of two for each row
+// into the middle of fp16's range (exact but for elements below 2^-28 of the row's
+// largest).
 //
 // Weights are rounded to fp16 for the product with V: e^(s - m) b 2^6 relative to
 // the largest such product so far, moved when it is outgrown by 2^8, so they stay
 // below 2^15 and what is below 2^-30 of the largest one is lost.  The sum l has a
 // maximum of its own (of s alone), in fp32.
+//
+// 256 sequences of up to 4096 keys, 32/8 heads of 128: 194 to 214 us (1.17 GB, 5.5 to
+// 6.1 TB/s; which of these GPUs it was made the difference), 402 over a bf16 cache.
+// Rows of a key lie HKV D bytes apart, and with one head, where they follow one another,
+// memory gives 6% more.  64 sequences over 4096 keys, heads of 64: 62 us (4.3 TB/s): half
+// the bytes for the same instructions, 57% of the issue slots.  One token over 131072
+// keys, 16/2 heads: 25 us, 10 of them loads, the rest start, plan, first loads and joining.
+// Three blocks to an SM, with two stages each, gave 205 for 215 us of the first and 31 for
+// 25.5 of the last; four of four warps 204 for 194 and 31 for 26.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -189,7 +203,7 @@ __device__ __forceinline__ void run(const AttnArgs &a, unsigned char *sm) {
     // The pages of 32 steps, a lane each.
     int page = 0;
     auto look_up = [&](int i) {
-      const int key = min((first + (i + lane) * kStride) * kSlice, u.len - 1);
+      const int key = (first + min(i + lane, steps - 1) * kStride) * kSlice;
       page = __ldg(a.table + (long long)u.seq * a.max_pages + (a.page_log >= 0 ? key >> a.page_log : key / a.page_size));
       if ((unsigned)page >= (unsigned)a.n_pages) {  // reads as zeros
         page = -1;

@@ -8,8 +8,9 @@
 // through all pairs once: n^2 / blocks comparisons, 108 for each thread with 4096 pairs.
 //
 // A copy, bound by memory: 16 bytes to a thread, eight in flight (with four, in blocks of
-// 512 threads, 4096 pages of an 8-bit cache took 183 us for 175); a pair is split between
-// blocks while there are fewer pairs than the SMs want.
+// 512 threads, 4096 pages of an 8-bit cache took 183 us for 177: 6.1 TB/s read and
+// written); a pair is split between blocks while there are fewer pairs than the SMs want.
+// 32 pages of 64 tokens, 8 heads of 128 in bf16: 4.3 us.
 #include <stdint.h>
 
 #include "gdn_internal.h"

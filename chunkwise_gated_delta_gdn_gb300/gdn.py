@@ -10,6 +10,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional, Tuple
@@ -722,6 +723,12 @@ def gdn_attn_paged_fp8_fwd_workspace_bytes(B: int, T: int, H: int, HKV: int, d: 
                                                              max_pages))
 
 
+@functools.lru_cache(maxsize=1024)
+def _fp8_workspace_bytes(device: int, *shape) -> int:
+    """The query's answer for a shape (it depends on nothing else but the device)."""
+    return load().gdn_attn_paged_fp8_fwd_workspace_bytes(*shape)
+
+
 def gdn_attn_paged_fp8_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                            k_scale: torch.Tensor, v_scale: torch.Tensor,
                            block_table: torch.Tensor, kv_lens: torch.Tensor, *,
@@ -763,17 +770,14 @@ def gdn_attn_paged_fp8_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
             v_scale.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), o.data_ptr(),
             _addr(lse), _addr(cu_seqlens), n_seqs, B, T, H, HKV, d, qs, page_size, max_pages,
             n_pages, scale, dt, _addr(flags))
-    raw = torch._C._cuda_getCurrentRawStream(dev.index)
     if workspace is not None:
-        status = lib.gdn_attn_paged_fp8_fwd(*args, workspace.data_ptr(),
-                                            workspace.numel() * workspace.element_size(), raw)
+        nbytes = workspace.numel() * workspace.element_size()
     else:
-        status = lib.gdn_attn_paged_fp8_fwd(*args, None, 0, raw)
-        if status == GDN_ERR_WORKSPACE:
-            nbytes = lib.gdn_attn_paged_fp8_fwd_workspace_bytes(B, T, H, HKV, d, n_seqs, page_size,
-                                                                max_pages)
+        nbytes = _fp8_workspace_bytes(dev.index, B, T, H, HKV, d, n_seqs, page_size, max_pages)
+        if nbytes:
             workspace = _workspace(nbytes, dev)
-            status = lib.gdn_attn_paged_fp8_fwd(*args, workspace.data_ptr(), nbytes, raw)
+    status = lib.gdn_attn_paged_fp8_fwd(*args, _addr(workspace), nbytes,
+                                        torch._C._cuda_getCurrentRawStream(dev.index))
     if status != GDN_OK:
         raise GdnError(status, "gdn_attn_paged_fp8_fwd")
     return o, lse
