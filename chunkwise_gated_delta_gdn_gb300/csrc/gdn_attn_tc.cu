@@ -600,17 +600,18 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             }
             moved = t != first;  // before, there is no output
             break;
-          }
+          } else {
 #pragma unroll 1
-          for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
-            uint32_t o[16];
-            tmem_ld16_nowait(o_at + c, o);
-            tmem_wait_ld();
+            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+              uint32_t o[16];
+              tmem_ld16_nowait(o_at + c, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st16_nowait(o_at + c, o);
+              for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16_nowait(o_at + c, o);
+            }
+            meet_half();
           }
-          meet_half();
         }
         tmem_st32_nowait(p_at, packed);
         if constexpr (FP8) {

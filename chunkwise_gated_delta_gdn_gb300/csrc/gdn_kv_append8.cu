@@ -10,9 +10,10 @@
 //
 // A warp has a block of one head, keys or values: 16 rows, eight elements of a row
 // to a lane.  A copy by its cost: bound by memory, and by launch and three reads in a
-// row (length, page, scale) for a decode step.  32768 tokens of 8 heads of 128: 35 us,
-// 5.7 TB/s read and written (120 us where each row's read was waited for before the
-// next one's); 256 sequences of one token: 4.8 us.
+// row (length, page, scale) for a decode step.  32768 tokens of 8 heads of 128: 31.5 us,
+// 6.4 TB/s read and written (120 us where each row's read was waited for before the
+// next one's; 34.5 with 24 warps to an SM in blocks of eight, 32.8 in blocks of four, so
+// 32 warps); 256 sequences of one token: 4.2 us.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -22,7 +23,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 // all lanes: the last n with at(n) <= x, at non-decreasing and at(0) <= x
 template <class F>
@@ -103,7 +104,7 @@ struct Eight<float> {
 // A block of warps has the heads, keys and values, of a slot (of a block of tokens),
 // several blocks where there are more than kWarps of them.
 template <int D, typename T>
-__global__ void __launch_bounds__(kWarps * 32) gdn_kv_append8_kernel(const Append8Args a, const int per_seq) {
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 8 : 4) gdn_kv_append8_kernel(const Append8Args a, const int per_seq) {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kPasses = kScaleBlock / kAtOnce;
   const int lane = threadIdx.x & 31;
   if (a.cu && a.flags && blockIdx.y == 0)  // a slot finds its sequence, and so need not meet a malformed one
