@@ -757,7 +757,9 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         unit_parity ^= 1;
         wait(bars.q_full(), q_phase, abort);
         q_phase ^= 1;
-        // Q: this warp's 32 rows of each row tile, four at a time, 8 lanes to a row
+        // Q: this warp's 32 rows of each row tile, four at a time, 8 lanes to a row.  Rows of
+        // the next sequence, and of tokens that see no key, do not count for the power.
+        const int blind = uniform(min(max(-u.pos0, 0), u.n_tok) * u.gp);
         for (int r0 = w * 32; r0 < rows; r0 += 128) {
           const uint32_t at = sQ + (r0 >> 7) * SM::kTileBytes + (w * 32 + (lane >> 3)) * 128 + (lane & 7) * 16;
           const int steps = min((rows - r0 + 3) >> 2, 8);
@@ -770,6 +772,8 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
               for (int p = 0; p < kPanels; p++) {
                 const uint4 x = shared_uint4(at + i * 512 + p * kPanel);
                 const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                const int row = r0 + i * 4 + (lane >> 3);
+                if (row < blind || row >= rows) continue;
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
                   const uint32_t lo = in[c] & 0x7fffu, hi = in[c] >> 16 & 0x7fffu;

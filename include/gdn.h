@@ -479,7 +479,8 @@ GDN_API gdn_status gdn_kv_cache_append_fp8(const void *k, const void *v, void *k
  * (dtype BF16; others are GDN_ERR_UNSUPPORTED).  Scales are any positive finite
  * numbers; what others give is not specified.  A non-finite v reaches back as there.
  * Numerics: e4m3 values are exact in the tensor cores' operands (fp16), q too but
- * for elements below 2^-28 of the largest one beside it; scores, maxima, sums and
+ * for elements below 2^-28 of the largest one beside it (in its token's head, or in
+ * 32 neighbouring tokens and heads of its sequence); scores, maxima, sums and
  * the output's accumulation in fp32; the weights, times v's scale, are rounded to fp16 for
  * their product with v, and those below 2^-30 of the largest one count as zero.
  * For sequences with more than 16 new tokens times heads for a key/value head, scales

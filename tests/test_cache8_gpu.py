@@ -305,6 +305,28 @@ def test_rows_of_zeros_and_small_elements():
     check_paged(run(x), x, [3], 128)
 
 
+@pytest.mark.parametrize("H, HKV, q_lens, kv_lens", [
+    (2, 2, [33, 40, 1], [90, 300, 7]),   # the next sequence's rows lie beside the first one's last row
+    (3, 1, [35, 7, 50], [200, 20, 60]),
+    (2, 2, [40, 45], [20, 30]),          # and tokens that see no key before those that see one
+], ids=str)
+def test_other_rows_queries_do_not_matter(room, H, HKV, q_lens, kv_lens):
+    """Queries of another sequence, or of tokens that see no key, of any size: the same bits."""
+    x = paged(q_lens, kv_lens, H, HKV, 64, 16, seed=8)
+    want = run(x)
+    check_paged(want, x, q_lens, 64)
+    at = np.concatenate([[0], np.cumsum(q_lens)])
+    alone = torch.zeros(at[-1], dtype=torch.bool)  # tokens whose outputs are looked at
+    for n in range(0, len(q_lens), 2):
+        alone[at[n] + max(q_lens[n] - kv_lens[n], 0):at[n + 1]] = True
+    for size in (1e30, 1e-30, float("inf"), float("nan")):
+        y = {**x, "q": x["q"].clone()}
+        y["q"][0, ~alone] = (y["q"][0, ~alone].float() * size).to(torch.bfloat16)
+        got = run(y)
+        for a, b, what in zip(got, want, ("o", "lse")):
+            assert torch.equal(a.cpu()[0, alone], b.cpu()[0, alone]), (size, what)
+
+
 @pytest.mark.parametrize("nq", [1, 30])
 def test_malformed_lengths_and_pages_are_flagged(room, nq):
     H, HKV, d, page = 4, 2, 64, 16
