@@ -173,7 +173,8 @@ gdn_status gdn_kv_cache_copy_pages(void *k_cache, void *v_cache, float *k_scale,
   const gdn_status st = check_cache(page_size, 1, n_pages);
   if (st != GDN_OK) return st;
   if (d != 64 && d != 128) return GDN_ERR_UNSUPPORTED;
-  if (HKV > 65535) return GDN_ERR_UNSUPPORTED;
+  // pairs are compared with one another: without a bound a call could take minutes
+  if (HKV > 65535 || n_copies > gdn::kMaxCopies) return GDN_ERR_UNSUPPORTED;
   if (!k_cache || !v_cache || (n_copies > 0 && (!src || !dst))) return GDN_ERR_INVALID_ARG;
   // scales belong to a cache in 8 bits, and to no other
   if ((dtype == GDN_E4M3) != (k_scale != nullptr) || (dtype == GDN_E4M3) != (v_scale != nullptr))

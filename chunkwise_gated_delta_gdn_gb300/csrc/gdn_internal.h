@@ -174,6 +174,7 @@ struct Append8Args {
   int page_size, max_pages, n_pages, max_len;
   uint32_t *flags;
 };
+constexpr int kMaxCopies = 1 << 20;  // of a call
 // Copies pages of a cache (gdn_kv_copy.cu): arrays of `bytes[i]` bytes a page.
 struct CopyPagesArgs {
   char *base[4];       // k, v, and of a cache in 8 bits their scales (or nullptr)

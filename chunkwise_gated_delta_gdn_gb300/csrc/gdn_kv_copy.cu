@@ -4,13 +4,15 @@
 //
 // Every pair reads what was there before the call: a page that is the destination of
 // two pairs, or of one and the source of another, is left as it is, and reported.  A
-// block looks that up for the pairs that it copies, kOwn at a time, while it goes
-// through all pairs once: n^2 / blocks comparisons, 108 for each thread with 4096 pairs.
+// block looks that up for the pairs that it copies, kOwn at a time, in chains by their
+// destinations, while it goes through all pairs once.  So it takes n^2 / kOwn reads in
+// all: 1.8 ms for 131072 pairs, 66 for 2^20, the most of a call (32 pairs compared one by
+// one, without chains: 11 and 649).
 //
 // A copy, bound by memory: 16 bytes to a thread, eight in flight (with four, in blocks of
-// 512 threads, 4096 pages of an 8-bit cache took 183 us for 177: 6.1 TB/s read and
-// written); a pair is split between blocks while there are fewer pairs than the SMs want.
-// 32 pages of 64 tokens, 8 heads of 128 in bf16: 4.3 us.
+// 512 threads, 4096 pages of an 8-bit cache took 6 us more); a pair is split between
+// blocks while there are fewer pairs than the SMs want.  These 4096 pages: 171 us, 6.3
+// TB/s read and written; 32 pages of 64 tokens, 8 heads of 128 in bf16: 4.6 us.
 #include <stdint.h>
 
 #include "gdn_internal.h"
@@ -21,7 +23,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kFlight = 8;
 constexpr int kPiece = 8192;  // bytes of an array's page for a block, at least
-constexpr int kOwn = 32;
+constexpr int kOwn = 128;
+constexpr int kHeads = 256;
 
 // A part of a page of two arrays at once, so that a small part's reads are all on their way.
 __device__ __forceinline__ void copy(char *const (&base)[2], long long bytes, int dst, int src, int part, int parts) {
@@ -53,9 +56,12 @@ __device__ __forceinline__ void copy(char *const (&base)[2], long long bytes, in
 
 __global__ void __launch_bounds__(kThreads) gdn_kv_copy_kernel(const CopyPagesArgs a, const int parts) {
   __shared__ int own_src[kOwn], own_dst[kOwn], bad[kOwn];
+  __shared__ int head[kHeads], behind[kOwn];  // own pairs in chains, by their destination
   const int tid = threadIdx.x, part = blockIdx.x % parts;
   const int step = gridDim.x / parts;  // pairs of all blocks at a time
   for (long long i0 = blockIdx.x / parts; i0 < a.n; i0 += (long long)step * kOwn) {
+    __syncthreads();
+    for (int i = tid; i < kHeads; i += kThreads) head[i] = -1;
     __syncthreads();
     const int mine = (int)min((long long)kOwn, (a.n - i0 + step - 1) / step);
     if (tid < mine) {
@@ -63,12 +69,18 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_copy_kernel(const CopyPagesAr
       own_src[tid] = __ldg(a.src + i);
       own_dst[tid] = __ldg(a.dst + i);
       bad[tid] = (unsigned)own_src[tid] >= (unsigned)a.n_pages || (unsigned)own_dst[tid] >= (unsigned)a.n_pages;
+      behind[tid] = atomicExch(&head[(unsigned)own_dst[tid] % kHeads], tid);
     }
     __syncthreads();
+#pragma unroll 4
     for (int j = tid; j < a.n; j += kThreads) {
       const int s = __ldg(a.src + j), d = __ldg(a.dst + j);
-      for (int k = 0; k < mine; k++)
-        if ((s == own_dst[k] || d == own_dst[k]) && j != i0 + (long long)k * step) bad[k] = 1;
+      auto look = [&](int page) {
+        for (int k = head[(unsigned)page % kHeads]; k >= 0; k = behind[k])
+          if (own_dst[k] == page && j != i0 + (long long)k * step) bad[k] = 1;
+      };
+      look(s);
+      look(d);
     }
     __syncthreads();
     for (int k = 0; k < mine; k++) {

@@ -504,7 +504,8 @@ GDN_API gdn_status gdn_attn_paged_fp8_fwd(const void *q, const void *k_cache, co
 /*
  * gdn_kv_cache_copy_pages -- page src[i] to page dst[i] (int32 [n_copies], device)
  * of both caches, i < n_copies: as a sequence forks (both go on writing to its
- * last page) or a pool is put in order.  dtype F32, BF16 or E4M3; k_scale and
+ * last page) or a pool is put in order; up to 2^20 pairs a call (more are
+ * GDN_ERR_UNSUPPORTED).  dtype F32, BF16 or E4M3; k_scale and
  * v_scale for E4M3 (copied too), NULL for the others.  Every source is read as it
  * was before the call: a page that is the destination of two pairs, or of one and
  * the source of another, is left as it is, and so is one with a page number out of

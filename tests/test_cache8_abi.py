@@ -58,6 +58,7 @@ def test_append_refusals(lib, kw, status):  # noqa: F811
 @pytest.mark.parametrize("kw, status", [
     (dict(n=-1), ARG), (dict(HKV=0), ARG), (dict(d=0), ARG), (dict(dtype=3), ARG), (dict(d=96), UNSUPPORTED),
     (dict(HKV=1 << 16), UNSUPPORTED), (dict(page_size=24), UNSUPPORTED), (dict(page_size=0), ARG), (dict(n_pages=0), ARG),
+    (dict(n=(1 << 20) + 1), UNSUPPORTED), (dict(n=(1 << 31) - 1), UNSUPPORTED),  # each is compared with all
     (dict(k_cache=None), ARG), (dict(v_cache=None), ARG), (dict(src=None), ARG), (dict(dst=None), ARG),
     (dict(k_cache=addr(0, 8)), ARG), (dict(src=addr(2, 2)), ARG), (dict(flags=addr(4, 1)), ARG),
     (dict(dtype=2), ARG),                                       # an 8-bit cache without scales
