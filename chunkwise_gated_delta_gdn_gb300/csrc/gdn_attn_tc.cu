@@ -37,11 +37,11 @@
 //
 // Over a cache in 8 bits (FP8; paged, more than 16 or 32 rows): four warps more turn
 // loaded e4m3 tiles, and a unit's queries, into fp16 in place; see there.  512 tokens over
-// 32768 keys, 32/8 heads: 280 us where keys differ in size (252 where they do not; 225
-// over a bf16 cache), 975 TFLOP/s.  What it costs more: rows that move their maximum, with
-// keys of different sizes in a third of the tiles (40 us); turning tiles (12) and fetching
-// scales (10), as instructions beside the softmax and as reads and writes of shared
-// memory, which the products read at full rate meanwhile.
+// 32768 keys, 32/8 heads: 259 us where keys differ in size (249 where they do not; 225
+// over a bf16 cache), 1.05 PFLOP/s.  What it costs more: turning tiles and fetching
+// scales, as instructions beside the softmax and as reads and writes of shared
+// memory, which the products read at full rate meanwhile; and rows that move their maximum,
+// with keys of different sizes in a third of the tiles.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -767,16 +767,16 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
           bool odd = false;  // something is not finite
           auto look = [&](bool all) {
             top = 0;
+#pragma unroll 1
             for (int i = 0; i < steps; i++)
 #pragma unroll
               for (int p = 0; p < kPanels; p++) {
                 const uint4 x = shared_uint4(at + i * 512 + p * kPanel);
                 const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                const int row = r0 + i * 4 + (lane >> 3);
-                if (row < blind || row >= rows) continue;
+                const uint32_t keep = (unsigned)(r0 + i * 4 + (lane >> 3) - blind) < (unsigned)(rows - blind) ? 0x7fffu : 0u;
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
-                  const uint32_t lo = in[c] & 0x7fffu, hi = in[c] >> 16 & 0x7fffu;
+                  const uint32_t lo = in[c] & keep, hi = in[c] >> 16 & keep;
                   top = max(top, max(all || lo < 0x7f80u ? lo : 0u, all || hi < 0x7f80u ? hi : 0u));
                 }
               }
@@ -788,6 +788,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
           // 2^up brings the largest element to [2^14, 2^15)
           const int up = top == 0 ? 0 : 14 - ((int)(top >> 7) - 127);
           const float f1 = two_to(up / 2), f2 = two_to(up - up / 2);
+#pragma unroll 1
           for (int i = 0; i < steps; i++)
 #pragma unroll
             for (int p = 0; p < kPanels; p++) {
@@ -832,13 +833,15 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             return shared_uint4(raw + row * D + ((D == 128 ? j ^ r : j ^ ((r >> 1) & 3)) << 4));
           };
           auto write = [&](int group, int j, const uint4 &x) {
-            const uint32_t g = f[group >> 1];
+            const uint32_t g = group >> 1 ? f[1] : f[0];
             const uint32_t to = region + group * kGroup + (j >> 2) * 1024 + r * 128;
             const int c0 = (2 * j) & 7;
             store_uint4(to + ((c0 ^ r) << 4), f16_of<false>(x.x, g), f16_of<true>(x.x, g), f16_of<false>(x.y, g), f16_of<true>(x.y, g));
             store_uint4(to + (((c0 + 1) ^ r) << 4), f16_of<false>(x.z, g), f16_of<true>(x.z, g), f16_of<false>(x.w, g), f16_of<true>(x.w, g));
           };
-#pragma unroll
+          // one after the other: unrolled, with more reads on their way at once, these warps were
+          // in the softmax's way (512 tokens over 32768 keys 277 us for 259)
+#pragma unroll 1
           for (int g = 0; g < 4; g++) {
             uint4 x[kPieces / 4];
 #pragma unroll

@@ -599,3 +599,27 @@ def test_copy_pages_that_conflict(n):
     gdn.gdn_kv_cache_copy_pages(kd, vd, perm[:3].cuda(), perm[:3].cuda(), flags=flags)
     gdn.gdn_kv_cache_copy_pages(kd, vd, perm[:0].cuda(), perm[:0].cuda())
     assert gdn.gdn_read_device_flags(flags) == 0 and torch.equal(kd.cpu(), k) and torch.equal(vd.cpu(), v)
+
+
+def test_copy_very_many_pages():
+    """More pairs than blocks have room for at a time, some in conflict."""
+    n, pool = 200000, 400000
+    gen = torch.Generator().manual_seed(1)
+    k, v = (torch.randint(0, 256, (pool, 16, 1, 64), dtype=torch.uint8, generator=gen).cuda() for _ in range(2))
+    ks, vs = (torch.rand((pool, 1, 1), generator=gen).cuda() for _ in range(2))
+    perm = torch.randperm(pool, generator=gen).to(torch.int32)
+    src, dst = perm[:n].clone(), perm[n:].clone()
+    at = torch.randperm(n, generator=gen)[:80]
+    dst[at[:20]] = dst[at[20:40]]  # destinations twice
+    dst[at[40:60]] = src[at[60:]]  # destinations that are sources
+    good = torch.ones(n, dtype=torch.bool)
+    good[at[:60]] = False
+    want = []
+    for a in (k, v, ks, vs):
+        w = a.clone()
+        w[dst[good].long().cuda()] = a[src[good].long().cuda()]
+        want.append(w)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdn.gdn_kv_cache_copy_pages(k.view(E4M3), v.view(E4M3), src.cuda(), dst.cuda(), k_scale=ks, v_scale=vs, flags=flags)
+    assert gdn.gdn_read_device_flags(flags) == gdn.GDN_FLAG_BAD_SEQLENS
+    assert all(torch.equal(a, w) for a, w in zip((k, v, ks, vs), want))
