@@ -544,9 +544,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kerne
     tiles = __reduce_add_sync(0xffffffffu, tiles);
     seqs = __reduce_add_sync(0xffffffffu, seqs);
     // (without places for partial results there is a warp for each unit)
-    if (!a.jobs || tiles <= kShort * (unsigned long long)seqs) return run<D, NT, true, true>(a, sm);
+    if (!a.jobs || tiles <= kShort * (unsigned long long)seqs) run<D, NT, true, true>(a, sm);
+    else run<D, NT, false, true>(a, sm);
+  } else {
+    run<D, NT, false, false>(a, sm);
   }
-  run<D, NT, false, MANY>(a, sm);
+  // Behind the kernel for many rows this one begins as that one's blocks end (2 chunks of
+  // up to 500 tokens among 14 single ones 154 -> 150 us): what follows waits for both.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Joins the pieces of the unit that block or warp blockIdx.x of the plan began and did
@@ -603,16 +608,38 @@ __global__ void __launch_bounds__(kMergeThreads) gdn_attn8_merge_kernel(const At
 template <int D, int NT, bool MANY>
 std::atomic<uint64_t> allowed{0};
 
+// behind: the kernel for many rows has just been launched, on other sequences
 template <int D, int NT, bool MANY>
-cudaError_t launch(const AttnArgs &a, const AttnLaunch &l, cudaStream_t stream) {
+cudaError_t launch(const AttnArgs &a, const AttnLaunch &l, bool behind, cudaStream_t stream) {
   constexpr int kBytes = Smem<D, NT, MANY>::kBytes;
   const cudaError_t e = allow_smem(reinterpret_cast<const void *>(&gdn_attn8_kernel<D, NT, MANY>), kBytes, allowed<D, NT, MANY>);
   if (e != cudaSuccess) return e;
   const int blocks = MANY ? (l.blocks + kWarps - 1) / kWarps : l.blocks;
-  gdn_attn8_kernel<D, NT, MANY><<<blocks, kThreads, kBytes, stream>>>(a);
-  const cudaError_t k = cudaGetLastError();
-  if (k != cudaSuccess || !l.split || l.blocks < 2) return k;
-  if constexpr (!MANY) return launch_attn8_merge(a, D, l.rows, l.blocks, stream);
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(blocks);
+  config.blockDim = dim3(kThreads);
+  config.dynamicSmemBytes = kBytes;
+  config.stream = stream;
+  config.attrs = &early;
+  config.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&config, gdn_attn8_kernel<D, NT, MANY>, a);
+}
+
+template <int D>
+cudaError_t launch_few(const Attn8Launch &l, cudaStream_t stream) {
+  const AttnLaunch &f = l.few_launch;
+  if (l.groups == 4) return launch<D, 4, false>(l.few, f, l.has_many, stream);
+  if (l.groups == 2) return launch<D, 2, false>(l.few, f, l.has_many, stream);
+  return l.warps ? launch<D, 1, true>(l.few, f, l.has_many, stream) : launch<D, 1, false>(l.few, f, l.has_many, stream);
+}
+
+// Joins what a plan has cut.
+cudaError_t join(const AttnArgs &a, int d, const AttnLaunch &l, bool warps, cudaStream_t stream) {
+  if (!l.split || l.blocks < 2) return cudaSuccess;
+  if (!warps) return launch_attn8_merge(a, d, l.rows, l.blocks, stream);
   // may be set up while the attention kernel still runs
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -623,15 +650,7 @@ cudaError_t launch(const AttnArgs &a, const AttnLaunch &l, cudaStream_t stream) 
   config.stream = stream;
   config.attrs = &early;
   config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, gdn_attn8_merge_kernel<D>, a);
-}
-
-template <int D>
-cudaError_t launch_few(const Attn8Launch &l, cudaStream_t stream) {
-  const AttnLaunch &f = l.few_launch;
-  if (l.groups == 4) return launch<D, 4, false>(l.few, f, stream);
-  if (l.groups == 2) return launch<D, 2, false>(l.few, f, stream);
-  return l.warps ? launch<D, 1, true>(l.few, f, stream) : launch<D, 1, false>(l.few, f, stream);
+  return d == 64 ? cudaLaunchKernelEx(&config, gdn_attn8_merge_kernel<64>, a) : cudaLaunchKernelEx(&config, gdn_attn8_merge_kernel<128>, a);
 }
 
 }  // namespace
@@ -666,16 +685,12 @@ bool attn8_launch(const AttnArgs &a, int d, Attn8Launch &l) {
 }
 
 cudaError_t launch_attn8(const Attn8Launch &l, int d, cudaStream_t stream) {
-  if (l.has_many) {
-    const cudaError_t e = launch_attn8_tc(l.many, d, l.many_launch.blocks, stream);
-    if (e != cudaSuccess) return e;
-    if (l.many_launch.split && l.many_launch.blocks > 1) {
-      const cudaError_t m = launch_attn8_merge(l.many, d, l.many_launch.rows, l.many_launch.blocks, stream);
-      if (m != cudaSuccess) return m;
-    }
-  }
-  if (!l.has_few) return cudaSuccess;
-  return d == 64 ? launch_few<64>(l, stream) : launch_few<128>(l, stream);
+  cudaError_t e = cudaSuccess;
+  if (l.has_many) e = launch_attn8_tc(l.many, d, l.many_launch.blocks, stream);
+  if (e == cudaSuccess && l.has_few) e = d == 64 ? launch_few<64>(l, stream) : launch_few<128>(l, stream);
+  if (e == cudaSuccess && l.has_many) e = join(l.many, d, l.many_launch, false, stream);
+  if (e == cudaSuccess && l.has_few) e = join(l.few, d, l.few_launch, l.warps, stream);
+  return e;
 }
 
 }  // namespace gdn
