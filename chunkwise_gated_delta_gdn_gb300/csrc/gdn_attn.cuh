@@ -88,6 +88,9 @@ struct AttnShape {
   static constexpr int kWide = WIDE, kOver = OVER, kNarrow = NARROW, kPackedOver = PACKED_OVER;
   // sequences: all; 1: with at most AttnArgs::few_rows rows for a key/value head; 2: with more
   static constexpr int kOnly = 0;
+  // tiles more than an equal share that a grain may have: they cost less than a second
+  // unit's start and end
+  static constexpr int kSlack = 4;
 };
 // The bf16 kernel's (gdn_attn_tc.cu).  A packed unit's tile takes 3/4 of an
 // unpacked one's: 1/2, 2/3, 3/4 and 1 gave 129, 107, 104 and 109 us for two
@@ -108,6 +111,14 @@ struct FewShape8 : AttnShape<ROWS, ROWS, 128, 2, 4, 2, 4, ROWS, 1, 3> {
 // where a unit is one warp's
 struct SoloShape8 : AttnShape<16, 16, 128, 4, 2, 4, 2, 16, 1, 3> {
   static constexpr int kOnly = 1;
+};
+// where a unit is eight heads', each a warp's: to the plan one head with eight times the rows.
+// Tiles are half as long, since they are eight times as much work for a block (256 sequences
+// of up to 4096 keys 198 us with 128 keys, 194 so); an unequal share costs more than a
+// second piece.
+struct TeamShape8 : AttnShape<64, 64, 64, 2, 2, 2, 2, 64, 1, 3> {
+  static constexpr int kOnly = 1;
+  static constexpr int kSlack = 0;
 };
 struct TcShape8 : TcShape {
   static constexpr int kOnly = 2;
@@ -386,9 +397,6 @@ struct AttnPlan {
   // Returns it for the plan that was chosen.
   template <class F>
   __host__ __device__ AttnCost choose(int n_blocks, F total) {
-    // a grain of up to kSlack tiles more than an equal share costs less than a
-    // second unit's start and end
-    constexpr int kSlack = 4;
     AttnCost weighted = 0, share = 0;
     int log = least - 1;
     stream(1);
@@ -404,7 +412,7 @@ struct AttnPlan {
         log++;
       }
       while (log <= kMaxGrain && (2u << log) < share / S::kWide) log++;  // far too many grains
-      if (log > kMaxGrain || (log > least && (1u << log) > share / S::kNarrow + kSlack)) break;
+      if (log > kMaxGrain || (log > least && (1u << log) > share / S::kNarrow + S::kSlack)) break;
       grains(log);
     }
     stream(share < S::kWide ? S::kWide : share);

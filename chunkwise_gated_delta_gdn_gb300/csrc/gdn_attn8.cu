@@ -11,8 +11,8 @@
 // kept small: a unit (a sequence's rows of one key/value head, at most 16 or 32) has
 // eight warps, each of which takes every eighth block of 16 keys by itself, from
 // copying it (cp.async into a ring of its own) to the weighted sum; nothing
-// synchronises warps until a unit's end.  Thousands of short units (kShort) are one
-// warp's each, and nothing is joined but what the plan has cut.  With the keys as the M
+// synchronises warps until a unit's end.  In larger calls a unit is eight heads', each a
+// warp's, or, where there are thousands of short ones, a warp's (kShort).  With the keys as the M
 // and the query rows as the N dimension of mma.sync (m16n8k16), 8 rows cost no more
 // than there are:
 //   S^T = K Q^T   (16 keys x 8 rows),  O^T += V^T P^T  (D x 8 rows)
@@ -31,10 +31,8 @@
 // below 2^15 and what is below 2^-30 of the largest one is lost.  The sum l has a
 // maximum of its own (of s alone), in fp32.
 //
-// 256 sequences of up to 4096 keys, 32/8 heads of 128: 194 to 214 us (1.17 GB, 5.5 to
-// 6.1 TB/s; which of these GPUs it was made the difference), 402 over a bf16 cache.
-// Rows of a key lie HKV D bytes apart, and with one head, where they follow one another,
-// memory gives 6% more.  64 sequences over 4096 keys, heads of 64: 62 us (4.3 TB/s): half
+// 256 sequences of up to 4096 keys, 32/8 heads of 128: 186 us (1.17 GB, 6.3 TB/s), 402 over
+// a bf16 cache.  64 sequences over 4096 keys, heads of 64: 55 us (4.9 TB/s): half
 // the bytes for the same instructions, 57% of the issue slots.  One token over 131072
 // keys, 16/2 heads: 25 us, 10 of them loads, the rest start, plan, first loads and joining.
 // Three blocks to an SM, with two stages each, gave 205 for 215 us of the first and 31 for
@@ -56,10 +54,12 @@ using namespace sm100;
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kSlice = kScaleBlock;  // keys of a warp's step
-template <int NT, bool SOLO = false>
-using Shape8 = std::conditional_t<SOLO, SoloShape8, FewShape8<NT == 4 ? 32 : 16>>;
-constexpr int kSlices = Shape8<1>::kTile / kSlice;
-static_assert(kSlices == kWarps, "a slice of each tile for each warp");
+// How a unit is shared by a block's warps: each has every eighth slice of its keys, one of
+// its eight heads, or a unit of its own.
+enum Share { kKeys, kHeads, kUnits };
+template <int NT, Share SHARE = kKeys>
+using Shape8 = std::conditional_t<SHARE == kUnits, SoloShape8, std::conditional_t<SHARE == kHeads, TeamShape8, FewShape8<NT == 4 ? 32 : 16>>>;
+static_assert(Shape8<1>::kTile / kSlice == kWarps, "a slice of each tile for each warp");
 // Blocks of an SM: 32 rows take 255 registers of a thread for their output alone.
 template <int NT>
 constexpr int blocks_per_sm() { return NT == 4 ? 1 : 2; }
@@ -67,6 +67,9 @@ constexpr float kLag = 8.f;    // log2 growth of a maximum that is let stand
 constexpr float kNone = -0x1p120f;  // a maximum before any key: finite, so that -inf scores weigh 0
 constexpr float kShift = 6.f;  // log2 of the weights' factor
 
+// How many units there are: few; enough for the GPU's warps; enough for its blocks, eight
+// heads at a time.
+enum Units { kFewUnits, kForWarps, kForBlocks };
 template <int D, int NT, bool MANY = false>
 struct Smem {
   static constexpr int kSliceBytes = 2 * kSlice * D;
@@ -146,13 +149,16 @@ __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_gro
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// NT: groups of 8 rows.  SOLO: a unit is one warp's, all of its keys, so that nothing
+// NT: groups of 8 rows.  SOLO: a row is one warp's, all of its keys, so that nothing
 // but the plan's start is shared by a block's warps.  MANY: partial results lie as
 // gdn_attn8_merge_kernel reads them.  All threads of a block, lengths staged.
-template <int D, int NT, bool SOLO, bool MANY>
+template <int D, int NT, Share SHARE, Units UNITS>
 __device__ __forceinline__ void run(const AttnArgs &a, unsigned char *sm) {
+  constexpr bool MANY = UNITS != kFewUnits;
   using SM = Smem<D, NT, MANY>;
-  using S = Shape8<NT, SOLO>;
+  using S = Shape8<NT, SHARE>;
+  constexpr bool SOLO = SHARE != kKeys;  // a warp has whole rows by itself
+  constexpr int kSlices = S::kTile / kSlice;
   constexpr int kStride = SOLO ? 1 : kWarps;  // steps from one of a warp's to the next
   constexpr int kSteps = D / 16;          // of 16 elements
   constexpr int kWords = D / 16;          // 32-bit words of a key that a thread takes
@@ -163,18 +169,19 @@ __device__ __forceinline__ void run(const AttnArgs &a, unsigned char *sm) {
   [[maybe_unused]] float *join = reinterpret_cast<float *>(sm + SM::kJoin);
   const uint32_t q_at = smem_addr(sm + SM::kQ) + (SOLO ? warp * SM::kQBytes : 0);
   // what the plan deals to: blocks, or warps
-  const int me = SOLO ? blockIdx.x * kWarps + warp : blockIdx.x, all = SOLO ? gridDim.x * kWarps : gridDim.x;
-  const bool speaks = SOLO ? lane == 0 : tid == 0;
+  const int me = SHARE == kUnits ? blockIdx.x * kWarps + warp : blockIdx.x, all = SHARE == kUnits ? gridDim.x * kWarps : gridDim.x;
+  const bool speaks = SHARE == kUnits ? lane == 0 : tid == 0;
   auto meet = [] {
     if constexpr (SOLO) __syncwarp();
     else __syncthreads();
   };
-  AttnPlan<S> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
+  AttnPlan<S> plan(a.H, SHARE == kHeads ? a.HKV / kWarps : a.HKV, a.plan_coarse, a.plan_least);
   const AttnStaged *staged = reinterpret_cast<const AttnStaged *>(sm);  // until the first copies
   const AttnStart st = attn_start(a, plan, staged, me, all);  // each warp for itself
   AttnWalk<S> walk(a, plan, st, me, all);
   if (a.jobs && speaks) a.jobs[me].rows = 0;
-  if (MANY && !SOLO && a.jobs)  // the merge kernel looks at a job for each warp
+  if (MANY && a.jobs && speaks) a.jobs[me].pad[0] = S::kRows;  // the merge kernel goes by it
+  if (UNITS == kForWarps && SHARE != kUnits && a.jobs)  // the merge kernel looks at a job for each warp
     for (int i = all + me * (kWarps - 1) + tid; i < all + (me + 1) * (kWarps - 1); i += kThreads) a.jobs[i].rows = 0;
   __syncthreads();  // what was staged has been read
   const uint64_t once = l2_evict_first();
@@ -195,7 +202,16 @@ __device__ __forceinline__ void run(const AttnArgs &a, unsigned char *sm) {
       if (speaks && a.flags) atomicOr(a.flags, kFlagLaunchConfig);
       continue;
     }
-    if (speaks && u.slot == 2 * me + 1) a.jobs[me] = attn_job(u);
+    if (speaks && u.slot == 2 * me + 1) {
+      AttnJob job = attn_job(u);
+      job.pad[0] = S::kRows;
+      a.jobs[me] = job;
+    }
+    if constexpr (SHARE == kHeads) {  // this warp's
+      u.gp /= kWarps;
+      u.kvh = u.kvh * kWarps + warp;
+      u.head0 += warp * u.gp;
+    }
     meet();  // the previous unit's (or the plan's) shared memory has been read
     const int end = min(u.t1 * S::kTile, max(u.pos0 + u.n_tok, 0));  // behind the last key that anybody sees
     const int first = u.t0 * kSlices + (SOLO ? 0 : warp), n_slices = (end + kSlice - 1) / kSlice;
@@ -446,10 +462,11 @@ __device__ __forceinline__ void run(const AttnArgs &a, unsigned char *sm) {
           }
           const long long at = (long long)(u.row0 + r / u.gp) * a.H + u.head0 + r % u.gp;
           if (part) {
+            const long long to = (long long)u.slot * S::kRows + (SHARE == kHeads ? (r / u.gp * kWarps + warp) * u.gp + r % u.gp : r);
 #pragma unroll
             for (int j = 0; j < D / 8; j += 4)
-              a.part_o[((long long)u.slot * S::kRows + r) * (D / 4) + g * (D / 32) + j / 4] = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-            if (g == 0) a.part_ml[(long long)u.slot * S::kRows + r] = make_float2(top, sum);
+              a.part_o[to * (D / 4) + g * (D / 32) + j / 4] = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+            if (g == 0) a.part_ml[to] = make_float2(top, sum);
           } else {
             uint32_t z[D / 16];
 #pragma unroll
@@ -521,19 +538,26 @@ __device__ __forceinline__ void run(const AttnArgs &a, unsigned char *sm) {
   }
 }
 
-// MANY: there are units enough for thousands of warps.  Where they are short, each is
-// one warp's: 256 sequences over 300 keys, 8 key/value heads, 54.7 us as blocks', 36.7 as
-// warps'; 1000 over 50 keys 104 and 57; but 256 over 1000, 16 heads, 192 and 205, since
-// 2432 warps each somewhere else in its unit read memory in a worse order.
-constexpr int kShort = 6;  // key tiles of a unit, on average
-template <int D, int NT, bool MANY>
+// With units enough a block has eight heads of a sequence at a time, a warp each: its
+// warps read neighbouring 128-byte rows at about the same time, which memory gives faster
+// than rows 1 KB apart, and nothing is joined but what the plan has cut.  256 sequences of
+// up to 4096 keys, 32/8 heads of 128, 215 us as blocks of one head's, 186 so; 64 over 4096
+// keys 105 and 90; 128 over 4096, 32/32 heads, 751 and 632.  (The heads of all sequences one
+// after the other instead, so that blocks read neighbouring rows, gave 212 for 215.)
+// With units for thousands of warps, short ones are a warp's each: 256 sequences over 300
+// keys, 8 key/value heads, 54.7 us as blocks', 34.5 as warps'; 1000 over 50 keys 104 and 57;
+// but 256 over 1000, 16 heads, 192 and 205, since 2432 warps each somewhere else in its unit
+// read memory in a worse order.
+constexpr int kShort = 6;      // key tiles of a unit, on average
+constexpr int kShortTeam = 1;  // where eight heads may be a unit (2000 over 300: 266 us, 231 as teams')
+template <int D, int NT, Units UNITS>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kernel(const AttnArgs a) {
   extern __shared__ __align__(128) unsigned char sm[];
   AttnStaged *staged = reinterpret_cast<AttnStaged *>(sm);
   attn_stage<kThreads, Shape8<NT>>(a, staged, blockIdx.x);
   asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel waits for this one's end
   __syncthreads();
-  if constexpr (MANY) {
+  if constexpr (UNITS != kFewUnits) {
     // every warp for itself, of the first kStaged sequences
     uint32_t tiles = 0, seqs = 0;
     for (int n = threadIdx.x & 31; n < a.n_seqs && n < kStaged; n += 32)
@@ -543,30 +567,38 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) gdn_attn8_kerne
       }
     tiles = __reduce_add_sync(0xffffffffu, tiles);
     seqs = __reduce_add_sync(0xffffffffu, seqs);
-    // (without places for partial results there is a warp for each unit)
-    if (!a.jobs || tiles <= kShort * (unsigned long long)seqs) run<D, NT, true, true>(a, sm);
-    else run<D, NT, false, true>(a, sm);
+    // (without places for partial results there is a warp or block for each unit)
+    if (UNITS == kForWarps && (!a.jobs || tiles <= (a.HKV % kWarps == 0 ? kShortTeam : kShort) * (unsigned long long)seqs)) run<D, NT, kUnits, kForWarps>(a, sm);
+    else if (a.HKV % kWarps == 0 && a.jobs) run<D, NT, kHeads, UNITS>(a, sm);
+    else run<D, NT, kKeys, UNITS>(a, sm);
   } else {
-    run<D, NT, false, false>(a, sm);
+    run<D, NT, kKeys, kFewUnits>(a, sm);
   }
   // Behind the kernel for many rows this one begins as that one's blocks end (2 chunks of
   // up to 500 tokens among 14 single ones 154 -> 150 us): what follows waits for both.
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Joins the pieces of the unit that block or warp blockIdx.x of the plan began and did
-// not end, in their order: a thread has four columns of a row.  There are a few pieces to
-// a unit, and thousands of units.
+// Joins the pieces of a unit that a block or warp of the plan began and did not end, in
+// their order: a thread has four columns of a row.  There are `jobs` of them; eight blocks
+// share one where a unit is eight heads', of which there are `teams` (64 sequences over 4096
+// keys of 8 heads, five pieces each: 98 us in all with a block for each, 90 so).
 constexpr int kMergeThreads = 128;
+static_assert(TeamShape8::kRows <= kWarps * SoloShape8::kRows, "places for warps' units are enough for teams'");
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) gdn_attn8_merge_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kMergeThreads) gdn_attn8_merge_kernel(const AttnArgs a, const int jobs, const int teams) {
   // launched while the attention kernel runs; its results are there after this
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const AttnJob job = a.jobs[blockIdx.x];
-  const int n = job.last - (int)blockIdx.x + 1;  // pieces
-  auto slot = [&](int i) { return (long long)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)); };
+  const int part = blockIdx.x / teams, of_team = blockIdx.x - part * teams;
+  const bool shared = a.jobs[of_team].pad[0] == TeamShape8::kRows;
+  const int first = shared ? of_team : blockIdx.x;  // block or warp of the plan
+  if (first >= jobs) return;
+  const AttnJob job = a.jobs[first];
+  const int row0 = shared ? (job.rows + 7) / 8 * part : 0, rows = shared ? min(job.rows, (job.rows + 7) / 8 * (part + 1)) : job.rows;
+  const int n = job.last - first + 1;  // pieces
+  auto slot = [&](int i) { return (long long)(i == 0 ? 2 * first + 1 : 2 * (first + i)); };
   bool finite = true;
-  for (int item = threadIdx.x; item < job.rows * (D / 4); item += kMergeThreads) {
+  for (int item = row0 * (D / 4) + threadIdx.x; item < rows * (D / 4); item += kMergeThreads) {
     const int r = item / (D / 4), d4 = item % (D / 4);
     float top = -CUDART_INF_F, sum = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -575,7 +607,7 @@ __global__ void __launch_bounds__(kMergeThreads) gdn_attn8_merge_kernel(const At
       float4 x[4];
 #pragma unroll
       for (int k = 0; k < 4; k++) {
-        const long long at = slot(i0 + k < n ? i0 + k : i0) * SoloShape8::kRows + r;
+        const long long at = slot(i0 + k < n ? i0 + k : i0) * job.pad[0] + r;
         ml[k] = i0 + k < n ? a.part_ml[at] : make_float2(-CUDART_INF_F, 0.f);
         x[k] = a.part_o[at * (D / 4) + d4];
       }
@@ -605,52 +637,55 @@ __global__ void __launch_bounds__(kMergeThreads) gdn_attn8_merge_kernel(const At
   if (!finite && a.flags) atomicOr(a.flags, kFlagNonfinite);
 }
 
-template <int D, int NT, bool MANY>
+template <int D, int NT, Units UNITS>
 std::atomic<uint64_t> allowed{0};
 
 // behind: the kernel for many rows has just been launched, on other sequences
-template <int D, int NT, bool MANY>
+template <int D, int NT, Units UNITS>
 cudaError_t launch(const AttnArgs &a, const AttnLaunch &l, bool behind, cudaStream_t stream) {
-  constexpr int kBytes = Smem<D, NT, MANY>::kBytes;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void *>(&gdn_attn8_kernel<D, NT, MANY>), kBytes, allowed<D, NT, MANY>);
+  constexpr int kBytes = Smem<D, NT, UNITS != kFewUnits>::kBytes;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void *>(&gdn_attn8_kernel<D, NT, UNITS>), kBytes, allowed<D, NT, UNITS>);
   if (e != cudaSuccess) return e;
-  const int blocks = MANY ? (l.blocks + kWarps - 1) / kWarps : l.blocks;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t config{};
-  config.gridDim = dim3(blocks);
+  config.gridDim = dim3(UNITS == kForWarps ? (l.blocks + kWarps - 1) / kWarps : l.blocks);
   config.blockDim = dim3(kThreads);
   config.dynamicSmemBytes = kBytes;
   config.stream = stream;
   config.attrs = &early;
   config.numAttrs = behind ? 1 : 0;
-  return cudaLaunchKernelEx(&config, gdn_attn8_kernel<D, NT, MANY>, a);
+  return cudaLaunchKernelEx(&config, gdn_attn8_kernel<D, NT, UNITS>, a);
 }
 
 template <int D>
 cudaError_t launch_few(const Attn8Launch &l, cudaStream_t stream) {
   const AttnLaunch &f = l.few_launch;
-  if (l.groups == 4) return launch<D, 4, false>(l.few, f, l.has_many, stream);
-  if (l.groups == 2) return launch<D, 2, false>(l.few, f, l.has_many, stream);
-  return l.warps ? launch<D, 1, true>(l.few, f, l.has_many, stream) : launch<D, 1, false>(l.few, f, l.has_many, stream);
+  if (l.groups == 4) return launch<D, 4, kFewUnits>(l.few, f, l.has_many, stream);
+  if (l.groups == 2) return launch<D, 2, kFewUnits>(l.few, f, l.has_many, stream);
+  if (l.warps) return launch<D, 1, kForWarps>(l.few, f, l.has_many, stream);
+  return l.teams ? launch<D, 1, kForBlocks>(l.few, f, l.has_many, stream) : launch<D, 1, kFewUnits>(l.few, f, l.has_many, stream);
 }
 
 // Joins what a plan has cut.
-cudaError_t join(const AttnArgs &a, int d, const AttnLaunch &l, bool warps, cudaStream_t stream) {
+// by_rows: partial results lie row by row; warps: the plan deals to warps
+cudaError_t join(const AttnArgs &a, int d, const AttnLaunch &l, bool by_rows, bool warps, cudaStream_t stream) {
   if (!l.split || l.blocks < 2) return cudaSuccess;
-  if (!warps) return launch_attn8_merge(a, d, l.rows, l.blocks, stream);
+  if (!by_rows) return launch_attn8_merge(a, d, l.rows, l.blocks, stream);
   // may be set up while the attention kernel still runs
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t config{};
-  config.gridDim = dim3(l.blocks - 1);
+  const int teams = warps ? l.blocks / kWarps : l.blocks;
+  config.gridDim = dim3(kWarps * teams - 1);
   config.blockDim = dim3(kMergeThreads);
   config.stream = stream;
   config.attrs = &early;
   config.numAttrs = 1;
-  return d == 64 ? cudaLaunchKernelEx(&config, gdn_attn8_merge_kernel<64>, a) : cudaLaunchKernelEx(&config, gdn_attn8_merge_kernel<128>, a);
+  return d == 64 ? cudaLaunchKernelEx(&config, gdn_attn8_merge_kernel<64>, a, l.blocks, teams)
+                 : cudaLaunchKernelEx(&config, gdn_attn8_merge_kernel<128>, a, l.blocks, teams);
 }
 
 }  // namespace
@@ -674,10 +709,16 @@ bool attn8_launch(const AttnArgs &a, int d, Attn8Launch &l) {
   l.groups = a.cu ? (G <= 16 ? 2 : 4) : most <= 8 ? 1 : most <= 16 || most > 32 ? 2 : 4;
   l.few_launch = l.many_launch = AttnLaunch{};
   // Enough units that a warp's equal share is not a small part of one: its pieces are few.
+  // Where eight heads may be a unit, nearly one for each warp (of 2432): 100 sequences over
+  // 1000 keys, 16 key/value heads, 82 us as warps', 71 as teams'; 256 over 300, 8 heads, 34.5
+  // and 39.7.  With fewer than 48 units of eight heads each is in many pieces: 32 sequences
+  // over 4000 keys 47 us as blocks', 50 as teams'; 48 of them 80 and 71.
   const int blocks = blocks_per_sm<2>() * sm_count();
-  l.warps = l.groups == 1 && 4LL * a.n_seqs * a.HKV >= (long long)blocks * kWarps;
+  l.warps = l.groups == 1 && (a.HKV % kWarps == 0 ? 1.25 : 4.) * a.n_seqs * a.HKV >= (double)blocks * kWarps;
+  l.teams = l.groups == 1 && !l.warps && a.HKV % kWarps == 0 && (long long)a.n_seqs * (a.HKV / kWarps) >= 48;
   if (l.has_few)
     l.few_launch = l.warps ? attn_plan_launch<SoloShape8>(l.few, blocks * kWarps)
+                   : l.teams ? attn_plan_launch<TeamShape8>(l.few, blocks)
                    : l.groups == 4 ? attn_plan_launch<Shape8<4>>(l.few, blocks_per_sm<4>() * sm_count())
                                    : attn_plan_launch<Shape8<2>>(l.few, blocks);
   if (l.has_many) l.many_launch = attn_plan_launch<TcShape8>(l.many, sm_count());
@@ -688,8 +729,8 @@ cudaError_t launch_attn8(const Attn8Launch &l, int d, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (l.has_many) e = launch_attn8_tc(l.many, d, l.many_launch.blocks, stream);
   if (e == cudaSuccess && l.has_few) e = d == 64 ? launch_few<64>(l, stream) : launch_few<128>(l, stream);
-  if (e == cudaSuccess && l.has_many) e = join(l.many, d, l.many_launch, false, stream);
-  if (e == cudaSuccess && l.has_few) e = join(l.few, d, l.few_launch, l.warps, stream);
+  if (e == cudaSuccess && l.has_many) e = join(l.many, d, l.many_launch, false, false, stream);
+  if (e == cudaSuccess && l.has_few) e = join(l.few, d, l.few_launch, l.warps || l.teams, l.warps, stream);
   return e;
 }
 

@@ -291,6 +291,7 @@ struct Attn8Launch {
   AttnLaunch few_launch, many_launch;
   bool has_few, has_many;  // a call may have such sequences
   int groups;              // of 8 rows, that the kernel for few rows has: 1, 2 or 4
+  bool teams;              // of few rows, enough units of eight heads for `blocks` of the plan
   bool warps;              // there are so many units of few rows that `blocks` of the plan may be
                            // warps: a unit is then one warp's where they are short
 };

@@ -225,6 +225,46 @@ def test_many_short_sequences(d, H, HKV, T, lens):
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
 
+@pytest.mark.parametrize("d, H, HKV, T, n, page", [
+    (128, 32, 8, 1, 60, 64), (64, 8, 8, 8, 70, 48), (128, 16, 16, 2, 40, 16), (64, 64, 8, 1, 50, 128), (128, 24, 8, 2, 260, 64)])
+def test_eight_heads_at_a_time(d, H, HKV, T, n, page):
+    """Enough units of eight heads: a warp has one of them.  Empty sequences, one much longer than the others,
+    malformed ones and bad pages among them; the same bits again, also on another stream and replayed."""
+    rng = np.random.RandomState(n)
+    kv = [int(x) for x in rng.randint(0, 1500 if n < 100 else 500, n)]
+    kv[3], kv[n // 2], kv[n - 1] = 0, 6000, 1
+    x = paged([T] * n, kv, H, HKV, d, page, seed=n + d)
+    x["q"] = x["q"].reshape(n, T, H, d)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = run(x, cu_seqlens=None, flags=flags)
+    assert gdn.gdn_read_device_flags(flags) == 0
+    check_paged(want, x, [T] * n, d)
+    q, cache = x["q"].cuda(), device(x)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gdn.gdn_attn_paged_fp8_fwd(q, *cache)
+        with torch.cuda.graph(graph, stream=side):
+            o, lse = gdn.gdn_attn_paged_fp8_fwd(q, *cache)
+        for _ in range(2):
+            o.fill_(7), lse.fill_(7)
+            graph.replay()
+            side.synchronize()
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    # one sequence of malformed length, and a page that is none (which reads as zeros)
+    a, b = 5, n // 2 + 1
+    x["lens"][a] = -3
+    x["table"][b, 0] = 1 << 24
+    for values in x["values"]:
+        values[b][:page] = 0
+    o = torch.full_like(want[0], 5.0)
+    got = run(x, cu_seqlens=None, flags=flags, o=o)
+    assert gdn.gdn_read_device_flags(flags) == gdn.GDN_FLAG_BAD_SEQLENS
+    assert (o[a] == 5.0).all()
+    rest = [i for i in range(n) if i != a]
+    check([y[rest] for y in got], x["q"][rest], *([values[i] for i in rest] for values in x["values"]), [T] * len(rest), d ** -0.5)
+
+
 @pytest.mark.parametrize("q_lens", [[1], [64]], ids=str)
 @pytest.mark.parametrize("spread", [0.0, 12.0, 40.0])
 def test_scales_far_apart(room, q_lens, spread):

@@ -38,22 +38,25 @@ static int rnd(int lo, int hi) {
   state = state * 1664525u + 1013904223u;
   return lo + (int)((state >> 8) % (unsigned)(hi - lo + 1));
 }
-static int seen[8];  // calls with few, many, both, a warp each, a block each of many, cut, whole, 32 rows
+static int seen[10];  // calls with few, many, both, a warp each, a block each of many, cut, whole, 32 rows, eight heads' (of enough units for warps, for blocks)
 
 struct Piece { int t0, t1, nt, slot, last, me; };
 using Key = std::tuple<int, int, int>;  // sequence, token row, head
 
 // Every row's pieces, in the order of the blocks.
 template <class S>
-bool walk_all(const AttnArgs &a, int all, const AttnLaunch &l, std::map<Key, std::vector<Piece>> &rows) {
+bool walk_all(const AttnArgs &a, int all, const AttnLaunch &l, std::map<Key, std::vector<Piece>> &rows, int heads_of_unit = 1) {
   std::vector<AttnStaged> staged(kStaged);
   for (int i = 0; i < 7; i++) attn_stage<S>(a, staged.data(), i, 7, true);
   for (int me = 0; me < all; me++) {
-    AttnPlan<S> plan(a.H, a.HKV, a.plan_coarse, a.plan_least);
+    AttnPlan<S> plan(a.H, a.HKV / heads_of_unit, a.plan_coarse, a.plan_least);
     const AttnStart st = attn_start(a, plan, staged.data(), me, all);
     AttnWalk<S> walk(a, plan, st, me, all);
     AttnUnit u;
     while (walk.next(u)) {
+      CHECK(u.slot < 0 || (long long)(u.slot + 1) * S::kRows <= 2LL * l.blocks * l.rows);  // within the workspace
+      // each of its heads a warp's, of at most eight rows
+      CHECK(heads_of_unit == 1 || (u.gp == a.H / a.HKV * heads_of_unit && u.n_tok * u.gp <= 8 * heads_of_unit));
       CHECK(u.t0 < u.t1 && u.t1 <= u.nt && u.n_tok * u.gp <= S::kRows);
       CHECK(u.slot == -1 || (l.split && u.slot < 2 * l.blocks && me < l.blocks));
       CHECK((u.slot == -1) == (u.t0 == 0 && u.t1 == u.nt));
@@ -74,10 +77,15 @@ bool one(const std::vector<int32_t> &q, const std::vector<int32_t> &kv, bool pac
   Attn8Launch l;
   CHECK(attn8_launch(a, d, l));
   std::map<Key, std::vector<Piece>> few, many;
+  int few_tile = 128;
   if (l.has_few) {
     const int grid = l.warps ? (l.few_launch.blocks + kWarps - 1) / kWarps : l.few_launch.blocks;
     bool ok;
-    if (l.warps) {
+    if (l.teams) {
+      seen[l.few_launch.split ? 9 : 4]++;
+      if (l.few_launch.split) few_tile = TeamShape8::kTile;
+      ok = l.few_launch.split ? walk_all<TeamShape8>(l.few, grid, l.few_launch, few, kWarps) : walk_all<Shape8<1>>(l.few, grid, l.few_launch, few);
+    } else if (l.warps) {
       // the device's choice
       unsigned long long tiles = 0, seqs = 0;
       for (size_t i = 0; i < q.size(); i++)
@@ -85,9 +93,12 @@ bool one(const std::vector<int32_t> &q, const std::vector<int32_t> &kv, bool pac
           tiles += AttnPlan<SoloShape8>::tiles((kv[i] > q[i] ? kv[i] - q[i] : 0) + q[i]);
           seqs++;
         }
-      const bool solo = !l.few_launch.split || tiles <= kShort * seqs;
-      seen[solo ? 3 : 4]++;
-      ok = solo ? walk_all<SoloShape8>(l.few, grid * kWarps, l.few_launch, few) : walk_all<Shape8<1>>(l.few, grid, l.few_launch, few);
+      const bool eight = HKV % kWarps == 0, solo = !l.few_launch.split || tiles <= (eight ? kShortTeam : kShort) * seqs;
+      seen[solo ? 3 : eight ? 8 : 4]++;
+      if (!solo && eight) few_tile = TeamShape8::kTile;
+      ok = solo ? walk_all<SoloShape8>(l.few, grid * kWarps, l.few_launch, few)
+           : eight ? walk_all<TeamShape8>(l.few, grid, l.few_launch, few, kWarps)
+                   : walk_all<Shape8<1>>(l.few, grid, l.few_launch, few);
     } else if (l.groups == 4) {
       seen[7]++;
       ok = walk_all<Shape8<4>>(l.few, grid, l.few_launch, few);
@@ -117,7 +128,7 @@ bool one(const std::vector<int32_t> &q, const std::vector<int32_t> &kv, bool pac
           else CHECK(p[i].slot == 2 * p[i].me + (i == 0 ? 1 : 0) && p[i].me == p[0].me + (int)i);
         }
         const int past = kv[n] - q[n], last = (past > 0 ? past : 0) + t + 1;  // keys that the token sees, or tiles count to
-        CHECK(at == p.back().nt && (long long)at * 128 >= last);
+        CHECK(at == p.back().nt && (long long)at * (f ? few_tile : 128) >= last);
         if (p.size() > 1) CHECK(p[0].last == p.back().me);
         seen[p.size() > 1 ? 5 : 6]++;
       }
@@ -147,13 +158,19 @@ int main() {
     }
     if (!one(q, kv, packed, h[0], h[1], kind == 4 ? 20480 : longest + 100, 128)) return 1;
   }
+  // enough units for warps, but long ones, and heads that are no multiple of eight: a block's each
+  for (int n = 160; n < 400; n += 25) {
+    std::vector<int32_t> q(n, 1), kv;
+    for (int s = 0; s < n; s++) kv.push_back(rnd(800, 2500));
+    if (!one(q, kv, false, 8, 4, 20480, 64)) return 1;
+  }
   // short tables: nothing is cut, whatever the number of sequences
   for (int n = 1; n < 900; n += 37) {
     std::vector<int32_t> q(n, 1), kv;
     for (int s = 0; s < n; s++) kv.push_back(rnd(0, 1000));
     if (!one(q, kv, false, 8, 2, 1024, 64)) return 1;
   }
-  for (int k = 0; k < 8; k++)
+  for (int k = 0; k < 10; k++)
     if (seen[k] < 8) { std::printf("kind %d: %d\n", k, seen[k]); return 1; }
   std::printf("ok\n");
   return 0;
