@@ -61,7 +61,8 @@ constexpr int kThreads8 = 768;         // over a cache in 8 bits: four warps mor
 constexpr int kUnits = 4;              // unit ring
 constexpr int kPanel = 128 * 128;      // bytes of 128 rows x 64 bf16
 constexpr float kRescale = 8.f;        // log2 growth of a row maximum that is let stand
-constexpr float kShift8 = 6.f;         // 8 bits: log2 of the weights' factor (fp16, below 2^14)
+constexpr float kShift8 = 6.f;         // 8 bits: log2 of the weights' factor (fp16, below 2^15)
+constexpr float kNone = -0x1p100f;     // 8 bits: a maximum before any visible key; finite
 
 template <int D, bool FP8 = false>
 struct Smem {
@@ -80,12 +81,11 @@ struct Smem {
   static constexpr int kBarCount = (20 + 2 * kUnits + (FP8 ? 3 * kStages + 1 + kScaleSlots : 2 * kStages) + 1) / 2 * 2;
   // tensor memory, abort, [X] stages that the scores free
   static constexpr int kSlot = kBars + kBarCount * 8;
-  // 8 bits: scales of key tiles and of the values that go with them [slot][16], Q's
-  // powers [two units][row tile][32 rows], what a tile's values are relative to [stage]
-  // and [X], and whether a stage has values
-  static constexpr int kScale = kSlot + 16, kUp = kScale + kScaleSlots * 64, kRef = kUp + 64;
-  static constexpr int kKind = kRef + kStages * 4, kTileRef = kKind + kStages * 4;
-  static constexpr int kBytes = FP8 ? kTileRef + 8 : kScale;
+  // 8 bits: scales of key tiles and the log2 of those of the values that go with them
+  // [slot][16], Q's powers [two units][row tile][32 rows], and whether a stage has values
+  static constexpr int kScale = kSlot + 16, kUp = kScale + kScaleSlots * 64;
+  static constexpr int kKind = kUp + 64;
+  static constexpr int kBytes = FP8 ? kKind + kStages * 4 : kScale;
   static_assert(kSlot % 16 == 0, "read at once");
 };
 static_assert(kStaged * sizeof(AttnStaged) + kThreads * sizeof(AttnChunk) <= Smem<128>::kStages * Smem<128>::kTileBytes,
@@ -123,16 +123,14 @@ struct Maps {
 __device__ __forceinline__ void store_uint4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-// two e4m3 values (the low or high half of x) times f, a pair of the same, as two fp16
+// two e4m3 values (the low or high half of x) as two fp16
 template <bool HIGH>
-__device__ __forceinline__ uint32_t f16_of(uint32_t x, uint32_t f) {
+__device__ __forceinline__ uint32_t f16_of(uint32_t x) {
   uint32_t r;
   if constexpr (HIGH)
-    asm("{\n .reg .b16 l, h;\n .reg .b32 p;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 p, h;\n mul.rn.f16x2 %0, p, %2;\n}"
-        : "=r"(r) : "r"(x), "r"(f));
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(x));
   else
-    asm("{\n .reg .b16 l, h;\n .reg .b32 p;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 p, l;\n mul.rn.f16x2 %0, p, %2;\n}"
-        : "=r"(r) : "r"(x), "r"(f));
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -146,9 +144,12 @@ __device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
 }
 // a whole number within 1 of x
 __device__ __forceinline__ float whole(float x) { return __fadd_rn(__fadd_rn(x, 0x1.8p23f), -0x1.8p23f); }
-// exponent of the power of two that is x or the next above it, within -117 .. 120
-__device__ __forceinline__ int ref_exponent(float x) {
-  return min(max((int)((__float_as_uint(x) + 0x7fffffu) >> 23 & 255) - 127, -117), 120);
+// log2 of a scale: exact for powers of two; not below -127 (zero: of a bad page, whose
+// values are zeros)
+__device__ __forceinline__ float scale_log2_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const float part = __uint_as_float((b & 0x7fffffu) | 0x3f800000u);
+  return (float)((int)(b >> 23 & 255) - 127) + (part == 1.f ? 0.f : __log2f(part));
 }
 __device__ __forceinline__ float two_to(int e) { return __int_as_float((127 + e) << 23); }
 __device__ __forceinline__ int shared_int(uint32_t at) {
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
       swap_phase[i] ^= 1;
     };
     AttnUnit u;
-    [[maybe_unused]] int unit_parity = 1;
+    [[maybe_unused]] int unit_parity = 1, tiles_before = 0;  // key tiles of the units before
     while (units.next(u)) {
       if constexpr (FP8) unit_parity ^= 1;
       const int t0 = uniform(u.t0), t1 = uniform(u.t1), rows = uniform(u.n_tok * u.gp);
@@ -451,14 +452,13 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
       const int limit = u.pos0 + min(tok, u.n_tok - 1) - half * 64;  // last visible key, this half's columns
       const int all_see = __reduce_min_sync(0xffffffffu, limit);
       // 8 bits: m is the maximum of log2(weight times V's scale), a whole number, so that
-      // the factor between two of them is exact in fp16.  Scores are 2^-up (K's
-      // scale) S, and weights have V's scale 2^vs in them, which is taken out of l again;
-      // the scales are those that the tile's operands are relative to.
-      float m = -CUDART_INF_F, l = 0.f;
-      [[maybe_unused]] float row_factor = 0.f;
-      // Values below 2^-90 count as that for m: l, which has weights without scales in
-      // units of 2^m, stays below 2^98 for each key.
-      [[maybe_unused]] float xs = sl2, vs = 0.f, vs_top = 0.f, vs_inv = 1.f;
+      // the factor between two of them is exact in fp16.  A score is S times 2^-up and K's
+      // scale of its block of 16 keys; weights have their block's scale of V in them, as a
+      // summand of the exponent.  For l that is taken out again.  l has a maximum of its own,
+      // lam, of the scores alone and of this half of the columns: a common one would be
+      // one more number to exchange for each tile, so the halves' sums meet at the end.
+      float m = FP8 ? kNone : -CUDART_INF_F, l = 0.f;
+      [[maybe_unused]] float row_factor = 0.f, lam = kNone;
       const int first = narrow ? t0 + x : t0;
       const bool mine = first < t1;
       // rows past the unit's last one (most of a decode step's tile): their
@@ -499,11 +499,19 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             const int up = shared_int(smem_addr(sm + SM::kUp) + (unit_parity * 8 + (row >> 5)) * 4);
             row_factor = sl2 * two_to(-(up / 2)) * two_to(up / 2 - up);
           }
-          const int ref = shared_int(smem_addr(sm + SM::kTileRef) + x * 4), k_ref = ref >> 16, v_ref = (short)ref;
-          xs = fmaxf(row_factor * two_to(k_ref), 1e-37f);  // -inf times it stays that
-          vs = (float)v_ref;
-          vs_top = (float)max(v_ref, -90);
-          vs_inv = two_to(-v_ref);
+        }
+        // 8 bits: of this half's four blocks, K's scale times the row's factor and V's
+        // log2; tile_max is that of the scores with V's scale then, own_max without
+        [[maybe_unused]] float xs[4], vs[4], own_max;
+        if constexpr (FP8) {
+          const uint32_t at = smem_addr(sm + SM::kScale) + ((tiles_before + t - t0) & (SM::kScaleSlots - 1)) * 64 + half * 16;
+          const uint4 ks = shared_uint4(at), lb = shared_uint4(at + 32);
+          const uint32_t k4[4] = {ks.x, ks.y, ks.z, ks.w}, v4[4] = {lb.x, lb.y, lb.z, lb.w};
+#pragma unroll
+          for (int b = 0; b < 4; b++) {
+            xs[b] = fmaxf(row_factor * __uint_as_float(k4[b]), 1e-37f);  // -inf times it stays that
+            vs[b] = __uint_as_float(v4[b]);
+          }
         }
         float s[64], tile_max;
         auto load_scores = [&] {
@@ -519,12 +527,27 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             for (int c = 0; c < 64; c++)
               if (c > lim) s[c] = -CUDART_INF_F;
           }
-          float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+          if constexpr (FP8) {
+            float y[4];
 #pragma unroll
-          for (int c = 0; c < 64; c += 8)
+            for (int b = 0; b < 4; b++) {
+              float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-            for (int i = 0; i < 4; i++) top[i] = max3(top[i], s[c + 2 * i], s[c + 2 * i + 1]);
-          tile_max = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+              for (int c = 0; c < 16; c += 4)
+#pragma unroll
+                for (int i = 0; i < 2; i++) top[i] = max3(top[i], s[16 * b + c + 2 * i], s[16 * b + c + 2 * i + 1]);
+              y[b] = fmaxf(top[0], top[1]) * xs[b];
+            }
+            own_max = fmaxf(max3(y[0], y[1], y[2]), y[3]);
+            tile_max = fmaxf(max3(y[0] + vs[0], y[1] + vs[1], y[2] + vs[2]), y[3] + vs[3]);
+          } else {
+            float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+            for (int c = 0; c < 64; c += 8)
+#pragma unroll
+              for (int i = 0; i < 4; i++) top[i] = max3(top[i], s[c + 2 * i], s[c + 2 * i + 1]);
+            tile_max = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+          }
           *own_ex = tile_max;
           fence_before_sync();
           __syncwarp();
@@ -557,30 +580,54 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
           // us).
           float at_hand = m;
           if constexpr (FP8) {
-            const float y = fmaf(tile_max, xs, vs_top);
-            if (y > m + kRescale) at_hand = whole(y);
-          }
-          // nothing visible yet: weights 0
-          const float off = FP8 ? (at_hand == -CUDART_INF_F ? 0.f : at_hand - kShift8) - vs : m == -CUDART_INF_F ? 0.f : m * sl2;
-          const uint64_t scale2 = FP8 ? pair(xs, xs) : pair(sl2, sl2), off2 = pair(-off, -off);
-          sum[0] = sum[1] = 0;
+            if (tile_max > m + kRescale) at_hand = whole(tile_max);
+            const float next = own_max > lam + kRescale ? whole(own_max) : lam;
+            l *= ex2(lam - next);
+            lam = next;
+            // Where a block's values are so much smaller than others' that its weights, with
+            // V's scale, would vanish in 32 bits, they still count for l.  So a weight is
+            // made at least 2^-40 of what it is without V's scale (2^-32 where lam lags):
+            // zero in fp16, as with it.
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            float p0, p1;
-            unpair(fma2(pair(s[c], s[c + 1]), scale2, off2), p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair(p0, p1));
-            packed[c >> 1] = FP8 ? pack_f16(p0, p1) : pack2(p0, p1);
+            for (int b = 0; b < 4; b++) {
+              const float off = fminf(at_hand - kShift8 - vs[b], lam + 40.f);
+              const uint64_t scale2 = pair(xs[b], xs[b]), off2 = pair(-off, -off);
+              uint64_t sums = 0;
+#pragma unroll
+              for (int c = 16 * b; c < 16 * b + 16; c += 2) {
+                float p0, p1;
+                unpair(fma2(pair(s[c], s[c + 1]), scale2, off2), p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                sums = add2(sums, pair(p0, p1));
+                packed[c >> 1] = pack_f16(p0, p1);
+              }
+              float l0, l1;
+              unpair(sums, l0, l1);
+              l = fmaf(l0 + l1, ex2(off - lam), l);
+            }
+          } else {
+            const float off = m == -CUDART_INF_F ? 0.f : m * sl2;  // nothing visible yet: weights 0
+            const uint64_t scale2 = pair(sl2, sl2), off2 = pair(-off, -off);
+            sum[0] = sum[1] = 0;
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              float p0, p1;
+              unpair(fma2(pair(s[c], s[c + 1]), scale2, off2), p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair(p0, p1));
+              packed[c >> 1] = pack2(p0, p1);
+            }
           }
           other_half();
-          float top = FP8 ? fmaf(tile_max, xs, vs_top) : tile_max;
+          float top = tile_max;
           const bool move = top > m + (FP8 ? kRescale : grow);
           if constexpr (FP8) top = whole(top);
           if (__builtin_expect(!__any_sync(0xffffffffu, move), 1)) break;
           f = move ? ex2(FP8 ? m - top : (m - top) * sl2) : 1.f;
           if (move) m = top;
-          l *= f;
+          if constexpr (!FP8) l *= f;
           if constexpr (FP8) {
             // a power of two; below 2^-24 in two steps: weights of up to 2^14 times 2^-38
             // still count
@@ -594,9 +641,6 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
               };
               scale_weights(fmaxf(e, -24.f));
               if (__any_sync(0xffffffffu, e < -24.f)) scale_weights(fminf(e + 24.f, 0.f));
-              const float g = ex2(e);
-              sum[0] = mul2(sum[0], pair(g, g));
-              sum[1] = mul2(sum[1], pair(g, g));
             }
             moved = t != first;  // before, there is no output
             break;
@@ -632,9 +676,11 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             }
           }
         }
-        float l0, l1;
-        unpair(add2(sum[0], sum[1]), l0, l1);
-        l += FP8 ? (l0 + l1) * vs_inv : l0 + l1;
+        if constexpr (!FP8) {
+          float l0, l1;
+          unpair(add2(sum[0], sum[1]), l0, l1);
+          l += l0 + l1;
+        }
         tmem_wait_st();
         fence_before_sync();
         __syncwarp();
@@ -646,7 +692,21 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         o_phase ^= 1;
         fence_after_sync();
       }
-      float m_scaled = FP8 ? m - kShift8 : m * sl2, f_own = 1.f, f_other = 0.f;
+      if constexpr (FP8) {
+        tiles_before += t1 - t0;
+        // l of both halves relative to the larger lam
+        if (mine && !idle) {
+          *own_ex = lam;
+          meet_half();
+          const float top = fmaxf(lam, *other_ex);
+          l *= ex2(lam - top);
+          lam = top;
+          meet_half();  // read, before it is written again
+        }
+      }
+      // m_scaled: log2 of l's unit; `up`: of what the output's unit is more
+      float m_scaled = FP8 ? (lam == kNone ? -CUDART_INF_F : lam) : m * sl2, f_own = 1.f, f_other = 0.f;
+      [[maybe_unused]] const float up = FP8 ? (lam == kNone ? 0.f : m - kShift8 - lam) : 0.f;
       if (both) {
         // Row sums and maxima of both X: the sum of the halves and the maximum
         // in the places of the two halves' tile maxima.  The meeting also says
@@ -669,12 +729,20 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         f_own = ex2(m_scaled - base);
         f_other = ex2(other[128] - base);
         l = f_own * place[0] + f_other * other[0];
+        if constexpr (FP8) {  // and the output's units
+          meet_all(1);  // read, before it is written again
+          if (half == 0 && !idle) place[0] = up;
+          meet_all(0);
+          f_own = ex2(m_scaled - base + up);
+          f_other = ex2(other[128] - base + other[0]);
+        }
         m_scaled = top;
       } else if (mine && !idle) {
         *own_ex = l;
         meet_half();
         l += *other_ex;
         meet_half();  // read, before the next tile's maximum is written
+        if constexpr (FP8) f_own = ex2(up);
       }
       if (mine && !idle) {
         const bool valid = tok < u.n_tok;
@@ -698,6 +766,9 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < kCols; i++) y[i] = f_own * y[i] + f_other * other[i];
+          } else if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < kCols; i++) y[i] *= f_own;
           }
           if (valid && part) {
 #pragma unroll
@@ -733,21 +804,22 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
   } else {
     if (FP8 && warp >= 20) {
       // ------------------------------------------------------ 8 bits to fp16
-      // Operands are fp16 here: an e4m3 value is exact in it, times its block's scale
-      // relative to the tile's largest one (a power of two, down to 2^-24 of it); 32 rows
+      // Operands are fp16 here: an e4m3 value is exact in it, without its scale (the
+      // softmax has those: relative to one for the whole tile, values of small blocks
+      // lost bits beside larger ones, those of later tokens among them); 32 rows
       // of Q are scaled by a power of two into the middle of its range, which leaves a
-      // score's error below 2^-39 of the largest one's products.  (bf16 could hold values
-      // with their scales, but takes six instructions for two values where this takes
-      // two: 512 tokens over 32768 keys 367 us.)
+      // score's error below 2^-39 of the largest one's products.  (bf16 takes more
+      // instructions for two values.)
       // A warp has 32 rows of every tile, and turns them where they lie: they were
       // loaded into the second half of the place that they take as fp16, so eight rows
-      // after the other never overwrite what all lanes have not read.  Lanes 0-7 have 8 rows of one 16-byte piece (16 columns), whose
-      // 16-byte pieces of fp16 lie in different banks.
+      // after the other never overwrite what all lanes have not read.  Lanes 0-7 have 8
+      // rows of one 16-byte piece (16 columns), whose 16-byte pieces of fp16 lie in
+      // different banks.
       constexpr int kRegion = SM::kTileBytes / 4, kPieces = D / 16;
       const int w = warp - 20, r = lane & 7, j0 = lane >> 3;
       Units units{unit_ring, bars, abort, {}};
       Ring<SM::kStages> ring;
-      uint32_t n_keys = 0, n_values = 0;  // tiles so far
+      uint32_t n_keys = 0;  // tiles so far
       uint32_t q_phase = 0;
       int unit_parity = 1;
       AttnUnit u;
@@ -808,36 +880,25 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         for (int i = 0; i < tiles; i++) {
           wait(bars.kv_full(ring.i), ring.round, abort);
           const uint32_t region = sRing + ring.i * SM::kTileBytes + w * kRegion, raw = region + kRegion / 2;
-          const bool values = shared_int(smem_addr(sm + SM::kKind) + ring.i * 4) != 0;
-          const int slot_i = (values ? n_values : n_keys) & (SM::kScaleSlots - 1);
-          const uint32_t scale_at = smem_addr(sm + SM::kScale) + slot_i * 64 + (values ? 32 : 0);
-          if (values) {
-            n_values++;
-          } else {
+          if (w == 0 && shared_int(smem_addr(sm + SM::kKind) + ring.i * 4) == 0) {
+            // keys: their scales, and those of the values that go with them as log2
+            const int slot_i = n_keys & (SM::kScaleSlots - 1);
+            const uint32_t at = smem_addr(sm + SM::kScale) + (slot_i * 16 + (lane & 15)) * 4;
             wait(bars.scales(slot_i), n_keys / SM::kScaleSlots & 1, abort);
             n_keys++;
+            const float b = __int_as_float(shared_int(at));
+            if (lane < 16) store_int(at, __float_as_int(lane < 8 ? b : scale_log2_of(b)));
+            __syncwarp();
           }
-          auto largest = [&](uint32_t at) {
-            const uint4 x = shared_uint4(at), y = shared_uint4(at + 16);
-            return fmaxf(fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)), fmaxf(__uint_as_float(x.z), __uint_as_float(x.w))),
-                         fmaxf(fmaxf(__uint_as_float(y.x), __uint_as_float(y.y)), fmaxf(__uint_as_float(y.z), __uint_as_float(y.w))));
-          };
-          const int ref = ref_exponent(largest(scale_at));
-          if (!values && w == 0 && lane == 0)  // also that of the values that go with it
-            store_int(smem_addr(sm + SM::kRef) + ring.i * 4, (int)((uint32_t)ref << 16) | (ref_exponent(largest(scale_at + 32)) & 0xffff));
-          const uint4 four = shared_uint4(scale_at + (w >> 1) * 16);  // rows 0-15 and 16-31 of this warp's: two of these
-          const float s0 = __uint_as_float(w & 1 ? four.z : four.x) * two_to(-ref), s1 = __uint_as_float(w & 1 ? four.w : four.y) * two_to(-ref);
-          const uint32_t f[2] = {pack_f16(s0, s0), pack_f16(s1, s1)};
           auto read = [&](int group, int j) {
             const int row = group * 8 + r;
             return shared_uint4(raw + row * D + ((D == 128 ? j ^ r : j ^ ((r >> 1) & 3)) << 4));
           };
           auto write = [&](int group, int j, const uint4 &x) {
-            const uint32_t g = group >> 1 ? f[1] : f[0];
             const uint32_t to = region + group * kGroup + (j >> 2) * 1024 + r * 128;
             const int c0 = (2 * j) & 7;
-            store_uint4(to + ((c0 ^ r) << 4), f16_of<false>(x.x, g), f16_of<true>(x.x, g), f16_of<false>(x.y, g), f16_of<true>(x.y, g));
-            store_uint4(to + (((c0 + 1) ^ r) << 4), f16_of<false>(x.z, g), f16_of<true>(x.z, g), f16_of<false>(x.w, g), f16_of<true>(x.w, g));
+            store_uint4(to + ((c0 ^ r) << 4), f16_of<false>(x.x), f16_of<true>(x.x), f16_of<false>(x.y), f16_of<true>(x.y));
+            store_uint4(to + (((c0 + 1) ^ r) << 4), f16_of<false>(x.z), f16_of<true>(x.z), f16_of<false>(x.w), f16_of<true>(x.w));
           };
           // one after the other: unrolled, with more reads on their way at once, these warps were
           // in the softmax's way (512 tokens over 32768 keys 277 us for 259)
@@ -948,9 +1009,9 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
               tma_load_4d(dst + (my_key >> 5) * (SM::kTileBytes / 4) + SM::kTileBytes / 8 + (my_key & 31) * D, map, 0, 0, group,
                           w.kvh, full, w.n_tok * w.gp <= 128 ? once : often);
             // With a key tile come its scales (lanes 0-7) and those of its values (8-15),
-            // which follow in the same order: zero in a bad page and past the last key.  A
-            // slot's values have been turned before its next filling: that is for a key
-            // tile behind at least as many stages.
+            // which follow in the same order: zero in a bad page and past the last key.  The
+            // softmax has read a slot before its next filling: that is for a key tile at least
+            // as many stages behind the values, whose products wait for their weights.
             if (which == 0) {
               const int k1 = min(key + (lane & 7) * kScaleBlock, last), page1 = page_of(max(k1, 0));
               const int from = __shfl_sync(0xffffffffu, pages.page, (page1 - pages.base) & 31);
@@ -1092,7 +1153,6 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
                               kIdS, lane == 0);
         if (lane == 0) {
           mma_commit(bars.s_full(x));
-          if constexpr (FP8) store_int(smem_addr(sm + SM::kTileRef) + x * 4, shared_int(smem_addr(sm + SM::kRef) + k * 4));
           used[x] = k | (free_v + 1) << 8;
           mbar_arrive(bars.s_full(x));
         }

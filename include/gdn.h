@@ -477,15 +477,15 @@ GDN_API gdn_status gdn_kv_cache_append_fp8(const void *k, const void *v, void *k
 /*
  * gdn_attn_paged_fp8_fwd -- gdn_attn_paged_fwd over such a cache; q and o bf16
  * (dtype BF16; others are GDN_ERR_UNSUPPORTED).  Scales are any positive finite
- * numbers; what others give is not specified.  A non-finite v reaches back as there.
+ * numbers; what others give is not specified.  A non-finite v reaches back as there; other
+ * keys and values, and their scales, reach no token that does not see them.
  * Numerics: e4m3 values are exact in the tensor cores' operands (fp16), q too but
  * for elements below 2^-28 of the largest one beside it (in its token's head, or in
- * 32 neighbouring tokens and heads of its sequence); scores, maxima, sums and
- * the output's accumulation in fp32; the weights, times v's scale, are rounded to fp16 for
- * their product with v, and those below 2^-30 of the largest one count as zero.
- * For sequences with more than 16 new tokens times heads for a key/value head, scales
- * are taken relative to the largest among 128 neighbouring keys: one that is no power
- * of two is rounded to 11 bits, one below 2^-24 of that counts as zero.
+ * 32 neighbouring tokens and heads of its sequence).  Scales are applied in fp32, to the
+ * scores and weights of their 16 keys; scores, maxima, sums and the output's accumulation
+ * are fp32.  The weights, times v's scale, are rounded to fp16 for their product
+ * with v, and those below 2^-30 of the largest one count as zero there (not in lse).
+ * Scores are up to 2^21 in magnitude: larger ones may give NaN (GDN_FLAG_NONFINITE).
  * Results are the same from call to call, bit for bit; which of its kernels has a
  * sequence depends on the call's shape (B, T, heads, max_pages) and lengths.
  */
