@@ -400,7 +400,10 @@ __device__ __forceinline__ void run(const AttnArgs &a, unsigned char *sm) {
         float w[4];
 #pragma unroll
         for (int c = 0; c < 2; c++) {
-          const float p0 = ex2(fmaf(s[n][c], fk[n][c], -m[n][c])), p1 = ex2(fmaf(s[n][2 + c], fk[n][c], -m[n][c])), fw = scale.y * ratio[n][c];
+          const float p0 = ex2(fmaf(s[n][c], fk[n][c], -m[n][c])), p1 = ex2(fmaf(s[n][2 + c], fk[n][c], -m[n][c]));
+          // finite: where a row has met zero values alone so far (`ratio` up to 2^123) and large
+          // ones come that it does not see, 0 times this is 0
+          const float fw = fminf(scale.y * ratio[n][c], 0x1p126f);
           l[n][c] += p0 + p1;
           w[c] = p0 * fw;
           w[2 + c] = p1 * fw;

@@ -484,7 +484,8 @@ GDN_API gdn_status gdn_kv_cache_append_fp8(const void *k, const void *v, void *k
  * 32 neighbouring tokens and heads of its sequence).  Scales are applied in fp32, to the
  * scores and weights of their 16 keys; scores, maxima, sums and the output's accumulation
  * are fp32.  The weights, times v's scale, are rounded to fp16 for their product
- * with v, and those below 2^-30 of the largest one count as zero there (not in lse).
+ * with v, and those below 2^-30 of the largest one count as zero there (not in lse);
+ * without v's scale, those below 2^-110 may.
  * Scores are up to 2^21 in magnitude: larger ones may give NaN (GDN_FLAG_NONFINITE).
  * Results are the same from call to call, bit for bit; which of its kernels has a
  * sequence depends on the call's shape (B, T, heads, max_pages) and lengths.

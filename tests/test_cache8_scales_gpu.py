@@ -155,3 +155,30 @@ def test_tiles_of_zero_values_keep_their_weight(room, d, nq, size):  # noqa: F81
 
     x = paged([nq], [900], 4, 2, d, 64, seed=19, spread=0.0, change=change)
     close(run(x), x, [nq], d, whole=nq > 1)
+
+
+@pytest.mark.parametrize("H, HKV, n", [(4, 2, 1), (8, 8, 60), (16, 4, 700)], ids=["blocks", "eight heads", "warps"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq", [1, 2, 8])
+def test_large_values_behind_zeros(d, nq, H, HKV, n):
+    """A token that has seen zero values alone, or nearly so by its weights, beside keys that it does not see (or that weigh
+    nothing) with very large ones: its output is zero (or theirs), not NaN."""
+    nq = min(nq, 8 * HKV // H)
+
+    def change(which, c, s, i):
+        if which:
+            c[:144], s[:9] = 0, 2.0 ** -117
+            s[9:] *= np.float32(2.0 ** 20)
+        elif nq == 1:  # the last keys weigh 2^-250 and less
+            c[:] = 0
+            c[144:], s[9:] = 0xe4, 2.0 ** 4
+        return c, s
+
+    L = [144 + (nq + 1) // 2 + i % 3 % nq for i in range(n)]
+    x = paged([nq] * n, L, H, HKV, d, 16, seed=23, spread=0.0, q_std=0.5, change=change)
+    x["q"] = x["q"].abs().reshape(n, nq, H, d) + 0.5
+    got = run(x, cu_seqlens=None)
+    close(got, x, [nq] * n, d, whole=False)
+    blind = 144 - (np.array(L) - nq)  # a sequence's tokens that see zeros alone
+    for i in range(n):
+        assert (got[0][i, :max(blind[i], 0)] == 0).all()
