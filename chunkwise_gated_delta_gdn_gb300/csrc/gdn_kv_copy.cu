@@ -6,8 +6,9 @@
 // two pairs, or of one and the source of another, is left as it is, and reported.  A
 // block looks that up for the pairs that it copies, kOwn at a time, in chains by their
 // destinations, while it goes through all pairs once.  So it takes n^2 / kOwn reads in
-// all: 1.8 ms for 131072 pairs, 66 for 2^20, the most of a call (32 pairs compared one by
-// one, without chains: 11 and 649).
+// all: 1.7 ms for 131072 pairs, 66 for 2^20, the most of a call, whatever order their pages
+// have (32 pairs compared one by one, without chains: 11 and 649; chains by the last bits
+// of a page's number, destinations in order: 8.4 and 507).
 //
 // A copy, bound by memory: 16 bytes to a thread, eight in flight (with four, in blocks of
 // 512 threads, 4096 pages of an 8-bit cache took 6 us more); a pair is split between
@@ -25,6 +26,16 @@ constexpr int kFlight = 8;
 constexpr int kPiece = 8192;  // bytes of an array's page for a block, at least
 constexpr int kOwn = 128;
 constexpr int kHeads = 256;
+
+// The chain that a page is in.  Pages in order or evenly spaced, as where a pool is put in
+// order, are spread like random ones: a block's own pairs are thousands apart in the list, so by their
+// last bits alone its destinations fell into four chains, or one.
+__host__ __device__ __forceinline__ unsigned chain_of(int page) {
+  uint32_t x = (uint32_t)page * 0x9e3779b1u;
+  x = (x ^ x >> 15) * 0x85ebca77u;
+  return x >> 24;
+}
+static_assert(kHeads == 256, "chain_of()");
 
 // A part of a page of two arrays at once, so that a small part's reads are all on their way.
 __device__ __forceinline__ void copy(char *const (&base)[2], long long bytes, int dst, int src, int part, int parts) {
@@ -69,14 +80,14 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_copy_kernel(const CopyPagesAr
       own_src[tid] = __ldg(a.src + i);
       own_dst[tid] = __ldg(a.dst + i);
       bad[tid] = (unsigned)own_src[tid] >= (unsigned)a.n_pages || (unsigned)own_dst[tid] >= (unsigned)a.n_pages;
-      behind[tid] = atomicExch(&head[(unsigned)own_dst[tid] % kHeads], tid);
+      behind[tid] = atomicExch(&head[chain_of(own_dst[tid])], tid);
     }
     __syncthreads();
 #pragma unroll 4
     for (int j = tid; j < a.n; j += kThreads) {
       const int s = __ldg(a.src + j), d = __ldg(a.dst + j);
       auto look = [&](int page) {
-        for (int k = head[(unsigned)page % kHeads]; k >= 0; k = behind[k])
+        for (int k = head[chain_of(page)]; k >= 0; k = behind[k])
           if (own_dst[k] == page && j != i0 + (long long)k * step) bad[k] = 1;
       };
       look(s);
