@@ -170,6 +170,16 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _stream(dev, stream: Optional[torch.cuda.Stream]) -> torch.cuda.Stream:
+    """The stream of a call: the one given, or the current one of the tensors' device, which has to
+    be a GPU (the library would take addresses of host memory as they are)."""
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, not {dev}")
+    return stream
+
+
 def _call(entry: str, q, k, v, g, beta, h0, scale, chunk, cu_seqlens, o, hT,
           output_final_state, workspace, stream):
     lib = load()
@@ -206,8 +216,7 @@ def _call(entry: str, q, k, v, g, beta, h0, scale, chunk, cu_seqlens, o, hT,
     nbytes = gdn_chunk_fwd_workspace_bytes(B, T, H, HV, dk, dv, chunk, gate_mode, n_seqs, dt)
     if workspace is None:
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    stream = _stream(dev, stream)
     status = getattr(lib, entry)(
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(o), _ptr(hT),
         _ptr(cu_seqlens), n_seqs, B, T, H, HV, dk, dv, int(chunk), float(scale),
@@ -317,8 +326,7 @@ def gdn_recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torc
         o = torch.empty((B, T, HV, dv), dtype=q.dtype, device=dev)
     if hT is None and output_final_state:
         hT = torch.empty((n_seqs, HV, dk, dv), dtype=torch.float32, device=dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    stream = _stream(dev, stream)
     status = lib.gdn_recurrent_fwd(
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(o), _ptr(hT),
         _ptr(cu_seqlens), n_seqs, B, T, H, HV, dk, dv, float(scale), gate_mode, dt,
@@ -362,8 +370,7 @@ def gdn_causal_conv1d_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch
         y = torch.empty_like(x)
     if hT is None and output_final_state:
         hT = torch.empty((n_seqs, D, W - 1), dtype=torch.float32, device=dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    stream = _stream(dev, stream)
     status = lib.gdn_causal_conv1d_fwd(
         _ptr(x), _ptr(w), _ptr(bias), _ptr(h0), _ptr(y), _ptr(hT), _ptr(cu_seqlens), n_seqs, B,
         T, D, W, int(activation), _dtype_code(x.dtype), _ptr(flags),
@@ -381,8 +388,7 @@ def gdn_l2norm_fwd(x: torch.Tensor, *, eps: float = 1e-6, y: Optional[torch.Tens
     _check(y, "y", x.device)
     if y is None:
         y = torch.empty_like(x)
-    if stream is None:
-        stream = torch.cuda.current_stream(x.device)
+    stream = _stream(x.device, stream)
     dim = x.shape[-1]
     status = lib.gdn_l2norm_fwd(_ptr(x), _ptr(y), x.numel() // max(dim, 1), dim, float(eps),
                                 _dtype_code(x.dtype), ctypes.c_void_p(stream.cuda_stream))
@@ -405,8 +411,7 @@ def gdn_rmsnorm_gated_fwd(x: torch.Tensor, weight: torch.Tensor, z: Optional[tor
         raise ValueError("z must match x in shape and dtype")
     if y is None:
         y = torch.empty_like(x)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    stream = _stream(dev, stream)
     dim = x.shape[-1]
     status = lib.gdn_rmsnorm_gated_fwd(_ptr(x), _ptr(z), _ptr(weight), _ptr(y),
                                        x.numel() // max(dim, 1), dim, float(eps),
@@ -432,8 +437,7 @@ def gdn_state_combine(M: torch.Tensor, S_in: torch.Tensor, S_seg: torch.Tensor, 
         raise ValueError("M [N, HV, dk, dk] and S_seg [N, HV, dk, dv] must match S_in")
     if out is None:
         out = torch.empty_like(S_seg)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    stream = _stream(dev, stream)
     status = lib.gdn_state_combine(_ptr(M), _ptr(S_in), _ptr(S_seg), _ptr(out), N, HV, dk, dv,
                                    ctypes.c_void_p(stream.cuda_stream))
     if status != GDN_OK:
@@ -656,7 +660,8 @@ def gdn_kv_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
                                            dtype, dev)
     if flags is not None:
         _given(k, None, None, flags, None, dev)
-    raw = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream)
+    raw = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
+           else _stream(dev, stream).cuda_stream)
     status = lib.gdn_kv_cache_append(
         k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
         kv_lens.data_ptr(), _addr(cu_seqlens), n_seqs, B, T, HKV, d, ks, vs, page_size, max_pages,
@@ -708,7 +713,8 @@ def gdn_kv_cache_append_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Ten
     _scales(k_scale, v_scale, k_cache, dev)
     if flags is not None:
         _given(k, None, None, flags, None, dev)
-    raw = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream)
+    raw = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
+           else _stream(dev, stream).cuda_stream)
     status = lib.gdn_kv_cache_append_fp8(
         k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
         v_scale.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), _addr(cu_seqlens), n_seqs,
@@ -811,7 +817,8 @@ def gdn_kv_cache_copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, src: t
         _scales(k_scale, v_scale, k_cache, dev)
     if flags is not None:
         _given(k_cache, None, None, flags, None, dev)
-    raw = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream)
+    raw = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
+           else _stream(dev, stream).cuda_stream)
     n_pages, page_size, HKV, d = shape
     status = lib.gdn_kv_cache_copy_pages(
         k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), src.data_ptr(),
@@ -939,8 +946,7 @@ def gdn_selftest_wait(flags: torch.Tensor, budget_cycles: int, complete: bool, *
     _check(flags, "flags", flags.device)
     if flags.dtype != torch.int32 or flags.numel() < 1:
         raise TypeError("flags must be an int32 tensor of at least one element")
-    if stream is None:
-        stream = torch.cuda.current_stream(flags.device)
+    stream = _stream(flags.device, stream)
     status = lib.gdn_selftest_wait(_ptr(flags), int(budget_cycles), int(bool(complete)),
                                    ctypes.c_void_p(stream.cuda_stream))
     if status != GDN_OK:
@@ -952,8 +958,7 @@ def gdn_read_device_flags(workspace: torch.Tensor,
     """Status word (GDN_FLAG_*) of the last call that used ``workspace`` (or,
     for gdn_recurrent_fwd, the ``flags`` tensor)."""
     lib = load()
-    if stream is None:
-        stream = torch.cuda.current_stream(workspace.device)
+    stream = _stream(workspace.device, stream)
     out = ctypes.c_uint32(0)
     status = lib.gdn_read_device_flags(_ptr(workspace), ctypes.byref(out),
                                        ctypes.c_void_p(stream.cuda_stream))
