@@ -57,7 +57,8 @@ class Stack:
         """An empty cache for each layer, and the pages that the sequences hold: here each
         sequence's are given to it at once, in no order."""
         dev, per = self.device, -(-max_len // PAGE)
-        self.table = torch.randperm(n_seqs * per).to(torch.int32).view(n_seqs, per).to(dev)
+        self.own = torch.randperm(n_seqs * per).to(torch.int32).view(n_seqs, per).to(dev)
+        self.table = self.own.clone()
         self.lens = torch.zeros(n_seqs, dtype=torch.int32, device=dev)
         self.cache = []
         for kind, _ in self.layers:
@@ -116,10 +117,14 @@ class Stack:
             x = x + (self.attention(p, y, cache, cu, whole) if kind == "A" else self.delta(p, y, cache, cu))
         return x
 
-
     def fork(self, parent, child):
         """Sequence `child` becomes a copy of `parent` (both indices).  Full pages are shared, the
-        one that `parent` is in the middle of is copied; `child` keeps its own pages for later."""
+        one that `parent` is in the middle of is copied; `child` goes on in its own pages, which no
+        other sequence may share by then."""
+        others = torch.cat([self.table[:child], self.table[child + 1:]])
+        if parent == child or torch.isin(self.own[child], others).any():
+            raise ValueError(f"sequence {child} has pages that are still shared")
+        self.table[child] = self.own[child]
         held = int(self.lens[parent])
         full, rest = held // PAGE, held % PAGE
         page = self.table[[parent, child], min(full, self.table.shape[1] - 1)]
