@@ -6,9 +6,12 @@
 // a head is copied.  Backward: the same with -sin (the transpose).
 //
 // A far position's angle has to be exact modulo a turn: p f in fp32 is off by 2^-7 at
-// 131072.  So f / 2 pi is taken as a 64-bit fraction of a turn in integer arithmetic
+// 131072.  So, as in the published reduction of large arguments by a long 1 / 2 pi (Payne and
+// Hanek), f / 2 pi is taken as a 64-bit fraction of a turn in integer arithmetic
 // (fp64 is slow here), times p modulo 2^64: whole turns fall away, and what is left is
-// off by at most 2^-32 of a turn, for every 32-bit position.
+// off by less than 2^-33 of a turn from f's places cut off (32-bit positions) and 2^-32 from those
+// of the product.  The rest, at most 1/8 of a turn, is then taken to fp32, which adds 2^-28
+// of a turn at most: 2^-25.2 in all.
 //
 // Bound by memory.  A block turns a few tokens: their sines and cosines once, into
 // shared memory, for all heads; then each thread takes two 16-byte pieces, those that

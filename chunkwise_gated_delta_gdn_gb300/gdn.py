@@ -925,7 +925,9 @@ def rope_inv_freq(rot: int, base: float = 10000.0, *, stretch: float = 1.0,
     divided by it (positions are squeezed into the trained range), or, with ``trained`` (the
     length trained on) given, each by its wavelength: pairs that turn ``fast`` times or more
     within that length keep theirs, those that turn ``slow`` times or less are divided, those
-    between in part.  The mscale that is usual with the latter is 0.1 ln(stretch) + 1.
+    between in part.  The mscale that is usual with the latter is 0.1 ln(stretch) + 1.  That part
+    goes evenly by the turns; a model whose own code lets it go by the pair's index has other
+    frequencies there, and wants a table of its own.
     """
     if rot <= 0 or rot % 2 or not base > 0 or not stretch >= 1 or not fast > slow:
         raise ValueError("rot even and positive, base positive, stretch at least 1, fast above slow")

@@ -527,8 +527,10 @@ GDN_API gdn_status gdn_kv_cache_copy_pages(void *k_cache, void *v_cache, float *
  * Pair i is elements (i, i + rot / 2), or, interleaved = 1, (2 i, 2 i + 1); the
  * other d - rot elements are copied.  inv_freq [rot / 2] fp32, finite and below
  * 2^63 in magnitude: frequencies stretched for long contexts are the caller's
- * choice, mscale the factor that goes with them (1: none).  Angles are off by at
- * most 2^-29 for every position; outputs rounded once.
+ * choice, mscale the factor that goes with them (1: none).  For every position an angle,
+ * less whole turns, is exact to 1.5 * 2^-32 of a turn before it is taken to fp32, and off by
+ * at most 2^-25 after; outputs by at most 6 * 2^-24 mscale (|x| + |y|) in fp32, and
+ * that rounded once in bf16.
  * gdn_rope_bwd -- its gradient: dq, dk of the outputs to those of the inputs (the
  * same with -sin).
  *
