@@ -510,19 +510,28 @@ __device__ __forceinline__ void run(const AttnArgs &a, unsigned char *sm) {
     __syncthreads();
     for (int item = tid; item < rows * (D / 4); item += kThreads) {
       const int r = item / (D / 4), d4 = item % (D / 4);
-      float top = kNone, sum = 0.f;
+      float top = kNone, top_v = kNone, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; w++) top = fmaxf(top, join[(w * NT * 8 + r) * 3]);
+      for (int w = 0; w < kWarps; w++) {
+        top = fmaxf(top, join[(w * NT * 8 + r) * 3]);
+        top_v = fmaxf(top_v, join[(w * NT * 8 + r) * 3 + 2]);
+      }
       const float base = top;
+      // of the smallest values a factor could vanish: 2^64 too large then, and made good at the end
+      const bool tiny = top_v - base < -64.f;
+      const float shift = tiny ? kShift - 64.f : kShift;
       if (top <= kNone) top = -CUDART_INF_F;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; w++) {
         const float *x = join + (w * NT * 8 + r) * 3;
         sum += x[1] * ex2(x[0] - base);
-        const float fo = ex2(x[2] - base - kShift);
+        const float fo = ex2(x[2] - base - shift);
         const float4 z = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm) + (w * NT * 8 + r) * SM::kRow + d4 * 4);
         y.x += fo * z.x; y.y += fo * z.y; y.z += fo * z.z; y.w += fo * z.w;
+      }
+      if (tiny) {
+        y.x *= 0x1p-64f; y.y *= 0x1p-64f; y.z *= 0x1p-64f; y.w *= 0x1p-64f;
       }
       if (part) {
         a.part_o[MANY ? ((long long)u.slot * S::kRows + r) * (D / 4) + d4 : ((long long)u.slot * (D / 4) + d4) * S::kRows + r] = y;

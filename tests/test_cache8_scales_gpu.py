@@ -9,8 +9,8 @@ A = sum_j w_j |v_j|, E = sum_j w_j |s|_j, P = sum_j w_j |s|_j |v_j|, Z = max_j (
 * A weight times its scale is rounded to fp16 (2^-11 of it) once.  Below fp16's normal numbers the step is 2^-24, and
   the largest of them is at least 2^5.5, so a rounding there is at most 2^-30.5 of that; there are up to three where
   a maximum moves (two steps of a factor): 2^-28 Z.
-* The output is rounded to bf16 once: 2^-8 |o|.
-So |d o| <= 1.01 (2^-11 A + 2^-8 |o|) + 2^-28 Z + 2^-18 (P + E A) + (2^-20 |lse| + 2^-17) A.  Over many random values
+* The output is rounded to bf16 once: 2^-8 |o|, or half the step below its normal numbers, 2^-134.
+So |d o| <= 1.01 (2^-11 A + 2^-8 |o|) + 2^-134 + 2^-28 Z + 2^-18 (P + E A) + (2^-20 |lse| + 2^-17) A.  Over many random values
 a rounding's root mean square is at most its largest error over sqrt(3): sqrt(2^-16 + 2^-22) / sqrt(3) = 2.28e-3 of
 the norm.
 """
@@ -70,9 +70,9 @@ def close(got, x, q_lens, d, rows=None, scale=None, whole=True):
     of_lse = 2.0 ** -20 * np.where(sees, np.abs(ref_lse), 0)
     worst = np.abs(lse[sees] - ref_lse[sees]) / (2.0 ** -18 * E + of_lse + 1e-6)[sees]
     assert worst.size == 0 or worst.max() <= 1, ("lse", worst.max(), int((worst > 1).sum()))
-    bound = (1.01 * (2.0 ** -11 * A + 2.0 ** -8 * np.abs(ref)) + 2.0 ** -28 * Z + 2.0 ** -18 * (P + E[..., None] * A)
+    bound = (1.01 * (2.0 ** -11 * A + 2.0 ** -8 * np.abs(ref)) + 2.0 ** -134 + 2.0 ** -28 * Z + 2.0 ** -18 * (P + E[..., None] * A)
              + (of_lse[..., None] + 2.0 ** -17) * A)
-    worst = np.abs(o - ref) / np.maximum(bound, 1e-300)
+    worst = np.abs(o - ref) / bound
     assert worst.max() <= 1, ("o", worst.max(), int((worst > 1).sum()))
     if whole:
         assert np.linalg.norm(o - ref) <= 2.28e-3 * np.linalg.norm(ref)
@@ -182,3 +182,17 @@ def test_large_values_behind_zeros(d, nq, H, HKV, n):
     blind = 144 - (np.array(L) - nq)  # a sequence's tokens that see zeros alone
     for i in range(n):
         assert (got[0][i, :max(blind[i], 0)] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_lens", [[1, 1], [64, 200]], ids=str)
+@pytest.mark.parametrize("size", [2.0 ** -117, 2.0 ** -126, 1.25 * 2.0 ** -130, 2.0 ** 110])
+def test_scales_at_both_ends(d, q_lens, size):
+    """All values' scales near the smallest or largest numbers, also below the normal ones."""
+    def change(which, c, s, n):
+        if which:
+            s[:] = np.float32(size)
+        return c, s
+
+    x = paged(q_lens, [300, 700], 4, 2, d, 16, seed=29, spread=0.0, q_std=0.5, change=change)
+    close(run(x), x, q_lens, d, whole=False)
