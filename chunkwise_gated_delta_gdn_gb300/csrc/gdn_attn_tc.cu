@@ -144,12 +144,13 @@ __device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
 }
 // a whole number within 1 of x
 __device__ __forceinline__ float whole(float x) { return __fadd_rn(__fadd_rn(x, 0x1.8p23f), -0x1.8p23f); }
-// log2 of a scale: exact for powers of two; not below -127 (zero: of a bad page, whose
-// values are zeros)
+// log2 of a scale: exact for powers of two; -191 for zero (of a bad page, whose values are
+// zeros)
 __device__ __forceinline__ float scale_log2_of(float x) {
-  const uint32_t b = __float_as_uint(x);
+  const bool small = x < 0x1p-100f;  // and maybe below the normal numbers
+  const uint32_t b = __float_as_uint(small ? x * 0x1p64f : x);
   const float part = __uint_as_float((b & 0x7fffffu) | 0x3f800000u);
-  return (float)((int)(b >> 23 & 255) - 127) + (part == 1.f ? 0.f : __log2f(part));
+  return (float)((int)(b >> 23 & 255) - (small ? 191 : 127)) + (part == 1.f ? 0.f : __log2f(part));
 }
 __device__ __forceinline__ float two_to(int e) { return __int_as_float((127 + e) << 23); }
 __device__ __forceinline__ int shared_int(uint32_t at) {
@@ -707,6 +708,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
       // m_scaled: log2 of l's unit; `up`: of what the output's unit is more
       float m_scaled = FP8 ? (lam == kNone ? -CUDART_INF_F : lam) : m * sl2, f_own = 1.f, f_other = 0.f;
       [[maybe_unused]] const float up = FP8 ? (lam == kNone ? 0.f : m - kShift8 - lam) : 0.f;
+      [[maybe_unused]] bool tiny = false;  // the output's factors are 2^64 too large: they could vanish
       if (both) {
         // Row sums and maxima of both X: the sum of the halves and the maximum
         // in the places of the two halves' tile maxima.  The meeting also says
@@ -733,8 +735,10 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
           meet_all(1);  // read, before it is written again
           if (half == 0 && !idle) place[0] = up;
           meet_all(0);
-          f_own = ex2(m_scaled - base + up);
-          f_other = ex2(other[128] - base + other[0]);
+          const float own = m_scaled - base + up, others = other[128] - base + other[0];
+          tiny = fmaxf(own, others) < -64.f;
+          f_own = ex2(own + (tiny ? 64.f : 0.f));
+          f_other = ex2(others + (tiny ? 64.f : 0.f));
         }
         m_scaled = top;
       } else if (mine && !idle) {
@@ -742,7 +746,10 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         meet_half();
         l += *other_ex;
         meet_half();  // read, before the next tile's maximum is written
-        if constexpr (FP8) f_own = ex2(up);
+        if constexpr (FP8) {
+          tiny = up < -64.f;
+          f_own = ex2(up + (tiny ? 64.f : 0.f));
+        }
       }
       if (mine && !idle) {
         const bool valid = tok < u.n_tok;
@@ -769,6 +776,10 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
           } else if constexpr (FP8) {
 #pragma unroll
             for (int i = 0; i < kCols; i++) y[i] *= f_own;
+          }
+          if (FP8 && tiny) {
+#pragma unroll
+            for (int i = 0; i < kCols; i++) y[i] *= 0x1p-64f;
           }
           if (valid && part) {
 #pragma unroll

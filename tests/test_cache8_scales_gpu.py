@@ -187,7 +187,7 @@ def test_large_values_behind_zeros(d, nq, H, HKV, n):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("q_lens", [[1, 1], [64, 200]], ids=str)
 @pytest.mark.parametrize("size", [2.0 ** -117, 2.0 ** -126, 1.25 * 2.0 ** -130, 2.0 ** 110])
-def test_scales_at_both_ends(d, q_lens, size):
+def test_scales_at_both_ends(room, d, q_lens, size):  # noqa: F811
     """All values' scales near the smallest or largest numbers, also below the normal ones."""
     def change(which, c, s, n):
         if which:
@@ -196,3 +196,20 @@ def test_scales_at_both_ends(d, q_lens, size):
 
     x = paged(q_lens, [300, 700], 4, 2, d, 16, seed=29, spread=0.0, q_std=0.5, change=change)
     close(run(x), x, q_lens, d, whole=False)
+
+
+@pytest.mark.parametrize("nq", [1, 64])
+def test_a_maximum_that_lags_over_the_smallest_values(room, nq):  # noqa: F811
+    """The smallest scale of the write, scores that rise by less than what a maximum is let stand."""
+    L, d = 512, 64
+
+    def change(which, c, s, n):
+        if which:
+            s[:] = 2.0 ** -117
+        else:  # scores 0, then 7.5 (in powers of two) from the second key tile on
+            c[:128], c[128:], s[:] = 0, 0x38, 7.5 * np.log(2) / 8
+        return c, s
+
+    x = paged([nq], [L], 4, 2, d, 16, seed=37, spread=0.0, change=change)
+    x["q"] = torch.ones_like(x["q"])
+    close(run(x), x, [nq], d, whole=False)
