@@ -36,12 +36,14 @@
 // and end take about 10 us.
 //
 // Over a cache in 8 bits (FP8; paged, more than 16 or 32 rows): four warps more turn
-// loaded e4m3 tiles, and a unit's queries, into fp16 in place; see there.  512 tokens over
-// 32768 keys, 32/8 heads: 259 us where keys differ in size (249 where they do not; 225
-// over a bf16 cache), 1.05 PFLOP/s.  What it costs more: turning tiles and fetching
-// scales, as instructions beside the softmax and as reads and writes of shared
-// memory, which the products read at full rate meanwhile; and rows that move their maximum,
-// with keys of different sizes in a third of the tiles.
+// loaded e4m3 tiles, and a unit's queries, into fp16 in place, and the softmax applies the
+// scales of 16 keys each; see there.  512 tokens over 32768 keys, 32/8 heads: 264 us where
+// keys differ in size, 1.04 PFLOP/s (286 over a bf16 cache of the same values), 252 where
+// they do not (226).  What it costs more: turning tiles and fetching scales, as
+// instructions beside the softmax and as reads and writes of shared memory, which the
+// products read at full rate meanwhile; 16 keys' maxima and factors in the softmax (5 us
+// of the 264); and rows that move their maximum, with keys of different sizes in a third of the
+// tiles.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -252,7 +254,7 @@ struct Bars {
   __device__ uint32_t unit_empty(int i) const { return at(20 + kUnits + i); }
   __device__ uint32_t kv_full(int i) const { return at(20 + 2 * kUnits + i); }
   __device__ uint32_t kv_empty(int i) const { return at(20 + 2 * kUnits + stages + i); }
-  // 8 bits: what was loaded is there as bf16
+  // 8 bits: what was loaded is there as fp16
   __device__ uint32_t kv_ready(int i) const { return at(20 + 2 * kUnits + 2 * stages + i); }
   __device__ uint32_t q_ready() const { return at(20 + 2 * kUnits + 3 * stages); }
   __device__ uint32_t scales(int i) const { return at(21 + 2 * kUnits + 3 * stages + i); }
@@ -1345,7 +1347,7 @@ cudaError_t launch_attn_tc(const AttnArgs &a, int d, int blocks, cudaStream_t st
 }
 
 cudaError_t launch_attn8_tc(const AttnArgs &a, int d, int blocks, cudaStream_t stream) {
-  // rows of one warp's share of a tile at most: they are turned to bf16 in place
+  // rows of one warp's share of a tile at most: they are turned to fp16 in place
   const int box = (a.page_size & -a.page_size) < 32 ? a.page_size & -a.page_size : 32;
   Maps maps;
   if (!make_maps(maps, a, d, box, true)) return cudaErrorInvalidValue;

@@ -897,7 +897,8 @@ def gdn_rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Ten
     (:func:`rope_inv_freq`), and multiplied by mscale.  Positions are those of attention: the
     new tokens are the last of kv_lens (int32 ``[N]``, new tokens included), or, without
     kv_lens, the whole sequence.  q and k may be slices of one projection's output; pass
-    ``q_out=q, k_out=k`` to turn them in place.
+    ``q_out=q, k_out=k`` to turn them in place.  As nowhere in this module, no graph for
+    autograd is recorded: :func:`gdn_rope_bwd` is the gradient.
     """
     return _rope("gdn_rope_fwd", q, k, inv_freq, interleaved, mscale, kv_lens, cu_seqlens, q_out,
                  k_out, flags, stream)

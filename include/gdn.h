@@ -440,7 +440,8 @@ GDN_API gdn_status gdn_kv_cache_append(const void *k, const void *v, void *k_cac
 
 /*
  * A cache in 8 bits.  Half the bytes of a bf16 cache, and so up to twice the
- * sequences or lengths in the same memory and half the time of a decode step.
+ * sequences or lengths in the same memory and half the time of a decode step.  (More than 32
+ * new tokens times heads for a key/value head take 0.9 to 1.3 times as long as over a bf16 one.)
  *   k_cache, v_cache  [n_pages, page_size, HKV, d] e4m3 (bytes: 4 exponent, 3
  *               mantissa bits, bias 7, largest 448, 0x7f and 0xff NaN)
  *   k_scale, v_scale  [n_pages, page_size / 16, HKV] fp32: a scale for each
