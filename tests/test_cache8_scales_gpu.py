@@ -213,3 +213,14 @@ def test_a_maximum_that_lags_over_the_smallest_values(room, nq):  # noqa: F811
     x = paged([nq], [L], 4, 2, d, 16, seed=37, spread=0.0, change=change)
     x["q"] = torch.ones_like(x["q"])
     close(run(x), x, [nq], d, whole=False)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_lens", [[1, 1], [64, 200]], ids=str)
+def test_scores_of_the_largest_size(room, d, q_lens):  # noqa: F811
+    """Scores of up to 2^21 in magnitude, over blocks of different sizes."""
+    x = paged(q_lens, [300, 700], 4, 2, d, 16, seed=43, spread=2.0)
+    q = f64(x["q"])[0]
+    top = max(float(np.abs(q[:, 2 * h:2 * h + 2] @ k[:, h].T).max()) for k in x["values"][0] for h in range(2))
+    scale = float(np.float32(2.0 ** 21 / top))
+    close(run(x, scale=scale), x, q_lens, d, scale=scale, whole=False)
